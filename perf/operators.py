@@ -164,6 +164,7 @@ def prepare(case, seed):
         s["positions"] = torch.randint(lo, lo + case["span"], shape, generator=g, device=dev, dtype=torch.int32)
         s["turns"] = torch.tensor(_turns(case["rotated"], case["axes"], case["stretch"]), dtype=torch.int64, device=dev)
         s["sections"] = tuple(_sections(case["rotated"] // 2, case["axes"]))
+        s["axis"] = torch.tensor([a for a, n in enumerate(s["sections"]) for _ in range(n)], device=dev)
         s["amplitude"] = 0.1 * math.log(case["stretch"]) + 1.0
     elif case["op"] == "norm":
         t, c = case["tokens"], case["width"]
@@ -200,9 +201,7 @@ def prepare(case, seed):
 def _plain_rotary(s):
     case, sign = s["case"], -1.0 if s["case"]["backward"] else 1.0
     at = s["positions"].reshape(case["tokens"], -1)
-    axis = torch.repeat_interleave(torch.arange(at.shape[1], device=at.device),
-                                   torch.tensor(s["sections"], device=at.device), output_size=s["turns"].numel())
-    phase = at[:, axis].to(torch.int64) * s["turns"]  # whole turns wrap around
+    phase = at.to(torch.int64)[:, s["axis"]] * s["turns"]  # whole turns wrap around
     angle = (phase >> 32).to(torch.float32) * (math.pi / 2 ** 31)
     cos = (torch.cos(angle) * s["amplitude"])[:, None]
     sin = (torch.sin(angle) * (s["amplitude"] * sign))[:, None]
