@@ -419,6 +419,152 @@ TB_API int32_t tb_set_node_mode(int32_t mode);
  * (mode unchanged) for a mode outside 0..4. */
 TB_API int32_t tb_set_kmap_mode(int32_t mode);
 
+/* ------------------------------------------------------------------------
+ * Sequence operators over voxel tokens (library extension, no counterpart on
+ * the pages).  A model that reads a batch's voxels as sequences holds one row
+ * per active voxel in the batch's voxel order, grid after grid, with an int64
+ * offset per grid; these calls work on such rows in place of a padded batch.
+ *
+ * Conventions.  Rows, states and outputs are device memory of the caller; no
+ * call allocates, blocks the host or keeps anything from one call for the
+ * next, so every call can be captured in a CUDA graph.  Row tensors have
+ * elements of one `type`, unit stride inside a head and any strides (in
+ * elements) between rows and heads; 16-byte aligned pointers and strides take
+ * the vector kernels.  Sums, states and norms are held in 32 bits.  Sizes of
+ * zero are valid.  A non-finite input element reaches the outputs that the
+ * formula makes depend on it. */
+typedef enum { TB_TYPE_F32 = 0, TB_TYPE_F16 = 1, TB_TYPE_BF16 = 2 } tb_type;
+
+/* Rotary positions of queries and keys.  Pair p of a head turns by the angle
+ * 2 pi * position[axis(p)] * turns[p]:
+ *   (x, y) -> amplitude * (x cos - y sin, y cos + x sin),
+ * and by the opposite angle with inverse != 0, which is the gradient.  `turns`
+ * holds turns per unit of position as 64-bit fixed-point fractions, so
+ * that position * turns wraps at whole turns exactly for every 32-bit
+ * position (64-bit positions wrap the same way).  layout 0 pairs element p
+ * with p + pairs ("half"), layout 1 elements 2p and 2p + 1 ("interleaved").
+ * Elements from 2 * pairs on pass through unchanged.  With axes > 1, position
+ * rows hold one value per axis (a voxel's coordinates) and pairs below
+ * section[0] take axis 0, the next section[1] axis 1, the others axis 2.
+ * Outputs may be the inputs themselves (in place), or any buffers that do not
+ * overlap them.  A NULL k (or q) with no heads is left out. */
+typedef struct tb_rotary_args {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const void* positions;      /* int32 or int64 [tokens, axes]             */
+  const int64_t* turns;       /* [pairs]                                   */
+  int64_t tokens;
+  int64_t q_row, q_head, k_row, k_head;
+  int64_t q_out_row, q_out_head, k_out_row, k_out_head;
+  int64_t position_row;       /* elements between tokens' positions        */
+  int32_t q_heads, k_heads;
+  int32_t dim, pairs;         /* dim <= 256, 1 <= pairs <= dim / 2         */
+  int32_t axes;               /* 1, 2 or 3                                 */
+  int32_t section[2];
+  int32_t layout, type, positions64, inverse;
+  float amplitude;
+} tb_rotary_args;
+TB_API tb_status tb_rotary(const tb_rotary_args* args, tb_stream stream);
+
+/* Root-mean-square norm of rows with the residual stream's addition:
+ *   h = x + residual (in 32 bits),  y = h / sqrt(mean(h^2) + eps) * weight.
+ * h_out (NULL: not written; only with a residual) gets h rounded to `type`;
+ * y is computed from the unrounded h.  With fp8 != 0, `y` gets e4m3 bytes of
+ * y / scale and scale[row] = max |y| / 448 (a row of zeros: scale 0, bytes
+ * 0); else `y` has `type` and `scale` is NULL.  width <= 16384. */
+typedef struct tb_norm_args {
+  const void *x, *residual, *weight;
+  void *y, *h_out;
+  float* scale;
+  int64_t rows, x_row, residual_row, y_row, h_row;
+  int32_t width, type, fp8;
+  float eps;
+} tb_norm_args;
+TB_API tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream);
+
+/* Gradient of the norm.  h: the normed rows as tb_rms_norm wrote them (or x
+ * where there is no residual); dh (NULL: none): the gradient that reaches h
+ * past the norm.  With r = 1 / sqrt(mean(h^2) + eps):
+ *   dx = r weight dy - h r^3 mean(weight dy h) + dh,  dweight = sum over rows of dy h r.
+ * dx is the gradient of both x and residual.  dweight is summed in 32 bits in
+ * a fixed order and written in `type`.  width <= 16384.  workspace: 16-byte
+ * aligned, at least tb_rms_norm_backward_workspace(rows, width) bytes. */
+typedef struct tb_norm_backward_args {
+  const void *dy, *h, *weight, *dh;
+  void *dx, *dweight;
+  float* workspace;
+  int64_t rows, dy_row, h_row, dh_row, dx_row;
+  int64_t workspace_bytes;
+  int32_t width, type;
+  float eps;
+} tb_norm_backward_args;
+TB_API int64_t tb_rms_norm_backward_workspace(int64_t rows, int32_t width);
+TB_API tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stream);
+
+/* Linear attention with a decay for each head, over the rows of each grid:
+ *   S_t = decay S_{t-1} + k_t v_t^T,  o_t = scale q_t S_t
+ * with q, k rows [tokens, heads, key], v and o rows [tokens, heads, value]
+ * and 32-bit states [grids, heads, key, value].  decay[head] is in [0, 1].
+ * offsets: int64 [grids + 1] on the device, from 0 to tokens, not decreasing
+ * (values outside are clamped to the rows; rows of no grid are not written);
+ * NULL: one grid.  state: the states that grids start from (NULL: zero);
+ * state_out (or NULL): the states after each grid's last row, which for a
+ * grid without rows is its first.  key, value <= 128.
+ *
+ * The backward call gives, for gradients `grad` of o and dstate_out (NULL:
+ * zero) of state_out, with U_t = decay U_{t+1} + scale q_t do_t^T from
+ * U = dstate_out after the last row:
+ *   dq_t = scale S_t do_t,  dk_t = U_t v_t,  dv_t = U_t^T k_t
+ * and dstate (or NULL), the gradient of `state`.  The decay is a constant of
+ * the model: it has no gradient here.
+ *
+ * workspace: at least tb_linear_attention_workspace(...) bytes, 256-byte
+ * aligned (NULL where that is 0). */
+typedef struct tb_linear_args {
+  const void *q, *k, *v;
+  void* out;
+  const float* decay;
+  const int64_t* offsets;
+  const float* state;
+  float* state_out;
+  void* workspace;
+  int64_t tokens;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+  int64_t workspace_bytes;
+  int32_t grids, heads, key, value, type;
+  float scale;
+} tb_linear_args;
+typedef struct tb_linear_backward_args {
+  tb_linear_args f;           /* f.out and f.state_out are not used        */
+  const void* grad;
+  const float* dstate_out;
+  void *dq, *dk, *dv;
+  float* dstate;
+  int64_t grad_row, grad_head, dq_row, dq_head, dk_row, dk_head, dv_row, dv_head;
+} tb_linear_backward_args;
+TB_API int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int32_t heads, int32_t key, int32_t value,
+                                             int32_t type, int32_t backward);
+TB_API tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream);
+TB_API tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_stream stream);
+
+/* One token of each of `streams` sequences: the state of stream n (slot
+ * slots[n] of `state`; NULL: slot n) is decayed, takes k_n v_n^T in, and
+ * gives o_n = scale q_n S, all in place.  A stream whose slot is outside
+ * [0, num_slots) touches no state and its output is zero.  No two streams may
+ * share a slot.  states [num_slots, heads, key, value]; key, value <= 256. */
+typedef struct tb_linear_step_args {
+  const void *q, *k, *v;
+  void* out;
+  const float* decay;
+  float* state;
+  const int32_t* slots;
+  int64_t streams, num_slots;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head, out_row, out_head;
+  int32_t heads, key, value, type;
+  float scale;
+} tb_linear_step_args;
+TB_API tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream stream);
+
 /* Number of kernels this thread has launched through the library so far. */
 TB_API int64_t tb_kernel_launch_count(void);
 

@@ -31,6 +31,7 @@
 #include "tb_common.cuh"
 #include "tb_launch.h"
 #include "tb_layout.h"
+#include "tb_seq.h"
 
 using namespace tb;
 
@@ -73,12 +74,14 @@ thread_local long long t_launches = 0;
 
 enum KernelKind {
   kKPrepassLeaves, kKChain, kKWrite0, kKValidate = kKWrite0 + kNumOps, kKWriteMulti, kKPrune, kKKmap, kKKmapPrep,
-  kKExport, kKMember, kKNumKinds
+  kKExport, kKMember, kKSeq, kKNumKinds = kKSeq + kSeqNumKernels
 };
 const char* const kKernelNames[kKNumKinds] = {"prepass_leaves", "chain",         "write_ijk",
                                               "write_leaves",  "write_refine",   "write_coarsen", "write_dilate",
                                               "write_refine_dilate", "validate", "write_multi",   "prune",
-                                              "kernel_map",    "kmap_prep",    "export",        "member"};
+                                              "kernel_map",    "kmap_prep",    "export",        "member",
+                                              "rotary",        "norm",         "norm_backward", "norm_weight",
+                                              "linear_step",   "linear_scan",  "linear_states", "linear_combine"};
 
 struct ProfRec {
   int kind;
@@ -1300,6 +1303,20 @@ tb_status chain_specs(const tb_op* ops, int32_t n_ops, std::vector<PassSpec>* sp
 }  // namespace
 
 void tb::set_error_message(const char* msg) { t_err = msg; }
+
+cudaError_t tb::seq_launch(SeqKernel kind, cudaStream_t s, SeqLaunch f, const void* args) {
+  return launch(kKSeq + kind, s, [&] { return f(args, s); });
+}
+
+tb_status tb::seq_fail(tb_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  t_err = buf;
+  return st;
+}
 
 // ================================================================ C ABI
 

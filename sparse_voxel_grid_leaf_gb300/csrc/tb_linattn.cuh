@@ -1,0 +1,96 @@
+// Which rows a block of the linear-attention kernels walks: whole grids, or
+// the segments of a call that splits its grids along the rows.
+#pragma once
+
+#include "tb_seq.h"
+
+namespace tb {
+
+struct LinSegment {
+  int grid;          // -1: the slot holds no segment
+  int index, count;  // of the grid's segments
+  int64_t begin, end;  // the grid's rows
+  int64_t first;     // the segment's places in the order of the walk: [first, first + len)
+  int len;
+};
+
+__device__ __forceinline__ void lin_grid_rows(const LinLaunch& l, int b, int64_t& begin, int64_t& end) {
+  if (!l.offsets) {
+    begin = 0;
+    end = l.tokens;
+    return;
+  }
+  begin = min(max(l.offsets[b], (int64_t)0), l.tokens);
+  end = min(max(l.offsets[b + 1], begin), l.tokens);
+}
+
+__device__ __forceinline__ int lin_segments_of(const LinLaunch& l, int64_t rows) {
+  return rows > 0 ? (int)((rows + l.segment - 1) / l.segment) : 1;
+}
+
+// The segment slot of grid b's first segment.  One warp; the same in all lanes.
+__device__ __forceinline__ int lin_first_slot(const LinLaunch& l, int b) {
+  int sum = 0;
+  for (int i = threadIdx.x & 31; i < b; i += 32) {
+    int64_t begin, end;
+    lin_grid_rows(l, i, begin, end);
+    sum += lin_segments_of(l, end - begin);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
+}
+
+// The segment of a slot, found by one warp; the same in all lanes.
+__device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) {
+  LinSegment s;
+  s.grid = -1;
+  s.len = 0;
+  if (l.segment == 0) {
+    s.grid = slot;
+    s.index = 0;
+    s.count = 1;
+    lin_grid_rows(l, slot, s.begin, s.end);
+    s.first = 0;
+    s.len = (int)(s.end - s.begin);
+    return s;
+  }
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int base = 0; base < l.grids; base += 32) {
+    int64_t begin = 0, end = 0;
+    int n = 0;
+    if (base + lane < l.grids) {
+      lin_grid_rows(l, base + lane, begin, end);
+      n = lin_segments_of(l, end - begin);
+    }
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > slot);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      s.grid = base + src;
+      s.count = __shfl_sync(0xffffffffu, n, src);
+      s.index = slot - before - __shfl_sync(0xffffffffu, upto - n, src);
+      s.begin = __shfl_sync(0xffffffffu, begin, src);
+      s.end = __shfl_sync(0xffffffffu, end, src);
+      s.first = (int64_t)s.index * l.segment;
+      s.len = (int)min((int64_t)l.segment, s.end - s.begin - s.first);
+      return s;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return s;
+}
+
+// decay^n for n >= 0.  The logarithm's relative error of 2^-24 moves the
+// result by n |log2 decay| 2^-24, which is small wherever the power is not.
+__device__ __forceinline__ float lin_power(float decay, float n) {
+  return n > 0.f ? exp2f(n * log2f(decay)) : 1.f;
+}
+
+}  // namespace tb

@@ -1,0 +1,95 @@
+// Host-side launchers of the sequence operators' kernels (internal to libtb.so).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tb.h"
+
+namespace tb {
+
+// Kernel kinds of tb_profile_read, continued by the sequence operators.
+enum SeqKernel {
+  kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqStates, kSeqCombine, kSeqNumKernels
+};
+
+// Every launch of a sequence operator is counted, and timed when profiling is
+// enabled on the calling thread (defined next to the pass kernels' own).
+typedef cudaError_t (*SeqLaunch)(const void* args, cudaStream_t s);
+cudaError_t seq_launch(SeqKernel kind, cudaStream_t s, SeqLaunch f, const void* args);
+tb_status seq_fail(tb_status st, const char* fmt, ...);
+// Multiprocessors of the current device (0: no device).
+int seq_sms();
+
+// ------------------------------------------------------------------- rotary
+struct RotaryLaunch {
+  tb_rotary_args a;
+  int vec;        // 16-byte vectors everywhere, else one element at a time
+  int per_block;  // tokens of one block
+};
+cudaError_t launch_rotary(const void* args, cudaStream_t s);
+
+// --------------------------------------------------------------------- norm
+struct NormLaunch {
+  tb_norm_args a;
+  int vec, per_row, nv, rows;  // threads of a row, vectors of a thread, rows of a block
+  int blocks;
+};
+cudaError_t launch_norm(const void* args, cudaStream_t s);
+struct NormBackwardLaunch {
+  tb_norm_backward_args a;
+  int vec, per_row, nv, rows;
+  int blocks;
+};
+cudaError_t launch_norm_backward(const void* args, cudaStream_t s);
+cudaError_t launch_norm_weight(const void* args, cudaStream_t s);
+
+// --------------------------------------------------------- linear attention
+struct StepLaunch {
+  tb_linear_step_args a;
+};
+cudaError_t launch_linear_step(const void* args, cudaStream_t s);
+
+// One sum over the earlier rows of every grid, in the order of `reverse`:
+//   U_t = d U_{t-1} + fold * b_t c_t^T,   out_t = mul * a_t U_t
+// over rows a, b [T, H, K] and c, out [T, H, V].  The forward pass and the
+// three gradients are this sum over different rows:
+//   o  = sum(q, k, v)             forward,  state S,   mul = scale
+//   dq = sum(do, v, k)            forward,  state S^T, mul = scale
+//   dv = sum(k, q, do)            reverse,  state U,   fold = scale
+//   dk = sum(v, do, q)            reverse,  state U^T, fold = scale
+// The carried state X of the forward order is S after a token (decayed as the
+// next one enters, late = 0); that of the reverse order is decayed as a token
+// leaves (late = 1), so that the gradient of a grid's last state enters its
+// last token undecayed and the gradient of its first state comes out decayed.
+struct LinProblem {
+  const void *a, *b, *c;
+  void* out;                  // NULL: the states alone
+  int64_t a_row, a_head, b_row, b_head, c_row, c_head, o_row, o_head;
+  int32_t K, V;
+  const float* first;         // [B, H] states a grid starts from, or NULL: zero
+  int64_t first_k, first_v;   // element strides of one state (transposed reads)
+  float* last;                // [B, H, K, V] states that come out, or NULL
+  float* seg;                 // [segments, H, K, V]: states of the segments of a split call
+  float mul, fold;
+  int32_t reverse, late;
+};
+constexpr int kLinMaxProblems = 3;
+struct LinLaunch {
+  LinProblem p[kLinMaxProblems];
+  int32_t n;
+  int32_t type;
+  int32_t heads;
+  int32_t grids;
+  int64_t tokens;
+  const int64_t* offsets;     // NULL: one grid of all tokens
+  const float* decay;
+  int32_t segment;            // tokens of one segment; 0: a grid is one segment
+  int32_t segments;           // segment slots: the grid's x extent
+  int32_t phase;              // 0: whole grids; 1: states of segments; 2: outputs of segments
+};
+cudaError_t launch_linear_scan(const void* args, cudaStream_t s);
+cudaError_t launch_linear_combine(const void* args, cudaStream_t s);
+
+}  // namespace tb

@@ -1,0 +1,356 @@
+// C entry points of the sequence operators: checks of the arguments, the
+// choice of a kernel's shape, the launches.  No allocation and no wait.
+#include <atomic>
+#include <cstring>
+
+#include "tb_seq.h"
+
+using namespace tb;
+
+namespace {
+
+constexpr int64_t kMaxRows = (1ll << 31) - 1;
+
+#define TB_SEQ_CUDA(expr)                                                                          \
+  do {                                                                                             \
+    const cudaError_t e_ = (expr);                                                                 \
+    if (e_ != cudaSuccess) return seq_fail(TB_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_)); \
+  } while (0)
+
+int type_size(int32_t type) { return type == TB_TYPE_F32 ? 4 : 2; }
+bool type_ok(int32_t type) { return type >= TB_TYPE_F32 && type <= TB_TYPE_BF16; }
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool whole(int64_t stride, int size) { return stride * size % 16 == 0; }
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Threads and vectors per row of a norm kernel.  Few rows: one vector a
+// thread, for the shortest chain of loads.  Many rows: up to `most` vectors,
+// in the shape that leaves the fewest idle lanes (the larger nv on a tie, so
+// that a row needs no barrier).
+void norm_shape(int64_t rows, int vecs, int sms, int most, const int* counts, int n, int* per_row, int* nv,
+                int* per_block) {
+  const bool many = rows >= 4ll * sms;
+  int best = -1;
+  int64_t waste = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t threads = up(up(vecs, counts[i]), 32) * 32;
+    if (threads > 512) continue;
+    const int64_t idle = threads * counts[i] - vecs;
+    if (best < 0 || (many && counts[i] <= most && idle <= waste)) {
+      best = i;
+      waste = idle;
+      *per_row = (int)threads;
+    }
+  }
+  *nv = counts[best];
+  *per_block = many ? (*per_row >= 256 ? 1 : 256 / *per_row) : 1;
+}
+
+}  // namespace
+
+int tb::seq_sms() {
+  static std::atomic<int> sms[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return 0;
+  }
+  int n = sms[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+extern "C" {
+
+// ------------------------------------------------------------------- rotary
+
+tb_status tb_rotary(const tb_rotary_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: args is NULL");
+  RotaryLaunch r;
+  r.a = *args;
+  tb_rotary_args& a = r.a;
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: unknown type %d", a.type);
+  if (a.tokens < 0 || a.q_heads < 0 || a.k_heads < 0)
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: negative size");
+  if (a.dim < 1 || a.dim > 256 || a.pairs < 1 || 2 * a.pairs > a.dim)
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: %d pairs of a head of %d elements (at most 256)", a.pairs, a.dim);
+  if (a.layout < 0 || a.layout > 1) return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: unknown layout %d", a.layout);
+  if (a.axes < 1 || a.axes > 3) return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: %d position axes (1 to 3)", a.axes);
+  if (a.axes > 1) {
+    const int64_t two = (int64_t)a.section[0] + a.section[1];
+    if (a.section[0] < 0 || a.section[1] < 0 || two > a.pairs || (a.axes == 2 && two != a.pairs))
+      return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: sections %d, %d of %d pairs", a.section[0], a.section[1], a.pairs);
+  }
+  if (a.tokens == 0 || a.q_heads + (int64_t)a.k_heads == 0) return TB_OK;
+  if (a.tokens > kMaxRows || a.q_heads + (int64_t)a.k_heads > 65535)
+    return seq_fail(TB_ERR_TOO_LARGE, "tb_rotary: 2^31 tokens or 65536 heads, or more");
+  if (!a.positions || !a.turns || (a.q_heads && (!a.q || !a.q_out)) || (a.k_heads && (!a.k || !a.k_out)))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rotary: bad pointer");
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "tb_rotary: no device");
+  const int size = type_size(a.type), vec = 16 / size;
+  r.vec = a.pairs % vec == 0 && (a.dim - 2 * a.pairs) % vec == 0;
+  if (a.q_heads)
+    r.vec = r.vec && aligned16(a.q) && aligned16(a.q_out) && whole(a.q_row, size) && whole(a.q_head, size) &&
+            whole(a.q_out_row, size) && whole(a.q_out_head, size);
+  if (a.k_heads)
+    r.vec = r.vec && aligned16(a.k) && aligned16(a.k_out) && whole(a.k_row, size) && whole(a.k_head, size) &&
+            whole(a.k_out_row, size) && whole(a.k_out_head, size);
+  // A block's threads take 8 rows (token, head) each, unless that leaves
+  // multiprocessors idle; the table stays within 16 KB.
+  const int units = r.vec ? a.pairs / vec + (a.dim - 2 * a.pairs) / vec : a.dim - a.pairs;
+  const int heads = a.q_heads + a.k_heads;
+  int64_t per = up(8ll * (256 / units), heads);
+  const int64_t fit = 16384 / (8 * a.pairs);
+  if (per > fit) per = fit;
+  if (per > a.tokens / (4 * sms)) per = a.tokens / (4 * sms);
+  r.per_block = per < 1 ? 1 : (int)per;
+  TB_SEQ_CUDA(seq_launch(kSeqRotary, (cudaStream_t)stream, launch_rotary, &r));
+  return TB_OK;
+}
+
+// --------------------------------------------------------------------- norm
+
+tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: args is NULL");
+  NormLaunch n;
+  n.a = *args;
+  tb_norm_args& a = n.a;
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: unknown type %d", a.type);
+  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: bad size");
+  if (a.width > 16384 || a.rows > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "tb_rms_norm: rows of %d elements (at most 16384), or 2^31 rows", a.width);
+  if (a.rows == 0) return TB_OK;
+  if (!a.x || !a.weight || !a.y || (a.h_out && !a.residual) || (a.fp8 != 0) != (a.scale != nullptr))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: bad pointer");
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "tb_rms_norm: no device");
+  const int size = type_size(a.type), vec = 16 / size;
+  n.vec = a.width % vec == 0 && aligned16(a.x) && aligned16(a.weight) && whole(a.x_row, size);
+  if (a.residual) n.vec = n.vec && aligned16(a.residual) && whole(a.residual_row, size);
+  if (a.h_out) n.vec = n.vec && aligned16(a.h_out) && whole(a.h_row, size);
+  if (a.fp8) n.vec = n.vec && ((uintptr_t)a.y & (vec - 1)) == 0 && a.y_row % vec == 0;
+  else n.vec = n.vec && aligned16(a.y) && whole(a.y_row, size);
+  static const int kVecs[] = {1, 2, 4, 8}, kOnes[] = {8, 32};
+  if (n.vec) norm_shape(a.rows, a.width / vec, sms, 4, kVecs, 4, &n.per_row, &n.nv, &n.rows);
+  else norm_shape(a.rows, a.width, sms, 8, kOnes, 2, &n.per_row, &n.nv, &n.rows);
+  n.blocks = (int)up(a.rows, n.rows);
+  TB_SEQ_CUDA(seq_launch(kSeqNorm, (cudaStream_t)stream, launch_norm, &n));
+  return TB_OK;
+}
+
+static int64_t norm_backward_blocks(int64_t rows, int sms) {
+  const int64_t most = 4ll * sms;
+  return rows < most ? rows : most;
+}
+
+int64_t tb_rms_norm_backward_workspace(int64_t rows, int32_t width) {
+  if (rows < 0 || width < 1) return 0;
+  const int sms = seq_sms();
+  return norm_backward_blocks(rows, sms ? sms : 256) * width * (int64_t)sizeof(float);
+}
+
+tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: args is NULL");
+  NormBackwardLaunch n;
+  n.a = *args;
+  tb_norm_backward_args& a = n.a;
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: unknown type %d", a.type);
+  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: bad size");
+  if (a.width > 16384 || a.rows > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "tb_rms_norm_backward: rows of %d elements (at most 16384), or 2^31 rows", a.width);
+  if (!a.dweight || (a.rows && (!a.dy || !a.h || !a.weight || !a.dx || !a.workspace)))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: bad pointer");
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "tb_rms_norm_backward: no device");
+  const int64_t most = norm_backward_blocks(a.rows, sms);
+  if (a.workspace_bytes < most * a.width * (int64_t)sizeof(float) || !aligned16(a.workspace))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: a workspace of %lld bytes, %lld needed",
+                    (long long)a.workspace_bytes, (long long)(most * a.width * 4));
+  const int size = type_size(a.type), vec = 16 / size;
+  n.vec = a.width % vec == 0 && aligned16(a.dy) && aligned16(a.h) && aligned16(a.weight) && aligned16(a.dx) &&
+          whole(a.dy_row, size) && whole(a.h_row, size) && whole(a.dx_row, size);
+  if (a.dh) n.vec = n.vec && aligned16(a.dh) && whole(a.dh_row, size);
+  static const int kVecs[] = {1, 2, 4, 8}, kOnes[] = {8, 32};
+  if (n.vec) norm_shape(a.rows, a.width / vec, sms, 4, kVecs, 4, &n.per_row, &n.nv, &n.rows);
+  else norm_shape(a.rows, a.width, sms, 8, kOnes, 2, &n.per_row, &n.nv, &n.rows);
+  // a block's parts of dweight meet in shared memory
+  while (n.rows > 1 && (int64_t)n.rows * n.per_row * n.nv * (n.vec ? vec : 1) * 4 > 40 * 1024) n.rows /= 2;
+  const int64_t blocks = up(a.rows, n.rows);
+  n.blocks = (int)(blocks < most ? blocks : most);
+  if (a.rows) TB_SEQ_CUDA(seq_launch(kSeqNormBackward, (cudaStream_t)stream, launch_norm_backward, &n));
+  TB_SEQ_CUDA(seq_launch(kSeqNormWeight, (cudaStream_t)stream, launch_norm_weight, &n));
+  return TB_OK;
+}
+
+// --------------------------------------------------------- linear attention
+
+// Tokens of a segment, 0: grids are walked whole.  A walk is sequential along
+// a grid, so a call with few grids and heads is split along the rows: the
+// segments' own states first, their joining, then the outputs.  The states
+// pass reads the keys and values once more, and pays where it fills the
+// multiprocessors: where whole grids leave less than four blocks for each.
+static int32_t segment_tokens(int64_t tokens, int32_t grids, int32_t heads, int problems, int sms) {
+  const int64_t walks = (int64_t)heads * problems;
+  const int64_t want = 4ll * sms;
+  if (grids <= 0 || grids * walks >= want) return 0;
+  int64_t seg = up(up(tokens * walks, want), 64) * 64;
+  if (seg < 256) seg = 256;
+  return tokens >= 2 * seg * grids ? (int32_t)seg : 0;
+}
+
+static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
+  return segment ? tokens / segment + grids : grids;
+}
+
+int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int32_t heads, int32_t key, int32_t value,
+                                      int32_t type, int32_t backward) {
+  (void)type;
+  if (tokens < 0 || grids < 0 || heads < 1 || key < 1 || value < 1) return 0;
+  const int sms = seq_sms();
+  const int problems = backward ? 3 : 1;
+  const int32_t seg = segment_tokens(tokens, grids, heads, problems, sms ? sms : 256);
+  return seg ? segment_slots(tokens, grids, seg) * heads * key * value * 4 * problems : 0;
+}
+
+static tb_status linear_check(const char* what, const tb_linear_args& a) {
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "%s: unknown type %d", what, a.type);
+  if (a.tokens < 0 || a.grids < 0 || a.heads < 1 || a.key < 1 || a.value < 1)
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (a.key > 128 || a.value > 128)
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: heads of %d keys and %d values (at most 128)", what, a.key, a.value);
+  if (a.tokens > kMaxRows || a.heads > 65535 || (int64_t)a.grids * a.heads > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 tokens, 65536 heads or 2^31 states, or more", what);
+  if (!a.offsets && a.grids != 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d grids without offsets", what, a.grids);
+  if (a.grids == 0 && a.tokens) return seq_fail(TB_ERR_INVALID_ARG, "%s: tokens without grids", what);
+  if ((a.tokens && (!a.q || !a.k || !a.v)) || !a.decay) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  return TB_OK;
+}
+
+static tb_status linear_run(const char* what, const tb_linear_args& a, LinLaunch& l, cudaStream_t s) {
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  l.type = a.type;
+  l.heads = a.heads;
+  l.grids = a.grids;
+  l.tokens = a.tokens;
+  l.offsets = a.offsets;
+  l.decay = a.decay;
+  l.segment = segment_tokens(a.tokens, a.grids, a.heads, l.n, sms);
+  const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
+  l.segments = (int32_t)slots;
+  if (l.segment) {
+    const int64_t one = slots * a.heads * a.key * a.value;
+    if (!a.workspace || a.workspace_bytes < one * 4 * l.n || ((uintptr_t)a.workspace & 255))
+      return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what,
+                      (long long)a.workspace_bytes, (long long)(one * 4 * l.n));
+    for (int i = 0; i < l.n; ++i) l.p[i].seg = (float*)a.workspace + i * one;
+    l.phase = 1;
+    TB_SEQ_CUDA(seq_launch(kSeqStates, s, launch_linear_scan, &l));
+    TB_SEQ_CUDA(seq_launch(kSeqCombine, s, launch_linear_combine, &l));
+    l.phase = 2;
+  } else {
+    l.phase = 0;
+  }
+  TB_SEQ_CUDA(seq_launch(kSeqScan, s, launch_linear_scan, &l));
+  return TB_OK;
+}
+
+tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention: args is NULL");
+  const tb_linear_args& a = *args;
+  const tb_status st = linear_check("tb_linear_attention", a);
+  if (st != TB_OK) return st;
+  if (a.tokens && !a.out) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention: bad pointer");
+  if (a.grids == 0 || (a.tokens == 0 && !a.state_out)) return TB_OK;
+  LinLaunch l;
+  memset(&l, 0, sizeof l);
+  l.n = 1;
+  LinProblem& p = l.p[0];
+  p.a = a.q, p.a_row = a.q_row, p.a_head = a.q_head;
+  p.b = a.k, p.b_row = a.k_row, p.b_head = a.k_head;
+  p.c = a.v, p.c_row = a.v_row, p.c_head = a.v_head;
+  p.out = a.out, p.o_row = a.out_row, p.o_head = a.out_head;
+  p.K = a.key, p.V = a.value;
+  p.first = a.state, p.first_k = a.value, p.first_v = 1;
+  p.last = a.state_out;
+  p.mul = a.scale, p.fold = 1.f;
+  return linear_run("tb_linear_attention", a, l, (cudaStream_t)stream);
+}
+
+tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_backward: args is NULL");
+  const tb_linear_args& a = args->f;
+  const tb_linear_backward_args& g = *args;
+  const tb_status st = linear_check("tb_linear_attention_backward", a);
+  if (st != TB_OK) return st;
+  if (a.tokens && (!g.grad || !g.dq || !g.dk || !g.dv))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_backward: bad pointer");
+  if (a.grids == 0 || (a.tokens == 0 && !g.dstate)) return TB_OK;
+  LinLaunch l;
+  memset(&l, 0, sizeof l);
+  l.n = 3;
+  {  // dv, with the state U and its end, the gradient of the first state
+    LinProblem& p = l.p[0];
+    p.a = a.k, p.a_row = a.k_row, p.a_head = a.k_head;
+    p.b = a.q, p.b_row = a.q_row, p.b_head = a.q_head;
+    p.c = g.grad, p.c_row = g.grad_row, p.c_head = g.grad_head;
+    p.out = g.dv, p.o_row = g.dv_row, p.o_head = g.dv_head;
+    p.K = a.key, p.V = a.value;
+    p.first = g.dstate_out, p.first_k = a.value, p.first_v = 1;
+    p.last = g.dstate;
+    p.mul = 1.f, p.fold = a.scale;
+    p.reverse = p.late = 1;
+  }
+  {  // dk, with U^T
+    LinProblem& p = l.p[1];
+    p.a = a.v, p.a_row = a.v_row, p.a_head = a.v_head;
+    p.b = g.grad, p.b_row = g.grad_row, p.b_head = g.grad_head;
+    p.c = a.q, p.c_row = a.q_row, p.c_head = a.q_head;
+    p.out = g.dk, p.o_row = g.dk_row, p.o_head = g.dk_head;
+    p.K = a.value, p.V = a.key;
+    p.first = g.dstate_out, p.first_k = 1, p.first_v = a.value;
+    p.mul = 1.f, p.fold = a.scale;
+    p.reverse = p.late = 1;
+  }
+  {  // dq, with S^T
+    LinProblem& p = l.p[2];
+    p.a = g.grad, p.a_row = g.grad_row, p.a_head = g.grad_head;
+    p.b = a.v, p.b_row = a.v_row, p.b_head = a.v_head;
+    p.c = a.k, p.c_row = a.k_row, p.c_head = a.k_head;
+    p.out = g.dq, p.o_row = g.dq_row, p.o_head = g.dq_head;
+    p.K = a.value, p.V = a.key;
+    p.first = a.state, p.first_k = 1, p.first_v = a.value;
+    p.mul = a.scale, p.fold = 1.f;
+  }
+  return linear_run("tb_linear_attention_backward", a, l, (cudaStream_t)stream);
+}
+
+tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: args is NULL");
+  StepLaunch l;
+  l.a = *args;
+  const tb_linear_step_args& a = l.a;
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: unknown type %d", a.type);
+  if (a.streams < 0 || a.num_slots < 0 || a.heads < 1 || a.key < 1 || a.value < 1)
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: bad size");
+  if (a.key > 256 || a.value > 256 || a.streams * a.heads > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "tb_linear_attention_step: heads of %d keys and %d values (at most 256), or 2^31 states",
+                    a.key, a.value);
+  if (a.streams == 0) return TB_OK;
+  if (!a.slots && a.num_slots < a.streams)
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: %lld streams, %lld states", (long long)a.streams,
+                    (long long)a.num_slots);
+  if (!a.q || !a.k || !a.v || !a.out || !a.decay || (a.num_slots && (!a.state || !aligned16(a.state))))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: bad pointer");
+  TB_SEQ_CUDA(seq_launch(kSeqStep, (cudaStream_t)stream, launch_linear_step, &l));
+  return TB_OK;
+}
+
+}  // extern "C"
