@@ -547,6 +547,11 @@ TB_API int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int3
 TB_API tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream);
 TB_API tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_stream stream);
 
+/* Whether a bounded wait inside a linear-attention kernel gave up since the
+ * last such call (TB_ERR_DEVICE_TIMEOUT: outputs of calls since are not to be
+ * used).  Blocks until `stream` is done. */
+TB_API tb_status tb_linear_attention_status(tb_stream stream);
+
 /* One token of each of `streams` sequences: the state of stream n (slot
  * slots[n] of `state`; NULL: slot n) is decayed, takes k_n v_n^T in, and
  * gives o_n = scale q_n S, all in place.  A stream whose slot is outside

@@ -612,5 +612,6 @@ def export_many(batches: Sequence[Batch], origins=None, masks=None, voxel_offset
                                       plist(leaf_offsets), ctypes.c_void_p(_stream(stream))))
 
 
-from .seq import (linear_attention, linear_attention_backward, linear_attention_step, rms_norm,  # noqa: E402,F401
-                  rms_norm_backward, rms_norm_fp8, rotary, rotary_backward, rotary_frequencies)
+from .seq import (linear_attention, linear_attention_backward, linear_attention_status,  # noqa: E402,F401
+                  linear_attention_step, rms_norm, rms_norm_backward, rms_norm_fp8, rotary, rotary_backward,
+                  rotary_frequencies)

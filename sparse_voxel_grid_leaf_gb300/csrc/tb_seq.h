@@ -1,6 +1,7 @@
 // Host-side launchers of the sequence operators' kernels (internal to libtb.so).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -11,7 +12,8 @@ namespace tb {
 
 // Kernel kinds of tb_profile_read, continued by the sequence operators.
 enum SeqKernel {
-  kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqStates, kSeqCombine, kSeqNumKernels
+  kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqScanStates,
+  kSeqChunks, kSeqChunkStates, kSeqCombine, kSeqNumKernels
 };
 
 // Every launch of a sequence operator is counted, and timed when profiling is
@@ -89,6 +91,18 @@ struct LinLaunch {
   int32_t segments;           // segment slots: the grid's x extent
   int32_t phase;              // 0: whole grids; 1: states of segments; 2: outputs of segments
 };
+// The chunk kernel's call (tb_linattn_chunk.cu): the walk and the row tensors
+// as the copy engine reads them.
+struct ChunkLaunch {
+  LinLaunch l;
+  CUtensorMap map[4];
+  uint8_t a[kLinMaxProblems], b[kLinMaxProblems], c[kLinMaxProblems];  // the maps of a problem's rows
+};
+// Completes g for its g.l; false where the chunk kernel does not take the rows.
+bool linear_chunk_plan(ChunkLaunch& g);
+cudaError_t launch_linear_chunks(const void* args, cudaStream_t s);
+// Whether a bounded wait of the chunk kernel gave up since the last call.  Blocks.
+cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up);
 cudaError_t launch_linear_scan(const void* args, cudaStream_t s);
 cudaError_t launch_linear_combine(const void* args, cudaStream_t s);
 

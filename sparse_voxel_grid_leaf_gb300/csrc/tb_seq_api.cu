@@ -195,10 +195,11 @@ tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stre
 // a grid, so a call with few grids and heads is split along the rows: the
 // segments' own states first, their joining, then the outputs.  The states
 // pass reads the keys and values once more, and pays where it fills the
-// multiprocessors: where whole grids leave less than four blocks for each.
-static int32_t segment_tokens(int64_t tokens, int32_t grids, int32_t heads, int problems, int sms) {
+// multiprocessors: one block of the chunk kernel (16-bit rows) runs on each,
+// four of the recurrence.
+static int32_t segment_tokens(int64_t tokens, int32_t grids, int32_t heads, int problems, int32_t type, int sms) {
   const int64_t walks = (int64_t)heads * problems;
-  const int64_t want = 4ll * sms;
+  const int64_t want = (type == TB_TYPE_BF16 ? 2ll : 4ll) * sms;
   if (grids <= 0 || grids * walks >= want) return 0;
   int64_t seg = up(up(tokens * walks, want), 64) * 64;
   if (seg < 256) seg = 256;
@@ -211,11 +212,10 @@ static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
 
 int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int32_t heads, int32_t key, int32_t value,
                                       int32_t type, int32_t backward) {
-  (void)type;
   if (tokens < 0 || grids < 0 || heads < 1 || key < 1 || value < 1) return 0;
   const int sms = seq_sms();
   const int problems = backward ? 3 : 1;
-  const int32_t seg = segment_tokens(tokens, grids, heads, problems, sms ? sms : 256);
+  const int32_t seg = segment_tokens(tokens, grids, heads, problems, type, sms ? sms : 256);
   return seg ? segment_slots(tokens, grids, seg) * heads * key * value * 4 * problems : 0;
 }
 
@@ -233,7 +233,8 @@ static tb_status linear_check(const char* what, const tb_linear_args& a) {
   return TB_OK;
 }
 
-static tb_status linear_run(const char* what, const tb_linear_args& a, LinLaunch& l, cudaStream_t s) {
+static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaunch& g, cudaStream_t s) {
+  LinLaunch& l = g.l;
   const int sms = seq_sms();
   if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
   l.type = a.type;
@@ -242,7 +243,7 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, LinLaunch
   l.tokens = a.tokens;
   l.offsets = a.offsets;
   l.decay = a.decay;
-  l.segment = segment_tokens(a.tokens, a.grids, a.heads, l.n, sms);
+  l.segment = segment_tokens(a.tokens, a.grids, a.heads, l.n, a.type, sms);
   const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
   l.segments = (int32_t)slots;
   if (l.segment) {
@@ -251,14 +252,19 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, LinLaunch
       return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what,
                       (long long)a.workspace_bytes, (long long)(one * 4 * l.n));
     for (int i = 0; i < l.n; ++i) l.p[i].seg = (float*)a.workspace + i * one;
+  }
+  // A chunk of 64 rows costs the tensor cores the same with one row in it.
+  const bool chunks = a.tokens >= 16ll * a.grids && linear_chunk_plan(g);
+  l.phase = 0;
+  if (l.segment) {
     l.phase = 1;
-    TB_SEQ_CUDA(seq_launch(kSeqStates, s, launch_linear_scan, &l));
+    if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunkStates, s, launch_linear_chunks, &g));
+    else TB_SEQ_CUDA(seq_launch(kSeqScanStates, s, launch_linear_scan, &l));
     TB_SEQ_CUDA(seq_launch(kSeqCombine, s, launch_linear_combine, &l));
     l.phase = 2;
-  } else {
-    l.phase = 0;
   }
-  TB_SEQ_CUDA(seq_launch(kSeqScan, s, launch_linear_scan, &l));
+  if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunks, s, launch_linear_chunks, &g));
+  else TB_SEQ_CUDA(seq_launch(kSeqScan, s, launch_linear_scan, &l));
   return TB_OK;
 }
 
@@ -269,8 +275,9 @@ tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream) {
   if (st != TB_OK) return st;
   if (a.tokens && !a.out) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention: bad pointer");
   if (a.grids == 0 || (a.tokens == 0 && !a.state_out)) return TB_OK;
-  LinLaunch l;
-  memset(&l, 0, sizeof l);
+  ChunkLaunch g;
+  memset(&g, 0, sizeof g);
+  LinLaunch& l = g.l;
   l.n = 1;
   LinProblem& p = l.p[0];
   p.a = a.q, p.a_row = a.q_row, p.a_head = a.q_head;
@@ -281,7 +288,7 @@ tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream) {
   p.first = a.state, p.first_k = a.value, p.first_v = 1;
   p.last = a.state_out;
   p.mul = a.scale, p.fold = 1.f;
-  return linear_run("tb_linear_attention", a, l, (cudaStream_t)stream);
+  return linear_run("tb_linear_attention", a, g, (cudaStream_t)stream);
 }
 
 tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_stream stream) {
@@ -293,8 +300,9 @@ tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_s
   if (a.tokens && (!g.grad || !g.dq || !g.dk || !g.dv))
     return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_backward: bad pointer");
   if (a.grids == 0 || (a.tokens == 0 && !g.dstate)) return TB_OK;
-  LinLaunch l;
-  memset(&l, 0, sizeof l);
+  ChunkLaunch plan;
+  memset(&plan, 0, sizeof plan);
+  LinLaunch& l = plan.l;
   l.n = 3;
   {  // dv, with the state U and its end, the gradient of the first state
     LinProblem& p = l.p[0];
@@ -329,7 +337,14 @@ tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_s
     p.first = a.state, p.first_k = 1, p.first_v = a.value;
     p.mul = a.scale, p.fold = 1.f;
   }
-  return linear_run("tb_linear_attention_backward", a, l, (cudaStream_t)stream);
+  return linear_run("tb_linear_attention_backward", a, plan, (cudaStream_t)stream);
+}
+
+tb_status tb_linear_attention_status(tb_stream stream) {
+  bool gave_up = false;
+  TB_SEQ_CUDA(linear_gave_up((cudaStream_t)stream, &gave_up));
+  if (gave_up) return seq_fail(TB_ERR_DEVICE_TIMEOUT, "tb_linear_attention: a device-side wait timed out");
+  return TB_OK;
 }
 
 tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream stream) {

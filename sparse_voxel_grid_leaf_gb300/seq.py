@@ -20,7 +20,7 @@ import struct
 from typing import Optional, Sequence, Tuple
 
 __all__ = ["rotary_frequencies", "rotary", "rotary_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
-           "linear_attention", "linear_attention_backward", "linear_attention_step"]
+           "linear_attention", "linear_attention_backward", "linear_attention_step", "linear_attention_status"]
 
 # the argument structs of include/tb.h, field by field
 _ROTARY = struct.Struct("@6P10q11if")
@@ -495,6 +495,15 @@ def linear_attention_backward(do, q, k, v, decay, offsets=None, state=None, scal
     is the gradient of ``state`` (None without one)."""
     scale = q.shape[-1] ** -0.5 if scale is None else scale
     return _linear_backward(do, q, k, v, decay, offsets, state, scale, dstate, state is not None)
+
+
+def linear_attention_status(stream=None):
+    """Waits for the stream; raises TBError(TB_ERR_DEVICE_TIMEOUT) where a
+    bounded wait inside a linear-attention kernel gave up since the last call."""
+    from . import TBError, _stream, lib
+    status = lib().tb_linear_attention_status(ctypes.c_void_p(_stream(stream)))
+    if status:
+        raise TBError(status, lib().tb_last_error().decode())
 
 
 @_streamed
