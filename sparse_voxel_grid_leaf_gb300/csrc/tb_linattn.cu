@@ -227,6 +227,8 @@ __global__ void __launch_bounds__(256) k_scan(LinLaunch l) {
     }
 }
 
+constexpr int kCombineBatch = 16;
+
 // Joins the segments of a split call: the state that enters each segment, in
 // place of the segment's own, and the state that leaves the grid.
 __global__ void __launch_bounds__(256) k_combine(LinLaunch l) {
@@ -241,19 +243,25 @@ __global__ void __launch_bounds__(256) k_combine(LinLaunch l) {
   const float rest = lin_power(decay, (float)(end - begin - (int64_t)(n - 1) * l.segment));
   const int size = p.K * p.V;
   const int64_t state_at = ((int64_t)b * l.heads + h) * size;
-  const int stride = gridDim.y * blockDim.x;
-  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < size; i += stride) {
-    float x = p.first ? p.first[state_at + i / p.V * p.first_k + i % p.V * p.first_v] : 0.f;
-    float* at = p.seg + ((int64_t)slot0 * l.heads + h) * size + i;
-    const int64_t next = (int64_t)l.heads * size;
-    for (int s = 0; s < n; ++s, at += next) {
-      const bool last = s + 1 == n;
-      const float own = last && !p.last ? 0.f : *at;
-      *at = x;
-      x = fmaf(x, last ? rest : whole, own);
-    }
-    if (p.last) p.last[state_at + i] = x;
+  const int i = blockIdx.y * blockDim.x + threadIdx.x;
+  if (i >= size) return;
+  float x = p.first ? p.first[state_at + i / p.V * p.first_k + i % p.V * p.first_v] : 0.f;
+  float* at = p.seg + ((int64_t)slot0 * l.heads + h) * size + i;
+  const int64_t next = (int64_t)l.heads * size;
+  // the segments' own states are loaded ahead of the chain that joins them
+  for (int s0 = 0; s0 < n; s0 += kCombineBatch) {
+    float own[kCombineBatch];
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j)
+      own[j] = s0 + j < n - (p.last ? 0 : 1) ? at[(s0 + j) * next] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j)
+      if (s0 + j < n) {
+        at[(s0 + j) * next] = x;
+        x = fmaf(x, s0 + j + 1 == n ? rest : whole, own[j]);
+      }
   }
+  if (p.last) p.last[state_at + i] = x;
 }
 
 template <class T>
@@ -292,7 +300,9 @@ cudaError_t launch_linear_scan(const void* args, cudaStream_t s) {
 
 cudaError_t launch_linear_combine(const void* args, cudaStream_t s) {
   const LinLaunch& l = *(const LinLaunch*)args;
-  const dim3 grid((unsigned)(l.grids * l.heads), 8, l.n);
+  int size = 0;
+  for (int i = 0; i < l.n; ++i) size = l.p[i].K * l.p[i].V > size ? l.p[i].K * l.p[i].V : size;
+  const dim3 grid((unsigned)(l.grids * l.heads), (size + 255) / 256, l.n);
   k_combine<<<grid, 256, 0, s>>>(l);
   return cudaGetLastError();
 }

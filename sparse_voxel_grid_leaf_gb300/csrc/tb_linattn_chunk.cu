@@ -34,27 +34,32 @@ namespace {
 
 constexpr int kC = 64;            // rows of a chunk
 constexpr int kTile = 8192;       // 64 rows x 128 bytes
-constexpr int kStages = 4;
-constexpr int kThreads = 18 * 32;
-constexpr int kWarpTma = 16, kWarpMma = 17;
+constexpr int kMaxStages = 4;
+// Warps: 8 of the state, the copies, the products, 2 of P, 4 of the output.
+// Sixteen leave 128 registers a thread, which hold the state of 128 keys
+// without spills (eighteen left 96, and the spills cost more than a third).
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpP = 10, kWarpOut = 12;
+constexpr int threads_of(bool states) { return (states ? kWarpP : 16) * 32; }
+
+constexpr int stages_of(int KP) { return KP == 64 ? 4 : 3; }
 
 // Set when a wait gave up (a bug, or a GPU that stands still): read and
 // cleared by launch_linear_status.
 __device__ unsigned int g_gave_up;
 
 enum Bars {
-  kFull = 0, kEmpty = kFull + kStages, kPReady = kEmpty + kStages, kPFull = kPReady + 2, kWFull = kPFull + 2, kCFull,
-  kCFree = kCFull + 2, kKvReady = kCFree + 2, kKvFree, kStFull, kStFree, kOReady, kOFree, kDrain, kBars
+  kFull = 0, kEmpty = kFull + kMaxStages, kPReady = kEmpty + kMaxStages, kPFull = kPReady + 2, kWFull = kPFull + 2, kCFull,
+  kCFree = kCFull + 2, kKvReady = kCFree + 2, kKvFree, kStFull, kStFree, kOReady, kOFree, kZeros, kDrain, kBars
 };
 
 struct Shared {
   uint64_t bar[kBars];
   uint32_t tmem;
   volatile uint32_t gave_up;
-  volatile uint32_t bad[kStages];  // chunk + 1 whose values are not all finite
+  volatile uint32_t bad[kMaxStages];  // chunk + 1 whose values are not all finite
   LinSegment seg;
   float pow[kC + 1];               // decay^n
-  float fold[kC + 1];              // fold mul decay^n
+  float fold[2 * kC + 1];          // fold mul decay^(n - 64), 0 for n < 64
   __align__(16) float up[kC];      // decay^(m+1), times fold (reverse) or mul (forward)
   __align__(16) float down[4][2 * kC];  // decay^(63-m), 0 past m = 63: copy s starts at m = s
 };
@@ -67,21 +72,40 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 __device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ float shared_bf16(uint32_t at) {
+  uint16_t bits;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));
+  return __uint_as_float((uint32_t)bits << 16);
+}
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// Adds P_ij c_j of the rows j whose value is not finite to the rows i that see
+// them, in a warp's staged output (the product had zeros in their place).
+__device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t p_tile, uint32_t c_tile, int n, bool reverse) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t col = (lane & 7) * 2;
+  const int warp_chunk = ((threadIdx.x >> 5) & 1) * 4 + (lane >> 3);  // the lane's 8 values within 64
+  for (int j = 0; j < n; ++j) {
+    const float c = shared_bf16(c_tile + j * 128 + ((warp_chunk ^ (j & 7)) << 4) + col);
+    if (!not_finite(c)) continue;
+    for (int i = reverse ? 0 : j; i <= (reverse ? j : n - 1); ++i) {
+      const uint32_t at = stage + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + col;
+      const float pij = shared_bf16(p_tile + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2);
+      const float o = fmaf(pij, c, shared_bf16(at));
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)(bf16x2(o, o) & 0xffffu)) : "memory");
+    }
+  }
 }
 
 // KP: keys of a tile, 64 or 128 (fewer are padded with zeros by the copies).
 // kStates: the states of segments alone, without outputs.
 template <int KP, int kTerms, bool kStates>
-__global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
+__global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
   constexpr int kCt = KP == 128 && kTerms == 3 ? 1 : 2;  // buffers of C^T in tensor memory
   constexpr uint32_t kColP = 0, kColOi = 128, kColKv = 192, kColCt = kColKv + KP, kColW = kColCt + 32 * kCt,
                      kColSt = kColW + 32 * kTerms;
   static_assert(kColSt + KP / 2 <= 512, "tensor memory");
-  constexpr int kBlocks = KP / 64;
+  constexpr int kBlocks = KP / 64, kStages = stages_of(KP);
   constexpr int kStageBytes = (2 * kBlocks + 2) * kTile;  // A, B, C
 
   extern __shared__ char s_raw[];
@@ -92,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
 
   const LinLaunch& l = g.l;
   const LinProblem& p = l.p[blockIdx.z];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int h = blockIdx.y;
   auto bar = [&](int i) { return smem_addr(&s.bar[i]); };
   const bool reverse = p.reverse;
@@ -120,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
       mbar_init(bar(kStFree), 1);
       mbar_init(bar(kOReady), 1);
       mbar_init(bar(kOFree), 4);
+      mbar_init(bar(kZeros), 8);
       mbar_init(bar(kDrain), 1);
       s.gave_up = 0;
       fence_mbar_init();
@@ -132,9 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
     if (i <= kC) {
       const float x = lin_power(d, (float)i);
       s.pow[i] = x;
-      s.fold[i] = p.fold * p.mul * x;
+      s.fold[kC + i] = p.fold * p.mul * x;
       if (i) s.up[i - 1] = x * (reverse ? p.fold : p.mul);
     }
+    if (i < kC) s.fold[i] = 0.f;
     for (int c = 0; c < 4; ++c) s.down[c][i] = i + c < kC ? lin_power(d, (float)(kC - 1 - i - c)) : 0.f;
   }
   tc_fence_before();
@@ -160,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
   const int value_blocks = p.V > 64 ? 2 : 1;
 
   if (warp == kWarpTma) {
-    if (lane == 0) {
+    if (elect_one()) {
       const CUtensorMap* ma = &g.map[g.a[blockIdx.z]];
       const CUtensorMap* mb = &g.map[g.b[blockIdx.z]];
       const CUtensorMap* mc = &g.map[g.c[blockIdx.z]];
@@ -189,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
       }
     }
   } else if (warp == kWarpMma) {
-    if (lane == 0 && chunks) {
+    if (chunks && elect_one()) {
       constexpr uint32_t kPDesc = mma_desc(128, kC, false);
       constexpr uint32_t kKvDesc = mma_desc(128, KP, true);
       auto scores = [&](int t) {  // A B^T, rows i in lanes 64 to 127
@@ -276,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
       const uint32_t at = stage0 + st * kStageBytes;
       if (!wait(kFull + st, t / kStages)) break;
       if (n < kC) {
-        // rows past the segment belong to others: no NaN of theirs may meet the zeros that the decayed values hold
-        for (int i = threadIdx.x; i < kBlocks * (kC - n) * 8; i += 256) {
+        // rows past the segment belong to others: no NaN of theirs may meet the zeros that their weights are
+        for (int i = threadIdx.x; i < (kBlocks + value_blocks) * (kC - n) * 8; i += 256) {
           const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                            at + (kBlocks + blk) * kTile + n * 128 + r * 16),
@@ -285,60 +311,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
                        : "memory");
         }
         fence_async_smem();
+        arrive(kZeros);  // once: only the last chunk is short
+        if (!wait(kZeros, 0)) break;
       }
       if (!kStates && t >= kCt && !wait(kCFree + t % kCt, t / kCt - 1)) break;
       if (live) {
-        const uint32_t col = at + (2 * kBlocks + (v >> 6)) * kTile + (v & 7) * 2;
-        const float* w = reverse ? s.up + half * 32 : s.down[(kC - n) & 3] + ((kC - n) & ~3) + half * 32;
+        // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a value
+        const float* w = (reverse ? s.up : s.down[(kC - n) & 3] + ((kC - n) & ~3)) + half * 32 + 2 * (lane & 3);
+        float2 wv[4];
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 16) {
+        for (int m = 0; m < 4; ++m) wv[m] = *reinterpret_cast<const float2*>(w + 8 * m);
+        const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
+        const uint32_t rows = at + (2 * kBlocks + ((warp & 3) >> 1)) * kTile + r * 128;
+#pragma unroll
+        for (int g16 = 0; g16 < 2; ++g16) {
           uint32_t ct[8], x[kTerms][8];
-          float finite = 0.f;
+          const uint32_t from = rows + ((((warp & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+          ldmatrix_trans4(from, ct[0], ct[1], ct[2], ct[3]);
+          ldmatrix_trans4(from + 16 * 128, ct[4], ct[5], ct[6], ct[7]);
+          uint32_t finite = 0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 wv = *reinterpret_cast<const float4*>(w + r0 + j);
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = half * 32 + r0 + j + i;
-              uint16_t bits;
-              asm volatile("ld.shared.u16 %0, [%1];"
-                           : "=h"(bits)
-                           : "r"(col + r * 128 + ((((v & 63) >> 3) ^ (r & 7)) << 4)));
-              f[i] = r < n ? __uint_as_float((uint32_t)bits << 16) : 0.f;
-              finite = fmaf(f[i], 0.f, finite);
-            }
-            const float t0 = f[0] * wv.x, t1 = f[1] * wv.y, t2 = f[2] * wv.z, t3 = f[3] * wv.w;
-            ct[j / 2] = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x7632);
-            ct[j / 2 + 1] = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x7632);
-            float e0 = t0, e1 = t1, e2 = t2, e3 = t3;
+          for (int i = 0; i < 8; ++i) {
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(finite) : "r"(ct[i]), "r"(0));
+            float e0 = low(ct[i]) * wv[i / 2].x, e1 = high(ct[i]) * wv[i / 2].y;
 #pragma unroll
             for (int term = 0; term < kTerms; ++term) {
-              const uint32_t a = bf16x2(e0, e1), b = bf16x2(e2, e3);
-              x[term][j / 2] = a;
-              x[term][j / 2 + 1] = b;
-              if (term + 1 < kTerms) {
-                e0 -= low(a);
-                e1 -= high(a);
-                e2 -= low(b);
-                e3 -= high(b);
-              }
+              x[term][i] = bf16x2(e0, e1);
+              e0 -= low(x[term][i]);
+              e1 -= high(x[term][i]);
             }
           }
-          if (finite != finite) {
-            // 0 x infinity of a later row is not part of an earlier row's sum: the product takes zeros, and the
+          const bool bad = not_finite(low(finite)) || not_finite(high(finite));
+          if (__any_sync(0xffffffffu, bad)) {
+            // 0 x infinity of a later row is no part of an earlier row's sum: the product takes zeros, and the
             // output warps add these values to the rows that see them
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if ((ct[j] & 0x7f80u) == 0x7f80u) ct[j] &= 0xffff0000u;
-              if ((ct[j] & 0x7f800000u) == 0x7f800000u) ct[j] &= 0xffffu;
+            for (int i = 0; i < 8; ++i) {
+              if (not_finite(low(ct[i]))) ct[i] &= 0xffff0000u;
+              if (not_finite(high(ct[i]))) ct[i] &= 0xffffu;
             }
             s.bad[st] = t + 1;
           }
-          __syncwarp();
+          const uint32_t to = lanes + ((uint32_t)g16 << 20) + half * 16;
 #pragma unroll
-          for (int term = 0; term < kTerms; ++term) tmem_st8(lanes + kColW + term * 32 + half * 16 + r0 / 2, x[term]);
-          if (!kStates) tmem_st8(lanes + kColCt + t % kCt * 32 + half * 16 + r0 / 2, ct);
+          for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + kColW + term * 32, x[term]);
+          if (!kStates) tmem_st_16x16(to + kColCt + t % kCt * 32, ct);
         }
         tmem_wait_st();
       }
@@ -386,101 +403,127 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
         if (k < p.K) dst[(int64_t)k * p.V + v] = u[i];
       }
     }
-  } else if (!kStates && warp < 12) {
+  } else if (!kStates && warp < kWarpOut) {
     // ------------------------------------------------------------------- P
-    if ((warp & 3) >= 2) {
-      const int i = (warp & 1) * 32 + lane;
-      const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-      for (int t = 0; t < chunks; ++t) {
-        const int n = rows_of(t);
-        if (!wait(kPReady + (t & 1), t >> 1)) break;
-        tc_fence_after();
-        const uint32_t row = tiles + (t & 1) * kTile + i * 128;
+    const int half = warp & 1, i = half * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    for (int t = 0; t < chunks; ++t) {
+      const int n = rows_of(t);
+      if (!wait(kPReady + (t & 1), t >> 1)) break;
+      tc_fence_after();
+      const uint32_t row = tiles + (t & 1) * kTile + i * 128;
 #pragma unroll
-        for (int j0 = 0; j0 < kC; j0 += 16) {
-          uint32_t x[16];
-          tmem_ld16(lanes + kColP + (t & 1) * 64 + j0, x);
+      for (int b = 0; b < 2; ++b) {  // columns 32 b to 32 b + 31
+        uint32_t x[32];
+        if (reverse ? b >= half : b <= half) {
+          tmem_ld32(lanes + kColP + (t & 1) * 64 + 32 * b, x);
           tmem_wait_ld();
-          float f[16];
+          // fold[|i - j|]; on the diagonal block and past the rows the index may be negative, and P is 0
+          if (reverse) {
+            const float* w = s.fold + kC + 32 * b - i;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int jj = j0 + j, back = reverse ? jj - i : i - jj;
-            const float w = s.fold[max(back, 0)];
-            f[j] = back >= 0 && jj < n ? __uint_as_float(x[j]) * w : 0.f;
+            for (int j = 0; j < 32; ++j) {
+              const float f = __uint_as_float(x[j]) * w[j];
+              x[j] = 32 * b + j >= i && 32 * b + j < n ? __float_as_uint(f) : 0u;
+            }
+          } else {
+            const float* w = s.fold + kC + i - 32 * b;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float f = __uint_as_float(x[j]) * w[-j];
+              x[j] = b < half || j <= lane ? __float_as_uint(f) : 0u;
+            }
           }
+        } else {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((j0 / 8 + q) ^ (i & 7)) << 4)),
-                         "r"(bf16x2(f[8 * q], f[8 * q + 1])), "r"(bf16x2(f[8 * q + 2], f[8 * q + 3])),
-                         "r"(bf16x2(f[8 * q + 4], f[8 * q + 5])), "r"(bf16x2(f[8 * q + 6], f[8 * q + 7]))
-                         : "memory");
+          for (int j = 0; j < 32; ++j) x[j] = 0u;
         }
-        fence_async_smem();
-        tc_fence_before();
-        arrive(kPFull + (t & 1));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((b * 4 + q) ^ (i & 7)) << 4)),
+                       "r"(bf16x2(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]))),
+                       "r"(bf16x2(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]))),
+                       "r"(bf16x2(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]))),
+                       "r"(bf16x2(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7])))
+                       : "memory");
       }
+      fence_async_smem();
+      tc_fence_before();
+      arrive(kPFull + (t & 1));
     }
-  } else if (!kStates && warp < 16) {
+  } else if (!kStates) {
     // -------------------------------------------------------------- output
-    const int v = (warp & 3) * 32 + lane;
     const bool live = (warp & 3) * 32 < p.V;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t out0 = stage0 + kStages * kStageBytes + (warp & 3) * 2 * 4096;  // two buffers of 64 rows x 64 bytes
+    const CUtensorMap* map = &g.map[kLinMaxRows + blockIdx.z];
     for (int t = 0; t < chunks; ++t) {
       const int st = t % kStages, n = rows_of(t);
       if (!wait(kOReady, t)) break;
       tc_fence_after();
       if (live) {
-        const float* w = reverse ? s.down[(kC - n) & 3] + ((kC - n) & ~3) : s.up;
-        __nv_bfloat16* out = (__nv_bfloat16*)p.out + row_of(t) * p.o_row + h * p.o_head + v;
+        const float* w = (reverse ? s.down[(kC - n) & 3] + ((kC - n) & ~3) : s.up) + 2 * (lane & 3);
         const bool bad = s.bad[st] == (uint32_t)t + 1;
+        const uint32_t buf = out0 + (t & 1) * 4096;
+        if (lane == 0) tma_store_wait<1>();
+        __syncwarp();
+        const int row = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-        for (int i0 = 0; i0 < kC; i0 += 16) {
-          uint32_t x[16], y[16];
-          tmem_ld16(lanes + kColP + (t & 1) * 64 + i0, x);
-          tmem_ld16(lanes + kColOi + i0, y);
+        for (int g16 = 0; g16 < 2; ++g16) {
+          uint32_t x[32], y[32];
+          tmem_ld_16x64(lanes + ((uint32_t)g16 << 20) + kColP + (t & 1) * 64, x);
+          tmem_ld_16x64(lanes + ((uint32_t)g16 << 20) + kColOi, y);
           tmem_wait_ld();
-          float o[16];
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 wv = *reinterpret_cast<const float4*>(w + i0 + i);
-            o[i] = fmaf(__uint_as_float(y[i]), wv.x, __uint_as_float(x[i]));
-            o[i + 1] = fmaf(__uint_as_float(y[i + 1]), wv.y, __uint_as_float(x[i + 1]));
-            o[i + 2] = fmaf(__uint_as_float(y[i + 2]), wv.z, __uint_as_float(x[i + 2]));
-            o[i + 3] = fmaf(__uint_as_float(y[i + 3]), wv.w, __uint_as_float(x[i + 3]));
+          if (g16 == 1 && !bad) {
+            tc_fence_before();
+            arrive(kOFree);
           }
-          if (bad) {
-            const uint32_t col = stage0 + st * kStageBytes + (2 * kBlocks + (v >> 6)) * kTile + (v & 7) * 2;
-            for (int j = 0; j < n; ++j) {
-              uint16_t bits;
-              asm volatile("ld.shared.u16 %0, [%1];"
-                           : "=h"(bits)
-                           : "r"(col + j * 128 + ((((v & 63) >> 3) ^ (j & 7)) << 4)));
-              if ((bits & 0x7f80) != 0x7f80) continue;
+          const uint32_t to = buf + row * 64 + (((g16 * 2 + ((lane >> 3) & 1)) ^ ((row >> 1) & 3)) << 4);
+          uint32_t o[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int ii = i0 + i;
-                if (reverse ? ii <= j : ii >= j) {
-                  uint16_t pb;
-                  asm volatile("ld.shared.u16 %0, [%1];"
-                               : "=h"(pb)
-                               : "r"(tiles + (t & 1) * kTile + ii * 128 + (((j >> 3) ^ (ii & 7)) << 4) + (j & 7) * 2));
-                  o[i] = fmaf(__uint_as_float((uint32_t)pb << 16), __uint_as_float((uint32_t)bits << 16), o[i]);
-                }
-              }
-            }
+          for (int m = 0; m < 8; ++m) {
+            const float2 wv = *reinterpret_cast<const float2*>(w + 8 * m);
+            auto both = [&](int i) {
+              return bf16x2(fmaf(__uint_as_float(y[i]), wv.x, __uint_as_float(x[i])),
+                            fmaf(__uint_as_float(y[i + 1]), wv.y, __uint_as_float(x[i + 1])));
+            };
+            o[2 * m] = both(4 * m);
+            o[2 * m + 1] = both(4 * m + 2);
           }
-          if (v < p.V) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (i0 + i < n) out[(i0 + i) * p.o_row] = __float2bfloat16_rn(o[i]);
-          }
-          __syncwarp();
+          for (int m = 0; m < 4; ++m)
+            stmatrix_trans4(to + m * 16 * 64, o[4 * m], o[4 * m + 1], o[4 * m + 2], o[4 * m + 3]);
         }
+        __syncwarp();
+        if (bad) {
+          add_not_finite(buf, tiles + (t & 1) * kTile, stage0 + st * kStageBytes + (2 * kBlocks + ((warp & 3) >> 1)) * kTile,
+                         n, reverse);
+          tc_fence_before();
+          arrive(kOFree);
+        }
+        const int64_t row0 = row_of(t);
+        if (n == kC) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_3d(map, (warp & 3) * 32, h, (int)row0, buf);
+        } else {
+          // the rows that follow are not this segment's: plain stores
+          for (int i = lane; i < n * 4; i += 32) {
+            const int rr = i >> 2, v = (warp & 3) * 32 + (i & 3) * 8;
+            uint4 o;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                         : "r"(buf + rr * 64 + (((i & 3) ^ ((rr >> 1) & 3)) << 4)));
+            if (v < p.V) *reinterpret_cast<uint4*>((__nv_bfloat16*)p.out + (row0 + rr) * p.o_row + h * p.o_head + v) = o;
+          }
+        }
+      } else {
+        tc_fence_before();
+        arrive(kOFree);
       }
-      tc_fence_before();
-      arrive(kOFree);
       arrive(kEmpty + st);
     }
+    if (lane == 0) tma_store_wait<0>();
   }
 
   tc_fence_before();
@@ -492,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunks(const __grid_constant__ 
 
 template <int KP, int kTerms, bool kStates>
 cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
-  constexpr int bytes = 1024 + 2 * kTile + kStages * (2 * (KP / 64) + 2) * kTile;
+  constexpr int bytes = 1024 + 2 * kTile + stages_of(KP) * (2 * (KP / 64) + 2) * kTile + (kStates ? 0 : 4 * 2 * 4096);
+  static_assert(bytes > 116 * 1024 && bytes < 224 * 1024, "one block a multiprocessor: tensor memory is not shared");
   static bool ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -503,7 +547,7 @@ cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
   const dim3 grid(g.l.segments, g.l.heads, g.l.n);
-  k_chunks<KP, kTerms, kStates><<<grid, kThreads, bytes, s>>>(g);
+  k_chunks<KP, kTerms, kStates><<<grid, threads_of(kStates), bytes, s>>>(g);
   return cudaGetLastError();
 }
 
@@ -525,9 +569,9 @@ Encode encoder() {
   return fn;
 }
 
-// Rows [tokens, heads, size] as the copy engine reads them: 64 elements x 64
-// rows of one head a box.  False where it cannot.
-bool row_map(CUtensorMap* m, const void* at, int size, int heads, int64_t tokens, int64_t row, int64_t head) {
+// Rows [tokens, heads, size] as the copy engine takes them, a box of 64 rows of
+// one head: 64 elements of it read, or 32 written.  False where it cannot.
+bool row_map(CUtensorMap* m, const void* at, int size, int heads, int64_t tokens, int64_t row, int64_t head, int box_size) {
   if (!encoder() || ((uintptr_t)at & 15)) return false;
   // a stride that nothing is reached by still has to be one the encoding takes
   if (heads == 1) head = size;
@@ -535,9 +579,9 @@ bool row_map(CUtensorMap* m, const void* at, int size, int heads, int64_t tokens
   if (head <= 0 || row <= 0 || head % 8 || row % 8 || head >= 1ll << 38 || row >= 1ll << 38) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)size, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)row * 2};
-  const cuuint32_t box[3] = {64, 1, kC}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_size, 1, kC}, step[3] = {1, 1, 1};
   return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(at), dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, box_size == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -549,7 +593,7 @@ bool linear_chunk_plan(ChunkLaunch& g) {
     const void* at;
     int size;
     int64_t row, head;
-  } known[4];
+  } known[kLinMaxRows];
   int n = 0;
   auto find = [&](const Rows& x, uint8_t* to) {
     for (int i = 0; i < n; ++i)
@@ -557,7 +601,7 @@ bool linear_chunk_plan(ChunkLaunch& g) {
         *to = (uint8_t)i;
         return true;
       }
-    if (n == 4 || !row_map(&g.map[n], x.at, x.size, l.heads, l.tokens, x.row, x.head)) return false;
+    if (n == kLinMaxRows || !row_map(&g.map[n], x.at, x.size, l.heads, l.tokens, x.row, x.head, 64)) return false;
     known[n] = x;
     *to = (uint8_t)n++;
     return true;
@@ -567,7 +611,8 @@ bool linear_chunk_plan(ChunkLaunch& g) {
     const LinProblem& p = l.p[i];
     if (p.K % 8 || p.V % 8 || p.reverse != p.late || (p.reverse ? p.mul : p.fold) != 1.f) return false;
     if (!find({p.a, p.K, p.a_row, p.a_head}, &g.a[i]) || !find({p.b, p.K, p.b_row, p.b_head}, &g.b[i]) ||
-        !find({p.c, p.V, p.c_row, p.c_head}, &g.c[i]))
+        !find({p.c, p.V, p.c_row, p.c_head}, &g.c[i]) ||
+        !row_map(&g.map[kLinMaxRows + i], p.out, p.V, l.heads, l.tokens, p.o_row, p.o_head, 32))
       return false;
   }
   return true;

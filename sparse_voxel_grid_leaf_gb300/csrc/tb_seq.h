@@ -93,9 +93,10 @@ struct LinLaunch {
 };
 // The chunk kernel's call (tb_linattn_chunk.cu): the walk and the row tensors
 // as the copy engine reads them.
+constexpr int kLinMaxRows = 4;
 struct ChunkLaunch {
   LinLaunch l;
-  CUtensorMap map[4];
+  CUtensorMap map[kLinMaxRows + kLinMaxProblems];  // rows that are read, then the problems' outputs
   uint8_t a[kLinMaxProblems], b[kLinMaxProblems], c[kLinMaxProblems];  // the maps of a problem's rows
 };
 // Completes g for its g.l; false where the chunk kernel does not take the rows.
