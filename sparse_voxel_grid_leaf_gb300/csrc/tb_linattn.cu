@@ -11,6 +11,7 @@
 // block stages in shared memory as floats.  Two multiply-adds and a multiply
 // per state element and row in packed pairs (fma.rn.f32x2) bound it.
 #include "tb_linattn.cuh"
+#include "tb_linattn_scan.cuh"
 #include "tb_seq.cuh"
 
 namespace tb {
@@ -95,136 +96,12 @@ cudaError_t go_step(const StepLaunch& l, cudaStream_t s) {
 
 // ------------------------------------------------------------- the recurrence
 
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 halves(f32x2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-constexpr int kScanRows = 16;  // rows staged at a time
-
-// KS: keys of one thread; 4 KS >= K.  A warp's four key slices interleave by
-// four keys, so that their 16-byte reads of a staged row are consecutive.
 template <class T, int KS>
 __global__ void __launch_bounds__(256) k_scan(LinLaunch l) {
-  constexpr int KP = 4 * KS;
-  const LinProblem& p = l.p[blockIdx.z];
-  __shared__ __align__(16) float s_a[kScanRows][KP], s_b[kScanRows][KP];
-  __shared__ float s_c[kScanRows][128];
+  __shared__ __align__(16) float s_rows[scan_floats(KS)];
   const LinSegment seg = lin_segment(l, blockIdx.x);
   if (seg.grid < 0) return;
-  const int h = blockIdx.y;
-  const bool want_out = p.out && l.phase != 1;
-  if (l.phase == 1 && seg.index + 1 == seg.count && !p.last) return;  // nobody reads this segment's state
-  const float decay = l.decay[h];
-  const int lane = threadIdx.x & 31, slice = lane & 3;
-  const int v0 = (threadIdx.x >> 5) * 16 + (lane >> 2) * 2;
-  const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
-  float* seg_state = p.seg ? p.seg + ((int64_t)blockIdx.x * l.heads + h) * p.K * p.V : nullptr;
-
-  f32x2 u[2][KS / 2];
-  auto key = [&](int i) { return (i / 4 * 4 + slice) * 4 + i % 4; };
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < KS; i += 2) {
-      float x[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = key(i + j), v = v0 + c;
-        x[j] = 0.f;
-        if (k < p.K && v < p.V) {
-          if (l.phase == 2) x[j] = seg_state[(int64_t)k * p.V + v];
-          else if (l.phase == 0 && p.first) x[j] = p.first[state_at + k * p.first_k + v * p.first_v];
-        }
-      }
-      u[c][i / 2] = pair(x[0], x[1]);
-    }
-
-  const int64_t origin = p.reverse ? seg.end - 1 - seg.first : seg.begin + seg.first;
-  const int64_t dir = p.reverse ? -1 : 1;
-  const f32x2 fold = pair(p.fold, p.fold);
-  for (int t0 = 0; t0 < seg.len; t0 += kScanRows) {
-    const int nt = min(kScanRows, seg.len - t0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * KP; i += blockDim.x) {
-      const int t = i / KP, k = i % KP;
-      const int64_t row = origin + dir * (t0 + t);
-      s_a[t][k] = want_out && k < p.K ? RowType<T>::to(((const T*)p.a)[row * p.a_row + h * p.a_head + k]) : 0.f;
-      s_b[t][k] = k < p.K ? RowType<T>::to(((const T*)p.b)[row * p.b_row + h * p.b_head + k]) : 0.f;
-    }
-    for (int i = threadIdx.x; i < nt * 128; i += blockDim.x) {
-      const int t = i / 128, v = i % 128;
-      const int64_t row = origin + dir * (t0 + t);
-      s_c[t][v] = v < p.V ? RowType<T>::to(((const T*)p.c)[row * p.c_row + h * p.c_head + v]) : 0.f;
-    }
-    __syncthreads();
-    for (int t = 0; t < nt; ++t) {
-      const float d = p.late && t0 + t == 0 ? 1.f : decay;
-      const f32x2 d2 = pair(d, d);
-      const f32x2 c0 = mul2(pair(s_c[t][v0], s_c[t][v0]), fold);
-      const f32x2 c1 = mul2(pair(s_c[t][v0 + 1], s_c[t][v0 + 1]), fold);
-      f32x2 o0 = 0ull, o1 = 0ull;
-#pragma unroll
-      for (int i = 0; i < KS; i += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(&s_b[t][(i + slice) * 4]);
-        const f32x2 b0 = pair(b.x, b.y), b1 = pair(b.z, b.w);
-        u[0][i / 2] = fma2(u[0][i / 2], d2, mul2(b0, c0));
-        u[1][i / 2] = fma2(u[1][i / 2], d2, mul2(b0, c1));
-        u[0][i / 2 + 1] = fma2(u[0][i / 2 + 1], d2, mul2(b1, c0));
-        u[1][i / 2 + 1] = fma2(u[1][i / 2 + 1], d2, mul2(b1, c1));
-        if (want_out) {
-          const float4 a = *reinterpret_cast<const float4*>(&s_a[t][(i + slice) * 4]);
-          const f32x2 a0 = pair(a.x, a.y), a1 = pair(a.z, a.w);
-          o0 = fma2(a0, u[0][i / 2], o0);
-          o1 = fma2(a0, u[1][i / 2], o1);
-          o0 = fma2(a1, u[0][i / 2 + 1], o0);
-          o1 = fma2(a1, u[1][i / 2 + 1], o1);
-        }
-      }
-      if (want_out) {
-        float x = halves(o0).x + halves(o0).y, y = halves(o1).x + halves(o1).y;
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        y += __shfl_xor_sync(0xffffffffu, y, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
-        y += __shfl_xor_sync(0xffffffffu, y, 2);
-        const int v = v0 + slice;
-        if (slice < 2 && v < p.V) {
-          const int64_t row = origin + dir * (t0 + t);
-          ((T*)p.out)[row * p.o_row + h * p.o_head + v] = RowType<T>::from((slice ? y : x) * p.mul);
-        }
-      }
-    }
-  }
-
-  float* dst = l.phase == 1 ? seg_state : l.phase == 0 && p.last ? p.last + state_at : nullptr;
-  if (!dst) return;
-  const float leave = p.late && seg.len > 0 ? decay : 1.f;
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < KS; i += 2) {
-      const float2 x = halves(u[c][i / 2]);
-      const int v = v0 + c;
-      if (v < p.V && key(i) < p.K) dst[(int64_t)key(i) * p.V + v] = x.x * leave;
-      if (v < p.V && key(i + 1) < p.K) dst[(int64_t)key(i + 1) * p.V + v] = x.y * leave;
-    }
+  scan_walk<T, KS>(l, l.p[blockIdx.z], seg, blockIdx.y, s_rows, blockDim.x);
 }
 
 constexpr int kCombineBatch = 16;

@@ -1,31 +1,40 @@
 // Linear attention with a decay for each head on the tensor cores: bfloat16
 // rows, heads of up to 128 keys and values, in chunks of 64 rows.
 //
-// Over a chunk of rows i, j (in the order of the walk) with entering state X:
-//   P_ij   = fold mul decay^(i-j) (a_i . b_j) for j <= i, else 0
-//   out_i  = sum_j P_ij c_j + mul decay^(i+e) a_i X       e = 1 forward, 0 reverse
-//   X'     = decay^n X + sum_j fold decay^(n-e-j) b_j c_j^T
-// Four products a chunk, each with the values (or, for P, the rows i) along
-// the 128 lanes of tensor memory:
-//   A B^T                   both operands in shared memory      -> P
-//   C^T P^T, X^T A^T        left operand in tensor memory       -> out^T
-//   (decayed C)^T B         left operand in tensor memory       -> X'^T - decay^n X^T
-// so that the state X^T stays in the registers of the threads of its lanes (a
-// value each), is multiplied by decay^n there in 32 bits, and goes back to
-// tensor memory as bfloat16 only as an operand.
+// Over a chunk of n rows (i, j count the rows in the order of the walk) with
+// entering state X, and with r = 31, e = 1 forward and 0 in reverse order:
+//   W_j   = fold decay^(r-j) c_j
+//   A_i   = sum_(j<=i) (a_i . b_j) W_j + a_i (decay^(r+e) X)
+//   out_i = mul decay^(i-r) A_i
+//   X'    = decay^n X + decay^(n-e-r) sum_j b_j W_j
+// The powers belong to single rows, so the scores a_i . b_j are only masked,
+// both parts of an output meet in one accumulator, and the state goes through
+// the chunks as Z = decay^(r+e) X, the operand itself: Z' = decay^64 (Z + B^T W).
+// Exponents run from -32 to 32, which 32 bits (and bfloat16) hold with room
+// for the values where the decay is in [kSteep, 1 / kSteep]; heads outside
+// that range forget within a few rows and take the recurrence.
 //
-// Roundings to 16 bits: P (as any attention's weights), X as an operand, and
-// the output; the decayed values are split into two bfloat16 terms (16 bits
-// of the product of a value and a power), or three (24 bits) where states are
-// an output, so the 32-bit states keep 32-bit accuracy.
+// Four products a chunk, each with the values (or, for the scores, the rows i)
+// along the 128 lanes of tensor memory:
+//   A B^T                     both operands in shared memory    -> scores
+//   Z^T A^T  +  W^T scores^T  left operands in tensor memory    -> A^T
+//   W^T B                     left operand in tensor memory     -> (B^T W)^T
+// so that the state Z^T stays in the registers of the threads of its lanes (a
+// value each), in 32 bits, and is rounded only as an operand.
+//
+// Roundings to 16 bits: the scores (as any attention's weights), Z as an
+// operand, and the output; W is split into two bfloat16 terms (16 bits of the
+// product of a value and a power), or three (24 bits) where states are an
+// output, so that 32-bit states keep 32-bit accuracy.
 //
 // A block walks one segment of one head: the copy engine fills a ring of row
-// tiles, one thread issues the products, and warps take the steps between
-// them -- state and decayed values (8 warps), P (2), output (4) -- each on
-// its own chunk, through barriers in shared memory.
+// tiles and empties the outputs', one thread issues the products, and warps
+// take the steps between them -- state and W (8 warps), scores (2), output (4)
+// -- each at its own chunk, through barriers in shared memory.
 #include <cstring>
 
 #include "tb_linattn.cuh"
+#include "tb_linattn_scan.cuh"
 #include "tb_seq.cuh"
 #include "tb_tc.cuh"
 
@@ -34,22 +43,25 @@ namespace {
 
 constexpr int kC = 64;            // rows of a chunk
 constexpr int kTile = 8192;       // 64 rows x 128 bytes
+constexpr int kOutTile = 4096;    // 64 rows x 64 bytes
 constexpr int kMaxStages = 4;
-// Warps: 8 of the state, the copies, the products, 2 of P, 4 of the output.
-// Sixteen leave 128 registers a thread, which hold the state of 128 keys
-// without spills (eighteen left 96, and the spills cost more than a third).
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpP = 10, kWarpOut = 12;
-constexpr int threads_of(bool states) { return (states ? kWarpP : 16) * 32; }
-
 constexpr int stages_of(int KP) { return KP == 64 ? 4 : 3; }
+// decay^32 within 2^50: half of the exponents that 32-bit floats have are left
+// to the values.
+constexpr float kSteep = 0.34f;
+// Warps: 8 of the state, the copies, the products, 2 of the scores, 4 of the
+// output.  Sixteen leave 128 registers a thread, which the state of 128 keys
+// and the blocks of W need.
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScores = 10, kWarpOut = 12;
+constexpr int threads_of(bool states) { return (states ? kWarpScores : 16) * 32; }
 
 // Set when a wait gave up (a bug, or a GPU that stands still): read and
-// cleared by launch_linear_status.
+// cleared by linear_gave_up.
 __device__ unsigned int g_gave_up;
 
 enum Bars {
-  kFull = 0, kEmpty = kFull + kMaxStages, kPReady = kEmpty + kMaxStages, kPFull = kPReady + 2, kWFull = kPFull + 2, kCFull,
-  kCFree = kCFull + 2, kKvReady = kCFree + 2, kKvFree, kStFull, kStFree, kOReady, kOFree, kZeros, kDrain, kBars
+  kFull = 0, kEmpty = kFull + kMaxStages, kSReady = kEmpty + kMaxStages, kSFull, kWFull, kWFree = kWFull + 2,
+  kKvReady = kWFree + 2, kKvFree, kStFull, kStFree, kOReady, kOFree = kOReady + 2, kZeros = kOFree + 2, kDrain, kBars
 };
 
 struct Shared {
@@ -58,10 +70,10 @@ struct Shared {
   volatile uint32_t gave_up;
   volatile uint32_t bad[kMaxStages];  // chunk + 1 whose values are not all finite
   LinSegment seg;
-  float pow[kC + 1];               // decay^n
-  float fold[2 * kC + 1];          // fold mul decay^(n - 64), 0 for n < 64
-  __align__(16) float up[kC];      // decay^(m+1), times fold (reverse) or mul (forward)
-  __align__(16) float down[4][2 * kC];  // decay^(63-m), 0 past m = 63: copy s starts at m = s
+  // powers for the rows of a chunk, 0 past the 64th; copy s starts at row s
+  __align__(8) float w[2][2 * kC + 2];  // fold decay^(31-m), reverse: fold decay^(m-32)
+  __align__(8) float o[2][2 * kC + 2];  // mul decay^(m-31), reverse: mul decay^(32-m)
+  uint2 w2[2][kC + 1];                  // rows 2 m and 2 m + 1 of w as bfloat16 pairs: the value, and what it leaves
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -69,48 +81,95 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 __device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-
 __device__ __forceinline__ float shared_bf16(uint32_t at) {
   uint16_t bits;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));
   return __uint_as_float((uint32_t)bits << 16);
 }
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+// Element x of row r in a tile of 64-element rows.
+__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int x) {
+  return tile + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + (x & 7) * 2;
+}
 
-// Adds P_ij c_j of the rows j whose value is not finite to the rows i that see
-// them, in a warp's staged output (the product had zeros in their place).
-__device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t p_tile, uint32_t c_tile, int n, bool reverse) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t col = (lane & 7) * 2;
-  const int warp_chunk = ((threadIdx.x >> 5) & 1) * 4 + (lane >> 3);  // the lane's 8 values within 64
+// Adds the scores times c_j of the rows j whose value is not finite to the
+// rows i that see them, in a warp's staged output of 32 values (the product
+// had zeros in their place).
+__device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t scores, uint32_t c_tile, int n, bool reverse) {
+  const int lane = threadIdx.x & 31, v = ((threadIdx.x >> 5) & 1) * 32 + lane;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
-    const float c = shared_bf16(c_tile + j * 128 + ((warp_chunk ^ (j & 7)) << 4) + col);
+    const float c = shared_bf16(tile_at(c_tile, j, v));
     if (!not_finite(c)) continue;
+#pragma unroll 1
     for (int i = reverse ? 0 : j; i <= (reverse ? j : n - 1); ++i) {
-      const uint32_t at = stage + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + col;
-      const float pij = shared_bf16(p_tile + i * 128 + (((j >> 3) ^ (i & 7)) << 4) + (j & 7) * 2);
-      const float o = fmaf(pij, c, shared_bf16(at));
+      const uint32_t at = stage + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2;
+      const float o = fmaf(shared_bf16(tile_at(scores, i, j)), c, shared_bf16(at));
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)(bf16x2(o, o) & 0xffffu)) : "memory");
     }
   }
+}
+
+// The same for the state: adds b_j c_j of those rows to (B^T W)^T in tensor
+// memory, the weights of a value that is not finite left out.  The columns
+// hold keys from `key` on; the lane's value is v % 64 of the tile.
+__device__ __noinline__ void add_not_finite_state(uint32_t columns, int keys, uint32_t b_tile, int key, uint32_t c_tile,
+                                                  int n) {
+  const int v = ((threadIdx.x >> 5) & 1) * 32 + (threadIdx.x & 31);
+#pragma unroll 1
+  for (int k0 = 0; k0 < keys; k0 += 16) {
+    uint32_t y[16];
+    tmem_ld16(columns + k0, y);
+    tmem_wait_ld();
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float c = shared_bf16(tile_at(c_tile, j, v));
+      if (!not_finite(c)) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = key + k0 + i;
+        y[i] = __float_as_uint(fmaf(shared_bf16(tile_at(b_tile + (k >> 6) * kTile, j, k & 63)), c, __uint_as_float(y[i])));
+      }
+    }
+    __syncwarp();
+    tmem_st16(columns + k0, y);
+  }
+  tmem_wait_st();
+}
+
+// The recurrence by the block's first 8 warps; apart, so that its registers are
+// not the chunks'.
+template <int KP>
+__device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, const LinSegment& seg, int h,
+                                       float* s_rows) {
+  scan_walk<__nv_bfloat16, KP / 4>(l, p, seg, h, s_rows, 256);
 }
 
 // KP: keys of a tile, 64 or 128 (fewer are padded with zeros by the copies).
 // kStates: the states of segments alone, without outputs.
 template <int KP, int kTerms, bool kStates>
 __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
-  constexpr int kCt = KP == 128 && kTerms == 3 ? 1 : 2;  // buffers of C^T in tensor memory
-  constexpr uint32_t kColP = 0, kColOi = 128, kColKv = 192, kColCt = kColKv + KP, kColW = kColCt + 32 * kCt,
-                     kColSt = kColW + 32 * kTerms;
-  static_assert(kColSt + KP / 2 <= 512, "tensor memory");
   constexpr int kBlocks = KP / 64, kStages = stages_of(KP);
+  constexpr int kWs = KP == 128 && kTerms == 3 ? 1 : 2;  // buffers of W^T in tensor memory
+  constexpr uint32_t kColS = 0, kColO = 64, kColKv = 192, kColW = kColKv + KP, kColZ = kColW + 32 * kTerms * kWs;
+  static_assert(kColZ + KP / 2 <= 512, "tensor memory");
   constexpr int kStageBytes = (2 * kBlocks + 2) * kTile;  // A, B, C
 
   extern __shared__ char s_raw[];
   __shared__ Shared s;
-  // two P tiles, then the stages (the product A B^T reads the 8 KB before A too)
+  // two score tiles, then the stages (the product A B^T reads the 8 KB before A too), then the outputs
   const uint32_t tiles = (smem_addr(s_raw) + 1023) & ~1023u;
   const uint32_t stage0 = tiles + 2 * kTile;
 
@@ -120,30 +179,30 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   const int h = blockIdx.y;
   auto bar = [&](int i) { return smem_addr(&s.bar[i]); };
   const bool reverse = p.reverse;
+  const float decay = l.decay[h];
 
   if (warp == 0) {
     const LinSegment seg = lin_segment(l, blockIdx.x);
     if (lane == 0) s.seg = seg;
   } else if (warp == 1) {
     if (lane == 0) {
-      for (int i = 0; i < kStages; ++i) {
+      for (int i = 0; i < kMaxStages; ++i) {
         mbar_init(bar(kFull + i), 1);
         mbar_init(bar(kEmpty + i), kStates ? 9 : 13);  // products, state warps, output warps
         s.bad[i] = 0;
       }
       for (int i = 0; i < 2; ++i) {
-        mbar_init(bar(kPReady + i), 1);
-        mbar_init(bar(kPFull + i), 2);
-        mbar_init(bar(kCFree + i), 1);
-        mbar_init(bar(kCFull + i), 8);
+        mbar_init(bar(kWFull + i), 8);
+        mbar_init(bar(kWFree + i), 1);
+        mbar_init(bar(kOReady + i), 1);
+        mbar_init(bar(kOFree + i), 4);
       }
-      mbar_init(bar(kWFull), 8);
+      mbar_init(bar(kSReady), 1);
+      mbar_init(bar(kSFull), 2);
       mbar_init(bar(kKvReady), 1);
       mbar_init(bar(kKvFree), 8);
       mbar_init(bar(kStFull), 8);
       mbar_init(bar(kStFree), 1);
-      mbar_init(bar(kOReady), 1);
-      mbar_init(bar(kOFree), 4);
       mbar_init(bar(kZeros), 8);
       mbar_init(bar(kDrain), 1);
       s.gave_up = 0;
@@ -152,16 +211,19 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   } else if (warp == kWarpMma) {
     tmem_alloc(smem_addr(&s.tmem), 512);
   } else if (warp >= 4 && warp < 8) {
-    const int i = threadIdx.x - 128;
-    const float d = l.decay[h];
-    if (i <= kC) {
-      const float x = lin_power(d, (float)i);
-      s.pow[i] = x;
-      s.fold[kC + i] = p.fold * p.mul * x;
-      if (i) s.up[i - 1] = x * (reverse ? p.fold : p.mul);
-    }
-    if (i < kC) s.fold[i] = 0.f;
-    for (int c = 0; c < 4; ++c) s.down[c][i] = i + c < kC ? lin_power(d, (float)(kC - 1 - i - c)) : 0.f;
+    const float log = log2f(decay);
+    for (int i = threadIdx.x - 128; i < 2 * kC + 2; i += 128)
+      for (int c = 0; c < 2; ++c) {
+        const int m = i + c;
+        const float x = reverse ? (float)(m - 32) : (float)(31 - m);
+        s.w[c][i] = m < kC ? p.fold * exp2f(x * log) : 0.f;
+        s.o[c][i] = m < kC ? p.mul * exp2f(-x * log) : 0.f;
+        if ((i & 1) == 0) {
+          const float y0 = s.w[c][i], y1 = m + 1 < kC ? p.fold * exp2f((reverse ? x + 1.f : x - 1.f) * log) : 0.f;
+          const uint32_t hi = bf16x2(y0, y1);
+          s.w2[c][i / 2] = make_uint2(hi, bf16x2(y0 - low(hi), y1 - high(hi)));
+        }
+      }
   }
   tc_fence_before();
   __syncthreads();
@@ -171,7 +233,8 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   const uint32_t tmem = s.tmem;
   // a slot without a segment, or a segment whose state nobody reads
   const bool idle = seg.grid < 0 || (kStates && seg.index + 1 == seg.count && !p.last);
-  const int chunks = idle ? 0 : (seg.len + kC - 1) / kC;
+  const bool steep = !(decay >= kSteep && decay <= 1.f / kSteep);
+  const int chunks = idle || steep ? 0 : (seg.len + kC - 1) / kC;
   auto rows_of = [&](int t) { return min(kC, seg.len - t * kC); };
   auto row_of = [&](int t) {
     return reverse ? seg.end - seg.first - (int64_t)t * kC - rows_of(t) : seg.begin + seg.first + (int64_t)t * kC;
@@ -185,25 +248,25 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   };
   const int value_blocks = p.V > 64 ? 2 : 1;
 
-  if (warp == kWarpTma) {
+  if (steep && !idle) {
+    if (warp < 8) walk_rows<KP>(l, p, s.seg, h, reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw))));
+  } else if (warp == kWarpTma) {
     if (elect_one()) {
       const CUtensorMap* ma = &g.map[g.a[blockIdx.z]];
       const CUtensorMap* mb = &g.map[g.b[blockIdx.z]];
       const CUtensorMap* mc = &g.map[g.c[blockIdx.z]];
-      tma_prefetch(ma);
-      tma_prefetch(mb);
-      tma_prefetch(mc);
       const uint32_t bytes = ((kStates ? 1 : 2) * kBlocks + value_blocks) * kTile;
       int t = 0;
+#pragma unroll 1
       for (; t < chunks; ++t) {
         const int st = t % kStages;
         if (t >= kStages && !mbar_wait(bar(kEmpty + st), (t / kStages - 1) & 1, &s.gave_up)) break;
         const uint32_t at = stage0 + st * kStageBytes;
         const int row = (int)row_of(t);
         mbar_expect(bar(kFull + st), bytes);
-        for (int i = 0; i < kBlocks; ++i) tma_load_3d(at + (kBlocks + i) * kTile, mb, 64 * i, h, row, bar(kFull + st));
         for (int i = 0; i < value_blocks; ++i)
           tma_load_3d(at + (2 * kBlocks + i) * kTile, mc, 64 * i, h, row, bar(kFull + st));
+        for (int i = 0; i < kBlocks; ++i) tma_load_3d(at + (kBlocks + i) * kTile, mb, 64 * i, h, row, bar(kFull + st));
         if (!kStates)
           for (int i = 0; i < kBlocks; ++i) tma_load_3d(at + i * kTile, ma, 64 * i, h, row, bar(kFull + st));
       }
@@ -216,62 +279,66 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     }
   } else if (warp == kWarpMma) {
     if (chunks && elect_one()) {
-      constexpr uint32_t kPDesc = mma_desc(128, kC, false);
+      constexpr uint32_t kRowDesc = mma_desc(128, kC, false);
       constexpr uint32_t kKvDesc = mma_desc(128, KP, true);
+      auto one = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1, &s.gave_up); };
       auto scores = [&](int t) {  // A B^T, rows i in lanes 64 to 127
         const uint32_t at = stage0 + t % kStages * kStageBytes;
 #pragma unroll
         for (int k = 0; k < KP / 16; ++k) {
           const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-          mma_ss(tmem + kColP + (t & 1) * 64, smem_desc(at - kTile + off, 16),
-                 smem_desc(at + kBlocks * kTile + off, 16), kPDesc, k > 0);
+          mma_ss(tmem + kColS, smem_desc(at - kTile + off, 16), smem_desc(at + kBlocks * kTile + off, 16), kRowDesc,
+                 k > 0);
         }
-        mma_commit(bar(kPReady + (t & 1)));
-      };
-      auto one = [&](int i, uint32_t parity) {
-        const bool ok = mbar_wait(bar(i), parity & 1, &s.gave_up);
-        tc_fence_after();
-        return ok;
+        mma_commit(bar(kSReady));
       };
       bool ok = one(kFull, 0);
+      if (ok && rows_of(0) < kC) ok = one(kZeros, 0);
+      tc_fence_after();
       if (ok && !kStates) scores(0);
+#pragma unroll 1
       for (int t = 0; ok && t < chunks; ++t) {
-        const uint32_t at = stage0 + t % kStages * kStageBytes;
-        if (!kStates && t + 1 < chunks) {
-          ok = one(kFull + (t + 1) % kStages, (t + 1) / kStages) && (t == 0 || one(kOFree, t - 1));
-          if (!ok) break;
-          scores(t + 1);
-        }
-        // (decayed C)^T B
-        ok = one(kFull + t % kStages, t / kStages) && one(kWFull, t) && (t == 0 || one(kKvFree, t - 1));
+        const int st = t % kStages, wb = t % kWs;
+        const uint32_t at = stage0 + st * kStageBytes;
+        const uint32_t w = tmem + kColW + wb * 32 * kTerms, o = tmem + kColO + (t & 1) * 64;
+        // W^T B (W full: the tile is)
+        ok = one(kWFull + wb, t / kWs) && (t == 0 || one(kKvFree, t - 1));
         if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColKv, tmem + kColW + term * 32 + j * 8, smem_desc(at + kBlocks * kTile + j * 2048, kTile),
-                   kKvDesc, term > 0 || j > 0);
+            mma_ts(tmem + kColKv, w + term * 32 + j * 8, smem_desc(at + kBlocks * kTile + j * 2048, kTile), kKvDesc,
+                   term > 0 || j > 0);
         mma_commit(bar(kKvReady));
         if (!kStates) {
-          // X^T A^T
-          ok = one(kStFull, t) && (t == 0 || one(kOFree, t - 1));
+          // Z^T A^T
+          ok = one(kStFull, t) && (t < 2 || one(kOFree + (t & 1), t / 2 - 1));
           if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int k = 0; k < KP / 16; ++k)
-            mma_ts(tmem + kColOi, tmem + kColSt + k * 8, smem_desc(at + (k >> 2) * kTile + (k & 3) * 32, 16), kPDesc,
-                   k > 0);
+            mma_ts(o, tmem + kColZ + k * 8, smem_desc(at + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, k > 0);
           mma_commit(bar(kStFree));
-          // C^T P^T
-          ok = one(kCFull + t % kCt, t / kCt) && one(kPFull + (t & 1), t >> 1);
+          // the next chunk's scores, once this chunk's are out of tensor memory
+          ok = one(kSFull, t) && (t + 1 >= chunks || one(kFull + (t + 1) % kStages, (t + 1) / kStages));
           if (!ok) break;
+          tc_fence_after();
+          if (t + 1 < chunks) {
+            if (rows_of(t + 1) < kC && !(ok = one(kZeros, 0))) break;
+            scores(t + 1);
+          }
+          // W^T scores^T (two terms of W are more than the scores have)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColP + (t & 1) * 64, tmem + kColCt + t % kCt * 32 + j * 8,
-                   smem_desc(tiles + (t & 1) * kTile + j * 32, 16), kPDesc, j > 0);
-          mma_commit(bar(kOReady));
-          mma_commit(bar(kCFree + t % kCt));
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_ts(o, w + term * 32 + j * 8, smem_desc(tiles + (t & 1) * kTile + j * 32, 16), kRowDesc, true);
+          mma_commit(bar(kOReady + (t & 1)));
         }
-        mma_commit(bar(kEmpty + t % kStages));
+        mma_commit(bar(kWFree + wb));
+        mma_commit(bar(kEmpty + st));
       }
       if (!ok) {  // products in flight finish before tensor memory is given back
         uint32_t flag = 0;
@@ -280,236 +347,259 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       }
     }
   } else if (warp < 8) {
-    // ------------------------------------------ state, decayed values, C^T
+    // ------------------------------------------------------------ state, W
     constexpr int NK = KP / 2;  // keys of a thread
-    const int half = warp >> 2, v = (warp & 3) * 32 + lane;
-    const bool live = (warp & 3) * 32 < p.V;  // warp-uniform
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    const int half = warp >> 2, quarter = warp & 3, v = quarter * 32 + lane;
+    const bool live = quarter * 32 < p.V;  // warp-uniform
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
     float* seg_state = p.seg ? p.seg + ((int64_t)blockIdx.x * l.heads + h) * p.K * p.V : nullptr;
-    float u[NK];
+    const float log = log2f(decay);
+    const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
+    f32x2 u[NK / 2];  // Z, by pairs of keys
+    {
+      const float* from = l.phase == 2 ? seg_state : p.first ? p.first + state_at : nullptr;
+      const int64_t step = l.phase == 2 ? p.V : p.first_k;
+      const int keys = kStates || idle || !from || v >= p.V ? 0 : p.K - half * NK;
+      if (from) from += half * NK * step + v * (l.phase == 2 ? 1 : p.first_v);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int k = half * NK + i;
-      u[i] = 0.f;
-      if (!kStates && !idle && k < p.K && v < p.V) {
-        if (l.phase == 2) u[i] = seg_state[(int64_t)k * p.V + v];
-        else if (p.first) u[i] = p.first[state_at + k * p.first_k + v * p.first_v];
-      }
+      for (int i = 0; i < NK; i += 2, from += 2 * step)
+        u[i / 2] = pair(i < keys ? from[0] * enter : 0.f, i + 1 < keys ? from[step] * enter : 0.f);
     }
-    for (int t = 0; t < chunks; ++t) {
-      const int st = t % kStages, n = rows_of(t);
-      const uint32_t at = stage0 + st * kStageBytes;
-      if (!wait(kFull + st, t / kStages)) break;
-      if (n < kC) {
-        // rows past the segment belong to others: no NaN of theirs may meet the zeros that their weights are
-        for (int i = threadIdx.x; i < (kBlocks + value_blocks) * (kC - n) * 8; i += 256) {
-          const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           at + (kBlocks + blk) * kTile + n * 128 + r * 16),
-                       "r"(0)
-                       : "memory");
-        }
-        fence_async_smem();
-        arrive(kZeros);  // once: only the last chunk is short
-        if (!wait(kZeros, 0)) break;
-      }
-      if (!kStates && t >= kCt && !wait(kCFree + t % kCt, t / kCt - 1)) break;
-      if (live) {
-        // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a value
-        const float* w = (reverse ? s.up : s.down[(kC - n) & 3] + ((kC - n) & ~3)) + half * 32 + 2 * (lane & 3);
-        float2 wv[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) wv[m] = *reinterpret_cast<const float2*>(w + 8 * m);
-        const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
-        const uint32_t rows = at + (2 * kBlocks + ((warp & 3) >> 1)) * kTile + r * 128;
-#pragma unroll
-        for (int g16 = 0; g16 < 2; ++g16) {
-          uint32_t ct[8], x[kTerms][8];
-          const uint32_t from = rows + ((((warp & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
-          ldmatrix_trans4(from, ct[0], ct[1], ct[2], ct[3]);
-          ldmatrix_trans4(from + 16 * 128, ct[4], ct[5], ct[6], ct[7]);
-          uint32_t finite = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(finite) : "r"(ct[i]), "r"(0));
-            float e0 = low(ct[i]) * wv[i / 2].x, e1 = high(ct[i]) * wv[i / 2].y;
-#pragma unroll
-            for (int term = 0; term < kTerms; ++term) {
-              x[term][i] = bf16x2(e0, e1);
-              e0 -= low(x[term][i]);
-              e1 -= high(x[term][i]);
-            }
+#pragma unroll 1
+    for (int t = -1; t < chunks; ++t) {
+      if (t + 1 < chunks) {
+        // ---- W of the next chunk
+        const int x = t + 1, st = x % kStages, n = rows_of(x);
+        const uint32_t at = stage0 + st * kStageBytes;
+        if (!wait(kFull + st, x / kStages)) break;
+        if (n < kC) {
+          // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
+#pragma unroll 1
+          for (int i = threadIdx.x; i < (kBlocks + value_blocks) * (kC - n) * 8; i += 256) {
+            const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             at + (kBlocks + blk) * kTile + n * 128 + r * 16),
+                         "r"(0)
+                         : "memory");
           }
-          const bool bad = not_finite(low(finite)) || not_finite(high(finite));
-          if (__any_sync(0xffffffffu, bad)) {
-            // 0 x infinity of a later row is no part of an earlier row's sum: the product takes zeros, and the
-            // output warps add these values to the rows that see them
+          fence_async_smem();
+          arrive(kZeros);  // once: only the last chunk is short
+          if (!wait(kZeros, 0)) break;
+        }
+        if (x >= kWs && !wait(kWFree + x % kWs, x / kWs - 1)) break;
+        tc_fence_after();
+        if (live) {
+          // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
+          // value
+          const int skip = reverse ? kC - n : 0;
+          const float* w = s.w[skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
+          const uint2* w2 = s.w2[skip & 1] + skip / 2 + half * 16 + (lane & 3);
+          const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
+          const uint32_t rows = at + (2 * kBlocks + (quarter >> 1)) * kTile + r * 128;
+#pragma unroll
+          for (int g16 = 0; g16 < 2; ++g16) {
+            uint32_t c[8], y[kTerms][8];
+            const uint32_t from = rows + ((((quarter & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+            ldmatrix_trans4(from, c[0], c[1], c[2], c[3]);
+            ldmatrix_trans4(from + 16 * 128, c[4], c[5], c[6], c[7]);
+            uint32_t finite = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) finite = fma_bf16x2(c[i], 0u, finite);
+            if (__any_sync(0xffffffffu, not_finite(low(finite)) || not_finite(high(finite)))) {
+              // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
+              // warps of the output and of the state add these values to what sees them
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (not_finite(low(c[i]))) c[i] &= 0xffff0000u;
+                if (not_finite(high(c[i]))) c[i] &= 0xffffu;
+              }
+              s.bad[st] = x + 1;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (not_finite(low(ct[i]))) ct[i] &= 0xffff0000u;
-              if (not_finite(high(ct[i]))) ct[i] &= 0xffffu;
-            }
-            s.bad[st] = t + 1;
-          }
-          const uint32_t to = lanes + ((uint32_t)g16 << 20) + half * 16;
+              if constexpr (kTerms == 2) {
+                // c (w + w') = hi + lo: hi = round(c w), c w - hi is exact in 16 bits
+                const uint2 wv = w2[(i / 2) * 4];
+                y[0][i] = mul_bf16x2(c[i], wv.x);
+                y[1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[0][i] ^ 0x80008000u));
+              } else {
+                const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
+                float e0 = low(c[i]) * wv.x, e1 = high(c[i]) * wv.y;
 #pragma unroll
-          for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + kColW + term * 32, x[term]);
-          if (!kStates) tmem_st_16x16(to + kColCt + t % kCt * 32, ct);
+                for (int term = 0; term < kTerms; ++term) {
+                  y[term][i] = bf16x2(e0, e1);
+                  e0 -= low(y[term][i]);
+                  e1 -= high(y[term][i]);
+                }
+              }
+            }
+            const uint32_t to = lanes + ((uint32_t)g16 << 20) + kColW + x % kWs * 32 * kTerms + half * 16;
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + term * 32, y[term]);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
+        tc_fence_before();
+        arrive(kWFull + x % kWs);
       }
-      tc_fence_before();
-      arrive(kWFull);
-      if (!kStates) arrive(kCFull + t % kCt);
-      arrive(kEmpty + st);
-      if (!kStates) {
-        // X^T, as an operand, for this chunk
-        if (t > 0 && !wait(kStFree, t - 1)) break;
+      if (t >= 0) {
+        // ---- the state after this chunk
+        const int st = t % kStages, n = rows_of(t);
+        if (!wait(kKvReady, t)) break;
+        tc_fence_after();
+        // after the last chunk the state itself: decay^n X + decay^(n-e-r) B^T W
+        const float d = t + 1 < chunks ? full : exp2f((float)(n - (reverse ? 31 : 32)) * log);
+        if (live) {
+          if (s.bad[st] == (uint32_t)t + 1) {
+            const uint32_t at = stage0 + st * kStageBytes;
+            add_not_finite_state(lanes + kColKv + half * NK, NK, at + kBlocks * kTile, half * NK,
+                                 at + (2 * kBlocks + (v >> 6)) * kTile, n);
+          }
+          const f32x2 d2 = pair(d, d);
+#pragma unroll
+          for (int k0 = 0; k0 < NK; k0 += 16) {
+            uint32_t y[16];
+            tmem_ld16(lanes + kColKv + half * NK + k0, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              u[(k0 + i) / 2] = mul2(add2(u[(k0 + i) / 2], pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1]))), d2);
+          }
+        }
+        tc_fence_before();
+        arrive(kKvFree);
+        arrive(kEmpty + st);
+      }
+      if (!kStates && t + 1 < chunks) {
+        // ---- Z^T as the next chunk's operand
+        if (t >= 0 && !wait(kStFree, t)) break;
+        tc_fence_after();
         if (live) {
 #pragma unroll
           for (int k0 = 0; k0 < NK; k0 += 32) {
-            uint32_t x[16];
+            uint32_t y[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = bf16x2(u[k0 + 2 * i], u[k0 + 2 * i + 1]);
-            tmem_st16(lanes + kColSt + (half * NK + k0) / 2, x);
+            for (int i = 0; i < 16; ++i) y[i] = bf16x2(halves(u[k0 / 2 + i]).x, halves(u[k0 / 2 + i]).y);
+            tmem_st16(lanes + kColZ + (half * NK + k0) / 2, y);
           }
           tmem_wait_st();
         }
         tc_fence_before();
         arrive(kStFull);
       }
-      if (!wait(kKvReady, t)) break;
-      tc_fence_after();
-      const float d = s.pow[n];
-      if (live) {
-#pragma unroll
-        for (int k0 = 0; k0 < NK; k0 += 16) {
-          uint32_t x[16];
-          tmem_ld16(lanes + kColKv + half * NK + k0, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) u[k0 + i] = fmaf(u[k0 + i], d, __uint_as_float(x[i]));
-        }
-      }
-      tc_fence_before();
-      arrive(kKvFree);
     }
     float* dst = kStates ? seg_state : l.phase == 0 && p.last ? p.last + state_at : nullptr;
     if (!idle && dst && !s.gave_up && v < p.V) {
+      dst += half * NK * p.V + v;
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const int k = half * NK + i;
-        if (k < p.K) dst[(int64_t)k * p.V + v] = u[i];
+      for (int i = 0; i < NK; i += 2, dst += 2 * p.V) {
+        if (i < p.K - half * NK) dst[0] = halves(u[i / 2]).x;
+        if (i + 1 < p.K - half * NK) dst[p.V] = halves(u[i / 2]).y;
       }
     }
   } else if (!kStates && warp < kWarpOut) {
-    // ------------------------------------------------------------------- P
+    // -------------------------------------------------------------- scores
+    // Rows past a segment's end need no mask: their b are zeros before the scores are computed, and rows i past it
+    // are not written.
     const int half = warp & 1, i = half * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    uint32_t diagonal[16];  // of pairs of columns in the 32 x 32 block on the diagonal
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      diagonal[j] = ((reverse ? 2 * j >= lane : 2 * j <= lane) ? 0xffffu : 0u) |
+                    ((reverse ? 2 * j + 1 >= lane : 2 * j + 1 <= lane) ? 0xffff0000u : 0u);
+#pragma unroll 1
     for (int t = 0; t < chunks; ++t) {
-      const int n = rows_of(t);
-      if (!wait(kPReady + (t & 1), t >> 1)) break;
+      if (!wait(kSReady, t)) break;
+      // the output warps may still read the tile's last scores where they add values that are not finite
+      if (t >= 2 && s.bad[(t - 2) % kStages] == (uint32_t)t - 1 && !wait(kOFree + (t & 1), t / 2 - 1)) break;
       tc_fence_after();
       const uint32_t row = tiles + (t & 1) * kTile + i * 128;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {  // columns 32 b to 32 b + 31
-        uint32_t x[32];
-        if (reverse ? b >= half : b <= half) {
-          tmem_ld32(lanes + kColP + (t & 1) * 64 + 32 * b, x);
+        const bool some = reverse ? b >= half : b <= half;
+        if (!some && t >= 2) continue;  // the tile's other half stays zero
+        uint32_t x[32], y[16];
+        if (some) {
+          tmem_ld32(lanes + kColS + 32 * b, x);
           tmem_wait_ld();
-          // fold[|i - j|]; on the diagonal block and past the rows the index may be negative, and P is 0
-          if (reverse) {
-            const float* w = s.fold + kC + 32 * b - i;
+        }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float f = __uint_as_float(x[j]) * w[j];
-              x[j] = 32 * b + j >= i && 32 * b + j < n ? __float_as_uint(f) : 0u;
-            }
-          } else {
-            const float* w = s.fold + kC + i - 32 * b;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float f = __uint_as_float(x[j]) * w[-j];
-              x[j] = b < half || j <= lane ? __float_as_uint(f) : 0u;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = 0u;
+        for (int j = 0; j < 16; ++j) {
+          y[j] = bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+          y[j] = !some ? 0u : b == half ? y[j] & diagonal[j] : y[j];
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((b * 4 + q) ^ (i & 7)) << 4)),
-                       "r"(bf16x2(__uint_as_float(x[8 * q]), __uint_as_float(x[8 * q + 1]))),
-                       "r"(bf16x2(__uint_as_float(x[8 * q + 2]), __uint_as_float(x[8 * q + 3]))),
-                       "r"(bf16x2(__uint_as_float(x[8 * q + 4]), __uint_as_float(x[8 * q + 5]))),
-                       "r"(bf16x2(__uint_as_float(x[8 * q + 6]), __uint_as_float(x[8 * q + 7])))
+                       "r"(y[4 * q]), "r"(y[4 * q + 1]), "r"(y[4 * q + 2]), "r"(y[4 * q + 3])
                        : "memory");
       }
       fence_async_smem();
       tc_fence_before();
-      arrive(kPFull + (t & 1));
+      arrive(kSFull);
     }
   } else if (!kStates) {
     // -------------------------------------------------------------- output
-    const bool live = (warp & 3) * 32 < p.V;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t out0 = stage0 + kStages * kStageBytes + (warp & 3) * 2 * 4096;  // two buffers of 64 rows x 64 bytes
+    const int quarter = warp & 3;
+    const bool live = quarter * 32 < p.V;
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+    const uint32_t out0 = stage0 + kStages * kStageBytes + quarter * 2 * kOutTile;
     const CUtensorMap* map = &g.map[kLinMaxRows + blockIdx.z];
+#pragma unroll 1
     for (int t = 0; t < chunks; ++t) {
       const int st = t % kStages, n = rows_of(t);
-      if (!wait(kOReady, t)) break;
+      if (!wait(kOReady + (t & 1), t >> 1)) break;
       tc_fence_after();
       if (live) {
-        const float* w = (reverse ? s.down[(kC - n) & 3] + ((kC - n) & ~3) : s.up) + 2 * (lane & 3);
+        const int skip = reverse ? kC - n : 0;
+        const float* w = s.o[skip & 1] + (skip & ~1) + 2 * (lane & 3);
         const bool bad = s.bad[st] == (uint32_t)t + 1;
-        const uint32_t buf = out0 + (t & 1) * 4096;
+        const uint32_t buf = out0 + (t & 1) * kOutTile;
+        const int row = (lane >> 4) * 8 + (lane & 7);
         if (lane == 0) tma_store_wait<1>();
         __syncwarp();
-        const int row = (lane >> 4) * 8 + (lane & 7);
+        uint32_t x[2][32];
+        tmem_ld_16x64(lanes + kColO + (t & 1) * 64, x[0]);
+        tmem_ld_16x64(lanes + (1u << 20) + kColO + (t & 1) * 64, x[1]);
+        tmem_wait_ld();
+        if (!bad) {
+          tc_fence_before();
+          arrive(kOFree + (t & 1));
+        }
 #pragma unroll
-        for (int g16 = 0; g16 < 2; ++g16) {
-          uint32_t x[32], y[32];
-          tmem_ld_16x64(lanes + ((uint32_t)g16 << 20) + kColP + (t & 1) * 64, x);
-          tmem_ld_16x64(lanes + ((uint32_t)g16 << 20) + kColOi, y);
-          tmem_wait_ld();
-          if (g16 == 1 && !bad) {
-            tc_fence_before();
-            arrive(kOFree);
-          }
-          const uint32_t to = buf + row * 64 + (((g16 * 2 + ((lane >> 3) & 1)) ^ ((row >> 1) & 3)) << 4);
-          uint32_t o[16];
+        for (int m = 0; m < 8; m += 2) {
+          const float2 w0 = *reinterpret_cast<const float2*>(w + 8 * m), w1 = *reinterpret_cast<const float2*>(w + 8 * m + 8);
+          const f32x2 w0p = pair(w0.x, w0.y), w1p = pair(w1.x, w1.y);
 #pragma unroll
-          for (int m = 0; m < 8; ++m) {
-            const float2 wv = *reinterpret_cast<const float2*>(w + 8 * m);
-            auto both = [&](int i) {
-              return bf16x2(fmaf(__uint_as_float(y[i]), wv.x, __uint_as_float(x[i])),
-                            fmaf(__uint_as_float(y[i + 1]), wv.y, __uint_as_float(x[i + 1])));
+          for (int g16 = 0; g16 < 2; ++g16) {
+            const uint32_t* y = x[g16] + 4 * m;
+            auto both = [&](int i, f32x2 wp) {
+              const float2 o = halves(mul2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), wp));
+              return bf16x2(o.x, o.y);
             };
-            o[2 * m] = both(4 * m);
-            o[2 * m + 1] = both(4 * m + 2);
+            stmatrix_trans4(buf + row * 64 + (((g16 * 2 + ((lane >> 3) & 1)) ^ ((row >> 1) & 3)) << 4) + m * 8 * 64,
+                            both(0, w0p), both(2, w0p), both(4, w1p), both(6, w1p));
           }
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            stmatrix_trans4(to + m * 16 * 64, o[4 * m], o[4 * m + 1], o[4 * m + 2], o[4 * m + 3]);
         }
         __syncwarp();
         if (bad) {
-          add_not_finite(buf, tiles + (t & 1) * kTile, stage0 + st * kStageBytes + (2 * kBlocks + ((warp & 3) >> 1)) * kTile,
+          add_not_finite(buf, tiles + (t & 1) * kTile, stage0 + st * kStageBytes + (2 * kBlocks + (quarter >> 1)) * kTile,
                          n, reverse);
           tc_fence_before();
-          arrive(kOFree);
+          arrive(kOFree + (t & 1));
         }
         const int64_t row0 = row_of(t);
         if (n == kC) {
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) tma_store_3d(map, (warp & 3) * 32, h, (int)row0, buf);
+          if (lane == 0) tma_store_3d(map, quarter * 32, h, (int)row0, buf);
         } else {
           // the rows that follow are not this segment's: plain stores
+#pragma unroll 1
           for (int i = lane; i < n * 4; i += 32) {
-            const int rr = i >> 2, v = (warp & 3) * 32 + (i & 3) * 8;
+            const int rr = i >> 2, v = quarter * 32 + (i & 3) * 8;
             uint4 o;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
@@ -519,7 +609,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         }
       } else {
         tc_fence_before();
-        arrive(kOFree);
+        arrive(kOFree + (t & 1));
       }
       arrive(kEmpty + st);
     }
@@ -535,7 +625,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
 
 template <int KP, int kTerms, bool kStates>
 cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
-  constexpr int bytes = 1024 + 2 * kTile + stages_of(KP) * (2 * (KP / 64) + 2) * kTile + (kStates ? 0 : 4 * 2 * 4096);
+  constexpr int bytes = 1024 + 2 * kTile + stages_of(KP) * (2 * (KP / 64) + 2) * kTile + (kStates ? 0 : 4 * 2 * kOutTile);
   static_assert(bytes > 116 * 1024 && bytes < 224 * 1024, "one block a multiprocessor: tensor memory is not shared");
   static bool ready[64];
   int dev = 0;

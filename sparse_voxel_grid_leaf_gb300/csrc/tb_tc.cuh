@@ -46,14 +46,17 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // *gave_up set, after kWaitPolls polls (a tenth of a second at least, where
 // a phase takes microseconds) or once another wait of the block gave up.
 constexpr uint32_t kWaitPolls = 1u << 22;
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
-  if (mbar_try(bar, parity)) return true;
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+#pragma unroll 1
   for (uint32_t i = 1; i < kWaitPolls; ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 255) == 0 && *gave_up) return false;
   }
   *gave_up = 1;
   return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+  return mbar_try(bar, parity) || mbar_wait_long(bar, parity, gave_up);
 }
 __device__ __forceinline__ void fence_mbar_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
