@@ -61,7 +61,7 @@ __device__ unsigned int g_gave_up;
 
 enum Bars {
   kFull = 0, kEmpty = kFull + kMaxStages, kSReady = kEmpty + kMaxStages, kSFull, kWFull, kWFree = kWFull + 2,
-  kKvReady = kWFree + 2, kKvFree, kStFull, kStFree, kOReady, kOFree = kOReady + 2, kZeros = kOFree + 2, kDrain, kBars
+  kKvReady = kWFree + 2, kKvFree = kKvReady + 2, kStFull = kKvFree + 2, kStFree, kOReady, kOFree = kOReady + 2, kZeros = kOFree + 2, kDrain, kBars
 };
 
 struct Shared {
@@ -162,8 +162,10 @@ __device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, 
 template <int KP, int kTerms, bool kStates>
 __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
   constexpr int kBlocks = KP / 64, kStages = stages_of(KP);
-  constexpr int kWs = KP == 128 && kTerms == 3 ? 1 : 2;  // buffers of W^T in tensor memory
-  constexpr uint32_t kColS = 0, kColO = 64, kColKv = 192, kColW = kColKv + KP, kColZ = kColW + 32 * kTerms * kWs;
+  // Buffers in tensor memory: of W^T, and of its product with B.
+  constexpr int kWs = !kStates && KP == 128 && kTerms == 3 ? 1 : 2, kKvs = kStates ? 2 : 1;
+  constexpr uint32_t kColS = 0, kColO = 64, kColKv = kStates ? 0 : 192, kColW = kColKv + KP * kKvs,
+                     kColZ = kColW + 32 * kTerms * kWs;
   static_assert(kColZ + KP / 2 <= 512, "tensor memory");
   constexpr int kStageBytes = (2 * kBlocks + 2) * kTile;  // A, B, C
 
@@ -194,13 +196,13 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(kWFull + i), 8);
         mbar_init(bar(kWFree + i), 1);
+        mbar_init(bar(kKvReady + i), 1);
+        mbar_init(bar(kKvFree + i), 8);
         mbar_init(bar(kOReady + i), 1);
         mbar_init(bar(kOFree + i), 4);
       }
       mbar_init(bar(kSReady), 1);
       mbar_init(bar(kSFull), 2);
-      mbar_init(bar(kKvReady), 1);
-      mbar_init(bar(kKvFree), 8);
       mbar_init(bar(kStFull), 8);
       mbar_init(bar(kStFree), 1);
       mbar_init(bar(kZeros), 8);
@@ -298,20 +300,20 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       if (ok && !kStates) scores(0);
 #pragma unroll 1
       for (int t = 0; ok && t < chunks; ++t) {
-        const int st = t % kStages, wb = t % kWs;
+        const int st = t % kStages, wb = t % kWs, kv = t % kKvs;
         const uint32_t at = stage0 + st * kStageBytes;
         const uint32_t w = tmem + kColW + wb * 32 * kTerms, o = tmem + kColO + (t & 1) * 64;
         // W^T B (W full: the tile is)
-        ok = one(kWFull + wb, t / kWs) && (t == 0 || one(kKvFree, t - 1));
+        ok = one(kWFull + wb, t / kWs) && (t < kKvs || one(kKvFree + kv, t / kKvs - 1));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColKv, w + term * 32 + j * 8, smem_desc(at + kBlocks * kTile + j * 2048, kTile), kKvDesc,
+            mma_ts(tmem + kColKv + kv * KP, w + term * 32 + j * 8, smem_desc(at + kBlocks * kTile + j * 2048, kTile), kKvDesc,
                    term > 0 || j > 0);
-        mma_commit(bar(kKvReady));
+        mma_commit(bar(kKvReady + kv));
         if (!kStates) {
           // Z^T A^T
           ok = one(kStFull, t) && (t < 2 || one(kOFree + (t & 1), t / 2 - 1));
@@ -446,21 +448,21 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       if (t >= 0) {
         // ---- the state after this chunk
         const int st = t % kStages, n = rows_of(t);
-        if (!wait(kKvReady, t)) break;
+        if (!wait(kKvReady + t % kKvs, t / kKvs)) break;
         tc_fence_after();
         // after the last chunk the state itself: decay^n X + decay^(n-e-r) B^T W
         const float d = t + 1 < chunks ? full : exp2f((float)(n - (reverse ? 31 : 32)) * log);
         if (live) {
           if (s.bad[st] == (uint32_t)t + 1) {
             const uint32_t at = stage0 + st * kStageBytes;
-            add_not_finite_state(lanes + kColKv + half * NK, NK, at + kBlocks * kTile, half * NK,
+            add_not_finite_state(lanes + kColKv + t % kKvs * KP + half * NK, NK, at + kBlocks * kTile, half * NK,
                                  at + (2 * kBlocks + (v >> 6)) * kTile, n);
           }
           const f32x2 d2 = pair(d, d);
 #pragma unroll
           for (int k0 = 0; k0 < NK; k0 += 16) {
             uint32_t y[16];
-            tmem_ld16(lanes + kColKv + half * NK + k0, y);
+            tmem_ld16(lanes + kColKv + t % kKvs * KP + half * NK + k0, y);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
           }
         }
         tc_fence_before();
-        arrive(kKvFree);
+        arrive(kKvFree + t % kKvs);
         arrive(kEmpty + st);
       }
       if (!kStates && t + 1 < chunks) {
