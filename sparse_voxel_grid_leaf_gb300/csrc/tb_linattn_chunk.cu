@@ -44,23 +44,24 @@ namespace {
 constexpr int kC = 64;            // rows of a chunk
 constexpr int kTile = 8192;       // 64 rows x 128 bytes
 constexpr int kOutTile = 4096;    // 64 rows x 64 bytes
-constexpr int kMaxStages = 4;
-constexpr int stages_of(int KP) { return KP == 64 ? 4 : 3; }
+constexpr int kStages = 3;
+constexpr int kStageBytes = 6 * kTile;  // two tiles each of A, B, C
 // decay^32 within 2^50: half of the exponents that 32-bit floats have are left
 // to the values.
 constexpr float kSteep = 0.34f;
-// Warps: 8 of the state, the copies, the products, 2 of the scores, 4 of the
-// output.  Sixteen leave 128 registers a thread, which the state of 128 keys
-// and the blocks of W need.
-constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScores = 10, kWarpOut = 12;
-constexpr int threads_of(bool states) { return (states ? kWarpScores : 16) * 32; }
+// Warps: 8 of the state, the copies, the products, 2 of the scores (lanes 64 to
+// 127), 4 of the output, and for pairs of heads 2 more of the scores.  Sixteen
+// leave 128 registers a thread, which the state of 128 keys and the blocks of W
+// need; pairs hold half as many keys.
+constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScores = 10, kWarpOut = 12, kWarpScores2 = 16;
+constexpr int threads_of(bool pair, bool states) { return (states ? kWarpScores : pair ? 18 : 16) * 32; }
 
 // Set when a wait gave up (a bug, or a GPU that stands still): read and
 // cleared by linear_gave_up.
 __device__ unsigned int g_gave_up;
 
 enum Bars {
-  kFull = 0, kEmpty = kFull + kMaxStages, kSReady = kEmpty + kMaxStages, kSFull, kWFull, kWFree = kWFull + 2,
+  kFull = 0, kEmpty = kFull + kStages, kSReady = kEmpty + kStages, kSFull, kWFull, kWFree = kWFull + 2,
   kKvReady = kWFree + 2, kKvFree = kKvReady + 2, kStFull = kKvFree + 2, kStFree, kOReady, kOFree = kOReady + 2, kZeros = kOFree + 2, kDrain, kBars
 };
 
@@ -68,12 +69,12 @@ struct Shared {
   uint64_t bar[kBars];
   uint32_t tmem;
   volatile uint32_t gave_up;
-  volatile uint32_t bad[kMaxStages];  // chunk + 1 whose values are not all finite
+  volatile uint32_t bad[kStages];  // chunk + 1 whose values are not all finite
   LinSegment seg;
-  // powers for the rows of a chunk, 0 past the 64th; copy s starts at row s
-  __align__(8) float w[2][2 * kC + 2];  // fold decay^(31-m), reverse: fold decay^(m-32)
-  __align__(8) float o[2][2 * kC + 2];  // mul decay^(m-31), reverse: mul decay^(32-m)
-  uint2 w2[2][kC + 1];                  // rows 2 m and 2 m + 1 of w as bfloat16 pairs: the value, and what it leaves
+  // powers for the rows of a chunk, 0 past the 64th; per head, copy s starts at row s
+  __align__(8) float w[2][2][2 * kC + 2];  // fold decay^(31-m), reverse: fold decay^(m-32)
+  __align__(8) float o[2][2][2 * kC + 2];  // mul decay^(m-31), reverse: mul decay^(32-m)
+  uint2 w2[2][2][kC + 1];                  // rows 2 m, 2 m + 1 of w as bfloat16 pairs: the value, and what it leaves
 };
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -151,44 +152,58 @@ __device__ __noinline__ void add_not_finite_state(uint32_t columns, int keys, ui
 
 // The recurrence by the block's first 8 warps; apart, so that its registers are
 // not the chunks'.
-template <int KP>
+template <int KS>
 __device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, const LinSegment& seg, int h,
                                        float* s_rows) {
-  scan_walk<__nv_bfloat16, KP / 4>(l, p, seg, h, s_rows, 256);
+  scan_walk<__nv_bfloat16, KS>(l, p, seg, h, s_rows, 256);
 }
 
-// KP: keys of a tile, 64 or 128 (fewer are padded with zeros by the copies).
+// kPair: two heads of up to 64 keys and values, one in each half of the 128
+// lanes.  Every product then takes both heads' tiles, which lie next to each
+// other, as 128 columns: a lane's own head is one half of its columns, the
+// other half is not read.  Else one head, of up to 128 (fewer keys and values
+// are padded with zeros by the copies).
 // kStates: the states of segments alone, without outputs.
-template <int KP, int kTerms, bool kStates>
-__global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
-  constexpr int kBlocks = KP / 64, kStages = stages_of(KP);
-  // Buffers in tensor memory: of W^T, and of its product with B.
-  constexpr int kWs = !kStates && KP == 128 && kTerms == 3 ? 1 : 2, kKvs = kStates ? 2 : 1;
-  constexpr uint32_t kColS = 0, kColO = 64, kColKv = kStates ? 0 : 192, kColW = kColKv + KP * kKvs,
+template <bool kPair, int kTerms, bool kStates>
+__global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
+  constexpr int kHeads = kPair ? 2 : 1;
+  constexpr int kKeys = kPair ? 64 : 128;                  // of a head
+  constexpr int kRows = kHeads * kC;                       // columns of the products over rows
+  // Buffers in tensor memory: of W^T, of its product with B, of the output.
+  constexpr int kWs = kStates || (!kPair && kTerms == 2) ? 2 : 1, kKvs = kStates ? 2 : 1, kOs = kPair ? 1 : 2;
+  constexpr uint32_t kColS = 0, kColO = kRows, kColKv = kStates ? 0 : kColO + kOs * kRows, kColW = kColKv + 128 * kKvs,
                      kColZ = kColW + 32 * kTerms * kWs;
-  static_assert(kColZ + KP / 2 <= 512, "tensor memory");
-  constexpr int kStageBytes = (2 * kBlocks + 2) * kTile;  // A, B, C
+  static_assert(kColZ + kKeys / 2 <= 512, "tensor memory");
 
   extern __shared__ char s_raw[];
   __shared__ Shared s;
-  // two score tiles, then the stages (the product A B^T reads the 8 KB before A too), then the outputs
+  // two score tiles for each head, then the stages (with one head the product A B^T reads the 8 KB before A too),
+  // then the outputs
   const uint32_t tiles = (smem_addr(s_raw) + 1023) & ~1023u;
-  const uint32_t stage0 = tiles + 2 * kTile;
+  const uint32_t stage0 = tiles + 2 * kHeads * kTile;
 
   const LinLaunch& l = g.l;
   const LinProblem& p = l.p[blockIdx.z];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int h = blockIdx.y;
+  const int h0 = blockIdx.y * kHeads;
   auto bar = [&](int i) { return smem_addr(&s.bar[i]); };
   const bool reverse = p.reverse;
-  const float decay = l.decay[h];
+  // The heads that go by chunks, and their decays; the recurrence takes the others that exist.
+  float decay[kHeads];
+  bool present[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const float d = h0 + i < l.heads ? l.decay[h0 + i] : 0.f;
+    present[i] = d >= kSteep && d <= 1.f / kSteep;
+    decay[i] = present[i] ? d : 1.f;
+  }
 
   if (warp == 0) {
     const LinSegment seg = lin_segment(l, blockIdx.x);
     if (lane == 0) s.seg = seg;
   } else if (warp == 1) {
     if (lane == 0) {
-      for (int i = 0; i < kMaxStages; ++i) {
+      for (int i = 0; i < kStages; ++i) {
         mbar_init(bar(kFull + i), 1);
         mbar_init(bar(kEmpty + i), kStates ? 9 : 13);  // products, state warps, output warps
         s.bad[i] = 0;
@@ -202,7 +217,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         mbar_init(bar(kOFree + i), 4);
       }
       mbar_init(bar(kSReady), 1);
-      mbar_init(bar(kSFull), 2);
+      mbar_init(bar(kSFull), kPair ? 4 : 2);
       mbar_init(bar(kStFull), 8);
       mbar_init(bar(kStFree), 1);
       mbar_init(bar(kZeros), 8);
@@ -213,19 +228,23 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   } else if (warp == kWarpMma) {
     tmem_alloc(smem_addr(&s.tmem), 512);
   } else if (warp >= 4 && warp < 8) {
-    const float log = log2f(decay);
-    for (int i = threadIdx.x - 128; i < 2 * kC + 2; i += 128)
-      for (int c = 0; c < 2; ++c) {
-        const int m = i + c;
+#pragma unroll
+    for (int hd = 0; hd < kHeads; ++hd) {
+      const float log = log2f(decay[hd]);
+#pragma unroll 1
+      for (int j = threadIdx.x - 128; j < 2 * (2 * kC + 2); j += 128) {
+        const int c = j & 1, i = j >> 1, m = i + c;
         const float x = reverse ? (float)(m - 32) : (float)(31 - m);
-        s.w[c][i] = m < kC ? p.fold * exp2f(x * log) : 0.f;
-        s.o[c][i] = m < kC ? p.mul * exp2f(-x * log) : 0.f;
+        const float w0 = m < kC ? p.fold * exp2f(x * log) : 0.f;
+        s.w[hd][c][i] = w0;
+        s.o[hd][c][i] = m < kC ? p.mul * exp2f(-x * log) : 0.f;
         if ((i & 1) == 0) {
-          const float y0 = s.w[c][i], y1 = m + 1 < kC ? p.fold * exp2f((reverse ? x + 1.f : x - 1.f) * log) : 0.f;
-          const uint32_t hi = bf16x2(y0, y1);
-          s.w2[c][i / 2] = make_uint2(hi, bf16x2(y0 - low(hi), y1 - high(hi)));
+          const float w1 = m + 1 < kC ? p.fold * exp2f((reverse ? x + 1.f : x - 1.f) * log) : 0.f;
+          const uint32_t hi = bf16x2(w0, w1);
+          s.w2[hd][c][i / 2] = make_uint2(hi, bf16x2(w0 - low(hi), w1 - high(hi)));
         }
       }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -235,8 +254,8 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   const uint32_t tmem = s.tmem;
   // a slot without a segment, or a segment whose state nobody reads
   const bool idle = seg.grid < 0 || (kStates && seg.index + 1 == seg.count && !p.last);
-  const bool steep = !(decay >= kSteep && decay <= 1.f / kSteep);
-  const int chunks = idle || steep ? 0 : (seg.len + kC - 1) / kC;
+  const bool any = present[0] || present[kHeads - 1];
+  const int chunks = idle || !any ? 0 : (seg.len + kC - 1) / kC;
   auto rows_of = [&](int t) { return min(kC, seg.len - t * kC); };
   auto row_of = [&](int t) {
     return reverse ? seg.end - seg.first - (int64_t)t * kC - rows_of(t) : seg.begin + seg.first + (int64_t)t * kC;
@@ -248,16 +267,19 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(i));
   };
-  const int value_blocks = p.V > 64 ? 2 : 1;
+  const int value_tiles = kPair || p.V > 64 ? 2 : 1;
+  // A quarter of the lanes: its head, its first value there, whether it has any.
+  const int quarter = warp & 3, head = kPair ? quarter >> 1 : 0, value0 = (kPair ? quarter & 1 : quarter) * 32;
+  const bool live = (kPair && head ? present[kHeads - 1] : present[0]) && value0 < p.V;
+  const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+  const int h = h0 + head;
 
-  if (steep && !idle) {
-    if (warp < 8) walk_rows<KP>(l, p, s.seg, h, reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw))));
-  } else if (warp == kWarpTma) {
+  if (warp == kWarpTma) {
     if (elect_one()) {
       const CUtensorMap* ma = &g.map[g.a[blockIdx.z]];
       const CUtensorMap* mb = &g.map[g.b[blockIdx.z]];
       const CUtensorMap* mc = &g.map[g.c[blockIdx.z]];
-      const uint32_t bytes = ((kStates ? 1 : 2) * kBlocks + value_blocks) * kTile;
+      const uint32_t bytes = ((kStates ? 2 : 4) + value_tiles) * kTile;
       int t = 0;
 #pragma unroll 1
       for (; t < chunks; ++t) {
@@ -266,11 +288,13 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         const uint32_t at = stage0 + st * kStageBytes;
         const int row = (int)row_of(t);
         mbar_expect(bar(kFull + st), bytes);
-        for (int i = 0; i < value_blocks; ++i)
-          tma_load_3d(at + (2 * kBlocks + i) * kTile, mc, 64 * i, h, row, bar(kFull + st));
-        for (int i = 0; i < kBlocks; ++i) tma_load_3d(at + (kBlocks + i) * kTile, mb, 64 * i, h, row, bar(kFull + st));
+        auto load = [&](int tile, const CUtensorMap* map, int i) {
+          tma_load_3d(at + (tile + i) * kTile, map, kPair ? 0 : 64 * i, kPair ? h0 + i : h0, row, bar(kFull + st));
+        };
+        for (int i = 0; i < value_tiles; ++i) load(4, mc, i);
+        for (int i = 0; i < 2; ++i) load(2, mb, i);
         if (!kStates)
-          for (int i = 0; i < kBlocks; ++i) tma_load_3d(at + i * kTile, ma, 64 * i, h, row, bar(kFull + st));
+          for (int i = 0; i < 2; ++i) load(0, ma, i);
       }
       if (s.gave_up) {  // copies in flight land before the block ends
         for (int i = t > kStages ? t - kStages : 0; i < t; ++i) {
@@ -281,15 +305,17 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     }
   } else if (warp == kWarpMma) {
     if (chunks && elect_one()) {
-      constexpr uint32_t kRowDesc = mma_desc(128, kC, false);
-      constexpr uint32_t kKvDesc = mma_desc(128, KP, true);
+      constexpr uint32_t kRowDesc = mma_desc(128, kRows, false);
+      constexpr uint32_t kKvDesc = mma_desc(128, 128, true);
       auto one = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1, &s.gave_up); };
-      auto scores = [&](int t) {  // A B^T, rows i in lanes 64 to 127
+      // A B^T: the rows of one head in lanes 64 to 127 (lanes 0 to 63 get whatever lies before A), of two heads in
+      // 0 to 63 and 64 to 127
+      auto scores = [&](int t) {
         const uint32_t at = stage0 + t % kStages * kStageBytes;
 #pragma unroll
-        for (int k = 0; k < KP / 16; ++k) {
+        for (int k = 0; k < kKeys / 16; ++k) {
           const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-          mma_ss(tmem + kColS, smem_desc(at - kTile + off, 16), smem_desc(at + kBlocks * kTile + off, 16), kRowDesc,
+          mma_ss(tmem + kColS, smem_desc(at - (kPair ? 0 : kTile) + off, 16), smem_desc(at + 2 * kTile + off, 16), kRowDesc,
                  k > 0);
         }
         mma_commit(bar(kSReady));
@@ -302,7 +328,8 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       for (int t = 0; ok && t < chunks; ++t) {
         const int st = t % kStages, wb = t % kWs, kv = t % kKvs;
         const uint32_t at = stage0 + st * kStageBytes;
-        const uint32_t w = tmem + kColW + wb * 32 * kTerms, o = tmem + kColO + (t & 1) * 64;
+        const int ob = t % kOs;
+        const uint32_t w = tmem + kColW + wb * 32 * kTerms, o = tmem + kColO + ob * kRows;
         // W^T B (W full: the tile is)
         ok = one(kWFull + wb, t / kWs) && (t < kKvs || one(kKvFree + kv, t / kKvs - 1));
         if (!ok) break;
@@ -311,16 +338,16 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColKv + kv * KP, w + term * 32 + j * 8, smem_desc(at + kBlocks * kTile + j * 2048, kTile), kKvDesc,
+            mma_ts(tmem + kColKv + kv * 128, w + term * 32 + j * 8, smem_desc(at + 2 * kTile + j * 2048, kTile), kKvDesc,
                    term > 0 || j > 0);
         mma_commit(bar(kKvReady + kv));
         if (!kStates) {
           // Z^T A^T
-          ok = one(kStFull, t) && (t < 2 || one(kOFree + (t & 1), t / 2 - 1));
+          ok = one(kStFull, t) && (t < kOs || one(kOFree + ob, t / kOs - 1));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < KP / 16; ++k)
+          for (int k = 0; k < kKeys / 16; ++k)
             mma_ts(o, tmem + kColZ + k * 8, smem_desc(at + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, k > 0);
           mma_commit(bar(kStFree));
           // the next chunk's scores, once this chunk's are out of tensor memory
@@ -336,8 +363,8 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_ts(o, w + term * 32 + j * 8, smem_desc(tiles + (t & 1) * kTile + j * 32, 16), kRowDesc, true);
-          mma_commit(bar(kOReady + (t & 1)));
+              mma_ts(o, w + term * 32 + j * 8, smem_desc(tiles + (t & 1) * kHeads * kTile + j * 32, 16), kRowDesc, true);
+          mma_commit(bar(kOReady + ob));
         }
         mma_commit(bar(kWFree + wb));
         mma_commit(bar(kEmpty + st));
@@ -350,19 +377,17 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------ state, W
-    constexpr int NK = KP / 2;  // keys of a thread
-    const int half = warp >> 2, quarter = warp & 3, v = quarter * 32 + lane;
-    const bool live = quarter * 32 < p.V;  // warp-uniform
-    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+    constexpr int NK = kKeys / 2;  // keys of a thread
+    const int half = warp >> 2, v = value0 + lane;
     const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
     float* seg_state = p.seg ? p.seg + ((int64_t)blockIdx.x * l.heads + h) * p.K * p.V : nullptr;
-    const float log = log2f(decay);
+    const float log = log2f(kPair && head ? decay[kHeads - 1] : decay[0]);
     const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
     f32x2 u[NK / 2];  // Z, by pairs of keys
     {
       const float* from = l.phase == 2 ? seg_state : p.first ? p.first + state_at : nullptr;
       const int64_t step = l.phase == 2 ? p.V : p.first_k;
-      const int keys = kStates || idle || !from || v >= p.V ? 0 : p.K - half * NK;
+      const int keys = kStates || idle || !live || !from || v >= p.V ? 0 : p.K - half * NK;
       if (from) from += half * NK * step + v * (l.phase == 2 ? 1 : p.first_v);
 #pragma unroll
       for (int i = 0; i < NK; i += 2, from += 2 * step)
@@ -378,10 +403,10 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         if (n < kC) {
           // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
 #pragma unroll 1
-          for (int i = threadIdx.x; i < (kBlocks + value_blocks) * (kC - n) * 8; i += 256) {
+          for (int i = threadIdx.x; i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
             const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             at + (kBlocks + blk) * kTile + n * 128 + r * 16),
+                             at + (2 + blk) * kTile + n * 128 + r * 16),
                          "r"(0)
                          : "memory");
           }
@@ -395,10 +420,10 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
           // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
           // value
           const int skip = reverse ? kC - n : 0;
-          const float* w = s.w[skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
-          const uint2* w2 = s.w2[skip & 1] + skip / 2 + half * 16 + (lane & 3);
+          const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
+          const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
           const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
-          const uint32_t rows = at + (2 * kBlocks + (quarter >> 1)) * kTile + r * 128;
+          const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
 #pragma unroll
           for (int g16 = 0; g16 < 2; ++g16) {
             uint32_t c[8], y[kTerms][8];
@@ -455,14 +480,14 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         if (live) {
           if (s.bad[st] == (uint32_t)t + 1) {
             const uint32_t at = stage0 + st * kStageBytes;
-            add_not_finite_state(lanes + kColKv + t % kKvs * KP + half * NK, NK, at + kBlocks * kTile, half * NK,
-                                 at + (2 * kBlocks + (v >> 6)) * kTile, n);
+            add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (2 + head) * kTile,
+                                 half * NK, at + (4 + (quarter >> 1)) * kTile, n);
           }
           const f32x2 d2 = pair(d, d);
 #pragma unroll
           for (int k0 = 0; k0 < NK; k0 += 16) {
             uint32_t y[16];
-            tmem_ld16(lanes + kColKv + t % kKvs * KP + half * NK + k0, y);
+            tmem_ld16(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK + k0, y);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; i += 2)
@@ -492,7 +517,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
       }
     }
     float* dst = kStates ? seg_state : l.phase == 0 && p.last ? p.last + state_at : nullptr;
-    if (!idle && dst && !s.gave_up && v < p.V) {
+    if (!idle && live && dst && !s.gave_up && v < p.V) {
       dst += half * NK * p.V + v;
 #pragma unroll
       for (int i = 0; i < NK; i += 2, dst += 2 * p.V) {
@@ -500,12 +525,11 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         if (i + 1 < p.K - half * NK) dst[p.V] = halves(u[i / 2]).y;
       }
     }
-  } else if (!kStates && warp < kWarpOut) {
+  } else if (!kStates && (warp < kWarpOut || warp >= kWarpScores2)) {
     // -------------------------------------------------------------- scores
     // Rows past a segment's end need no mask: their b are zeros before the scores are computed, and rows i past it
     // are not written.
     const int half = warp & 1, i = half * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
     uint32_t diagonal[16];  // of pairs of columns in the 32 x 32 block on the diagonal
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -515,16 +539,16 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     for (int t = 0; t < chunks; ++t) {
       if (!wait(kSReady, t)) break;
       // the output warps may still read the tile's last scores where they add values that are not finite
-      if (t >= 2 && s.bad[(t - 2) % kStages] == (uint32_t)t - 1 && !wait(kOFree + (t & 1), t / 2 - 1)) break;
+      if (t >= 2 && s.bad[(t - 2) % kStages] == (uint32_t)t - 1 && !wait(kOFree + t % kOs, t / kOs - 1)) break;
       tc_fence_after();
-      const uint32_t row = tiles + (t & 1) * kTile + i * 128;
+      const uint32_t row = tiles + ((t & 1) * kHeads + head) * kTile + i * 128;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {  // columns 32 b to 32 b + 31
         const bool some = reverse ? b >= half : b <= half;
         if (!some && t >= 2) continue;  // the tile's other half stays zero
         uint32_t x[32], y[16];
         if (some) {
-          tmem_ld32(lanes + kColS + 32 * b, x);
+          tmem_ld32(lanes + kColS + head * 64 + 32 * b, x);
           tmem_wait_ld();
         }
 #pragma unroll
@@ -544,31 +568,29 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
     }
   } else if (!kStates) {
     // -------------------------------------------------------------- output
-    const int quarter = warp & 3;
-    const bool live = quarter * 32 < p.V;
-    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
     const uint32_t out0 = stage0 + kStages * kStageBytes + quarter * 2 * kOutTile;
     const CUtensorMap* map = &g.map[kLinMaxRows + blockIdx.z];
 #pragma unroll 1
     for (int t = 0; t < chunks; ++t) {
       const int st = t % kStages, n = rows_of(t);
-      if (!wait(kOReady + (t & 1), t >> 1)) break;
+      if (!wait(kOReady + t % kOs, t / kOs)) break;
       tc_fence_after();
       if (live) {
         const int skip = reverse ? kC - n : 0;
-        const float* w = s.o[skip & 1] + (skip & ~1) + 2 * (lane & 3);
+        const float* w = s.o[head][skip & 1] + (skip & ~1) + 2 * (lane & 3);
         const bool bad = s.bad[st] == (uint32_t)t + 1;
         const uint32_t buf = out0 + (t & 1) * kOutTile;
         const int row = (lane >> 4) * 8 + (lane & 7);
         if (lane == 0) tma_store_wait<1>();
         __syncwarp();
         uint32_t x[2][32];
-        tmem_ld_16x64(lanes + kColO + (t & 1) * 64, x[0]);
-        tmem_ld_16x64(lanes + (1u << 20) + kColO + (t & 1) * 64, x[1]);
+        const uint32_t from = lanes + kColO + t % kOs * kRows + head * 64;
+        tmem_ld_16x64(from, x[0]);
+        tmem_ld_16x64(from + (1u << 20), x[1]);
         tmem_wait_ld();
         if (!bad) {
           tc_fence_before();
-          arrive(kOFree + (t & 1));
+          arrive(kOFree + t % kOs);
         }
 #pragma unroll
         for (int m = 0; m < 8; m += 2) {
@@ -587,21 +609,21 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         }
         __syncwarp();
         if (bad) {
-          add_not_finite(buf, tiles + (t & 1) * kTile, stage0 + st * kStageBytes + (2 * kBlocks + (quarter >> 1)) * kTile,
-                         n, reverse);
+          add_not_finite(buf, tiles + ((t & 1) * kHeads + head) * kTile,
+                         stage0 + st * kStageBytes + (4 + (quarter >> 1)) * kTile, n, reverse);
           tc_fence_before();
-          arrive(kOFree + (t & 1));
+          arrive(kOFree + t % kOs);
         }
         const int64_t row0 = row_of(t);
         if (n == kC) {
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) tma_store_3d(map, quarter * 32, h, (int)row0, buf);
+          if (lane == 0) tma_store_3d(map, value0, h, (int)row0, buf);
         } else {
           // the rows that follow are not this segment's: plain stores
 #pragma unroll 1
           for (int i = lane; i < n * 4; i += 32) {
-            const int rr = i >> 2, v = quarter * 32 + (i & 3) * 8;
+            const int rr = i >> 2, v = value0 + (i & 3) * 8;
             uint4 o;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
@@ -611,7 +633,7 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
         }
       } else {
         tc_fence_before();
-        arrive(kOFree + (t & 1));
+        arrive(kOFree + t % kOs);
       }
       arrive(kEmpty + st);
     }
@@ -623,23 +645,28 @@ __global__ void __launch_bounds__(threads_of(kStates), 1) k_chunks(const __grid_
   tc_fence_after();
   if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
   if (warp == kWarpMma) tmem_free(tmem, 512);
+  if (idle || warp >= 8) return;
+#pragma unroll 1
+  for (int i = 0; i < kHeads; ++i)
+    if (!(i ? present[kHeads - 1] : present[0]) && h0 + i < l.heads)
+      walk_rows<kKeys / 4>(l, p, s.seg, h0 + i, reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw))));
 }
 
-template <int KP, int kTerms, bool kStates>
+template <bool kPair, int kTerms, bool kStates>
 cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
-  constexpr int bytes = 1024 + 2 * kTile + stages_of(KP) * (2 * (KP / 64) + 2) * kTile + (kStates ? 0 : 4 * 2 * kOutTile);
-  static_assert(bytes > 116 * 1024 && bytes < 224 * 1024, "one block a multiprocessor: tensor memory is not shared");
+  constexpr int bytes = 1024 + (kPair ? 4 : 2) * kTile + kStages * kStageBytes + (kStates ? 0 : 4 * 2 * kOutTile);
+  static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
   static bool ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_chunks<KP, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(k_chunks<kPair, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  const dim3 grid(g.l.segments, g.l.heads, g.l.n);
-  k_chunks<KP, kTerms, kStates><<<grid, threads_of(kStates), bytes, s>>>(g);
+  const dim3 grid(g.l.segments, kPair ? (g.l.heads + 1) / 2 : g.l.heads, g.l.n);
+  k_chunks<kPair, kTerms, kStates><<<grid, threads_of(kPair, kStates), bytes, s>>>(g);
   return cudaGetLastError();
 }
 
@@ -712,18 +739,18 @@ bool linear_chunk_plan(ChunkLaunch& g) {
 
 cudaError_t launch_linear_chunks(const void* args, cudaStream_t s) {
   const ChunkLaunch& g = *(const ChunkLaunch*)args;
-  bool wide = false, exact = false;
+  bool pair = g.l.heads > 1, exact = false;
   for (int i = 0; i < g.l.n; ++i) {
-    wide = wide || g.l.p[i].K > 64;
+    pair = pair && g.l.p[i].K <= 64 && g.l.p[i].V <= 64;
     exact = exact || g.l.p[i].last;
   }
   if (g.l.phase == 1) {
-    if (wide) return exact ? go<128, 3, true>(g, s) : go<128, 2, true>(g, s);
-    return exact ? go<64, 3, true>(g, s) : go<64, 2, true>(g, s);
+    if (pair) return exact ? go<true, 3, true>(g, s) : go<true, 2, true>(g, s);
+    return exact ? go<false, 3, true>(g, s) : go<false, 2, true>(g, s);
   }
   if (g.l.phase == 2) exact = false;  // the states that leave come from phase 1
-  if (wide) return exact ? go<128, 3, false>(g, s) : go<128, 2, false>(g, s);
-  return exact ? go<64, 3, false>(g, s) : go<64, 2, false>(g, s);
+  if (pair) return exact ? go<true, 3, false>(g, s) : go<true, 2, false>(g, s);
+  return exact ? go<false, 3, false>(g, s) : go<false, 2, false>(g, s);
 }
 
 cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up) {
