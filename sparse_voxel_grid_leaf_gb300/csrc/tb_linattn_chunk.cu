@@ -352,12 +352,10 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
           mma_commit(bar(kStFree));
           // the next chunk's scores, once this chunk's are out of tensor memory
           ok = one(kSFull, t) && (t + 1 >= chunks || one(kFull + (t + 1) % kStages, (t + 1) / kStages));
+          if (ok && t + 1 < chunks && rows_of(t + 1) < kC) ok = one(kZeros, 0);
           if (!ok) break;
           tc_fence_after();
-          if (t + 1 < chunks) {
-            if (rows_of(t + 1) < kC && !(ok = one(kZeros, 0))) break;
-            scores(t + 1);
-          }
+          if (kWs == 2 && t + 1 < chunks) scores(t + 1);
           // W^T scores^T (two terms of W are more than the scores have)
 #pragma unroll
           for (int term = 0; term < 2; ++term)
@@ -367,6 +365,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
           mma_commit(bar(kOReady + ob));
         }
         mma_commit(bar(kWFree + wb));
+        if (kWs == 1 && !kStates && t + 1 < chunks) scores(t + 1);  // after what frees W^T
         mma_commit(bar(kEmpty + st));
       }
       if (!ok) {  // products in flight finish before tensor memory is given back
@@ -393,128 +392,150 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       for (int i = 0; i < NK; i += 2, from += 2 * step)
         u[i / 2] = pair(i < keys ? from[0] * enter : 0.f, i + 1 < keys ? from[step] * enter : 0.f);
     }
+    // W^T of chunk x: its terms in registers, then in tensor memory.
+    uint32_t y[2][kTerms][8];
+    auto make_w = [&](int x) {
+      const int st = x % kStages, n = rows_of(x);
+      const uint32_t at = stage0 + st * kStageBytes;
+      if (!wait(kFull + st, x / kStages)) return false;
+      if (n < kC) {
+        // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
 #pragma unroll 1
-    for (int t = -1; t < chunks; ++t) {
-      if (t + 1 < chunks) {
-        // ---- W of the next chunk
-        const int x = t + 1, st = x % kStages, n = rows_of(x);
-        const uint32_t at = stage0 + st * kStageBytes;
-        if (!wait(kFull + st, x / kStages)) break;
-        if (n < kC) {
-          // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
-#pragma unroll 1
-          for (int i = threadIdx.x; i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
-            const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             at + (2 + blk) * kTile + n * 128 + r * 16),
-                         "r"(0)
-                         : "memory");
-          }
-          fence_async_smem();
-          arrive(kZeros);  // once: only the last chunk is short
-          if (!wait(kZeros, 0)) break;
+        for (int i = threadIdx.x; i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
+          const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           at + (2 + blk) * kTile + n * 128 + r * 16),
+                       "r"(0)
+                       : "memory");
         }
-        if (x >= kWs && !wait(kWFree + x % kWs, x / kWs - 1)) break;
-        tc_fence_after();
-        if (live) {
-          // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
-          // value
-          const int skip = reverse ? kC - n : 0;
-          const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
-          const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
-          const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
-          const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
+        fence_async_smem();
+        arrive(kZeros);  // once: only the last chunk is short
+        if (!wait(kZeros, 0)) return false;
+      }
+      if (live) {
+        // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
+        // value
+        const int skip = reverse ? kC - n : 0;
+        const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
+        const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
+        const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
+        const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
 #pragma unroll
-          for (int g16 = 0; g16 < 2; ++g16) {
-            uint32_t c[8], y[kTerms][8];
-            const uint32_t from = rows + ((((quarter & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
-            ldmatrix_trans4(from, c[0], c[1], c[2], c[3]);
-            ldmatrix_trans4(from + 16 * 128, c[4], c[5], c[6], c[7]);
-            uint32_t finite = 0;
+        for (int g16 = 0; g16 < 2; ++g16) {
+          uint32_t c[8];
+          const uint32_t from = rows + ((((quarter & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+          ldmatrix_trans4(from, c[0], c[1], c[2], c[3]);
+          ldmatrix_trans4(from + 16 * 128, c[4], c[5], c[6], c[7]);
+          uint32_t finite = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) finite = fma_bf16x2(c[i], 0u, finite);
-            if (__any_sync(0xffffffffu, not_finite(low(finite)) || not_finite(high(finite)))) {
-              // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
-              // warps of the output and of the state add these values to what sees them
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (not_finite(low(c[i]))) c[i] &= 0xffff0000u;
-                if (not_finite(high(c[i]))) c[i] &= 0xffffu;
-              }
-              s.bad[st] = x + 1;
-            }
+          for (int i = 0; i < 8; ++i) finite = fma_bf16x2(c[i], 0u, finite);
+          if (__any_sync(0xffffffffu, not_finite(low(finite)) || not_finite(high(finite)))) {
+            // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
+            // warps of the output and of the state add these values to what sees them
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if constexpr (kTerms == 2) {
-                // c (w + w') = hi + lo: hi = round(c w), c w - hi is exact in 16 bits
-                const uint2 wv = w2[(i / 2) * 4];
-                y[0][i] = mul_bf16x2(c[i], wv.x);
-                y[1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[0][i] ^ 0x80008000u));
-              } else {
-                const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
-                float e0 = low(c[i]) * wv.x, e1 = high(c[i]) * wv.y;
+              if (not_finite(low(c[i]))) c[i] &= 0xffff0000u;
+              if (not_finite(high(c[i]))) c[i] &= 0xffffu;
+            }
+            s.bad[st] = x + 1;
+          }
 #pragma unroll
-                for (int term = 0; term < kTerms; ++term) {
-                  y[term][i] = bf16x2(e0, e1);
-                  e0 -= low(y[term][i]);
-                  e1 -= high(y[term][i]);
-                }
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kTerms == 2) {
+              // c (w + w') = hi + lo: hi = round(c w), c w - hi is exact in 16 bits
+              const uint2 wv = w2[(i / 2) * 4];
+              y[g16][0][i] = mul_bf16x2(c[i], wv.x);
+              y[g16][1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[g16][0][i] ^ 0x80008000u));
+            } else {
+              const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
+              float e0 = low(c[i]) * wv.x, e1 = high(c[i]) * wv.y;
+#pragma unroll
+              for (int term = 0; term < kTerms; ++term) {
+                y[g16][term][i] = bf16x2(e0, e1);
+                e0 -= low(y[g16][term][i]);
+                e1 -= high(y[g16][term][i]);
               }
             }
-            const uint32_t to = lanes + ((uint32_t)g16 << 20) + kColW + x % kWs * 32 * kTerms + half * 16;
-#pragma unroll
-            for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + term * 32, y[term]);
-          }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        arrive(kWFull + x % kWs);
-      }
-      if (t >= 0) {
-        // ---- the state after this chunk
-        const int st = t % kStages, n = rows_of(t);
-        if (!wait(kKvReady + t % kKvs, t / kKvs)) break;
-        tc_fence_after();
-        // after the last chunk the state itself: decay^n X + decay^(n-e-r) B^T W
-        const float d = t + 1 < chunks ? full : exp2f((float)(n - (reverse ? 31 : 32)) * log);
-        if (live) {
-          if (s.bad[st] == (uint32_t)t + 1) {
-            const uint32_t at = stage0 + st * kStageBytes;
-            add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (2 + head) * kTile,
-                                 half * NK, at + (4 + (quarter >> 1)) * kTile, n);
-          }
-          const f32x2 d2 = pair(d, d);
-#pragma unroll
-          for (int k0 = 0; k0 < NK; k0 += 16) {
-            uint32_t y[16];
-            tmem_ld16(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK + k0, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              u[(k0 + i) / 2] = mul2(add2(u[(k0 + i) / 2], pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1]))), d2);
           }
         }
-        tc_fence_before();
-        arrive(kKvFree + t % kKvs);
-        arrive(kEmpty + st);
       }
-      if (!kStates && t + 1 < chunks) {
-        // ---- Z^T as the next chunk's operand
-        if (t >= 0 && !wait(kStFree, t)) break;
-        tc_fence_after();
-        if (live) {
+      return true;
+    };
+    auto put_w = [&](int x) {
+      if (x >= kWs && !wait(kWFree + x % kWs, x / kWs - 1)) return false;
+      tc_fence_after();
+      if (live) {
 #pragma unroll
-          for (int k0 = 0; k0 < NK; k0 += 32) {
-            uint32_t y[16];
+        for (int g16 = 0; g16 < 2; ++g16) {
+          const uint32_t to = lanes + ((uint32_t)g16 << 20) + kColW + x % kWs * 32 * kTerms + half * 16;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = bf16x2(halves(u[k0 / 2 + i]).x, halves(u[k0 / 2 + i]).y);
-            tmem_st16(lanes + kColZ + (half * NK + k0) / 2, y);
-          }
-          tmem_wait_st();
+          for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + term * 32, y[g16][term]);
         }
-        tc_fence_before();
-        arrive(kStFull);
+        tmem_wait_st();
       }
+      tc_fence_before();
+      arrive(kWFull + x % kWs);
+      return true;
+    };
+    // The state after chunk t.
+    auto update = [&](int t) {
+      const int st = t % kStages, n = rows_of(t);
+      if (!wait(kKvReady + t % kKvs, t / kKvs)) return false;
+      tc_fence_after();
+      // after the last chunk the state itself: decay^n X + decay^(n-e-r) B^T W
+      const float d = t + 1 < chunks ? full : exp2f((float)(n - (reverse ? 31 : 32)) * log);
+      if (live) {
+        if (s.bad[st] == (uint32_t)t + 1) {
+          const uint32_t at = stage0 + st * kStageBytes;
+          add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (2 + head) * kTile,
+                               half * NK, at + (4 + (quarter >> 1)) * kTile, n);
+        }
+        const f32x2 d2 = pair(d, d);
+#pragma unroll
+        for (int k0 = 0; k0 < NK; k0 += 16) {
+          uint32_t z[16];
+          tmem_ld16(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK + k0, z);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            u[(k0 + i) / 2] = mul2(add2(u[(k0 + i) / 2], pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1]))), d2);
+        }
+      }
+      tc_fence_before();
+      arrive(kKvFree + t % kKvs);
+      arrive(kEmpty + st);
+      return true;
+    };
+    // Z^T as chunk x's operand.
+    auto put_z = [&](int x) {
+      if (x > 0 && !wait(kStFree, x - 1)) return false;
+      tc_fence_after();
+      if (live) {
+#pragma unroll
+        for (int k0 = 0; k0 < NK; k0 += 32) {
+          uint32_t z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = bf16x2(halves(u[k0 / 2 + i]).x, halves(u[k0 / 2 + i]).y);
+          tmem_st16(lanes + kColZ + (half * NK + k0) / 2, z);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      arrive(kStFull);
+      return true;
+    };
+    // With one buffer of W^T it is free only after the chunk's last product: the state's turn comes before, and a
+    // pair's state leaves the registers to hold W^T meanwhile.
+    constexpr bool kAhead = kWs == 2 || kPair;
+#pragma unroll 1
+    for (int t = -1; t < chunks; ++t) {
+      const bool more = t + 1 < chunks;
+      if (kAhead && more && !make_w(t + 1)) break;
+      if (kWs == 2 && more && !put_w(t + 1)) break;
+      if (t >= 0 && !update(t)) break;
+      if (!kStates && more && !put_z(t + 1)) break;
+      if (!kAhead && more && !make_w(t + 1)) break;
+      if (kWs == 1 && more && !put_w(t + 1)) break;
     }
     float* dst = kStates ? seg_state : l.phase == 0 && p.last ? p.last + state_at : nullptr;
     if (!idle && live && dst && !s.gave_up && v < p.V) {

@@ -46,7 +46,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // *gave_up set, after kWaitPolls polls (a tenth of a second at least, where
 // a phase takes microseconds) or once another wait of the block gave up.
 constexpr uint32_t kWaitPolls = 1u << 22;
-static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
 #pragma unroll 1
   for (uint32_t i = 1; i < kWaitPolls; ++i) {
     if (mbar_try(bar, parity)) return true;
