@@ -8,6 +8,7 @@ namespace tb {
 
 struct LinSegment {
   int grid;          // -1: the slot holds no segment
+  int slot;
   int index, count;  // of the grid's segments
   int64_t begin, end;  // the grid's rows
   int64_t first;     // the segment's places in the order of the walk: [first, first + len)
@@ -45,6 +46,7 @@ __device__ __forceinline__ int lin_first_slot(const LinLaunch& l, int b) {
 __device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) {
   LinSegment s;
   s.grid = -1;
+  s.slot = slot;
   s.len = 0;
   if (l.segment == 0) {
     s.grid = slot;
@@ -85,6 +87,39 @@ __device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) 
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
   return s;
+}
+
+// The grid that has `rank` longer ones (ties: the lower index first), of at
+// most kLinMaxSorted grids.  One warp; the same in all lanes.
+__device__ __forceinline__ int lin_grid_of_rank(const LinLaunch& l, int rank) {
+  const int lane = threadIdx.x & 31;
+  int64_t rows[kLinMaxSorted / 32];
+  int ahead[kLinMaxSorted / 32], found = 0;
+#pragma unroll
+  for (int i = 0; i < kLinMaxSorted / 32; ++i) {
+    rows[i] = -1;
+    ahead[i] = 0;
+    if (32 * i + lane < l.grids) {
+      int64_t begin, end;
+      lin_grid_rows(l, 32 * i + lane, begin, end);
+      rows[i] = end - begin;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kLinMaxSorted / 32; ++j)
+#pragma unroll 1
+    for (int k = 0; k < 32 && 32 * j + k < l.grids; ++k) {
+      const int64_t x = __shfl_sync(0xffffffffu, rows[j], k);
+#pragma unroll
+      for (int i = 0; i < kLinMaxSorted / 32; ++i)
+        ahead[i] += x > rows[i] || (x == rows[i] && 32 * j + k < 32 * i + lane);
+    }
+#pragma unroll
+  for (int i = 0; i < kLinMaxSorted / 32; ++i) {
+    const unsigned hit = __ballot_sync(0xffffffffu, 32 * i + lane < l.grids && ahead[i] == rank);
+    if (hit) found = 32 * i + __ffs(hit) - 1;
+  }
+  return found;
 }
 
 // decay^n for n >= 0.  The logarithm's relative error of 2^-24 moves the

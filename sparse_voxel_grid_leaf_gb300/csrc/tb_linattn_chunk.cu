@@ -183,9 +183,12 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   const uint32_t stage0 = tiles + 2 * kHeads * kTile;
 
   const LinLaunch& l = g.l;
-  const LinProblem& p = l.p[blockIdx.z];
+  // blocks in the order of their segments, longest grids first where they are walked whole
+  const int walks = (l.heads + kHeads - 1) / kHeads;
+  const int slot0 = blockIdx.x / (walks * l.n), walk = blockIdx.x % (walks * l.n), problem = walk / walks;
+  const LinProblem& p = l.p[problem];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int h0 = blockIdx.y * kHeads;
+  const int h0 = (walk - problem * walks) * kHeads;
   auto bar = [&](int i) { return smem_addr(&s.bar[i]); };
   const bool reverse = p.reverse;
   // The heads that go by chunks, and their decays; the recurrence takes the others that exist.
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   }
 
   if (warp == 0) {
-    const LinSegment seg = lin_segment(l, blockIdx.x);
+    const LinSegment seg = lin_segment(l, l.sorted ? lin_grid_of_rank(l, slot0) : slot0);
     if (lane == 0) s.seg = seg;
   } else if (warp == 1) {
     if (lane == 0) {
@@ -276,9 +279,9 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 
   if (warp == kWarpTma) {
     if (elect_one()) {
-      const CUtensorMap* ma = &g.map[g.a[blockIdx.z]];
-      const CUtensorMap* mb = &g.map[g.b[blockIdx.z]];
-      const CUtensorMap* mc = &g.map[g.c[blockIdx.z]];
+      const CUtensorMap* ma = &g.map[g.a[problem]];
+      const CUtensorMap* mb = &g.map[g.b[problem]];
+      const CUtensorMap* mc = &g.map[g.c[problem]];
       const uint32_t bytes = ((kStates ? 2 : 4) + value_tiles) * kTile;
       int t = 0;
 #pragma unroll 1
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
     constexpr int NK = kKeys / 2;  // keys of a thread
     const int half = warp >> 2, v = value0 + lane;
     const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
-    float* seg_state = p.seg ? p.seg + ((int64_t)blockIdx.x * l.heads + h) * p.K * p.V : nullptr;
+    float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
     const float log = log2f(kPair && head ? decay[kHeads - 1] : decay[0]);
     const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
     f32x2 u[NK / 2];  // Z, by pairs of keys
@@ -448,12 +451,12 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
               y[g16][1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[g16][0][i] ^ 0x80008000u));
             } else {
               const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
-              float e0 = low(c[i]) * wv.x, e1 = high(c[i]) * wv.y;
+              f32x2 e = mul2(pair(low(c[i]), high(c[i])), pair(wv.x, wv.y));
 #pragma unroll
               for (int term = 0; term < kTerms; ++term) {
-                y[g16][term][i] = bf16x2(e0, e1);
-                e0 -= low(y[g16][term][i]);
-                e1 -= high(y[g16][term][i]);
+                const uint32_t x2 = bf16x2(halves(e).x, halves(e).y);
+                y[g16][term][i] = x2;
+                if (term + 1 < kTerms) e = fma2(pair(low(x2), high(x2)), pair(-1.f, -1.f), e);
               }
             }
           }
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   } else if (!kStates) {
     // -------------------------------------------------------------- output
     const uint32_t out0 = stage0 + kStages * kStageBytes + quarter * 2 * kOutTile;
-    const CUtensorMap* map = &g.map[kLinMaxRows + blockIdx.z];
+    const CUtensorMap* map = &g.map[kLinMaxRows + problem];
 #pragma unroll 1
     for (int t = 0; t < chunks; ++t) {
       const int st = t % kStages, n = rows_of(t);
@@ -686,8 +689,8 @@ cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
-  const dim3 grid(g.l.segments, kPair ? (g.l.heads + 1) / 2 : g.l.heads, g.l.n);
-  k_chunks<kPair, kTerms, kStates><<<grid, threads_of(kPair, kStates), bytes, s>>>(g);
+  const int64_t blocks = (int64_t)g.l.segments * (kPair ? (g.l.heads + 1) / 2 : g.l.heads) * g.l.n;
+  k_chunks<kPair, kTerms, kStates><<<(unsigned)blocks, threads_of(kPair, kStates), bytes, s>>>(g);
   return cudaGetLastError();
 }
 
@@ -760,11 +763,9 @@ bool linear_chunk_plan(ChunkLaunch& g) {
 
 cudaError_t launch_linear_chunks(const void* args, cudaStream_t s) {
   const ChunkLaunch& g = *(const ChunkLaunch*)args;
-  bool pair = g.l.heads > 1, exact = false;
-  for (int i = 0; i < g.l.n; ++i) {
-    pair = pair && g.l.p[i].K <= 64 && g.l.p[i].V <= 64;
-    exact = exact || g.l.p[i].last;
-  }
+  const bool pair = linear_pairs(g.l.heads, g.l.p[0].K, g.l.p[0].V);
+  bool exact = false;
+  for (int i = 0; i < g.l.n; ++i) exact = exact || g.l.p[i].last;
   if (g.l.phase == 1) {
     if (pair) return exact ? go<true, 3, true>(g, s) : go<true, 2, true>(g, s);
     return exact ? go<false, 3, true>(g, s) : go<false, 2, true>(g, s);

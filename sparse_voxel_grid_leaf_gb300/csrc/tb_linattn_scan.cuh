@@ -59,7 +59,7 @@ __device__ __forceinline__ void scan_walk(const LinLaunch& l, const LinProblem& 
   const int lane = threadIdx.x & 31, slice = lane & 3;
   const int v0 = (threadIdx.x >> 5) * 16 + (lane >> 2) * 2;
   const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
-  float* seg_state = p.seg ? p.seg + ((int64_t)blockIdx.x * l.heads + h) * p.K * p.V : nullptr;
+  float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
 
   f32x2 u[2][KS / 2];
   auto key = [&](int i) { return (i / 4 * 4 + slice) * 4 + i % 4; };

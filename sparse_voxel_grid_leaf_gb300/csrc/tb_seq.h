@@ -90,7 +90,11 @@ struct LinLaunch {
   int32_t segment;            // tokens of one segment; 0: a grid is one segment
   int32_t segments;           // segment slots: the grid's x extent
   int32_t phase;              // 0: whole grids; 1: states of segments; 2: outputs of segments
+  int32_t sorted;             // chunk kernel, whole grids: the longest ones first
 };
+constexpr int kLinMaxSorted = 64;  // grids that a warp sorts
+// Whether a block of the chunk kernel takes two heads.
+inline bool linear_pairs(int heads, int K, int V) { return heads > 1 && K <= 64 && V <= 64; }
 // The chunk kernel's call (tb_linattn_chunk.cu): the walk and the row tensors
 // as the copy engine reads them.
 constexpr int kLinMaxRows = 4;

@@ -191,19 +191,25 @@ tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stre
 
 // --------------------------------------------------------- linear attention
 
+struct LinSizes {
+  int64_t tokens;
+  int32_t grids, heads, key, value, type;
+};
+
 // Tokens of a segment, 0: grids are walked whole.  A walk is sequential along
 // a grid, so a call with few grids and heads is split along the rows: the
 // segments' own states first, their joining, then the outputs.  The states
 // pass reads the keys and values once more, and pays where it fills the
-// multiprocessors: one block of the chunk kernel (16-bit rows) runs on each,
-// four of the recurrence.
-static int32_t segment_tokens(int64_t tokens, int32_t grids, int32_t heads, int problems, int32_t type, int sms) {
-  const int64_t walks = (int64_t)heads * problems;
-  const int64_t want = (type == TB_TYPE_BF16 ? 2ll : 4ll) * sms;
-  if (grids <= 0 || grids * walks >= want) return 0;
-  int64_t seg = up(up(tokens * walks, want), 64) * 64;
+// multiprocessors: one block of the chunk kernel (16-bit rows; of two heads,
+// where they are small) runs on each, four of the recurrence.
+static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
+  const bool chunks = z.type == TB_TYPE_BF16;
+  const int64_t heads = chunks && linear_pairs(z.heads, z.key, z.value) ? (z.heads + 1) / 2 : z.heads;
+  const int64_t walks = heads * problems, want = (chunks ? 2ll : 4ll) * sms;
+  if (z.grids <= 0 || z.grids * walks >= want) return 0;
+  int64_t seg = up(up(z.tokens * walks, want), 64) * 64;
   if (seg < 256) seg = 256;
-  return tokens >= 2 * seg * grids ? (int32_t)seg : 0;
+  return z.tokens >= 2 * seg * z.grids ? (int32_t)seg : 0;
 }
 
 static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
@@ -215,7 +221,7 @@ int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int32_t hea
   if (tokens < 0 || grids < 0 || heads < 1 || key < 1 || value < 1) return 0;
   const int sms = seq_sms();
   const int problems = backward ? 3 : 1;
-  const int32_t seg = segment_tokens(tokens, grids, heads, problems, type, sms ? sms : 256);
+  const int32_t seg = segment_tokens({tokens, grids, heads, key, value, type}, problems, sms ? sms : 256);
   return seg ? segment_slots(tokens, grids, seg) * heads * key * value * 4 * problems : 0;
 }
 
@@ -243,8 +249,9 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaun
   l.tokens = a.tokens;
   l.offsets = a.offsets;
   l.decay = a.decay;
-  l.segment = segment_tokens(a.tokens, a.grids, a.heads, l.n, a.type, sms);
+  l.segment = segment_tokens({a.tokens, a.grids, a.heads, a.key, a.value, a.type}, l.n, sms);
   const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
+  if (slots * a.heads * l.n > kMaxRows) return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 walks or more", what);
   l.segments = (int32_t)slots;
   if (l.segment) {
     const int64_t one = slots * a.heads * a.key * a.value;
@@ -256,6 +263,8 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaun
   // A chunk of 64 rows costs the tensor cores the same with one row in it.
   const bool chunks = a.tokens >= 16ll * a.grids && linear_chunk_plan(g);
   l.phase = 0;
+  // With more walks than multiprocessors the last to start should be short ones.
+  l.sorted = !l.segment && a.grids > 1 && a.grids <= kLinMaxSorted && (int64_t)a.grids * a.heads * l.n > sms;
   if (l.segment) {
     l.phase = 1;
     if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunkStates, s, launch_linear_chunks, &g));
