@@ -1,4 +1,5 @@
-"""Builds libtb.so in-tree with nvcc for sm_103a (GB300).
+"""Builds libtb.so in-tree with nvcc for sm_103a (GB300), and _seq.so, the
+Python entry points of its sequence operators, with the host compiler.
 
 The translation units compile in parallel and are linked with the static
 CUDA runtime, so the library needs only the NVIDIA driver at run time.
@@ -8,11 +9,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtb.so")
+SEQ = os.path.join(HERE, "_seq.so")
 SOURCES = ["tb_api.cu", "tb_prepass.cu", "tb_chain.cu", "tb_noalloc.cu", "tb_kmap.cu",
            "tb_seq_api.cu", "tb_rotary.cu", "tb_norm.cu", "tb_linattn.cu",
            "tb_linattn_chunk.cu"]
@@ -33,6 +36,18 @@ def _stale(out, deps):
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch_command():
+    """The compiler command of _seq.so up to its inputs, and torch's library folder."""
+    import importlib.util
+    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"] + [x for i in inc for x in ("-isystem", i)], \
+        os.path.join(root, "lib")
 
 
 def build(force=False, verbose=False, extra_flags=()):
@@ -59,12 +74,23 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stderr, file=sys.stderr)
         return r
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    seq_src, seq_obj = os.path.join(CSRC, "tb_seq_py.cpp"), os.path.join(BUILD, "tb_seq_py.o")
+    cxx, torch_lib = _torch_command()
+    built = len(jobs)
+    if force or _stale(seq_obj, [seq_src] + headers):
+        jobs.append([*cxx, "-c", seq_src, "-o", seq_obj])
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
+    if force or built or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if force or _stale(SEQ, [seq_obj, LIB]):
+        tmp = SEQ + ".tmp%d" % os.getpid()
+        run([cxx[0], "-shared", "-o", tmp, seq_obj, "-L", HERE, "-l:libtb.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"])
+        os.replace(tmp, SEQ)
     return LIB
 
 
