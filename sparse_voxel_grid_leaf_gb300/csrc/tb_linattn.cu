@@ -20,9 +20,9 @@ namespace {
 // ---------------------------------------------------------------- one token
 
 constexpr int kStepThreads = 256;
-constexpr int kStepBatch = 16;  // state vectors in flight per thread
 
-template <class T, int V>
+// kBatch: state vectors in flight per thread.
+template <class T, int V, int kStepBatch>
 __global__ void __launch_bounds__(kStepThreads) k_step(StepLaunch l) {
   const tb_linear_step_args& a = l.a;
   __shared__ float s_q[256], s_k[256];
@@ -66,12 +66,14 @@ __global__ void __launch_bounds__(kStepThreads) k_step(StepLaunch l) {
       const int r = base + i * rows;
       if (live && r < a.key) {
         const float kk = s_k[r], qq = s_q[r];
+        float f[V];
+        unpack<float, V>(x[i], f);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          x[i].e[j] = fmaf(x[i].e[j], decay, kk * vv[j]);
-          o[j] = fmaf(qq, x[i].e[j], o[j]);
+          f[j] = fmaf(f[j], decay, kk * vv[j]);
+          o[j] = fmaf(qq, f[j], o[j]);
         }
-        store_pack<float, V>(state + (int64_t)r * a.value, x[i]);
+        store_pack<float, V>(state + (int64_t)r * a.value, pack<float, V>(f));
       }
     }
   }
@@ -89,8 +91,12 @@ __global__ void __launch_bounds__(kStepThreads) k_step(StepLaunch l) {
 template <class T>
 cudaError_t go_step(const StepLaunch& l, cudaStream_t s) {
   const unsigned blocks = (unsigned)(l.a.streams * l.a.heads);
-  if (l.a.value % 4 == 0) k_step<T, 4><<<blocks, kStepThreads, 0, s>>>(l);
-  else k_step<T, 1><<<blocks, kStepThreads, 0, s>>>(l);
+  // as many vectors as a thread has of the state, up to 8: with more the registers leave too few blocks
+  const bool vec = l.a.value % 4 == 0;
+  const int rows = kStepThreads / (vec ? l.a.value / 4 : l.a.value), sweep = (l.a.key + rows - 1) / rows;
+  if (!vec) k_step<T, 1, 8><<<blocks, kStepThreads, 0, s>>>(l);
+  else if (sweep <= 4) k_step<T, 4, 4><<<blocks, kStepThreads, 0, s>>>(l);
+  else k_step<T, 4, 8><<<blocks, kStepThreads, 0, s>>>(l);
   return cudaGetLastError();
 }
 

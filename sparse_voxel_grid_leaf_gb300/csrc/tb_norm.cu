@@ -13,105 +13,129 @@ namespace tb {
 namespace {
 
 constexpr int kMaxThreads = 512;
+__host__ __device__ constexpr int up_to(int x, int m) { return (x + m - 1) / m * m; }
 
-// Sum (or maximum) of one value over the threads of a row: threadIdx.x runs
-// over the row, warps are whole.  Rows of one warp need no barrier.
+// Sums (the second one: sum or maximum) of two values over the threads of a
+// row: threadIdx.x runs over the row, warps are whole.  Rows of one warp need
+// no barrier.
 template <bool kMax>
-__device__ __forceinline__ float row_reduce(float x, float* s, int& turn) {
-  x = kMax ? warp_max(x) : warp_sum(x);
+__device__ __forceinline__ float2 row_reduce(float x, float y, float2* s, int& turn) {
+  x = warp_sum(x);
+  y = kMax ? warp_max(y) : warp_sum(y);
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return x;
-  float* at = s + (turn ^= 1) * 32;
-  if ((threadIdx.x & 31) == 0) at[threadIdx.y * warps + (threadIdx.x >> 5)] = x;
+  if (warps == 1) return make_float2(x, y);
+  float2* at = s + (turn ^= 1) * 32;
+  if ((threadIdx.x & 31) == 0) at[threadIdx.y * warps + (threadIdx.x >> 5)] = make_float2(x, y);
   __syncthreads();
-  float v = at[threadIdx.y * warps];
-  for (int i = 1; i < warps; ++i) v = kMax ? fmaxf(v, at[threadIdx.y * warps + i]) : v + at[threadIdx.y * warps + i];
+  float2 v = at[threadIdx.y * warps];
+  for (int i = 1; i < warps; ++i) {
+    const float2 w = at[threadIdx.y * warps + i];
+    v.x += w.x;
+    v.y = kMax ? fmaxf(v.y, w.y) : v.y + w.y;
+  }
   return v;
 }
 
+// Blocks stay and walk over rows; a row's elements are loaded while the one
+// before it is normed, and held as they came (16-bit pairs): the sum of the
+// residual stream is computed once for the mean and once for the output.
 template <class T, int V, int NV, bool kFp8>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
   const tb_norm_args& a = n.a;
-  __shared__ float s_red[64];
+  __shared__ float2 s_red[64];
   int turn = 0;
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
-  const T* w = (const T*)a.weight;
-  // block-uniform trip count: the barriers of row_reduce are passed by all
-  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.rows; base += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t row = base + threadIdx.y;
-    const bool live = row < a.rows;
-    float f[NV][V];
+  const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+  Pack<T, V> w[NV], px[NV], pr[NV];
+  auto load = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.x_row;
     const T* res = (const T*)a.residual + row * a.residual_row;
-    float sum = 0.f;
-    {
-      Pack<T, V> px[NV], pr[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (live && v < vecs) {
-          px[i] = load_pack<T, V>(x + (int64_t)v * V);
-          if (a.residual) pr[i] = load_pack<T, V>(res + (int64_t)v * V);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (live && v < vecs) {
-          unpack<T, V>(px[i], f[i]);
-          if (a.residual) {
-            float g[V];
-            unpack<T, V>(pr[i], g);
-#pragma unroll
-            for (int j = 0; j < V; ++j) f[i][j] += g[j];
-            if (a.h_out) store_pack<T, V>((T*)a.h_out + row * a.h_row + (int64_t)v * V, pack<T, V>(f[i]));
-          }
-#pragma unroll
-          for (int j = 0; j < V; ++j) sum = fmaf(f[i][j], f[i][j], sum);
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (row < a.rows && v < vecs) {
+        px[i] = load_pack<T, V>(x + (int64_t)v * V);
+        if (a.residual) pr[i] = load_pack<T, V>(res + (int64_t)v * V);
       }
     }
-    sum = row_reduce<false>(sum, s_red, turn);
-    const float r = rsqrtf(fmaf(sum, inv_width, a.eps));
-    float top = 0.f;
+  };
+  int64_t base = (int64_t)blockIdx.x * blockDim.y;
+  load(base + threadIdx.y);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < vecs) w[i] = load_pack<T, V>((const T*)a.weight + (int64_t)v * V);
+  }
+  // block-uniform trip count: the barriers of row_reduce are passed by all
+  for (; base < a.rows; base += stride) {
+    const int64_t row = base + threadIdx.y;
+    const bool live = row < a.rows;
+    Pack<T, V> cx[NV], cr[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      cx[i] = px[i];
+      cr[i] = pr[i];
+    }
+    load(row + stride);
+    auto sum_of = [&](int i, float (&f)[V]) {
+      unpack<T, V>(cx[i], f);
+      if (a.residual) {
+        float g[V];
+        unpack<T, V>(cr[i], g);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] += g[j];
+      }
+    };
+    float sum = 0.f, top = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (live && v < vecs) {
-        float g[V];
-        unpack<T, V>(load_pack<T, V>(w + (int64_t)v * V), g);
+        float f[V];
+        sum_of(i, f);
+        if (a.h_out) store_pack<T, V>((T*)a.h_out + row * a.h_row + (int64_t)v * V, pack<T, V>(f));
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          f[i][j] *= r * g[j];
-          if (kFp8) top = fmaxf(top, fabsf(f[i][j]));
+        for (int j = 0; j < V; ++j) sum = fmaf(f[j], f[j], sum);
+        if constexpr (kFp8) {
+          float g[V];
+          unpack<T, V>(w[i], g);
+#pragma unroll
+          for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(f[j] * g[j]));
         }
-        if constexpr (!kFp8)
-          store_pack<T, V>((T*)a.y + row * a.y_row + (int64_t)v * V, pack<T, V>(f[i]));
       }
     }
+    const float2 all = row_reduce<true>(sum, top, s_red, turn);
+    const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
+    float by = r;
     if constexpr (kFp8) {
-      // A NaN in a row makes all of its y NaN; fmaxf drops them (scale 0) and
-      // the conversion keeps them.
-      top = row_reduce<true>(top, s_red, turn);
-      const float scale = top * (1.f / 448.f);
-      const float inv = top > 0.f ? 448.f / top : 0.f;
-      if (live && threadIdx.x == 0) a.scale[row] = scale;
+      // max |y| is r max |h w|.  A NaN in a row makes all of its y NaN; fmaxf
+      // drops them (scale 0 or finite) and the conversion keeps them.
+      top = all.y * r;
+      if (live && threadIdx.x == 0) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
+      by = top > 0.f ? 448.f / all.y : top == 0.f ? 0.f : r;
+    }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (live && v < vecs) {
+    for (int i = 0; i < NV; ++i) {
+      const int v = threadIdx.x + i * blockDim.x;
+      if (live && v < vecs) {
+        float f[V], g[V];
+        sum_of(i, f);
+        unpack<T, V>(w[i], g);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] *= by * g[j];
+        if constexpr (!kFp8) {
+          store_pack<T, V>((T*)a.y + row * a.y_row + (int64_t)v * V, pack<T, V>(f));
+        } else {
           uint8_t* dst = (uint8_t*)a.y + row * a.y_row + (int64_t)v * V;
           if constexpr (V == 1) {
-            *dst = __nv_cvt_float_to_fp8(f[i][0] * inv, __NV_SATFINITE, __NV_E4M3);
+            *dst = __nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
           } else {
             uint32_t word[V / 4];
 #pragma unroll
             for (int j = 0; j < V; j += 4) {
-              const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[i][j] * inv, f[i][j + 1] * inv),
-                                                           __NV_SATFINITE, __NV_E4M3);
-              const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[i][j + 2] * inv, f[i][j + 3] * inv),
-                                                           __NV_SATFINITE, __NV_E4M3);
+              const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[j], f[j + 1]), __NV_SATFINITE, __NV_E4M3);
+              const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[j + 2], f[j + 3]), __NV_SATFINITE, __NV_E4M3);
               word[j / 4] = lo | hi << 16;
             }
             if constexpr (V == 8) *(uint2*)dst = make_uint2(word[0], word[1]);
@@ -129,57 +153,74 @@ template <class T, int V, int NV>
 __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunch n) {
   const tb_norm_backward_args& a = n.a;
   extern __shared__ float s_part[];  // [rows, per_row * NV * V] where a block has more than one row
-  __shared__ float s_red[64];
+  __shared__ float2 s_red[64];
   int turn = 0;
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
+  const int64_t stride = (int64_t)gridDim.x * blockDim.y;
   float dw[NV][V] = {};
-  for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.rows; base += (int64_t)gridDim.x * blockDim.y) {
-    const int64_t row = base + threadIdx.y;
-    const bool live = row < a.rows;
-    Pack<T, V> ph[NV], pd[NV], pg[NV];
+  Pack<T, V> w[NV], ph[NV], pd[NV], pg[NV];
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
-      if (live && v < vecs) {
+      if (row < a.rows && v < vecs) {
         ph[i] = load_pack<T, V>((const T*)a.h + row * a.h_row + (int64_t)v * V);
         pd[i] = load_pack<T, V>((const T*)a.dy + row * a.dy_row + (int64_t)v * V);
         if (a.dh) pg[i] = load_pack<T, V>((const T*)a.dh + row * a.dh_row + (int64_t)v * V);
       }
     }
+  };
+  int64_t base = (int64_t)blockIdx.x * blockDim.y;
+  load(base + threadIdx.y);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = threadIdx.x + i * blockDim.x;
+    if (v < vecs) w[i] = load_pack<T, V>((const T*)a.weight + (int64_t)v * V);
+  }
+  for (; base < a.rows; base += stride) {
+    const int64_t row = base + threadIdx.y;
+    const bool live = row < a.rows;
+    Pack<T, V> ch[NV], cd[NV], cg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      ch[i] = ph[i];
+      cd[i] = pd[i];
+      cg[i] = pg[i];
+    }
+    load(row + stride);
     float hh = 0.f, hd = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (live && v < vecs) {
-        float h[V], d[V], w[V];
-        unpack<T, V>(ph[i], h);
-        unpack<T, V>(pd[i], d);
-        unpack<T, V>(load_pack<T, V>((const T*)a.weight + (int64_t)v * V), w);
+        float h[V], d[V], g[V];
+        unpack<T, V>(ch[i], h);
+        unpack<T, V>(cd[i], d);
+        unpack<T, V>(w[i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           hh = fmaf(h[j], h[j], hh);
-          hd = fmaf(h[j] * w[j], d[j], hd);
+          hd = fmaf(h[j] * g[j], d[j], hd);
         }
       }
     }
-    hh = row_reduce<false>(hh, s_red, turn);
-    hd = row_reduce<false>(hd, s_red, turn);
-    const float r = rsqrtf(fmaf(hh, inv_width, a.eps));
-    const float m = r * r * r * hd * inv_width;
+    const float2 all = row_reduce<false>(hh, hd, s_red, turn);
+    const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
+    const float m = r * r * r * all.y * inv_width;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
       if (live && v < vecs) {
-        float h[V], d[V], w[V], g[V];
-        unpack<T, V>(ph[i], h);
-        unpack<T, V>(pd[i], d);
-        unpack<T, V>(load_pack<T, V>((const T*)a.weight + (int64_t)v * V), w);
-        if (a.dh) unpack<T, V>(pg[i], g);
+        float h[V], d[V], f[V], g[V];
+        unpack<T, V>(ch[i], h);
+        unpack<T, V>(cd[i], d);
+        unpack<T, V>(w[i], f);
+        if (a.dh) unpack<T, V>(cg[i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           dw[i][j] = fmaf(d[j], h[j] * r, dw[i][j]);
-          const float x = fmaf(-m, h[j], r * w[j] * d[j]);
+          const float x = fmaf(-m, h[j], r * f[j] * d[j]);
           h[j] = a.dh ? x + g[j] : x;
         }
         store_pack<T, V>((T*)a.dx + row * a.dx_row + (int64_t)v * V, pack<T, V>(h));
@@ -213,6 +254,202 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
   }
 }
 
+// ------------------------------------------- rows that no vector boundary meets
+//
+// A row of an odd width starts anywhere, but kGroup = 16 / sizeof(T) rows of a
+// dense tensor are a whole number of vectors: blocks move such groups through
+// shared memory, 16 bytes at a time, the next group while one is normed, and
+// read single elements there (50000 rows of 777 in 16 bits: 67 us, 125 element by element;
+// the gradient 74 us and 133).
+
+template <class T>
+constexpr int group_of() {
+  return 16 / (int)sizeof(T);
+}
+
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
+// Group `c` of rows, on its way into `dst`; the last group's tail byte-exact.
+template <class T>
+__device__ __forceinline__ void fetch_group(T* dst, const void* src, int64_t c, int64_t rows, int width) {
+  constexpr int G = group_of<T>();
+  const int64_t left = rows - c * G;
+  const T* from = (const T*)src + c * G * width;
+  const int n = (int)(left < G ? left : G) * width, vecs = n / G;
+  for (int i = threadIdx.x; i < vecs; i += blockDim.x) copy_async(dst + i * G, from + i * G);
+  for (int i = vecs * G + threadIdx.x; i < n; i += blockDim.x) dst[i] = from[i];
+}
+template <class T>
+__device__ __forceinline__ void put_group(void* dst, const T* src, int64_t c, int64_t rows, int width) {
+  constexpr int G = group_of<T>();
+  const int64_t left = rows - c * G;
+  T* to = (T*)dst + c * G * width;
+  const int n = (int)(left < G ? left : G) * width, vecs = n / G;
+  for (int i = threadIdx.x; i < vecs; i += blockDim.x)
+    *reinterpret_cast<uint4*>(to + i * G) = *reinterpret_cast<const uint4*>(src + i * G);
+  for (int i = vecs * G + threadIdx.x; i < n; i += blockDim.x) to[i] = src[i];
+}
+
+// Shared memory: the weight, then `stages` buffers of a group of x, residual.
+template <class T, bool kFp8>
+__global__ void __launch_bounds__(32 * 8) k_norm_groups(NormLaunch n) {
+  const tb_norm_args& a = n.a;
+  constexpr int G = group_of<T>();
+  extern __shared__ __align__(16) char s_group[];
+  const int width = a.width, lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int tensors = a.residual ? 2 : 1;
+  T* w = reinterpret_cast<T*>(s_group);
+  T* buf = w + up_to(width, G);
+  const float inv_width = 1.f / (float)width;
+  const int64_t groups = (a.rows + G - 1) / G;
+  for (int i = threadIdx.x; i < width; i += blockDim.x) w[i] = ((const T*)a.weight)[i];
+  auto fetch = [&](int64_t c, int st) {
+    if (c < groups) {
+      T* to = buf + (size_t)st * tensors * G * width;
+      fetch_group(to, a.x, c, a.rows, width);
+      if (a.residual) fetch_group(to + G * width, a.residual, c, a.rows, width);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int st = 0;
+  if (n.nv > 1) fetch(blockIdx.x, 0);
+  for (int64_t c = blockIdx.x; c < groups; c += gridDim.x) {
+    if (n.nv > 1) {
+      fetch(c + gridDim.x, st ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      fetch(c, 0);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    T* x = buf + (size_t)st * tensors * G * width;
+    T* res = x + G * width;
+    const int64_t row = c * G + g;
+    if (row < a.rows) {
+      T* xr = x + g * width;
+      T* rr = res + g * width;
+      float sum = 0.f, top = 0.f;
+      for (int i = lane; i < width; i += 32) {
+        float f = RowType<T>::to(xr[i]);
+        if (a.residual) f += RowType<T>::to(rr[i]);
+        sum = fmaf(f, f, sum);
+        if (kFp8) top = fmaxf(top, fabsf(f * RowType<T>::to(w[i])));
+      }
+      sum = warp_sum(sum);
+      const float r = rsqrtf(fmaf(sum, inv_width, a.eps));
+      float by = r;
+      if (kFp8) {
+        top = warp_max(top);
+        const float all = top;
+        top *= r;
+        if (lane == 0) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
+        by = top > 0.f ? 448.f / all : top == 0.f ? 0.f : r;
+      }
+      uint8_t* q = (uint8_t*)a.y + row * width;
+      for (int i = lane; i < width; i += 32) {
+        float f = RowType<T>::to(xr[i]);
+        if (a.residual) {
+          f += RowType<T>::to(rr[i]);
+          rr[i] = RowType<T>::from(f);
+        }
+        f *= by * RowType<T>::to(w[i]);
+        if (kFp8) q[i] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
+        else xr[i] = RowType<T>::from(f);
+      }
+    }
+    __syncthreads();
+    if (!kFp8) put_group(a.y, x, c, a.rows, width);
+    if (a.h_out) put_group(a.h_out, res, c, a.rows, width);
+    if (n.nv > 1) st ^= 1;
+    __syncthreads();  // the group's buffer may be filled again
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Shared memory: the weight and dweight's part in 32 bits, then `stages`
+// buffers of a group of h, dy, dh; dx takes dy's place.
+template <class T>
+__global__ void __launch_bounds__(32 * 8) k_norm_backward_groups(NormBackwardLaunch n) {
+  const tb_norm_backward_args& a = n.a;
+  constexpr int G = group_of<T>();
+  extern __shared__ __align__(16) char s_group[];
+  __shared__ float2 s_row[G];  // r and the factor of h
+  const int width = a.width, lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int tensors = a.dh ? 3 : 2;
+  float* w = reinterpret_cast<float*>(s_group);
+  float* dw = w + up_to(width, 4);
+  T* buf = reinterpret_cast<T*>(dw + up_to(width, 4));
+  const float inv_width = 1.f / (float)width;
+  const int64_t groups = (a.rows + G - 1) / G;
+  for (int i = threadIdx.x; i < width; i += blockDim.x) {
+    w[i] = RowType<T>::to(((const T*)a.weight)[i]);
+    dw[i] = 0.f;
+  }
+  auto fetch = [&](int64_t c, int st) {
+    if (c < groups) {
+      T* to = buf + (size_t)st * tensors * G * width;
+      fetch_group(to, a.h, c, a.rows, width);
+      fetch_group(to + G * width, a.dy, c, a.rows, width);
+      if (a.dh) fetch_group(to + 2 * G * width, a.dh, c, a.rows, width);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int st = 0;
+  if (n.nv > 1) fetch(blockIdx.x, 0);
+  for (int64_t c = blockIdx.x; c < groups; c += gridDim.x) {
+    if (n.nv > 1) {
+      fetch(c + gridDim.x, st ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      fetch(c, 0);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    T* h = buf + (size_t)st * tensors * G * width;
+    T* d = h + G * width;
+    const T* dh = d + G * width;
+    const int rows = (int)min((int64_t)G, a.rows - c * G);
+    if (g < rows) {
+      float hh = 0.f, hd = 0.f;
+      for (int i = lane; i < width; i += 32) {
+        const float f = RowType<T>::to(h[g * width + i]);
+        hh = fmaf(f, f, hh);
+        hd = fmaf(f * w[i], RowType<T>::to(d[g * width + i]), hd);
+      }
+      hh = warp_sum(hh);
+      hd = warp_sum(hd);
+      const float r = rsqrtf(fmaf(hh, inv_width, a.eps));
+      if (lane == 0) s_row[g] = make_float2(r, -(r * r * r * hd * inv_width));
+    }
+    __syncthreads();
+    // by columns: a thread's part of dweight stays its own
+    for (int i = threadIdx.x; i < width; i += blockDim.x) {
+      const float wi = w[i];
+      float sum = dw[i];
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        if (k >= rows) break;
+        const float2 rm = s_row[k];
+        const float f = RowType<T>::to(h[k * width + i]), e = RowType<T>::to(d[k * width + i]);
+        sum = fmaf(e, f * rm.x, sum);
+        float x = fmaf(rm.y, f, rm.x * wi * e);
+        if (a.dh) x += RowType<T>::to(dh[k * width + i]);
+        d[k * width + i] = RowType<T>::from(x);
+      }
+      dw[i] = sum;
+    }
+    __syncthreads();
+    put_group(a.dx, d, c, a.rows, width);
+    if (n.nv > 1) st ^= 1;
+    __syncthreads();  // the group's buffer may be filled again
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  for (int i = threadIdx.x; i < width; i += blockDim.x) a.workspace[(int64_t)blockIdx.x * width + i] = dw[i];
+}
+
 // dweight = the blocks' parts summed: 32 columns a block, 32 groups of parts.
 template <class T>
 __global__ void __launch_bounds__(1024) k_norm_weight(NormBackwardLaunch n) {
@@ -228,6 +465,30 @@ __global__ void __launch_bounds__(1024) k_norm_weight(NormBackwardLaunch n) {
   if (threadIdx.x == 0 && o < n.a.width) ((T*)n.a.dweight)[o] = RowType<T>::from(all);
 }
 
+// Lets a kernel take `bytes` of shared memory.
+template <class K>
+cudaError_t allow(K* kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <class T, bool kFp8>
+cudaError_t go_groups(const NormLaunch& n, cudaStream_t s) {
+  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.residual ? 2 : 1, n.nv, sizeof(T));
+  const cudaError_t e = allow(k_norm_groups<T, kFp8>, bytes);
+  if (e != cudaSuccess) return e;
+  k_norm_groups<T, kFp8><<<n.blocks, 32 * group_of<T>(), bytes, s>>>(n);
+  return cudaGetLastError();
+}
+template <class T>
+cudaError_t go_back_groups(const NormBackwardLaunch& n, cudaStream_t s) {
+  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.nv, 8);
+  const cudaError_t e = allow(k_norm_backward_groups<T>, bytes);
+  if (e != cudaSuccess) return e;
+  k_norm_backward_groups<T><<<n.blocks, 32 * group_of<T>(), bytes, s>>>(n);
+  return cudaGetLastError();
+}
+
 template <class T, int V, int NV>
 cudaError_t go(const NormLaunch& n, cudaStream_t s) {
   const dim3 block(n.per_row, n.rows);
@@ -239,6 +500,7 @@ cudaError_t go(const NormLaunch& n, cudaStream_t s) {
 template <class T>
 cudaError_t pick(const NormLaunch& n, cudaStream_t s) {
   constexpr int V = RowType<T>::kVec;
+  if (n.groups) return n.a.fp8 ? go_groups<T, true>(n, s) : go_groups<T, false>(n, s);
   if (n.vec) {
     switch (n.nv) {
       case 1: return go<T, V, 1>(n, s);
@@ -247,7 +509,11 @@ cudaError_t pick(const NormLaunch& n, cudaStream_t s) {
       default: return go<T, V, 8>(n, s);
     }
   }
-  return n.nv <= 8 ? go<T, 1, 8>(n, s) : go<T, 1, 32>(n, s);
+  switch (n.nv) {
+    case 4: return go<T, 1, 4>(n, s);
+    case 8: return go<T, 1, 8>(n, s);
+    default: return go<T, 1, 32>(n, s);
+  }
 }
 
 template <class T, int V, int NV>
@@ -261,6 +527,7 @@ cudaError_t go_back(const NormBackwardLaunch& n, cudaStream_t s) {
 template <class T>
 cudaError_t pick_back(const NormBackwardLaunch& n, cudaStream_t s) {
   constexpr int V = RowType<T>::kVec;
+  if (n.groups) return go_back_groups<T>(n, s);
   if (n.vec) {
     switch (n.nv) {
       case 1: return go_back<T, V, 1>(n, s);

@@ -33,38 +33,21 @@ __global__ void __launch_bounds__(kThreads) k_rotary(RotaryLaunch r) {
   const int turned = pairs / V;                          // units that turn
   const int units = turned + (a.dim - 2 * pairs) / V;    // and that pass through
 
-  const float sign = a.inverse ? -a.amplitude : a.amplitude;
-  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-    const int t = i / pairs, p = i - t * pairs;
-    int axis = 0;
-    if (a.axes > 1) {
-      const int s1 = a.section[0], s2 = s1 + a.section[1];
-      axis = p < s1 ? 0 : (p < s2 || a.axes == 2) ? 1 : 2;
-    }
-    const int64_t at = (t0 + t) * a.position_row + axis;
-    const int64_t pos = a.positions64 ? ((const int64_t*)a.positions)[at] : (int64_t)((const int32_t*)a.positions)[at];
-    const uint64_t phase = (uint64_t)pos * (uint64_t)a.turns[p];
-    float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    s_cs[t * pairs + p % V * turned + p / V] = make_float2(c * a.amplitude, s * sign);
-  }
-  __syncthreads();
-
   const int heads = a.q_heads + a.k_heads;
   const int rows = kThreads / units;
   const int u = threadIdx.x % units, r0 = threadIdx.x / units;
-  if (r0 >= rows) return;
   const bool turn = u < turned;
   // element offsets of the unit's one or two vectors
   const int e0 = turn ? (kHalf ? u * V : 2 * u * V) : 2 * pairs + (u - turned) * V;
   const int e1 = kHalf ? e0 + pairs : e0 + V;
   const int step_t = rows / heads, step_h = rows - step_t * heads;
   int t = r0 / heads, h = r0 - t * heads;
+  if (r0 >= rows) t = nt;  // threads past the last whole row
 
-  while (t < nt) {
-    Pack<T, V> x[kBatch], y[kBatch];
-    T* dst[kBatch];
-    int tok[kBatch];
+  Pack<T, V> x[kBatch], y[kBatch];
+  T* dst[kBatch];
+  int tok[kBatch];
+  auto load = [&] {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       tok[i] = t;
@@ -85,6 +68,27 @@ __global__ void __launch_bounds__(kThreads) k_rotary(RotaryLaunch r) {
         ++t;
       }
     }
+  };
+  load();  // on their way while the table is made
+
+  const float sign = a.inverse ? -a.amplitude : a.amplitude;
+  for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
+    const int t = i / pairs, p = i - t * pairs;
+    int axis = 0;
+    if (a.axes > 1) {
+      const int s1 = a.section[0], s2 = s1 + a.section[1];
+      axis = p < s1 ? 0 : (p < s2 || a.axes == 2) ? 1 : 2;
+    }
+    const int64_t at = (t0 + t) * a.position_row + axis;
+    const int64_t pos = a.positions64 ? ((const int64_t*)a.positions)[at] : (int64_t)((const int32_t*)a.positions)[at];
+    const uint64_t phase = (uint64_t)pos * (uint64_t)a.turns[p];
+    float s, c;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    s_cs[t * pairs + p % V * turned + p / V] = make_float2(c * a.amplitude, s * sign);
+  }
+  __syncthreads();
+
+  while (tok[0] < nt) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (tok[i] >= nt) break;
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(kThreads) k_rotary(RotaryLaunch r) {
         store_pack<T, V>(dst[i] + e0, x[i]);
       }
     }
+    load();
   }
 }
 

@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 namespace tb {
 
@@ -29,54 +30,85 @@ template <> struct RowType<__nv_bfloat16> {
   __device__ static __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
 };
 
-// V elements of T as one register vector: 16 bytes for V = RowType<T>::kVec,
-// one element for V = 1.
-template <class T, int V> struct alignas(V * sizeof(T)) Pack {
-  T e[V];
+// V elements of T as they lie in memory, in whole registers (an array of
+// 16-bit elements would take a register each): 16 bytes for V =
+// RowType<T>::kVec, one element for V = 1.
+template <class T, int V> struct Pack {
+  static_assert(V * sizeof(T) == 16, "16-byte vectors");
+  uint32_t w[4];
+};
+template <class T> struct Pack<T, 1> {
+  T e;
 };
 
 template <class T, int V>
 __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  Pack<T, V> r;
   if constexpr (V == 1) {
-    Pack<T, 1> r;
-    r.e[0] = *p;
-    return r;
+    r.e = *p;
   } else {
-    static_assert(sizeof(Pack<T, V>) == 16, "16-byte vectors");
-    union {
-      uint4 u;
-      Pack<T, V> v;
-    } r;
-    r.u = *reinterpret_cast<const uint4*>(p);
-    return r.v;
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
   }
+  return r;
 }
 
 template <class T, int V>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v) {
-  if constexpr (V == 1) {
-    *p = v.e[0];
-  } else {
-    union {
-      uint4 u;
-      Pack<T, V> v;
-    } r;
-    r.v = v;
-    *reinterpret_cast<uint4*>(p) = r.u;
-  }
+  if constexpr (V == 1) *p = v.e;
+  else *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+
+__device__ __forceinline__ float2 halves_of(uint32_t w, __half) {
+  __half2 h;
+  memcpy(&h, &w, 4);
+  return __half22float2(h);
+}
+__device__ __forceinline__ float2 halves_of(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t word_of(float lo, float hi, __half) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+__device__ __forceinline__ uint32_t word_of(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
 }
 
 template <class T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& v, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = RowType<T>::to(v.e);
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = RowType<T>::to(v.e[i]);
+    for (int i = 0; i < V; ++i) f[i] = __uint_as_float(v.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 x = halves_of(v.w[i], T());
+      f[2 * i] = x.x;
+      f[2 * i + 1] = x.y;
+    }
+  }
 }
 
 template <class T, int V>
 __device__ __forceinline__ Pack<T, V> pack(const float (&f)[V]) {
   Pack<T, V> r;
+  if constexpr (V == 1) {
+    r.e = RowType<T>::from(f[0]);
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) r.e[i] = RowType<T>::from(f[i]);
+    for (int i = 0; i < V; ++i) r.w[i] = __float_as_uint(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) r.w[i] = word_of(f[2 * i], f[2 * i + 1], T());
+  }
   return r;
 }
 

@@ -36,12 +36,20 @@ cudaError_t launch_rotary(const void* args, cudaStream_t s);
 struct NormLaunch {
   tb_norm_args a;
   int vec, per_row, nv, rows;  // threads of a row, vectors of a thread, rows of a block
+  int groups;                  // through shared memory by groups of rows, nv buffers deep
   int blocks;
 };
+// Shared memory of the kernels that move groups of rows: `fixed` bytes an
+// element of a row (a multiple of 16 in all), then the buffers.
+inline size_t norm_group_bytes(int width, int size, int tensors, int stages, int fixed) {
+  const size_t head = fixed == 8 ? 2 * (((size_t)width + 3) / 4 * 16) : ((size_t)width * size + 15) / 16 * 16;
+  return head + (size_t)stages * tensors * 16 * width;
+}
 cudaError_t launch_norm(const void* args, cudaStream_t s);
 struct NormBackwardLaunch {
   tb_norm_backward_args a;
   int vec, per_row, nv, rows;
+  int groups;
   int blocks;
 };
 cudaError_t launch_norm_backward(const void* args, cudaStream_t s);

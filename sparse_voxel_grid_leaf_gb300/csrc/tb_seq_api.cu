@@ -23,27 +23,39 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 bool whole(int64_t stride, int size) { return stride * size % 16 == 0; }
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Threads and vectors per row of a norm kernel.  Few rows: one vector a
-// thread, for the shortest chain of loads.  Many rows: up to `most` vectors,
-// in the shape that leaves the fewest idle lanes (the larger nv on a tie, so
-// that a row needs no barrier).
-void norm_shape(int64_t rows, int vecs, int sms, int most, const int* counts, int n, int* per_row, int* nv,
-                int* per_block) {
-  const bool many = rows >= 4ll * sms;
-  int best = -1;
-  int64_t waste = 0;
+// Threads of a row, groups of elements (vectors, or single elements) of a
+// thread and rows of a block of the norm kernels, which exist for `counts`
+// groups a thread.  One group while that takes at most `wide` threads; else
+// the fewest that take at most `most`, as joining many warps costs a wide row
+// more than it loads (rows of 4096: 16 warps a row 154 us, 4 warps 150;
+// with the 8-bit output 130 and 90).  Few rows: one group, for the shortest
+// chain of loads.
+struct NormShape {
+  int per_row, nv, rows;
+};
+NormShape norm_shape(bool many, int groups, const int* counts, int n, int wide, int most) {
+  NormShape r{};
   for (int i = 0; i < n; ++i) {
-    const int64_t threads = up(up(vecs, counts[i]), 32) * 32;
-    if (threads > 512) continue;
-    const int64_t idle = threads * counts[i] - vecs;
-    if (best < 0 || (many && counts[i] <= most && idle <= waste)) {
-      best = i;
-      waste = idle;
-      *per_row = (int)threads;
-    }
+    r.nv = counts[i];
+    r.per_row = (int)(up(up(groups, counts[i]), 32) * 32);
+    if (r.per_row <= (!many ? 512 : i == 0 ? wide : most)) break;
   }
-  *nv = counts[best];
-  *per_block = many ? (*per_row >= 256 ? 1 : 256 / *per_row) : 1;
+  r.rows = many && r.per_row < 128 ? 128 / r.per_row : 1;
+  return r;
+}
+constexpr int kVecs[] = {1, 2, 4, 8}, kOnes[] = {4, 8, 32};
+
+// Buffers for groups of rows through shared memory: two where two blocks then
+// fit a multiprocessor, else one, else none.
+int norm_stages(int width, int size, int tensors, int fixed) {
+  if (norm_group_bytes(width, size, tensors, 2, fixed) <= 100 * 1024) return 2;
+  return norm_group_bytes(width, size, tensors, 1, fixed) <= 200 * 1024 ? 1 : 0;
+}
+int64_t norm_group_blocks(int64_t rows, int width, int size, int tensors, int stages, int fixed, int sms) {
+  int64_t fit = 208 * 1024 / (int64_t)(norm_group_bytes(width, size, tensors, stages, fixed) + 1024);
+  if (fit > 8) fit = 8;
+  const int64_t groups = up(rows, 16 / size);
+  return groups < fit * sms ? groups : fit * sms;
 }
 
 }  // namespace
@@ -102,11 +114,11 @@ tb_status tb_rotary(const tb_rotary_args* args, tb_stream stream) {
   if (a.k_heads)
     r.vec = r.vec && aligned16(a.k) && aligned16(a.k_out) && whole(a.k_row, size) && whole(a.k_head, size) &&
             whole(a.k_out_row, size) && whole(a.k_out_head, size);
-  // A block's threads take 8 rows (token, head) each, unless that leaves
+  // A block's threads take 4 rows (token, head) each, unless that leaves
   // multiprocessors idle; the table stays within 16 KB.
   const int units = r.vec ? a.pairs / vec + (a.dim - 2 * a.pairs) / vec : a.dim - a.pairs;
   const int heads = a.q_heads + a.k_heads;
-  int64_t per = up(8ll * (256 / units), heads);
+  int64_t per = 4ll * (256 / units) / heads;
   const int64_t fit = 16384 / (8 * a.pairs);
   if (per > fit) per = fit;
   if (per > a.tokens / (4 * sms)) per = a.tokens / (4 * sms);
@@ -137,16 +149,31 @@ tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
   if (a.h_out) n.vec = n.vec && aligned16(a.h_out) && whole(a.h_row, size);
   if (a.fp8) n.vec = n.vec && ((uintptr_t)a.y & (vec - 1)) == 0 && a.y_row % vec == 0;
   else n.vec = n.vec && aligned16(a.y) && whole(a.y_row, size);
-  static const int kVecs[] = {1, 2, 4, 8}, kOnes[] = {8, 32};
-  if (n.vec) norm_shape(a.rows, a.width / vec, sms, 4, kVecs, 4, &n.per_row, &n.nv, &n.rows);
-  else norm_shape(a.rows, a.width, sms, 8, kOnes, 2, &n.per_row, &n.nv, &n.rows);
-  n.blocks = (int)up(a.rows, n.rows);
+  const bool many = a.rows >= 4ll * sms;
+  const int tensors = a.residual ? 2 : 1;
+  const bool dense = aligned16(a.x) && a.x_row == a.width && a.y_row == a.width && (a.fp8 || aligned16(a.y)) &&
+                     (!a.residual || (aligned16(a.residual) && a.residual_row == a.width)) &&
+                     (!a.h_out || (aligned16(a.h_out) && a.h_row == a.width));
+  const int stages = !n.vec && many && dense ? norm_stages(a.width, size, tensors, size) : 0;
+  n.groups = stages > 0;
+  if (n.groups) {
+    n.nv = stages;
+    n.per_row = n.rows = 0;
+    n.blocks = (int)norm_group_blocks(a.rows, a.width, size, tensors, stages, size, sms);
+  } else {
+    const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 256, 128) : norm_shape(many, a.width, kOnes, 3, 32, 128);
+    n.per_row = z.per_row, n.nv = z.nv, n.rows = z.rows;
+    // blocks stay: as many as run at once, twice that many where a thread has more than a vector
+    const int64_t fit = up(z.nv <= 1 ? 1024 : 2048, n.per_row * n.rows), blocks = up(a.rows, n.rows);
+    n.blocks = (int)(blocks < sms * fit ? blocks : sms * fit);
+  }
   TB_SEQ_CUDA(seq_launch(kSeqNorm, (cudaStream_t)stream, launch_norm, &n));
   return TB_OK;
 }
 
+// Each block writes a part of dweight, which is read once more.
 static int64_t norm_backward_blocks(int64_t rows, int sms) {
-  const int64_t most = 4ll * sms;
+  const int64_t most = 6ll * sms;
   return rows < most ? rows : most;
 }
 
@@ -177,12 +204,28 @@ tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stre
   n.vec = a.width % vec == 0 && aligned16(a.dy) && aligned16(a.h) && aligned16(a.weight) && aligned16(a.dx) &&
           whole(a.dy_row, size) && whole(a.h_row, size) && whole(a.dx_row, size);
   if (a.dh) n.vec = n.vec && aligned16(a.dh) && whole(a.dh_row, size);
-  static const int kVecs[] = {1, 2, 4, 8}, kOnes[] = {8, 32};
-  if (n.vec) norm_shape(a.rows, a.width / vec, sms, 4, kVecs, 4, &n.per_row, &n.nv, &n.rows);
-  else norm_shape(a.rows, a.width, sms, 8, kOnes, 2, &n.per_row, &n.nv, &n.rows);
-  // a block's parts of dweight meet in shared memory
-  while (n.rows > 1 && (int64_t)n.rows * n.per_row * n.nv * (n.vec ? vec : 1) * 4 > 40 * 1024) n.rows /= 2;
-  const int64_t blocks = up(a.rows, n.rows);
+  const bool many = a.rows >= 4ll * sms;
+  const int tensors = a.dh ? 3 : 2;
+  const bool dense = aligned16(a.dy) && aligned16(a.h) && aligned16(a.dx) && a.dy_row == a.width && a.h_row == a.width &&
+                     a.dx_row == a.width && (!a.dh || (aligned16(a.dh) && a.dh_row == a.width));
+  const int stages = !n.vec && many && dense ? norm_stages(a.width, size, tensors, 8) : 0;
+  int64_t blocks;
+  n.groups = stages > 0;
+  if (n.groups) {
+    n.nv = stages;
+    n.per_row = n.rows = 0;
+    blocks = norm_group_blocks(a.rows, a.width, size, tensors, stages, 8, sms);
+  } else {
+    // dweight takes registers: up to two vectors a thread while the row fits 512
+    const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 256, 512)
+                              : norm_shape(many, a.width, kOnes + 1, 2, 128, 128);
+    n.per_row = z.per_row, n.nv = z.nv, n.rows = z.rows;
+    // a block's parts of dweight meet in shared memory
+    while (n.rows > 1 && (int64_t)n.rows * n.per_row * n.nv * (n.vec ? vec : 1) * 4 > 40 * 1024) n.rows /= 2;
+    const int64_t fit = sms * up(768, n.per_row * n.rows);
+    blocks = up(a.rows, n.rows);
+    if (blocks > fit) blocks = fit;
+  }
   n.blocks = (int)(blocks < most ? blocks : most);
   if (a.rows) TB_SEQ_CUDA(seq_launch(kSeqNormBackward, (cudaStream_t)stream, launch_norm_backward, &n));
   TB_SEQ_CUDA(seq_launch(kSeqNormWeight, (cudaStream_t)stream, launch_norm_weight, &n));
