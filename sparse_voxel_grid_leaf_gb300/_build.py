@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libtb.so")
 SEQ = os.path.join(HERE, "_seq.so")
 SOURCES = ["tb_api.cu", "tb_prepass.cu", "tb_chain.cu", "tb_noalloc.cu", "tb_kmap.cu",
            "tb_seq_api.cu", "tb_rotary.cu", "tb_norm.cu", "tb_linattn.cu",
-           "tb_linattn_chunk.cu"]
+           "tb_linattn_chunk.cu", "tb_linattn_split.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -82,7 +82,8 @@ const char* const kKernelNames[kKNumKinds] = {"prepass_leaves", "chain",        
                                               "kernel_map",    "kmap_prep",    "export",        "member",
                                               "rotary",        "norm",         "norm_backward", "norm_weight",
                                               "linear_step",   "linear_scan",  "linear_scan_states",
-                                              "linear_chunks", "linear_chunk_states", "linear_combine"};
+                                              "linear_chunks", "linear_chunk_states", "linear_split", "linear_split_states",
+                                              "linear_combine"};
 
 struct ProfRec {
   int kind;

@@ -36,19 +36,14 @@
 #include "tb_linattn.cuh"
 #include "tb_linattn_scan.cuh"
 #include "tb_seq.cuh"
-#include "tb_tc.cuh"
+#include "tb_linattn_tc.cuh"
 
 namespace tb {
 namespace {
 
-constexpr int kC = 64;            // rows of a chunk
-constexpr int kTile = 8192;       // 64 rows x 128 bytes
 constexpr int kOutTile = 4096;    // 64 rows x 64 bytes
 constexpr int kStages = 3;
 constexpr int kStageBytes = 6 * kTile;  // two tiles each of A, B, C
-// decay^32 within 2^50: half of the exponents that 32-bit floats have are left
-// to the values.
-constexpr float kSteep = 0.34f;
 // Warps: 8 of the state, the copies, the products, 2 of the scores (lanes 64 to
 // 127), 4 of the output, and for pairs of heads 2 more of the scores.  Sixteen
 // leave 128 registers a thread, which the state of 128 keys and the blocks of W
@@ -76,34 +71,6 @@ struct Shared {
   __align__(8) float o[2][2][2 * kC + 2];  // mul decay^(m-31), reverse: mul decay^(32-m)
   uint2 w2[2][2][kC + 1];                  // rows 2 m, 2 m + 1 of w as bfloat16 pairs: the value, and what it leaves
 };
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-__device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-__device__ __forceinline__ float shared_bf16(uint32_t at) {
-  uint16_t bits;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));
-  return __uint_as_float((uint32_t)bits << 16);
-}
-__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
-// Element x of row r in a tile of 64-element rows.
-__device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int x) {
-  return tile + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + (x & 7) * 2;
-}
 
 // Adds the scores times c_j of the rows j whose value is not finite to the
 // rows i that see them, in a warp's staged output of 32 values (the product

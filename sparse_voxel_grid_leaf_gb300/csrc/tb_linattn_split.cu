@@ -1,0 +1,598 @@
+// Linear attention with a decay for each head on the tensor cores for rows in
+// 32 or 16 bits of any type, stride and head size up to 128: the chunks of
+// tb_linattn_chunk.cu with every operand split into kTerms bfloat16 terms.
+//
+// A float is the sum of three bfloat16 terms (24 bits), a half of two (11
+// bits).  Three terms: the six products of terms whose ranks add up to two or
+// less leave 2^-24 of a product out, so sums keep 32-bit accuracy; two terms:
+// three products, 2^-16, for 16-bit outputs.  Scores, W = decayed values and
+// the state are split the same way as they become operands.  Six products in
+// place of one still are a third of what the recurrence costs in packed
+// 32-bit multiply-adds (64 rows of 128 keys and values: 7200 clocks of the
+// tensor cores, 24600 of the FP32 pipes).
+//
+// A block walks one segment of one head.  Three warps read rows, split them
+// and lay them out as tiles; one thread issues the products; 8 warps hold the
+// state and make W, straight from memory (a lane is a value); 4 warps take the
+// scores (lanes 64 to 127) and then the output, which lies in the columns that
+// the scores leave.
+#include "tb_linattn_tc.cuh"
+
+namespace tb {
+namespace {
+
+constexpr int kThreads = 512;
+// 8 warps of the state and W, 3 of the rows, the products, 4 of the scores and the output
+constexpr int kWarpLoad = 8, kLoadWarps = 3, kWarpMma = 11;
+
+__device__ unsigned int g_gave_up;
+
+enum Bars {
+  kFull = 0, kEmpty = kFull + 2, kSReady = kEmpty + 2, kSFull, kWFull, kWFree, kKvReady, kKvFree, kStFull, kStFree,
+  kOReady, kOFree, kDrain, kBars
+};
+
+struct Shared {
+  uint64_t bar[kBars];
+  uint32_t tmem;
+  volatile uint32_t gave_up;
+  volatile uint32_t bad[2];  // chunk + 1 whose values are not all finite, by the chunk's parity
+  LinSegment seg;
+  float w[2 * kC];           // fold decay^(31-m), reverse: fold decay^(m-32); 0 past the 64th
+  float o[2 * kC];           // mul decay^(m-31), reverse: mul decay^(32-m)
+};
+
+// Eight elements from x on, as floats: a vector or two, or one by one up to
+// `left` of them.
+__device__ __forceinline__ void load8(float (&f)[8], const void* x, int64_t at, int type, bool vec, int left) {
+  if (vec) {
+    if (type == TB_TYPE_F32) {
+      const float4 a = *reinterpret_cast<const float4*>((const float*)x + at);
+      const float4 b = *reinterpret_cast<const float4*>((const float*)x + at + 4);
+      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)x + at);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = type == TB_TYPE_F16 ? halves_of(w[i], __half()) : halves_of(w[i], __nv_bfloat16());
+        f[2 * i] = y.x;
+        f[2 * i + 1] = y.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f[i] = i >= left                ? 0.f
+             : type == TB_TYPE_F32    ? ((const float*)x)[at + i]
+             : type == TB_TYPE_F16    ? __half2float(((const __half*)x)[at + i])
+                                      : __bfloat162float(((const __nv_bfloat16*)x)[at + i]);
+  }
+}
+__device__ __forceinline__ float load1(const void* x, int64_t at, int type) {
+  return type == TB_TYPE_F32   ? ((const float*)x)[at]
+         : type == TB_TYPE_F16 ? __half2float(((const __half*)x)[at])
+                               : __bfloat162float(((const __nv_bfloat16*)x)[at]);
+}
+__device__ __forceinline__ void store1(void* x, int64_t at, int type, float f) {
+  if (type == TB_TYPE_F32) ((float*)x)[at] = f;
+  else if (type == TB_TYPE_F16) ((__half*)x)[at] = __float2half_rn(f);
+  else ((__nv_bfloat16*)x)[at] = __float2bfloat16_rn(f);
+}
+
+// The next term of a pair of floats, taken off them.
+__device__ __forceinline__ uint32_t take_term(f32x2& e) {
+  const uint32_t x = bf16x2(halves(e).x, halves(e).y);
+  e = fma2(pair(low(x), high(x)), pair(-1.f, -1.f), e);
+  return x;
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Rows j whose value is not finite, which W has zeros for: their scores times
+// the value join the rows i that see them, in the output as this thread wrote it.
+__device__ __noinline__ void add_not_finite_split(const LinProblem& p, int type, int64_t row0, int h, int v, int n,
+                                                  uint32_t scores, int terms) {
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const float c = load1(p.c, (row0 + j) * p.c_row + h * p.c_head + v, type);
+    if (!not_finite(c)) continue;
+#pragma unroll 1
+    for (int i = p.reverse ? 0 : j; i <= (p.reverse ? j : n - 1); ++i) {
+      float s = 0.f;
+      for (int t = 0; t < terms; ++t) s += shared_bf16(tile_at(scores + t * kTile, i, j));
+      const int64_t at = (row0 + i) * p.o_row + h * p.o_head + v;
+      store1(p.out, at, type, fmaf(s, c, load1(p.out, at, type)));
+    }
+  }
+}
+// And b_j c_j the state's update.
+__device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, int type, int64_t row0, int h, int v, int n,
+                                                        uint32_t columns, int key, int keys) {
+#pragma unroll 1
+  for (int k0 = 0; k0 < keys; k0 += 16) {
+    uint32_t y[16];
+    tmem_ld16(columns + k0, y);
+    tmem_wait_ld();
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float c = v < p.V ? load1(p.c, (row0 + j) * p.c_row + h * p.c_head + v, type) : 0.f;
+      if (!not_finite(c)) continue;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = key + k0 + i;
+        if (k < p.K)
+          y[i] = __float_as_uint(
+              fmaf(load1(p.b, (row0 + j) * p.b_row + h * p.b_head + k, type), c, __uint_as_float(y[i])));
+      }
+    }
+    __syncwarp();
+    tmem_st16(columns + k0, y);
+  }
+  tmem_wait_st();
+}
+
+template <class T>
+__device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, const LinSegment& seg, int h,
+                                       float* s_rows) {
+  scan_walk<T, 32>(l, p, seg, h, s_rows, 256);
+}
+
+// kStates: the states of segments alone, without outputs.
+template <int kTerms, bool kStates>
+__global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ LinLaunch l) {
+  constexpr uint32_t kColS = 0, kColKv = 64, kColW = 192, kColZ = kColW + 32 * kTerms;
+  static_assert(kColZ + 64 * kTerms <= 512, "tensor memory");
+  constexpr int kStageBytes = 2 * kTerms * 2 * kTile;  // A, B: terms of two 64-key blocks
+  constexpr int kProducts = kTerms == 3 ? 6 : 3;
+
+  extern __shared__ char s_raw[];
+  __shared__ Shared s;
+  // score tiles of each term, then the stages (the product A B^T reads the 8 KB before A too)
+  const uint32_t tiles = (smem_addr(s_raw) + 1023) & ~1023u;
+  const uint32_t stage0 = tiles + kTerms * kTile;
+
+  const int slot0 = blockIdx.x / (l.heads * l.n), walk = blockIdx.x % (l.heads * l.n);
+  const LinProblem& p = l.p[walk / l.heads];
+  const int h = walk % l.heads;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return smem_addr(&s.bar[i]); };
+  const bool reverse = p.reverse;
+  const float decay = l.decay[h];
+  const bool steep = !(decay >= kSteep && decay <= 1.f / kSteep);
+  const int type = l.type;
+
+  if (warp == 0) {
+    const LinSegment seg = lin_segment(l, l.sorted ? lin_grid_of_rank(l, slot0) : slot0);
+    if (lane == 0) s.seg = seg;
+  } else if (warp == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(kFull + i), kLoadWarps);
+        mbar_init(bar(kEmpty + i), 1);
+      }
+      mbar_init(bar(kSReady), 1);
+      mbar_init(bar(kSFull), 2);
+      mbar_init(bar(kWFull), 8);
+      mbar_init(bar(kWFree), 1);
+      mbar_init(bar(kKvReady), 1);
+      mbar_init(bar(kKvFree), 8);
+      mbar_init(bar(kStFull), 8);
+      mbar_init(bar(kStFree), 1);
+      mbar_init(bar(kOReady), 1);
+      mbar_init(bar(kOFree), 4);
+      mbar_init(bar(kDrain), 1);
+      s.gave_up = 0;
+      s.bad[0] = s.bad[1] = 0;
+      fence_mbar_init();
+    }
+  } else if (warp == kWarpMma) {
+    tmem_alloc(smem_addr(&s.tmem), 512);
+  } else if (warp >= 4 && warp < 8 && !steep) {
+    const int m = threadIdx.x - 128;
+    const float log = log2f(decay), x = reverse ? (float)(m - 32) : (float)(31 - m);
+    s.w[m] = m < kC ? p.fold * exp2f(x * log) : 0.f;
+    s.o[m] = m < kC ? p.mul * exp2f(-x * log) : 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  const LinSegment seg = s.seg;
+  const uint32_t tmem = s.tmem;
+  // a slot without a segment, or a segment whose state nobody reads
+  const bool idle = seg.grid < 0 || (kStates && seg.index + 1 == seg.count && !p.last);
+  const int chunks = idle || steep ? 0 : (seg.len + kC - 1) / kC;
+  auto rows_of = [&](int t) { return min(kC, seg.len - t * kC); };
+  auto row_of = [&](int t) {
+    return reverse ? seg.end - seg.first - (int64_t)t * kC - rows_of(t) : seg.begin + seg.first + (int64_t)t * kC;
+  };
+  auto wait = [&](int i, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1, &s.gave_up));
+  };
+  auto arrive = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(i));
+  };
+  const int keys = p.K > 64 ? 128 : 64;  // of the tiles
+  const int quarter = warp & 3, v = quarter * 32 + lane;
+  const bool live = quarter * 32 < p.V;  // warp-uniform
+  const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
+  // the tiles of a stage: term x of A, of B
+  auto tile_a = [&](uint32_t at, int x) { return at + x * 2 * kTile; };
+  auto tile_b = [&](uint32_t at, int x) { return at + (kTerms + x) * 2 * kTile; };
+
+  if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
+    // ---------------------------------------------------------------- rows
+    const int groups = keys / 8, total = (kStates ? 1 : 2) * kC * groups;
+#pragma unroll 1
+    for (int t = 0; t < chunks; ++t) {
+      if (t >= 2 && !wait(kEmpty + (t & 1), t / 2 - 1)) break;
+      const uint32_t at = stage0 + (t & 1) * kStageBytes;
+      const int n = rows_of(t);
+      const int64_t row0 = row_of(t);
+      constexpr int kBatch = 4;
+#pragma unroll 1
+      for (int i0 = threadIdx.x - kWarpLoad * 32; i0 < total; i0 += kBatch * kLoadWarps * 32) {
+        float f[kBatch][8];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kLoadWarps * 32;
+          const bool is_b = i < kC * groups;
+          const int r = (is_b ? i : i - kC * groups) / groups, k = (i % groups) * 8;
+          if (i < total && r < n && k < p.K) {
+            const int64_t row = row0 + r;
+            if (is_b) load8(f[b], p.b, row * p.b_row + h * p.b_head + k, type, p.vec & 2, p.K - k);
+            else load8(f[b], p.a, row * p.a_row + h * p.a_head + k, type, p.vec & 1, p.K - k);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[b][j] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kLoadWarps * 32;
+          if (i >= total) break;
+          const bool is_b = i < kC * groups;
+          const int r = (is_b ? i : i - kC * groups) / groups, c = i % groups;
+          const uint32_t to = (is_b ? tile_b(at, 0) : tile_a(at, 0)) + (c >> 3) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          f32x2 e[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[j] = pair(f[b][2 * j], f[b][2 * j + 1]);
+#pragma unroll
+          for (int x = 0; x < kTerms; ++x) {
+            uint32_t y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = take_term(e[j]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + x * 2 * kTile), "r"(y[0]), "r"(y[1]),
+                         "r"(y[2]), "r"(y[3])
+                         : "memory");
+          }
+        }
+      }
+      fence_async_smem();
+      arrive(kFull + (t & 1));
+    }
+  } else if (warp == kWarpMma) {
+    if (chunks && elect_one()) {
+      const uint32_t kv_desc = mma_desc(128, 64, true) + (keys > 64 ? (uint32_t)(64 / 8) << 17 : 0u);
+      constexpr uint32_t kRowDesc = mma_desc(128, kC, false);
+      auto one = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1, &s.gave_up); };
+      // the products of terms x and y of the left and the right operand, the largest last
+      auto left_term = [](int i) { return kTerms == 3 ? (i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0) : i == 0 ? 1 : 0; };
+      auto right_term = [](int i) { return kTerms == 3 ? (i == 1 ? 2 : i == 2 || i == 4 ? 1 : 0) : i == 1 ? 1 : 0; };
+      const int steps = keys / 16;
+      bool ok = true;
+#pragma unroll 1
+      for (int t = 0; ok && t < chunks; ++t) {
+        const uint32_t at = stage0 + (t & 1) * kStageBytes;
+        ok = one(kFull + (t & 1), t >> 1);
+        if (!kStates) {
+          // A B^T, rows i in lanes 64 to 127
+          ok = ok && (t == 0 || one(kOFree, t - 1));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < kProducts; ++i)
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k) {
+              const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
+              mma_ss(tmem + kColS, smem_desc(tile_a(at, left_term(i)) - kTile + off, 16),
+                     smem_desc(tile_b(at, right_term(i)) + off, 16), kRowDesc, i > 0 || k > 0);
+            }
+          mma_commit(bar(kSReady));
+        }
+        // W^T B
+        ok = ok && one(kWFull, t) && (t == 0 || one(kKvFree, t - 1));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < kProducts; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_ts(tmem + kColKv, tmem + kColW + left_term(i) * 32 + j * 8,
+                   smem_desc(tile_b(at, right_term(i)) + j * 2048, kTile), kv_desc, i > 0 || j > 0);
+        mma_commit(bar(kKvReady));
+        if (!kStates) {
+          // Z^T A^T, where the scores were
+          ok = one(kStFull, t) && one(kSFull, t);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < kProducts; ++i)
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              mma_ts(tmem + kColS, tmem + kColZ + left_term(i) * 64 + k * 8,
+                     smem_desc(tile_a(at, right_term(i)) + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, i > 0 || k > 0);
+          mma_commit(bar(kStFree));
+          // W^T scores^T
+#pragma unroll 1
+          for (int i = 0; i < kProducts; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_ts(tmem + kColS, tmem + kColW + left_term(i) * 32 + j * 8,
+                     smem_desc(tiles + right_term(i) * kTile + j * 32, 16), kRowDesc, true);
+          mma_commit(bar(kOReady));
+        }
+        mma_commit(bar(kWFree));
+        mma_commit(bar(kEmpty + (t & 1)));
+      }
+      if (!ok) {  // products in flight finish before tensor memory is given back
+        uint32_t flag = 0;
+        mma_commit(bar(kDrain));
+        mbar_wait(bar(kDrain), 0, &flag);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ state, W
+    const int half = warp >> 2, own = keys / 2;  // keys of a thread
+    const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
+    float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
+    const float log = log2f(decay);
+    const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
+    f32x2 u[32];  // Z, by pairs of keys
+    {
+      const float* from = l.phase == 2 ? seg_state : p.first ? p.first + state_at : nullptr;
+      const int64_t step = l.phase == 2 ? p.V : p.first_k;
+      const int left = kStates || idle || steep || !from || v >= p.V ? 0 : min(own, p.K - half * own);
+      if (from) from += half * own * step + v * (l.phase == 2 ? 1 : p.first_v);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2, from += 2 * step)
+        u[i / 2] = pair(i < left ? from[0] * enter : 0.f, i + 1 < left ? from[step] * enter : 0.f);
+    }
+    float c[32];  // this thread's value of its half of a chunk's rows
+#pragma unroll 1
+    for (int t = -1; t < chunks; ++t) {
+      const int x = t + 1;
+      const bool more = x < chunks;
+      if (more) {
+        const int n = rows_of(x);
+        const int64_t at = (row_of(x) + half * 32) * p.c_row + h * p.c_head + v;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          c[i] = half * 32 + i < n && v < p.V ? load1(p.c, at + i * p.c_row, type) : 0.f;
+      }
+      if (t >= 0) {
+        // the state after this chunk
+        const int n = rows_of(t);
+        if (!wait(kKvReady, t)) break;
+        tc_fence_after();
+        const float d = t + 1 < chunks ? full : exp2f((float)(n - (reverse ? 31 : 32)) * log);
+        if (live) {
+          const uint32_t columns = lanes + kColKv + half * own;
+          if (s.bad[t & 1] == (uint32_t)t + 1)
+            add_not_finite_state_split(p, type, row_of(t), h, v, n, columns, half * own, own);
+          const f32x2 d2 = pair(d, d);
+#pragma unroll
+          for (int k0 = 0; k0 < 64; k0 += 16) {
+            if (k0 >= own) break;
+            uint32_t z[16];
+            tmem_ld16(columns + k0, z);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              u[(k0 + i) / 2] = mul2(add2(u[(k0 + i) / 2], pair(__uint_as_float(z[i]), __uint_as_float(z[i + 1]))), d2);
+          }
+        }
+        tc_fence_before();
+        arrive(kKvFree);
+      }
+      if (!kStates && more) {
+        // Z^T as the next chunk's operand
+        if (x > 0 && !wait(kStFree, x - 1)) break;
+        tc_fence_after();
+        if (live) {
+#pragma unroll
+          for (int k0 = 0; k0 < 64; k0 += 16) {
+            if (k0 >= own) break;
+            f32x2 e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = u[k0 / 2 + i];
+#pragma unroll
+            for (int y = 0; y < kTerms; ++y) {
+              uint32_t z[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[i] = take_term(e[i]);
+              tmem_st8(lanes + kColZ + y * 64 + (half * own + k0) / 2, z);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        arrive(kStFull);
+      }
+      if (more) {
+        // W^T, in its one buffer once the last chunk's products are done with it
+        if (x > 0 && !wait(kWFree, x - 1)) break;
+        tc_fence_after();
+        if (live) {
+          const int n = rows_of(x);
+          const float* w = s.w + (reverse ? kC - n : 0) + half * 32;
+          float finite = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) finite = fmaf(c[i], 0.f, finite);
+          if (finite != finite) {
+            // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
+            // warps of the output and of the state add these values to what sees them
+#pragma unroll
+            for (int i = 0; i < 32; ++i) c[i] = not_finite(c[i]) ? 0.f : c[i];
+            s.bad[x & 1] = x + 1;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 16) {
+            f32x2 e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              e[i] = mul2(pair(c[r0 + 2 * i], c[r0 + 2 * i + 1]), pair(w[r0 + 2 * i], w[r0 + 2 * i + 1]));
+#pragma unroll
+            for (int y = 0; y < kTerms; ++y) {
+              uint32_t z[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[i] = take_term(e[i]);
+              tmem_st8(lanes + kColW + y * 32 + half * 16 + r0 / 2, z);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        arrive(kWFull);
+      }
+    }
+    float* dst = kStates ? seg_state : l.phase == 0 && p.last ? p.last + state_at : nullptr;
+    if (!idle && !steep && dst && !s.gave_up && v < p.V) {
+      dst += half * own * p.V + v;
+      const int left = min(own, p.K - half * own);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2, dst += 2 * p.V) {
+        if (i < left) dst[0] = halves(u[i / 2]).x;
+        if (i + 1 < left) dst[p.V] = halves(u[i / 2]).y;
+      }
+    }
+  } else if (!kStates) {
+    // ------------------------------------------------------ scores, output
+#pragma unroll 1
+    for (int t = 0; t < chunks; ++t) {
+      const int n = rows_of(t);
+      if (quarter >= 2) {
+        const int i = (quarter - 2) * 32 + lane;
+        if (!wait(kSReady, t)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int j0 = 0; j0 < kC; j0 += 16) {
+          uint32_t x[16];
+          tmem_ld16(lanes + kColS + j0, x);
+          tmem_wait_ld();
+          f32x2 e[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int k = j0 + 2 * j;
+            e[j] = pair((reverse ? k >= i : k <= i) ? __uint_as_float(x[2 * j]) : 0.f,
+                        (reverse ? k + 1 >= i : k + 1 <= i) ? __uint_as_float(x[2 * j + 1]) : 0.f);
+          }
+#pragma unroll
+          for (int y = 0; y < kTerms; ++y) {
+            uint32_t z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = take_term(e[j]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               tiles + y * kTile + i * 128 + (((j0 / 8 + q) ^ (i & 7)) << 4)),
+                           "r"(z[4 * q]), "r"(z[4 * q + 1]), "r"(z[4 * q + 2]), "r"(z[4 * q + 3])
+                           : "memory");
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        arrive(kSFull);
+      }
+      if (!wait(kOReady, t)) break;
+      tc_fence_after();
+      if (live) {
+        uint32_t x[4][16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld16(lanes + kColS + 16 * i, x[i]);
+        tmem_wait_ld();
+        const bool bad = s.bad[t & 1] == (uint32_t)t + 1;
+        if (!bad) {
+          tc_fence_before();
+          arrive(kOFree);
+        }
+        const int64_t row0 = row_of(t);
+        const float* w = s.o + (reverse ? kC - n : 0);
+        if (v < p.V) {
+          int64_t at = row0 * p.o_row + h * p.o_head + v;
+#pragma unroll
+          for (int i = 0; i < kC; ++i, at += p.o_row)
+            if (i < n) store1(p.out, at, type, __uint_as_float(x[i / 16][i % 16]) * w[i]);
+          if (bad) add_not_finite_split(p, type, row0, h, v, n, tiles, kTerms);
+        }
+        __syncwarp();
+        if (bad) {
+          tc_fence_before();
+          arrive(kOFree);
+        }
+      } else {
+        tc_fence_before();
+        arrive(kOFree);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
+  if (warp == kWarpMma) tmem_free(tmem, 512);
+  if (!steep || idle || warp >= 8) return;
+  float* rows = reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw)));
+  if (type == TB_TYPE_F32) walk_rows<float>(l, p, s.seg, h, rows);
+  else if (type == TB_TYPE_F16) walk_rows<__half>(l, p, s.seg, h, rows);
+  else walk_rows<__nv_bfloat16>(l, p, s.seg, h, rows);
+}
+
+template <int kTerms, bool kStates>
+cudaError_t go(const LinLaunch& l, cudaStream_t s) {
+  constexpr int bytes = 1024 + kTerms * kTile + 2 * 2 * kTerms * 2 * kTile;
+  static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
+  static bool ready[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(k_split<kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev] = true;
+  }
+  const int64_t blocks = (int64_t)l.segments * l.heads * l.n;
+  k_split<kTerms, kStates><<<(unsigned)blocks, kThreads, bytes, s>>>(l);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_split(const void* args, cudaStream_t s) {
+  const LinLaunch& l = *(const LinLaunch*)args;
+  bool exact = l.type == TB_TYPE_F32;  // 32-bit outputs
+  for (int i = 0; i < l.n; ++i) exact = exact || (l.p[i].last && l.phase != 2);
+  if (l.phase == 1) return exact ? go<3, true>(l, s) : go<2, true>(l, s);
+  return exact ? go<3, false>(l, s) : go<2, false>(l, s);
+}
+
+cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up) {
+  void* at = nullptr;
+  unsigned int got = 0;
+  cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&got, at, sizeof got, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof got, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  *gave_up = got != 0;
+  return e;
+}
+
+}  // namespace tb

@@ -13,7 +13,7 @@ namespace tb {
 // Kernel kinds of tb_profile_read, continued by the sequence operators.
 enum SeqKernel {
   kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqScanStates,
-  kSeqChunks, kSeqChunkStates, kSeqCombine, kSeqNumKernels
+  kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqNumKernels
 };
 
 // Every launch of a sequence operator is counted, and timed when profiling is
@@ -84,6 +84,7 @@ struct LinProblem {
   float* seg;                 // [segments, H, K, V]: states of the segments of a split call
   float mul, fold;
   int32_t reverse, late;
+  int32_t vec;                // rows of a (1) and b (2) that 16-byte vectors of 8 elements can read
 };
 constexpr int kLinMaxProblems = 3;
 struct LinLaunch {
@@ -114,7 +115,10 @@ struct ChunkLaunch {
 // Completes g for its g.l; false where the chunk kernel does not take the rows.
 bool linear_chunk_plan(ChunkLaunch& g);
 cudaError_t launch_linear_chunks(const void* args, cudaStream_t s);
-// Whether a bounded wait of the chunk kernel gave up since the last call.  Blocks.
+// The same chunks for any rows, as sums of bfloat16 terms (tb_linattn_split.cu).
+cudaError_t launch_linear_split(const void* args, cudaStream_t s);
+// Whether a bounded wait of a chunk kernel gave up since the last call.  Blocks.
+cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up);
 cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up);
 cudaError_t launch_linear_scan(const void* args, cudaStream_t s);
 cudaError_t launch_linear_combine(const void* args, cudaStream_t s);

@@ -243,12 +243,12 @@ struct LinSizes {
 // a grid, so a call with few grids and heads is split along the rows: the
 // segments' own states first, their joining, then the outputs.  The states
 // pass reads the keys and values once more, and pays where it fills the
-// multiprocessors: one block of the chunk kernel (16-bit rows; of two heads,
-// where they are small) runs on each, four of the recurrence.
+// multiprocessors: one block of a chunk kernel (of two heads, where they are
+// small) runs on each.
 static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
-  const bool chunks = z.type == TB_TYPE_BF16;
-  const int64_t heads = chunks && linear_pairs(z.heads, z.key, z.value) ? (z.heads + 1) / 2 : z.heads;
-  const int64_t walks = heads * problems, want = (chunks ? 2ll : 4ll) * sms;
+  const bool pairs = z.type == TB_TYPE_BF16 && linear_pairs(z.heads, z.key, z.value);
+  const int64_t heads = pairs ? (z.heads + 1) / 2 : z.heads;
+  const int64_t walks = heads * problems, want = 2ll * sms;
   if (z.grids <= 0 || z.grids * walks >= want) return 0;
   int64_t seg = up(up(z.tokens * walks, want), 64) * 64;
   if (seg < 256) seg = 256;
@@ -303,19 +303,29 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaun
                       (long long)a.workspace_bytes, (long long)(one * 4 * l.n));
     for (int i = 0; i < l.n; ++i) l.p[i].seg = (float*)a.workspace + i * one;
   }
-  // A chunk of 64 rows costs the tensor cores the same with one row in it.
-  const bool chunks = a.tokens >= 16ll * a.grids && linear_chunk_plan(g);
+  // A chunk of 64 rows costs the tensor cores the same with one row in it: short grids take the recurrence.
+  const bool longer = a.tokens >= 16ll * a.grids;
+  const bool chunks = longer && linear_chunk_plan(g);
+  for (int i = 0; i < l.n; ++i) {
+    LinProblem& p = l.p[i];
+    const int size = type_size(a.type);
+    p.vec = p.K % 8 == 0 ? (aligned16(p.a) && whole(p.a_row, size) && whole(p.a_head, size) ? 1 : 0) |
+                               (aligned16(p.b) && whole(p.b_row, size) && whole(p.b_head, size) ? 2 : 0)
+                         : 0;
+  }
   l.phase = 0;
   // With more walks than multiprocessors the last to start should be short ones.
   l.sorted = !l.segment && a.grids > 1 && a.grids <= kLinMaxSorted && (int64_t)a.grids * a.heads * l.n > sms;
   if (l.segment) {
     l.phase = 1;
     if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunkStates, s, launch_linear_chunks, &g));
+    else if (longer) TB_SEQ_CUDA(seq_launch(kSeqSplitStates, s, launch_linear_split, &l));
     else TB_SEQ_CUDA(seq_launch(kSeqScanStates, s, launch_linear_scan, &l));
     TB_SEQ_CUDA(seq_launch(kSeqCombine, s, launch_linear_combine, &l));
     l.phase = 2;
   }
   if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunks, s, launch_linear_chunks, &g));
+  else if (longer) TB_SEQ_CUDA(seq_launch(kSeqSplit, s, launch_linear_split, &l));
   else TB_SEQ_CUDA(seq_launch(kSeqScan, s, launch_linear_scan, &l));
   return TB_OK;
 }
@@ -395,6 +405,9 @@ tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_s
 tb_status tb_linear_attention_status(tb_stream stream) {
   bool gave_up = false;
   TB_SEQ_CUDA(linear_gave_up((cudaStream_t)stream, &gave_up));
+  bool split = false;
+  TB_SEQ_CUDA(linear_split_gave_up((cudaStream_t)stream, &split));
+  gave_up = gave_up || split;
   if (gave_up) return seq_fail(TB_ERR_DEVICE_TIMEOUT, "tb_linear_attention: a device-side wait timed out");
   return TB_OK;
 }
