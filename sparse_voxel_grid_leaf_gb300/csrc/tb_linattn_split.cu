@@ -42,42 +42,60 @@ struct Shared {
   float o[2 * kC];           // mul decay^(m-31), reverse: mul decay^(32-m)
 };
 
-// Eight elements from x on, as floats: a vector or two, or one by one up to
-// `left` of them.
-__device__ __forceinline__ void load8(float (&f)[8], const void* x, int64_t at, int type, bool vec, int left) {
+// Elements of E: floats, or 16 bits that are halves or bfloat16 numbers by
+// `half` (the loads are the same, and what differs is outside their loops).
+template <class E>
+__device__ __forceinline__ float value(E x, bool half) {
+  if constexpr (sizeof(E) == 4) return x;
+  else return half ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+}
+template <class E>
+__device__ __forceinline__ float load1(const void* x, int64_t at, bool half) {
+  return value<E>(((const E*)x)[at], half);
+}
+template <class E>
+__device__ __forceinline__ void store1(void* x, int64_t at, bool half, float f) {
+  if constexpr (sizeof(E) == 4) ((E*)x)[at] = f;
+  else ((E*)x)[at] = half ? __half_as_ushort(__float2half_rn(f)) : (E)(bf16x2(f, f) & 0xffffu);
+}
+// Eight elements: one 16-byte vector or two.
+template <class E>
+struct Eight {
+  uint4 w[sizeof(E) / 2];
+};
+template <class E>
+__device__ __forceinline__ void load8(Eight<E>& r, const E* x, bool vec, int left) {
   if (vec) {
-    if (type == TB_TYPE_F32) {
-      const float4 a = *reinterpret_cast<const float4*>((const float*)x + at);
-      const float4 b = *reinterpret_cast<const float4*>((const float*)x + at + 4);
-      f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>((const uint16_t*)x + at);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = type == TB_TYPE_F16 ? halves_of(w[i], __half()) : halves_of(w[i], __nv_bfloat16());
-        f[2 * i] = y.x;
-        f[2 * i + 1] = y.y;
-      }
-    }
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4*>(x) + i);
   } else {
+    auto bits = [&](int i) -> uint32_t {
+      if (i >= left) return 0u;
+      if constexpr (sizeof(E) == 4) return __float_as_uint(x[i]);
+      else return x[i];
+    };
+    auto word = [&](int i) { return sizeof(E) == 4 ? bits(i) : bits(2 * i) | bits(2 * i + 1) << 16; };
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = i >= left                ? 0.f
-             : type == TB_TYPE_F32    ? ((const float*)x)[at + i]
-             : type == TB_TYPE_F16    ? __half2float(((const __half*)x)[at + i])
-                                      : __bfloat162float(((const __nv_bfloat16*)x)[at + i]);
+    for (int i = 0; i < (int)sizeof(E) / 2; ++i)
+      r.w[i] = make_uint4(word(4 * i), word(4 * i + 1), word(4 * i + 2), word(4 * i + 3));
   }
 }
-__device__ __forceinline__ float load1(const void* x, int64_t at, int type) {
-  return type == TB_TYPE_F32   ? ((const float*)x)[at]
-         : type == TB_TYPE_F16 ? __half2float(((const __half*)x)[at])
-                               : __bfloat162float(((const __nv_bfloat16*)x)[at]);
-}
-__device__ __forceinline__ void store1(void* x, int64_t at, int type, float f) {
-  if (type == TB_TYPE_F32) ((float*)x)[at] = f;
-  else if (type == TB_TYPE_F16) ((__half*)x)[at] = __float2half_rn(f);
-  else ((__nv_bfloat16*)x)[at] = __float2bfloat16_rn(f);
+template <class E>
+__device__ __forceinline__ void values8(const Eight<E>& r, bool half, f32x2 (&f)[4]) {
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = pair(__uint_as_float(r.w[i].x), __uint_as_float(r.w[i].y));
+      f[2 * i + 1] = pair(__uint_as_float(r.w[i].z), __uint_as_float(r.w[i].w));
+    }
+  } else {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = half ? halves_of(w[i], __half()) : halves_of(w[i], __nv_bfloat16());
+      f[i] = pair(y.x, y.y);
+    }
+  }
 }
 
 // The next term of a pair of floats, taken off them.
@@ -95,23 +113,25 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
 
 // Rows j whose value is not finite, which W has zeros for: their scores times
 // the value join the rows i that see them, in the output as this thread wrote it.
-__device__ __noinline__ void add_not_finite_split(const LinProblem& p, int type, int64_t row0, int h, int v, int n,
+template <class E>
+__device__ __noinline__ void add_not_finite_split(const LinProblem& p, bool is_half, int64_t row0, int h, int v, int n,
                                                   uint32_t scores, int terms) {
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
-    const float c = load1(p.c, (row0 + j) * p.c_row + h * p.c_head + v, type);
+    const float c = load1<E>(p.c, (row0 + j) * p.c_row + h * p.c_head + v, is_half);
     if (!not_finite(c)) continue;
 #pragma unroll 1
     for (int i = p.reverse ? 0 : j; i <= (p.reverse ? j : n - 1); ++i) {
       float s = 0.f;
       for (int t = 0; t < terms; ++t) s += shared_bf16(tile_at(scores + t * kTile, i, j));
       const int64_t at = (row0 + i) * p.o_row + h * p.o_head + v;
-      store1(p.out, at, type, fmaf(s, c, load1(p.out, at, type)));
+      store1<E>(p.out, at, is_half, fmaf(s, c, load1<E>(p.out, at, is_half)));
     }
   }
 }
 // And b_j c_j the state's update.
-__device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, int type, int64_t row0, int h, int v, int n,
+template <class E>
+__device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, bool is_half, int64_t row0, int h, int v, int n,
                                                         uint32_t columns, int key, int keys) {
 #pragma unroll 1
   for (int k0 = 0; k0 < keys; k0 += 16) {
@@ -120,14 +140,14 @@ __device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, int
     tmem_wait_ld();
 #pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const float c = v < p.V ? load1(p.c, (row0 + j) * p.c_row + h * p.c_head + v, type) : 0.f;
+      const float c = v < p.V ? load1<E>(p.c, (row0 + j) * p.c_row + h * p.c_head + v, is_half) : 0.f;
       if (!not_finite(c)) continue;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int k = key + k0 + i;
         if (k < p.K)
           y[i] = __float_as_uint(
-              fmaf(load1(p.b, (row0 + j) * p.b_row + h * p.b_head + k, type), c, __uint_as_float(y[i])));
+              fmaf(load1<E>(p.b, (row0 + j) * p.b_row + h * p.b_head + k, is_half), c, __uint_as_float(y[i])));
       }
     }
     __syncwarp();
@@ -143,7 +163,7 @@ __device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, 
 }
 
 // kStates: the states of segments alone, without outputs.
-template <int kTerms, bool kStates>
+template <class E, int kTerms, bool kStates>
 __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ LinLaunch l) {
   constexpr uint32_t kColS = 0, kColKv = 64, kColW = 192, kColZ = kColW + 32 * kTerms;
   static_assert(kColZ + 64 * kTerms <= 512, "tensor memory");
@@ -164,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
   const bool reverse = p.reverse;
   const float decay = l.decay[h];
   const bool steep = !(decay >= kSteep && decay <= 1.f / kSteep);
-  const int type = l.type;
+  const bool is_half = l.type == TB_TYPE_F16;
 
   if (warp == 0) {
     const LinSegment seg = lin_segment(l, l.sorted ? lin_grid_of_rank(l, slot0) : slot0);
@@ -228,41 +248,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
 
   if (warp >= kWarpLoad && warp < kWarpLoad + kLoadWarps) {
     // ---------------------------------------------------------------- rows
-    const int groups = keys / 8, total = (kStates ? 1 : 2) * kC * groups;
+    // A thread takes the same 8 elements of every kRowStep-th row of B, then of A; a batch of rows is loaded while
+    // the one before it is split.
+    const int shift = keys > 64 ? 4 : 3, me = threadIdx.x - kWarpLoad * 32;
+    const int k = (me & ((1 << shift) - 1)) * 8, r0 = me >> shift, step = kLoadWarps * 32 >> shift;
+    const int sweeps = (kC + step - 1) / step, total = (kStates ? 1 : 2) * sweeps;
+    const uint32_t to0 = (k >> 6) * kTile + r0 * 128;
+    constexpr int kBatch = 4;
+    Eight<E> next[kBatch];
+    auto load = [&](int t, int q0) {
+      const int n = rows_of(t);
+      const int64_t row0 = row_of(t);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int q = q0 + b;
+        const bool is_b = q < sweeps;
+        const int r = r0 + (is_b ? q : q - sweeps) * step;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(E) / 2; ++i) next[b].w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (q < total && r < n && k < p.K)
+          load8<E>(next[b],
+                   (const E*)(is_b ? p.b : p.a) + (row0 + r) * (is_b ? p.b_row : p.a_row) +
+                       h * (is_b ? p.b_head : p.a_head) + k,
+                   p.vec & (is_b ? 2 : 1), p.K - k);
+      }
+    };
+    if (chunks) load(0, 0);
 #pragma unroll 1
     for (int t = 0; t < chunks; ++t) {
       if (t >= 2 && !wait(kEmpty + (t & 1), t / 2 - 1)) break;
       const uint32_t at = stage0 + (t & 1) * kStageBytes;
-      const int n = rows_of(t);
-      const int64_t row0 = row_of(t);
-      constexpr int kBatch = 4;
 #pragma unroll 1
-      for (int i0 = threadIdx.x - kWarpLoad * 32; i0 < total; i0 += kBatch * kLoadWarps * 32) {
-        float f[kBatch][8];
+      for (int q0 = 0; q0 < total; q0 += kBatch) {
+        Eight<E> now[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) now[b] = next[b];
+        if (q0 + kBatch < total) load(t, q0 + kBatch);
+        else if (t + 1 < chunks) load(t + 1, 0);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kLoadWarps * 32;
-          const bool is_b = i < kC * groups;
-          const int r = (is_b ? i : i - kC * groups) / groups, k = (i % groups) * 8;
-          if (i < total && r < n && k < p.K) {
-            const int64_t row = row0 + r;
-            if (is_b) load8(f[b], p.b, row * p.b_row + h * p.b_head + k, type, p.vec & 2, p.K - k);
-            else load8(f[b], p.a, row * p.a_row + h * p.a_head + k, type, p.vec & 1, p.K - k);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[b][j] = 0.f;
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kLoadWarps * 32;
-          if (i >= total) break;
-          const bool is_b = i < kC * groups;
-          const int r = (is_b ? i : i - kC * groups) / groups, c = i % groups;
-          const uint32_t to = (is_b ? tile_b(at, 0) : tile_a(at, 0)) + (c >> 3) * kTile + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          const int q = q0 + b;
+          const bool is_b = q < sweeps;
+          const int move = (is_b ? q : q - sweeps) * step, r = r0 + move;
+          if (q >= total || r >= kC) continue;
+          const uint32_t to = (is_b ? tile_b(at, 0) : tile_a(at, 0)) + to0 + move * 128 + ((((k >> 3) & 7) ^ (r & 7)) << 4);
           f32x2 e[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = pair(f[b][2 * j], f[b][2 * j + 1]);
+          values8<E>(now[b], is_half, e);
 #pragma unroll
           for (int x = 0; x < kTerms; ++x) {
             uint32_t y[4];
@@ -282,9 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
       const uint32_t kv_desc = mma_desc(128, 64, true) + (keys > 64 ? (uint32_t)(64 / 8) << 17 : 0u);
       constexpr uint32_t kRowDesc = mma_desc(128, kC, false);
       auto one = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1, &s.gave_up); };
-      // the products of terms x and y of the left and the right operand, the largest last
-      auto left_term = [](int i) { return kTerms == 3 ? (i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0) : i == 0 ? 1 : 0; };
-      auto right_term = [](int i) { return kTerms == 3 ? (i == 1 ? 2 : i == 2 || i == 4 ? 1 : 0) : i == 1 ? 1 : 0; };
+      // the products of terms x and y of the left and the right operand, the largest last: a sum is then rounded at
+      // its full size only as often as it has steps of 16
+      constexpr int kLeft[6] = {kTerms == 3 ? 2 : 1, 0, kTerms == 3 ? 1 : 0, 1, 0, 0};
+      constexpr int kRight[6] = {0, kTerms == 3 ? 2 : 1, kTerms == 3 ? 1 : 0, 0, 1, 0};
+      constexpr uint32_t kTermStep = 2 * kTile >> 4;  // of a descriptor, from a term's tiles to the next term's
       const int steps = keys / 16;
       bool ok = true;
 #pragma unroll 1
@@ -296,13 +329,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
           ok = ok && (t == 0 || one(kOFree, t - 1));
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1
+          const uint64_t left = smem_desc(tile_a(at, 0) - kTile, 16), right = smem_desc(tile_b(at, 0), 16);
+#pragma unroll
           for (int i = 0; i < kProducts; ++i)
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-              mma_ss(tmem + kColS, smem_desc(tile_a(at, left_term(i)) - kTile + off, 16),
-                     smem_desc(tile_b(at, right_term(i)) + off, 16), kRowDesc, i > 0 || k > 0);
+            for (int k = 0; k < steps; k += 4) {
+              const uint32_t off = (k >> 2) * kTile >> 4;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mma_ss(tmem + kColS, left + off + kLeft[i] * kTermStep + 2 * q, right + off + kRight[i] * kTermStep + 2 * q,
+                       kRowDesc, i > 0 || k > 0 || q > 0);
             }
           mma_commit(bar(kSReady));
         }
@@ -310,32 +346,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
         ok = ok && one(kWFull, t) && (t == 0 || one(kKvFree, t - 1));
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int i = 0; i < kProducts; ++i)
+        {
+          const uint64_t right = smem_desc(tile_b(at, 0), kTile);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColKv, tmem + kColW + left_term(i) * 32 + j * 8,
-                   smem_desc(tile_b(at, right_term(i)) + j * 2048, kTile), kv_desc, i > 0 || j > 0);
+          for (int i = 0; i < kProducts; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma_ts(tmem + kColKv, tmem + kColW + kLeft[i] * 32 + j * 8, right + kRight[i] * kTermStep + j * (2048 >> 4),
+                     kv_desc, i > 0 || j > 0);
+        }
         mma_commit(bar(kKvReady));
         if (!kStates) {
           // Z^T A^T, where the scores were
           ok = one(kStFull, t) && one(kSFull, t);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll 1
+          const uint64_t rows = smem_desc(tile_a(at, 0), 16), weights = smem_desc(tiles, 16);
+#pragma unroll
           for (int i = 0; i < kProducts; ++i)
 #pragma unroll 1
-            for (int k = 0; k < steps; ++k)
-              mma_ts(tmem + kColS, tmem + kColZ + left_term(i) * 64 + k * 8,
-                     smem_desc(tile_a(at, right_term(i)) + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, i > 0 || k > 0);
+            for (int k = 0; k < steps; k += 4) {
+              const uint32_t off = (k >> 2) * kTile >> 4;
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mma_ts(tmem + kColS, tmem + kColZ + kLeft[i] * 64 + k * 8 + q * 8, rows + off + kRight[i] * kTermStep + 2 * q,
+                       kRowDesc, i > 0 || k > 0 || q > 0);
+            }
           mma_commit(bar(kStFree));
           // W^T scores^T
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < kProducts; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              mma_ts(tmem + kColS, tmem + kColW + left_term(i) * 32 + j * 8,
-                     smem_desc(tiles + right_term(i) * kTile + j * 32, 16), kRowDesc, true);
+              mma_ts(tmem + kColS, tmem + kColW + kLeft[i] * 32 + j * 8, weights + (kRight[i] * kTile >> 4) + j * 2, kRowDesc,
+                     true);
           mma_commit(bar(kOReady));
         }
         mma_commit(bar(kWFree));
@@ -364,17 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
       for (int i = 0; i < 64; i += 2, from += 2 * step)
         u[i / 2] = pair(i < left ? from[0] * enter : 0.f, i + 1 < left ? from[step] * enter : 0.f);
     }
-    float c[32];  // this thread's value of its half of a chunk's rows
 #pragma unroll 1
     for (int t = -1; t < chunks; ++t) {
       const int x = t + 1;
       const bool more = x < chunks;
-      if (more) {
-        const int n = rows_of(x);
-        const int64_t at = (row_of(x) + half * 32) * p.c_row + h * p.c_head + v;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          c[i] = half * 32 + i < n && v < p.V ? load1(p.c, at + i * p.c_row, type) : 0.f;
+      if (more && live) {
+        // this chunk's values on their way to L2, a line of 32 for every row (registers that held them would spill)
+        const int n = rows_of(x), r = half * 32 + lane;
+        if (r < n)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"((const E*)p.c + (row_of(x) + r) * p.c_row + h * p.c_head +
+                                                         quarter * 32));
       }
       if (t >= 0) {
         // the state after this chunk
@@ -385,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
         if (live) {
           const uint32_t columns = lanes + kColKv + half * own;
           if (s.bad[t & 1] == (uint32_t)t + 1)
-            add_not_finite_state_split(p, type, row_of(t), h, v, n, columns, half * own, own);
+            add_not_finite_state_split<E>(p, is_half, row_of(t), h, v, n, columns, half * own, own);
           const f32x2 d2 = pair(d, d);
 #pragma unroll
           for (int k0 = 0; k0 < 64; k0 += 16) {
@@ -432,23 +475,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
         if (live) {
           const int n = rows_of(x);
           const float* w = s.w + (reverse ? kC - n : 0) + half * 32;
-          float finite = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) finite = fmaf(c[i], 0.f, finite);
-          if (finite != finite) {
-            // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
-            // warps of the output and of the state add these values to what sees them
-#pragma unroll
-            for (int i = 0; i < 32; ++i) c[i] = not_finite(c[i]) ? 0.f : c[i];
-            s.bad[x & 1] = x + 1;
-          }
-          __syncwarp();
-#pragma unroll
+          const E* from = (const E*)p.c + (row_of(x) + half * 32) * p.c_row + h * p.c_head + v;
+#pragma unroll 1
           for (int r0 = 0; r0 < 32; r0 += 16) {
+            E raw[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i, from += p.c_row)
+              raw[i] = half * 32 + r0 + i < n && v < p.V ? __ldg(from) : E(0);
+            float c[16], finite = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              c[i] = value<E>(raw[i], is_half);
+              finite = fmaf(c[i], 0.f, finite);
+            }
+            if (finite != finite) {
+              // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
+              // warps of the output and of the state add these values to what sees them
+#pragma unroll
+              for (int i = 0; i < 16; ++i) c[i] = not_finite(c[i]) ? 0.f : c[i];
+              s.bad[x & 1] = x + 1;
+            }
+            __syncwarp();
             f32x2 e[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              e[i] = mul2(pair(c[r0 + 2 * i], c[r0 + 2 * i + 1]), pair(w[r0 + 2 * i], w[r0 + 2 * i + 1]));
+              e[i] = mul2(pair(c[2 * i], c[2 * i + 1]), pair(w[r0 + 2 * i], w[r0 + 2 * i + 1]));
 #pragma unroll
             for (int y = 0; y < kTerms; ++y) {
               uint32_t z[8];
@@ -526,11 +577,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
         const int64_t row0 = row_of(t);
         const float* w = s.o + (reverse ? kC - n : 0);
         if (v < p.V) {
-          int64_t at = row0 * p.o_row + h * p.o_head + v;
+          E* out = (E*)p.out + row0 * p.o_row + h * p.o_head + v;
+          auto put = [&](int i) {
+            store1<E>(out, 0, is_half, __uint_as_float(x[i / 16][i % 16]) * w[i]);
+            out += p.o_row;
+          };
+          if (n == kC) {
 #pragma unroll
-          for (int i = 0; i < kC; ++i, at += p.o_row)
-            if (i < n) store1(p.out, at, type, __uint_as_float(x[i / 16][i % 16]) * w[i]);
-          if (bad) add_not_finite_split(p, type, row0, h, v, n, tiles, kTerms);
+            for (int i = 0; i < kC; ++i) put(i);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+              if (i >= n) break;
+              put(i);
+            }
+          }
+          if (bad) add_not_finite_split<E>(p, is_half, row0, h, v, n, tiles, kTerms);
         }
         __syncwarp();
         if (bad) {
@@ -551,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
   if (warp == kWarpMma) tmem_free(tmem, 512);
   if (!steep || idle || warp >= 8) return;
   float* rows = reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw)));
-  if (type == TB_TYPE_F32) walk_rows<float>(l, p, s.seg, h, rows);
-  else if (type == TB_TYPE_F16) walk_rows<__half>(l, p, s.seg, h, rows);
+  if constexpr (sizeof(E) == 4) walk_rows<float>(l, p, s.seg, h, rows);
+  else if (is_half) walk_rows<__half>(l, p, s.seg, h, rows);
   else walk_rows<__nv_bfloat16>(l, p, s.seg, h, rows);
 }
 
-template <int kTerms, bool kStates>
+template <class E, int kTerms, bool kStates>
 cudaError_t go(const LinLaunch& l, cudaStream_t s) {
   constexpr int bytes = 1024 + kTerms * kTile + 2 * 2 * kTerms * 2 * kTile;
   static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
@@ -565,12 +627,12 @@ cudaError_t go(const LinLaunch& l, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_split<kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(k_split<E, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
   const int64_t blocks = (int64_t)l.segments * l.heads * l.n;
-  k_split<kTerms, kStates><<<(unsigned)blocks, kThreads, bytes, s>>>(l);
+  k_split<E, kTerms, kStates><<<(unsigned)blocks, kThreads, bytes, s>>>(l);
   return cudaGetLastError();
 }
 
@@ -578,10 +640,11 @@ cudaError_t go(const LinLaunch& l, cudaStream_t s) {
 
 cudaError_t launch_linear_split(const void* args, cudaStream_t s) {
   const LinLaunch& l = *(const LinLaunch*)args;
-  bool exact = l.type == TB_TYPE_F32;  // 32-bit outputs
+  if (l.type == TB_TYPE_F32) return l.phase == 1 ? go<float, 3, true>(l, s) : go<float, 3, false>(l, s);
+  bool exact = false;  // 32-bit states come out
   for (int i = 0; i < l.n; ++i) exact = exact || (l.p[i].last && l.phase != 2);
-  if (l.phase == 1) return exact ? go<3, true>(l, s) : go<2, true>(l, s);
-  return exact ? go<3, false>(l, s) : go<2, false>(l, s);
+  if (l.phase == 1) return exact ? go<uint16_t, 3, true>(l, s) : go<uint16_t, 2, true>(l, s);
+  return exact ? go<uint16_t, 3, false>(l, s) : go<uint16_t, 2, false>(l, s);
 }
 
 cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up) {
