@@ -47,9 +47,10 @@ constexpr int kStageBytes = 6 * kTile;  // two tiles each of A, B, C
 // Warps: 8 of the state, the copies, the products, 2 of the scores (lanes 64 to
 // 127), 4 of the output, and for pairs of heads 2 more of the scores.  Sixteen
 // leave 128 registers a thread, which the state of 128 keys and the blocks of W
-// need; pairs hold half as many keys.
+// need; pairs hold half as many keys.  Where only states are made, 8 other warps
+// make W: together they took one warp's turn a chunk each (2400 clocks).
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScores = 10, kWarpOut = 12, kWarpScores2 = 16;
-constexpr int threads_of(bool pair, bool states) { return (states ? kWarpScores : pair ? 18 : 16) * 32; }
+constexpr int threads_of(bool pair, bool states) { return (states || pair ? 18 : 16) * 32; }
 
 // Set when a wait gave up (a bug, or a GPU that stands still): read and
 // cleared by linear_gave_up.
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         mbar_init(bar(kFull + i), 1);
-        mbar_init(bar(kEmpty + i), kStates ? 9 : 13);  // products, state warps, output warps
+        mbar_init(bar(kEmpty + i), kStates ? 17 : 13);  // products, state warps, W's or output warps
         s.bad[i] = 0;
       }
       for (int i = 0; i < 2; ++i) {
@@ -243,6 +244,93 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   const bool live = (kPair && head ? present[kHeads - 1] : present[0]) && value0 < p.V;
   const uint32_t lanes = tmem + ((uint32_t)quarter << 21);
   const int h = h0 + head;
+
+  const int half = kStates && warp >= kWarpScores ? (warp - kWarpScores) >> 2 : warp >> 2;  // of the keys, of a chunk's rows
+  // W^T of chunk x: its terms in registers, then in tensor memory.
+  uint32_t y[2][kTerms][8];
+  auto make_w = [&](int x) {
+    const int st = x % kStages, n = rows_of(x);
+    const uint32_t at = stage0 + st * kStageBytes;
+    if (!wait(kFull + st, x / kStages)) return false;
+    if (n < kC) {
+      // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
+#pragma unroll 1
+      for (int i = threadIdx.x - (kStates ? kWarpScores * 32 : 0); i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
+        const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         at + (2 + blk) * kTile + n * 128 + r * 16),
+                     "r"(0)
+                     : "memory");
+      }
+      fence_async_smem();
+      arrive(kZeros);  // once: only the last chunk is short
+      if (!wait(kZeros, 0)) return false;
+    }
+    if (live) {
+      // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
+      // value
+      const int skip = reverse ? kC - n : 0;
+      const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
+      const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
+      const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
+      const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
+#pragma unroll
+      for (int g16 = 0; g16 < 2; ++g16) {
+        uint32_t c[8];
+        const uint32_t from = rows + ((((quarter & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+        ldmatrix_trans4(from, c[0], c[1], c[2], c[3]);
+        ldmatrix_trans4(from + 16 * 128, c[4], c[5], c[6], c[7]);
+        uint32_t finite = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) finite = fma_bf16x2(c[i], 0u, finite);
+        if (__any_sync(0xffffffffu, not_finite(low(finite)) || not_finite(high(finite)))) {
+          // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
+          // warps of the output and of the state add these values to what sees them
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (not_finite(low(c[i]))) c[i] &= 0xffff0000u;
+            if (not_finite(high(c[i]))) c[i] &= 0xffffu;
+          }
+          s.bad[st] = x + 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (kTerms == 2) {
+            // c (w + w') = hi + lo: hi = round(c w), c w - hi is exact in 16 bits
+            const uint2 wv = w2[(i / 2) * 4];
+            y[g16][0][i] = mul_bf16x2(c[i], wv.x);
+            y[g16][1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[g16][0][i] ^ 0x80008000u));
+          } else {
+            const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
+            f32x2 e = mul2(pair(low(c[i]), high(c[i])), pair(wv.x, wv.y));
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term) {
+              const uint32_t x2 = bf16x2(halves(e).x, halves(e).y);
+              y[g16][term][i] = x2;
+              if (term + 1 < kTerms) e = fma2(pair(low(x2), high(x2)), pair(-1.f, -1.f), e);
+            }
+          }
+        }
+      }
+    }
+    return true;
+  };
+  auto put_w = [&](int x) {
+    if (x >= kWs && !wait(kWFree + x % kWs, x / kWs - 1)) return false;
+    tc_fence_after();
+    if (live) {
+#pragma unroll
+      for (int g16 = 0; g16 < 2; ++g16) {
+        const uint32_t to = lanes + ((uint32_t)g16 << 20) + kColW + x % kWs * 32 * kTerms + half * 16;
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + term * 32, y[g16][term]);
+      }
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    arrive(kWFull + x % kWs);
+    return true;
+  };
 
   if (warp == kWarpTma) {
     if (elect_one()) {
@@ -347,7 +435,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   } else if (warp < 8) {
     // ------------------------------------------------------------ state, W
     constexpr int NK = kKeys / 2;  // keys of a thread
-    const int half = warp >> 2, v = value0 + lane;
+    const int v = value0 + lane;
     const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
     float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
     const float log = log2f(kPair && head ? decay[kHeads - 1] : decay[0]);
@@ -362,91 +450,6 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       for (int i = 0; i < NK; i += 2, from += 2 * step)
         u[i / 2] = pair(i < keys ? from[0] * enter : 0.f, i + 1 < keys ? from[step] * enter : 0.f);
     }
-    // W^T of chunk x: its terms in registers, then in tensor memory.
-    uint32_t y[2][kTerms][8];
-    auto make_w = [&](int x) {
-      const int st = x % kStages, n = rows_of(x);
-      const uint32_t at = stage0 + st * kStageBytes;
-      if (!wait(kFull + st, x / kStages)) return false;
-      if (n < kC) {
-        // rows past the segment belong to others: no NaN of theirs may meet the zeros that stand for them
-#pragma unroll 1
-        for (int i = threadIdx.x; i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
-          const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           at + (2 + blk) * kTile + n * 128 + r * 16),
-                       "r"(0)
-                       : "memory");
-        }
-        fence_async_smem();
-        arrive(kZeros);  // once: only the last chunk is short
-        if (!wait(kZeros, 0)) return false;
-      }
-      if (live) {
-        // this warp's 32 values x its half of the rows, as 8 x 8 blocks read across: a register is two rows of a
-        // value
-        const int skip = reverse ? kC - n : 0;
-        const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
-        const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
-        const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
-        const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
-#pragma unroll
-        for (int g16 = 0; g16 < 2; ++g16) {
-          uint32_t c[8];
-          const uint32_t from = rows + ((((quarter & 1) * 4 + g16 * 2 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
-          ldmatrix_trans4(from, c[0], c[1], c[2], c[3]);
-          ldmatrix_trans4(from + 16 * 128, c[4], c[5], c[6], c[7]);
-          uint32_t finite = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) finite = fma_bf16x2(c[i], 0u, finite);
-          if (__any_sync(0xffffffffu, not_finite(low(finite)) || not_finite(high(finite)))) {
-            // 0 x infinity of a later row is no part of an earlier row's sum: the products take zeros, and the
-            // warps of the output and of the state add these values to what sees them
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (not_finite(low(c[i]))) c[i] &= 0xffff0000u;
-              if (not_finite(high(c[i]))) c[i] &= 0xffffu;
-            }
-            s.bad[st] = x + 1;
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (kTerms == 2) {
-              // c (w + w') = hi + lo: hi = round(c w), c w - hi is exact in 16 bits
-              const uint2 wv = w2[(i / 2) * 4];
-              y[g16][0][i] = mul_bf16x2(c[i], wv.x);
-              y[g16][1][i] = fma_bf16x2(c[i], wv.y, fma_bf16x2(c[i], wv.x, y[g16][0][i] ^ 0x80008000u));
-            } else {
-              const float2 wv = *reinterpret_cast<const float2*>(w + (i / 2) * 8);
-              f32x2 e = mul2(pair(low(c[i]), high(c[i])), pair(wv.x, wv.y));
-#pragma unroll
-              for (int term = 0; term < kTerms; ++term) {
-                const uint32_t x2 = bf16x2(halves(e).x, halves(e).y);
-                y[g16][term][i] = x2;
-                if (term + 1 < kTerms) e = fma2(pair(low(x2), high(x2)), pair(-1.f, -1.f), e);
-              }
-            }
-          }
-        }
-      }
-      return true;
-    };
-    auto put_w = [&](int x) {
-      if (x >= kWs && !wait(kWFree + x % kWs, x / kWs - 1)) return false;
-      tc_fence_after();
-      if (live) {
-#pragma unroll
-        for (int g16 = 0; g16 < 2; ++g16) {
-          const uint32_t to = lanes + ((uint32_t)g16 << 20) + kColW + x % kWs * 32 * kTerms + half * 16;
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term) tmem_st_16x16(to + term * 32, y[g16][term]);
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      arrive(kWFull + x % kWs);
-      return true;
-    };
     // The state after chunk t.
     auto update = [&](int t) {
       const int st = t % kStages, n = rows_of(t);
@@ -500,8 +503,8 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 #pragma unroll 1
     for (int t = -1; t < chunks; ++t) {
       const bool more = t + 1 < chunks;
-      if (kAhead && more && !make_w(t + 1)) break;
-      if (kWs == 2 && more && !put_w(t + 1)) break;
+      if (kAhead && !kStates && more && !make_w(t + 1)) break;
+      if (kWs == 2 && !kStates && more && !put_w(t + 1)) break;
       if (t >= 0 && !update(t)) break;
       if (!kStates && more && !put_z(t + 1)) break;
       if (!kAhead && more && !make_w(t + 1)) break;
@@ -516,11 +519,18 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         if (i + 1 < p.K - half * NK) dst[p.V] = halves(u[i / 2]).y;
       }
     }
-  } else if (!kStates && (warp < kWarpOut || warp >= kWarpScores2)) {
+  } else if (kStates) {
+    // ------------------------------------------------------------------- W
+#pragma unroll 1
+    for (int x = 0; x < chunks; ++x) {
+      if (!make_w(x) || !put_w(x)) break;
+      arrive(kEmpty + x % kStages);
+    }
+  } else if (warp < kWarpOut || warp >= kWarpScores2) {
     // -------------------------------------------------------------- scores
     // Rows past a segment's end need no mask: their b are zeros before the scores are computed, and rows i past it
     // are not written.
-    const int half = warp & 1, i = half * 32 + lane;
+    const int block = warp & 1, i = block * 32 + lane;
     uint32_t diagonal[16];  // of pairs of columns in the 32 x 32 block on the diagonal
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -535,7 +545,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       const uint32_t row = tiles + ((t & 1) * kHeads + head) * kTile + i * 128;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {  // columns 32 b to 32 b + 31
-        const bool some = reverse ? b >= half : b <= half;
+        const bool some = reverse ? b >= block : b <= block;
         if (!some && t >= 2) continue;  // the tile's other half stays zero
         uint32_t x[32], y[16];
         if (some) {
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           y[j] = bf16x2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-          y[j] = !some ? 0u : b == half ? y[j] & diagonal[j] : y[j];
+          y[j] = !some ? 0u : b == block ? y[j] & diagonal[j] : y[j];
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -557,7 +567,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       tc_fence_before();
       arrive(kSFull);
     }
-  } else if (!kStates) {
+  } else {
     // -------------------------------------------------------------- output
     const uint32_t out0 = stage0 + kStages * kStageBytes + quarter * 2 * kOutTile;
     const CUtensorMap* map = &g.map[kLinMaxRows + problem];
