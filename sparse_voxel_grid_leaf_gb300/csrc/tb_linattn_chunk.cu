@@ -42,8 +42,13 @@ namespace tb {
 namespace {
 
 constexpr int kOutTile = 4096;    // 64 rows x 64 bytes
-constexpr int kStages = 3;
-constexpr int kStageBytes = 6 * kTile;  // two tiles each of A, B, C
+// A ring of stages of two tiles each of B, C and A (which states do without):
+// what the copies are ahead by has to cover a chunk's time in the block and the
+// memory's latency (three stages stalled the segment states every third chunk:
+// 124 us for the states of a 65537-token prompt, 106 with six).
+constexpr int kMaxStages = 6;
+constexpr int stages_of(bool states) { return states ? 6 : 3; }
+constexpr int stage_bytes(bool states) { return (states ? 4 : 6) * kTile; }
 // Warps: 8 of the state, the copies, the products, 2 of the scores (lanes 64 to
 // 127), 4 of the output, and for pairs of heads 2 more of the scores.  Sixteen
 // leave 128 registers a thread, which the state of 128 keys and the blocks of W
@@ -57,7 +62,7 @@ constexpr int threads_of(bool pair, bool states) { return (states || pair ? 18 :
 __device__ unsigned int g_gave_up;
 
 enum Bars {
-  kFull = 0, kEmpty = kFull + kStages, kSReady = kEmpty + kStages, kSFull, kWFull, kWFree = kWFull + 2,
+  kFull = 0, kEmpty = kFull + kMaxStages, kSReady = kEmpty + kMaxStages, kSFull, kWFull, kWFree = kWFull + 2,
   kKvReady = kWFree + 2, kKvFree = kKvReady + 2, kStFull = kKvFree + 2, kStFree, kOReady, kOFree = kOReady + 2, kZeros = kOFree + 2, kDrain, kBars
 };
 
@@ -65,7 +70,7 @@ struct Shared {
   uint64_t bar[kBars];
   uint32_t tmem;
   volatile uint32_t gave_up;
-  volatile uint32_t bad[kStages];  // chunk + 1 whose values are not all finite
+  volatile uint32_t bad[kMaxStages];  // chunk + 1 whose values are not all finite
   LinSegment seg;
   // powers for the rows of a chunk, 0 past the 64th; per head, copy s starts at row s
   __align__(8) float w[2][2][2 * kC + 2];  // fold decay^(31-m), reverse: fold decay^(m-32)
@@ -134,7 +139,8 @@ __device__ __noinline__ void walk_rows(const LinLaunch& l, const LinProblem& p, 
 // kStates: the states of segments alone, without outputs.
 template <bool kPair, int kTerms, bool kStates>
 __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const __grid_constant__ ChunkLaunch g) {
-  constexpr int kHeads = kPair ? 2 : 1;
+  constexpr int kHeads = kPair ? 2 : 1, kStages = stages_of(kStates), kStageBytes = stage_bytes(kStates);
+  constexpr int kTileB = 0, kTileC = 2, kTileA = 4;        // of a stage
   constexpr int kKeys = kPair ? 64 : 128;                  // of a head
   constexpr int kRows = kHeads * kC;                       // columns of the products over rows
   // Buffers in tensor memory: of W^T, of its product with B, of the output.
@@ -145,10 +151,10 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 
   extern __shared__ char s_raw[];
   __shared__ Shared s;
-  // two score tiles for each head, then the stages (with one head the product A B^T reads the 8 KB before A too),
+  // two score tiles for each head, then the stages (with one head the product A B^T reads the 8 KB before A too, C),
   // then the outputs
   const uint32_t tiles = (smem_addr(s_raw) + 1023) & ~1023u;
-  const uint32_t stage0 = tiles + 2 * kHeads * kTile;
+  const uint32_t stage0 = tiles + (kStates ? 0 : 2 * kHeads * kTile);
 
   const LinLaunch& l = g.l;
   // blocks in the order of their segments, longest grids first where they are walked whole
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       for (int i = threadIdx.x - (kStates ? kWarpScores * 32 : 0); i < (2 + value_tiles) * (kC - n) * 8; i += 256) {
         const int blk = i / ((kC - n) * 8), r = i % ((kC - n) * 8);
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                         at + (2 + blk) * kTile + n * 128 + r * 16),
+                         at + blk * kTile + n * 128 + r * 16),
                      "r"(0)
                      : "memory");
       }
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       const float* w = s.w[head][skip & 1] + (skip & ~1) + half * 32 + 2 * (lane & 3);
       const uint2* w2 = s.w2[head][skip & 1] + skip / 2 + half * 16 + (lane & 3);
       const int r = half * 32 + (lane >> 4) * 8 + (lane & 7);
-      const uint32_t rows = at + (4 + (quarter >> 1)) * kTile + r * 128;
+      const uint32_t rows = at + (kTileC + (quarter >> 1)) * kTile + r * 128;
 #pragma unroll
       for (int g16 = 0; g16 < 2; ++g16) {
         uint32_t c[8];
@@ -349,10 +355,10 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         auto load = [&](int tile, const CUtensorMap* map, int i) {
           tma_load_3d(at + (tile + i) * kTile, map, kPair ? 0 : 64 * i, kPair ? h0 + i : h0, row, bar(kFull + st));
         };
-        for (int i = 0; i < value_tiles; ++i) load(4, mc, i);
-        for (int i = 0; i < 2; ++i) load(2, mb, i);
+        for (int i = 0; i < value_tiles; ++i) load(kTileC, mc, i);
+        for (int i = 0; i < 2; ++i) load(kTileB, mb, i);
         if (!kStates)
-          for (int i = 0; i < 2; ++i) load(0, ma, i);
+          for (int i = 0; i < 2; ++i) load(kTileA, ma, i);
       }
       if (s.gave_up) {  // copies in flight land before the block ends
         for (int i = t > kStages ? t - kStages : 0; i < t; ++i) {
@@ -373,8 +379,8 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k) {
           const uint32_t off = (k >> 2) * kTile + (k & 3) * 32;
-          mma_ss(tmem + kColS, smem_desc(at - (kPair ? 0 : kTile) + off, 16), smem_desc(at + 2 * kTile + off, 16), kRowDesc,
-                 k > 0);
+          mma_ss(tmem + kColS, smem_desc(at + (kPair ? kTileA : kTileA - 1) * kTile + off, 16),
+                 smem_desc(at + kTileB * kTile + off, 16), kRowDesc, k > 0);
         }
         mma_commit(bar(kSReady));
       };
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_ts(tmem + kColKv + kv * 128, w + term * 32 + j * 8, smem_desc(at + 2 * kTile + j * 2048, kTile), kKvDesc,
+            mma_ts(tmem + kColKv + kv * 128, w + term * 32 + j * 8, smem_desc(at + kTileB * kTile + j * 2048, kTile), kKvDesc,
                    term > 0 || j > 0);
         mma_commit(bar(kKvReady + kv));
         if (!kStates) {
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            mma_ts(o, tmem + kColZ + k * 8, smem_desc(at + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, k > 0);
+            mma_ts(o, tmem + kColZ + k * 8, smem_desc(at + kTileA * kTile + (k >> 2) * kTile + (k & 3) * 32, 16), kRowDesc, k > 0);
           mma_commit(bar(kStFree));
           // the next chunk's scores, once this chunk's are out of tensor memory
           ok = one(kSFull, t) && (t + 1 >= chunks || one(kFull + (t + 1) % kStages, (t + 1) / kStages));
@@ -460,8 +466,8 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
       if (live) {
         if (s.bad[st] == (uint32_t)t + 1) {
           const uint32_t at = stage0 + st * kStageBytes;
-          add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (2 + head) * kTile,
-                               half * NK, at + (4 + (quarter >> 1)) * kTile, n);
+          add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (kTileB + head) * kTile,
+                               half * NK, at + (kTileC + (quarter >> 1)) * kTile, n);
         }
         const f32x2 d2 = pair(d, d);
 #pragma unroll
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         __syncwarp();
         if (bad) {
           add_not_finite(buf, tiles + ((t & 1) * kHeads + head) * kTile,
-                         stage0 + st * kStageBytes + (4 + (quarter >> 1)) * kTile, n, reverse);
+                         stage0 + st * kStageBytes + (kTileC + (quarter >> 1)) * kTile, n, reverse);
           tc_fence_before();
           arrive(kOFree + t % kOs);
         }
@@ -655,7 +661,8 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
 
 template <bool kPair, int kTerms, bool kStates>
 cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
-  constexpr int bytes = 1024 + (kPair ? 4 : 2) * kTile + kStages * kStageBytes + (kStates ? 0 : 4 * 2 * kOutTile);
+  constexpr int bytes = 1024 + stages_of(kStates) * stage_bytes(kStates) +
+                        (kStates ? 0 : (kPair ? 4 : 2) * kTile + 4 * 2 * kOutTile);
   static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
   static bool ready[64];
   int dev = 0;

@@ -450,19 +450,33 @@ __global__ void __launch_bounds__(32 * 8) k_norm_backward_groups(NormBackwardLau
   for (int i = threadIdx.x; i < width; i += blockDim.x) a.workspace[(int64_t)blockIdx.x * width + i] = dw[i];
 }
 
-// dweight = the blocks' parts summed: 32 columns a block, 32 groups of parts.
+// dweight = the blocks' parts summed, in a fixed order: 8 columns a block, 64
+// rows of parts at a time, four in flight a thread.
 template <class T>
-__global__ void __launch_bounds__(1024) k_norm_weight(NormBackwardLaunch n) {
-  __shared__ float s[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
+__global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
+  constexpr int kCols = 8, kRows = 64;
+  __shared__ float s[kRows][kCols + 1];
+  const int x = threadIdx.x % kCols, y = threadIdx.x / kCols, c = blockIdx.x * kCols + x;
   float sum = 0.f;
-  if (c < n.a.width)
-    for (int b = threadIdx.y; b < n.blocks; b += 32) sum += n.a.workspace[(int64_t)b * n.a.width + c];
-  s[threadIdx.y][threadIdx.x] = sum;
+  if (c < n.a.width) {
+    const float* part = n.a.workspace + c;
+    int b = y;
+    for (; b + 3 * kRows < n.blocks; b += 4 * kRows) {
+      float f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = part[(int64_t)(b + i * kRows) * n.a.width];
+      sum += (f[0] + f[1]) + (f[2] + f[3]);
+    }
+    for (; b < n.blocks; b += kRows) sum += part[(int64_t)b * n.a.width];
+  }
+  s[y][x] = sum;
   __syncthreads();
-  const float all = warp_sum(s[threadIdx.x][threadIdx.y]);
-  const int o = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && o < n.a.width) ((T*)n.a.dweight)[o] = RowType<T>::from(all);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < kCols) {
+    const float all = warp_sum(s[lane][warp] + s[lane + 32][warp]);
+    const int o = blockIdx.x * kCols + warp;
+    if (lane == 0 && o < n.a.width) ((T*)n.a.dweight)[o] = RowType<T>::from(all);
+  }
 }
 
 // Lets a kernel take `bytes` of shared memory.
@@ -561,8 +575,7 @@ cudaError_t launch_norm_backward(const void* args, cudaStream_t s) {
 
 cudaError_t launch_norm_weight(const void* args, cudaStream_t s) {
   const NormBackwardLaunch& n = *(const NormBackwardLaunch*)args;
-  const dim3 block(32, 32);
-  const int blocks = (n.a.width + 31) / 32;
+  const int block = 512, blocks = (n.a.width + 7) / 8;
   switch (n.a.type) {
     case TB_TYPE_F32: k_norm_weight<float><<<blocks, block, 0, s>>>(n); break;
     case TB_TYPE_F16: k_norm_weight<__half><<<blocks, block, 0, s>>>(n); break;
