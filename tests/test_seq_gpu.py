@@ -494,3 +494,33 @@ def test_offsets_outside_the_rows_are_clamped():
     o, _ = tb.linear_attention(q, k, v, decay, torch.tensor([-5, 64, 1 << 40], device="cuda"))
     want, _ = tb.linear_attention(q, k, v, decay)
     assert torch.equal(o, want)
+
+
+def test_the_example_learns_and_walks():
+    """examples/voxel_sequence.py: the operators together, in training and voxel by voxel."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "voxel_sequence.py")
+    spec = importlib.util.spec_from_file_location("voxel_sequence", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, off_by = example.run(steps=30, say=None)
+    assert all(math.isfinite(x) for x in losses) and losses[-1] < 0.9 * losses[0]
+    # two paths through two blocks in bfloat16: outputs of size one, a few units of 2^-8 each
+    assert off_by <= 16 * 2.0 ** -8
+
+
+def test_example_coordinates_are_the_batch_order():
+    import importlib.util
+    import os
+
+    import numpy as np
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "voxel_sequence.py")
+    spec = importlib.util.spec_from_file_location("voxel_sequence", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    ijk = np.array([[9, 0, 0], [0, 0, 1], [0, 0, 0], [-1, 2, 3], [5, 5, 5]], np.int32)
+    b = tb.from_ijk(torch.from_numpy(ijk).cuda(), torch.tensor([0, 3, 3, 5]).cuda())
+    at, offsets = example.voxel_coordinates(b)
+    assert offsets.tolist() == [0, 3, 3, 5]
+    assert at.tolist() == [[0, 0, 0], [0, 0, 1], [9, 0, 0], [-1, 2, 3], [5, 5, 5]]
