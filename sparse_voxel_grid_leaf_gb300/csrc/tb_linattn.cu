@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(256) k_combine(LinLaunch l) {
   const int slot0 = lin_first_slot(l, b);
   int64_t begin, end;
   lin_grid_rows(l, b, begin, end);
-  const int n = lin_segments_of(l, end - begin);
+  // offsets that decrease name rows twice: their segments are more than the slots, which bound the walk
+  const int n = min(lin_segments_of(l, end - begin), max(0, l.segments - slot0));
   const float decay = l.decay[h];
   const float whole = lin_power(decay, (float)l.segment);
   const float rest = lin_power(decay, (float)(end - begin - (int64_t)(n - 1) * l.segment));
