@@ -114,6 +114,7 @@ constexpr int kCombineBatch = 8;
 // the chain that joins them: 40 MB of states in 18 us an element at a time.
 template <int N>
 __global__ void __launch_bounds__(256) k_combine(LinLaunch l) {
+  let_next_kernel_start();
   const LinProblem& p = l.p[blockIdx.z];
   const int b = blockIdx.x / l.heads, h = blockIdx.x % l.heads;
   const int slot0 = lin_first_slot(l, b);
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(256) k_combine(LinLaunch l) {
   const int64_t state_at = ((int64_t)b * l.heads + h) * size;
   const int i = (blockIdx.y * blockDim.x + threadIdx.x) * N;
   if (i >= size) return;
+  wait_for_last_kernel();
   float x[N];
 #pragma unroll
   for (int k = 0; k < N; ++k)
@@ -198,9 +200,7 @@ cudaError_t launch_linear_combine(const void* args, cudaStream_t s) {
   }
   const int n = vec ? 4 : 1;
   const dim3 grid((unsigned)(l.grids * l.heads), (size + 256 * n - 1) / (256 * n), l.n);
-  if (vec) k_combine<4><<<grid, 256, 0, s>>>(l);
-  else k_combine<1><<<grid, 256, 0, s>>>(l);
-  return cudaGetLastError();
+  return launch_early(vec ? k_combine<4> : k_combine<1>, grid, 256, 0, s, true, l);
 }
 
 }  // namespace tb

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
                      kColZ = kColW + 32 * kTerms * kWs;
   static_assert(kColZ + kKeys / 2 <= 512, "tensor memory");
 
+  if (kStates) let_next_kernel_start();
   extern __shared__ char s_raw[];
   __shared__ Shared s;
   // two score tiles for each head, then the stages (with one head the product A B^T reads the 8 KB before A too, C),
@@ -446,6 +447,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
     float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
     const float log = log2f(kPair && head ? decay[kHeads - 1] : decay[0]);
     const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
+    if (l.phase == 2) wait_for_last_kernel();  // the states that enter
     f32x2 u[NK / 2];  // Z, by pairs of keys
     {
       const float* from = l.phase == 2 ? seg_state : p.first ? p.first + state_at : nullptr;
@@ -653,6 +655,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
   if (warp == kWarpMma) tmem_free(tmem, 512);
   if (idle || warp >= 8) return;
+  if (l.phase == 2) wait_for_last_kernel();
 #pragma unroll 1
   for (int i = 0; i < kHeads; ++i)
     if (!(i ? present[kHeads - 1] : present[0]) && h0 + i < l.heads)
@@ -674,8 +677,8 @@ cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
   const int64_t blocks = (int64_t)g.l.segments * (kPair ? (g.l.heads + 1) / 2 : g.l.heads) * g.l.n;
-  k_chunks<kPair, kTerms, kStates><<<(unsigned)blocks, threads_of(kPair, kStates), bytes, s>>>(g);
-  return cudaGetLastError();
+  return launch_early(k_chunks<kPair, kTerms, kStates>, (unsigned)blocks, threads_of(kPair, kStates), bytes, s,
+                      g.l.phase == 2, g);
 }
 
 typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,

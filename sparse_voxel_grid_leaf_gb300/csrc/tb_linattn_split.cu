@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
   constexpr int kStageBytes = 2 * kTerms * 2 * kTile;  // A, B: terms of two 64-key blocks
   constexpr int kProducts = kTerms == 3 ? 6 : 3;
 
+  if (kStates) let_next_kernel_start();
   extern __shared__ char s_raw[];
   __shared__ Shared s;
   // score tiles of each term, then the stages (the product A B^T reads the 8 KB before A too)
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
     float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
     const float log = log2f(decay);
     const float enter = chunks ? exp2f((reverse ? 31.f : 32.f) * log) : 1.f, full = exp2f(64.f * log);
+    if (l.phase == 2) wait_for_last_kernel();  // the states that enter
     f32x2 u[32];  // Z, by pairs of keys
     {
       const float* from = l.phase == 2 ? seg_state : p.first ? p.first + state_at : nullptr;
@@ -612,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
   if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
   if (warp == kWarpMma) tmem_free(tmem, 512);
   if (!steep || idle || warp >= 8) return;
+  if (l.phase == 2) wait_for_last_kernel();
   float* rows = reinterpret_cast<float*>(s_raw + (tiles - smem_addr(s_raw)));
   if constexpr (sizeof(E) == 4) walk_rows<float>(l, p, s.seg, h, rows);
   else if (is_half) walk_rows<__half>(l, p, s.seg, h, rows);
@@ -632,8 +635,7 @@ cudaError_t go(const LinLaunch& l, cudaStream_t s) {
     if (dev >= 0 && dev < 64) ready[dev] = true;
   }
   const int64_t blocks = (int64_t)l.segments * l.heads * l.n;
-  k_split<E, kTerms, kStates><<<(unsigned)blocks, kThreads, bytes, s>>>(l);
-  return cudaGetLastError();
+  return launch_early(k_split<E, kTerms, kStates>, (unsigned)blocks, kThreads, bytes, s, l.phase == 2, l);
 }
 
 }  // namespace

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
 // [blocks, width] in the workspace, summed by k_norm_weight in a fixed order.
 template <class T, int V, int NV>
 __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunch n) {
+  let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
   extern __shared__ float s_part[];  // [rows, per_row * NV * V] where a block has more than one row
   __shared__ float2 s_red[64];
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(32 * 8) k_norm_groups(NormLaunch n) {
 // buffers of a group of h, dy, dh; dx takes dy's place.
 template <class T>
 __global__ void __launch_bounds__(32 * 8) k_norm_backward_groups(NormBackwardLaunch n) {
+  let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
   constexpr int G = group_of<T>();
   extern __shared__ __align__(16) char s_group[];
@@ -457,6 +459,7 @@ __global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
   constexpr int kCols = 8, kRows = 64;
   __shared__ float s[kRows][kCols + 1];
   const int x = threadIdx.x % kCols, y = threadIdx.x / kCols, c = blockIdx.x * kCols + x;
+  wait_for_last_kernel();
   float sum = 0.f;
   if (c < n.a.width) {
     const float* part = n.a.workspace + c;
@@ -575,13 +578,12 @@ cudaError_t launch_norm_backward(const void* args, cudaStream_t s) {
 
 cudaError_t launch_norm_weight(const void* args, cudaStream_t s) {
   const NormBackwardLaunch& n = *(const NormBackwardLaunch*)args;
-  const int block = 512, blocks = (n.a.width + 7) / 8;
+  auto go = [&](auto kernel) { return launch_early(kernel, (n.a.width + 7) / 8, 512, 0, s, n.a.rows > 0, n); };
   switch (n.a.type) {
-    case TB_TYPE_F32: k_norm_weight<float><<<blocks, block, 0, s>>>(n); break;
-    case TB_TYPE_F16: k_norm_weight<__half><<<blocks, block, 0, s>>>(n); break;
-    default: k_norm_weight<__nv_bfloat16><<<blocks, block, 0, s>>>(n); break;
+    case TB_TYPE_F32: return go(k_norm_weight<float>);
+    case TB_TYPE_F16: return go(k_norm_weight<__half>);
+    default: return go(k_norm_weight<__nv_bfloat16>);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace tb

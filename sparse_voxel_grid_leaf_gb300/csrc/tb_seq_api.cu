@@ -244,19 +244,19 @@ struct LinSizes {
 // segments' own states first, their joining, then the outputs.  One block of a
 // chunk kernel (of two heads, where they are small) runs on a multiprocessor;
 // the states pass is as long as a walk nearly, and the two more launches take
-// 11 us.  So it pays where whole grids leave more than half the
-// multiprocessors idle (10 grids of 3000 rows and 6 heads, 60 walks: 90 us
-// split, 72 whole; 16 unequal grids, 64 walks: 170 and 275), and where a grid
-// is several segments (one grid of 600 rows: 25 us split, 19 whole; of 1000:
-// 25 and 26; of 2000: 26 and 45; in 32 bits, where a chunk takes three times
-// as long, of 600: 41 and 42).
+// 6 us.  So it pays where whole grids leave more than half the
+// multiprocessors idle (10 grids of 3000 rows and 6 heads, 60 walks: 85 us
+// split, 72 whole; 16 unequal grids, 64 walks: 164 and 275), and where a grid
+// is several segments (one grid of 600 rows: 20 us split, 19 whole; of 1000:
+// 20 and 26; of 2000: 21 and 45; in 32 bits, where a chunk takes three times
+// as long, of 600: 35 and 42).
 static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
   const bool tc = z.type == TB_TYPE_BF16, pairs = tc && linear_pairs(z.heads, z.key, z.value);
   const int64_t walks = (int64_t)(pairs ? (z.heads + 1) / 2 : z.heads) * problems, want = 2ll * sms;
   if (z.grids <= 0 || 20ll * z.grids * walks > 9ll * sms) return 0;
   int64_t seg = up(up(z.tokens * walks, want), 64) * 64;
   if (seg < 256) seg = 256;
-  return z.tokens >= (tc ? 3 : 2) * seg * z.grids && z.tokens >= (tc ? 900ll : 512ll) * z.grids ? (int32_t)seg : 0;
+  return z.tokens >= (tc ? 3 : 2) * seg * z.grids ? (int32_t)seg : 0;
 }
 
 static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
