@@ -16,13 +16,21 @@ constexpr int kMaxThreads = 512;
 __host__ __device__ constexpr int up_to(int x, int m) { return (x + m - 1) / m * m; }
 
 // Sums (the second one: sum or maximum) of two values over the threads of a
-// row: threadIdx.x runs over the row, warps are whole.  Rows of one warp need
-// no barrier.
+// row: threadIdx.x runs over the row, which has whole warps, or 4, 8 or 16
+// lanes of one.  Rows of one warp or less need no barrier.
 template <bool kMax>
 __device__ __forceinline__ float2 row_reduce(float x, float y, float2* s, int& turn) {
+  const int warps = blockDim.x >> 5;
+  if (!warps) {
+    for (int o = blockDim.x >> 1; o; o >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      const float z = __shfl_xor_sync(0xffffffffu, y, o);
+      y = kMax ? fmaxf(y, z) : y + z;
+    }
+    return make_float2(x, y);
+  }
   x = warp_sum(x);
   y = kMax ? warp_max(y) : warp_sum(y);
-  const int warps = blockDim.x >> 5;
   if (warps == 1) return make_float2(x, y);
   float2* at = s + (turn ^= 1) * 32;
   if ((threadIdx.x & 31) == 0) at[threadIdx.y * warps + (threadIdx.x >> 5)] = make_float2(x, y);
@@ -36,6 +44,15 @@ __device__ __forceinline__ float2 row_reduce(float x, float y, float2* s, int& t
   return v;
 }
 
+// Whether a thread has registers for the next row and the weight next to its
+// row (30000 rows of 4096 in 16 bits, four vectors a thread: 89 us so, 113 with
+// the loads at the row; of 8192, eight vectors: 492 and 181).  The gradient
+// holds dweight as well (15000 rows of 16384, four vectors: 869 and 367).
+template <class T, int V, int NV, bool kBackward>
+constexpr bool ahead() {
+  return NV * (V * (int)sizeof(T) + 3) / 4 <= (kBackward ? 16 : 32);
+}
+
 // Blocks stay and walk over rows; a row's elements are loaded while the one
 // before it is normed, and held as they came (16-bit pairs): the sum of the
 // residual stream is computed once for the mean and once for the output.
@@ -47,6 +64,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+  constexpr bool kAhead = ahead<T, V, NV, false>();
   Pack<T, V> w[NV], px[NV], pr[NV];
   auto load = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.x_row;
@@ -61,23 +79,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
     }
   };
   int64_t base = (int64_t)blockIdx.x * blockDim.y;
-  load(base + threadIdx.y);
+  if (kAhead) load(base + threadIdx.y);
+  auto weight = [&](int i) { return load_pack<T, V>((const T*)a.weight + (int64_t)(threadIdx.x + i * blockDim.x) * V); };
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if (v < vecs) w[i] = load_pack<T, V>((const T*)a.weight + (int64_t)v * V);
-  }
+  for (int i = 0; i < NV; ++i)
+    if (kAhead && threadIdx.x + i * blockDim.x < vecs) w[i] = weight(i);
   // block-uniform trip count: the barriers of row_reduce are passed by all
   for (; base < a.rows; base += stride) {
     const int64_t row = base + threadIdx.y;
     const bool live = row < a.rows;
     Pack<T, V> cx[NV], cr[NV];
+    if (!kAhead) load(row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       cx[i] = px[i];
       cr[i] = pr[i];
     }
-    load(row + stride);
+    if (kAhead) load(row + stride);
     auto sum_of = [&](int i, float (&f)[V]) {
       unpack<T, V>(cx[i], f);
       if (a.residual) {
@@ -99,7 +117,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
         for (int j = 0; j < V; ++j) sum = fmaf(f[j], f[j], sum);
         if constexpr (kFp8) {
           float g[V];
-          unpack<T, V>(w[i], g);
+          unpack<T, V>(kAhead ? w[i] : weight(i), g);
 #pragma unroll
           for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(f[j] * g[j]));
         }
@@ -121,7 +139,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
       if (live && v < vecs) {
         float f[V], g[V];
         sum_of(i, f);
-        unpack<T, V>(w[i], g);
+        unpack<T, V>(kAhead ? w[i] : weight(i), g);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] *= by * g[j];
         if constexpr (!kFp8) {
@@ -159,6 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
+  constexpr bool kAhead = ahead<T, V, NV, true>();
   float dw[NV][V] = {};
   Pack<T, V> w[NV], ph[NV], pd[NV], pg[NV];
   auto load = [&](int64_t row) {
@@ -173,23 +192,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
     }
   };
   int64_t base = (int64_t)blockIdx.x * blockDim.y;
-  load(base + threadIdx.y);
+  if (kAhead) load(base + threadIdx.y);
+  auto weight = [&](int i) { return load_pack<T, V>((const T*)a.weight + (int64_t)(threadIdx.x + i * blockDim.x) * V); };
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = threadIdx.x + i * blockDim.x;
-    if (v < vecs) w[i] = load_pack<T, V>((const T*)a.weight + (int64_t)v * V);
-  }
+  for (int i = 0; i < NV; ++i)
+    if (kAhead && threadIdx.x + i * blockDim.x < vecs) w[i] = weight(i);
   for (; base < a.rows; base += stride) {
     const int64_t row = base + threadIdx.y;
     const bool live = row < a.rows;
     Pack<T, V> ch[NV], cd[NV], cg[NV];
+    if (!kAhead) load(row);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       ch[i] = ph[i];
       cd[i] = pd[i];
       cg[i] = pg[i];
     }
-    load(row + stride);
+    if (kAhead) load(row + stride);
     float hh = 0.f, hd = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
         float h[V], d[V], g[V];
         unpack<T, V>(ch[i], h);
         unpack<T, V>(cd[i], d);
-        unpack<T, V>(w[i], g);
+        unpack<T, V>(kAhead ? w[i] : weight(i), g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           hh = fmaf(h[j], h[j], hh);
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
         float h[V], d[V], f[V], g[V];
         unpack<T, V>(ch[i], h);
         unpack<T, V>(cd[i], d);
-        unpack<T, V>(w[i], f);
+        unpack<T, V>(kAhead ? w[i] : weight(i), f);
         if (a.dh) unpack<T, V>(cg[i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -257,183 +276,206 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
 
 // ------------------------------------------- rows that no vector boundary meets
 //
-// A row of an odd width starts anywhere, but kGroup = 16 / sizeof(T) rows of a
-// dense tensor are a whole number of vectors: blocks move such groups through
-// shared memory, 16 bytes at a time, the next group while one is normed, and
-// read single elements there (50000 rows of 777 in 16 bits: 67 us, 125 element by element;
-// the gradient 74 us and 133).
-
-template <class T>
-constexpr int group_of() {
-  return 16 / (int)sizeof(T);
-}
+// A row of an odd width starts anywhere in a vector of 16 bytes.  Blocks move
+// groups of whole rows of a dense tensor through shared memory by the vectors
+// they lie in, the next group while one is normed, and read single elements
+// there (50000 rows of 777 in 16 bits: 67 us, 125 element by element; the
+// gradient 74 us and 133).  A group has up to 16 / sizeof(T) rows, a whole
+// number of vectors; fewer, with more warps each, where rows are wide.
+constexpr int kGroupWarps = 32;  // at most
 
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
                : "memory");
 }
 
-// Group `c` of rows, on its way into `dst`; the last group's tail byte-exact.
+// Rows [row, row + rows) of a dense tensor of `all` rows, on their way into
+// `dst`, as far into a vector as they lie in theirs: that offset, in elements.
+// The vectors at the ends come whole, but for the tensor's last.
 template <class T>
-__device__ __forceinline__ void fetch_group(T* dst, const void* src, int64_t c, int64_t rows, int width) {
-  constexpr int G = group_of<T>();
-  const int64_t left = rows - c * G;
-  const T* from = (const T*)src + c * G * width;
-  const int n = (int)(left < G ? left : G) * width, vecs = n / G;
-  for (int i = threadIdx.x; i < vecs; i += blockDim.x) copy_async(dst + i * G, from + i * G);
-  for (int i = vecs * G + threadIdx.x; i < n; i += blockDim.x) dst[i] = from[i];
+__device__ __forceinline__ int group_phase(int64_t row, int width) {
+  return (int)(row * width % (16 / (int)sizeof(T)));
 }
 template <class T>
-__device__ __forceinline__ void put_group(void* dst, const T* src, int64_t c, int64_t rows, int width) {
-  constexpr int G = group_of<T>();
-  const int64_t left = rows - c * G;
-  T* to = (T*)dst + c * G * width;
-  const int n = (int)(left < G ? left : G) * width, vecs = n / G;
-  for (int i = threadIdx.x; i < vecs; i += blockDim.x)
-    *reinterpret_cast<uint4*>(to + i * G) = *reinterpret_cast<const uint4*>(src + i * G);
-  for (int i = vecs * G + threadIdx.x; i < n; i += blockDim.x) to[i] = src[i];
+__device__ __forceinline__ void fetch_group(T* dst, const void* src, int64_t row, int rows, int64_t all, int width) {
+  constexpr int G = 16 / (int)sizeof(T);
+  const int phase = group_phase<T>(row, width);
+  const T* from = (const T*)src + row * width - phase;
+  const int end = phase + (int)min((int64_t)rows, all - row) * width;
+  const int64_t last = phase + (all - row) * width;
+  for (int i = threadIdx.x * G; i < end; i += blockDim.x * G) {
+    if (i + G <= last) copy_async(dst + i, from + i);
+    else
+      for (int j = i; j < end; ++j) dst[j] = from[j];
+  }
+}
+template <class T>
+__device__ __forceinline__ void put_group(void* dst, const T* src, int64_t row, int rows, int64_t all, int width) {
+  constexpr int G = 16 / (int)sizeof(T);
+  const int phase = group_phase<T>(row, width);
+  T* to = (T*)dst + row * width - phase;
+  const int end = phase + (int)min((int64_t)rows, all - row) * width;
+  for (int i = threadIdx.x * G; i < end; i += blockDim.x * G) {
+    if (i >= phase && i + G <= end) *reinterpret_cast<uint4*>(to + i) = *reinterpret_cast<const uint4*>(src + i);
+    else
+      for (int j = max(i, phase); j < min(i + G, end); ++j) to[j] = src[j];
+  }
 }
 
-// Shared memory: the weight, then `stages` buffers of a group of x, residual.
+// Sums (the second one: sum or maximum) over the warps of each row of a group.
+template <bool kMax>
+__device__ __forceinline__ float2 group_reduce(float x, float y, float2* s, int per_row) {
+  x = warp_sum(x);
+  y = kMax ? warp_max(y) : warp_sum(y);
+  if (per_row == 1) return make_float2(x, y);
+  const int warp = threadIdx.x >> 5, first = warp / per_row * per_row;
+  if ((threadIdx.x & 31) == 0) s[warp] = make_float2(x, y);
+  __syncthreads();
+  float2 v = s[first];
+  for (int i = 1; i < per_row; ++i) {
+    v.x += s[first + i].x;
+    v.y = kMax ? fmaxf(v.y, s[first + i].y) : v.y + s[first + i].y;
+  }
+  return v;
+}
+
+// Shared memory: the weight, then `nv` buffers of a group of x, residual.
 template <class T, bool kFp8>
-__global__ void __launch_bounds__(32 * 8) k_norm_groups(NormLaunch n) {
+__global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) {
   const tb_norm_args& a = n.a;
-  constexpr int G = group_of<T>();
   extern __shared__ __align__(16) char s_group[];
-  const int width = a.width, lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  __shared__ float2 s_red[kGroupWarps];
+  const int width = a.width, per_row = (int)(blockDim.x >> 5) / n.rows, g = (threadIdx.x >> 5) / per_row;
+  const int first = threadIdx.x - g * per_row * 32, step = per_row * 32;
   const int tensors = a.residual ? 2 : 1;
+  const int span = (int)(norm_buffer_bytes(width, sizeof(T), n.rows) / sizeof(T));
   T* w = reinterpret_cast<T*>(s_group);
-  T* buf = w + up_to(width, G);
+  T* buf = w + up_to(width, 16 / (int)sizeof(T));
   const float inv_width = 1.f / (float)width;
-  const int64_t groups = (a.rows + G - 1) / G;
+  const int64_t stride = (int64_t)gridDim.x * n.rows;
   for (int i = threadIdx.x; i < width; i += blockDim.x) w[i] = ((const T*)a.weight)[i];
-  auto fetch = [&](int64_t c, int st) {
-    if (c < groups) {
-      T* to = buf + (size_t)st * tensors * G * width;
-      fetch_group(to, a.x, c, a.rows, width);
-      if (a.residual) fetch_group(to + G * width, a.residual, c, a.rows, width);
+  auto fetch = [&](int64_t base, int st) {
+    if (base < a.rows) {
+      T* to = buf + (size_t)st * tensors * span;
+      fetch_group(to, a.x, base, n.rows, a.rows, width);
+      if (a.residual) fetch_group(to + span, a.residual, base, n.rows, a.rows, width);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int st = 0;
-  if (n.nv > 1) fetch(blockIdx.x, 0);
-  for (int64_t c = blockIdx.x; c < groups; c += gridDim.x) {
+  if (n.nv > 1) fetch((int64_t)blockIdx.x * n.rows, 0);
+  for (int64_t base = (int64_t)blockIdx.x * n.rows; base < a.rows; base += stride) {
     if (n.nv > 1) {
-      fetch(c + gridDim.x, st ^ 1);
+      fetch(base + stride, st ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
-      fetch(c, 0);
+      fetch(base, 0);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    T* x = buf + (size_t)st * tensors * G * width;
-    T* res = x + G * width;
-    const int64_t row = c * G + g;
-    if (row < a.rows) {
-      T* xr = x + g * width;
-      T* rr = res + g * width;
-      float sum = 0.f, top = 0.f;
-      for (int i = lane; i < width; i += 32) {
-        float f = RowType<T>::to(xr[i]);
-        if (a.residual) f += RowType<T>::to(rr[i]);
-        sum = fmaf(f, f, sum);
-        if (kFp8) top = fmaxf(top, fabsf(f * RowType<T>::to(w[i])));
+    T* x = buf + (size_t)st * tensors * span;
+    T* res = x + span;
+    const int64_t row = base + g;
+    const int at = group_phase<T>(base, width) + g * width;
+    const int mine = row < a.rows ? width : 0;
+    float sum = 0.f, top = 0.f;
+    for (int i = first; i < mine; i += step) {
+      float f = RowType<T>::to(x[at + i]);
+      if (a.residual) f += RowType<T>::to(res[at + i]);
+      sum = fmaf(f, f, sum);
+      if (kFp8) top = fmaxf(top, fabsf(f * RowType<T>::to(w[i])));
+    }
+    const float2 all = group_reduce<true>(sum, top, s_red, per_row);
+    const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
+    float by = r;
+    if (kFp8) {
+      top = all.y * r;
+      if (first == 0 && mine) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
+      by = top > 0.f ? 448.f / all.y : top == 0.f ? 0.f : r;
+    }
+    uint8_t* q = (uint8_t*)a.y + row * width;
+    for (int i = first; i < mine; i += step) {
+      float f = RowType<T>::to(x[at + i]);
+      if (a.residual) {
+        f += RowType<T>::to(res[at + i]);
+        res[at + i] = RowType<T>::from(f);
       }
-      sum = warp_sum(sum);
-      const float r = rsqrtf(fmaf(sum, inv_width, a.eps));
-      float by = r;
-      if (kFp8) {
-        top = warp_max(top);
-        const float all = top;
-        top *= r;
-        if (lane == 0) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
-        by = top > 0.f ? 448.f / all : top == 0.f ? 0.f : r;
-      }
-      uint8_t* q = (uint8_t*)a.y + row * width;
-      for (int i = lane; i < width; i += 32) {
-        float f = RowType<T>::to(xr[i]);
-        if (a.residual) {
-          f += RowType<T>::to(rr[i]);
-          rr[i] = RowType<T>::from(f);
-        }
-        f *= by * RowType<T>::to(w[i]);
-        if (kFp8) q[i] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
-        else xr[i] = RowType<T>::from(f);
-      }
+      f *= by * RowType<T>::to(w[i]);
+      if (kFp8) q[i] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
+      else x[at + i] = RowType<T>::from(f);
     }
     __syncthreads();
-    if (!kFp8) put_group(a.y, x, c, a.rows, width);
-    if (a.h_out) put_group(a.h_out, res, c, a.rows, width);
+    if (!kFp8) put_group(a.y, x, base, n.rows, a.rows, width);
+    if (a.h_out) put_group(a.h_out, res, base, n.rows, a.rows, width);
     if (n.nv > 1) st ^= 1;
     __syncthreads();  // the group's buffer may be filled again
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Shared memory: the weight and dweight's part in 32 bits, then `stages`
-// buffers of a group of h, dy, dh; dx takes dy's place.
+// Shared memory: the weight and dweight's part in 32 bits, then `nv` buffers
+// of a group of h, dy, dh; dx takes dy's place.
 template <class T>
-__global__ void __launch_bounds__(32 * 8) k_norm_backward_groups(NormBackwardLaunch n) {
+__global__ void __launch_bounds__(32 * kGroupWarps) k_norm_backward_groups(NormBackwardLaunch n) {
   let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
-  constexpr int G = group_of<T>();
   extern __shared__ __align__(16) char s_group[];
-  __shared__ float2 s_row[G];  // r and the factor of h
-  const int width = a.width, lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  __shared__ float2 s_red[kGroupWarps], s_row[8];  // r and the factor of h
+  const int width = a.width, per_row = (int)(blockDim.x >> 5) / n.rows, g = (threadIdx.x >> 5) / per_row;
+  const int first = threadIdx.x - g * per_row * 32, step = per_row * 32;
   const int tensors = a.dh ? 3 : 2;
+  const int span = (int)(norm_buffer_bytes(width, sizeof(T), n.rows) / sizeof(T));
   float* w = reinterpret_cast<float*>(s_group);
   float* dw = w + up_to(width, 4);
   T* buf = reinterpret_cast<T*>(dw + up_to(width, 4));
   const float inv_width = 1.f / (float)width;
-  const int64_t groups = (a.rows + G - 1) / G;
+  const int64_t stride = (int64_t)gridDim.x * n.rows;
   for (int i = threadIdx.x; i < width; i += blockDim.x) {
     w[i] = RowType<T>::to(((const T*)a.weight)[i]);
     dw[i] = 0.f;
   }
-  auto fetch = [&](int64_t c, int st) {
-    if (c < groups) {
-      T* to = buf + (size_t)st * tensors * G * width;
-      fetch_group(to, a.h, c, a.rows, width);
-      fetch_group(to + G * width, a.dy, c, a.rows, width);
-      if (a.dh) fetch_group(to + 2 * G * width, a.dh, c, a.rows, width);
+  auto fetch = [&](int64_t base, int st) {
+    if (base < a.rows) {
+      T* to = buf + (size_t)st * tensors * span;
+      fetch_group(to, a.h, base, n.rows, a.rows, width);
+      fetch_group(to + span, a.dy, base, n.rows, a.rows, width);
+      if (a.dh) fetch_group(to + 2 * span, a.dh, base, n.rows, a.rows, width);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int st = 0;
-  if (n.nv > 1) fetch(blockIdx.x, 0);
-  for (int64_t c = blockIdx.x; c < groups; c += gridDim.x) {
+  if (n.nv > 1) fetch((int64_t)blockIdx.x * n.rows, 0);
+  for (int64_t base = (int64_t)blockIdx.x * n.rows; base < a.rows; base += stride) {
     if (n.nv > 1) {
-      fetch(c + gridDim.x, st ^ 1);
+      fetch(base + stride, st ^ 1);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
     } else {
-      fetch(c, 0);
+      fetch(base, 0);
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    T* h = buf + (size_t)st * tensors * G * width;
-    T* d = h + G * width;
-    const T* dh = d + G * width;
-    const int rows = (int)min((int64_t)G, a.rows - c * G);
-    if (g < rows) {
-      float hh = 0.f, hd = 0.f;
-      for (int i = lane; i < width; i += 32) {
-        const float f = RowType<T>::to(h[g * width + i]);
-        hh = fmaf(f, f, hh);
-        hd = fmaf(f * w[i], RowType<T>::to(d[g * width + i]), hd);
-      }
-      hh = warp_sum(hh);
-      hd = warp_sum(hd);
-      const float r = rsqrtf(fmaf(hh, inv_width, a.eps));
-      if (lane == 0) s_row[g] = make_float2(r, -(r * r * r * hd * inv_width));
+    const int phase = group_phase<T>(base, width);
+    T* h = buf + (size_t)st * tensors * span + phase;
+    T* d = h + span;
+    const T* dh = d + span;
+    const int rows = (int)min((int64_t)n.rows, a.rows - base);
+    const int mine = g < rows ? width : 0;
+    float hh = 0.f, hd = 0.f;
+    for (int i = first; i < mine; i += step) {
+      const float f = RowType<T>::to(h[g * width + i]);
+      hh = fmaf(f, f, hh);
+      hd = fmaf(f * w[i], RowType<T>::to(d[g * width + i]), hd);
     }
+    const float2 all = group_reduce<false>(hh, hd, s_red, per_row);
+    const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
+    if (first == 0) s_row[g] = make_float2(r, -(r * r * r * all.y * inv_width));
     __syncthreads();
     // by columns: a thread's part of dweight stays its own
     for (int i = threadIdx.x; i < width; i += blockDim.x) {
       const float wi = w[i];
       float sum = dw[i];
-#pragma unroll
-      for (int k = 0; k < G; ++k) {
-        if (k >= rows) break;
+#pragma unroll 4
+      for (int k = 0; k < rows; ++k) {
         const float2 rm = s_row[k];
         const float f = RowType<T>::to(h[k * width + i]), e = RowType<T>::to(d[k * width + i]);
         sum = fmaf(e, f * rm.x, sum);
@@ -444,7 +486,7 @@ __global__ void __launch_bounds__(32 * 8) k_norm_backward_groups(NormBackwardLau
       dw[i] = sum;
     }
     __syncthreads();
-    put_group(a.dx, d, c, a.rows, width);
+    put_group(a.dx, d - phase, base, n.rows, a.rows, width);
     if (n.nv > 1) st ^= 1;
     __syncthreads();  // the group's buffer may be filled again
   }
@@ -491,18 +533,18 @@ cudaError_t allow(K* kernel, size_t bytes) {
 
 template <class T, bool kFp8>
 cudaError_t go_groups(const NormLaunch& n, cudaStream_t s) {
-  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.residual ? 2 : 1, n.nv, sizeof(T));
+  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.residual ? 2 : 1, n.rows, n.nv, sizeof(T));
   const cudaError_t e = allow(k_norm_groups<T, kFp8>, bytes);
   if (e != cudaSuccess) return e;
-  k_norm_groups<T, kFp8><<<n.blocks, 32 * group_of<T>(), bytes, s>>>(n);
+  k_norm_groups<T, kFp8><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();
 }
 template <class T>
 cudaError_t go_back_groups(const NormBackwardLaunch& n, cudaStream_t s) {
-  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.nv, 8);
+  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.rows, n.nv, 8);
   const cudaError_t e = allow(k_norm_backward_groups<T>, bytes);
   if (e != cudaSuccess) return e;
-  k_norm_backward_groups<T><<<n.blocks, 32 * group_of<T>(), bytes, s>>>(n);
+  k_norm_backward_groups<T><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();
 }
 

@@ -36,14 +36,18 @@ cudaError_t launch_rotary(const void* args, cudaStream_t s);
 struct NormLaunch {
   tb_norm_args a;
   int vec, per_row, nv, rows;  // threads of a row, vectors of a thread, rows of a block
-  int groups;                  // through shared memory by groups of rows, nv buffers deep
+  int groups;                  // through shared memory by groups of `rows` rows, nv buffers deep, per_row threads a block; 0: not
   int blocks;
 };
+// Bytes of a buffer for a group of rows, which starts anywhere in a vector.
+constexpr size_t norm_buffer_bytes(int width, int size, int rows) {
+  return ((size_t)rows * width * size + ((size_t)rows * width * size % 16 ? 15 + 16 : 0)) / 16 * 16;
+}
 // Shared memory of the kernels that move groups of rows: `fixed` bytes an
 // element of a row (a multiple of 16 in all), then the buffers.
-inline size_t norm_group_bytes(int width, int size, int tensors, int stages, int fixed) {
+inline size_t norm_group_bytes(int width, int size, int tensors, int rows, int stages, int fixed) {
   const size_t head = fixed == 8 ? 2 * (((size_t)width + 3) / 4 * 16) : ((size_t)width * size + 15) / 16 * 16;
-  return head + (size_t)stages * tensors * 16 * width;
+  return head + stages * tensors * norm_buffer_bytes(width, size, rows);
 }
 cudaError_t launch_norm(const void* args, cudaStream_t s);
 struct NormBackwardLaunch {

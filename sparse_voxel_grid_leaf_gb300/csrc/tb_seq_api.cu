@@ -27,9 +27,10 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // thread and rows of a block of the norm kernels, which exist for `counts`
 // groups a thread.  One group while that takes at most `wide` threads; else
 // the fewest that take at most `most`, as joining many warps costs a wide row
-// more than it loads (rows of 4096: 16 warps a row 154 us, 4 warps 150;
-// with the 8-bit output 130 and 90).  Few rows: one group, for the shortest
-// chain of loads.
+// more than it loads (60000 rows of 1536 in 16 bits: 6 warps a row 107 us, 3
+// warps 83; of 4096: 16 warps 154, 4 warps 150).  Rows of half a warp and less
+// share one (67722 rows of 64: 11 us, 17 with a warp each; the gradient 17 and
+// 29).  Few rows: one group, for the shortest chain of loads.
 struct NormShape {
   int per_row, nv, rows;
 };
@@ -38,6 +39,7 @@ NormShape norm_shape(bool many, int groups, const int* counts, int n, int wide, 
   for (int i = 0; i < n; ++i) {
     r.nv = counts[i];
     r.per_row = (int)(up(up(groups, counts[i]), 32) * 32);
+    while (many && r.per_row <= 32 && r.per_row > 4 && r.per_row / 2 * counts[i] >= groups) r.per_row /= 2;
     if (r.per_row <= (!many ? 512 : i == 0 ? wide : most)) break;
   }
   r.rows = many && r.per_row < 128 ? 128 / r.per_row : 1;
@@ -45,17 +47,31 @@ NormShape norm_shape(bool many, int groups, const int* counts, int n, int wide, 
 }
 constexpr int kVecs[] = {1, 2, 4, 8}, kOnes[] = {4, 8, 32};
 
-// Buffers for groups of rows through shared memory: two where two blocks then
-// fit a multiprocessor, else one, else none.
-int norm_stages(int width, int size, int tensors, int fixed) {
-  if (norm_group_bytes(width, size, tensors, 2, fixed) <= 100 * 1024) return 2;
-  return norm_group_bytes(width, size, tensors, 1, fixed) <= 200 * 1024 ? 1 : 0;
+// Rows of a group through shared memory and buffers for groups: as many rows
+// as make whole vectors where two buffers leave room for two blocks on a
+// multiprocessor, fewer rows where they are wide, down to a row and a buffer
+// (3598 rows of 5819, the gradient in 16 bits: 79 us by single rows, 530 element
+// by element).
+struct NormGroups {
+  int rows, stages;
+};
+NormGroups norm_groups(int width, int size, int tensors, int fixed) {
+  for (int rows = 16 / size; rows; rows /= 2)
+    if (norm_group_bytes(width, size, tensors, rows, 2, fixed) <= 100 * 1024) return {rows, 2};
+  for (int stages = 2; stages; --stages)
+    if (norm_group_bytes(width, size, tensors, 1, stages, fixed) <= 200 * 1024) return {1, stages};
+  return {0, 0};
 }
-int64_t norm_group_blocks(int64_t rows, int width, int size, int tensors, int stages, int fixed, int sms) {
-  int64_t fit = 208 * 1024 / (int64_t)(norm_group_bytes(width, size, tensors, stages, fixed) + 1024);
+// Blocks, and their threads: the more, the fewer blocks a multiprocessor holds
+// (10000 rows of 8191 in 16 bits, one block: the gradient 488 us with 256
+// threads, 322 with 1024; 50000 of 777 in 32 bits, three blocks: 113 with 256
+// each, 141 with 512).
+int norm_group_blocks(int64_t rows, int width, int size, int tensors, NormGroups g, int fixed, int sms, int* threads) {
+  int64_t fit = 208 * 1024 / (int64_t)(norm_group_bytes(width, size, tensors, g.rows, g.stages, fixed) + 1024);
   if (fit > 8) fit = 8;
-  const int64_t groups = up(rows, 16 / size);
-  return groups < fit * sms ? groups : fit * sms;
+  *threads = fit > 2 ? 256 : fit > 1 ? 512 : 1024;
+  const int64_t groups = up(rows, g.rows);
+  return (int)(groups < fit * sms ? groups : fit * sms);
 }
 
 }  // namespace
@@ -154,14 +170,14 @@ tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
   const bool dense = aligned16(a.x) && a.x_row == a.width && a.y_row == a.width && (a.fp8 || aligned16(a.y)) &&
                      (!a.residual || (aligned16(a.residual) && a.residual_row == a.width)) &&
                      (!a.h_out || (aligned16(a.h_out) && a.h_row == a.width));
-  const int stages = !n.vec && many && dense ? norm_stages(a.width, size, tensors, size) : 0;
-  n.groups = stages > 0;
+  const NormGroups groups = !n.vec && (many || a.width > 4096) && dense ? norm_groups(a.width, size, tensors, size) : NormGroups{0, 0};
+  n.groups = groups.rows > 0;
   if (n.groups) {
-    n.nv = stages;
-    n.per_row = n.rows = 0;
-    n.blocks = (int)norm_group_blocks(a.rows, a.width, size, tensors, stages, size, sms);
+    n.nv = groups.stages;
+    n.rows = groups.rows;
+    n.blocks = norm_group_blocks(a.rows, a.width, size, tensors, groups, size, sms, &n.per_row);
   } else {
-    const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 256, 128) : norm_shape(many, a.width, kOnes, 3, 32, 128);
+    const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 128, 128) : norm_shape(many, a.width, kOnes, 3, 32, 128);
     n.per_row = z.per_row, n.nv = z.nv, n.rows = z.rows;
     // blocks stay: as many as run at once, twice that many where a thread has more than a vector
     const int64_t fit = up(z.nv <= 1 ? 1024 : 2048, n.per_row * n.rows), blocks = up(a.rows, n.rows);
@@ -208,13 +224,13 @@ tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stre
   const int tensors = a.dh ? 3 : 2;
   const bool dense = aligned16(a.dy) && aligned16(a.h) && aligned16(a.dx) && a.dy_row == a.width && a.h_row == a.width &&
                      a.dx_row == a.width && (!a.dh || (aligned16(a.dh) && a.dh_row == a.width));
-  const int stages = !n.vec && many && dense ? norm_stages(a.width, size, tensors, 8) : 0;
+  const NormGroups groups = !n.vec && (many || a.width > 4096) && dense ? norm_groups(a.width, size, tensors, 8) : NormGroups{0, 0};
   int64_t blocks;
-  n.groups = stages > 0;
+  n.groups = groups.rows > 0;
   if (n.groups) {
-    n.nv = stages;
-    n.per_row = n.rows = 0;
-    blocks = norm_group_blocks(a.rows, a.width, size, tensors, stages, 8, sms);
+    n.nv = groups.stages;
+    n.rows = groups.rows;
+    blocks = norm_group_blocks(a.rows, a.width, size, tensors, groups, 8, sms, &n.per_row);
   } else {
     // dweight takes registers: up to two vectors a thread while the row fits 512
     const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 256, 512)

@@ -178,6 +178,32 @@ def test_norm_backward(dtype, rows, width, passing):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,width", [(700, 1001), (613, 5819), (40, 8191), (3, 16381), (1300, 40), (5000, 8), (700, 3)])
+def test_norm_of_rows_that_start_anywhere(dtype, rows, width):
+    """Dense rows of odd widths, from narrower than a warp to as wide as they may be."""
+    g = gen(rows + width)
+    x, r, dy = (normal(g, rows, width, dtype=dtype, scale=s) for s in (2.0, 3.0, 1.0))
+    w = normal(g, width, dtype=dtype)
+    for res in (None, r):
+        y, h = tb.rms_norm(x, w, res, eps=1e-5)
+        want, sum_ = R.norm(x, w, res, 1e-5)
+        near(y, want, want.abs(), dtype, terms=width + 16, what="y")
+        if res is not None:
+            near(h, sum_, sum_.abs(), dtype, terms=2, what="h")
+        q, scale, _ = tb.rms_norm_fp8(x, w, res, eps=1e-5)
+        top = want.abs().amax(-1) / 448
+        assert ((scale.double() - top).abs() <= (width + 20) * 2.0 ** -24 * top).all()
+        back, real = q.double(), want / top[:, None].clamp(min=1e-300)
+        assert ((back - real).abs() <= 2.0 ** -4 * real.abs().clamp(min=2.0 ** -6) * (1 + 1e-3) + (width + 40) * 2.0 ** -23).all()
+        dx, dw = tb.rms_norm_backward(dy, x, w, res, eps=1e-5)
+        want, wantw, size, sizew = R.norm_backward(dy, x, w, res, 1e-5)
+        near(dx, want, size, dtype, terms=3 * width + 30, what="dx")
+        near(dw, wantw, sizew, dtype, terms=rows + width + 30, what="dweight")
+        again = tb.rms_norm_backward(dy, x, w, res, eps=1e-5)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 def test_norm_gradient_against_differences():
     g = gen(3)
     x, r, w = (normal(g, 40, 96, scale=2.0), normal(g, 40, 96), normal(g, 96))
