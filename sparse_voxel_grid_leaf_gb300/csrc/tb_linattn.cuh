@@ -90,11 +90,12 @@ __device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) 
 }
 
 // The grid that has `rank` longer ones (ties: the lower index first), of at
-// most kLinMaxSorted grids.  One warp; the same in all lanes.
+// most kLinMaxSorted grids.  One warp; the same in all lanes.  Every block
+// does it, so it is short: 32 bits, eight shuffles in flight (64
+// grids of 32 rows, 8 heads of 128 x 128, 512 blocks: 29 us, 25 unsorted).
 __device__ __forceinline__ int lin_grid_of_rank(const LinLaunch& l, int rank) {
   const int lane = threadIdx.x & 31;
-  int64_t rows[kLinMaxSorted / 32];
-  int ahead[kLinMaxSorted / 32], found = 0;
+  int rows[kLinMaxSorted / 32], ahead[kLinMaxSorted / 32], found = 0;
 #pragma unroll
   for (int i = 0; i < kLinMaxSorted / 32; ++i) {
     rows[i] = -1;
@@ -102,18 +103,19 @@ __device__ __forceinline__ int lin_grid_of_rank(const LinLaunch& l, int rank) {
     if (32 * i + lane < l.grids) {
       int64_t begin, end;
       lin_grid_rows(l, 32 * i + lane, begin, end);
-      rows[i] = end - begin;
+      rows[i] = (int)(end - begin);
     }
   }
 #pragma unroll
   for (int j = 0; j < kLinMaxSorted / 32; ++j)
 #pragma unroll 1
-    for (int k = 0; k < 32 && 32 * j + k < l.grids; ++k) {
-      const int64_t x = __shfl_sync(0xffffffffu, rows[j], k);
+    for (int k0 = 0; k0 < 32 && 32 * j + k0 < l.grids; k0 += 8)
 #pragma unroll
-      for (int i = 0; i < kLinMaxSorted / 32; ++i)
-        ahead[i] += x > rows[i] || (x == rows[i] && 32 * j + k < 32 * i + lane);
-    }
+      for (int k = k0; k < k0 + 8; ++k) {  // of the lanes without a grid, -1 is ahead of none
+        const int x = __shfl_sync(0xffffffffu, rows[j], k);
+#pragma unroll
+        for (int i = 0; i < kLinMaxSorted / 32; ++i) ahead[i] += x + (32 * j + k < 32 * i + lane) > rows[i];
+      }
 #pragma unroll
   for (int i = 0; i < kLinMaxSorted / 32; ++i) {
     const unsigned hit = __ballot_sync(0xffffffffu, 32 * i + lane < l.grids && ahead[i] == rank);

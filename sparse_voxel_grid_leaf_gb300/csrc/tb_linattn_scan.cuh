@@ -56,29 +56,28 @@ __device__ __forceinline__ void scan_walk(const LinLaunch& l, const LinProblem& 
   const bool want_out = p.out && l.phase != 1;
   if (l.phase == 1 && seg.index + 1 == seg.count && !p.last) return;  // nobody reads this segment's state
   const float decay = l.decay[h];
-  const int lane = threadIdx.x & 31, slice = lane & 3;
+  const int lane = threadIdx.x & 31, slice = lane & 3, warp = threadIdx.x >> 5, warps = threads >> 5;
+  const T zero = RowType<T>::from(0.f);
   const int v0 = (threadIdx.x >> 5) * 16 + (lane >> 2) * 2;
   const int64_t state_at = ((int64_t)seg.grid * l.heads + h) * p.K * p.V;
   float* seg_state = p.seg ? p.seg + ((int64_t)seg.slot * l.heads + h) * p.K * p.V : nullptr;
 
-  f32x2 u[2][KS / 2];
+  f32x2 u[2][KS / 2] = {};
   auto key = [&](int i) { return (i / 4 * 4 + slice) * 4 + i % 4; };
+  const float* from = l.phase == 2 ? seg_state : l.phase == 0 && p.first ? p.first + state_at : nullptr;
+  if (from) {
+    const int64_t by_k = l.phase == 2 ? p.V : p.first_k, by_v = l.phase == 2 ? 1 : p.first_v;
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < KS; i += 2) {
-      float x[2];
+      for (int i = 0; i < KS; i += 2) {
+        float x[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = key(i + j), v = v0 + c;
-        x[j] = 0.f;
-        if (k < p.K && v < p.V) {
-          if (l.phase == 2) x[j] = seg_state[(int64_t)k * p.V + v];
-          else if (l.phase == 0 && p.first) x[j] = p.first[state_at + k * p.first_k + v * p.first_v];
-        }
+        for (int j = 0; j < 2; ++j)
+          x[j] = key(i + j) < p.K && v0 + c < p.V ? from[key(i + j) * by_k + (v0 + c) * by_v] : 0.f;
+        u[c][i / 2] = pair(x[0], x[1]);
       }
-      u[c][i / 2] = pair(x[0], x[1]);
-    }
+  }
 
   const int64_t origin = p.reverse ? seg.end - 1 - seg.first : seg.begin + seg.first;
   const int64_t dir = p.reverse ? -1 : 1;
@@ -87,16 +86,35 @@ __device__ __forceinline__ void scan_walk(const LinLaunch& l, const LinProblem& 
   for (int t0 = 0; t0 < seg.len; t0 += kScanRows) {
     const int nt = min(kScanRows, seg.len - t0);
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
-    for (int i = threadIdx.x; i < nt * KP; i += threads) {
-      const int t = i / KP, k = i % KP;
-      const int64_t row = origin + dir * (t0 + t);
-      s_a[t][k] = want_out && k < p.K ? RowType<T>::to(((const T*)p.a)[row * p.a_row + h * p.a_head + k]) : 0.f;
-      s_b[t][k] = k < p.K ? RowType<T>::to(((const T*)p.b)[row * p.b_row + h * p.b_head + k]) : 0.f;
-    }
-    for (int i = threadIdx.x; i < nt * 128; i += threads) {
-      const int t = i / 128, v = i % 128;
-      const int64_t row = origin + dir * (t0 + t);
-      s_c[t][v] = v < p.V ? RowType<T>::to(((const T*)p.c)[row * p.c_row + h * p.c_head + v]) : 0.f;
+    // two rows of a warp in flight
+    for (int t = 2 * warp; t < nt; t += 2 * warps) {
+      T x[2][KP / 32], y[2][KP / 32], z[2][4];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int64_t row = origin + dir * (t0 + t + r);
+        const T* a = (const T*)p.a + row * p.a_row + h * p.a_head;
+        const T* b = (const T*)p.b + row * p.b_row + h * p.b_head;
+        const T* c = (const T*)p.c + row * p.c_row + h * p.c_head;
+        const bool live = t + r < nt;
+#pragma unroll
+        for (int i = 0; i < KP / 32; ++i) {
+          const int k = i * 32 + lane;
+          x[r][i] = live && want_out && k < p.K ? a[k] : zero;
+          y[r][i] = live && k < p.K ? b[k] : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[r][i] = live && i * 32 + lane < p.V ? c[i * 32 + lane] : zero;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int i = 0; i < KP / 32; ++i) {
+          s_a[t + r][i * 32 + lane] = RowType<T>::to(x[r][i]);
+          s_b[t + r][i * 32 + lane] = RowType<T>::to(y[r][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_c[t + r][i * 32 + lane] = RowType<T>::to(z[r][i]);
+      }
     }
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 #pragma unroll 1

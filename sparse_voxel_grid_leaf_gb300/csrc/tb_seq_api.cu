@@ -265,11 +265,15 @@ struct LinSizes {
 // split, 72 whole; 16 unequal grids, 64 walks: 164 and 275), and where a grid
 // is several segments (one grid of 600 rows: 20 us split, 19 whole; of 1000:
 // 20 and 26; of 2000: 21 and 45; in 32 bits, where a chunk takes three times
-// as long, of 600: 35 and 42).
+// as long, of 600: 35 and 42).  Long grids leave up to a third idle (8 grids of
+// 7500 rows, the gradient of 4 heads of 128, 96 walks: 217 us split, 254 whole;
+// of 2500: 106 and 89), less long ones where the chunk is slowest (14 of 1400
+// in fp16, the gradient of 2 heads of 96 x 128, 84 walks: 143 and 238).
 static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
   const bool tc = z.type == TB_TYPE_BF16, pairs = tc && linear_pairs(z.heads, z.key, z.value);
   const int64_t walks = (int64_t)(pairs ? (z.heads + 1) / 2 : z.heads) * problems, want = 2ll * sms;
-  if (z.grids <= 0 || 20ll * z.grids * walks > 9ll * sms) return 0;
+  const bool slow = !tc && (z.key > 64 || z.value > 64), lengthy = z.tokens >= (slow ? 1024ll : 4096ll) * z.grids;
+  if (z.grids <= 0 || 20ll * z.grids * walks > (lengthy ? 14ll : 9ll) * sms) return 0;
   int64_t seg = up(up(z.tokens * walks, want), 64) * 64;
   if (seg < 256) seg = 256;
   return z.tokens >= (tc ? 3 : 2) * seg * z.grids ? (int32_t)seg : 0;
@@ -323,8 +327,9 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaun
                       (long long)a.workspace_bytes, (long long)(one * 4 * l.n));
     for (int i = 0; i < l.n; ++i) l.p[i].seg = (float*)a.workspace + i * one;
   }
-  // A chunk of 64 rows costs the tensor cores the same with one row in it: short grids take the recurrence.
-  const bool longer = a.tokens >= 16ll * a.grids;
+  // A chunk of 64 rows costs the tensor cores the same with one row in it: short grids take the recurrence (512 grids, 8
+  // heads of 128 x 128, us: 15 rows in bf16 167, 16 by chunks 149; 24 rows in fp16 267, 270 by chunks, in fp32 271 and 315).
+  const bool longer = a.tokens >= (a.type == TB_TYPE_BF16 ? 16ll : 24ll) * a.grids;
   const bool chunks = longer && linear_chunk_plan(g);
   for (int i = 0; i < l.n; ++i) {
     LinProblem& p = l.p[i];
