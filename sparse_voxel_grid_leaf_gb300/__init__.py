@@ -15,6 +15,9 @@ Follow-ups paragraph:
 * ``refine(b, f)``, ``coarsen(b, f)``  f in {2, 4, 8}
 * ``box_dilate(b, lo, hi)``  Minkowski sum with [lo, hi]^3 (unit boxes)
 * ``chain(b, ops)``  several passes with intermediate results on the device
+
+``seq`` has the operators of sequence models over voxel rows: ``rotary``,
+``rms_norm``, ``linear_attention`` and its single-token step.
 """
 from __future__ import annotations
 

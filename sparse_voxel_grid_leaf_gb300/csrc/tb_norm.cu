@@ -5,7 +5,12 @@
 // All bytes are read once and written once, so the bound is memory: a row's
 // elements stay in the registers of its threads between the sum of squares
 // and the output (per_row threads of nv vectors each; rows narrower than
-// a block share it).
+// a block share it).  The gradient adds two sums of a row and holds a part of
+// dweight in registers as well; its blocks' parts, a few MB, are joined by a
+// second kernel.  Measured, bf16: 124807 rows of 1024 with the residual's
+// addition 155 us, 6.58 TB/s; the gradient of 60013 rows of 1536 133 us, 5.5
+// TB/s (its instructions take 73% of the issue slots, as the forward's do);
+// 16 rows of 2048 to e4m3 5.5 us, most of it the launch.
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 

@@ -9,7 +9,10 @@
 // Every element is read once and written once, so the bound is memory.  The
 // sines and cosines depend on the token and the pair but not on the head: a
 // block takes a few tokens, computes their table once into shared memory and
-// streams all heads of q and k past it, 16 bytes at a time.
+// streams all heads of q and k past it, 16 bytes at a time, four rows of a
+// thread in flight.  Measured: 124807 tokens of 8 + 8 heads of 64 in bf16 with
+// three position axes 84 us, 6.07 TB/s; the inverse of 20011 tokens of 12 + 4
+// heads of 96 in fp32 43 us, 5.71 TB/s; 32 tokens 4.8 us, most of it the launch.
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 
