@@ -761,7 +761,7 @@ bool linear_chunk_plan(ChunkLaunch& g) {
 
 cudaError_t launch_linear_chunks(const void* args, cudaStream_t s) {
   const ChunkLaunch& g = *(const ChunkLaunch*)args;
-  const bool pair = linear_pairs(g.l.heads, g.l.p[0].K, g.l.p[0].V);
+  const bool pair = linear_pairs(g.l.p[0].K, g.l.p[0].V);
   bool exact = false;
   for (int i = 0; i < g.l.n; ++i) exact = exact || g.l.p[i].last;
   if (g.l.phase == 1) {

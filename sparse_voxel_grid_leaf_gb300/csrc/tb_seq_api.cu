@@ -270,7 +270,7 @@ struct LinSizes {
 // of 2500: 106 and 89), less long ones where the chunk is slowest (14 of 1400
 // in fp16, the gradient of 2 heads of 96 x 128, 84 walks: 143 and 238).
 static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
-  const bool tc = z.type == TB_TYPE_BF16, pairs = tc && linear_pairs(z.heads, z.key, z.value);
+  const bool tc = z.type == TB_TYPE_BF16, pairs = tc && linear_pairs(z.key, z.value);
   const int64_t walks = (int64_t)(pairs ? (z.heads + 1) / 2 : z.heads) * problems, want = 2ll * sms;
   const bool slow = !tc && (z.key > 64 || z.value > 64), lengthy = z.tokens >= (slow ? 1024ll : 4096ll) * z.grids;
   if (z.grids <= 0 || 20ll * z.grids * walks > (lengthy ? 14ll : 9ll) * sms) return 0;
