@@ -263,20 +263,30 @@ struct LinSizes {
 // 6 us.  So it pays where whole grids leave more than half the
 // multiprocessors idle (10 grids of 3000 rows and 6 heads, 60 walks: 85 us
 // split, 72 whole; 16 unequal grids, 64 walks: 164 and 275), and where a grid
-// is several segments (one grid of 600 rows: 20 us split, 19 whole; of 1000:
-// 20 and 26; of 2000: 21 and 45; in 32 bits, where a chunk takes three times
-// as long, of 600: 35 and 42).  Long grids leave up to a third idle (8 grids of
-// 7500 rows, the gradient of 4 heads of 128, 96 walks: 217 us split, 254 whole;
-// of 2500: 106 and 89), less long ones where the chunk is slowest (14 of 1400
-// in fp16, the gradient of 2 heads of 96 x 128, 84 walks: 143 and 238).
+// is several segments (one grid of 600 rows: 18.6 us whole, 16.5 split; 4 of 600
+// with 4 heads of 128: 18.6 and 20.6).  Long grids leave up to a third idle (8
+// grids of 7500 rows, the gradient of 4 heads of 128, 96 walks: 217 us split,
+// 254 whole; of 2500: 106 and 89), less long ones where the chunk is slowest
+// (14 of 1400 in fp16, the gradient of 2 heads of 96 x 128, 84 walks: 143 and
+// 238).
+// Segments are as short as gives each multiprocessor one, the chain being what
+// costs (in fp32 one grid of 1000 rows and 4 heads: 20.6 us by 64 rows, 34.9 by
+// 256; 5 unequal ones, 1333 rows, 20.6 split so, 41 whole), but in bf16 two
+// chunks (one grid of 2000 rows, 4 heads of 128: 20.6 us by 128 rows, 26.3 by
+// 64); where that takes more than 256 rows, two a multiprocessor.
 static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
   const bool tc = z.type == TB_TYPE_BF16, pairs = tc && linear_pairs(z.key, z.value);
-  const int64_t walks = (int64_t)(pairs ? (z.heads + 1) / 2 : z.heads) * problems, want = 2ll * sms;
+  const int64_t walks = (int64_t)(pairs ? (z.heads + 1) / 2 : z.heads) * problems;
   const bool slow = !tc && (z.key > 64 || z.value > 64), lengthy = z.tokens >= (slow ? 1024ll : 4096ll) * z.grids;
   if (z.grids <= 0 || 20ll * z.grids * walks > (lengthy ? 14ll : 9ll) * sms) return 0;
-  int64_t seg = up(up(z.tokens * walks, want), 64) * 64;
-  if (seg < 256) seg = 256;
-  return z.tokens >= (tc ? 3 : 2) * seg * z.grids ? (int32_t)seg : 0;
+  int64_t seg = up(up(z.tokens * walks, sms - z.grids * walks), 64) * 64;
+  if (seg > 256) {
+    seg = up(up(z.tokens * walks, 2 * sms), 64) * 64;
+    if (seg < 256) seg = 256;
+  }
+  if (tc && seg < 128) seg = 128;
+  const int64_t least = tc ? (seg < 256 ? 768 : 3 * seg) : seg < 96 ? 192 : 2 * seg;
+  return z.tokens >= least * z.grids ? (int32_t)seg : 0;
 }
 
 static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
