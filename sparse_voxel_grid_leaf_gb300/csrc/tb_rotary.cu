@@ -145,9 +145,11 @@ cudaError_t go(const RotaryLaunch& r, cudaStream_t s) {
 cudaError_t launch_rotary(const void* args, cudaStream_t s) {
   const RotaryLaunch& r = *(const RotaryLaunch*)args;
   switch (r.a.type) {
-    case TB_TYPE_F32: return r.vec ? go<float, 4>(r, s) : go<float, 1>(r, s);
-    case TB_TYPE_F16: return r.vec ? go<__half, 8>(r, s) : go<__half, 1>(r, s);
-    default: return r.vec ? go<__nv_bfloat16, 8>(r, s) : go<__nv_bfloat16, 1>(r, s);
+    case TB_TYPE_F32: return r.vec == 4 ? go<float, 4>(r, s) : go<float, 1>(r, s);
+    case TB_TYPE_F16: return r.vec == 8 ? go<__half, 8>(r, s) : r.vec == 4 ? go<__half, 4>(r, s) : go<__half, 1>(r, s);
+    default:
+      return r.vec == 8 ? go<__nv_bfloat16, 8>(r, s)
+             : r.vec == 4 ? go<__nv_bfloat16, 4>(r, s) : go<__nv_bfloat16, 1>(r, s);
   }
 }
 

@@ -34,8 +34,8 @@ template <> struct RowType<__nv_bfloat16> {
 // 16-bit elements would take a register each): 16 bytes for V =
 // RowType<T>::kVec, one element for V = 1.
 template <class T, int V> struct Pack {
-  static_assert(V * sizeof(T) == 16, "16-byte vectors");
-  uint32_t w[4];
+  static_assert(V * sizeof(T) == 16 || V * sizeof(T) == 8, "vectors of 16 or 8 bytes");
+  uint32_t w[V * sizeof(T) / 4];
 };
 template <class T> struct Pack<T, 1> {
   T e;
@@ -46,6 +46,9 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
   Pack<T, V> r;
   if constexpr (V == 1) {
     r.e = *p;
+  } else if constexpr (V * sizeof(T) == 8) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = u.x, r.w[1] = u.y;
   } else {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
     r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
@@ -56,6 +59,7 @@ __device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
 template <class T, int V>
 __device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& v) {
   if constexpr (V == 1) *p = v.e;
+  else if constexpr (V * sizeof(T) == 8) *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
   else *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
 }
 

@@ -27,7 +27,7 @@ int seq_sms();
 // ------------------------------------------------------------------- rotary
 struct RotaryLaunch {
   tb_rotary_args a;
-  int vec;        // 16-byte vectors everywhere, else one element at a time
+  int vec;        // elements of the vectors that rows are moved by
   int per_block;  // tokens of one block
 };
 cudaError_t launch_rotary(const void* args, cudaStream_t s);

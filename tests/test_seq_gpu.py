@@ -78,6 +78,14 @@ def test_rotary(dtype, layout, tokens, heads, kv, dim, rotated, axes):
     assert torch.equal(qkv[:, heads + kv:], kept[:, heads + kv:])
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("tokens,heads,kv,dim,rotated,axes", [
+    (257, 4, 1, 48, 24, 3), (3000, 2, 2, 80, 40, 3), (19, 3, 1, 12, 8, 1), (700, 1, 1, 20, 20, 1), (65, 5, 3, 44, 36, 2)])
+def test_rotary_of_rows_at_any_four_elements(dtype, layout, tokens, heads, kv, dim, rotated, axes):
+    test_rotary(dtype, layout, tokens, heads, kv, dim, rotated, axes)
+
+
 def test_rotary_positions():
     """64-bit positions beyond 2^31, one huge section, positions as columns of a wider tensor, no keys."""
     g = gen(4)
