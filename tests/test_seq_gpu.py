@@ -437,6 +437,33 @@ def test_steps_follow_the_prompt(dtype):
     near(state, last.double(), size[1], torch.float32, terms=500)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+def test_rows_past_32_bits(dtype):
+    """Rows of one buffer of more than 2^31 elements give what the same rows give by themselves."""
+    g = gen(8)
+    rows, stride = 36000, 60008
+    wide = torch.empty(rows, stride, device="cuda", dtype=dtype)
+    assert wide.numel() > 2 ** 31
+    parts = []
+    for i in range(4):  # q, k, v and an output gradient of two heads, near the ends of the rows
+        part = normal(g, rows, 2, 64, dtype=dtype)
+        view = wide[:, stride - 128 * (i + 1):stride - 128 * i].unflatten(1, (2, 64))
+        view.copy_(part)
+        parts.append((part, view))
+    decay = torch.tensor([0.9, 0.99], device="cuda")
+    ends = torch.tensor([0, 20000, 20000, rows], device="cuda")
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    f, w = tb.rotary_frequencies(64), normal(g, 64, dtype=dtype)
+
+    def every(q, k, v, do):
+        return [*tb.rotary(q, k, pos, f), tb.rms_norm(q[:, 1], w)[0], *tb.rms_norm_backward(do[:, 1], q[:, 1], w),
+                tb.linear_attention(q, k, v, decay, ends),
+                *(x for x in tb.linear_attention_backward(do, q, k, v, decay, ends) if x is not None)]
+
+    for x, y in zip(every(*(p for p, _ in parts)), every(*(v for _, v in parts))):
+        assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------------------------------- streams, graphs, refusals
 
 def test_streams_and_graphs():
