@@ -518,6 +518,10 @@ TB_API tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stre
  * and dstate (or NULL), the gradient of `state`.  The decay is a constant of
  * the model: it has no gradient here.
  *
+ * Rows are summed 64 at a time with powers of the decay between 2^-50 and 2^50
+ * in 32 bits: finite values and states beyond 2^70 in magnitude may overflow
+ * where a walk row by row would not.
+ *
  * workspace: at least tb_linear_attention_workspace(...) bytes, 256-byte
  * aligned (NULL where that is 0). */
 typedef struct tb_linear_args {

@@ -457,7 +457,7 @@ def test_rows_past_32_bits(dtype):
 
     def every(q, k, v, do):
         return [*tb.rotary(q, k, pos, f), tb.rms_norm(q[:, 1], w)[0], *tb.rms_norm_backward(do[:, 1], q[:, 1], w),
-                tb.linear_attention(q, k, v, decay, ends),
+                tb.linear_attention(q, k, v, decay, ends)[0],
                 *(x for x in tb.linear_attention_backward(do, q, k, v, decay, ends) if x is not None)]
 
     for x, y in zip(every(*(p for p, _ in parts)), every(*(v for _, v in parts))):
