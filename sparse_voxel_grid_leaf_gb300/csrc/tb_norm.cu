@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
 // A row of an odd width starts anywhere in a vector of 16 bytes.  Blocks move
 // groups of whole rows of a dense tensor through shared memory by the vectors
 // they lie in, the next group while one is normed, and read single elements
-// there (50000 rows of 777 in 16 bits: 67 us, 125 element by element; the
-// gradient 74 us and 133).  A group has up to 16 / sizeof(T) rows, a whole
+// there (50000 rows of 777 in 16 bits: 49 us, 82 element by element; the
+// gradient 81 us and 141).  A group has up to 16 / sizeof(T) rows, a whole
 // number of vectors; fewer, with more warps each, where rows are wide.
 constexpr int kGroupWarps = 32;  // at most
 
