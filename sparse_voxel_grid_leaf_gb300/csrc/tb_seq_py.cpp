@@ -97,6 +97,9 @@ bool tracked(const T*... t) {
   return c10::GradMode::is_enabled() && ((t && t->requires_grad()) || ...);
 }
 
+// The backward calls record nothing.
+[[noreturn]] void refuse_second(const char* what) { refuse("%s: gradients of gradients are not made", what); }
+
 int device_of(const char* what, const at::Tensor& t) {
   if (!t.is_cuda()) refuse("%s: tensors must be on the GPU", what);
   const int d = t.get_device(), now = c10::cuda::current_device();
@@ -369,6 +372,7 @@ TB_ENTRY(norm_backward, 5) {
   const at::Tensor& h = tensor(what, "h", a[1]);
   const at::Tensor& weight = tensor(what, "weight", a[2]);
   const at::Tensor* dh = maybe(what, "dh", a[3]);
+  if (tracked(&dy, &h, &weight, dh)) refuse_second(what);
   const int device = device_of(what, h);
   tb_norm_backward_args r{};
   r.type = type_of(what, h);
@@ -479,9 +483,12 @@ TB_ENTRY(linear, 8) {
 // or None, want) -> (dq, dk, dv, gradient of the first states or None)
 TB_ENTRY(linear_backward, 10) {
   const char* what = "linear_attention_backward";
-  Linear l(what, a);
   const at::Tensor& grad = tensor(what, "do", a[7]);
   const at::Tensor* dstate = maybe(what, "dstate", a[8]);
+  if (tracked(&tensor(what, "q", a[0]), &tensor(what, "k", a[1]), &tensor(what, "v", a[2]), &tensor(what, "decay", a[3]),
+              maybe(what, "state", a[5]), &grad, dstate))
+    refuse_second(what);
+  Linear l(what, a);
   const int64_t shape_o[3] = {l.q.rows, l.q.heads, l.v.dim}, shape_s[4] = {l.r.grids, l.r.heads, l.r.key, l.r.value};
   same(what, "do", grad, shape_o, l.dtype, l.device);
   const Rows g(what, "do", grad);

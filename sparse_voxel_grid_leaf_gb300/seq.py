@@ -111,8 +111,10 @@ def rotary_frequencies(dim: int, base: float = 10000.0, axes: int = 1, sections:
 
 @functools.lru_cache(None)
 def _functions():
-    """The autograd functions, made once torch is loaded."""
+    """The autograd functions, made once torch is loaded.  Their backward calls
+    record nothing, so gradients of their gradients are refused."""
     import torch
+    from torch.autograd.function import once_differentiable
 
     class Rotary(torch.autograd.Function):
         @staticmethod
@@ -122,9 +124,9 @@ def _functions():
             return _native.rotary(q, k, positions, frequencies, *how, False, False)
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dq, dk):
-            dq, dk = _native.rotary(dq.detach(), None if dk is None else dk.detach(), *ctx.saved_tensors, *ctx.how,
-                                    False, True)
+            dq, dk = _native.rotary(dq, dk, *ctx.saved_tensors, *ctx.how, False, True)
             return dq, dk, None, None, None, None, None
 
     class Norm(torch.autograd.Function):
@@ -136,6 +138,7 @@ def _functions():
             return (y, h) if residual is not None else y
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, dy, dh=None):
             h, weight = ctx.saved_tensors
             dx, dw = _native.norm_backward(dy, h, weight, dh, ctx.eps)
@@ -150,6 +153,7 @@ def _functions():
             return (o, last) if return_state else o
 
         @staticmethod
+        @once_differentiable
         def backward(ctx, do, dstate=None):
             dq, dk, dv, first = _native.linear_backward(*ctx.saved_tensors, ctx.scale, do, dstate,
                                                         ctx.needs_input_grad[5])
