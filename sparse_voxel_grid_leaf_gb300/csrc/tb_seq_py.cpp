@@ -100,6 +100,10 @@ bool tracked(const T*... t) {
 // The backward calls record nothing.
 [[noreturn]] void refuse_second(const char* what) { refuse("%s: gradients of gradients are not made", what); }
 
+// Tells autograd of a write to t's memory: a backward pass that saved it, or a
+// view of the same memory, then raises instead of reading what is new.
+void written(const at::Tensor& t) { t.unsafeGetTensorImpl()->bump_version(); }
+
 int device_of(const char* what, const at::Tensor& t) {
   if (!t.is_cuda()) refuse("%s: tensors must be on the GPU", what);
   const int d = t.get_device(), now = c10::cuda::current_device();
@@ -303,6 +307,8 @@ TB_ENTRY(rotary, 9) {
   if (inplace) {
     r.q_out = rq.p, r.q_out_row = rq.row, r.q_out_head = rq.head;
     r.k_out = rk.p, r.k_out_row = rk.row, r.k_out_head = rk.head;
+    written(q);
+    if (k) written(*k);
   } else {
     qo = empty({rq.rows, rq.heads, rq.dim}, q.scalar_type(), device);
     r.q_out = qo.data_ptr(), r.q_out_row = rq.heads * rq.dim, r.q_out_head = rq.dim;
@@ -553,6 +559,7 @@ TB_ENTRY(step, 7) {
   r.streams = q.rows, r.num_slots = shape_s[0];
   r.heads = (int32_t)q.heads, r.key = (int32_t)q.dim, r.value = (int32_t)v.dim;
   r.scale = a[6] == Py_None ? 1.f / std::sqrt((float)q.dim) : (float)number(a[6]);
+  written(state);
   check(tb_linear_attention_step(&r, stream_of(device)));
   return wrap(out);
 }

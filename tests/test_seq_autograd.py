@@ -72,3 +72,33 @@ def test_backward_calls_refuse_tracked_tensors():
             call()
         with torch.no_grad():
             call()
+
+
+def test_a_step_is_a_write_of_its_states():
+    """States that a backward pass still needs: an error where the step has overwritten them."""
+    x, decay = rows(1), torch.tensor([0.9, 0.99], device="cuda")
+    state = torch.randn(1, 2, 64, 64, device="cuda")
+    q = rows().requires_grad_()
+    o, _ = tb.linear_attention(q, rows(), rows(), decay, torch.tensor([0, 24], device="cuda"), state=state)
+    before = state._version
+    tb.linear_attention_step(x, x, x, decay, state)
+    assert state._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+
+
+def test_a_turn_in_place_is_a_write():
+    pos, f = torch.arange(24, dtype=torch.int32, device="cuda"), tb.rotary_frequencies(64)
+    qk = rows(24, 4)
+    q, k = qk[:, :2], qk[:, 2:]
+    w = torch.randn(24, 2, 64, device="cuda", requires_grad=True)
+    for call, inputs in ((tb.rotary, (q, k)), (tb.rotary_backward, (q, k)), (tb.rotary, (q, None)), (tb.rotary, (k, None))):
+        y = w * qk[:, :2] + w * qk[:, 2:]  # saves both
+        before = qk._version
+        call(*inputs, pos, f, inplace=True)
+        assert qk._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+    before = qk._version
+    tb.rotary(q, k, pos, f)
+    assert qk._version == before
