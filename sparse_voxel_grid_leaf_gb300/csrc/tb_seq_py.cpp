@@ -92,9 +92,13 @@ bool truth(PyObject* o) {
   return x != 0;
 }
 
+// Whether a gradient is asked for, or one of the tensors carries a forward-mode
+// tangent, which the operators do not make either: the autograd functions, and
+// the calls that refuse, say so.
 template <class... T>
 bool tracked(const T*... t) {
-  return c10::GradMode::is_enabled() && ((t && t->requires_grad()) || ...);
+  return (c10::GradMode::is_enabled() && ((t && t->requires_grad()) || ...)) ||
+         ((t && t->_fw_grad(/*level=*/0).defined()) || ...);
 }
 
 // The backward calls record nothing.

@@ -7,6 +7,8 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():  # pragma: no cover - CPU containers
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
+import torch.autograd.forward_ad as fwAD  # noqa: E402
+
 import sparse_voxel_grid_leaf_gb300 as tb  # noqa: E402
 
 
@@ -102,3 +104,26 @@ def test_a_turn_in_place_is_a_write():
     before = qk._version
     tb.rotary(q, k, pos, f)
     assert qk._version == before
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_forward_mode_is_refused(name):
+    call = calls()[name]
+    with fwAD.dual_level():
+        x = fwAD.make_dual(rows(), rows())
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            call(x)
+
+
+def test_forward_mode_is_refused_in_place_and_backward():
+    x, w, decay = rows(), torch.ones(64, device="cuda"), torch.tensor([0.9, 0.99], device="cuda")
+    pos, f = torch.arange(24, dtype=torch.int32, device="cuda"), tb.rotary_frequencies(64)
+    state = torch.zeros(24, 2, 64, 64, device="cuda")
+    with fwAD.dual_level():
+        t = fwAD.make_dual(rows(), rows())
+        for call in (lambda: tb.rotary(t, None, pos, f, inplace=True), lambda: tb.rotary_backward(t, None, pos, f),
+                     lambda: tb.rms_norm_fp8(t, w), lambda: tb.rms_norm_backward(t, x, w),
+                     lambda: tb.linear_attention_backward(t, x, x, x, decay),
+                     lambda: tb.linear_attention_step(t, x, x, decay, state)):
+            with pytest.raises(tb.TBError):
+                call()
