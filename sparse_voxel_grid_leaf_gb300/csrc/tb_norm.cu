@@ -58,6 +58,21 @@ constexpr bool ahead() {
   return NV * (V * (int)sizeof(T) + 3) / 4 <= (kBackward ? 16 : 32);
 }
 
+// What takes a row's h w to e4m3, from top = max |h w| and r: max |y| is r top,
+// and y / scale is h w 448 / top.  448 / top is beyond 32 bits for a top below
+// 2^-119, so h w of rows below 2^-100 is raised by 2^100, exactly, before the
+// quotient meets it; and h meets w first, as a large weight may stand at a zero.
+// A NaN in a row makes all of its y NaN; fmaxf drops them (scale 0 or finite)
+// and the conversion keeps them.
+struct Fp8Row {
+  float scale, up, by;
+  __device__ __forceinline__ float operator()(float h, float w) const { return h * w * up * by; }
+};
+__device__ __forceinline__ Fp8Row fp8_row(float top, float r) {
+  const float most = top * r, up = top < 0x1p-100f ? 0x1p100f : 1.f;
+  return {most > 0.f ? most * (1.f / 448.f) : 0.f, up, most > 0.f ? 448.f / (top * up) : most == 0.f ? 0.f : r};
+}
+
 // Blocks stay and walk over rows; a row's elements are loaded while the one
 // before it is normed, and held as they came (16-bit pairs): the sum of the
 // residual stream is computed once for the mean and once for the output.
@@ -130,13 +145,10 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
     }
     const float2 all = row_reduce<true>(sum, top, s_red, turn);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
-    float by = r;
+    Fp8Row q8{};
     if constexpr (kFp8) {
-      // max |y| is r max |h w|.  A NaN in a row makes all of its y NaN; fmaxf
-      // drops them (scale 0 or finite) and the conversion keeps them.
-      top = all.y * r;
-      if (live && threadIdx.x == 0) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
-      by = top > 0.f ? 448.f / all.y : top == 0.f ? 0.f : r;
+      q8 = fp8_row(all.y, r);
+      if (live && threadIdx.x == 0) a.scale[row] = q8.scale;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -146,7 +158,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
         sum_of(i, f);
         unpack<T, V>(kAhead ? w[i] : weight(i), g);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] *= by * g[j];
+        for (int j = 0; j < V; ++j) f[j] = kFp8 ? q8(f[j], g[j]) : f[j] * (r * g[j]);
         if constexpr (!kFp8) {
           store_pack<T, V>((T*)a.y + row * a.y_row + (int64_t)v * V, pack<T, V>(f));
         } else {
@@ -392,12 +404,8 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) 
     }
     const float2 all = group_reduce<true>(sum, top, s_red, per_row);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
-    float by = r;
-    if (kFp8) {
-      top = all.y * r;
-      if (first == 0 && mine) a.scale[row] = top > 0.f ? top * (1.f / 448.f) : 0.f;
-      by = top > 0.f ? 448.f / all.y : top == 0.f ? 0.f : r;
-    }
+    const Fp8Row q8 = kFp8 ? fp8_row(all.y, r) : Fp8Row{};
+    if (kFp8 && first == 0 && mine) a.scale[row] = q8.scale;
     uint8_t* q = (uint8_t*)a.y + row * width;
     for (int i = first; i < mine; i += step) {
       float f = RowType<T>::to(x[at + i]);
@@ -405,9 +413,9 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) 
         f += RowType<T>::to(res[at + i]);
         res[at + i] = RowType<T>::from(f);
       }
-      f *= by * RowType<T>::to(w[i]);
-      if (kFp8) q[i] = __nv_cvt_float_to_fp8(f, __NV_SATFINITE, __NV_E4M3);
-      else x[at + i] = RowType<T>::from(f);
+      const float g = RowType<T>::to(w[i]);
+      if (kFp8) q[i] = __nv_cvt_float_to_fp8(q8(f, g), __NV_SATFINITE, __NV_E4M3);
+      else x[at + i] = RowType<T>::from(f * (r * g));
     }
     __syncthreads();
     if (!kFp8) put_group(a.y, x, base, n.rows, a.rows, width);
