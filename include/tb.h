@@ -505,11 +505,13 @@ TB_API tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stre
  *   S_t = decay S_{t-1} + k_t v_t^T,  o_t = scale q_t S_t
  * with q, k rows [tokens, heads, key], v and o rows [tokens, heads, value]
  * and 32-bit states [grids, heads, key, value].  decay[head] is in [0, 1].
- * offsets: int64 [grids + 1] on the device, from 0 to tokens, not decreasing
- * (values outside are clamped to the rows; rows of no grid are not written);
- * NULL: one grid.  state: the states that grids start from (NULL: zero);
- * state_out (or NULL): the states after each grid's last row, which for a
- * grid without rows is its first.  key, value <= 128.
+ * offsets: int64 [grids + 1] on the device, not decreasing (values outside the
+ * rows are clamped to them); NULL: one grid.  Rows before the first offset and
+ * past the last, as a buffer of a fixed capacity has them, belong to no grid:
+ * their values do not matter, and their outputs and gradients are zeros.
+ * state: the states that grids start from (NULL: zero); state_out (or NULL):
+ * the states after each grid's last row, which for a grid without rows is its
+ * first.  key, value <= 128.
  *
  * The backward call gives, for gradients `grad` of o and dstate_out (NULL:
  * zero) of state_out, with U_t = decay U_{t+1} + scale q_t do_t^T from

@@ -25,6 +25,55 @@ __device__ __forceinline__ void lin_grid_rows(const LinLaunch& l, int b, int64_t
   end = min(max(l.offsets[b + 1], begin), l.tokens);
 }
 
+// The rows that grids have are [begin, end): those before the first offset and
+// past the last one belong to none.
+struct LinCover {
+  int64_t begin, end;
+};
+__device__ __forceinline__ LinCover lin_cover(const LinLaunch& l) {
+  if (!l.offsets) return {0, l.tokens};
+  const int64_t begin = min(max(l.offsets[0], (int64_t)0), l.tokens);
+  return {begin, min(max(l.offsets[l.grids], begin), l.tokens)};
+}
+
+// Zeros for the output rows [r0, r1) of `heads` heads from h on, by `threads`
+// threads of which this is number `rank`, counting the rows that no grid has:
+// row r is row r of the call, past the cover's begin row r - begin + end.
+// E: any type of the outputs' size.
+template <class E>
+__device__ __noinline__ void lin_zero_rows(const LinProblem& p, LinCover c, int64_t r0, int64_t r1, int h, int heads,
+                                           int rank, int threads) {
+  constexpr int kVec = 16 / (int)sizeof(E);
+  const bool vec = ((uintptr_t)p.out & 15) == 0 && p.o_row % kVec == 0 && p.o_head % kVec == 0 && p.V % kVec == 0;
+  const int units = vec ? p.V / kVec : p.V;  // of a row's head; as many rows at a time as the threads take
+  const int many = threads / units, step = many ? units : threads;
+  if (many && rank >= many * units) return;
+  for (int64_t r = r0 + (many ? rank / units : 0); r < r1; r += many ? many : 1) {
+    E* to = (E*)p.out + (r < c.begin ? r : r - c.begin + c.end) * p.o_row + h * p.o_head;
+    for (int i = 0; i < heads; ++i, to += p.o_head)
+      for (int at = rank % step; at < units; at += step) {
+        if (vec) *reinterpret_cast<uint4*>(to + at * kVec) = make_uint4(0u, 0u, 0u, 0u);
+        else to[at] = E(0);
+      }
+  }
+}
+// A slot's share of all of them, in the kernel's prologue by warps that have no
+// part in it: calls whose offsets cover the rows take as long as before (32
+// grids of 2048 rows, 16 heads of 64 in bf16: 105 us), a buffer of 131072 rows
+// of 16 heads of 128 that holds one grid of 65536 358 us, 270 with its 268 MB of
+// other rows left alone.
+template <class E>
+__device__ __forceinline__ void lin_zero_share(const LinLaunch& l, const LinProblem& p, int slot, int h, int heads, int rank,
+                                               int threads) {
+  const LinCover c = lin_cover(l);
+  const int64_t rows = c.begin + l.tokens - c.end;
+  if (rows == 0) return;
+  const int64_t per = (rows + l.segments - 1) / l.segments, r0 = min(slot * per, rows);
+  lin_zero_rows<E>(p, c, r0, min(r0 + per, rows), h, heads, rank, threads);
+}
+template <int size> struct LinBits { typedef uint16_t type; };
+template <> struct LinBits<4> { typedef uint32_t type; };
+
 __device__ __forceinline__ int lin_segments_of(const LinLaunch& l, int64_t rows) {
   return rows > 0 ? (int)((rows + l.segment - 1) / l.segment) : 1;
 }

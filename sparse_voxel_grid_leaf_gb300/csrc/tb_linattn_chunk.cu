@@ -234,6 +234,9 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         }
       }
     }
+  } else if (!kStates && warp >= kWarpScores) {
+    constexpr int first = kWarpScores * 32;
+    lin_zero_share<uint16_t>(l, p, slot0, h0, min(kHeads, l.heads - h0), threadIdx.x - first, threads_of(kPair, kStates) - first);
   }
   tc_fence_before();
   __syncthreads();

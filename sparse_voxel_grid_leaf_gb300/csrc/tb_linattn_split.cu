@@ -222,6 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
     const float log = log2f(decay), x = reverse ? (float)(m - 32) : (float)(31 - m);
     s.w[m] = m < kC ? p.fold * exp2f(x * log) : 0.f;
     s.o[m] = m < kC ? p.mul * exp2f(-x * log) : 0.f;
+  } else if (!kStates && warp > kWarpMma) {
+    constexpr int first = (kWarpMma + 1) * 32;
+    lin_zero_share<typename LinBits<sizeof(E)>::type>(l, p, slot0, h, 1, threadIdx.x - first, kThreads - first);
   }
   tc_fence_before();
   __syncthreads();

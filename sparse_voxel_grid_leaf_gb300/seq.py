@@ -233,9 +233,11 @@ def linear_attention(q, k, v, decay, offsets=None, state=None, scale: Optional[f
     """Linear attention with a decay for each head over the rows of each grid:
     ``S_t = decay * S_(t-1) + k_t v_t^T``, ``o_t = scale * q_t S_t``.  q, k
     ``[T, H, K]``, v ``[T, H, V]`` of one type (K, V <= 128), decay float32
-    ``[H]`` in [0, 1], offsets int64 ``[B + 1]`` (None: one grid).  ``state``:
-    float32 ``[B, H, K, V]`` states to start from (None: zero).  ``scale``:
-    default ``K ** -0.5``.  Returns (o, last states or None)."""
+    ``[H]`` in [0, 1], offsets int64 ``[B + 1]``, not decreasing (None: one
+    grid).  Rows before the first offset or past the last belong to no grid:
+    their outputs and gradients are zeros.  ``state``: float32 ``[B, H, K, V]``
+    states to start from (None: zero).  ``scale``: default ``K ** -0.5``.
+    Returns (o, last states or None)."""
     if stream is not None:
         return _on_stream(linear_attention, stream, q, k, v, decay, offsets, state, scale, return_state)
     out = _native.linear(q, k, v, decay, offsets, state, scale, return_state)

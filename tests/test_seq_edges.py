@@ -10,7 +10,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU containers
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import sparse_voxel_grid_leaf_gb300 as tb  # noqa: E402
-from tests.test_seq_gpu import gen  # noqa: E402
+from tests.test_seq_gpu import attention_inputs, gen, near, normal  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -58,3 +58,62 @@ def test_fp8_norm_of_one_tiny_element(width):
     assert torch.equal(q.float(), want)
     assert torch.isfinite(scale).all() and (scale >= 0).all()
     assert ((scale[:2].double() - 1e-37 * 1e3 / 448).abs() <= 1e-6 * 1e-34 / 448).all()
+
+
+# ------------------------------------------------------------------------------------------- rows that no grid covers
+
+def poisoned(*shapes_and_types):
+    """Leaves NaN in memory that the allocator hands out next."""
+    for shape, dtype in shapes_and_types * 2:
+        torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+UNCOVERED = [([3, 50], 64), ([0, 20, 41], 64), ([10, 10, 64], 64), ([5, 5, 5], 33), ([70, 90], 64), ([-9, 30], 64),
+             ([2, 9, 17, 20], 30), ([700, 4000], 6000), ([1, 3000], 3001)]
+
+
+@pytest.mark.parametrize("dtype,key,value,pad", [
+    (torch.bfloat16, 64, 64, 0), (torch.bfloat16, 128, 128, 0), (torch.bfloat16, 64, 64, 3), (torch.float16, 128, 64, 0),
+    (torch.float32, 40, 72, 0), (torch.float32, 33, 17, 1)], ids=str)
+@pytest.mark.parametrize("offsets,tokens", UNCOVERED, ids=str)
+def test_rows_of_no_grid_are_zeros(dtype, key, value, pad, offsets, tokens):
+    """Outputs and gradients of rows before the first offset and past the last one are zeros; those of the grids are
+    the recurrence's.  Three heads: an ordinary one, one without memory, a pair's lone second half."""
+    heads, scale = 3, 0.4
+    q, k, v, decay, _, _, do, _ = attention_inputs(tokens, [tokens], heads, key, value, dtype, False,
+                                                   [0.97, 0.0, 0.9], pad)
+    off = torch.tensor(offsets, device="cuda")
+    shapes = [((tokens, heads, n), dtype) for n in (key, key, value)]
+    poisoned(*shapes)
+    o, _ = tb.linear_attention(q, k, v, decay, off, scale=scale)
+    poisoned(*shapes)
+    dq, dk, dv, _ = tb.linear_attention_backward(do, q, k, v, decay, off, scale=scale)
+    ends = [min(max(x, 0), tokens) for x in offsets]
+    inside = slice(ends[0], ends[-1])
+    lengths = [b - a for a, b in zip(ends, ends[1:])]
+    args = (q[inside], k[inside], v[inside], decay, lengths, None, scale, do[inside])
+    want, size = R.attention(*args), R.attention_sizes(*args)
+    terms = 2 * (max(key, value) + max(lengths) + 64)
+    for name, x, i in (("o", o, 0), ("dq", dq, 2), ("dk", dk, 3), ("dv", dv, 4)):
+        outside = torch.cat([x[:ends[0]], x[ends[-1]:]])
+        assert (outside == 0).all(), name
+        near(x[inside], want[i], size[i], dtype, terms=terms, roundings=3 if dtype == torch.bfloat16 else 0, what=name)
+
+
+def test_padding_rows_do_not_reach_a_weight():
+    """A buffer of a fixed capacity: what lies past the last grid is no part of the projection's gradient."""
+    g = gen(3)
+    x, w = normal(g, 4096, 32), normal(g, 32, 192).requires_grad_()
+    decay = torch.tensor([0.9], device="cuda")
+    grads = []
+    for n in (4096, 1000):
+        rows = x[:n]
+        poisoned(*[((n, 1, 64), torch.float32)] * 4)
+        q, k, v = (rows @ w).unflatten(1, (3, 1, 64)).unbind(1)
+        o, _ = tb.linear_attention(q, k, v, decay, torch.tensor([0, 400, 1000], device="cuda"))
+        grad, = torch.autograd.grad((o * 0.01).square().sum(), w)
+        grads.append(grad)
+    assert torch.isfinite(grads[0]).all()
+    size = grads[1].abs().max()
+    # 1000 roundings of 2^-24, of terms whose magnitudes add up to some sqrt(1000) times their sum
+    assert ((grads[0] - grads[1]).abs() <= 2e-3 * size).all()
