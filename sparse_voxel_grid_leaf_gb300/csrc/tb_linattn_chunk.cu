@@ -91,8 +91,9 @@ struct Shared {
 
 // Adds the scores times c_j of the rows j whose value is not finite to the
 // rows i that see them, in a warp's staged output of 32 values (the product
-// had zeros in their place).
-__device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t scores, uint32_t c_tile, int n, bool reverse) {
+// had zeros in their place).  sign: of the problem's scale.
+__device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t scores, uint32_t c_tile, int n, bool reverse,
+                                            float sign) {
   const int lane = threadIdx.x & 31, v = ((threadIdx.x >> 5) & 1) * 32 + lane;
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
@@ -101,7 +102,7 @@ __device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t scores, uin
 #pragma unroll 1
     for (int i = reverse ? 0 : j; i <= (reverse ? j : n - 1); ++i) {
       const uint32_t at = stage + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) << 4) + (lane & 7) * 2;
-      const float o = fmaf(shared_bf16(tile_at(scores, i, j)), c, shared_bf16(at));
+      const float o = fmaf(shared_bf16(tile_at(scores, i, j)) * sign, c, shared_bf16(at));
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)(bf16x2(o, o) & 0xffffu)) : "memory");
     }
   }
@@ -111,7 +112,7 @@ __device__ __noinline__ void add_not_finite(uint32_t stage, uint32_t scores, uin
 // memory, the weights of a value that is not finite left out.  The columns
 // hold keys from `key` on; the lane's value is v % 64 of the tile.
 __device__ __noinline__ void add_not_finite_state(uint32_t columns, int keys, uint32_t b_tile, int key, uint32_t c_tile,
-                                                  int n) {
+                                                  int n, float sign) {
   const int v = ((threadIdx.x >> 5) & 1) * 32 + (threadIdx.x & 31);
 #pragma unroll 1
   for (int k0 = 0; k0 < keys; k0 += 16) {
@@ -125,7 +126,8 @@ __device__ __noinline__ void add_not_finite_state(uint32_t columns, int keys, ui
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int k = key + k0 + i;
-        y[i] = __float_as_uint(fmaf(shared_bf16(tile_at(b_tile + (k >> 6) * kTile, j, k & 63)), c, __uint_as_float(y[i])));
+        y[i] = __float_as_uint(
+            fmaf(shared_bf16(tile_at(b_tile + (k >> 6) * kTile, j, k & 63)) * sign, c, __uint_as_float(y[i])));
       }
     }
     __syncwarp();
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         if (s.bad[st] == (uint32_t)t + 1) {
           const uint32_t at = stage0 + st * kStageBytes;
           add_not_finite_state(lanes + kColKv + t % kKvs * 128 + head * 64 + half * NK, NK, at + (kTileB + head) * kTile,
-                               half * NK, at + (kTileC + (quarter >> 1)) * kTile, n);
+                               half * NK, at + (kTileC + (quarter >> 1)) * kTile, n, sign_of(p.fold));
         }
         const f32x2 d2 = pair(d, d);
 #pragma unroll
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
         __syncwarp();
         if (bad) {
           add_not_finite(buf, tiles + ((t & 1) * kHeads + head) * kTile,
-                         stage0 + st * kStageBytes + (kTileC + (quarter >> 1)) * kTile, n, reverse);
+                         stage0 + st * kStageBytes + (kTileC + (quarter >> 1)) * kTile, n, reverse, sign_of(p.mul) * sign_of(p.fold));
           tc_fence_before();
           arrive(kOFree + t % kOs);
         }

@@ -120,6 +120,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&r)[8]) {
 template <class E>
 __device__ __noinline__ void add_not_finite_split(const LinProblem& p, bool is_half, int64_t row0, int h, int v, int n,
                                                   uint32_t scores, int terms) {
+  const float sign = sign_of(p.mul) * sign_of(p.fold);
 #pragma unroll 1
   for (int j = 0; j < n; ++j) {
     const float c = load1<E>(p.c, (row0 + j) * p.c_row + h * p.c_head + v, is_half);
@@ -129,7 +130,7 @@ __device__ __noinline__ void add_not_finite_split(const LinProblem& p, bool is_h
       float s = 0.f;
       for (int t = 0; t < terms; ++t) s += shared_bf16(tile_at(scores + t * kTile, i, j));
       const int64_t at = (row0 + i) * p.o_row + h * p.o_head + v;
-      store1<E>(p.out, at, is_half, fmaf(s, c, load1<E>(p.out, at, is_half)));
+      store1<E>(p.out, at, is_half, fmaf(s * sign, c, load1<E>(p.out, at, is_half)));
     }
   }
 }
@@ -137,6 +138,7 @@ __device__ __noinline__ void add_not_finite_split(const LinProblem& p, bool is_h
 template <class E>
 __device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, bool is_half, int64_t row0, int h, int v, int n,
                                                         uint32_t columns, int key, int keys) {
+  const float sign = sign_of(p.fold);
 #pragma unroll 1
   for (int k0 = 0; k0 < keys; k0 += 16) {
     uint32_t y[16];
@@ -151,7 +153,7 @@ __device__ __noinline__ void add_not_finite_state_split(const LinProblem& p, boo
         const int k = key + k0 + i;
         if (k < p.K)
           y[i] = __float_as_uint(
-              fmaf(load1<E>(p.b, (row0 + j) * p.b_row + h * p.b_head + k, is_half), c, __uint_as_float(y[i])));
+              fmaf(load1<E>(p.b, (row0 + j) * p.b_row + h * p.b_head + k, is_half) * sign, c, __uint_as_float(y[i])));
       }
     }
     __syncwarp();

@@ -37,6 +37,9 @@ __device__ __forceinline__ float shared_bf16(uint32_t at) {
   return __uint_as_float((uint32_t)bits << 16);
 }
 __device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+// What is left of a scale next to a value that is not finite: its sign, or 0 or
+// NaN, which make the product NaN.
+__device__ __forceinline__ float sign_of(float x) { return x > 0.f ? 1.f : x < 0.f ? -1.f : x; }
 // Element x of row r in a tile of 64-element rows.
 __device__ __forceinline__ uint32_t tile_at(uint32_t tile, int r, int x) {
   return tile + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + (x & 7) * 2;

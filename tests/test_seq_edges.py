@@ -117,3 +117,37 @@ def test_padding_rows_do_not_reach_a_weight():
     size = grads[1].abs().max()
     # 1000 roundings of 2^-24, of terms whose magnitudes add up to some sqrt(1000) times their sum
     assert ((grads[0] - grads[1]).abs() <= 2e-3 * size).all()
+
+
+# --------------------------------------------------------------------------------------------------------- infinities
+
+@pytest.mark.parametrize("dtype,key,value", [(torch.bfloat16, 64, 64), (torch.bfloat16, 128, 128),
+                                             (torch.float16, 64, 64), (torch.float32, 96, 64)], ids=str)
+@pytest.mark.parametrize("scale", [0.5, -0.5, 0.0])
+def test_sign_of_infinity(dtype, key, value, scale):
+    """One infinite element among positive ones: what it reaches has the scale's sign (NaN for a scale of zero)."""
+    g = gen(key)
+    q, k, v, do = (torch.rand(64, 2, n, generator=g, device="cuda").add(0.5).to(dtype) for n in (key, key, value, value))
+    decay, ends = torch.tensor([0.9, 0.99], device="cuda"), torch.tensor([0, 64], device="cuda")
+    first = torch.zeros(1, 2, key, value, device="cuda")
+
+    def reached(x):
+        assert (torch.isnan(x) if scale == 0 else x == (float("inf") if scale > 0 else -float("inf"))).all()
+
+    bad = v.clone()
+    bad[20, 1, 3] = float("inf")
+    o, last = tb.linear_attention(q, k, bad, decay, ends, scale=scale, return_state=True)
+    reached(o[20:, 1, 3])
+    assert torch.isfinite(o[:20]).all() and torch.isfinite(o[:, 0]).all() and torch.isfinite(o[:, 1, :3]).all()
+    assert (last[0, 1, :, 3] == float("inf")).all() and torch.isfinite(last[0, 0]).all()
+    bad = do.clone()
+    bad[20, 1, 3] = float("inf")
+    dq, dk, dv, dfirst = tb.linear_attention_backward(bad, q, k, v, decay, ends, state=first, scale=scale)
+    reached(dv[:21, 1, 3])
+    assert torch.isfinite(dv[21:]).all() and torch.isfinite(dv[:, 0]).all()
+    reached(dfirst[0, 1, :, 3])
+    bad = q.clone()
+    bad[20, 1, 3] = float("inf")
+    dq, dk, dv, _ = tb.linear_attention_backward(do, bad, k, v, decay, ends, state=first, scale=scale)
+    reached(dk[:21, 1, 3])
+    assert torch.isfinite(dk[21:]).all() and torch.isfinite(dk[:, 0]).all()
