@@ -562,7 +562,8 @@ TB_API tb_status tb_linear_attention_status(tb_stream stream);
  * slots[n] of `state`; NULL: slot n) is decayed, takes k_n v_n^T in, and
  * gives o_n = scale q_n S, all in place.  A stream whose slot is outside
  * [0, num_slots) touches no state and its output is zero.  No two streams may
- * share a slot.  states [num_slots, heads, key, value]; key, value <= 256. */
+ * share a slot.  states [num_slots, heads, key, value], 16-byte aligned where
+ * value is a multiple of 4; key, value <= 256. */
 typedef struct tb_linear_step_args {
   const void *q, *k, *v;
   void* out;

@@ -466,8 +466,11 @@ tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream st
   if (!a.slots && a.num_slots < a.streams)
     return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: %lld streams, %lld states", (long long)a.streams,
                     (long long)a.num_slots);
-  if (!a.q || !a.k || !a.v || !a.out || !a.decay || (a.num_slots && (!a.state || !aligned16(a.state))))
-    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: bad pointer");
+  // states of whole vectors are read by vectors, others element by element
+  if (!a.q || !a.k || !a.v || !a.out || !a.decay ||
+      (a.num_slots && (!a.state || (uintptr_t)a.state % (a.value % 4 == 0 ? 16 : 4))))
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: bad pointer (states are 16-byte aligned where the values "
+                    "of a head are a multiple of 4)");
   TB_SEQ_CUDA(seq_launch(kSeqStep, (cudaStream_t)stream, launch_linear_step, &l));
   return TB_OK;
 }

@@ -151,3 +151,21 @@ def test_sign_of_infinity(dtype, key, value, scale):
     dq, dk, dv, _ = tb.linear_attention_backward(do, bad, k, v, decay, ends, state=first, scale=scale)
     reached(dk[:21, 1, 3])
     assert torch.isfinite(dk[21:]).all() and torch.isfinite(dk[:, 0]).all()
+
+
+# ------------------------------------------------------------------------------------------------------------- states
+
+def test_step_of_states_at_any_element():
+    """Contiguous states that start off a 16-byte boundary, as a slice of a pool does for odd sizes."""
+    g = gen(5)
+    pool = normal(g, 4, 3, 5, 7)
+    q, k, v = (normal(g, 3, 3, n) for n in (5, 5, 7))
+    decay = torch.tensor([0.5, 0.9, 1.0], device="cuda")
+    before, state = pool.clone(), pool[1:]
+    assert state.data_ptr() % 16
+    o = tb.linear_attention_step(q, k, v, decay, state, scale=0.5)
+    want = R.attention(q, k, v, decay, [1, 1, 1], before[1:], 0.5)
+    size = R.attention_sizes(q, k, v, decay, [1, 1, 1], before[1:], 0.5)
+    near(o, want[0], size[0], torch.float32, terms=24)
+    near(state, want[1], size[1], torch.float32, terms=4)
+    assert torch.equal(pool[0], before[0])
