@@ -683,15 +683,9 @@ cudaError_t go(const ChunkLaunch& g, cudaStream_t s) {
   constexpr int bytes = 1024 + stages_of(kStates) * stage_bytes(kStates) +
                         (kStates ? 0 : (kPair ? 4 : 2) * kTile + 4 * 2 * kOutTile);
   static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
-  static bool ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<bool> ready[kMaxDevices];
+  const cudaError_t e = allow_shared(k_chunks<kPair, kTerms, kStates>, bytes, ready);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_chunks<kPair, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev] = true;
-  }
   const int64_t blocks = (int64_t)g.l.segments * (kPair ? (g.l.heads + 1) / 2 : g.l.heads) * g.l.n;
   return launch_early(k_chunks<kPair, kTerms, kStates>, (unsigned)blocks, threads_of(kPair, kStates), bytes, s,
                       g.l.phase == 2, g);

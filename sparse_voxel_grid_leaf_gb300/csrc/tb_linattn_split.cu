@@ -634,15 +634,9 @@ template <class E, int kTerms, bool kStates>
 cudaError_t go(const LinLaunch& l, cudaStream_t s) {
   constexpr int bytes = 1024 + kTerms * kTile + 2 * 2 * kTerms * 2 * kTile;
   static_assert(bytes > 116 * 1024 && bytes < 222 * 1024, "one block a multiprocessor: tensor memory is not shared");
-  static bool ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<bool> ready[kMaxDevices];
+  const cudaError_t e = allow_shared(k_split<E, kTerms, kStates>, bytes, ready);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(k_split<E, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) ready[dev] = true;
-  }
   const int64_t blocks = (int64_t)l.segments * l.heads * l.n;
   return launch_early(k_split<E, kTerms, kStates>, (unsigned)blocks, kThreads, bytes, s, l.phase == 2, l);
 }

@@ -537,17 +537,11 @@ __global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
   }
 }
 
-// Lets a kernel take `bytes` of shared memory.
-template <class K>
-cudaError_t allow(K* kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <class T, bool kFp8>
 cudaError_t go_groups(const NormLaunch& n, cudaStream_t s) {
   const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.residual ? 2 : 1, n.rows, n.nv, sizeof(T));
-  const cudaError_t e = allow(k_norm_groups<T, kFp8>, bytes);
+  static std::atomic<bool> ready[kMaxDevices];
+  const cudaError_t e = allow_shared(k_norm_groups<T, kFp8>, kNormGroupBytes, ready);
   if (e != cudaSuccess) return e;
   k_norm_groups<T, kFp8><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();
@@ -555,7 +549,8 @@ cudaError_t go_groups(const NormLaunch& n, cudaStream_t s) {
 template <class T>
 cudaError_t go_back_groups(const NormBackwardLaunch& n, cudaStream_t s) {
   const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.rows, n.nv, 8);
-  const cudaError_t e = allow(k_norm_backward_groups<T>, bytes);
+  static std::atomic<bool> ready[kMaxDevices];
+  const cudaError_t e = allow_shared(k_norm_backward_groups<T>, kNormGroupBytes, ready);
   if (e != cudaSuccess) return e;
   k_norm_backward_groups<T><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();

@@ -8,6 +8,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -135,6 +136,23 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   c.attrs = at;
   c.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
+// Lets a kernel take up to `bytes` of dynamic shared memory.  The limit belongs
+// to the kernel, not to the launch: it is set to the most that any call takes,
+// once for each device, so that calls from several host threads never lower it
+// under one another.  ready: the kernel's own.
+constexpr int kMaxDevices = 64;
+template <class K>
+cudaError_t allow_shared(K* kernel, int bytes, std::atomic<bool> (&ready)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known && ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) ready[dev].store(true, std::memory_order_release);
+  return e;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {

@@ -49,6 +49,7 @@ inline size_t norm_group_bytes(int width, int size, int tensors, int rows, int s
   const size_t head = fixed == 8 ? 2 * (((size_t)width + 3) / 4 * 16) : ((size_t)width * size + 15) / 16 * 16;
   return head + stages * tensors * norm_buffer_bytes(width, size, rows);
 }
+constexpr int kNormGroupBytes = 200 * 1024;  // at most
 cudaError_t launch_norm(const void* args, cudaStream_t s);
 struct NormBackwardLaunch {
   tb_norm_backward_args a;

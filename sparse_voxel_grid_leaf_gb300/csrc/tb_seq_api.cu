@@ -57,9 +57,9 @@ struct NormGroups {
 };
 NormGroups norm_groups(int width, int size, int tensors, int fixed) {
   for (int rows = 16 / size; rows; rows /= 2)
-    if (norm_group_bytes(width, size, tensors, rows, 2, fixed) <= 100 * 1024) return {rows, 2};
+    if (norm_group_bytes(width, size, tensors, rows, 2, fixed) <= kNormGroupBytes / 2) return {rows, 2};
   for (int stages = 2; stages; --stages)
-    if (norm_group_bytes(width, size, tensors, 1, stages, fixed) <= 200 * 1024) return {1, stages};
+    if (norm_group_bytes(width, size, tensors, 1, stages, fixed) <= kNormGroupBytes) return {1, stages};
   return {0, 0};
 }
 // Blocks, and their threads: the more, the fewer blocks a multiprocessor holds

@@ -1,7 +1,11 @@
 """The sequence operators on the GPU where their inputs are at an edge."""
+import ctypes
+import threading
+
 import pytest
 
 from tests import _seq_reference as R
+from tests.test_seq_abi import NORM
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +173,32 @@ def test_step_of_states_at_any_element():
     near(o, want[0], size[0], torch.float32, terms=24)
     near(state, want[1], size[1], torch.float32, terms=4)
     assert torch.equal(pool[0], before[0])
+
+
+# -------------------------------------------------------------------------------------------------- several host threads
+
+def test_two_threads_of_different_widths():
+    """Widths whose kernels take different amounts of shared memory, from two host threads at once."""
+    lib = tb.lib()
+    failed, start = [], threading.Barrier(2)
+
+    def go(width):
+        stream = torch.cuda.Stream()
+        x, w = torch.randn(700, width, device="cuda").bfloat16(), torch.ones(width, device="cuda").bfloat16()
+        y = torch.empty_like(x)
+        args = NORM.pack(x.data_ptr(), 0, w.data_ptr(), y.data_ptr(), 0, 0, 700, width, 0, width, 0, width, 2, 0, 1e-6)
+        torch.cuda.synchronize()
+        start.wait()
+        for _ in range(20000):
+            st = lib.tb_rms_norm(args, ctypes.c_void_p(stream.cuda_stream))
+            if st:
+                failed.append((width, st, lib.tb_last_error()))
+                break
+        stream.synchronize()
+
+    threads = [threading.Thread(target=go, args=(width,)) for width in (8191, 4001)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
