@@ -1,5 +1,6 @@
 """Builds libtb.so in-tree with nvcc for sm_103a (GB300), and _seq.so, the
-Python entry points of its sequence operators, with the host compiler.
+Python entry points of its sequence operators, with the host compiler where
+torch is installed.
 
 The translation units compile in parallel and are linked with the static
 CUDA runtime, so the library needs only the NVIDIA driver at run time.
@@ -15,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtb.so")
-SEQ = os.path.join(HERE, "_seq.so")
+SEQ, SEQ_OBJ = os.path.join(HERE, "_seq.so"), os.path.join(BUILD, "tb_seq_py.o")
 SOURCES = ["tb_api.cu", "tb_prepass.cu", "tb_chain.cu", "tb_noalloc.cu", "tb_kmap.cu",
            "tb_seq_api.cu", "tb_rotary.cu", "tb_norm.cu", "tb_linattn.cu",
            "tb_linattn_chunk.cu", "tb_linattn_split.cu"]
@@ -38,10 +39,15 @@ def _stale(out, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _torch_command():
-    """The compiler command of _seq.so up to its inputs, and torch's library folder."""
+def _torch():
+    """The folder of the installed torch, or None."""
     import importlib.util
-    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else None
+
+
+def _torch_command(root):
+    """The compiler command of _seq.so up to its inputs, and torch's library folder."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -74,11 +80,15 @@ def build(force=False, verbose=False, extra_flags=()):
             print(r.stderr, file=sys.stderr)
         return r
 
-    seq_src, seq_obj = os.path.join(CSRC, "tb_seq_py.cpp"), os.path.join(BUILD, "tb_seq_py.o")
-    cxx, torch_lib = _torch_command()
     built = len(jobs)
-    if force or _stale(seq_obj, [seq_src] + headers):
-        jobs.append([*cxx, "-c", seq_src, "-o", seq_obj])
+    seq_src, torch = os.path.join(CSRC, "tb_seq_py.cpp"), _torch()
+    if torch:
+        cxx, torch_lib = _torch_command(torch)
+        if force or _stale(SEQ_OBJ, [seq_src] + headers):
+            jobs.append([*cxx, "-c", seq_src, "-o", SEQ_OBJ])
+    else:
+        print("torch is not installed: _seq.so, the Python entry points of the sequence operators, is left out",
+              file=sys.stderr)
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, jobs))
@@ -86,9 +96,9 @@ def build(force=False, verbose=False, extra_flags=()):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if force or _stale(SEQ, [seq_obj, LIB]):
+    if torch and (force or _stale(SEQ, [SEQ_OBJ, LIB])):
         tmp = SEQ + ".tmp%d" % os.getpid()
-        run([cxx[0], "-shared", "-o", tmp, seq_obj, "-L", HERE, "-l:libtb.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
+        run([cxx[0], "-shared", "-o", tmp, SEQ_OBJ, "-L", HERE, "-l:libtb.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
              "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"])
         os.replace(tmp, SEQ)
     return LIB
