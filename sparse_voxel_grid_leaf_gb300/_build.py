@@ -46,6 +46,12 @@ def _torch():
     return os.path.dirname(spec.origin) if spec else None
 
 
+def _torch_version(root):
+    """What _seq.so is built for, as text: it links torch's C++ ABI, which differs between versions."""
+    with open(os.path.join(root, "version.py")) as f:
+        return f.read()
+
+
 def _torch_command(root):
     """The compiler command of _seq.so up to its inputs, and torch's library folder."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
@@ -84,7 +90,12 @@ def build(force=False, verbose=False, extra_flags=()):
     seq_src, torch = os.path.join(CSRC, "tb_seq_py.cpp"), _torch()
     if torch:
         cxx, torch_lib = _torch_command(torch)
-        if force or _stale(SEQ_OBJ, [seq_src] + headers):
+        made_for, target = SEQ_OBJ + ".torch", " ".join(cxx) + "\n" + _torch_version(torch)
+        other = True
+        if os.path.exists(made_for):
+            with open(made_for) as f:
+                other = f.read() != target
+        if force or other or _stale(SEQ_OBJ, [seq_src] + headers):
             jobs.append([*cxx, "-c", seq_src, "-o", SEQ_OBJ])
     else:
         print("torch is not installed: _seq.so, the Python entry points of the sequence operators, is left out",
@@ -96,11 +107,13 @@ def build(force=False, verbose=False, extra_flags=()):
         tmp = LIB + ".tmp%d" % os.getpid()
         run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if torch and (force or _stale(SEQ, [SEQ_OBJ, LIB])):
+    if torch and (force or other or _stale(SEQ, [SEQ_OBJ, LIB])):
         tmp = SEQ + ".tmp%d" % os.getpid()
         run([cxx[0], "-shared", "-o", tmp, SEQ_OBJ, "-L", HERE, "-l:libtb.so", "-Wl,-rpath,$ORIGIN", "-L", torch_lib,
              "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"])
         os.replace(tmp, SEQ)
+        with open(made_for, "w") as f:
+            f.write(target)
     return LIB
 
 

@@ -57,3 +57,28 @@ def test_a_second_build_does_nothing(built, commands):
     assert "tb_seq_py.cpp" in compiled(commands) and first == len(_build.SOURCES) + 3
     _build.build()
     assert len(commands) == first
+
+
+def test_another_torch_is_another_build(built, commands, monkeypatch, tmp_path):
+    """The entry points link torch's C++ ABI: another version, or another place, builds and links them again."""
+    _build.build()
+    other = tmp_path / "torch"
+    other.mkdir()
+    root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(root, "version.py")) as f:
+        (other / "version.py").write_text(f.read())
+    find = importlib.util.find_spec
+
+    class Spec:
+        origin = str(other / "__init__.py")
+
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: Spec if name == "torch" else find(name, *a))
+    for change in (None, "__version__ = '99.0'\n"):
+        if change:
+            (other / "version.py").write_text(change)
+        del commands[:]
+        _build.build()
+        assert compiled(commands) == ["tb_seq_py.cpp"] and len(commands) == 2
+        del commands[:]
+        _build.build()
+        assert not commands
