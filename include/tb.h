@@ -558,6 +558,12 @@ TB_API tb_status tb_linear_attention_backward(const tb_linear_backward_args* arg
  * used).  Blocks until `stream` is done. */
 TB_API tb_status tb_linear_attention_status(tb_stream stream);
 
+/* Self-test of that report without a GPU fault: one warp waits as the kernels
+ * do (kernel 0: the bfloat16 one, 1: the other) for a phase that nothing
+ * completes, and gives up after spin_limit polls (1 to 2^22).  Returns once it
+ * is queued on `stream`; the context stays usable. */
+TB_API tb_status tb_linear_attention_selftest_wait(int32_t kernel, int32_t spin_limit, tb_stream stream);
+
 /* One token of each of `streams` sequences: the state of stream n (slot
  * slots[n] of `state`; NULL: slot n) is decayed, takes k_n v_n^T in, and
  * gives o_n = scale q_n S, all in place.  A stream whose slot is outside

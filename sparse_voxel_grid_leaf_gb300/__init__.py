@@ -97,6 +97,8 @@ def lib():
                 "tb_kernel_map": [vp, vp, vp, vp, i32, i32, vp, i64, vp],
                 "tb_stride1_box": [i32, i32, vp, vp],
                 "tb_selftest_wait": [i32, i32, vp],
+                "tb_linear_attention_status": [vp],
+                "tb_linear_attention_selftest_wait": [i32, i32, vp],
                 "tb_batch_export_many": [vp, i32, vp, vp, vp, vp, vp],
                 "tb_validate": [vp, vp],
                 "tb_batch_get_view": [vp, ctypes.POINTER(_View)],

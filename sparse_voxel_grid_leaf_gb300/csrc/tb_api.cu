@@ -83,7 +83,7 @@ const char* const kKernelNames[kKNumKinds] = {"prepass_leaves", "chain",        
                                               "rotary",        "norm",         "norm_backward", "norm_weight",
                                               "linear_step",   "linear_scan",  "linear_scan_states",
                                               "linear_chunks", "linear_chunk_states", "linear_split", "linear_split_states",
-                                              "linear_combine"};
+                                              "linear_combine", "linear_selftest"};
 
 struct ProfRec {
   int kind;

@@ -725,6 +725,12 @@ bool row_map(CUtensorMap* m, const void* at, int size, int heads, int64_t tokens
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+__global__ void __launch_bounds__(32) k_wait_selftest(uint32_t polls) {
+  __shared__ uint64_t bar;
+  __shared__ volatile uint32_t gave_up;
+  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicOr(&g_gave_up, 1u);
+}
+
 }  // namespace
 
 bool linear_chunk_plan(ChunkLaunch& g) {
@@ -770,6 +776,11 @@ cudaError_t launch_linear_chunks(const void* args, cudaStream_t s) {
   if (g.l.phase == 2) exact = false;  // the states that leave come from phase 1
   if (pair) return exact ? go<true, 3, false>(g, s) : go<true, 2, false>(g, s);
   return exact ? go<false, 3, false>(g, s) : go<false, 2, false>(g, s);
+}
+
+cudaError_t linear_selftest(const void* args, cudaStream_t s) {
+  k_wait_selftest<<<1, 32, 0, s>>>(*(const uint32_t*)args);
+  return cudaGetLastError();
 }
 
 cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up) {

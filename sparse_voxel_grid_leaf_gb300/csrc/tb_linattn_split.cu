@@ -641,6 +641,12 @@ cudaError_t go(const LinLaunch& l, cudaStream_t s) {
   return launch_early(k_split<E, kTerms, kStates>, (unsigned)blocks, kThreads, bytes, s, l.phase == 2, l);
 }
 
+__global__ void __launch_bounds__(32) k_wait_selftest(uint32_t polls) {
+  __shared__ uint64_t bar;
+  __shared__ volatile uint32_t gave_up;
+  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicOr(&g_gave_up, 1u);
+}
+
 }  // namespace
 
 cudaError_t launch_linear_split(const void* args, cudaStream_t s) {
@@ -650,6 +656,11 @@ cudaError_t launch_linear_split(const void* args, cudaStream_t s) {
   for (int i = 0; i < l.n; ++i) exact = exact || (l.p[i].last && l.phase != 2);
   if (l.phase == 1) return exact ? go<uint16_t, 3, true>(l, s) : go<uint16_t, 2, true>(l, s);
   return exact ? go<uint16_t, 3, false>(l, s) : go<uint16_t, 2, false>(l, s);
+}
+
+cudaError_t linear_split_selftest(const void* args, cudaStream_t s) {
+  k_wait_selftest<<<1, 32, 0, s>>>(*(const uint32_t*)args);
+  return cudaGetLastError();
 }
 
 cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up) {

@@ -13,7 +13,7 @@ namespace tb {
 // Kernel kinds of tb_profile_read, continued by the sequence operators.
 enum SeqKernel {
   kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqScanStates,
-  kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqNumKernels
+  kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqSelftest, kSeqNumKernels
 };
 
 // Every launch of a sequence operator is counted, and timed when profiling is
@@ -127,6 +127,9 @@ cudaError_t launch_linear_split(const void* args, cudaStream_t s);
 // Whether a bounded wait of a chunk kernel gave up since the last call.  Blocks.
 cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up);
 cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up);
+// A wait of the given polls (uint32_t) that gives up.
+cudaError_t linear_selftest(const void* args, cudaStream_t s);
+cudaError_t linear_split_selftest(const void* args, cudaStream_t s);
 cudaError_t launch_linear_scan(const void* args, cudaStream_t s);
 cudaError_t launch_linear_combine(const void* args, cudaStream_t s);
 

@@ -451,6 +451,14 @@ tb_status tb_linear_attention_status(tb_stream stream) {
   return TB_OK;
 }
 
+tb_status tb_linear_attention_selftest_wait(int32_t kernel, int32_t spin_limit, tb_stream stream) {
+  if (kernel < 0 || kernel > 1 || spin_limit < 1 || spin_limit > 1 << 22)
+    return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_selftest_wait: kernel %d, %d polls", kernel, spin_limit);
+  const uint32_t polls = (uint32_t)spin_limit;
+  TB_SEQ_CUDA(seq_launch(kSeqSelftest, (cudaStream_t)stream, kernel ? linear_split_selftest : linear_selftest, &polls));
+  return TB_OK;
+}
+
 tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream stream) {
   if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_linear_attention_step: args is NULL");
   StepLaunch l;

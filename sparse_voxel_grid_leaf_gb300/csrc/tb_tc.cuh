@@ -46,9 +46,10 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // *gave_up set, after kWaitPolls polls (a tenth of a second at least, where
 // a phase takes microseconds) or once another wait of the block gave up.
 constexpr uint32_t kWaitPolls = 1u << 22;
-__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up) {
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up,
+                                               uint32_t polls = kWaitPolls) {
 #pragma unroll 1
-  for (uint32_t i = 1; i < kWaitPolls; ++i) {
+  for (uint32_t i = 1; i < polls; ++i) {
     if (mbar_try(bar, parity)) return true;
     if ((i & 255) == 0 && *gave_up) return false;
   }
@@ -60,6 +61,18 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 __device__ __forceinline__ void fence_mbar_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+// One warp's wait for a phase that nothing completes: true once it gave up.
+__device__ __forceinline__ bool mbar_selftest(uint64_t* bar, volatile uint32_t* gave_up, uint32_t polls) {
+  if (threadIdx.x == 0) {
+    *gave_up = 0;
+    mbar_init(smem_addr(bar), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  mbar_wait_long(smem_addr(bar), 0, gave_up, polls);
+  __syncwarp();
+  return *gave_up != 0;
 }
 // Orders this thread's shared-memory writes before the tensor cores' and
 // copy engine's accesses that follow a barrier.
