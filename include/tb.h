@@ -553,9 +553,11 @@ TB_API int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int3
 TB_API tb_status tb_linear_attention(const tb_linear_args* args, tb_stream stream);
 TB_API tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_stream stream);
 
-/* Whether a bounded wait inside a linear-attention kernel gave up since the
- * last such call (TB_ERR_DEVICE_TIMEOUT: outputs of calls since are not to be
- * used).  Blocks until `stream` is done. */
+/* Whether a bounded wait inside a linear-attention kernel, on any stream of the
+ * device, gave up since the last such call for this stream (or, at its first,
+ * since the library was loaded): TB_ERR_DEVICE_TIMEOUT, and outputs of calls
+ * since are not to be used.  Every stream gets its own report.  Blocks until
+ * `stream` is done; waits of other streams' running kernels are not seen yet. */
 TB_API tb_status tb_linear_attention_status(tb_stream stream);
 
 /* Self-test of that report without a GPU fault: one warp waits as the kernels

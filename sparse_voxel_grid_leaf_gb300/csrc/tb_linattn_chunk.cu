@@ -68,8 +68,9 @@ constexpr int stage_bytes(bool states) { return (states ? 4 : 6) * kTile; }
 constexpr int kWarpTma = 8, kWarpMma = 9, kWarpScores = 10, kWarpOut = 12, kWarpScores2 = 16;
 constexpr int threads_of(bool pair, bool states) { return (states || pair ? 18 : 16) * 32; }
 
-// Set when a wait gave up (a bug, or a GPU that stands still): read and
-// cleared by linear_gave_up.
+// Blocks in which a wait gave up (a bug, or a GPU that stands still) since the
+// library was loaded: read by linear_gave_up and never cleared, so that no
+// reader takes another one's report.
 __device__ unsigned int g_gave_up;
 
 enum Bars {
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(threads_of(kPair, kStates), 1) k_chunks(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
+  if (threadIdx.x == 0 && s.gave_up) atomicAdd(&g_gave_up, 1u);
   if (warp == kWarpMma) tmem_free(tmem, 512);
   if (idle || warp >= 8) return;
   if (l.phase == 2) wait_for_last_kernel();
@@ -728,7 +729,7 @@ bool row_map(CUtensorMap* m, const void* at, int size, int heads, int64_t tokens
 __global__ void __launch_bounds__(32) k_wait_selftest(uint32_t polls) {
   __shared__ uint64_t bar;
   __shared__ volatile uint32_t gave_up;
-  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicOr(&g_gave_up, 1u);
+  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicAdd(&g_gave_up, 1u);
 }
 
 }  // namespace
@@ -783,14 +784,11 @@ cudaError_t linear_selftest(const void* args, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up) {
+cudaError_t linear_gave_up(cudaStream_t s, unsigned int* count) {
   void* at = nullptr;
-  unsigned int got = 0;
   cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&got, at, sizeof got, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof got, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(count, at, sizeof *count, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *gave_up = got != 0;
   return e;
 }
 

@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_split(const __grid_constant__ L
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && s.gave_up) atomicOr(&g_gave_up, 1u);
+  if (threadIdx.x == 0 && s.gave_up) atomicAdd(&g_gave_up, 1u);
   if (warp == kWarpMma) tmem_free(tmem, 512);
   if (!steep || idle || warp >= 8) return;
   if (l.phase == 2) wait_for_last_kernel();
@@ -644,7 +644,7 @@ cudaError_t go(const LinLaunch& l, cudaStream_t s) {
 __global__ void __launch_bounds__(32) k_wait_selftest(uint32_t polls) {
   __shared__ uint64_t bar;
   __shared__ volatile uint32_t gave_up;
-  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicOr(&g_gave_up, 1u);
+  if (mbar_selftest(&bar, &gave_up, polls) && threadIdx.x == 0) atomicAdd(&g_gave_up, 1u);
 }
 
 }  // namespace
@@ -663,14 +663,11 @@ cudaError_t linear_split_selftest(const void* args, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up) {
+cudaError_t linear_split_gave_up(cudaStream_t s, unsigned int* count) {
   void* at = nullptr;
-  unsigned int got = 0;
   cudaError_t e = cudaGetSymbolAddress(&at, g_gave_up);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&got, at, sizeof got, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(at, 0, sizeof got, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(count, at, sizeof *count, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  *gave_up = got != 0;
   return e;
 }
 

@@ -124,9 +124,9 @@ bool linear_chunk_plan(ChunkLaunch& g);
 cudaError_t launch_linear_chunks(const void* args, cudaStream_t s);
 // The same chunks for any rows, as sums of bfloat16 terms (tb_linattn_split.cu).
 cudaError_t launch_linear_split(const void* args, cudaStream_t s);
-// Whether a bounded wait of a chunk kernel gave up since the last call.  Blocks.
-cudaError_t linear_split_gave_up(cudaStream_t s, bool* gave_up);
-cudaError_t linear_gave_up(cudaStream_t s, bool* gave_up);
+// Blocks of a chunk kernel in which a bounded wait gave up so far.  Waits for the stream.
+cudaError_t linear_split_gave_up(cudaStream_t s, unsigned int* count);
+cudaError_t linear_gave_up(cudaStream_t s, unsigned int* count);
 // A wait of the given polls (uint32_t) that gives up.
 cudaError_t linear_selftest(const void* args, cudaStream_t s);
 cudaError_t linear_split_selftest(const void* args, cudaStream_t s);

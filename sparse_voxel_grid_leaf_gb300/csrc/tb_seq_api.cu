@@ -2,6 +2,9 @@
 // choice of a kernel's shape, the launches.  No allocation and no wait.
 #include <atomic>
 #include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
 
 #include "tb_seq.h"
 
@@ -442,12 +445,23 @@ tb_status tb_linear_attention_backward(const tb_linear_backward_args* args, tb_s
 }
 
 tb_status tb_linear_attention_status(tb_stream stream) {
-  bool gave_up = false;
-  TB_SEQ_CUDA(linear_gave_up((cudaStream_t)stream, &gave_up));
-  bool split = false;
+  int dev = 0;
+  unsigned int chunks = 0, split = 0;
+  TB_SEQ_CUDA(cudaGetDevice(&dev));
+  TB_SEQ_CUDA(linear_gave_up((cudaStream_t)stream, &chunks));
   TB_SEQ_CUDA(linear_split_gave_up((cudaStream_t)stream, &split));
-  gave_up = gave_up || split;
-  if (gave_up) return seq_fail(TB_ERR_DEVICE_TIMEOUT, "tb_linear_attention: a device-side wait timed out");
+  bool news = false;
+  try {
+    static std::mutex lock;
+    static std::map<std::pair<int, tb_stream>, unsigned int> seen;  // of each stream's last call
+    const std::lock_guard<std::mutex> guard(lock);
+    unsigned int& last = seen[{dev, stream}];
+    news = (int)(chunks + split - last) > 0;
+    if (news) last = chunks + split;
+  } catch (...) {
+    return seq_fail(TB_ERR_OOM, "tb_linear_attention_status: out of host memory");
+  }
+  if (news) return seq_fail(TB_ERR_DEVICE_TIMEOUT, "tb_linear_attention: a device-side wait timed out");
   return TB_OK;
 }
 

@@ -270,7 +270,8 @@ def linear_attention_step(q, k, v, decay, state, slots=None, scale: Optional[flo
 
 def linear_attention_status(stream=None):
     """Waits for the stream; raises TBError(TB_ERR_DEVICE_TIMEOUT) where a
-    bounded wait inside a linear-attention kernel gave up since the last call."""
+    bounded wait inside a linear-attention kernel, on any stream, gave up since
+    the last call for this stream (or, at its first, since the library was loaded)."""
     from . import TBError, _stream, lib
     status = lib().tb_linear_attention_status(ctypes.c_void_p(_stream(stream)))
     if status:

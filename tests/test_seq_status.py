@@ -51,3 +51,20 @@ def test_refused_selftests():
     lib, stream = tb.lib(), torch.cuda.current_stream().cuda_stream
     for kernel, polls in ((-1, 8), (2, 8), (0, 0), (1, (1 << 22) + 1)):
         assert lib.tb_linear_attention_selftest_wait(kernel, polls, stream) == 1
+
+
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_every_stream_has_its_report(kernel):
+    """What gave up on one stream is not used up by a status call of another one."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (a, b):
+        reported(s)
+    assert not reported(a) and not reported(b)
+    give_up(kernel, b)
+    b.synchronize()
+    assert reported(a)  # its own outputs may be as good as they were: the report does not say which call it was
+    assert reported(b)
+    assert not reported(a) and not reported(b)
+    give_up(kernel, a)
+    a.synchronize()
+    assert reported(a) and not reported(a) and reported(b)
