@@ -182,6 +182,10 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
   }
 }
 
+// r^3 mean(w dy h), the factor of h in dx: r^3 alone is beyond 32 bits for rows
+// of small values under a small eps (r above 7e12), the mean being as small.
+__device__ __forceinline__ float norm_along(float r, float mean) { return r * mean * r * r; }
+
 // Rows of dx, and a block's part of dweight in registers over its rows: part
 // [blocks, width] in the workspace, summed by k_norm_weight in a fixed order.
 template <class T, int V, int NV>
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
     }
     const float2 all = row_reduce<false>(hh, hd, s_red, turn);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
-    const float m = r * r * r * all.y * inv_width;
+    const float m = norm_along(r, all.y * inv_width);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_backward_groups(NormB
     }
     const float2 all = group_reduce<false>(hh, hd, s_red, per_row);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
-    if (first == 0) s_row[g] = make_float2(r, -(r * r * r * all.y * inv_width));
+    if (first == 0) s_row[g] = make_float2(r, -norm_along(r, all.y * inv_width));
     __syncthreads();
     // by columns: a thread's part of dweight stays its own
     for (int i = threadIdx.x; i < width; i += blockDim.x) {

@@ -64,6 +64,20 @@ def test_fp8_norm_of_one_tiny_element(width):
     assert ((scale[:2].double() - 1e-37 * 1e3 / 448).abs() <= 1e-6 * 1e-34 / 448).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("rows,width", [(5, 128), (700, 128), (3, 77), (700, 777)], ids=str)
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_norm_gradient_of_small_rows(dtype, rows, width, eps):
+    """1 / the root mean square of a row may be far above the cube root of the largest number."""
+    g = gen(width)
+    h, dy = normal(g, rows, width, dtype=dtype, scale=1e-14), normal(g, rows, width, dtype=dtype)
+    w = normal(g, width, dtype=dtype)
+    dx, dw = tb.rms_norm_backward(dy, h, w, eps=eps)
+    want, wantw, size, sizew = R.norm_backward(dy, h, w, None, eps)
+    near(dx, want, size, dtype, terms=3 * width + 30, what="dx")
+    near(dw, wantw, sizew, dtype, terms=rows + width + 30, what="dweight")
+
+
 # ------------------------------------------------------------------------------------------- rows that no grid covers
 
 def poisoned(*shapes_and_types):
