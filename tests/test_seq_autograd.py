@@ -106,6 +106,21 @@ def test_a_turn_in_place_is_a_write():
     assert qk._version == before
 
 
+def test_writes_under_inference_mode():
+    """As torch's own writes in place: anything in it, none to its tensors outside."""
+    pos, f = torch.arange(24, dtype=torch.int32, device="cuda"), tb.rotary_frequencies(64)
+    decay, x, outside = torch.tensor([0.9, 0.99], device="cuda"), rows(), torch.zeros(24, 2, 64, 64, device="cuda")
+    with torch.inference_mode():
+        inside, q = torch.zeros(24, 2, 64, 64, device="cuda"), rows()
+        for state in (inside, outside):
+            tb.linear_attention_step(x, x, x, decay, state)
+        tb.rotary(q, None, pos, f, inplace=True)
+    assert torch.equal(inside, outside)
+    with pytest.raises(RuntimeError, match="inference tensor"):
+        tb.linear_attention_step(x, x, x, decay, inside)
+    assert torch.equal(inside, outside)
+
+
 @pytest.mark.parametrize("name", NAMES)
 def test_forward_mode_is_refused(name):
     call = calls()[name]
