@@ -81,7 +81,7 @@ const char* const kKernelNames[kKNumKinds] = {"prepass_leaves", "chain",        
                                               "write_refine_dilate", "validate", "write_multi",   "prune",
                                               "kernel_map",    "kmap_prep",    "export",        "member",
                                               "rotary",        "norm",         "norm_backward", "norm_weight",
-                                              "linear_step",   "linear_scan",  "linear_scan_states",
+                                              "linear_step",   "linear_scan",
                                               "linear_chunks", "linear_chunk_states", "linear_split", "linear_split_states",
                                               "linear_combine", "linear_selftest"};
 

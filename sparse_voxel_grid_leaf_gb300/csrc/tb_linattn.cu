@@ -105,11 +105,10 @@ __global__ void __launch_bounds__(256) k_scan(LinLaunch l) {
   const LinSegment seg = lin_segment(l, blockIdx.x);
   // the first grid's block has the rows before it, the last one's those past it: few, where grids are short (512 grids of 8
   // rows, 8 heads of 128 x 128: 97 us, 96 without)
-  if (l.phase == 0 && ((blockIdx.x == 0 && seg.begin > 0) || (blockIdx.x + 1 == gridDim.x && seg.end < l.tokens)))
+  if ((blockIdx.x == 0 && seg.begin > 0) || (blockIdx.x + 1 == gridDim.x && seg.end < l.tokens))
     lin_zero_rows<typename LinBits<sizeof(T)>::type>(
         p, {seg.begin, seg.end}, blockIdx.x == 0 ? 0 : seg.begin,
         blockIdx.x + 1 == gridDim.x ? seg.begin + l.tokens - seg.end : seg.begin, blockIdx.y, 1, threadIdx.x, blockDim.x);
-  if (seg.grid < 0) return;
   scan_walk<T, KS>(l, p, seg, blockIdx.y, s_rows, blockDim.x);
 }
 

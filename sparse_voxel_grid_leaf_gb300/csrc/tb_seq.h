@@ -12,7 +12,7 @@ namespace tb {
 
 // Kernel kinds of tb_profile_read, continued by the sequence operators.
 enum SeqKernel {
-  kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan, kSeqScanStates,
+  kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan,
   kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqSelftest, kSeqNumKernels
 };
 

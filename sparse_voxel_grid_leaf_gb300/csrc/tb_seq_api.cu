@@ -359,10 +359,9 @@ static tb_status linear_run(const char* what, const tb_linear_args& a, ChunkLaun
   // With more walks than multiprocessors the last to start should be short ones.
   l.sorted = !l.segment && a.grids > 1 && a.grids <= kLinMaxSorted && (int64_t)a.grids * a.heads * l.n > sms;
   if (l.segment) {
-    l.phase = 1;
+    l.phase = 1;  // of grids of 192 rows and more on average: never the recurrence
     if (chunks) TB_SEQ_CUDA(seq_launch(kSeqChunkStates, s, launch_linear_chunks, &g));
-    else if (longer) TB_SEQ_CUDA(seq_launch(kSeqSplitStates, s, launch_linear_split, &l));
-    else TB_SEQ_CUDA(seq_launch(kSeqScanStates, s, launch_linear_scan, &l));
+    else TB_SEQ_CUDA(seq_launch(kSeqSplitStates, s, launch_linear_split, &l));
     TB_SEQ_CUDA(seq_launch(kSeqCombine, s, launch_linear_combine, &l));
     l.phase = 2;
   }
