@@ -471,7 +471,9 @@ TB_API tb_status tb_rotary(const tb_rotary_args* args, tb_stream stream);
  * h_out (NULL: not written; only with a residual) gets h rounded to `type`;
  * y is computed from the unrounded h.  With fp8 != 0, `y` gets e4m3 bytes of
  * y / scale and scale[row] = max |y| / 448 (a row of zeros: scale 0, bytes
- * 0); else `y` has `type` and `scale` is NULL.  width <= 16384. */
+ * 0); else `y` has `type` and `scale` is NULL.  width <= 16384.  The sum of
+ * squares is in 32 bits: finite rows for which it overflows (elements beyond
+ * about 10^18) give zeros. */
 typedef struct tb_norm_args {
   const void *x, *residual, *weight;
   void *y, *h_out;
@@ -521,8 +523,9 @@ TB_API tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stre
  * the model: it has no gradient here.
  *
  * Rows are summed 64 at a time with powers of the decay between 2^-50 and 2^50
- * in 32 bits: finite values and states beyond 2^70 in magnitude may overflow
- * where a walk row by row would not.
+ * in 32 bits: finite values and states beyond 2^70 in magnitude may overflow,
+ * and 32-bit ones below 2^-60 lose their last bits, where a walk row by row
+ * would not.
  *
  * workspace: at least tb_linear_attention_workspace(...) bytes, 256-byte
  * aligned (NULL where that is 0). */

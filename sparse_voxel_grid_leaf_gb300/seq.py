@@ -8,8 +8,10 @@ marshal pointers, sizes and strides to ``libtb.so`` (C ABI in ``include/tb.h``)
 on torch's current stream; they never wait for the GPU.
 
 Training: ``rotary``, ``rms_norm`` and ``linear_attention`` take part in
-autograd; their ``*_backward`` calls are public too.  Generation:
-``linear_attention_step`` updates the states in place, one token per stream.
+autograd (first derivatives; second ones and forward mode are refused); their
+``*_backward`` calls are public too.  Generation: ``linear_attention_step``
+updates the states in place, one token per stream.  Writes in place raise
+torch's version counters.
 """
 from __future__ import annotations
 
