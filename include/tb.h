@@ -503,6 +503,20 @@ typedef struct tb_norm_backward_args {
 TB_API int64_t tb_rms_norm_backward_workspace(int64_t rows, int32_t width);
 TB_API tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stream);
 
+/* Layer norm of rows with the residual stream's addition:
+ *   h = x + residual (in 32 bits),  y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias
+ * over tb_norm_args with fp8 = 0 and scale = NULL; var is the mean of the
+ * squares of h - mean(h).  bias [width] (NULL: zero) has `type`. */
+TB_API tb_status tb_layer_norm(const tb_norm_args* args, const void* bias, tb_stream stream);
+
+/* Gradient of the layer norm, from h as tb_layer_norm wrote it (or x).  With u
+ * the normed row (h - mean(h)) r, r = 1 / sqrt(var(h) + eps), v = weight dy:
+ *   dx = r (v - mean(v) - u mean(v u)) + dh,  dweight = sum over rows of dy u,  dbias = sum of dy.
+ * dbias (NULL: not made) as dweight.  workspace: 16-byte aligned, at least
+ * tb_layer_norm_backward_workspace(rows, width) bytes. */
+TB_API int64_t tb_layer_norm_backward_workspace(int64_t rows, int32_t width);
+TB_API tb_status tb_layer_norm_backward(const tb_norm_backward_args* args, void* dbias, tb_stream stream);
+
 /* Linear attention with a decay for each head, over the rows of each grid:
  *   S_t = decay S_{t-1} + k_t v_t^T,  o_t = scale q_t S_t
  * with q, k rows [tokens, heads, key], v and o rows [tokens, heads, value]
@@ -587,6 +601,118 @@ typedef struct tb_linear_step_args {
   float scale;
 } tb_linear_step_args;
 TB_API tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_stream stream);
+
+/* Short causal convolution of every channel over the rows of each grid:
+ *   pre_t = bias + sum over j < taps of weight[c, j] x_(t - taps + 1 + j),  y_t = pre_t, or pre_t / (1 + exp(-pre_t)) with silu.
+ * x, y rows [tokens, channels]; weight [channels, taps], 2 to 4 taps, the last
+ * one for the row itself; bias [channels] or NULL.  The rows before a grid's
+ * first are its state [grids, taps - 1, channels], oldest first (NULL: zeros);
+ * state_out (or NULL) gets the last taps - 1 rows of state and grid together.
+ * All of one type.  offsets as in tb_linear_args: rows of no grid get zeros.
+ *
+ * The backward call gives, for the gradient dy of y and dstate_out (NULL: zero)
+ * of state_out, the gradients dx, dweight, dbias (NULL: not made) and dstate
+ * (NULL: not made) of `state`.  dweight and dbias are summed in 32 bits in a
+ * fixed order.  workspace: 16-byte aligned, at least
+ * tb_causal_conv_backward_workspace(...) bytes. */
+typedef struct tb_conv_args {
+  const void *x, *weight, *bias;
+  void* y;
+  const int64_t* offsets;     /* NULL: one grid of all tokens              */
+  const void* state;
+  void* state_out;
+  int64_t tokens, x_row, y_row;
+  int32_t grids, channels, taps, type, silu;
+} tb_conv_args;
+typedef struct tb_conv_backward_args {
+  tb_conv_args f;             /* f.y and f.state_out are not used          */
+  const void *dy, *dstate_out;
+  void *dx, *dweight, *dbias, *dstate;
+  float* workspace;
+  int64_t dy_row, dx_row, workspace_bytes;
+} tb_conv_backward_args;
+TB_API tb_status tb_causal_conv(const tb_conv_args* args, tb_stream stream);
+TB_API int64_t tb_causal_conv_backward_workspace(int64_t tokens, int32_t channels, int32_t taps);
+TB_API tb_status tb_causal_conv_backward(const tb_conv_backward_args* args, tb_stream stream);
+
+/* One row of each of `streams` sequences: y as above with the rows before from
+ * slot slots[n] (NULL: n) of state [num_slots, taps - 1, channels], which then
+ * drops its oldest row and takes x in.  A stream whose slot is outside
+ * [0, num_slots) touches no state and its output is zero.  No two streams may
+ * share a slot. */
+typedef struct tb_conv_step_args {
+  const void *x, *weight, *bias;
+  void *y, *state;
+  const int32_t* slots;
+  int64_t streams, num_slots, x_row, y_row;
+  int32_t channels, taps, type, silu;
+} tb_conv_step_args;
+TB_API tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream stream);
+
+/* Selective scan of every channel over the rows of each grid:
+ *   delta_t = dt_t + dt_bias, or log(1 + exp(dt_t + dt_bias)) with softplus,
+ *   h_t = exp(delta_t a) h_(t-1) + delta_t x_t b_t,
+ *   y_t = (c_t . h_t + d x_t), times z_t / (1 + exp(-z_t)) where z is given
+ * with h of `states` numbers a channel.  x, dt, z, y rows [tokens, channels]
+ * and b, c rows [tokens, groups, states] of `type`; channels / groups
+ * consecutive channels share a group's b and c.  a [channels, states], d and
+ * dt_bias [channels] (NULL: zero) in 32 bits, contiguous.  state, state_out
+ * [grids, channels, states] in 32 bits: the states that grids start from
+ * (NULL: zero) and those after each grid's last row, which for a grid without
+ * rows is its first.  states <= 256.  offsets as in tb_linear_args: rows of no
+ * grid get zeros.  In a channel that meets an infinity, outputs from there on
+ * may be NaN where the formula has an infinity.
+ *
+ * The backward call gives, for the gradient dy of y and dstate_out (NULL: zero)
+ * of state_out, the gradients of every input: dx, ddt, dz (with z), db, dc of
+ * `type`, da, dd, ddt_bias (NULL: not made) and dstate (NULL: not made) in 32
+ * bits.  db, dc are dense [tokens, groups, states].  All sums are in 32 bits in
+ * a fixed order.
+ *
+ * workspace: at least tb_selective_scan_workspace(...) bytes, 256-byte aligned
+ * (NULL where that is 0). */
+typedef struct tb_scan_args {
+  const void *x, *dt, *b, *c, *z;
+  void* y;
+  const float *a, *d, *dt_bias;
+  const int64_t* offsets;     /* NULL: one grid of all tokens              */
+  const float* state;
+  float* state_out;
+  void* workspace;
+  int64_t tokens;
+  int64_t x_row, dt_row, z_row, y_row, b_row, b_group, c_row, c_group;
+  int64_t workspace_bytes;
+  int32_t grids, channels, states, groups, type, softplus;
+} tb_scan_args;
+typedef struct tb_scan_backward_args {
+  tb_scan_args f;             /* f.y and f.state_out are not used          */
+  const void* dy;
+  const float* dstate_out;
+  void *dx, *ddt, *dz, *db, *dc;
+  float *da, *dd, *ddt_bias, *dstate;
+  int64_t dy_row, dx_row, ddt_row, dz_row;
+} tb_scan_backward_args;
+TB_API int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t channels, int32_t states, int32_t groups,
+                                           int32_t backward);
+TB_API tb_status tb_selective_scan(const tb_scan_args* args, tb_stream stream);
+TB_API tb_status tb_selective_scan_backward(const tb_scan_backward_args* args, tb_stream stream);
+
+/* One token of each of `streams` sequences: the state of stream n (slot
+ * slots[n] of `state`; NULL: slot n) takes the row in and gives y_n, in place.
+ * A stream whose slot is outside [0, num_slots) touches no state and its output
+ * is zero.  No two streams may share a slot.  state [num_slots, channels,
+ * states], 16-byte aligned where states is a multiple of 4; states <= 256. */
+typedef struct tb_scan_step_args {
+  const void *x, *dt, *b, *c, *z;
+  void* y;
+  const float *a, *d, *dt_bias;
+  float* state;
+  const int32_t* slots;
+  int64_t streams, num_slots;
+  int64_t x_row, dt_row, z_row, y_row, b_row, b_group, c_row, c_group;
+  int32_t channels, states, groups, type, softplus;
+} tb_scan_step_args;
+TB_API tb_status tb_selective_scan_step(const tb_scan_step_args* args, tb_stream stream);
 
 /* Number of kernels this thread has launched through the library so far. */
 TB_API int64_t tb_kernel_launch_count(void);

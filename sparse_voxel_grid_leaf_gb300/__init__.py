@@ -17,7 +17,8 @@ Follow-ups paragraph:
 * ``chain(b, ops)``  several passes with intermediate results on the device
 
 ``seq`` has the operators of sequence models over voxel rows: ``rotary``,
-``rms_norm``, ``linear_attention`` and its single-token step.
+``rms_norm``, ``layer_norm``, ``linear_attention``, ``causal_conv``,
+``selective_scan`` and their single-token steps.
 """
 from __future__ import annotations
 
@@ -617,6 +618,7 @@ def export_many(batches: Sequence[Batch], origins=None, masks=None, voxel_offset
                                       plist(leaf_offsets), ctypes.c_void_p(_stream(stream))))
 
 
-from .seq import (linear_attention, linear_attention_backward, linear_attention_status,  # noqa: E402,F401
+from .seq import (causal_conv, causal_conv_backward, causal_conv_step, layer_norm,  # noqa: E402,F401
+                  layer_norm_backward, linear_attention, linear_attention_backward, linear_attention_status,
                   linear_attention_step, rms_norm, rms_norm_backward, rms_norm_fp8, rotary, rotary_backward,
-                  rotary_frequencies)
+                  rotary_frequencies, selective_scan, selective_scan_backward, selective_scan_step)

@@ -83,7 +83,10 @@ const char* const kKernelNames[kKNumKinds] = {"prepass_leaves", "chain",        
                                               "rotary",        "norm",         "norm_backward", "norm_weight",
                                               "linear_step",   "linear_scan",
                                               "linear_chunks", "linear_chunk_states", "linear_split", "linear_split_states",
-                                              "linear_combine", "linear_selftest"};
+                                              "linear_combine", "linear_selftest",
+                                              "causal_conv",   "causal_conv_backward", "causal_conv_weight", "causal_conv_step",
+                                              "selective_scan", "selective_states", "selective_join", "selective_backward",
+                                              "selective_sums", "selective_step"};
 
 struct ProfRec {
   int kind;

@@ -1,5 +1,6 @@
-// Which rows a block of the linear-attention kernels walks: whole grids, or
-// the segments of a call that splits its grids along the rows.
+// Which rows a block of the linear-attention and selective-scan kernels walks:
+// whole grids, or the segments of a call that splits its grids along the rows.
+// L: a launch with offsets, tokens, grids and segment.
 #pragma once
 
 #include "tb_seq.h"
@@ -15,7 +16,8 @@ struct LinSegment {
   int len;
 };
 
-__device__ __forceinline__ void lin_grid_rows(const LinLaunch& l, int b, int64_t& begin, int64_t& end) {
+template <class L>
+__device__ __forceinline__ void lin_grid_rows(const L& l, int b, int64_t& begin, int64_t& end) {
   if (!l.offsets) {
     begin = 0;
     end = l.tokens;
@@ -30,7 +32,8 @@ __device__ __forceinline__ void lin_grid_rows(const LinLaunch& l, int b, int64_t
 struct LinCover {
   int64_t begin, end;
 };
-__device__ __forceinline__ LinCover lin_cover(const LinLaunch& l) {
+template <class L>
+__device__ __forceinline__ LinCover lin_cover(const L& l) {
   if (!l.offsets) return {0, l.tokens};
   const int64_t begin = min(max(l.offsets[0], (int64_t)0), l.tokens);
   return {begin, min(max(l.offsets[l.grids], begin), l.tokens)};
@@ -74,12 +77,14 @@ __device__ __forceinline__ void lin_zero_share(const LinLaunch& l, const LinProb
 template <int size> struct LinBits { typedef uint16_t type; };
 template <> struct LinBits<4> { typedef uint32_t type; };
 
-__device__ __forceinline__ int lin_segments_of(const LinLaunch& l, int64_t rows) {
+template <class L>
+__device__ __forceinline__ int lin_segments_of(const L& l, int64_t rows) {
   return rows > 0 ? (int)((rows + l.segment - 1) / l.segment) : 1;
 }
 
 // The segment slot of grid b's first segment.  One warp; the same in all lanes.
-__device__ __forceinline__ int lin_first_slot(const LinLaunch& l, int b) {
+template <class L>
+__device__ __forceinline__ int lin_first_slot(const L& l, int b) {
   int sum = 0;
   for (int i = threadIdx.x & 31; i < b; i += 32) {
     int64_t begin, end;
@@ -92,7 +97,8 @@ __device__ __forceinline__ int lin_first_slot(const LinLaunch& l, int b) {
 }
 
 // The segment of a slot, found by one warp; the same in all lanes.
-__device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) {
+template <class L>
+__device__ __forceinline__ LinSegment lin_segment(const L& l, int slot) {
   LinSegment s;
   s.grid = -1;
   s.slot = slot;

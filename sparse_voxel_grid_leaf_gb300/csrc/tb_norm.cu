@@ -1,6 +1,7 @@
 // Root-mean-square norm with the residual stream's addition, an output in
 // e4m3 with a scale for each row, and the gradient (tb_rms_norm,
-// tb_rms_norm_backward).
+// tb_rms_norm_backward); the layer norm (tb_layer_norm,
+// tb_layer_norm_backward).
 //
 // All bytes are read once and written once, so the bound is memory: a row's
 // elements stay in the registers of its threads between the sum of squares
@@ -11,6 +12,11 @@
 // addition 155 us, 6.58 TB/s; the gradient of 60013 rows of 1536 133 us, 5.5
 // TB/s (its instructions take 73% of the issue slots, as the forward's do);
 // 16 rows of 2048 to e4m3 5.5 us, most of it the launch.
+//
+// The layer norm is the same walk with one more sum of a row: its mean first,
+// then the squares of what differs from it (the squares' sum less the mean's
+// square would lose the digits of rows whose mean is large), both over the row
+// in registers.
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 
@@ -18,6 +24,7 @@ namespace tb {
 namespace {
 
 constexpr int kMaxThreads = 512;
+enum NormKind { kRms, kRmsFp8, kLayer };
 __host__ __device__ constexpr int up_to(int x, int m) { return (x + m - 1) / m * m; }
 
 // Sums (the second one: sum or maximum) of two values over the threads of a
@@ -76,8 +83,9 @@ __device__ __forceinline__ Fp8Row fp8_row(float top, float r) {
 // Blocks stay and walk over rows; a row's elements are loaded while the one
 // before it is normed, and held as they came (16-bit pairs): the sum of the
 // residual stream is computed once for the mean and once for the output.
-template <class T, int V, int NV, bool kFp8>
+template <class T, int V, int NV, NormKind kKind>
 __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
+  constexpr bool kFp8 = kKind == kRmsFp8, kMean = kKind == kLayer;
   const tb_norm_args& a = n.a;
   __shared__ float2 s_red[64];
   int turn = 0;
@@ -101,9 +109,15 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
   int64_t base = (int64_t)blockIdx.x * blockDim.y;
   if (kAhead) load(base + threadIdx.y);
   auto weight = [&](int i) { return load_pack<T, V>((const T*)a.weight + (int64_t)(threadIdx.x + i * blockDim.x) * V); };
+  auto bias = [&](int i) { return load_pack<T, V>((const T*)n.bias + (int64_t)(threadIdx.x + i * blockDim.x) * V); };
+  Pack<T, V> wb[kMean ? NV : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (kAhead && threadIdx.x + i * blockDim.x < vecs) w[i] = weight(i);
+    if (kAhead && threadIdx.x + i * blockDim.x < vecs) {
+      w[i] = weight(i);
+      if constexpr (kMean)
+        if (n.bias) wb[i] = bias(i);
+    }
   // block-uniform trip count: the barriers of row_reduce are passed by all
   for (; base < a.rows; base += stride) {
     const int64_t row = base + threadIdx.y;
@@ -134,7 +148,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
         sum_of(i, f);
         if (a.h_out) store_pack<T, V>((T*)a.h_out + row * a.h_row + (int64_t)v * V, pack<T, V>(f));
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum = fmaf(f[j], f[j], sum);
+        for (int j = 0; j < V; ++j) sum = kMean ? sum + f[j] : fmaf(f[j], f[j], sum);
         if constexpr (kFp8) {
           float g[V];
           unpack<T, V>(kAhead ? w[i] : weight(i), g);
@@ -143,7 +157,23 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
         }
       }
     }
-    const float2 all = row_reduce<true>(sum, top, s_red, turn);
+    float2 all = row_reduce<true>(sum, top, s_red, turn);
+    float mean = 0.f;
+    if constexpr (kMean) {
+      mean = all.x * inv_width;
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (live && v < vecs) {
+          float f[V];
+          sum_of(i, f);
+#pragma unroll
+          for (int j = 0; j < V; ++j) sum = fmaf(f[j] - mean, f[j] - mean, sum);
+        }
+      }
+      all = row_reduce<true>(sum, 0.f, s_red, turn);
+    }
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
     Fp8Row q8{};
     if constexpr (kFp8) {
@@ -157,8 +187,15 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
         float f[V], g[V];
         sum_of(i, f);
         unpack<T, V>(kAhead ? w[i] : weight(i), g);
+        if constexpr (kMean) {
+          float o[V] = {};
+          if (n.bias) unpack<T, V>(kAhead ? wb[i] : bias(i), o);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f[j] = kFp8 ? q8(f[j], g[j]) : f[j] * (r * g[j]);
+          for (int j = 0; j < V; ++j) f[j] = fmaf(f[j] - mean, r * g[j], o[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[j] = kFp8 ? q8(f[j], g[j]) : f[j] * (r * g[j]);
+        }
         if constexpr (!kFp8) {
           store_pack<T, V>((T*)a.y + row * a.y_row + (int64_t)v * V, pack<T, V>(f));
         } else {
@@ -188,7 +225,7 @@ __device__ __forceinline__ float norm_along(float r, float mean) { return r * me
 
 // Rows of dx, and a block's part of dweight in registers over its rows: part
 // [blocks, width] in the workspace, summed by k_norm_weight in a fixed order.
-template <class T, int V, int NV>
+template <class T, int V, int NV, bool kMean>
 __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunch n) {
   let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
@@ -199,7 +236,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
   const float inv_width = 1.f / (float)a.width;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
   constexpr bool kAhead = ahead<T, V, NV, true>();
-  float dw[NV][V] = {};
+  float dw[NV][V] = {}, db[kMean ? NV : 1][V] = {};
   Pack<T, V> w[NV], ph[NV], pd[NV], pg[NV];
   auto load = [&](int64_t row) {
 #pragma unroll
@@ -230,7 +267,28 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
       cg[i] = pg[i];
     }
     if (kAhead) load(row + stride);
-    float hh = 0.f, hd = 0.f;
+    float hh = 0.f, hd = 0.f, mean = 0.f, less = 0.f;
+    if constexpr (kMean) {  // of the row, and of weight dy
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (live && v < vecs) {
+          float h[V], d[V], g[V];
+          unpack<T, V>(ch[i], h);
+          unpack<T, V>(cd[i], d);
+          unpack<T, V>(kAhead ? w[i] : weight(i), g);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            hh += h[j];
+            hd = fmaf(g[j], d[j], hd);
+          }
+        }
+      }
+      const float2 sums = row_reduce<false>(hh, hd, s_red, turn);
+      mean = sums.x * inv_width;
+      less = sums.y * inv_width;
+      hh = hd = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -241,6 +299,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
         unpack<T, V>(kAhead ? w[i] : weight(i), g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+          if (kMean) h[j] -= mean;
           hh = fmaf(h[j], h[j], hh);
           hd = fmaf(h[j] * g[j], d[j], hd);
         }
@@ -249,6 +308,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
     const float2 all = row_reduce<false>(hh, hd, s_red, turn);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
     const float m = norm_along(r, all.y * inv_width);
+    less *= r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = threadIdx.x + i * blockDim.x;
@@ -260,39 +320,48 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
         if (a.dh) unpack<T, V>(cg[i], g);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+          if constexpr (kMean) {
+            h[j] -= mean;
+            db[i][j] += d[j];
+          }
           dw[i][j] = fmaf(d[j], h[j] * r, dw[i][j]);
-          const float x = fmaf(-m, h[j], r * f[j] * d[j]);
+          const float x = fmaf(-m, h[j], kMean ? fmaf(r * f[j], d[j], -less) : r * f[j] * d[j]);
           h[j] = a.dh ? x + g[j] : x;
         }
         store_pack<T, V>((T*)a.dx + row * a.dx_row + (int64_t)v * V, pack<T, V>(h));
       }
     }
   }
-  float* part = a.workspace + (int64_t)blockIdx.x * a.width;
-  if (blockDim.y > 1) {
-    const int span = blockDim.x * NV * V;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < V; ++j) s_part[threadIdx.y * span + (i * V + j) * blockDim.x + threadIdx.x] = dw[i][j];
-    __syncthreads();
-    if (threadIdx.y == 0) {
+  auto put = [&](float (&sum)[NV][V], int which) {
+    float* part = a.workspace + ((int64_t)which * gridDim.x + blockIdx.x) * a.width;
+    if (blockDim.y > 1) {
+      const int span = blockDim.x * NV * V;
+      if (which) __syncthreads();  // the other sum's parts have been read
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-          for (int y = 1; y < blockDim.y; ++y) dw[i][j] += s_part[y * span + (i * V + j) * blockDim.x + threadIdx.x];
-    }
-  }
-  if (threadIdx.y == 0) {
+        for (int j = 0; j < V; ++j) s_part[threadIdx.y * span + (i * V + j) * blockDim.x + threadIdx.x] = sum[i][j];
+      __syncthreads();
+      if (threadIdx.y == 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = threadIdx.x + i * blockDim.x;
-      if (v < vecs)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) part[v * V + j] = dw[i][j];
+          for (int j = 0; j < V; ++j)
+            for (int y = 1; y < blockDim.y; ++y) sum[i][j] += s_part[y * span + (i * V + j) * blockDim.x + threadIdx.x];
+      }
     }
-  }
+    if (threadIdx.y == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v < vecs)
+#pragma unroll
+          for (int j = 0; j < V; ++j) part[v * V + j] = sum[i][j];
+      }
+    }
+  };
+  put(dw, 0);
+  if constexpr (kMean) put(db, 1);
 }
 
 // ------------------------------------------- rows that no vector boundary meets
@@ -361,11 +430,12 @@ __device__ __forceinline__ float2 group_reduce(float x, float y, float2* s, int 
 }
 
 // Shared memory: the weight, then `nv` buffers of a group of x, residual.
-template <class T, bool kFp8>
+template <class T, NormKind kKind>
 __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) {
+  constexpr bool kFp8 = kKind == kRmsFp8, kMean = kKind == kLayer;
   const tb_norm_args& a = n.a;
   extern __shared__ __align__(16) char s_group[];
-  __shared__ float2 s_red[kGroupWarps];
+  __shared__ float2 s_red[2 * kGroupWarps];
   const int width = a.width, per_row = (int)(blockDim.x >> 5) / n.rows, g = (threadIdx.x >> 5) / per_row;
   const int first = threadIdx.x - g * per_row * 32, step = per_row * 32;
   const int tensors = a.residual ? 2 : 1;
@@ -403,10 +473,20 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) 
     for (int i = first; i < mine; i += step) {
       float f = RowType<T>::to(x[at + i]);
       if (a.residual) f += RowType<T>::to(res[at + i]);
-      sum = fmaf(f, f, sum);
+      sum = kMean ? sum + f : fmaf(f, f, sum);
       if (kFp8) top = fmaxf(top, fabsf(f * RowType<T>::to(w[i])));
     }
-    const float2 all = group_reduce<true>(sum, top, s_red, per_row);
+    float2 all = group_reduce<true>(sum, top, s_red, per_row);
+    const float mean = kMean ? all.x * inv_width : 0.f;
+    if constexpr (kMean) {
+      sum = 0.f;
+      for (int i = first; i < mine; i += step) {
+        float f = RowType<T>::to(x[at + i]);
+        if (a.residual) f += RowType<T>::to(res[at + i]);
+        sum = fmaf(f - mean, f - mean, sum);
+      }
+      all = group_reduce<true>(sum, 0.f, s_red + kGroupWarps, per_row);
+    }
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
     const Fp8Row q8 = kFp8 ? fp8_row(all.y, r) : Fp8Row{};
     if (kFp8 && first == 0 && mine) a.scale[row] = q8.scale;
@@ -419,6 +499,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) 
       }
       const float g = RowType<T>::to(w[i]);
       if (kFp8) q[i] = __nv_cvt_float_to_fp8(q8(f, g), __NV_SATFINITE, __NV_E4M3);
+      else if (kMean) x[at + i] = RowType<T>::from(fmaf(f - mean, r * g, n.bias ? RowType<T>::to(((const T*)n.bias)[i]) : 0.f));
       else x[at + i] = RowType<T>::from(f * (r * g));
     }
     __syncthreads();
@@ -430,26 +511,29 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_groups(NormLaunch n) 
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Shared memory: the weight and dweight's part in 32 bits, then `nv` buffers
-// of a group of h, dy, dh; dx takes dy's place.
-template <class T>
+// Shared memory: the weight and the parts of dweight and dbias in 32 bits, then
+// `nv` buffers of a group of h, dy, dh; dx takes dy's place.
+template <class T, bool kMean>
 __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_backward_groups(NormBackwardLaunch n) {
   let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
   extern __shared__ __align__(16) char s_group[];
-  __shared__ float2 s_red[kGroupWarps], s_row[8];  // r and the factor of h
+  __shared__ float2 s_red[2 * kGroupWarps], s_row[8];  // r and the factor of h
+  __shared__ float2 s_mean[8];                          // of h, and of weight dy times r
   const int width = a.width, per_row = (int)(blockDim.x >> 5) / n.rows, g = (threadIdx.x >> 5) / per_row;
   const int first = threadIdx.x - g * per_row * 32, step = per_row * 32;
   const int tensors = a.dh ? 3 : 2;
   const int span = (int)(norm_buffer_bytes(width, sizeof(T), n.rows) / sizeof(T));
   float* w = reinterpret_cast<float*>(s_group);
   float* dw = w + up_to(width, 4);
-  T* buf = reinterpret_cast<T*>(dw + up_to(width, 4));
+  float* db = dw + up_to(width, 4);
+  T* buf = reinterpret_cast<T*>(kMean ? db + up_to(width, 4) : db);
   const float inv_width = 1.f / (float)width;
   const int64_t stride = (int64_t)gridDim.x * n.rows;
   for (int i = threadIdx.x; i < width; i += blockDim.x) {
     w[i] = RowType<T>::to(((const T*)a.weight)[i]);
     dw[i] = 0.f;
+    if (kMean) db[i] = 0.f;
   }
   auto fetch = [&](int64_t base, int st) {
     if (base < a.rows) {
@@ -478,29 +562,45 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_backward_groups(NormB
     const int rows = (int)min((int64_t)n.rows, a.rows - base);
     const int mine = g < rows ? width : 0;
     float hh = 0.f, hd = 0.f;
+    float2 means = make_float2(0.f, 0.f);
+    if constexpr (kMean) {
+      for (int i = first; i < mine; i += step) {
+        hh += RowType<T>::to(h[g * width + i]);
+        hd = fmaf(w[i], RowType<T>::to(d[g * width + i]), hd);
+      }
+      means = group_reduce<false>(hh, hd, s_red + kGroupWarps, per_row);
+      means.x *= inv_width;
+      means.y *= inv_width;
+      hh = hd = 0.f;
+    }
     for (int i = first; i < mine; i += step) {
-      const float f = RowType<T>::to(h[g * width + i]);
+      const float f = RowType<T>::to(h[g * width + i]) - means.x;
       hh = fmaf(f, f, hh);
       hd = fmaf(f * w[i], RowType<T>::to(d[g * width + i]), hd);
     }
     const float2 all = group_reduce<false>(hh, hd, s_red, per_row);
     const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
-    if (first == 0) s_row[g] = make_float2(r, -norm_along(r, all.y * inv_width));
+    if (first == 0) {
+      s_row[g] = make_float2(r, -norm_along(r, all.y * inv_width));
+      if (kMean) s_mean[g] = make_float2(means.x, means.y * r);
+    }
     __syncthreads();
     // by columns: a thread's part of dweight stays its own
     for (int i = threadIdx.x; i < width; i += blockDim.x) {
       const float wi = w[i];
-      float sum = dw[i];
+      float sum = dw[i], bias = kMean ? db[i] : 0.f;
 #pragma unroll 4
       for (int k = 0; k < rows; ++k) {
-        const float2 rm = s_row[k];
-        const float f = RowType<T>::to(h[k * width + i]), e = RowType<T>::to(d[k * width + i]);
+        const float2 rm = s_row[k], mk = kMean ? s_mean[k] : make_float2(0.f, 0.f);
+        const float f = RowType<T>::to(h[k * width + i]) - mk.x, e = RowType<T>::to(d[k * width + i]);
         sum = fmaf(e, f * rm.x, sum);
-        float x = fmaf(rm.y, f, rm.x * wi * e);
+        bias += e;
+        float x = fmaf(rm.y, f, kMean ? fmaf(rm.x * wi, e, -mk.y) : rm.x * wi * e);
         if (a.dh) x += RowType<T>::to(dh[k * width + i]);
         d[k * width + i] = RowType<T>::from(x);
       }
       dw[i] = sum;
+      if (kMean) db[i] = bias;
     }
     __syncthreads();
     put_group(a.dx, d - phase, base, n.rows, a.rows, width);
@@ -508,11 +608,14 @@ __global__ void __launch_bounds__(32 * kGroupWarps) k_norm_backward_groups(NormB
     __syncthreads();  // the group's buffer may be filled again
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  for (int i = threadIdx.x; i < width; i += blockDim.x) a.workspace[(int64_t)blockIdx.x * width + i] = dw[i];
+  for (int i = threadIdx.x; i < width; i += blockDim.x) {
+    a.workspace[(int64_t)blockIdx.x * width + i] = dw[i];
+    if (kMean) a.workspace[((int64_t)gridDim.x + blockIdx.x) * width + i] = db[i];
+  }
 }
 
-// dweight = the blocks' parts summed, in a fixed order: 8 columns a block, 64
-// rows of parts at a time, four in flight a thread.
+// dweight, and in a second row of blocks dbias, = the blocks' parts summed, in
+// a fixed order: 8 columns a block, 64 rows of parts at a time, four in flight a thread.
 template <class T>
 __global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
   constexpr int kCols = 8, kRows = 64;
@@ -521,7 +624,7 @@ __global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
   wait_for_last_kernel();
   float sum = 0.f;
   if (c < n.a.width) {
-    const float* part = n.a.workspace + c;
+    const float* part = n.a.workspace + (int64_t)blockIdx.y * n.blocks * n.a.width + c;
     int b = y;
     for (; b + 3 * kRows < n.blocks; b += 4 * kRows) {
       float f[4];
@@ -537,41 +640,42 @@ __global__ void __launch_bounds__(512) k_norm_weight(NormBackwardLaunch n) {
   if (warp < kCols) {
     const float all = warp_sum(s[lane][warp] + s[lane + 32][warp]);
     const int o = blockIdx.x * kCols + warp;
-    if (lane == 0 && o < n.a.width) ((T*)n.a.dweight)[o] = RowType<T>::from(all);
+    if (lane == 0 && o < n.a.width) ((T*)(blockIdx.y ? n.dbias : n.a.dweight))[o] = RowType<T>::from(all);
   }
 }
 
-template <class T, bool kFp8>
+template <class T, NormKind kKind>
 cudaError_t go_groups(const NormLaunch& n, cudaStream_t s) {
   const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.residual ? 2 : 1, n.rows, n.nv, sizeof(T));
   static std::atomic<bool> ready[kMaxDevices];
-  const cudaError_t e = allow_shared(k_norm_groups<T, kFp8>, kNormGroupBytes, ready);
+  const cudaError_t e = allow_shared(k_norm_groups<T, kKind>, kNormGroupBytes, ready);
   if (e != cudaSuccess) return e;
-  k_norm_groups<T, kFp8><<<n.blocks, n.per_row, bytes, s>>>(n);
+  k_norm_groups<T, kKind><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();
 }
-template <class T>
+template <class T, bool kMean>
 cudaError_t go_back_groups(const NormBackwardLaunch& n, cudaStream_t s) {
-  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.rows, n.nv, 8);
+  const size_t bytes = norm_group_bytes(n.a.width, sizeof(T), n.a.dh ? 3 : 2, n.rows, n.nv, kMean ? 12 : 8);
   static std::atomic<bool> ready[kMaxDevices];
-  const cudaError_t e = allow_shared(k_norm_backward_groups<T>, kNormGroupBytes, ready);
+  const cudaError_t e = allow_shared(k_norm_backward_groups<T, kMean>, kNormGroupBytes, ready);
   if (e != cudaSuccess) return e;
-  k_norm_backward_groups<T><<<n.blocks, n.per_row, bytes, s>>>(n);
+  k_norm_backward_groups<T, kMean><<<n.blocks, n.per_row, bytes, s>>>(n);
   return cudaGetLastError();
 }
 
 template <class T, int V, int NV>
 cudaError_t go(const NormLaunch& n, cudaStream_t s) {
   const dim3 block(n.per_row, n.rows);
-  if (n.a.fp8) k_norm<T, V, NV, true><<<n.blocks, block, 0, s>>>(n);
-  else k_norm<T, V, NV, false><<<n.blocks, block, 0, s>>>(n);
+  if (n.layer) k_norm<T, V, NV, kLayer><<<n.blocks, block, 0, s>>>(n);
+  else if (n.a.fp8) k_norm<T, V, NV, kRmsFp8><<<n.blocks, block, 0, s>>>(n);
+  else k_norm<T, V, NV, kRms><<<n.blocks, block, 0, s>>>(n);
   return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t pick(const NormLaunch& n, cudaStream_t s) {
   constexpr int V = RowType<T>::kVec;
-  if (n.groups) return n.a.fp8 ? go_groups<T, true>(n, s) : go_groups<T, false>(n, s);
+  if (n.groups) return n.layer ? go_groups<T, kLayer>(n, s) : n.a.fp8 ? go_groups<T, kRmsFp8>(n, s) : go_groups<T, kRms>(n, s);
   if (n.vec) {
     switch (n.nv) {
       case 1: return go<T, V, 1>(n, s);
@@ -591,14 +695,15 @@ template <class T, int V, int NV>
 cudaError_t go_back(const NormBackwardLaunch& n, cudaStream_t s) {
   const dim3 block(n.per_row, n.rows);
   const size_t smem = n.rows > 1 ? sizeof(float) * n.rows * n.per_row * NV * V : 0;
-  k_norm_backward<T, V, NV><<<n.blocks, block, smem, s>>>(n);
+  if (n.layer) k_norm_backward<T, V, NV, true><<<n.blocks, block, smem, s>>>(n);
+  else k_norm_backward<T, V, NV, false><<<n.blocks, block, smem, s>>>(n);
   return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t pick_back(const NormBackwardLaunch& n, cudaStream_t s) {
   constexpr int V = RowType<T>::kVec;
-  if (n.groups) return go_back_groups<T>(n, s);
+  if (n.groups) return n.layer ? go_back_groups<T, true>(n, s) : go_back_groups<T, false>(n, s);
   if (n.vec) {
     switch (n.nv) {
       case 1: return go_back<T, V, 1>(n, s);
@@ -632,7 +737,8 @@ cudaError_t launch_norm_backward(const void* args, cudaStream_t s) {
 
 cudaError_t launch_norm_weight(const void* args, cudaStream_t s) {
   const NormBackwardLaunch& n = *(const NormBackwardLaunch*)args;
-  auto go = [&](auto kernel) { return launch_early(kernel, (n.a.width + 7) / 8, 512, 0, s, n.a.rows > 0, n); };
+  const dim3 grid((n.a.width + 7) / 8, n.dbias ? 2 : 1);
+  auto go = [&](auto kernel) { return launch_early(kernel, grid, 512, 0, s, n.a.rows > 0, n); };
   switch (n.a.type) {
     case TB_TYPE_F32: return go(k_norm_weight<float>);
     case TB_TYPE_F16: return go(k_norm_weight<__half>);

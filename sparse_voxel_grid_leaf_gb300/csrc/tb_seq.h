@@ -13,7 +13,10 @@ namespace tb {
 // Kernel kinds of tb_profile_read, continued by the sequence operators.
 enum SeqKernel {
   kSeqRotary, kSeqNorm, kSeqNormBackward, kSeqNormWeight, kSeqStep, kSeqScan,
-  kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqSelftest, kSeqNumKernels
+  kSeqChunks, kSeqChunkStates, kSeqSplit, kSeqSplitStates, kSeqCombine, kSeqSelftest,
+  kSeqConv, kSeqConvBackward, kSeqConvWeight, kSeqConvStep,
+  kSeqSelective, kSeqSelectiveStates, kSeqSelectiveJoin, kSeqSelectiveBackward, kSeqSelectiveSums, kSeqSelectiveStep,
+  kSeqNumKernels
 };
 
 // Every launch of a sequence operator is counted, and timed when profiling is
@@ -35,6 +38,8 @@ cudaError_t launch_rotary(const void* args, cudaStream_t s);
 // --------------------------------------------------------------------- norm
 struct NormLaunch {
   tb_norm_args a;
+  int layer;         // the layer norm: rows less their mean, and `bias` (or NULL) added
+  const void* bias;
   int vec, per_row, nv, rows;  // threads of a row, vectors of a thread, rows of a block
   int groups;                  // through shared memory by groups of `rows` rows, nv buffers deep, per_row threads a block; 0: not
   int blocks;
@@ -44,21 +49,86 @@ constexpr size_t norm_buffer_bytes(int width, int size, int rows) {
   return ((size_t)rows * width * size + ((size_t)rows * width * size % 16 ? 15 + 16 : 0)) / 16 * 16;
 }
 // Shared memory of the kernels that move groups of rows: `fixed` bytes an
-// element of a row (a multiple of 16 in all), then the buffers.
+// element of a row (the weight, or 4 for each of its 32-bit arrays where that
+// is 8 or 12; a multiple of 16 in all), then the buffers.
 inline size_t norm_group_bytes(int width, int size, int tensors, int rows, int stages, int fixed) {
-  const size_t head = fixed == 8 ? 2 * (((size_t)width + 3) / 4 * 16) : ((size_t)width * size + 15) / 16 * 16;
+  const size_t head = fixed >= 8 ? fixed / 4 * (((size_t)width + 3) / 4 * 16) : ((size_t)width * size + 15) / 16 * 16;
   return head + stages * tensors * norm_buffer_bytes(width, size, rows);
 }
 constexpr int kNormGroupBytes = 200 * 1024;  // at most
 cudaError_t launch_norm(const void* args, cudaStream_t s);
 struct NormBackwardLaunch {
   tb_norm_backward_args a;
+  int layer;
+  void* dbias;  // of the layer norm, or NULL
   int vec, per_row, nv, rows;
   int groups;
   int blocks;
 };
 cudaError_t launch_norm_backward(const void* args, cudaStream_t s);
 cudaError_t launch_norm_weight(const void* args, cudaStream_t s);
+
+// --------------------------------------------------------------- convolution
+struct ConvLaunch {
+  tb_conv_args a;
+  int vec;       // elements of the vectors that rows are moved by
+  int per_x;     // threads of a row in a block; the others take other runs of rows
+  int blocks_x;  // blocks of a row
+  int run;       // rows of a thread
+  int64_t runs;  // runs of rows, after which a block for each grid makes its state
+};
+cudaError_t launch_conv(const void* args, cudaStream_t s);
+struct ConvBackwardLaunch {
+  ConvLaunch f;
+  tb_conv_backward_args g;
+  int64_t parts;  // rows of the sums' parts: one for each block along the rows
+};
+cudaError_t launch_conv_backward(const void* args, cudaStream_t s);
+cudaError_t launch_conv_weight(const void* args, cudaStream_t s);
+struct ConvStepLaunch {
+  tb_conv_step_args a;
+  int vec;
+};
+cudaError_t launch_conv_step(const void* args, cudaStream_t s);
+
+// ------------------------------------------------------------- selective scan
+constexpr int kScanChannels = 32;  // of a warp
+constexpr int kScanChunk = 64;     // rows that the gradient takes at a time
+struct ScanLaunch {
+  tb_scan_args a;
+  const int64_t* offsets;     // as in LinLaunch: the walks of tb_linattn.cuh
+  int64_t tokens;
+  int32_t grids;
+  int32_t segment, segments;  // rows of one, 0: whole grids; slots
+  int32_t group_tiles;        // tiles of kScanChannels channels of a group
+  int32_t blocks_x;           // blocks of a slot
+  int32_t pad;                // states of a channel in the workspace, a multiple of 4 * nn
+  int32_t nn;                 // states of a lane
+  int32_t vec;                // rows that 16-byte copies can read
+  float* seg;                 // [segments, channels, pad]: states of the segments, then those they start from
+  float* sum;                 // [segments, channels]: their sums of delta
+};
+cudaError_t launch_scan(const void* args, cudaStream_t s);
+cudaError_t launch_scan_states(const void* args, cudaStream_t s);
+cudaError_t launch_scan_join(const void* args, cudaStream_t s);
+struct ScanBackwardLaunch {
+  ScanLaunch f;               // in chunks
+  tb_scan_backward_args g;
+  float* seg_back;            // [segments, channels, pad]: the gradient's own sums of the chunks, then what enters them
+  float* bc;                  // [quads, tokens, groups, 2, pad]: parts of db and dc
+  float* part_a;              // [runs, channels, pad]: parts of da
+  float* part_d;              // [runs, 2, channels]: parts of dd and ddt_bias
+  float* acc;                 // [tokens, channels, 3] sums over the states, where they are more than a pass takes; or NULL
+  int32_t quads, runs, per_run;
+};
+cudaError_t launch_scan_backward(const void* args, cudaStream_t s);
+cudaError_t launch_scan_back_states(const void* args, cudaStream_t s);
+cudaError_t launch_scan_back_join(const void* args, cudaStream_t s);
+cudaError_t launch_scan_sums(const void* args, cudaStream_t s);
+struct ScanStepLaunch {
+  tb_scan_step_args a;
+};
+cudaError_t launch_scan_step(const void* args, cudaStream_t s);
 
 // --------------------------------------------------------- linear attention
 struct StepLaunch {

@@ -152,22 +152,24 @@ tb_status tb_rotary(const tb_rotary_args* args, tb_stream stream) {
 
 // --------------------------------------------------------------------- norm
 
-tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
-  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: args is NULL");
+static tb_status norm_run(const char* what, const tb_norm_args* args, bool layer, const void* bias, tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
   NormLaunch n;
   n.a = *args;
+  n.layer = layer;
+  n.bias = bias;
   tb_norm_args& a = n.a;
-  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: unknown type %d", a.type);
-  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: bad size");
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "%s: unknown type %d", what, a.type);
+  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
   if (a.width > 16384 || a.rows > kMaxRows)
-    return seq_fail(TB_ERR_TOO_LARGE, "tb_rms_norm: rows of %d elements (at most 16384), or 2^31 rows", a.width);
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: rows of %d elements (at most 16384), or 2^31 rows", what, a.width);
   if (a.rows == 0) return TB_OK;
-  if (!a.x || !a.weight || !a.y || (a.h_out && !a.residual) || (a.fp8 != 0) != (a.scale != nullptr))
-    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm: bad pointer");
+  if (!a.x || !a.weight || !a.y || (a.h_out && !a.residual) || (a.fp8 != 0) != (a.scale != nullptr) || (layer && a.fp8))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
   const int sms = seq_sms();
-  if (!sms) return seq_fail(TB_ERR_CUDA, "tb_rms_norm: no device");
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
   const int size = type_size(a.type), vec = 16 / size;
-  n.vec = a.width % vec == 0 && aligned16(a.x) && aligned16(a.weight) && whole(a.x_row, size);
+  n.vec = a.width % vec == 0 && aligned16(a.x) && aligned16(a.weight) && aligned16(bias) && whole(a.x_row, size);
   if (a.residual) n.vec = n.vec && aligned16(a.residual) && whole(a.residual_row, size);
   if (a.h_out) n.vec = n.vec && aligned16(a.h_out) && whole(a.h_row, size);
   if (a.fp8) n.vec = n.vec && ((uintptr_t)a.y & (vec - 1)) == 0 && a.y_row % vec == 0;
@@ -194,6 +196,13 @@ tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
   return TB_OK;
 }
 
+tb_status tb_rms_norm(const tb_norm_args* args, tb_stream stream) {
+  return norm_run("tb_rms_norm", args, false, nullptr, stream);
+}
+tb_status tb_layer_norm(const tb_norm_args* args, const void* bias, tb_stream stream) {
+  return norm_run("tb_layer_norm", args, true, bias, stream);
+}
+
 // Each block writes a part of dweight, which is read once more.
 static int64_t norm_backward_blocks(int64_t rows, int sms) {
   const int64_t most = 6ll * sms;
@@ -206,38 +215,42 @@ int64_t tb_rms_norm_backward_workspace(int64_t rows, int32_t width) {
   return norm_backward_blocks(rows, sms ? sms : 256) * width * (int64_t)sizeof(float);
 }
 
-tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stream) {
-  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: args is NULL");
+static tb_status norm_backward_run(const char* what, const tb_norm_backward_args* args, bool layer, void* dbias,
+                                   tb_stream stream) {
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
   NormBackwardLaunch n;
   n.a = *args;
+  n.layer = layer;
+  n.dbias = dbias;
   tb_norm_backward_args& a = n.a;
-  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: unknown type %d", a.type);
-  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: bad size");
+  if (!type_ok(a.type)) return seq_fail(TB_ERR_INVALID_ARG, "%s: unknown type %d", what, a.type);
+  if (a.rows < 0 || a.width < 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
   if (a.width > 16384 || a.rows > kMaxRows)
-    return seq_fail(TB_ERR_TOO_LARGE, "tb_rms_norm_backward: rows of %d elements (at most 16384), or 2^31 rows", a.width);
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: rows of %d elements (at most 16384), or 2^31 rows", what, a.width);
   if (!a.dweight || (a.rows && (!a.dy || !a.h || !a.weight || !a.dx || !a.workspace)))
-    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: bad pointer");
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
   const int sms = seq_sms();
-  if (!sms) return seq_fail(TB_ERR_CUDA, "tb_rms_norm_backward: no device");
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
   const int64_t most = norm_backward_blocks(a.rows, sms);
-  if (a.workspace_bytes < most * a.width * (int64_t)sizeof(float) || !aligned16(a.workspace))
-    return seq_fail(TB_ERR_INVALID_ARG, "tb_rms_norm_backward: a workspace of %lld bytes, %lld needed",
-                    (long long)a.workspace_bytes, (long long)(most * a.width * 4));
+  const int64_t need = most * a.width * (int64_t)sizeof(float) * (layer ? 2 : 1);
+  if (a.workspace_bytes < need || !aligned16(a.workspace))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what,
+                    (long long)a.workspace_bytes, (long long)need);
   const int size = type_size(a.type), vec = 16 / size;
   n.vec = a.width % vec == 0 && aligned16(a.dy) && aligned16(a.h) && aligned16(a.weight) && aligned16(a.dx) &&
           whole(a.dy_row, size) && whole(a.h_row, size) && whole(a.dx_row, size);
   if (a.dh) n.vec = n.vec && aligned16(a.dh) && whole(a.dh_row, size);
   const bool many = a.rows >= 4ll * sms;
-  const int tensors = a.dh ? 3 : 2;
+  const int tensors = a.dh ? 3 : 2, fixed = layer ? 12 : 8;
   const bool dense = aligned16(a.dy) && aligned16(a.h) && aligned16(a.dx) && a.dy_row == a.width && a.h_row == a.width &&
                      a.dx_row == a.width && (!a.dh || (aligned16(a.dh) && a.dh_row == a.width));
-  const NormGroups groups = !n.vec && (many || a.width > 4096) && dense ? norm_groups(a.width, size, tensors, 8) : NormGroups{0, 0};
+  const NormGroups groups = !n.vec && (many || a.width > 4096) && dense ? norm_groups(a.width, size, tensors, fixed) : NormGroups{0, 0};
   int64_t blocks;
   n.groups = groups.rows > 0;
   if (n.groups) {
     n.nv = groups.stages;
     n.rows = groups.rows;
-    blocks = norm_group_blocks(a.rows, a.width, size, tensors, groups, 8, sms, &n.per_row);
+    blocks = norm_group_blocks(a.rows, a.width, size, tensors, groups, fixed, sms, &n.per_row);
   } else {
     // dweight takes registers: up to two vectors a thread while the row fits 512
     const NormShape z = n.vec ? norm_shape(many, a.width / vec, kVecs, 4, 256, 512)
@@ -252,6 +265,329 @@ tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stre
   n.blocks = (int)(blocks < most ? blocks : most);
   if (a.rows) TB_SEQ_CUDA(seq_launch(kSeqNormBackward, (cudaStream_t)stream, launch_norm_backward, &n));
   TB_SEQ_CUDA(seq_launch(kSeqNormWeight, (cudaStream_t)stream, launch_norm_weight, &n));
+  return TB_OK;
+}
+
+tb_status tb_rms_norm_backward(const tb_norm_backward_args* args, tb_stream stream) {
+  return norm_backward_run("tb_rms_norm_backward", args, false, nullptr, stream);
+}
+int64_t tb_layer_norm_backward_workspace(int64_t rows, int32_t width) {
+  return 2 * tb_rms_norm_backward_workspace(rows, width);
+}
+tb_status tb_layer_norm_backward(const tb_norm_backward_args* args, void* dbias, tb_stream stream) {
+  return norm_backward_run("tb_layer_norm_backward", args, true, dbias, stream);
+}
+
+// Segment slots of a call, its walks along the rows: the segments of any offsets, or the grids.
+static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
+  return segment ? tokens / segment + grids : grids;
+}
+
+// -------------------------------------------------------------- convolution
+
+static tb_status conv_sizes(const char* what, int64_t rows, int32_t channels, int32_t taps, int32_t type) {
+  if (!type_ok(type)) return seq_fail(TB_ERR_INVALID_ARG, "%s: unknown type %d", what, type);
+  if (rows < 0 || channels < 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (taps < 2 || taps > 4) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d taps (2 to 4)", what, taps);
+  if (rows > kMaxRows || up(channels, 128) * (rows + 1) > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 rows, or blocks of 128 channels of them, or more", what);
+  return TB_OK;
+}
+static tb_status conv_check(const char* what, const tb_conv_args& a) {
+  const tb_status st = conv_sizes(what, a.tokens + (a.grids > 0 ? a.grids : 0), a.channels, a.taps, a.type);
+  if (st != TB_OK) return st;
+  if (a.tokens < 0 || a.grids < 0) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (!a.offsets && a.grids != 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d grids without offsets", what, a.grids);
+  if (a.grids == 0 && a.tokens) return seq_fail(TB_ERR_INVALID_ARG, "%s: tokens without grids", what);
+  if (!a.weight || (a.tokens && !a.x)) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  return TB_OK;
+}
+// Threads along the channels: up to 128 of a block, evenly over the blocks; rows
+// of fewer share one.  Runs of rows are as long as gives every multiprocessor
+// `threads` threads, within bounds.
+static void conv_shape(ConvLaunch& l, int sms, int threads, int least, int most) {
+  const int64_t cols = l.a.channels / l.vec;
+  l.blocks_x = (int)up(cols, 128);
+  l.per_x = (int)up(cols, l.blocks_x);
+  const int64_t run = l.a.tokens * cols / ((int64_t)threads * sms);
+  l.run = (int)(run < least ? least : run > most ? most : run);
+  l.runs = up(l.a.tokens, l.run);
+}
+static bool conv_fits(int vec, int size, const void* p, int64_t row) {
+  return (uintptr_t)p % (vec * size) == 0 && row % vec == 0;
+}
+
+tb_status tb_causal_conv(const tb_conv_args* args, tb_stream stream) {
+  const char* what = "tb_causal_conv";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ConvLaunch l{};
+  l.a = *args;
+  const tb_conv_args& a = l.a;
+  const tb_status st = conv_check(what, a);
+  if (st != TB_OK) return st;
+  if (a.tokens && !a.y) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  if (a.grids == 0 || (a.tokens == 0 && !a.state_out)) return TB_OK;
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  const int size = type_size(a.type), vec = 16 / size;
+  const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, a.y, a.y_row) &&
+                    aligned16(a.state) && aligned16(a.state_out);
+  l.vec = fits ? vec : 1;
+  conv_shape(l, sms, 512, 4, 32);
+  TB_SEQ_CUDA(seq_launch(kSeqConv, (cudaStream_t)stream, launch_conv, &l));
+  return TB_OK;
+}
+
+constexpr int kConvBackThreads = 768, kConvBackLeast = 8, kConvBackMost = 256;
+
+int64_t tb_causal_conv_backward_workspace(int64_t tokens, int32_t channels, int32_t taps) {
+  if (tokens < 0 || channels < 1 || taps < 2 || taps > 4) return 0;
+  const int sms = seq_sms();
+  int64_t most = 0;
+  for (int vec = 1; vec <= 4; vec *= 2) {
+    if (channels % vec) continue;
+    ConvLaunch l{};
+    l.a.tokens = tokens, l.a.channels = channels, l.vec = vec;
+    conv_shape(l, sms ? sms : 256, kConvBackThreads, kConvBackLeast, kConvBackMost);
+    const int64_t parts = up(l.runs, 128 / l.per_x);
+    if (parts > most) most = parts;
+  }
+  return most * (taps + 1) * channels * (int64_t)sizeof(float);
+}
+
+tb_status tb_causal_conv_backward(const tb_conv_backward_args* args, tb_stream stream) {
+  const char* what = "tb_causal_conv_backward";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ConvBackwardLaunch l{};
+  l.f.a = args->f;
+  l.g = *args;
+  const tb_conv_args& a = l.f.a;
+  const tb_conv_backward_args& g = l.g;
+  const tb_status st = conv_check(what, a);
+  if (st != TB_OK) return st;
+  if (!g.dweight || (a.tokens && (!g.dy || !g.dx || !g.workspace))) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  const int64_t need = tb_causal_conv_backward_workspace(a.tokens, a.channels, a.taps);
+  if (g.workspace_bytes < need || !aligned16(g.workspace))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what, (long long)g.workspace_bytes,
+                    (long long)need);
+  // vectors of 8 bytes: the windows of x and of its gradient take twice the registers of the forward pass
+  const int size = type_size(a.type), vec = 8 / size;
+  const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, g.dy, g.dy_row) &&
+                    conv_fits(vec, size, g.dx, g.dx_row) && conv_fits(vec, size, a.state, 0) &&
+                    conv_fits(vec, size, g.dstate_out, 0) && conv_fits(vec, size, g.dstate, 0);
+  l.f.vec = fits ? vec : 1;
+  conv_shape(l.f, sms, kConvBackThreads, kConvBackLeast, kConvBackMost);
+  l.parts = up(l.f.runs, 128 / l.f.per_x);
+  if (a.tokens || (g.dstate && a.grids)) TB_SEQ_CUDA(seq_launch(kSeqConvBackward, (cudaStream_t)stream, launch_conv_backward, &l));
+  TB_SEQ_CUDA(seq_launch(kSeqConvWeight, (cudaStream_t)stream, launch_conv_weight, &l));
+  return TB_OK;
+}
+
+tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream stream) {
+  const char* what = "tb_causal_conv_step";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ConvStepLaunch l{};
+  l.a = *args;
+  const tb_conv_step_args& a = l.a;
+  const tb_status st = conv_sizes(what, a.streams, a.channels, a.taps, a.type);
+  if (st != TB_OK) return st;
+  if (a.num_slots < 0) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (a.streams == 0) return TB_OK;
+  if (!a.slots && a.num_slots < a.streams)
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: %lld streams, %lld states", what, (long long)a.streams, (long long)a.num_slots);
+  if (!a.x || !a.weight || !a.y || (a.num_slots && !a.state)) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  const int size = type_size(a.type), vec = 16 / size;
+  const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, a.y, a.y_row) &&
+                    aligned16(a.state);
+  l.vec = fits ? vec : 1;
+  TB_SEQ_CUDA(seq_launch(kSeqConvStep, (cudaStream_t)stream, launch_conv_step, &l));
+  return TB_OK;
+}
+
+// ----------------------------------------------------------- selective scan
+
+// Tiles of kScanChannels channels and blocks of states; 4 warps of tiles a block.
+static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t groups) {
+  l.group_tiles = (int32_t)up(channels / groups, kScanChannels);
+  l.blocks_x = (int32_t)up((int64_t)groups * l.group_tiles, 4);
+  l.nn = states <= 8 ? 2 : 4;
+  l.pad = (int32_t)up(states, 4 * l.nn) * 4 * l.nn;
+}
+
+// Rows of a segment of the forward pass, 0: grids are walked whole.  A walk is
+// sequential along a grid and a warp's, so a call with few of them is split; the
+// segments' own states cost most of a walk once more.
+static int32_t scan_segment(int64_t tokens, int32_t grids, int32_t groups, int32_t group_tiles, int sms) {
+  const int64_t walks = (int64_t)grids * groups * group_tiles;
+  if (grids <= 0 || walks >= 8ll * sms || tokens < 256ll * grids) return 0;
+  int64_t seg = up(up(tokens * groups * group_tiles, 12 * sms), 64) * 64;
+  if (seg < 64) seg = 64;
+  return tokens >= 2 * seg * grids ? (int32_t)seg : 0;
+}
+
+struct ScanCarve {
+  int64_t seg, sum, seg_back, bc, part_a, part_d, acc, bytes;
+  int32_t quads, runs, per_run;
+};
+static ScanCarve scan_carve(int64_t slots, int64_t tokens, int32_t channels, int32_t groups, const ScanLaunch& l, bool backward,
+                            int sms) {
+  ScanCarve c{};
+  auto take = [&](int64_t floats) {
+    const int64_t at = c.bytes;
+    c.bytes += up(floats * 4, 256) * 256;
+    return at;
+  };
+  c.seg = take(slots * channels * l.pad);
+  c.sum = take(slots * channels);
+  if (!backward) return c;
+  c.quads = (int32_t)up(l.group_tiles, 4);
+  // blocks take runs of chunks, whose parts of da they keep in registers: as many as make six waves or so
+  const int64_t blocks = slots * groups * c.quads;
+  c.per_run = (int32_t)up(blocks, 12ll * sms);
+  c.runs = (int32_t)up(slots, c.per_run > 0 ? c.per_run : 1);
+  c.seg_back = take(slots * channels * l.pad);
+  c.bc = take((int64_t)c.quads * tokens * groups * 2 * l.pad);
+  c.part_a = take((int64_t)c.runs * channels * l.pad);
+  c.part_d = take((int64_t)c.runs * 2 * channels);
+  if (l.pad > 4 * l.nn) c.acc = take(tokens * channels * 3);
+  return c;
+}
+
+int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t channels, int32_t states, int32_t groups,
+                                    int32_t backward) {
+  if (tokens < 0 || grids < 0 || channels < 1 || states < 1 || states > 256 || groups < 1 || channels % groups) return 0;
+  ScanLaunch l{};
+  scan_shape(l, channels, states, groups);
+  int sms = seq_sms();
+  if (!sms) sms = 256;
+  const int32_t seg = backward ? kScanChunk : scan_segment(tokens, grids, groups, l.group_tiles, sms);
+  if (!seg) return 0;
+  return scan_carve(segment_slots(tokens, grids, seg), tokens, channels, groups, l, backward, sms).bytes;
+}
+
+static tb_status scan_sizes(const char* what, int64_t rows, int32_t channels, int32_t states, int32_t groups, int32_t type) {
+  if (!type_ok(type)) return seq_fail(TB_ERR_INVALID_ARG, "%s: unknown type %d", what, type);
+  if (rows < 0 || channels < 1 || states < 1 || groups < 1 || channels % groups)
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size (%d channels in %d groups)", what, channels, groups);
+  if (states > 256 || rows > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: %d states a channel (at most 256), or 2^31 rows", what, states);
+  return TB_OK;
+}
+
+// Completes l for its l.a: the walk, and the carve of a workspace of a.workspace_bytes.
+static tb_status scan_plan(const char* what, ScanLaunch& l, bool backward, ScanCarve& c, int sms) {
+  const tb_scan_args& a = l.a;
+  const int size = type_size(a.type);
+  scan_shape(l, a.channels, a.states, a.groups);
+  l.offsets = a.offsets, l.tokens = a.tokens, l.grids = a.grids;
+  l.segment = backward ? kScanChunk : scan_segment(a.tokens, a.grids, a.groups, l.group_tiles, sms);
+  const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
+  const int64_t per_slot = (int64_t)a.groups * up(l.group_tiles, 4) + l.blocks_x;
+  const int64_t join = up((int64_t)a.channels * (l.pad / 4), 128);
+  if (slots > kMaxRows / per_slot || a.grids > kMaxRows / join ||
+      (backward && a.tokens > kMaxRows / (up((int64_t)a.groups * 2 * a.states, 512) + 1) - join * 32))
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 blocks or more", what);
+  l.segments = (int32_t)slots;
+  auto whole_rows = [&](const void* p, int64_t row) { return !p || (aligned16(p) && whole(row, size)); };
+  l.vec = whole_rows(a.x, a.x_row) && whole_rows(a.dt, a.dt_row) && whole_rows(a.z, a.z_row) &&
+          (a.groups == 1 || whole(a.channels / a.groups, size));
+  if (!l.segment) return TB_OK;
+  c = scan_carve(slots, a.tokens, a.channels, a.groups, l, backward, sms);
+  if (!a.workspace || a.workspace_bytes < c.bytes || ((uintptr_t)a.workspace & 255))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what, (long long)a.workspace_bytes,
+                    (long long)c.bytes);
+  l.seg = (float*)((char*)a.workspace + c.seg);
+  l.sum = (float*)((char*)a.workspace + c.sum);
+  return TB_OK;
+}
+
+static tb_status scan_check(const char* what, const tb_scan_args& a) {
+  const tb_status st = scan_sizes(what, a.tokens, a.channels, a.states, a.groups, a.type);
+  if (st != TB_OK) return st;
+  if (a.grids < 0) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (!a.offsets && a.grids != 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d grids without offsets", what, a.grids);
+  if (a.grids == 0 && a.tokens) return seq_fail(TB_ERR_INVALID_ARG, "%s: tokens without grids", what);
+  if (!a.a || (a.tokens && (!a.x || !a.dt || !a.b || !a.c))) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  return TB_OK;
+}
+
+tb_status tb_selective_scan(const tb_scan_args* args, tb_stream stream) {
+  const char* what = "tb_selective_scan";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ScanLaunch l{};
+  l.a = *args;
+  const tb_scan_args& a = l.a;
+  tb_status st = scan_check(what, a);
+  if (st != TB_OK) return st;
+  if (a.tokens && !a.y) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  if (a.grids == 0 || (a.tokens == 0 && !a.state_out)) return TB_OK;
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  ScanCarve c{};
+  st = scan_plan(what, l, false, c, sms);
+  if (st != TB_OK) return st;
+  if (l.segment) {
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, (cudaStream_t)stream, launch_scan_states, &l));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveJoin, (cudaStream_t)stream, launch_scan_join, &l));
+  }
+  TB_SEQ_CUDA(seq_launch(kSeqSelective, (cudaStream_t)stream, launch_scan, &l));
+  return TB_OK;
+}
+
+tb_status tb_selective_scan_backward(const tb_scan_backward_args* args, tb_stream stream) {
+  const char* what = "tb_selective_scan_backward";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ScanBackwardLaunch g{};
+  g.f.a = args->f;
+  g.g = *args;
+  const tb_scan_args& a = g.f.a;
+  tb_status st = scan_check(what, a);
+  if (st != TB_OK) return st;
+  if (!g.g.da || (a.tokens && (!g.g.dy || !g.g.dx || !g.g.ddt || !g.g.db || !g.g.dc || (a.z && !g.g.dz))))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  ScanCarve c{};
+  st = scan_plan(what, g.f, true, c, sms);
+  if (st != TB_OK) return st;
+  g.f.vec = g.f.vec && (!g.g.dy || (aligned16(g.g.dy) && whole(g.g.dy_row, type_size(a.type))));
+  char* const work = (char*)a.workspace;
+  g.seg_back = (float*)(work + c.seg_back);
+  g.bc = (float*)(work + c.bc);
+  g.part_a = (float*)(work + c.part_a);
+  g.part_d = (float*)(work + c.part_d);
+  g.acc = c.acc ? (float*)(work + c.acc) : nullptr;
+  g.quads = c.quads, g.runs = c.runs, g.per_run = c.per_run;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (a.grids) {
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, s, launch_scan_states, &g.f));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, s, launch_scan_back_states, &g));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveJoin, s, launch_scan_join, &g.f));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveJoin, s, launch_scan_back_join, &g));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveBackward, s, launch_scan_backward, &g));
+  }
+  TB_SEQ_CUDA(seq_launch(kSeqSelectiveSums, s, launch_scan_sums, &g));
+  return TB_OK;
+}
+
+tb_status tb_selective_scan_step(const tb_scan_step_args* args, tb_stream stream) {
+  const char* what = "tb_selective_scan_step";
+  if (!args) return seq_fail(TB_ERR_INVALID_ARG, "%s: args is NULL", what);
+  ScanStepLaunch l{};
+  l.a = *args;
+  const tb_scan_step_args& a = l.a;
+  const tb_status st = scan_sizes(what, a.streams, a.channels, a.states, a.groups, a.type);
+  if (st != TB_OK) return st;
+  if (a.num_slots < 0) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad size", what);
+  if (a.streams == 0) return TB_OK;
+  if (!a.slots && a.num_slots < a.streams)
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: %lld streams, %lld states", what, (long long)a.streams, (long long)a.num_slots);
+  if (!a.x || !a.dt || !a.a || !a.b || !a.c || !a.y ||
+      (a.num_slots && (!a.state || (uintptr_t)a.state % (a.states % 4 == 0 ? 16 : 4))))
+    return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer (states are 16-byte aligned where they are a multiple of 4)", what);
+  TB_SEQ_CUDA(seq_launch(kSeqSelectiveStep, (cudaStream_t)stream, launch_scan_step, &l));
   return TB_OK;
 }
 
@@ -294,10 +630,6 @@ static int32_t segment_tokens(const LinSizes& z, int problems, int sms) {
   if (tc && seg < 128) seg = 128;
   const int64_t least = tc ? (seg < 256 ? 768 : 3 * seg) : seg < 96 ? 192 : 2 * seg;
   return z.tokens >= least * z.grids ? (int32_t)seg : 0;
-}
-
-static int64_t segment_slots(int64_t tokens, int32_t grids, int32_t segment) {
-  return segment ? tokens / segment + grids : grids;
 }
 
 int64_t tb_linear_attention_workspace(int64_t tokens, int32_t grids, int32_t heads, int32_t key, int32_t value,

@@ -411,6 +411,437 @@ TB_ENTRY(norm_backward, 5) {
   return tuple({wrap(dx), wrap(dw)});
 }
 
+// (x, weight, bias or None, residual or None, eps) -> (y, h), h the input x
+// without a residual; or None where gradients are asked for
+TB_ENTRY(layer_norm, 5) {
+  const char* what = "layer_norm";
+  const at::Tensor& x = tensor(what, "x", a[0]);
+  const at::Tensor& weight = tensor(what, "weight", a[1]);
+  const at::Tensor* bias = maybe(what, "bias", a[2]);
+  const at::Tensor* residual = maybe(what, "residual", a[3]);
+  if (tracked(&x, &weight, bias, residual)) Py_RETURN_NONE;
+  const int device = device_of(what, x);
+  tb_norm_args r{};
+  r.type = type_of(what, x);
+  const Flat fx(what, "x", x);
+  Flat fr;
+  at::Tensor weight_copy, bias_copy, h;
+  const void* bias_at = nullptr;
+  const int64_t shape_w[1] = {fx.width};
+  weight_of(what, weight, fx.width, x, device, weight_copy, &r.weight);
+  if (bias) {
+    same(what, "bias", *bias, shape_w, x.scalar_type(), device);
+    bias_at = contiguous(*bias, bias_copy);
+  }
+  if (fx.width > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+  r.x = fx.p, r.x_row = fx.row, r.rows = fx.rows, r.width = (int32_t)fx.width;
+  if (residual) {
+    same(what, "residual", *residual, x.sizes(), x.scalar_type(), device);
+    fr = Flat(what, "residual", *residual);
+    h = empty(x.sizes(), x.scalar_type(), device);
+    r.residual = fr.p, r.residual_row = fr.row;
+    r.h_out = h.data_ptr(), r.h_row = fx.width;
+  }
+  at::Tensor y = empty(x.sizes(), x.scalar_type(), device);
+  r.y = y.data_ptr(), r.y_row = fx.width;
+  r.eps = (float)number(a[4]);
+  if (r.rows) check(tb_layer_norm(&r, bias_at, stream_of(device)));
+  return tuple({wrap(y), residual ? wrap(h) : keep(a[0])});
+}
+
+// (dy, h, weight, dh or None, eps) -> (dx, dweight, dbias)
+TB_ENTRY(layer_norm_backward, 5) {
+  const char* what = "layer_norm_backward";
+  const at::Tensor& dy = tensor(what, "dy", a[0]);
+  const at::Tensor& h = tensor(what, "h", a[1]);
+  const at::Tensor& weight = tensor(what, "weight", a[2]);
+  const at::Tensor* dh = maybe(what, "dh", a[3]);
+  if (tracked(&dy, &h, &weight, dh)) refuse_second(what);
+  const int device = device_of(what, h);
+  tb_norm_backward_args r{};
+  r.type = type_of(what, h);
+  const Flat fh(what, "h", h);
+  same(what, "dy", dy, h.sizes(), h.scalar_type(), device);
+  const Flat fd(what, "dy", dy);
+  Flat fg;
+  at::Tensor weight_copy;
+  weight_of(what, weight, fh.width, h, device, weight_copy, &r.weight);
+  if (dh) {
+    same(what, "dh", *dh, h.sizes(), h.scalar_type(), device);
+    fg = Flat(what, "dh", *dh);
+  }
+  if (fh.width > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+  at::Tensor dx = empty(h.sizes(), h.scalar_type(), device), dw = empty({fh.width}, h.scalar_type(), device),
+             db = empty({fh.width}, h.scalar_type(), device);
+  r.workspace_bytes = tb_layer_norm_backward_workspace(fh.rows, (int32_t)fh.width);
+  at::Tensor work = empty({r.workspace_bytes}, at::kByte, device);
+  r.dy = fd.p, r.dy_row = fd.row;
+  r.h = fh.p, r.h_row = fh.row, r.rows = fh.rows, r.width = (int32_t)fh.width;
+  r.dh = fg.p, r.dh_row = fg.row;
+  r.dx = dx.data_ptr(), r.dx_row = fh.width;
+  r.dweight = dw.data_ptr();
+  r.workspace = (float*)work.data_ptr();
+  r.eps = (float)number(a[4]);
+  check(tb_layer_norm_backward(&r, db.data_ptr(), stream_of(device)));
+  return tuple({wrap(dx), wrap(dw), wrap(db)});
+}
+
+// --------------------------------------------------------------- convolution
+
+// Rows [rows, channels].
+Flat matrix(const char* what, const char* name, const at::Tensor& t) {
+  if (t.dim() != 2) refuse("%s: %s must have 2 dimensions (rows, channels), got %d", what, name, (int)t.dim());
+  return Flat(what, name, t);
+}
+
+// Whole, as offsets of a call's grids; the number of grids.
+int64_t grids_of(const char* what, const at::Tensor* offsets, int device, const int64_t** p, at::Tensor& hold) {
+  if (!offsets) return 1;
+  const int64_t grids = offsets->dim() == 1 ? offsets->size(0) - 1 : -1;
+  if (grids < 0 || offsets->scalar_type() != at::kLong || !offsets->is_cuda() || offsets->get_device() != device)
+    refuse("%s: offsets must be int64 [grids + 1] on device %d", what, device);
+  if (grids > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+  *p = (const int64_t*)contiguous(*offsets, hold);
+  return grids;
+}
+
+bool silu_of(const char* what, PyObject* o) {
+  if (o == Py_None) return false;
+  const char* text = PyUnicode_Check(o) ? PyUnicode_AsUTF8(o) : nullptr;
+  if (!text) PyErr_Clear();
+  if (!text || std::string(text) != "silu") refuse("%s: the activation must be \"silu\" or None", what);
+  return true;
+}
+
+struct Conv {
+  int device;
+  Flat x;
+  at::Tensor weight_copy, bias_copy, offsets_copy, state_copy;
+  tb_conv_args r{};
+  at::ScalarType dtype;
+
+  // x, weight, bias or None, offsets or None, state or None, activation
+  Conv(const char* what, const at::Tensor& tx, const at::Tensor& weight, const at::Tensor* bias, const at::Tensor* offsets,
+       const at::Tensor* state, PyObject* activation) {
+    device = device_of(what, tx);
+    r.type = type_of(what, tx);
+    dtype = tx.scalar_type();
+    x = matrix(what, "x", tx);
+    const int64_t taps = weight.dim() == 2 ? weight.size(1) : 0, shape_w[2] = {x.width, taps}, shape_b[1] = {x.width};
+    same(what, "weight", weight, shape_w, dtype, device);
+    if (taps < 2 || taps > 4) refuse("%s: %lld taps (2 to 4)", what, (long long)taps);
+    r.weight = contiguous(weight, weight_copy);
+    if (bias) {
+      same(what, "bias", *bias, shape_b, dtype, device);
+      r.bias = contiguous(*bias, bias_copy);
+    }
+    const int64_t grids = grids_of(what, offsets, device, &r.offsets, offsets_copy), shape_s[3] = {grids, taps - 1, x.width};
+    if (state) {
+      same(what, "state", *state, shape_s, dtype, device);
+      r.state = contiguous(*state, state_copy);
+    }
+    if (x.width > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+    r.silu = silu_of(what, activation);
+    r.x = x.p, r.x_row = x.row;
+    r.tokens = x.rows;
+    r.grids = (int32_t)grids, r.channels = (int32_t)x.width, r.taps = (int32_t)taps;
+  }
+  at::Tensor rows() const { return empty({x.rows, x.width}, dtype, device); }
+  at::Tensor states() const { return empty({r.grids, r.taps - 1, x.width}, dtype, device); }
+};
+
+// (x, weight, bias or None, offsets or None, state or None, activation,
+// return_state) -> (y, last states or None), or None where gradients are asked for
+TB_ENTRY(conv, 7) {
+  const char* what = "causal_conv";
+  const at::Tensor& tx = tensor(what, "x", a[0]);
+  const at::Tensor& weight = tensor(what, "weight", a[1]);
+  const at::Tensor *bias = maybe(what, "bias", a[2]), *offsets = maybe(what, "offsets", a[3]), *state = maybe(what, "state", a[4]);
+  if (tracked(&tx, &weight, bias, state)) Py_RETURN_NONE;
+  Conv c(what, tx, weight, bias, offsets, state, a[5]);
+  at::Tensor y = c.rows(), last;
+  if (truth(a[6])) last = c.states();
+  c.r.y = y.data_ptr(), c.r.y_row = c.x.width;
+  c.r.state_out = last.defined() ? last.data_ptr() : nullptr;
+  check(tb_causal_conv(&c.r, stream_of(c.device)));
+  return tuple({wrap(y), wrap(last)});
+}
+
+// (dy, x, weight, bias or None, offsets or None, state or None, activation,
+// dstate or None) -> (dx, dweight, dbias or None, gradient of the first states or None)
+TB_ENTRY(conv_backward, 8) {
+  const char* what = "causal_conv_backward";
+  const at::Tensor& dy = tensor(what, "dy", a[0]);
+  const at::Tensor& tx = tensor(what, "x", a[1]);
+  const at::Tensor& weight = tensor(what, "weight", a[2]);
+  const at::Tensor *bias = maybe(what, "bias", a[3]), *offsets = maybe(what, "offsets", a[4]), *state = maybe(what, "state", a[5]);
+  const at::Tensor* dstate = maybe(what, "dstate", a[7]);
+  if (tracked(&dy, &tx, &weight, bias, state, dstate)) refuse_second(what);
+  Conv c(what, tx, weight, bias, offsets, state, a[6]);
+  same(what, "dy", dy, tx.sizes(), c.dtype, c.device);
+  const Flat fd(what, "dy", dy);
+  tb_conv_backward_args b{};
+  at::Tensor dstate_copy, dx = c.rows(), dw = empty({c.x.width, c.r.taps}, c.dtype, c.device), db, first;
+  if (dstate) {
+    const int64_t shape_s[3] = {c.r.grids, c.r.taps - 1, c.x.width};
+    same(what, "dstate", *dstate, shape_s, c.dtype, c.device);
+    b.dstate_out = contiguous(*dstate, dstate_copy);
+  }
+  if (bias) {
+    db = empty({c.x.width}, c.dtype, c.device);
+    b.dbias = db.data_ptr();
+  }
+  if (state) {
+    first = c.states();
+    b.dstate = first.data_ptr();
+  }
+  b.workspace_bytes = tb_causal_conv_backward_workspace(c.r.tokens, c.r.channels, c.r.taps);
+  at::Tensor work = empty({b.workspace_bytes}, at::kByte, c.device);
+  b.workspace = (float*)work.data_ptr();
+  b.f = c.r;
+  b.dy = fd.p, b.dy_row = fd.row;
+  b.dx = dx.data_ptr(), b.dx_row = c.x.width;
+  b.dweight = dw.data_ptr();
+  check(tb_causal_conv_backward(&b, stream_of(c.device)));
+  return tuple({wrap(dx), wrap(dw), wrap(db), wrap(first)});
+}
+
+// (x, weight, state, bias or None, slots or None, activation) -> y
+TB_ENTRY(conv_step, 6) {
+  const char* what = "causal_conv_step";
+  const at::Tensor& tx = tensor(what, "x", a[0]);
+  const at::Tensor& weight = tensor(what, "weight", a[1]);
+  const at::Tensor& state = tensor(what, "state", a[2]);
+  const at::Tensor *bias = maybe(what, "bias", a[3]), *slots = maybe(what, "slots", a[4]);
+  const int device = device_of(what, tx);
+  tb_conv_step_args r{};
+  r.type = type_of(what, tx);
+  const at::ScalarType dtype = tx.scalar_type();
+  const Flat x = matrix(what, "x", tx);
+  const int64_t taps = weight.dim() == 2 ? weight.size(1) : 0, shape_w[2] = {x.width, taps}, shape_b[1] = {x.width},
+                shape_s[3] = {state.dim() == 3 ? state.size(0) : 0, taps - 1, x.width};
+  same(what, "weight", weight, shape_w, dtype, device);
+  if (taps < 2 || taps > 4) refuse("%s: %lld taps (2 to 4)", what, (long long)taps);
+  same(what, "state", state, shape_s, dtype, device);
+  if (!state.is_contiguous()) refuse("%s: the states must be contiguous", what);
+  at::Tensor weight_copy, bias_copy, slots_copy;
+  if (bias) {
+    same(what, "bias", *bias, shape_b, dtype, device);
+    r.bias = contiguous(*bias, bias_copy);
+  }
+  if (slots) {
+    const int64_t shape_n[1] = {x.rows};
+    same(what, "slots", *slots, shape_n, at::kInt, device);
+    r.slots = (const int32_t*)contiguous(*slots, slots_copy);
+  }
+  if (tracked(&tx, &weight, bias, &state)) refuse("%s: a step in place has no gradient (causal_conv has)", what);
+  if (x.width > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+  r.silu = silu_of(what, a[5]);
+  r.weight = contiguous(weight, weight_copy);
+  at::Tensor y = empty({x.rows, x.width}, dtype, device);
+  r.x = x.p, r.x_row = x.row;
+  r.y = y.data_ptr(), r.y_row = x.width;
+  r.state = state.data_ptr();
+  r.streams = x.rows, r.num_slots = shape_s[0];
+  r.channels = (int32_t)x.width, r.taps = (int32_t)taps;
+  written(state);
+  check(tb_causal_conv_step(&r, stream_of(device)));
+  return wrap(y);
+}
+
+// ------------------------------------------------------------ selective scan
+
+// The rows and parameters that the scan and its step take:
+// x, dt, a, b, c [.., groups, states] or [.., states], d, z, dt_bias or None.
+struct ScanRows {
+  int device;
+  Flat x, dt, z;
+  Rows b, c;
+  at::Tensor b_three, c_three, a_copy, d_copy, bias_copy;
+  at::ScalarType dtype;
+  int32_t type;
+  int64_t states;
+  const float *rate, *d = nullptr, *bias = nullptr;
+
+  ScanRows(const char* what, PyObject* const* a) {
+    const at::Tensor& tx = tensor(what, "x", a[0]);
+    const at::Tensor& tdt = tensor(what, "dt", a[1]);
+    const at::Tensor& ta = tensor(what, "a", a[2]);
+    const at::Tensor *td = maybe(what, "d", a[5]), *tz = maybe(what, "z", a[6]), *tbias = maybe(what, "dt_bias", a[7]);
+    device = device_of(what, tx);
+    type = type_of(what, tx);
+    dtype = tx.scalar_type();
+    x = matrix(what, "x", tx);
+    same(what, "dt", tdt, tx.sizes(), dtype, device);
+    dt = Flat(what, "dt", tdt);
+    if (tz) {
+      same(what, "z", *tz, tx.sizes(), dtype, device);
+      z = Flat(what, "z", *tz);
+    }
+    states = ta.dim() == 2 ? ta.size(1) : 0;
+    const int64_t shape_a[2] = {x.width, states}, shape_d[1] = {x.width};
+    same(what, "a", ta, shape_a, at::kFloat, device);
+    rate = (const float*)contiguous(ta, a_copy);
+    if (td) {
+      same(what, "d", *td, shape_d, at::kFloat, device);
+      d = (const float*)contiguous(*td, d_copy);
+    }
+    if (tbias) {
+      same(what, "dt_bias", *tbias, shape_d, at::kFloat, device);
+      bias = (const float*)contiguous(*tbias, bias_copy);
+    }
+    auto rows = [&](const char* name, PyObject* o, at::Tensor& three) {
+      const at::Tensor* t = &tensor(what, name, o);
+      if (t->dim() == 2) {
+        three = t->unsqueeze(1);
+        t = &three;
+      }
+      const int64_t shape[3] = {x.rows, t->dim() == 3 ? t->size(1) : 0, states};
+      same(what, name, *t, shape, dtype, device);
+      return Rows(what, name, *t);
+    };
+    b = rows("b", a[3], b_three);
+    c = rows("c", a[4], c_three);
+    if (c.heads != b.heads) refuse("%s: b has %lld groups, c %lld", what, (long long)b.heads, (long long)c.heads);
+    if (x.width > INT32_MAX || b.heads > INT32_MAX || states > INT32_MAX) refuse("%s: sizes beyond 2^31", what);
+    if (b.heads < 1 || x.width % b.heads)
+      refuse("%s: %lld channels in %lld groups", what, (long long)x.width, (long long)b.heads);
+  }
+  template <class R>
+  void fill(R& r) const {
+    r.x = x.p, r.x_row = x.row;
+    r.dt = dt.p, r.dt_row = dt.row;
+    r.z = z.p, r.z_row = z.row;
+    r.b = b.p, r.b_row = b.row, r.b_group = b.head;
+    r.c = c.p, r.c_row = c.row, r.c_group = c.head;
+    r.a = rate, r.d = d, r.dt_bias = bias;
+    r.channels = (int32_t)x.width, r.states = (int32_t)states, r.groups = (int32_t)b.heads, r.type = type;
+  }
+  at::Tensor rows() const { return empty({x.rows, x.width}, dtype, device); }
+};
+
+struct Scan : ScanRows {
+  at::Tensor offsets_copy, state_copy, work;
+  tb_scan_args r{};
+  // as ScanRows, then softplus, offsets or None, state or None
+  Scan(const char* what, PyObject* const* a) : ScanRows(what, a) {
+    const at::Tensor *offsets = maybe(what, "offsets", a[9]), *state = maybe(what, "state", a[10]);
+    fill(r);
+    r.softplus = truth(a[8]);
+    const int64_t grids = grids_of(what, offsets, device, &r.offsets, offsets_copy), shape_s[3] = {grids, x.width, states};
+    if (state) {
+      same(what, "state", *state, shape_s, at::kFloat, device);
+      r.state = (const float*)contiguous(*state, state_copy);
+    }
+    r.tokens = x.rows;
+    r.grids = (int32_t)grids;
+  }
+  at::Tensor last() const { return empty({r.grids, x.width, states}, at::kFloat, device); }
+  void workspace(bool backward) {
+    r.workspace_bytes = tb_selective_scan_workspace(r.tokens, r.grids, r.channels, r.states, r.groups, backward);
+    if (!r.workspace_bytes) return;
+    work = empty({r.workspace_bytes}, at::kByte, device);
+    r.workspace = work.data_ptr();
+  }
+};
+
+bool scan_tracked(const char* what, PyObject* const* a) {
+  const at::Tensor* t[9];
+  const char* names[9] = {"x", "dt", "a", "b", "c", "d", "z", "dt_bias", "state"};
+  for (int i = 0; i < 9; ++i) t[i] = maybe(what, names[i], a[i < 8 ? i : 10]);
+  return tracked(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], t[8]);
+}
+
+// (x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state) ->
+// (y, last states or None), or None where gradients are asked for
+TB_ENTRY(scan, 12) {
+  const char* what = "selective_scan";
+  if (scan_tracked(what, a)) Py_RETURN_NONE;
+  Scan s(what, a);
+  at::Tensor y = s.rows(), last;
+  if (truth(a[11])) last = s.last();
+  s.r.y = y.data_ptr(), s.r.y_row = s.x.width;
+  s.r.state_out = last.defined() ? (float*)last.data_ptr() : nullptr;
+  s.workspace(false);
+  check(tb_selective_scan(&s.r, stream_of(s.device)));
+  return tuple({wrap(y), wrap(last)});
+}
+
+// (x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, dy, dstate or None)
+// -> (dx, ddt, da, db, dc, dd, dz, ddt_bias, gradient of the first states),
+// None where the input is None
+TB_ENTRY(scan_backward, 13) {
+  const char* what = "selective_scan_backward";
+  const at::Tensor& dy = tensor(what, "dy", a[11]);
+  const at::Tensor* dstate = maybe(what, "dstate", a[12]);
+  if (scan_tracked(what, a) || tracked(&dy, dstate)) refuse_second(what);
+  Scan s(what, a);
+  same(what, "dy", dy, tensor(what, "x", a[0]).sizes(), s.dtype, s.device);
+  const Flat fd(what, "dy", dy);
+  tb_scan_backward_args g{};
+  at::Tensor dstate_copy, dx = s.rows(), ddt = s.rows(), dz, dd, dbias, first,
+                          da = empty({s.x.width, s.states}, at::kFloat, s.device);
+  at::Tensor db = empty(tensor(what, "b", a[3]).sizes(), s.dtype, s.device),
+             dc = empty(tensor(what, "c", a[4]).sizes(), s.dtype, s.device);
+  if (dstate) {
+    const int64_t shape_s[3] = {s.r.grids, s.x.width, s.states};
+    same(what, "dstate", *dstate, shape_s, at::kFloat, s.device);
+    g.dstate_out = (const float*)contiguous(*dstate, dstate_copy);
+  }
+  if (s.d) {
+    dd = empty({s.x.width}, at::kFloat, s.device);
+    g.dd = (float*)dd.data_ptr();
+  }
+  if (s.bias) {
+    dbias = empty({s.x.width}, at::kFloat, s.device);
+    g.ddt_bias = (float*)dbias.data_ptr();
+  }
+  if (a[6] != Py_None) {
+    dz = s.rows();
+    g.dz = dz.data_ptr();
+  }
+  if (a[10] != Py_None) {
+    first = s.last();
+    g.dstate = (float*)first.data_ptr();
+  }
+  s.workspace(true);
+  g.f = s.r;
+  g.dy = fd.p, g.dy_row = fd.row;
+  g.dx = dx.data_ptr(), g.ddt = ddt.data_ptr();
+  g.dx_row = g.ddt_row = g.dz_row = s.x.width;
+  g.db = db.data_ptr(), g.dc = dc.data_ptr();
+  g.da = (float*)da.data_ptr();
+  check(tb_selective_scan_backward(&g, stream_of(s.device)));
+  return tuple({wrap(dx), wrap(ddt), wrap(da), wrap(db), wrap(dc), wrap(dd), wrap(dz), wrap(dbias), wrap(first)});
+}
+
+// (x, dt, a, b, c, d, z, dt_bias, softplus, slots or None, state) -> y
+TB_ENTRY(scan_step, 11) {
+  const char* what = "selective_scan_step";
+  const at::Tensor* slots = maybe(what, "slots", a[9]);
+  const at::Tensor& state = tensor(what, "state", a[10]);
+  const ScanRows s(what, a);
+  const int64_t shape_s[3] = {state.dim() == 3 ? state.size(0) : 0, s.x.width, s.states};
+  same(what, "state", state, shape_s, at::kFloat, s.device);
+  if (!state.is_contiguous()) refuse("%s: the states must be contiguous", what);
+  if (scan_tracked(what, a)) refuse("%s: a step in place has no gradient (selective_scan has)", what);
+  tb_scan_step_args r{};
+  s.fill(r);
+  r.softplus = truth(a[8]);
+  at::Tensor slots_copy, y = s.rows();
+  if (slots) {
+    const int64_t shape_n[1] = {s.x.rows};
+    same(what, "slots", *slots, shape_n, at::kInt, s.device);
+    r.slots = (const int32_t*)contiguous(*slots, slots_copy);
+  }
+  r.y = y.data_ptr(), r.y_row = s.x.width;
+  r.state = (float*)state.data_ptr();
+  r.streams = s.x.rows, r.num_slots = shape_s[0];
+  written(state);
+  check(tb_selective_scan_step(&r, stream_of(s.device)));
+  return wrap(y);
+}
+
 // ----------------------------------------------------------- linear attention
 
 struct Linear {
@@ -576,9 +1007,12 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 }
 
 #define TB_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {TB_METHOD(rotary),          TB_METHOD(norm), TB_METHOD(norm_backward), TB_METHOD(linear),
-                           TB_METHOD(linear_backward), TB_METHOD(step), {"set_error", set_error, METH_O, nullptr},
-                           {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {TB_METHOD(rotary),     TB_METHOD(norm),           TB_METHOD(norm_backward),
+                           TB_METHOD(layer_norm), TB_METHOD(layer_norm_backward),
+                           TB_METHOD(conv),       TB_METHOD(conv_backward),  TB_METHOD(conv_step),
+                           TB_METHOD(scan),       TB_METHOD(scan_backward),  TB_METHOD(scan_step),
+                           TB_METHOD(linear),     TB_METHOD(linear_backward), TB_METHOD(step),
+                           {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_seq", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,5 +1,6 @@
 """Sequence operators over voxel tokens: rotary positions, the root-mean-square
-norm, and linear attention with a decay for each head.
+and the layer norm, linear attention with a decay for each head, and the
+selective scan of a state-space model with its short causal convolution.
 
 A model that reads a batch's voxels as sequences holds one row per active voxel
 in the batch's voxel order, grid after grid; ``offsets`` (int64 ``[B + 1]`` on
@@ -7,11 +8,12 @@ the GPU) says where each grid's rows start.  Nothing is padded.  The calls
 marshal pointers, sizes and strides to ``libtb.so`` (C ABI in ``include/tb.h``)
 on torch's current stream; they never wait for the GPU.
 
-Training: ``rotary``, ``rms_norm`` and ``linear_attention`` take part in
-autograd (first derivatives; second ones and forward mode are refused); their
-``*_backward`` calls are public too.  Generation: ``linear_attention_step``
-updates the states in place, one token per stream.  Writes in place raise
-torch's version counters.
+Training: ``rotary``, ``rms_norm``, ``layer_norm``, ``linear_attention``,
+``causal_conv`` and ``selective_scan`` take part in autograd (first
+derivatives; second ones and forward mode are refused); their ``*_backward``
+calls are public too.  Generation: ``linear_attention_step``,
+``causal_conv_step`` and ``selective_scan_step`` update the states in place, one
+token per stream.  Writes in place raise torch's version counters.
 """
 from __future__ import annotations
 
@@ -22,7 +24,10 @@ import os
 from typing import Optional, Sequence, Tuple
 
 __all__ = ["rotary_frequencies", "rotary", "rotary_backward", "rms_norm", "rms_norm_fp8", "rms_norm_backward",
-           "linear_attention", "linear_attention_backward", "linear_attention_step", "linear_attention_status"]
+           "layer_norm", "layer_norm_backward",
+           "linear_attention", "linear_attention_backward", "linear_attention_step", "linear_attention_status",
+           "causal_conv", "causal_conv_backward", "causal_conv_step",
+           "selective_scan", "selective_scan_backward", "selective_scan_step"]
 
 
 class _Native:
@@ -161,7 +166,51 @@ def _functions():
                                                         ctx.needs_input_grad[5])
             return dq, dk, dv, None, None, first, None, None
 
-    return Rotary, Norm, Linear
+    class LayerNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, residual, eps):
+            y, h = _native.layer_norm(x, weight, bias, residual, eps)
+            ctx.save_for_backward(h, weight)
+            ctx.eps, ctx.biased, ctx.added = eps, bias is not None, residual is not None
+            return (y, h) if residual is not None else y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy, dh=None):
+            h, weight = ctx.saved_tensors
+            dx, dw, db = _native.layer_norm_backward(dy, h, weight, dh, ctx.eps)
+            return dx, dw, db if ctx.biased else None, dx if ctx.added else None, None
+
+    class Conv(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, offsets, state, activation, return_state):
+            ctx.save_for_backward(x, weight, bias, offsets, state)
+            ctx.activation = activation
+            y, last = _native.conv(x, weight, bias, offsets, state, activation, return_state)
+            return (y, last) if return_state else y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy, dstate=None):
+            dx, dw, db, first = _native.conv_backward(dy, *ctx.saved_tensors, ctx.activation, dstate)
+            return dx, dw, db, None, first, None, None
+
+    class Scan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state):
+            ctx.save_for_backward(x, dt, a, b, c, d, z, dt_bias, offsets, state)
+            ctx.softplus = softplus
+            y, last = _native.scan(x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state)
+            return (y, last) if return_state else y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy, dstate=None):
+            *rows, offsets, state = ctx.saved_tensors
+            *grads, first = _native.scan_backward(*rows, ctx.softplus, offsets, state, dy, dstate)
+            return (*grads, None, None, first, None)
+
+    return Rotary, Norm, Linear, LayerNorm, Conv, Scan
 
 
 def rotary(q, k, positions, frequencies, layout: str = "half", sections: Optional[Sequence[int]] = None,
@@ -228,6 +277,29 @@ def rms_norm_backward(dy, h, weight, dh=None, eps: float = 1e-6, stream=None):
     return _native.norm_backward(dy, h, weight, dh, eps)
 
 
+def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, stream=None):
+    """``h = x + residual`` and ``y = (h - mean(h)) / sqrt(var(h) + eps) *
+    weight + bias`` over the last dimension, var the mean of (h - mean(h)) ** 2;
+    returns (y, h).  Without a residual h is x.  The sum is held in 32 bits: y
+    is computed from it before h is rounded."""
+    if stream is not None:
+        return _on_stream(layer_norm, stream, x, weight, bias, residual, eps)
+    out = _native.layer_norm(x, weight, bias, residual, eps)
+    if out is not None:
+        return out
+    out = _functions()[3].apply(x, weight, bias, residual, eps)
+    return out if residual is not None else (out, x)
+
+
+def layer_norm_backward(dy, h, weight, dh=None, eps: float = 1e-5, stream=None):
+    """Gradients (dx, dweight, dbias) of ``layer_norm`` from dy and, where the
+    residual stream goes on, from h's own gradient ``dh``; h as the forward call
+    returned it.  dx is the gradient of both x and the residual."""
+    if stream is not None:
+        return _on_stream(layer_norm_backward, stream, dy, h, weight, dh, eps)
+    return _native.layer_norm_backward(dy, h, weight, dh, eps)
+
+
 # -------------------------------------------------------------------------------------------------- linear attention
 
 def linear_attention(q, k, v, decay, offsets=None, state=None, scale: Optional[float] = None,
@@ -278,3 +350,90 @@ def linear_attention_status(stream=None):
     status = lib().tb_linear_attention_status(ctypes.c_void_p(_stream(stream)))
     if status:
         raise TBError(status, lib().tb_last_error().decode())
+
+
+# ------------------------------------------------------------------------------------------------------- state space
+
+def causal_conv(x, weight, bias=None, offsets=None, state=None, activation: Optional[str] = "silu",
+                return_state: bool = False, stream=None):
+    """Short causal convolution of every channel over the rows of each grid:
+    ``y_t = act(bias + sum_j weight[:, j] * x_(t - W + 1 + j))`` with x ``[T,
+    C]``, weight ``[C, W]``, 2 to 4 taps, and bias ``[C]`` of one type, offsets
+    int64 ``[B + 1]``, not decreasing (None: one grid).  ``activation``: "silu"
+    or None.  ``state``: ``[B, W - 1, C]`` of the same type, the rows before each
+    grid's first, oldest first (None: zeros).  Rows before the first offset or
+    past the last belong to no grid: their outputs and gradients are zeros.
+    Returns (y, last states or None); the last states are the last W - 1 rows of
+    state and grid together."""
+    if stream is not None:
+        return _on_stream(causal_conv, stream, x, weight, bias, offsets, state, activation, return_state)
+    out = _native.conv(x, weight, bias, offsets, state, activation, return_state)
+    if out is not None:
+        return out
+    out = _functions()[4].apply(x, weight, bias, offsets, state, activation, return_state)
+    return out if return_state else (out, None)
+
+
+def causal_conv_backward(dy, x, weight, bias=None, offsets=None, state=None, activation: Optional[str] = "silu",
+                         dstate=None, stream=None):
+    """Gradients (dx, dweight, dbias, dstate0) of ``causal_conv`` from dy and,
+    where the last states were used, from their gradient ``dstate``.  dbias and
+    dstate0 are None where bias and state are."""
+    if stream is not None:
+        return _on_stream(causal_conv_backward, stream, dy, x, weight, bias, offsets, state, activation, dstate)
+    return _native.conv_backward(dy, x, weight, bias, offsets, state, activation, dstate)
+
+
+def causal_conv_step(x, weight, state, bias=None, slots=None, activation: Optional[str] = "silu", stream=None):
+    """One row for each of N streams: x ``[N, C]``.  ``state``: ``[S, W - 1, C]``
+    of x's type, updated in place (the oldest row leaves, x enters); stream n
+    uses the state of slot n, or of ``slots[n]`` (int32 [N]; a slot outside the
+    states, such as -1, is left out and gives zeros; no two streams may share
+    one).  Returns y ``[N, C]``."""
+    if stream is not None:
+        return _on_stream(causal_conv_step, stream, x, weight, state, bias, slots, activation)
+    return _native.conv_step(x, weight, state, bias, slots, activation)
+
+
+def selective_scan(x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus: bool = True, offsets=None, state=None,
+                   return_state: bool = False, stream=None):
+    """The scan of a selective state-space model over the rows of each grid:
+    ``delta_t = softplus(dt_t + dt_bias)``, ``h_t = exp(delta_t * a) * h_(t-1) +
+    delta_t * x_t * b_t``, ``y_t = (c_t . h_t + d * x_t) * silu(z_t)``.  x, dt, z
+    ``[T, C]`` and b, c ``[T, G, N]`` (or ``[T, N]``) of one type, C / G
+    consecutive channels to a group; a ``[C, N]``, d and dt_bias ``[C]`` float32;
+    N <= 256.  z None: no gate.  ``softplus`` False: delta is dt + dt_bias
+    itself.  offsets int64 ``[B + 1]``, not decreasing (None: one grid).  Rows
+    before the first offset or past the last belong to no grid: their outputs and
+    gradients are zeros.  ``state``: float32 ``[B, C, N]`` states to start from
+    (None: zero).  Returns (y, last states or None)."""
+    if stream is not None:
+        return _on_stream(selective_scan, stream, x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state)
+    out = _native.scan(x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state)
+    if out is not None:
+        return out
+    out = _functions()[5].apply(x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, return_state)
+    return out if return_state else (out, None)
+
+
+def selective_scan_backward(dy, x, dt, a, b, c, d=None, z=None, dt_bias=None, softplus: bool = True, offsets=None,
+                            state=None, dstate=None, stream=None):
+    """Gradients (dx, ddt, da, db, dc, dd, dz, ddt_bias, dstate0) of
+    ``selective_scan`` from dy and, where the last states were used, from their
+    gradient ``dstate``; None for inputs that are None."""
+    if stream is not None:
+        return _on_stream(selective_scan_backward, stream, dy, x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state,
+                          dstate)
+    return _native.scan_backward(x, dt, a, b, c, d, z, dt_bias, softplus, offsets, state, dy, dstate)
+
+
+def selective_scan_step(x, dt, a, b, c, state, d=None, z=None, dt_bias=None, softplus: bool = True, slots=None,
+                        stream=None):
+    """One token for each of N streams: rows as ``selective_scan`` takes them.
+    ``state``: float32 ``[S, C, N]``, updated in place; stream n uses the state
+    of slot n, or of ``slots[n]`` (int32 [N]; a slot outside the states, such as
+    -1, is left out and gives zeros; no two streams may share one).  Returns y
+    ``[N, C]``."""
+    if stream is not None:
+        return _on_stream(selective_scan_step, stream, x, dt, a, b, c, state, d, z, dt_bias, softplus, slots)
+    return _native.scan_step(x, dt, a, b, c, d, z, dt_bias, softplus, slots, state)
