@@ -20,13 +20,13 @@ template <class T, int NN, bool kOut>
 struct alignas(16) WalkShared {
   T raw[2][kOut ? 3 : 2][kScanRows][kScanChannels];  // x, dt, z of two tiles
   float delta[kScanRows][kScanChannels], dx[kScanRows][kScanChannels];
-  float b[kScanRows][4 * NN], c[kOut ? kScanRows : 1][4 * NN];
+  Two b[kScanRows][4 * NN], c[kOut ? kScanRows : 1][4 * NN];
   float part[kOut ? kScanRows : 1][4][kScanChannels];  // c . h over a lane's states
 };
 
 // kOut: the outputs from the states that the segments start from; else the
 // segments' own states from zero and their sums of delta.  kMany: more states
-// than a pass takes; those of a tile wait in shared memory (h, after the warps'
+// than a pass takes; those of a tile wait in shared memory (after the warps'
 // own part) while the others' pass.
 template <class T, int NN, bool kOut, bool kMany>
 __global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
@@ -35,10 +35,10 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
   if (kOut) wait_for_last_kernel();
   let_next_kernel_start();
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4;
   Shared& s = reinterpret_cast<Shared*>(s_raw)[warp];
-  const int blocks = l.pad / (4 * NN);  // of states
-  float* s_h = reinterpret_cast<float*>(s_raw + kWarps * sizeof(Shared)) + (int64_t)warp * blocks * 16 * NN * 8;
+  const int blocks = kMany ? l.pad / (4 * NN) : 1;  // of states
+  float* s_h = reinterpret_cast<float*>(s_raw + kWarps * sizeof(Shared)) + (int64_t)warp * blocks * 128 * NN;
   const int slot = (int)(blockIdx.x / l.blocks_x), at = (int)(blockIdx.x % l.blocks_x) * kWarps + warp;
   const ScanTile t = scan_tile(l, at / l.group_tiles, at % l.group_tiles);
   if (t.group >= a.groups) return;
@@ -47,42 +47,21 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
   if (seg.grid < 0 || (!kOut && seg.index + 1 == seg.count)) return;  // the last segment's own state joins no other
   const int64_t row0 = seg.begin + seg.first, state_at = (int64_t)seg.grid * a.channels * a.states;
   float* const own = l.seg + (int64_t)slot * a.channels * l.pad;
-  float h[4][NN], a2[4][NN];
-  auto load_a = [&](int n0) {
-    read_dense<NN>(a2, a.a, t, a.states, n0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int n = 0; n < NN; ++n) a2[i][n] *= kLog2e;
-  };
+  Two h[2][NN] = {}, a2[2][NN];
   auto first = [&](int n0) {
     if (kOut && l.segment) read_pad<NN>(h, own, t, l.pad, n0);
-    else read_dense<NN>(h, kOut && a.state ? a.state + state_at : nullptr, t, a.states, n0);
-  };
-  auto kept = [&](int k) { return reinterpret_cast<float4*>(s_h + k * 16 * NN * 8) + lane; };  // NN vectors, 32 apart
-  auto put = [&](int k) {
-#pragma unroll
-    for (int n = 0; n < NN; ++n) kept(k)[32 * n] = make_float4(h[0][n], h[1][n], h[2][n], h[3][n]);
-  };
-  auto get = [&](int k) {
-#pragma unroll
-    for (int n = 0; n < NN; ++n) {
-      const float4 v = kept(k)[32 * n];
-      h[0][n] = v.x, h[1][n] = v.y, h[2][n] = v.z, h[3][n] = v.w;
-    }
+    else if (kOut) read_dense<NN>(h, a.state ? a.state + state_at : nullptr, t, a.states, n0);
   };
   if (kMany) {
     for (int k = 0; k < blocks; ++k) {
       first(k * 4 * NN);
-      put(k);
+      keep_states<NN>(s_h + k * 128 * NN, h);
     }
   } else {
-    load_a(0);
+    read_rates<NN>(a2, a, t, 0);
     first(0);
   }
-  const bool here = lane < t.count;
-  const float bias = here && a.dt_bias ? a.dt_bias[t.first + lane] : 0.f;
-  const float skip = kOut && here && a.d ? a.d[t.first + lane] : 0.f;
+  const Two bias = channel_pair(a.dt_bias, t), skip = channel_pair(kOut ? a.d : nullptr, t);
   const int tiles = (seg.len + kScanRows - 1) / kScanRows;
   auto fetch = [&](int i) {
     const int n = min(kScanRows, seg.len - i * kScanRows);
@@ -96,15 +75,19 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
     }
     scan_fetched();
   };
-  ScanStates<T, NN> nb, nc;
+  ScanStates<T, NN> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, 0), nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, 0);
   auto load_states = [&](int i, int n0) {
-    const int64_t row = row0 + (int64_t)i * kScanRows;
     const int n = min(kScanRows, seg.len - i * kScanRows);
-    nb.load(a.b, a.b_row, t.group * a.b_group, row, n, a.states, n0);
-    if (kOut) nc.load(a.c, a.c_row, t.group * a.c_group, row, n, a.states, n0);
+    if (kMany) {
+      nb = ScanStates<T, NN>(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0);
+      if (kOut) nc = ScanStates<T, NN>(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+    }
+    nb.load(i * kScanRows, n);
+    if (kOut) nc.load(i * kScanRows, n);
   };
+  PairOut<T> out(a.y, a.y_row, row0, t);
   const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
-  float total = 0.f;
+  Two total = 0;
   fetch(0);
   load_states(0, 0);
   for (int i = 0; i < tiles; ++i) {
@@ -113,75 +96,72 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
     scan_wait<1>();
     auto& raw = s.raw[i & 1];
 #pragma unroll
-    for (int r = 0; r < kScanRows; ++r) {
-      const float v = RowType<T>::to(raw[1][r][lane]) + bias;
-      const float delta = r < n ? (a.softplus ? scan_softplus(v) : v) : 0.f;
-      total += delta;
-      s.delta[r][lane] = delta;
-      s.dx[r][lane] = delta * RowType<T>::to(raw[0][r][lane]);
+    for (int r = o; r < kScanRows; r += 2) {
+      Two delta = scan_step_of(row_pair<T>(raw[1][r]), bias, a.softplus);
+      if (r >= n) delta = 0;
+      total = add2(total, delta);
+      pair_of(s.delta[r]) = delta;
+      pair_of(s.dx[r]) = mul2(delta, row_pair<T>(raw[0][r]));
     }
-    for (int k = 0; k < (kMany ? blocks : 1); ++k) {
-      nb.store(&s.b[0][0]);
-      if (kOut) nc.store(&s.c[0][0]);
+    for (int k = 0; k < blocks; ++k) {
+      nb.store(s.b);
+      if constexpr (kOut) nc.store(s.c);
       __syncwarp();
       if (kMany) {
-        load_a(k * 4 * NN);
-        get(k);
-        if (k + 1 < blocks) load_states(i, (k + 1) * 4 * NN);
-        else load_states(i + 1, 0);
-      } else {
-        load_states(i + 1, 0);
+        read_rates<NN>(a2, a, t, k * 4 * NN);
+        kept_states<NN>(h, s_h + k * 128 * NN);
       }
+      if (kMany && k + 1 < blocks) load_states(i, (k + 1) * 4 * NN);
+      else load_states(i + 1, 0);
 #pragma unroll
       for (int r = 0; r < kScanRows; ++r) {
-        float d[4], x[4], b[NN], c[NN], y[4] = {};
-        read_channels(d, &s.delta[r][c4]);
-        read_channels(x, &s.dx[r][c4]);
-        read_states<NN>(b, &s.b[r][s4]);
-        if (kOut) read_states<NN>(c, &s.c[r][s4]);
+        Two d[2], x[2], b[NN], c[NN], y[2] = {};
+        read_pairs<2>(d, &s.delta[r][c4]);
+        read_pairs<2>(x, &s.dx[r][c4]);
+        read_pairs<NN>(b, &s.b[r][s4]);
+        if constexpr (kOut) read_pairs<NN>(c, &s.c[r][s4]);
 #pragma unroll
         for (int n = 0; n < NN; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[j][n] = fmaf(scan_decay(d[j], a2[j][n]), h[j][n], x[j] * b[n]);
-            if (kOut) y[j] = fmaf(c[n], h[j][n], y[j]);
+          for (int j = 0; j < 2; ++j) {
+            h[j][n] = fma2(scan_decay(d[j], a2[j][n]), h[j][n], mul2(x[j], b[n]));
+            if (kOut) y[j] = n ? fma2(c[n], h[j][n], y[j]) : mul2(c[n], h[j][n]);
           }
         if constexpr (kOut) {
           float* to = &s.part[r][lane % 4][c4];
           if (kMany && k) {
-            float f[4];
-            read_channels(f, to);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] += f[j];
+            Two f[2];
+            read_pairs<2>(f, to);
+            y[0] = add2(y[0], f[0]), y[1] = add2(y[1], f[1]);
           }
-          write_channels(to, y);
+          write_pairs(to, y);
         }
       }
-      if (kMany) put(k);
+      if (kMany) keep_states<NN>(s_h + k * 128 * NN, h);
       __syncwarp();
     }
     if constexpr (kOut) {
-      T* to = (T*)a.y + (row0 + (int64_t)i * kScanRows) * a.y_row + t.first + lane;
 #pragma unroll
-      for (int r = 0; r < kScanRows; ++r) {
-        float y = (s.part[r][0][lane] + s.part[r][1][lane]) + (s.part[r][2][lane] + s.part[r][3][lane]);
-        y = fmaf(skip, RowType<T>::to(raw[0][r][lane]), y);
+      for (int r = o; r < kScanRows; r += 2) {
+        Two y = add2(add2(pair_of(s.part[r][0]), pair_of(s.part[r][1])), add2(pair_of(s.part[r][2]), pair_of(s.part[r][3])));
+        y = fma2(skip, row_pair<T>(raw[0][r]), y);
         if (a.z) {
-          const float z = RowType<T>::to(raw[2][r][lane]);
-          y *= z * scan_sigmoid(z);
+          const Two z = row_pair<T>(raw[2][r]);
+          y = mul2(y, mul2(z, scan_sigmoid(z)));
         }
-        if (here && r < n) to[r * a.y_row] = RowType<T>::from(y);
+        if (r < n) out.put(r, y);
       }
+      out.at += kScanRows * out.stride;
       __syncwarp();
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  for (int k = 0; k < (kMany ? blocks : 1); ++k) {
-    if (kMany) get(k);
+  for (int k = 0; k < blocks; ++k) {
+    if (kMany) kept_states<NN>(h, s_h + k * 128 * NN);
     if (!kOut) write_pad<NN>(own, h, t, l.pad, k * 4 * NN);
     else if (a.state_out && seg.index + 1 == seg.count) write_dense<NN>(a.state_out + state_at, h, t, a.states, k * 4 * NN);
   }
-  if (!kOut && here) l.sum[(int64_t)slot * a.channels + t.first + lane] = total;
+  if (!kOut) scan_put_sum(l, slot, t, total);
 }
 
 // Joins the segments: the state that each one starts from, in place of its own.
@@ -288,7 +268,7 @@ __global__ void __launch_bounds__(128) k_scan_step(ScanStepLaunch l) {
 template <class T, int NN, bool kOut, bool kMany>
 cudaError_t go(const ScanLaunch& l, cudaStream_t s) {
   size_t bytes = kWarps * sizeof(WalkShared<T, NN, kOut>);
-  if (kMany) bytes += (size_t)kWarps * (l.pad / (4 * NN)) * 16 * NN * 8 * sizeof(float);
+  if (kMany) bytes += (size_t)kWarps * (l.pad / (4 * NN)) * 128 * NN * sizeof(float);
   static std::atomic<bool> ready[kMaxDevices];
   const cudaError_t e = allow_shared(k_scan<T, NN, kOut, kMany>, 227 * 1024, ready);
   if (e != cudaSuccess) return e;

@@ -4,11 +4,17 @@
 // A warp walks down the rows of a tile of 32 channels (kScanChannels) and 4 NN
 // states.  Lane l holds channels 4 (l / 4) .. + 4 and states NN (l % 4) .. + NN
 // of it, 4 NN numbers, so that a row costs it one 16-byte read each of delta
-// and delta x (of its channels) and one or two of b and c (of its states) for 4
-// NN updates of h; a sum over the states is one over its own and 4 lanes, a sum
+// and delta x (of its channels) and a few of b and c (of its states) for 4 NN
+// updates of h; a sum over the states is one over its own and 4 lanes, a sum
 // over the channels one over its own and 8 lanes.  Both go through shared
 // memory: a lane writes its own sums, and the lane of a channel (or state)
 // reads and adds what belongs to it.
+//
+// The walks are bound by the instructions that a multiprocessor issues, so
+// numbers go in pairs of neighbouring channels, two to an instruction
+// (fma.rn.f32x2); b and c lie in shared memory as pairs of one number twice.
+// What belongs to a row and a channel (steps, gates, outputs) is done by 16
+// lanes for a row's 32 channels, two rows at a time.
 #pragma once
 
 #include "tb_linattn.cuh"
@@ -19,9 +25,46 @@ namespace tb {
 constexpr int kScanRows = 8;  // of a tile in shared memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// ------------------------------------------------------------ pairs of numbers
+
+typedef unsigned long long Two;
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 parts(Two x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two both(float x) { return two(x, x); }
+
+// --------------------------------------------------------- functions of a step
+
 __device__ __forceinline__ float scan_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float scan_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // exp(delta a) for a2 = a log2(e).  The instruction rounds towards zero: over
@@ -29,26 +72,39 @@ __device__ __forceinline__ float scan_ex2(float x) {
 // many decays that a slow state goes through would add up.  2^-25 more in the
 // exponent takes most of that back, and costs nothing as a sum.
 __device__ __forceinline__ float scan_decay(float delta, float a2) { return scan_ex2(fmaf(delta, a2, 0x1p-25f)); }
+__device__ __forceinline__ Two scan_decay(Two delta, Two a2) {
+  const float2 x = parts(fma2(delta, a2, both(0x1p-25f)));
+  return two(scan_ex2(x.x), scan_ex2(x.y));
+}
 
 // log(1 + exp(v)) = max(v, 0) + log(1 + u), u = exp(-|v|), and log(1 + u) = 2
-// artanh(s), s = u / (2 + u) <= 1/3, by its series: small steps keep their
-// relative accuracy.  exp(-|v|) gets the rest of the product with log2(e) back.
-__device__ __forceinline__ float scan_softplus(float v) {
-  const float m = -fabsf(v), e = m * kLog2e;
-  const float rest = fmaf(m, kLog2e, -e) + m * 1.9259629e-8f;  // log2(e) in 32 bits is short of this
-  float u = scan_ex2(e);
-  u = fmaf(u, rest * kLn2, u);
-  if (v != v || e < -1e30f) u = scan_ex2(e);  // infinite: the rest is no number
-  const float s = __fdividef(u, 2.f + u), q = s * s;
-  float p = 1.f / 13.f;
-  p = fmaf(p, q, 1.f / 11.f);
-  p = fmaf(p, q, 1.f / 9.f);
-  p = fmaf(p, q, 1.f / 7.f);
-  p = fmaf(p, q, 1.f / 5.f);
-  p = fmaf(p, q, 1.f / 3.f);
-  return fmaxf(v, 0.f) + 2.f * fmaf(s * q, p, s);
+// artanh(s), s = u / (2 + u) <= 1/3: small steps keep their relative accuracy.
+// artanh(s) = s + s q P(q), q = s^2, with P of degree 3 fitted to its series on
+// [0, 1/9]: 6e-9 off at most.
+__device__ __forceinline__ Two scan_softplus(Two v) {
+  const float2 f = parts(v);
+  const Two e = mul2(two(-fabsf(f.x), -fabsf(f.y)), both(kLog2e));
+  const float2 g = parts(e);
+  const Two u = two(scan_ex2(g.x), scan_ex2(g.y));
+  const float2 w = parts(add2(u, both(2.f)));
+  const Two s = mul2(u, two(scan_rcp(w.x), scan_rcp(w.y))), q = mul2(s, s);
+  Two p = fma2(both(0.14005993f), q, both(0.14000903f));
+  p = fma2(p, q, both(0.20010763f));
+  p = fma2(p, q, both(0.3333321f));
+  const Two l = fma2(mul2(p, q), s, s);
+  return fma2(both(2.f), l, two(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
 }
-__device__ __forceinline__ float scan_sigmoid(float v) { return __fdividef(1.f, 1.f + scan_ex2(-v * kLog2e)); }
+__device__ __forceinline__ float scan_softplus(float v) { return parts(scan_softplus(both(v))).x; }
+
+// At the ends of the range the exponential is 0 or infinite and the quotient 1 or 0.
+__device__ __forceinline__ float scan_sigmoid(float v) { return scan_rcp(1.f + scan_ex2(-v * kLog2e)); }
+__device__ __forceinline__ Two scan_sigmoid(Two v) {
+  const float2 e = parts(mul2(v, both(-kLog2e)));
+  const float2 w = parts(add2(two(scan_ex2(e.x), scan_ex2(e.y)), both(1.f)));
+  return two(scan_rcp(w.x), scan_rcp(w.y));
+}
+
+// ------------------------------------------------------------ rows of a tile
 
 __device__ __forceinline__ void copy_row(void* dst, const void* src, int bytes) {  // 16 bytes, zeros past `bytes`
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes)
@@ -90,84 +146,199 @@ __device__ __forceinline__ void scan_wait() {
   __syncwarp();
 }
 
+// The two channels of a lane in what is done by rows and channels: 2 (lane %
+// 16), of row lane / 16 of two.
+template <class T>
+__device__ __forceinline__ Two row_pair(const T (&row)[kScanChannels]) {
+  const int p = threadIdx.x & 15;
+  if constexpr (sizeof(T) == 4) {
+    return reinterpret_cast<const Two*>(row)[p];
+  } else {
+    const float2 f = halves_of(reinterpret_cast<const uint32_t*>(row)[p], T());
+    return two(f.x, f.y);
+  }
+}
+__device__ __forceinline__ Two& pair_of(float (&row)[kScanChannels]) { return reinterpret_cast<Two*>(row)[threadIdx.x & 15]; }
+// A vector [channels] in 32 bits, zeros where it is NULL or past the tile.
+__device__ __forceinline__ Two channel_pair(const float* v, const ScanTile& t) {
+  const int c = 2 * (threadIdx.x & 15);
+  return two(v && c < t.count ? v[t.first + c] : 0.f, v && c + 1 < t.count ? v[t.first + c + 1] : 0.f);
+}
+// Writes rows of a tensor by such pairs.
+template <class T>
+struct PairOut {
+  T* at;
+  int64_t stride;
+  int count;   // channels of the lane: 0, 1 or 2
+  bool whole;  // pairs lie on their own size
+  __device__ __forceinline__ PairOut(void* p, int64_t stride, int64_t row, const ScanTile& t)
+      : at((T*)p + row * stride + t.first + 2 * (threadIdx.x & 15)), stride(stride), count(min(t.count - 2 * (int)(threadIdx.x & 15), 2)),
+        whole((uintptr_t)at % (2 * sizeof(T)) == 0 && stride % 2 == 0) {}
+  __device__ __forceinline__ void put(int r, Two v) const {
+    const float2 f = parts(v);
+    T* to = at + r * stride;
+    if (count == 2 && whole) {
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(to) = f;
+      else *reinterpret_cast<uint32_t*>(to) = word_of(f.x, f.y, T());
+    } else {
+      if (count > 0) to[0] = RowType<T>::from(f.x);
+      if (count > 1) to[1] = RowType<T>::from(f.y);
+    }
+  }
+};
+// The steps of a row's channels: dt + bias, or its softplus.
+__device__ __forceinline__ Two scan_step_of(Two dt, Two bias, int softplus) {
+  const Two v = add2(dt, bias);
+  return softplus ? scan_softplus(v) : v;
+}
+
 // Rows of b or c: 4 NN states from n0 on, elements 32 apart of kScanRows x 4 NN.
 template <class T, int NN>
 struct ScanStates {
-  static constexpr int kStates = 4 * NN, kEach = kScanRows * kStates / 32;
-  float f[kEach];
-  __device__ __forceinline__ void load(const void* src, int64_t stride, int64_t group, int64_t row, int n, int states, int n0) {
-    const int lane = threadIdx.x & 31, s = lane % kStates;
-    const T* from = (const T*)src + group + n0 + s;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int r = lane / kStates + i * (32 / kStates);
-      f[i] = r < n && n0 + s < states ? RowType<T>::to(from[(row + r) * stride]) : 0.f;
-    }
+  static constexpr int kStates = 4 * NN, kEach = kScanRows * kStates / 32, kStep = 32 / kStates;
+  const T* from;  // the lane's state of row lane / kStates of the first tile
+  int64_t stride;
+  bool is;
+  T f[kEach];
+  __device__ __forceinline__ ScanStates(const void* src, int64_t stride, int64_t group, int64_t row0, int states, int n0)
+      : stride(stride) {
+    const int lane = threadIdx.x & 31;
+    is = n0 + lane % kStates < states;
+    from = (const T*)src + group + n0 + lane % kStates + (row0 + lane / kStates) * stride;
   }
-  __device__ __forceinline__ void store(float* dst) const {  // [kScanRows][kStates]
+  __device__ __forceinline__ void load(int row, int n) {  // rows [row, row + n) after row0
+    const int r = (threadIdx.x & 31) / kStates;
+    const T* at = from + row * stride;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i, at += kStep * stride) f[i] = is && r + i * kStep < n ? *at : RowType<T>::from(0.f);
+  }
+  __device__ __forceinline__ void store(Two (&dst)[kScanRows][kStates]) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) dst[lane + 32 * i] = f[i];
+    for (int i = 0; i < kEach; ++i) (&dst[0][0])[lane + 32 * i] = both(RowType<T>::to(f[i]));
   }
 };
 
-template <int NN>
-__device__ __forceinline__ void read_states(float (&f)[NN], const float* at) {
-  if constexpr (NN == 4) {
-    const float4 v = *reinterpret_cast<const float4*>(at);
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-  } else {
-    const float2 v = *reinterpret_cast<const float2*>(at);
-    f[0] = v.x, f[1] = v.y;
+// N pairs that lie on 16 bytes.
+template <int N>
+__device__ __forceinline__ void read_pairs(Two (&f)[N], const void* at) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(at)[i / 2];
+    f[i] = v.x, f[i + 1] = v.y;
   }
 }
-__device__ __forceinline__ void read_channels(float (&f)[4], const float* at) { read_states<4>(f, at); }
-__device__ __forceinline__ void write_channels(float* at, const float (&f)[4]) {
-  *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]);
+__device__ __forceinline__ void write_pairs(void* at, const Two (&f)[2]) {
+  *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f[0], f[1]);
 }
 
-// A lane's numbers of a [.., channels, pad] array of the workspace: 16 or 8
-// bytes for each of its channels.
+// -------------------------------------------------- states outside a kernel
+//
+// A lane's numbers as h[j][n]: channels 4 (lane / 4) + 2 j and + 1, state n.
+
 template <int NN>
-__device__ __forceinline__ void read_pad(float (&h)[4][NN], const float* at, const ScanTile& t, int pad, int n0) {
-  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
+__device__ __forceinline__ void from_channels(Two (&h)[2][NN], const float (&f)[4][NN]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (c + i < t.count) read_states<NN>(h[i], at + (int64_t)(t.first + c + i) * pad + s);
-    else
-#pragma unroll
-      for (int n = 0; n < NN; ++n) h[i][n] = 0.f;
-  }
+  for (int n = 0; n < NN; ++n) h[0][n] = two(f[0][n], f[1][n]), h[1][n] = two(f[2][n], f[3][n]);
 }
 template <int NN>
-__device__ __forceinline__ void write_pad(float* at, const float (&h)[4][NN], const ScanTile& t, int pad, int n0) {
+__device__ __forceinline__ void to_channels(float (&f)[4][NN], const Two (&h)[2][NN]) {
+#pragma unroll
+  for (int n = 0; n < NN; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 v = parts(h[j][n]);
+      f[2 * j][n] = v.x, f[2 * j + 1][n] = v.y;
+    }
+}
+// Of a [.., channels, pad] array of the workspace: 16 or 8 bytes for each channel.
+template <int NN>
+__device__ __forceinline__ void read_pad(Two (&h)[2][NN], const float* at, const ScanTile& t, int pad, int n0) {
   const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
+  float f[4][NN] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < t.count) {
+      const float* from = at + (int64_t)(t.first + c + i) * pad + s;
+      if constexpr (NN == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(from);
+        f[i][0] = v.x, f[i][1] = v.y, f[i][2] = v.z, f[i][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(from);
+        f[i][0] = v.x, f[i][1] = v.y;
+      }
+    }
+  from_channels<NN>(h, f);
+}
+template <int NN>
+__device__ __forceinline__ void write_pad(float* at, const Two (&h)[2][NN], const ScanTile& t, int pad, int n0) {
+  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
+  float f[4][NN];
+  to_channels<NN>(f, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (c + i < t.count) {
       float* to = at + (int64_t)(t.first + c + i) * pad + s;
-      if constexpr (NN == 4) *reinterpret_cast<float4*>(to) = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
-      else *reinterpret_cast<float2*>(to) = make_float2(h[i][0], h[i][1]);
+      if constexpr (NN == 4) *reinterpret_cast<float4*>(to) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+      else *reinterpret_cast<float2*>(to) = make_float2(f[i][0], f[i][1]);
     }
 }
-// The same of a [channels, states] array, element by element (a is one of them).
+// Of a [channels, states] array, element by element (a is one of them); zeros where it is NULL.
 template <int NN>
-__device__ __forceinline__ void read_dense(float (&h)[4][NN], const float* at, const ScanTile& t, int states, int n0) {
+__device__ __forceinline__ void read_dense(Two (&h)[2][NN], const float* at, const ScanTile& t, int states, int n0) {
   const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
+  float f[4][NN];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int n = 0; n < NN; ++n)
-      h[i][n] = at && c + i < t.count && s + n < states ? at[(int64_t)(t.first + c + i) * states + s + n] : 0.f;
+      f[i][n] = at && c + i < t.count && s + n < states ? at[(int64_t)(t.first + c + i) * states + s + n] : 0.f;
+  from_channels<NN>(h, f);
 }
 template <int NN>
-__device__ __forceinline__ void write_dense(float* at, const float (&h)[4][NN], const ScanTile& t, int states, int n0) {
+__device__ __forceinline__ void write_dense(float* at, const Two (&h)[2][NN], const ScanTile& t, int states, int n0) {
   const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
+  float f[4][NN];
+  to_channels<NN>(f, h);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int n = 0; n < NN; ++n)
-      if (c + i < t.count && s + n < states) at[(int64_t)(t.first + c + i) * states + s + n] = h[i][n];
+      if (c + i < t.count && s + n < states) at[(int64_t)(t.first + c + i) * states + s + n] = f[i][n];
+}
+// a log2(e) of a lane.
+template <int NN>
+__device__ __forceinline__ void read_rates(Two (&a2)[2][NN], const tb_scan_args& a, const ScanTile& t, int n0) {
+  read_dense<NN>(a2, a.a, t, a.states, n0);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int n = 0; n < NN; ++n) a2[j][n] = mul2(a2[j][n], both(kLog2e));
+}
+
+// A lane's numbers in shared memory, 128 NN floats a warp.
+template <int NN>
+__device__ __forceinline__ void keep_states(float* at, const Two (&h)[2][NN]) {
+#pragma unroll
+  for (int n = 0; n < NN; ++n) reinterpret_cast<ulonglong2*>(at)[32 * n + (threadIdx.x & 31)] = make_ulonglong2(h[0][n], h[1][n]);
+}
+template <int NN>
+__device__ __forceinline__ void kept_states(Two (&h)[2][NN], const float* at) {
+#pragma unroll
+  for (int n = 0; n < NN; ++n) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(at)[32 * n + (threadIdx.x & 31)];
+    h[0][n] = v.x, h[1][n] = v.y;
+  }
+}
+
+// A segment's sums of delta, of which each half of the warp has every other row's.
+__device__ __forceinline__ void scan_put_sum(const ScanLaunch& l, int slot, const ScanTile& t, Two total) {
+  total = add2(total, __shfl_xor_sync(0xffffffffu, total, 16));
+  const int lane = threadIdx.x & 31, c = 2 * lane;
+  float* to = l.sum + (int64_t)slot * l.a.channels + t.first + c;
+  const float2 f = parts(total);
+  if (lane < 16 && c < t.count) to[0] = f.x;
+  if (lane < 16 && c + 1 < t.count) to[1] = f.y;
 }
 
 // Zeros for a tile's channels of the rows that no grid has: a slot's share.

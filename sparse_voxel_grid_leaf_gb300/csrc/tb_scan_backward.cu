@@ -29,7 +29,7 @@ template <class T, int NN>
 struct alignas(16) CarryShared {
   T raw[2][3][kScanRows][kScanChannels];  // dt, dy, z of two tiles
   float delta[kScanRows][kScanChannels], ds[kScanRows][kScanChannels];
-  float c[kScanRows][4 * NN];
+  Two c[kScanRows][4 * NN];
 };
 
 // One block of states a warp (blockIdx.y), as the walks are short.
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
   let_next_kernel_start();
   const ScanLaunch& l = g.f;
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4;
   CarryShared<T, NN>& s = reinterpret_cast<CarryShared<T, NN>*>(s_raw)[warp];
   const int slot = (int)(blockIdx.x / l.blocks_x), at = (int)(blockIdx.x % l.blocks_x) * kWarps + warp;
   const int n0 = blockIdx.y * 4 * NN;
@@ -48,14 +48,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
   const LinSegment seg = lin_segment(l, slot);
   if (seg.grid < 0 || (seg.index == 0 && !g.g.dstate)) return;  // the first chunk's goes nowhere else
   const int64_t row0 = seg.begin + seg.first;
-  float h[4][NN] = {}, a2[4][NN];
-  read_dense<NN>(a2, a.a, t, a.states, n0);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int n = 0; n < NN; ++n) a2[j][n] *= kLog2e;
-  const bool here = lane < t.count;
-  const float bias = here && a.dt_bias ? a.dt_bias[t.first + lane] : 0.f;
+  Two h[2][NN] = {}, a2[2][NN], total = 0;
+  read_rates<NN>(a2, a, t, n0);
+  const Two bias = channel_pair(a.dt_bias, t);
   const int tiles = (seg.len + kScanRows - 1) / kScanRows;
   auto fetch = [&](int i) {
     if (i >= 0) {
@@ -68,13 +63,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
     }
     scan_fetched();
   };
-  ScanStates<T, NN> nc;
-  auto load_states = [&](int i) {
-    nc.load(a.c, a.c_row, t.group * a.c_group, row0 + i * kScanRows, i < 0 ? 0 : min(kScanRows, seg.len - i * kScanRows),
-            a.states, n0);
-  };
+  ScanStates<T, NN> nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+  auto load_states = [&](int i) { nc.load(i * kScanRows, i < 0 ? 0 : min(kScanRows, seg.len - i * kScanRows)); };
   const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
-  float total = 0.f;
   fetch(tiles - 1);
   load_states(tiles - 1);
   for (int i = tiles - 1; i >= 0; --i) {
@@ -83,38 +74,37 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
     scan_wait<1>();
     auto& raw = s.raw[i & 1];
 #pragma unroll
-    for (int r = 0; r < kScanRows; ++r) {
-      const float v = RowType<T>::to(raw[0][r][lane]) + bias;
-      float ds = RowType<T>::to(raw[1][r][lane]);
+    for (int r = o; r < kScanRows; r += 2) {
+      Two ds = row_pair<T>(raw[1][r]);
       if (a.z) {
-        const float z = RowType<T>::to(raw[2][r][lane]);
-        ds *= z * scan_sigmoid(z);
+        const Two z = row_pair<T>(raw[2][r]);
+        ds = mul2(ds, mul2(z, scan_sigmoid(z)));
       }
-      const float delta = r < n ? (a.softplus ? scan_softplus(v) : v) : 0.f;
-      total += delta;
-      s.delta[r][lane] = delta;
-      s.ds[r][lane] = r < n ? ds : 0.f;
+      Two delta = scan_step_of(row_pair<T>(raw[0][r]), bias, a.softplus);
+      if (r >= n) delta = ds = 0;
+      total = add2(total, delta);
+      pair_of(s.delta[r]) = delta;
+      pair_of(s.ds[r]) = ds;
     }
-    nc.store(&s.c[0][0]);
+    nc.store(s.c);
     __syncwarp();
     load_states(i - 1);
 #pragma unroll
     for (int r = kScanRows - 1; r >= 0; --r) {
-      float d[4], ds[4], c[NN];
-      read_channels(d, &s.delta[r][c4]);
-      read_channels(ds, &s.ds[r][c4]);
-      read_states<NN>(c, &s.c[r][s4]);
+      Two d[2], ds[2], c[NN];
+      read_pairs<2>(d, &s.delta[r][c4]);
+      read_pairs<2>(ds, &s.ds[r][c4]);
+      read_pairs<NN>(c, &s.c[r][s4]);
 #pragma unroll
       for (int n = 0; n < NN; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j][n] = scan_decay(d[j], a2[j][n]) * fmaf(c[n], ds[j], h[j][n]);
+        for (int j = 0; j < 2; ++j) h[j][n] = mul2(scan_decay(d[j], a2[j][n]), fma2(c[n], ds[j], h[j][n]));
     }
     __syncwarp();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   write_pad<NN>(g.seg_back + (int64_t)slot * a.channels * l.pad, h, t, l.pad, n0);
-  // a grid's last chunk has no sum yet
-  if (here && blockIdx.y == 0) l.sum[(int64_t)slot * a.channels + t.first + lane] = total;
+  if (blockIdx.y == 0) scan_put_sum(l, slot, t, total);  // a grid's last chunk has none yet
 }
 
 // Joins what the chunks carry back, from a grid's last chunk to its first: what
@@ -176,11 +166,11 @@ __global__ void __launch_bounds__(128) k_scan_join_back(ScanBackwardLaunch g) {
 
 template <class T, int NN>
 struct alignas(16) BackShared {
-  float kept[kTiles - 1][32 * 4 * NN];  // the states before the tiles but the first
+  float kept[kTiles - 1][128 * NN];  // the states before the tiles but the first
   float delta[kScanRows][kScanChannels], dx[kScanRows][kScanChannels], ds[kScanRows][kScanChannels];
-  float b[kScanRows][4 * NN], c[kScanRows][4 * NN];
+  Two b[kScanRows][4 * NN], c[kScanRows][4 * NN];
   float sums[2][3][4][kScanChannels];  // of two rows: a lane's c . h, g . b, a . q
-  float bc[2][8][8 * NN];              // of two rows: a lane's channels of db, dc
+  float bc[2][2][36 * NN];             // of two rows: a lane's channels of db, dc; on different banks
   T raw[4][kScanRows][kScanChannels];  // x, dt, z, dy
 };
 
@@ -193,26 +183,21 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   let_next_kernel_start();
   const ScanLaunch& l = g.f;
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4, p = lane & 15;
   Shared& s = reinterpret_cast<Shared*>(s_raw)[warp];
-  float(*s_bc)[kScanRows][2 * kStates] = reinterpret_cast<float(*)[kScanRows][2 * kStates]>(s_raw + kWarps * sizeof(Shared));
+  Two(*s_bc)[kScanRows][kStates] = reinterpret_cast<Two(*)[kScanRows][kStates]>(s_raw + kWarps * sizeof(Shared));
   const int per_run = a.groups * g.quads, run = (int)(blockIdx.x / per_run), at = (int)(blockIdx.x % per_run);
   const int group = at / g.quads, quad = at % g.quads;
   const ScanTile t = scan_tile(l, group, quad * kWarps + warp);
-  const bool here = lane < t.count;
-  const int ch = t.first + lane, c4 = lane / 4 * 4, s4 = lane % 4 * NN;
-  const float bias = here && a.dt_bias ? a.dt_bias[ch] : 0.f, skip = here && a.d ? a.d[ch] : 0.f;
-  float sum_d = 0.f, sum_bias = 0.f;
-  const int blocks = l.pad / kStates;
-  for (int k = 0; k < (kMany ? blocks : 1); ++k) {
+  const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
+  const Two bias = channel_pair(a.dt_bias, t), skip = channel_pair(a.d, t);
+  Two sum_d = 0, sum_bias = 0;
+  const int blocks = kMany ? l.pad / kStates : 1;
+  for (int k = 0; k < blocks; ++k) {
     const int n0 = k * kStates;
-    const bool last = !kMany || k + 1 == blocks;
-    float a2[4][NN], da[4][NN] = {};
-    read_dense<NN>(a2, a.a, t, a.states, n0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int n = 0; n < NN; ++n) a2[j][n] *= kLog2e;
+    const bool last = k + 1 == blocks;
+    Two a2[2][NN], da[2][NN] = {};
+    read_rates<NN>(a2, a, t, n0);
     for (int slot = run * g.per_run; slot < min((run + 1) * g.per_run, l.segments); ++slot) {
       if (k == 0) {
         scan_zero_share<T>(l, g.g.dx, g.g.dx_row, slot, t);
@@ -223,11 +208,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
       if (seg.grid < 0 || seg.len == 0) continue;
       const int64_t row0 = seg.begin + seg.first, own = (int64_t)slot * a.channels * l.pad;
       const int tiles = (seg.len + kScanRows - 1) / kScanRows;
-      float h[4][NN];
+      const PairOut<T> out_x(g.g.dx, g.g.dx_row, row0, t), out_dt(g.g.ddt, g.g.ddt_row, row0, t), out_z(g.g.dz, g.g.dz_row, row0, t);
+      ScanStates<T, NN> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0), nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+      Two h[2][NN];
       auto stage = [&](int i, bool all) {
         const int64_t row = row0 + i * kScanRows;
         const int n = min(kScanRows, seg.len - i * kScanRows);
-        ScanStates<T, NN> b, c;
         scan_fetch<T>(&s.raw[0][0][0], a.x, a.x_row, row, n, t, l.vec);
         scan_fetch<T>(&s.raw[1][0][0], a.dt, a.dt_row, row, n, t, l.vec);
         if (all) {
@@ -235,39 +221,39 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           scan_fetch<T>(&s.raw[3][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
         }
         scan_fetched();
-        b.load(a.b, a.b_row, t.group * a.b_group, row, n, a.states, n0);
-        if (all) c.load(a.c, a.c_row, t.group * a.c_group, row, n, a.states, n0);
-        b.store(&s.b[0][0]);
-        if (all) c.store(&s.c[0][0]);
+        nb.load(i * kScanRows, n);
+        if (all) nc.load(i * kScanRows, n);
+        nb.store(s.b);
+        if (all) nc.store(s.c);
         scan_wait<0>();
 #pragma unroll
-        for (int r = 0; r < kScanRows; ++r) {
-          const float v = RowType<T>::to(s.raw[1][r][lane]) + bias;
-          const float delta = r < n ? (a.softplus ? scan_softplus(v) : v) : 0.f;
-          s.delta[r][lane] = delta;
-          s.dx[r][lane] = delta * RowType<T>::to(s.raw[0][r][lane]);
+        for (int r = o; r < kScanRows; r += 2) {
+          Two delta = scan_step_of(row_pair<T>(s.raw[1][r]), bias, a.softplus);
+          if (r >= n) delta = 0;
+          pair_of(s.delta[r]) = delta;
+          pair_of(s.dx[r]) = mul2(delta, row_pair<T>(s.raw[0][r]));
           if (all) {
-            float ds = RowType<T>::to(s.raw[3][r][lane]);
+            Two ds = row_pair<T>(s.raw[3][r]);
             if (a.z) {
-              const float z = RowType<T>::to(s.raw[2][r][lane]);
-              ds *= z * scan_sigmoid(z);
+              const Two z = row_pair<T>(s.raw[2][r]);
+              ds = mul2(ds, mul2(z, scan_sigmoid(z)));
             }
-            s.ds[r][lane] = r < n ? ds : 0.f;
+            pair_of(s.ds[r]) = r < n ? ds : 0;
           }
         }
         __syncwarp();
       };
-      auto forward = [&](int r, float (&e)[4][NN]) {
-        float d[4], x[4], b[NN];
-        read_channels(d, &s.delta[r][c4]);
-        read_channels(x, &s.dx[r][c4]);
-        read_states<NN>(b, &s.b[r][s4]);
+      auto forward = [&](int r, Two (&e)[2][NN]) {
+        Two d[2], x[2], b[NN];
+        read_pairs<2>(d, &s.delta[r][c4]);
+        read_pairs<2>(x, &s.dx[r][c4]);
+        read_pairs<NN>(b, &s.b[r][s4]);
 #pragma unroll
         for (int n = 0; n < NN; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             e[j][n] = scan_decay(d[j], a2[j][n]);
-            h[j][n] = fmaf(e[j][n], h[j][n], x[j] * b[n]);
+            h[j][n] = fma2(e[j][n], h[j][n], mul2(x[j], b[n]));
           }
       };
       read_pad<NN>(h, l.seg + own, t, l.pad, n0);
@@ -275,43 +261,34 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         stage(i, false);
 #pragma unroll
         for (int r = 0; r < kScanRows; ++r) {
-          float e[4][NN];
+          Two e[2][NN];
           forward(r, e);
         }
-#pragma unroll
-        for (int n = 0; n < NN; ++n)
-          reinterpret_cast<float4*>(s.kept[i])[32 * n + lane] = make_float4(h[0][n], h[1][n], h[2][n], h[3][n]);
+        keep_states<NN>(s.kept[i], h);
         __syncwarp();
       }
-      float carry[4][NN];
+      Two carry[2][NN];
       read_pad<NN>(carry, g.seg_back + own, t, l.pad, n0);
       for (int i = tiles - 1; i >= 0; --i) {
         const int rows = min(kScanRows, seg.len - i * kScanRows);
         stage(i, true);
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
-          if (i) {
-#pragma unroll
-            for (int n = 0; n < NN; ++n) {
-              const float4 v = reinterpret_cast<const float4*>(s.kept[i - 1])[32 * n + lane];
-              h[0][n] = v.x, h[1][n] = v.y, h[2][n] = v.z, h[3][n] = v.w;
-            }
-          } else {
-            read_pad<NN>(h, l.seg + own, t, l.pad, n0);
-          }
+          if (i) kept_states<NN>(h, s.kept[i - 1]);
+          else read_pad<NN>(h, l.seg + own, t, l.pad, n0);
           if (half) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              float e[4][NN];
+              Two e[2][NN];
               forward(r, e);
             }
           }
           // the states before four rows and after each, and the rows' decays
-          float hs[5][4][NN], e[4][4][NN];
+          Two hs[5][2][NN], e[4][2][NN];
 #pragma unroll
           for (int r = 0; r <= 4; ++r) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int n = 0; n < NN; ++n) hs[r][j][n] = h[j][n];
             if (r < 4) forward(4 * half + r, e[r]);
@@ -319,89 +296,97 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
           for (int r = 3; r >= 0; --r) {
             const int at_row = 4 * half + r;
-            float d[4], x[4], ds[4], b[NN], c[NN], y[4] = {}, into[4] = {}, qa[4] = {}, db[NN] = {}, dc[NN] = {};
-            read_channels(d, &s.delta[at_row][c4]);
-            read_channels(x, &s.dx[at_row][c4]);
-            read_channels(ds, &s.ds[at_row][c4]);
-            read_states<NN>(b, &s.b[at_row][s4]);
-            read_states<NN>(c, &s.c[at_row][s4]);
-#pragma unroll
-            for (int n = 0; n < NN; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float grad = fmaf(c[n], ds[j], carry[j][n]);
-                y[j] = fmaf(c[n], hs[r + 1][j][n], y[j]);
-                dc[n] = fmaf(ds[j], hs[r + 1][j][n], dc[n]);
-                db[n] = fmaf(grad, x[j], db[n]);
-                into[j] = fmaf(grad, b[n], into[j]);
-                carry[j][n] = grad * e[r][j][n];
-                const float q = carry[j][n] * hs[r][j][n];
-                qa[j] = fmaf(q, a2[j][n], qa[j]);
-                da[j][n] = fmaf(q, d[j], da[j][n]);
-              }
-            write_channels(&s.sums[r & 1][0][lane % 4][c4], y);
-            write_channels(&s.sums[r & 1][1][lane % 4][c4], into);
-            write_channels(&s.sums[r & 1][2][lane % 4][c4], qa);
+            Two d[2], x[2], ds[2], b[NN], c[NN], y[2] = {}, into[2] = {}, qa[2] = {};
+            float db[NN], dc[NN];
+            read_pairs<2>(d, &s.delta[at_row][c4]);
+            read_pairs<2>(x, &s.dx[at_row][c4]);
+            read_pairs<2>(ds, &s.ds[at_row][c4]);
+            read_pairs<NN>(b, &s.b[at_row][s4]);
+            read_pairs<NN>(c, &s.c[at_row][s4]);
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
-              s.bc[r & 1][lane / 4][s4 + n] = db[n];
-              s.bc[r & 1][lane / 4][kStates + s4 + n] = dc[n];
+              Two sum_b = 0, sum_c = 0;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const Two grad = fma2(c[n], ds[j], carry[j][n]);
+                y[j] = n ? fma2(c[n], hs[r + 1][j][n], y[j]) : mul2(c[n], hs[r + 1][j][n]);
+                sum_c = j ? fma2(ds[j], hs[r + 1][j][n], sum_c) : mul2(ds[j], hs[r + 1][j][n]);
+                sum_b = j ? fma2(grad, x[j], sum_b) : mul2(grad, x[j]);
+                into[j] = n ? fma2(grad, b[n], into[j]) : mul2(grad, b[n]);
+                carry[j][n] = mul2(grad, e[r][j][n]);
+                const Two q = mul2(carry[j][n], hs[r][j][n]);
+                qa[j] = n ? fma2(q, a2[j][n], qa[j]) : mul2(q, a2[j][n]);
+                da[j][n] = fma2(q, d[j], da[j][n]);
+              }
+              const float2 fb = parts(sum_b), fc = parts(sum_c);
+              db[n] = fb.x + fb.y;
+              dc[n] = fc.x + fc.y;
+            }
+            write_pairs(&s.sums[r & 1][0][lane % 4][c4], y);
+            write_pairs(&s.sums[r & 1][1][lane % 4][c4], into);
+            write_pairs(&s.sums[r & 1][2][lane % 4][c4], qa);
+#pragma unroll
+            for (int n = 0; n < NN; n += 2) {
+              const int to = lane / 4 * kStates + s4 + n;
+              *reinterpret_cast<float2*>(&s.bc[r & 1][0][to]) = make_float2(db[n], db[n + 1]);
+              *reinterpret_cast<float2*>(&s.bc[r & 1][1][to]) = make_float2(dc[n], dc[n + 1]);
             }
             if (r & 1) continue;
             __syncwarp();
-            // two rows' sums: lanes as channels, then as states of db and dc
+            // the sums of two rows, one each half of the warp: by channels, then by states of db and dc
+            const int rr = at_row + o;
+            Two sum[3];
 #pragma unroll
-            for (int o = 1; o >= 0; --o) {
-              const int rr = at_row + o;
-              float sum[3];
+            for (int v = 0; v < 3; ++v)
+              sum[v] = add2(add2(pair_of(s.sums[o][v][0]), pair_of(s.sums[o][v][1])),
+                            add2(pair_of(s.sums[o][v][2]), pair_of(s.sums[o][v][3])));
+            const int to = i * kScanRows + rr;
+            if (kMany && rr < rows) {
+              float* acc = g.acc + ((row0 + to) * a.channels + t.first + 2 * p) * 3;
 #pragma unroll
-              for (int v = 0; v < 3; ++v)
-                sum[v] = (s.sums[o][v][0][lane] + s.sums[o][v][1][lane]) + (s.sums[o][v][2][lane] + s.sums[o][v][3][lane]);
-              const int64_t row = row0 + i * kScanRows + rr;
-              const bool live = here && rr < rows;
-              if (kMany) {
-                float* acc = g.acc + (row * a.channels + ch) * 3;
-                if (live && k)
+              for (int m = 0; m < 2; ++m)
+                if (2 * p + m < t.count)
 #pragma unroll
-                  for (int v = 0; v < 3; ++v) sum[v] += acc[v];
-                if (live && !last)
-#pragma unroll
-                  for (int v = 0; v < 3; ++v) acc[v] = sum[v];
+                  for (int v = 0; v < 3; ++v) {
+                    float2 f = parts(sum[v]);
+                    float& mine = m ? f.y : f.x;
+                    if (k) mine += acc[3 * m + v];
+                    if (!last) acc[3 * m + v] = mine;
+                    sum[v] = two(f.x, f.y);
+                  }
+            }
+            if (rr < rows && last) {
+              const Two xf = row_pair<T>(s.raw[0][rr]), dsf = pair_of(s.ds[rr]);
+              const Two inner = fma2(skip, xf, sum[0]);
+              Two ddt = fma2(xf, sum[1], mul2(sum[2], both(kLn2)));
+              if (a.softplus) ddt = mul2(ddt, scan_sigmoid(add2(row_pair<T>(s.raw[1][rr]), bias)));
+              out_x.put(to, fma2(skip, dsf, mul2(pair_of(s.delta[rr]), sum[1])));
+              out_dt.put(to, ddt);
+              if (a.z) {
+                const Two z = row_pair<T>(s.raw[2][rr]), sg = scan_sigmoid(z);
+                const Two slope = mul2(sg, fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
+                out_z.put(to, mul2(mul2(row_pair<T>(s.raw[3][rr]), inner), slope));
               }
-              if (live && last) {
-                const float xf = RowType<T>::to(s.raw[0][rr][lane]), dsf = s.ds[rr][lane];
-                const float inner = fmaf(skip, xf, sum[0]);
-                float ddt = fmaf(xf, sum[1], sum[2] * kLn2);
-                if (a.softplus) ddt *= scan_sigmoid(RowType<T>::to(s.raw[1][rr][lane]) + bias);
-                ((T*)g.g.dx)[row * g.g.dx_row + ch] = RowType<T>::from(fmaf(skip, dsf, s.delta[rr][lane] * sum[1]));
-                ((T*)g.g.ddt)[row * g.g.ddt_row + ch] = RowType<T>::from(ddt);
-                if (a.z) {
-                  const float z = RowType<T>::to(s.raw[2][rr][lane]), sg = scan_sigmoid(z);
-                  const float dz = RowType<T>::to(s.raw[3][rr][lane]) * inner * (sg * fmaf(z, 1.f - sg, 1.f));
-                  ((T*)g.g.dz)[row * g.g.dz_row + ch] = RowType<T>::from(dz);
-                }
-                sum_d = fmaf(dsf, xf, sum_d);
-                sum_bias += ddt;
-              }
-              if (2 * kStates == 32 || lane / (2 * kStates) == o) {
-                const int v = lane % (2 * kStates);
-                float f = 0.f;
+              sum_d = fma2(dsf, xf, sum_d);
+              sum_bias = add2(sum_bias, ddt);
+            }
+            if (p < kStates) {
+              const Two* from = reinterpret_cast<const Two*>(&s.bc[o][p / (2 * NN)][0]) + p % (2 * NN);
+              Two f = from[0];
 #pragma unroll
-                for (int m = 0; m < 8; ++m) f += s.bc[o][m][v];
-                s_bc[warp][rr][v] = f;
-              }
+              for (int m = 1; m < 8; ++m) f = add2(f, from[m * 2 * NN]);
+              s_bc[warp][rr][p] = f;
             }
             __syncwarp();
           }
         }
         __syncthreads();
-#pragma unroll
-        for (int v = threadIdx.x; v < kScanRows * 2 * kStates; v += 32 * kWarps) {
-          const int r = v / (2 * kStates), n = v % (2 * kStates);
+        if (threadIdx.x < kScanRows * kStates) {
+          const int r = threadIdx.x / kStates, v = threadIdx.x % kStates;
           if (r < rows) {
-            const float f = (s_bc[0][r][n] + s_bc[1][r][n]) + (s_bc[2][r][n] + s_bc[3][r][n]);
-            const int64_t row = row0 + i * kScanRows + r;
-            g.bc[((((int64_t)quad * l.tokens + row) * a.groups + group) * 2 + n / kStates) * l.pad + n0 + n % kStates] = f;
+            const Two f = add2(add2(s_bc[0][r][v], s_bc[1][r][v]), add2(s_bc[2][r][v], s_bc[3][r][v]));
+            const int64_t row = ((int64_t)quad * l.tokens + row0 + i * kScanRows + r) * a.groups + group;
+            *reinterpret_cast<Two*>(&g.bc[(row * 2 + v / (2 * NN)) * l.pad + n0 + v % (2 * NN) * 2]) = f;
           }
         }
         __syncthreads();
@@ -409,9 +394,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
     }
     write_pad<NN>(g.part_a + (int64_t)run * a.channels * l.pad, da, t, l.pad, n0);
   }
-  if (here) {
-    g.part_d[((int64_t)run * 2) * a.channels + ch] = sum_d;
-    g.part_d[((int64_t)run * 2 + 1) * a.channels + ch] = sum_bias;
+  sum_d = add2(sum_d, __shfl_xor_sync(0xffffffffu, sum_d, 16));
+  sum_bias = add2(sum_bias, __shfl_xor_sync(0xffffffffu, sum_bias, 16));
+  if (o == 0) {
+    const float2 fd = parts(sum_d), fb = parts(sum_bias);
+    float* to = g.part_d + (int64_t)run * 2 * a.channels + t.first + 2 * p;
+    if (2 * p < t.count) to[0] = fd.x, to[a.channels] = fb.x;
+    if (2 * p + 1 < t.count) to[1] = fd.y, to[a.channels + 1] = fb.y;
   }
 }
 
