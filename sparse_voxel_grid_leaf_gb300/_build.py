@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libtb.so")
 SEQ, SEQ_OBJ = os.path.join(HERE, "_seq.so"), os.path.join(BUILD, "tb_seq_py.o")
 SOURCES = ["tb_api.cu", "tb_prepass.cu", "tb_chain.cu", "tb_noalloc.cu", "tb_kmap.cu",
            "tb_seq_api.cu", "tb_rotary.cu", "tb_norm.cu", "tb_linattn.cu",
-           "tb_linattn_chunk.cu", "tb_linattn_split.cu", "tb_conv.cu", "tb_scan.cu", "tb_scan_backward.cu"]
+           "tb_linattn_chunk.cu", "tb_linattn_split.cu", "tb_conv.cu", "tb_scan.cu",
+           "tb_scan_join.cu", "tb_scan_backward.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -13,202 +13,245 @@
 namespace tb {
 namespace {
 
-constexpr int kWarps = 4;  // of a block: neighbouring channels of the same rows
+constexpr int CH = kScanChannels;
 
 // One warp's shared memory.
 template <class T, int NN, bool kOut>
 struct alignas(16) WalkShared {
-  T raw[2][kOut ? 3 : 2][kScanRows][kScanChannels];  // x, dt, z of two tiles
-  float delta[kScanRows][kScanChannels], dx[kScanRows][kScanChannels];
-  Two b[kScanRows][4 * NN], c[kOut ? kScanRows : 1][4 * NN];
-  float part[kOut ? kScanRows : 1][4][kScanChannels];  // c . h over a lane's states
+  T raw[2][kOut ? 3 : 2][kTileRows][CH];  // x, dt, z of two tiles
+  float delta[kTileRows][CH], dx[kTileRows][CH];
+  float b[kTileRows][2 * NN], c[kOut ? kTileRows : 1][2 * NN];
+  float part[kOut ? kTileRows : 1][2][CH];  // c . h over a lane's states
 };
+template <int NN>
+constexpr int kept_floats() { return 32 * 4 * NN; }  // of a warp's states of a pass
 
-// kOut: the outputs from the states that the segments start from; else the
-// segments' own states from zero and their sums of delta.  kMany: more states
-// than a pass takes; those of a tile wait in shared memory (after the warps'
-// own part) while the others' pass.
-template <class T, int NN, bool kOut, bool kMany>
-__global__ void __launch_bounds__(32 * kWarps) k_scan(ScanLaunch l) {
+// What a walk does: the outputs from the states that the segments start from
+// (kOut); the segments' own last states from zero and their sums of delta
+// (kStates); and those before every tile as well, for the gradient (kTiles).
+enum Walk { kOut, kStates, kTiles };
+
+// kMany: more states than a pass takes; those of a tile wait in shared memory
+// (after the warps' own part) while the others' pass.
+template <class T, int NN, Walk kWalk, bool kMany>
+__global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
   extern __shared__ __align__(16) char s_raw[];
-  typedef WalkShared<T, NN, kOut> Shared;
-  if (kOut) wait_for_last_kernel();
+  constexpr bool kGives = kWalk == kOut;
+  typedef WalkShared<T, NN, kGives> Shared;
+  if (kGives) wait_for_last_kernel();
   let_next_kernel_start();
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Shared& s = reinterpret_cast<Shared*>(s_raw)[warp];
-  const int blocks = kMany ? l.pad / (4 * NN) : 1;  // of states
-  float* s_h = reinterpret_cast<float*>(s_raw + kWarps * sizeof(Shared)) + (int64_t)warp * blocks * 128 * NN;
-  const int slot = (int)(blockIdx.x / l.blocks_x), at = (int)(blockIdx.x % l.blocks_x) * kWarps + warp;
-  const ScanTile t = scan_tile(l, at / l.group_tiles, at % l.group_tiles);
+  const int blocks = kMany ? l.pad / (2 * NN) : 1;  // of states
+  float* s_h = reinterpret_cast<float*>(s_raw + l.warps * sizeof(Shared)) + warp * blocks * kept_floats<NN>();
+  const int slot = (int)(blockIdx.x / l.blocks_x), at = (int)(blockIdx.x % l.blocks_x) * l.warps + warp;
+  const ScanTile t = scan_tile<CH>(l, at / l.group_tiles, at % l.group_tiles);
   if (t.group >= a.groups) return;
   const LinSegment seg = lin_segment(l, slot);
-  if (kOut) scan_zero_share<T>(l, a.y, a.y_row, slot, t);
-  if (seg.grid < 0 || (!kOut && seg.index + 1 == seg.count)) return;  // the last segment's own state joins no other
+  if (kGives) scan_zero_share<T, CH>(l, a.y, a.y_row, slot, t);
+  if (seg.grid < 0 || (kWalk == kStates && seg.index + 1 == seg.count)) return;  // the last one's own state joins no other
   const int64_t row0 = seg.begin + seg.first, state_at = (int64_t)seg.grid * a.channels * a.states;
-  float* const own = l.seg + (int64_t)slot * a.channels * l.pad;
-  Two h[2][NN] = {}, a2[2][NN];
+  const int c4 = lane / 2 * 4, s0 = lane % 2 * NN;
+  const int64_t mine = (t.place + c4) * l.pad + s0;  // the lane's place in a slot of the workspace
+  float* const own = l.seg + (int64_t)slot * l.wide * l.pad + mine;
+  Two h[4][NN / 2] = {}, a2[4][NN / 2];
+  auto as_pairs = [&](Two(&p)[4][NN / 2], const float(&f)[4][NN], float by) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < NN; n += 2) p[j][n / 2] = two(f[j][n] * by, f[j][n + 1] * by);
+  };
+  auto rates = [&](int n0) {
+    float f[4][NN];
+    read_dense<NN>(f, a.a, t, a.states, c4, n0 + s0);
+    as_pairs(a2, f, kLog2e);
+  };
   auto first = [&](int n0) {
-    if (kOut && l.segment) read_pad<NN>(h, own, t, l.pad, n0);
-    else if (kOut) read_dense<NN>(h, a.state ? a.state + state_at : nullptr, t, a.states, n0);
+    if (!kGives) return;
+    float f[4][NN];
+    if (l.segment) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], own + n0 + j * l.pad);
+    } else {
+      read_dense<NN>(f, a.state ? a.state + state_at : nullptr, t, a.states, c4, n0 + s0);
+    }
+    as_pairs(h, f, 1.f);
+  };
+  auto write = [&](float* to) {  // in the workspace
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < NN / 2; n += 2) write_pairs(to + j * l.pad + 2 * n, h[j][n], h[j][n + 1]);
+  };
+  auto keep = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < NN; ++i)
+      write_pairs(s_h + k * kept_floats<NN>() + (i * 32 + lane) * 4, h[i * 2 / (NN / 2)][i * 2 % (NN / 2)], h[i * 2 / (NN / 2)][i * 2 % (NN / 2) + 1]);
+  };
+  auto kept = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < NN; ++i) {
+      Two f[2];
+      read_pairs<2>(f, s_h + k * kept_floats<NN>() + (i * 32 + lane) * 4);
+      h[i * 2 / (NN / 2)][i * 2 % (NN / 2)] = f[0], h[i * 2 / (NN / 2)][i * 2 % (NN / 2) + 1] = f[1];
+    }
   };
   if (kMany) {
     for (int k = 0; k < blocks; ++k) {
-      first(k * 4 * NN);
-      keep_states<NN>(s_h + k * 128 * NN, h);
+      first(k * 2 * NN);
+      keep(k);
     }
   } else {
-    read_rates<NN>(a2, a, t, 0);
+    rates(0);
     first(0);
   }
-  const Two bias = channel_pair(a.dt_bias, t), skip = channel_pair(kOut ? a.d : nullptr, t);
-  const int tiles = (seg.len + kScanRows - 1) / kScanRows;
+  const Two bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(kGives ? a.d : nullptr, t);
+  const int tiles = (seg.len + kTileRows - 1) / kTileRows;
   auto fetch = [&](int i) {
-    const int n = min(kScanRows, seg.len - i * kScanRows);
+    const int n = min(kTileRows, seg.len - i * kTileRows);
     if (n > 0) {
-      const int64_t row = row0 + (int64_t)i * kScanRows;
+      const int64_t row = row0 + (int64_t)i * kTileRows;
       auto& raw = s.raw[i & 1];
-      scan_fetch<T>(&raw[0][0][0], a.x, a.x_row, row, n, t, l.vec);
-      scan_fetch<T>(&raw[1][0][0], a.dt, a.dt_row, row, n, t, l.vec);
-      if constexpr (kOut)
-        if (a.z) scan_fetch<T>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
+      scan_fetch<T, CH>(&raw[0][0][0], a.x, a.x_row, row, n, t, l.vec);
+      scan_fetch<T, CH>(&raw[1][0][0], a.dt, a.dt_row, row, n, t, l.vec);
+      if constexpr (kGives)
+        if (a.z) scan_fetch<T, CH>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
     }
-    scan_fetched();
+    copies_on_their_way();
   };
-  ScanStates<T, NN> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, 0), nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, 0);
+  ScanStates<T, 2 * NN> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, 0), nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, 0);
   auto load_states = [&](int i, int n0) {
-    const int n = min(kScanRows, seg.len - i * kScanRows);
+    const int n = min(kTileRows, seg.len - i * kTileRows);
     if (kMany) {
-      nb = ScanStates<T, NN>(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0);
-      if (kOut) nc = ScanStates<T, NN>(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+      nb = ScanStates<T, 2 * NN>(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0);
+      if (kGives) nc = ScanStates<T, 2 * NN>(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
     }
-    nb.load(i * kScanRows, n);
-    if (kOut) nc.load(i * kScanRows, n);
+    nb.load(i * kTileRows, n);
+    if (kGives) nc.load(i * kTileRows, n);
   };
-  PairOut<T> out(a.y, a.y_row, row0, t);
-  const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
+  PairOut<T, CH> out(a.y, a.y_row, row0, t);
   Two total = 0;
   fetch(0);
   load_states(0, 0);
   for (int i = 0; i < tiles; ++i) {
-    const int n = min(kScanRows, seg.len - i * kScanRows);
+    const int n = min(kTileRows, seg.len - i * kTileRows);
     fetch(i + 1);
-    scan_wait<1>();
+    if (kWalk == kTiles && i) {
+      const int64_t tile = (int64_t)slot * (l.segment / kTileRows) + i;
+      if (!kMany) write(l.tile + tile * l.wide * l.pad + mine);
+      *reinterpret_cast<Two*>(l.tile_sum + tile * l.wide + t.place + 2 * lane) = total;
+    }
+    wait_for_copies<1>();
     auto& raw = s.raw[i & 1];
 #pragma unroll
-    for (int r = o; r < kScanRows; r += 2) {
-      Two delta = scan_step_of(row_pair<T>(raw[1][r]), bias, a.softplus);
+    for (int r = 0; r < kTileRows; ++r) {
+      Two delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus);
       if (r >= n) delta = 0;
       total = add2(total, delta);
-      pair_of(s.delta[r]) = delta;
-      pair_of(s.dx[r]) = mul2(delta, row_pair<T>(raw[0][r]));
+      pair_of<CH>(s.delta[r]) = delta;
+      pair_of<CH>(s.dx[r]) = mul2(delta, row_pair<T, CH>(raw[0][r]));
     }
     for (int k = 0; k < blocks; ++k) {
       nb.store(s.b);
-      if constexpr (kOut) nc.store(s.c);
+      if constexpr (kGives) nc.store(s.c);
       __syncwarp();
       if (kMany) {
-        read_rates<NN>(a2, a, t, k * 4 * NN);
-        kept_states<NN>(h, s_h + k * 128 * NN);
+        rates(k * 2 * NN);
+        kept(k);
+        if (kWalk == kTiles && i) write(l.tile + ((int64_t)slot * (l.segment / kTileRows) + i) * l.wide * l.pad + mine + k * 2 * NN);
       }
-      if (kMany && k + 1 < blocks) load_states(i, (k + 1) * 4 * NN);
+      if (kMany && k + 1 < blocks) load_states(i, (k + 1) * 2 * NN);
       else load_states(i + 1, 0);
 #pragma unroll
-      for (int r = 0; r < kScanRows; ++r) {
-        Two d[2], x[2], b[NN], c[NN], y[2] = {};
-        read_pairs<2>(d, &s.delta[r][c4]);
-        read_pairs<2>(x, &s.dx[r][c4]);
-        read_pairs<NN>(b, &s.b[r][s4]);
-        if constexpr (kOut) read_pairs<NN>(c, &s.c[r][s4]);
+      for (int r = 0; r < kTileRows; ++r) {
+        float d[4], x[4], y[4];
+        Two b[NN / 2], c[NN / 2];
+        read_numbers<4>(d, &s.delta[r][c4]);
+        read_numbers<4>(x, &s.dx[r][c4]);
+        read_pairs<NN / 2>(b, &s.b[r][s0]);
+        if constexpr (kGives) read_pairs<NN / 2>(c, &s.c[r][s0]);
 #pragma unroll
-        for (int n = 0; n < NN; ++n)
+        for (int j = 0; j < 4; ++j) {
+          const Two dd = both(d[j]), xx = both(x[j]);
+          Two sum = 0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            h[j][n] = fma2(scan_decay(d[j], a2[j][n]), h[j][n], mul2(x[j], b[n]));
-            if (kOut) y[j] = n ? fma2(c[n], h[j][n], y[j]) : mul2(c[n], h[j][n]);
+          for (int m = 0; m < NN / 2; ++m) {
+            h[j][m] = fma2(scan_decay(dd, a2[j][m]), h[j][m], mul2(xx, b[m]));
+            if (kGives) sum = m ? fma2(c[m], h[j][m], sum) : mul2(c[m], h[j][m]);
           }
-        if constexpr (kOut) {
-          float* to = &s.part[r][lane % 4][c4];
+          const float2 f = parts(sum);
+          y[j] = f.x + f.y;
+        }
+        if constexpr (kGives) {
+          float* to = &s.part[r][lane % 2][c4];
           if (kMany && k) {
-            Two f[2];
-            read_pairs<2>(f, to);
-            y[0] = add2(y[0], f[0]), y[1] = add2(y[1], f[1]);
+            float f[4];
+            read_numbers<4>(f, to);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] += f[j];
           }
-          write_pairs(to, y);
+          write_numbers<4>(to, y);
         }
       }
-      if (kMany) keep_states<NN>(s_h + k * 128 * NN, h);
+      if (kMany) keep(k);
       __syncwarp();
     }
-    if constexpr (kOut) {
+    if constexpr (kGives) {
 #pragma unroll
-      for (int r = o; r < kScanRows; r += 2) {
-        Two y = add2(add2(pair_of(s.part[r][0]), pair_of(s.part[r][1])), add2(pair_of(s.part[r][2]), pair_of(s.part[r][3])));
-        y = fma2(skip, row_pair<T>(raw[0][r]), y);
-        if (a.z) {
-          const Two z = row_pair<T>(raw[2][r]);
-          y = mul2(y, mul2(z, scan_sigmoid(z)));
-        }
+      for (int r = 0; r < kTileRows; ++r) {
+        Two y = add2(pair_of<CH>(s.part[r][0]), pair_of<CH>(s.part[r][1]));
+        y = fma2(skip, row_pair<T, CH>(raw[0][r]), y);
+        if (a.z) y = mul2(y, scan_gate(row_pair<T, CH>(raw[2][r])));
         if (r < n) out.put(r, y);
       }
-      out.at += kScanRows * out.stride;
+      out.at += kTileRows * out.stride;
       __syncwarp();
     }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  for (int k = 0; k < blocks; ++k) {
-    if (kMany) kept_states<NN>(h, s_h + k * 128 * NN);
-    if (!kOut) write_pad<NN>(own, h, t, l.pad, k * 4 * NN);
-    else if (a.state_out && seg.index + 1 == seg.count) write_dense<NN>(a.state_out + state_at, h, t, a.states, k * 4 * NN);
-  }
-  if (!kOut) scan_put_sum(l, slot, t, total);
+  wait_for_copies<0>();
+  const bool ends = kGives && a.state_out && seg.index + 1 == seg.count;
+  if (!kGives || ends)
+    for (int k = 0; k < blocks; ++k) {
+      if (kMany) kept(k);
+      if (!kGives) {
+        write(own + k * 2 * NN);
+      } else {
+        float f[4][NN];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int m = 0; m < NN / 2; ++m) {
+            const float2 v = parts(h[j][m]);
+            f[j][2 * m] = v.x, f[j][2 * m + 1] = v.y;
+          }
+        write_dense<NN>(a.state_out + state_at, f, t, a.states, c4, k * 2 * NN + s0);
+      }
+    }
+  if (!kGives) *reinterpret_cast<Two*>(l.sum + (int64_t)slot * l.wide + t.place + 2 * lane) = total;
 }
 
-// Joins the segments: the state that each one starts from, in place of its own.
-// A thread takes four states of a channel of a grid.
-constexpr int kJoinBatch = 8;
-__global__ void __launch_bounds__(128) k_scan_join(ScanLaunch l) {
-  let_next_kernel_start();
-  const tb_scan_args& a = l.a;
-  const int per = l.pad / 4, blocks = (int)(((int64_t)a.channels * per + blockDim.x - 1) / blockDim.x);
-  const int b = blockIdx.x / blocks, slot0 = lin_first_slot(l, b);
-  int64_t begin, end;
-  lin_grid_rows(l, b, begin, end);
-  // offsets that decrease name rows twice: their segments are more than the slots, which bound the walk
-  const int n = min(lin_segments_of(l, end - begin), max(0, l.segments - slot0));
-  const int64_t i = (int64_t)(blockIdx.x % blocks) * blockDim.x + threadIdx.x, c = i / per;
-  if (c >= a.channels) return;
-  const int s = (int)(i - c * per) * 4;
-  float a2[4], x[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const bool is = s + k < a.states;
-    a2[k] = is ? a.a[c * a.states + s + k] * kLog2e : 0.f;
-    x[k] = is && a.state ? a.state[((int64_t)b * a.channels + c) * a.states + s + k] : 0.f;
-  }
-  wait_for_last_kernel();
-  float* at = l.seg + ((int64_t)slot0 * a.channels + c) * l.pad + s;
-  const float* sum = l.sum + (int64_t)slot0 * a.channels + c;
-  const int64_t next = (int64_t)a.channels * l.pad;
-  for (int j0 = 0; j0 < n; j0 += kJoinBatch) {
-    float4 own[kJoinBatch];
-    float d[kJoinBatch];
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (j0 + j + 1 < n) {
-        own[j] = *reinterpret_cast<const float4*>(at + (j0 + j) * next);
-        d[j] = sum[(int64_t)(j0 + j) * a.channels];
-      }
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (j0 + j < n) {
-        *reinterpret_cast<float4*>(at + (j0 + j) * next) = make_float4(x[0], x[1], x[2], x[3]);
-        if (j0 + j + 1 < n) {
-          const float f[4] = {own[j].x, own[j].y, own[j].z, own[j].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = fmaf(scan_decay(d[j], a2[k]), x[k], f[k]);
-        }
-      }
+template <class T, int NN, Walk kWalk, bool kMany>
+cudaError_t go(const ScanLaunch& l, cudaStream_t s) {
+  size_t bytes = l.warps * sizeof(WalkShared<T, NN, kWalk == kOut>);
+  if (kMany) bytes += (size_t)l.warps * (l.pad / (2 * NN)) * kept_floats<NN>() * sizeof(float);
+  static std::atomic<bool> ready[kMaxDevices];
+  const cudaError_t e = allow_shared(k_scan<T, NN, kWalk, kMany>, 227 * 1024, ready);
+  if (e != cudaSuccess) return e;
+  return launch_early(k_scan<T, NN, kWalk, kMany>, (unsigned)((int64_t)l.segments * l.blocks_x), 32 * l.warps, bytes, s,
+                      kWalk == kOut && l.segment != 0, l);
+}
+template <class T, Walk kWalk>
+cudaError_t pick(const ScanLaunch& l, cudaStream_t s) {
+  if (l.pass == 8) return go<T, 4, kWalk, false>(l, s);
+  return l.pad == 16 ? go<T, 8, kWalk, false>(l, s) : go<T, 8, kWalk, true>(l, s);
+}
+template <Walk kWalk>
+cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
+  switch (l.a.type) {
+    case TB_TYPE_F32: return pick<float, kWalk>(l, s);
+    case TB_TYPE_F16: return pick<__half, kWalk>(l, s);
+    default: return pick<__nv_bfloat16, kWalk>(l, s);
   }
 }
 
@@ -265,39 +308,12 @@ __global__ void __launch_bounds__(128) k_scan_step(ScanStepLaunch l) {
   }
 }
 
-template <class T, int NN, bool kOut, bool kMany>
-cudaError_t go(const ScanLaunch& l, cudaStream_t s) {
-  size_t bytes = kWarps * sizeof(WalkShared<T, NN, kOut>);
-  if (kMany) bytes += (size_t)kWarps * (l.pad / (4 * NN)) * 128 * NN * sizeof(float);
-  static std::atomic<bool> ready[kMaxDevices];
-  const cudaError_t e = allow_shared(k_scan<T, NN, kOut, kMany>, 227 * 1024, ready);
-  if (e != cudaSuccess) return e;
-  return launch_early(k_scan<T, NN, kOut, kMany>, (unsigned)((int64_t)l.segments * l.blocks_x), 32 * kWarps, bytes, s,
-                      kOut && l.segment != 0, l);
-}
-template <class T, bool kOut>
-cudaError_t pick(const ScanLaunch& l, cudaStream_t s) {
-  if (l.nn == 2) return go<T, 2, kOut, false>(l, s);
-  return l.pad == 16 ? go<T, 4, kOut, false>(l, s) : go<T, 4, kOut, true>(l, s);
-}
-template <bool kOut>
-cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
-  switch (l.a.type) {
-    case TB_TYPE_F32: return pick<float, kOut>(l, s);
-    case TB_TYPE_F16: return pick<__half, kOut>(l, s);
-    default: return pick<__nv_bfloat16, kOut>(l, s);
-  }
-}
-
 }  // namespace
 
-cudaError_t launch_scan(const void* args, cudaStream_t s) { return by_type<true>(*(const ScanLaunch*)args, s); }
-cudaError_t launch_scan_states(const void* args, cudaStream_t s) { return by_type<false>(*(const ScanLaunch*)args, s); }
-
-cudaError_t launch_scan_join(const void* args, cudaStream_t s) {
+cudaError_t launch_scan(const void* args, cudaStream_t s) { return by_type<kOut>(*(const ScanLaunch*)args, s); }
+cudaError_t launch_scan_states(const void* args, cudaStream_t s) {
   const ScanLaunch& l = *(const ScanLaunch*)args;
-  const int64_t items = (int64_t)l.a.channels * (l.pad / 4);
-  return launch_early(k_scan_join, (unsigned)((items + 127) / 128 * l.grids), 128, 0, s, true, l);
+  return l.tile ? by_type<kTiles>(l, s) : by_type<kStates>(l, s);
 }
 
 cudaError_t launch_scan_step(const void* args, cudaStream_t s) {

@@ -1,20 +1,19 @@
 // What the kernels of the selective scan share: how a warp's lanes hold a tile
 // of channels and states, rows through shared memory, the functions of a step.
 //
-// A warp walks down the rows of a tile of 32 channels (kScanChannels) and 4 NN
-// states.  Lane l holds channels 4 (l / 4) .. + 4 and states NN (l % 4) .. + NN
-// of it, 4 NN numbers, so that a row costs it one 16-byte read each of delta
-// and delta x (of its channels) and a few of b and c (of its states) for 4 NN
-// updates of h; a sum over the states is one over its own and 4 lanes, a sum
-// over the channels one over its own and 8 lanes.  Both go through shared
-// memory: a lane writes its own sums, and the lane of a channel (or state)
-// reads and adds what belongs to it.
+// A warp takes the rows of a tile of channels and of up to 16 states, a lane 4
+// of the channels and NN of the states: a row costs it one 16-byte read each of
+// delta and delta x, and NN numbers each of b and c, for 4 NN updates of h.  The
+// walks (tb_scan.cu) hold 64 channels, two lanes to a channel's states, the
+// gradient (tb_scan_backward.cu), which keeps four rows' states at once, 32
+// channels and four lanes.  Sums over states or channels are a lane's own first
+// and then go through shared memory: a lane writes its part, and the lane of a
+// channel (or state) reads and adds what belongs to it.
 //
-// The walks are bound by the instructions that a multiprocessor issues, so
-// numbers go in pairs of neighbouring channels, two to an instruction
-// (fma.rn.f32x2); b and c lie in shared memory as pairs of one number twice.
-// What belongs to a row and a channel (steps, gates, outputs) is done by 16
-// lanes for a row's 32 channels, two rows at a time.
+// The walks are bound by issued instructions, shared memory and exponentials
+// in about equal parts, so numbers go in pairs, two to an instruction
+// (fma.rn.f32x2).  What belongs to a row and a channel (steps, gates, outputs)
+// is done by pairs of channels as well.
 #pragma once
 
 #include "tb_linattn.cuh"
@@ -22,7 +21,6 @@
 
 namespace tb {
 
-constexpr int kScanRows = 8;  // of a tile in shared memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------ pairs of numbers
@@ -110,47 +108,55 @@ __device__ __forceinline__ void copy_row(void* dst, const void* src, int bytes) 
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes)
                : "memory");
 }
-
-// The channels of a warp.
-struct ScanTile {
-  int group, first, count;  // first channel of all; count <= 0: none
-};
-__device__ __forceinline__ ScanTile scan_tile(const ScanLaunch& l, int group, int tile) {
-  const int per = l.a.channels / l.a.groups;
-  return {group, group * per + tile * kScanChannels, tile < l.group_tiles ? min(kScanChannels, per - tile * kScanChannels) : 0};
-}
-
-// Rows [row, row + n) of a tile's channels to dst [kScanRows][kScanChannels],
-// zeros past them; asynchronous where vectors fit.
-template <class T>
-__device__ __forceinline__ void scan_fetch(T* dst, const void* src, int64_t stride, int64_t row, int n, const ScanTile& t, bool vec) {
-  const int lane = threadIdx.x & 31;
-  const T* from = (const T*)src + t.first;
-  if (vec && t.count == kScanChannels) {
-    constexpr int kChunk = 16 / (int)sizeof(T), kPer = kScanChannels / kChunk;
-#pragma unroll
-    for (int i = lane; i < kScanRows * kPer; i += 32) {
-      const int r = i / kPer, c = i % kPer * kChunk;
-      copy_row(dst + r * kScanChannels + c, from + (row + min(r, max(n - 1, 0))) * stride + c, r < n ? 16 : 0);
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < kScanRows; ++r)
-      dst[r * kScanChannels + lane] = r < n && lane < t.count ? from[(row + r) * stride + lane] : RowType<T>::from(0.f);
-  }
-}
-__device__ __forceinline__ void scan_fetched() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_on_their_way() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void scan_wait() {
+__device__ __forceinline__ void wait_for_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
   __syncwarp();
 }
 
+// The channels of a warp.  The workspace's arrays have kScanPad channels for
+// each begun so many of a group, so that a tile's place in them is whole.
+struct ScanTile {
+  int group, first, count;  // first channel of all; count <= 0: none
+  int64_t place;            // first channel in the workspace
+};
+template <int CH>
+__device__ __forceinline__ ScanTile scan_tile(const ScanLaunch& l, int group, int tile) {
+  const int per = l.a.channels / l.a.groups;
+  return {group, group * per + tile * CH, min(CH, per - tile * CH), (int64_t)group * l.group_pad + tile * CH};
+}
+
+// Rows [row, row + n) of a tile's channels to dst [kTileRows][CH], zeros past
+// them; asynchronous where vectors fit.
+template <class T, int CH>
+__device__ __forceinline__ void scan_fetch(T* dst, const void* src, int64_t stride, int64_t row, int n, const ScanTile& t, bool vec) {
+  const int lane = threadIdx.x & 31;
+  const T* from = (const T*)src + t.first;
+  if (vec && t.count == CH) {
+    constexpr int kChunk = 16 / (int)sizeof(T), kPer = CH / kChunk;
+#pragma unroll
+    for (int k = 0; k < kTileRows * kPer / 32; ++k) {
+      const int i = k * 32 + lane, r = i / kPer, c = i % kPer * kChunk;
+      copy_row(dst + r * CH + c, from + (row + min(r, max(n - 1, 0))) * stride + c, r < n ? 16 : 0);
+    }
+  } else {
+    for (int r = 0; r < kTileRows; ++r)
+#pragma unroll
+      for (int c = lane; c < CH; c += 32)
+        dst[r * CH + c] = r < n && c < t.count ? from[(row + r) * stride + c] : RowType<T>::from(0.f);
+  }
+}
+
 // The two channels of a lane in what is done by rows and channels: 2 (lane %
-// 16), of row lane / 16 of two.
-template <class T>
-__device__ __forceinline__ Two row_pair(const T (&row)[kScanChannels]) {
-  const int p = threadIdx.x & 15;
+// (CH / 2)), of row lane / (CH / 2) of as many.
+template <int CH>
+__device__ __forceinline__ int lane_pair() { return (threadIdx.x & 31) % (CH / 2); }
+template <int CH>
+__device__ __forceinline__ int lane_row() { return (threadIdx.x & 31) / (CH / 2); }
+template <class T, int CH>
+__device__ __forceinline__ Two row_pair(const T (&row)[CH]) {
+  const int p = lane_pair<CH>();
   if constexpr (sizeof(T) == 4) {
     return reinterpret_cast<const Two*>(row)[p];
   } else {
@@ -158,21 +164,23 @@ __device__ __forceinline__ Two row_pair(const T (&row)[kScanChannels]) {
     return two(f.x, f.y);
   }
 }
-__device__ __forceinline__ Two& pair_of(float (&row)[kScanChannels]) { return reinterpret_cast<Two*>(row)[threadIdx.x & 15]; }
+template <int CH>
+__device__ __forceinline__ Two& pair_of(float (&row)[CH]) { return reinterpret_cast<Two*>(row)[lane_pair<CH>()]; }
 // A vector [channels] in 32 bits, zeros where it is NULL or past the tile.
+template <int CH>
 __device__ __forceinline__ Two channel_pair(const float* v, const ScanTile& t) {
-  const int c = 2 * (threadIdx.x & 15);
+  const int c = 2 * lane_pair<CH>();
   return two(v && c < t.count ? v[t.first + c] : 0.f, v && c + 1 < t.count ? v[t.first + c + 1] : 0.f);
 }
 // Writes rows of a tensor by such pairs.
-template <class T>
+template <class T, int CH>
 struct PairOut {
   T* at;
   int64_t stride;
   int count;   // channels of the lane: 0, 1 or 2
   bool whole;  // pairs lie on their own size
   __device__ __forceinline__ PairOut(void* p, int64_t stride, int64_t row, const ScanTile& t)
-      : at((T*)p + row * stride + t.first + 2 * (threadIdx.x & 15)), stride(stride), count(min(t.count - 2 * (int)(threadIdx.x & 15), 2)),
+      : at((T*)p + row * stride + t.first + 2 * lane_pair<CH>()), stride(stride), count(min(t.count - 2 * lane_pair<CH>(), 2)),
         whole((uintptr_t)at % (2 * sizeof(T)) == 0 && stride % 2 == 0) {}
   __device__ __forceinline__ void put(int r, Two v) const {
     const float2 f = parts(v);
@@ -191,12 +199,14 @@ __device__ __forceinline__ Two scan_step_of(Two dt, Two bias, int softplus) {
   const Two v = add2(dt, bias);
   return softplus ? scan_softplus(v) : v;
 }
+// z sigmoid(z).
+__device__ __forceinline__ Two scan_gate(Two z) { return mul2(z, scan_sigmoid(z)); }
 
-// Rows of b or c: 4 NN states from n0 on, elements 32 apart of kScanRows x 4 NN.
-template <class T, int NN>
+// Rows of b or c: kStates states from n0 on, elements 32 apart of kTileRows x kStates.
+template <class T, int kStates>
 struct ScanStates {
-  static constexpr int kStates = 4 * NN, kEach = kScanRows * kStates / 32, kStep = 32 / kStates;
-  const T* from;  // the lane's state of row lane / kStates of the first tile
+  static constexpr int kEach = kTileRows * kStates / 32, kStep = 32 / kStates;
+  const T* from;  // the lane's state of row lane / kStates
   int64_t stride;
   bool is;
   T f[kEach];
@@ -212,7 +222,12 @@ struct ScanStates {
 #pragma unroll
     for (int i = 0; i < kEach; ++i, at += kStep * stride) f[i] = is && r + i * kStep < n ? *at : RowType<T>::from(0.f);
   }
-  __device__ __forceinline__ void store(Two (&dst)[kScanRows][kStates]) const {
+  __device__ __forceinline__ void store(float (&dst)[kTileRows][kStates]) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) (&dst[0][0])[lane + 32 * i] = RowType<T>::to(f[i]);
+  }
+  __device__ __forceinline__ void store(Two (&dst)[kTileRows][kStates]) const {  // twice each
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) (&dst[0][0])[lane + 32 * i] = both(RowType<T>::to(f[i]));
@@ -228,130 +243,79 @@ __device__ __forceinline__ void read_pairs(Two (&f)[N], const void* at) {
     f[i] = v.x, f[i + 1] = v.y;
   }
 }
-__device__ __forceinline__ void write_pairs(void* at, const Two (&f)[2]) {
-  *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f[0], f[1]);
-}
+__device__ __forceinline__ void write_pairs(void* at, Two x, Two y) { *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(x, y); }
 
-// -------------------------------------------------- states outside a kernel
-//
-// A lane's numbers as h[j][n]: channels 4 (lane / 4) + 2 j and + 1, state n.
-
-template <int NN>
-__device__ __forceinline__ void from_channels(Two (&h)[2][NN], const float (&f)[4][NN]) {
+// N consecutive numbers: in the workspace on 4 N bytes, or on 16; of a dense
+// [channels, states] array anywhere.
+template <int N>
+__device__ __forceinline__ void read_numbers(float (&f)[N], const float* at) {
+  if constexpr (N == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(at);
+    f[0] = v.x, f[1] = v.y;
+  } else {
 #pragma unroll
-  for (int n = 0; n < NN; ++n) h[0][n] = two(f[0][n], f[1][n]), h[1][n] = two(f[2][n], f[3][n]);
-}
-template <int NN>
-__device__ __forceinline__ void to_channels(float (&f)[4][NN], const Two (&h)[2][NN]) {
-#pragma unroll
-  for (int n = 0; n < NN; ++n)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 v = parts(h[j][n]);
-      f[2 * j][n] = v.x, f[2 * j + 1][n] = v.y;
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(at + i);
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
     }
-}
-// Of a [.., channels, pad] array of the workspace: 16 or 8 bytes for each channel.
-template <int NN>
-__device__ __forceinline__ void read_pad(Two (&h)[2][NN], const float* at, const ScanTile& t, int pad, int n0) {
-  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
-  float f[4][NN] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (c + i < t.count) {
-      const float* from = at + (int64_t)(t.first + c + i) * pad + s;
-      if constexpr (NN == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(from);
-        f[i][0] = v.x, f[i][1] = v.y, f[i][2] = v.z, f[i][3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(from);
-        f[i][0] = v.x, f[i][1] = v.y;
-      }
-    }
-  from_channels<NN>(h, f);
-}
-template <int NN>
-__device__ __forceinline__ void write_pad(float* at, const Two (&h)[2][NN], const ScanTile& t, int pad, int n0) {
-  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
-  float f[4][NN];
-  to_channels<NN>(f, h);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (c + i < t.count) {
-      float* to = at + (int64_t)(t.first + c + i) * pad + s;
-      if constexpr (NN == 4) *reinterpret_cast<float4*>(to) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
-      else *reinterpret_cast<float2*>(to) = make_float2(f[i][0], f[i][1]);
-    }
-}
-// Of a [channels, states] array, element by element (a is one of them); zeros where it is NULL.
-template <int NN>
-__device__ __forceinline__ void read_dense(Two (&h)[2][NN], const float* at, const ScanTile& t, int states, int n0) {
-  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
-  float f[4][NN];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int n = 0; n < NN; ++n)
-      f[i][n] = at && c + i < t.count && s + n < states ? at[(int64_t)(t.first + c + i) * states + s + n] : 0.f;
-  from_channels<NN>(h, f);
-}
-template <int NN>
-__device__ __forceinline__ void write_dense(float* at, const Two (&h)[2][NN], const ScanTile& t, int states, int n0) {
-  const int lane = threadIdx.x & 31, c = lane / 4 * 4, s = n0 + lane % 4 * NN;
-  float f[4][NN];
-  to_channels<NN>(f, h);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int n = 0; n < NN; ++n)
-      if (c + i < t.count && s + n < states) at[(int64_t)(t.first + c + i) * states + s + n] = f[i][n];
-}
-// a log2(e) of a lane.
-template <int NN>
-__device__ __forceinline__ void read_rates(Two (&a2)[2][NN], const tb_scan_args& a, const ScanTile& t, int n0) {
-  read_dense<NN>(a2, a.a, t, a.states, n0);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int n = 0; n < NN; ++n) a2[j][n] = mul2(a2[j][n], both(kLog2e));
-}
-
-// A lane's numbers in shared memory, 128 NN floats a warp.
-template <int NN>
-__device__ __forceinline__ void keep_states(float* at, const Two (&h)[2][NN]) {
-#pragma unroll
-  for (int n = 0; n < NN; ++n) reinterpret_cast<ulonglong2*>(at)[32 * n + (threadIdx.x & 31)] = make_ulonglong2(h[0][n], h[1][n]);
-}
-template <int NN>
-__device__ __forceinline__ void kept_states(Two (&h)[2][NN], const float* at) {
-#pragma unroll
-  for (int n = 0; n < NN; ++n) {
-    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(at)[32 * n + (threadIdx.x & 31)];
-    h[0][n] = v.x, h[1][n] = v.y;
   }
 }
-
-// A segment's sums of delta, of which each half of the warp has every other row's.
-__device__ __forceinline__ void scan_put_sum(const ScanLaunch& l, int slot, const ScanTile& t, Two total) {
-  total = add2(total, __shfl_xor_sync(0xffffffffu, total, 16));
-  const int lane = threadIdx.x & 31, c = 2 * lane;
-  float* to = l.sum + (int64_t)slot * l.a.channels + t.first + c;
-  const float2 f = parts(total);
-  if (lane < 16 && c < t.count) to[0] = f.x;
-  if (lane < 16 && c + 1 < t.count) to[1] = f.y;
+template <int N>
+__device__ __forceinline__ void write_numbers(float* at, const float (&f)[N]) {
+  if constexpr (N == 2) {
+    *reinterpret_cast<float2*>(at) = make_float2(f[0], f[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(at + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  }
+}
+// A lane's 4 channels from c4 of the tile, NN states from s, of a dense array;
+// zeros where it is NULL or past it.
+template <int NN>
+__device__ __forceinline__ void read_dense(float (&f)[4][NN], const float* at, const ScanTile& t, int states, int c4, int s) {
+  const bool vec = NN % 4 == 0 && states % 4 == 0 && ((uintptr_t)at & 15) == 0 && s + NN <= states;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool is = at && c4 + i < t.count;
+    const float* from = at + (int64_t)(t.first + c4 + i) * states + s;
+#pragma unroll
+    for (int n = 0; n < NN; ++n) f[i][n] = 0.f;
+    if (is && vec) {
+      read_numbers<NN>(f[i], from);
+    } else if (is) {
+#pragma unroll
+      for (int n = 0; n < NN; ++n)
+        if (s + n < states) f[i][n] = from[n];
+    }
+  }
+}
+template <int NN>
+__device__ __forceinline__ void write_dense(float* at, const float (&f)[4][NN], const ScanTile& t, int states, int c4, int s) {
+  const bool vec = NN % 4 == 0 && states % 4 == 0 && ((uintptr_t)at & 15) == 0 && s + NN <= states;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c4 + i < t.count) {
+      float* to = at + (int64_t)(t.first + c4 + i) * states + s;
+      if (vec) {
+        write_numbers<NN>(to, f[i]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NN; ++n)
+          if (s + n < states) to[n] = f[i][n];
+      }
+    }
 }
 
 // Zeros for a tile's channels of the rows that no grid has: a slot's share.
-template <class T>
+template <class T, int CH>
 __device__ __forceinline__ void scan_zero_share(const ScanLaunch& l, void* out, int64_t stride, int slot, const ScanTile& t) {
   const LinCover c = lin_cover(l);
   const int64_t rows = c.begin + l.tokens - c.end;
   if (rows == 0) return;
   const int64_t per = (rows + l.segments - 1) / l.segments, r0 = min(slot * per, rows), r1 = min(r0 + per, rows);
-  const int lane = threadIdx.x & 31;
-  if (lane < t.count)
+  for (int i = threadIdx.x & 31; i < t.count; i += 32)
     for (int64_t r = r0; r < r1; ++r)
-      ((T*)out)[(r < c.begin ? r : r - c.begin + c.end) * stride + t.first + lane] = RowType<T>::from(0.f);
+      ((T*)out)[(r < c.begin ? r : r - c.begin + c.end) * stride + t.first + i] = RowType<T>::from(0.f);
 }
 
 }  // namespace tb

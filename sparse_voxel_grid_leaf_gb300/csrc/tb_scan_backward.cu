@@ -7,172 +7,139 @@
 //   into = g . b,  dx = d ds + delta into,  q = g exp(delta a) h_(t-1),
 //   ddelta = a . q + x into,  da = sum over rows q delta,  dz = dy s silu'(z).
 //
-// The rows are taken in chunks of kScanChunk.  First every chunk's own last
-// state and its own part of the carried exp(delta a) g, both from zero, and
-// their joining along the grids, forward and backward; then all chunks at once,
-// each with what enters it from both sides.  A warp walks its chunk forward,
-// keeping the state before every eighth row in shared memory, and then
-// backward, four rows at a time with their states and decays in registers.
-// Sums over channels go through shared memory over a block's four warps, and
-// over blocks through parts that a last kernel adds in a fixed order.
+// The rows are taken in chunks.  First every chunk's own states from zero,
+// before every tile of kTileRows rows (tb_scan.cu), and its own part of the
+// carried exp(delta a) g (k_scan_carry), then their joining along the grids,
+// forward and backward (tb_scan_join.cu); then all chunks at once, each with
+// what enters it from both sides, tile by tile from its last one.  The states
+// before a tile are its own part and what the chunk started from, decayed by
+// the sum of delta between.  Sums over channels go through shared memory over a
+// block's four warps, and over blocks through parts that a last kernel adds in
+// a fixed order.
 #include "tb_scan.cuh"
 
 namespace tb {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTiles = kScanChunk / kScanRows;
 
 // ------------------------------------------------- what the chunks carry back
 
 template <class T, int NN>
 struct alignas(16) CarryShared {
-  T raw[2][3][kScanRows][kScanChannels];  // dt, dy, z of two tiles
-  float delta[kScanRows][kScanChannels], ds[kScanRows][kScanChannels];
-  Two c[kScanRows][4 * NN];
+  T raw[2][3][kTileRows][kScanChannels];  // dt, dy, z of two tiles
+  float delta[kTileRows][kScanChannels], ds[kTileRows][kScanChannels];
+  float c[kTileRows][2 * NN];
 };
 
 // One block of states a warp (blockIdx.y), as the walks are short.
 template <class T, int NN>
 __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g) {
   extern __shared__ __align__(16) char s_raw[];
+  constexpr int CH = kScanChannels;
   let_next_kernel_start();
   const ScanLaunch& l = g.f;
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   CarryShared<T, NN>& s = reinterpret_cast<CarryShared<T, NN>*>(s_raw)[warp];
-  const int slot = (int)(blockIdx.x / l.blocks_x), at = (int)(blockIdx.x % l.blocks_x) * kWarps + warp;
-  const int n0 = blockIdx.y * 4 * NN;
-  const ScanTile t = scan_tile(l, at / l.group_tiles, at % l.group_tiles);
+  const int blocks_x = (a.groups * l.group_tiles + kWarps - 1) / kWarps;
+  const int slot = (int)(blockIdx.x / blocks_x), at = (int)(blockIdx.x % blocks_x) * kWarps + warp;
+  const int n0 = blockIdx.y * 2 * NN;
+  const ScanTile t = scan_tile<CH>(l, at / l.group_tiles, at % l.group_tiles);
   if (t.group >= a.groups) return;
   const LinSegment seg = lin_segment(l, slot);
   if (seg.grid < 0 || (seg.index == 0 && !g.g.dstate)) return;  // the first chunk's goes nowhere else
   const int64_t row0 = seg.begin + seg.first;
-  Two h[2][NN] = {}, a2[2][NN], total = 0;
-  read_rates<NN>(a2, a, t, n0);
-  const Two bias = channel_pair(a.dt_bias, t);
-  const int tiles = (seg.len + kScanRows - 1) / kScanRows;
+  const int c4 = lane / 2 * 4, s0 = lane % 2 * NN;
+  Two h[4][NN / 2] = {}, a2[4][NN / 2];
+  {
+    float f[4][NN];
+    read_dense<NN>(f, a.a, t, a.states, c4, n0 + s0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int m = 0; m < NN / 2; ++m) a2[j][m] = two(f[j][2 * m] * kLog2e, f[j][2 * m + 1] * kLog2e);
+  }
+  const Two bias = channel_pair<CH>(a.dt_bias, t);
+  const int tiles = (seg.len + kTileRows - 1) / kTileRows;
   auto fetch = [&](int i) {
     if (i >= 0) {
-      const int n = min(kScanRows, seg.len - i * kScanRows);
-      const int64_t row = row0 + i * kScanRows;
+      const int n = min(kTileRows, seg.len - i * kTileRows);
+      const int64_t row = row0 + i * kTileRows;
       auto& raw = s.raw[i & 1];
-      scan_fetch<T>(&raw[0][0][0], a.dt, a.dt_row, row, n, t, l.vec);
-      scan_fetch<T>(&raw[1][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
-      if (a.z) scan_fetch<T>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
+      scan_fetch<T, CH>(&raw[0][0][0], a.dt, a.dt_row, row, n, t, l.vec);
+      scan_fetch<T, CH>(&raw[1][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
+      if (a.z) scan_fetch<T, CH>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
     }
-    scan_fetched();
+    copies_on_their_way();
   };
-  ScanStates<T, NN> nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
-  auto load_states = [&](int i) { nc.load(i * kScanRows, i < 0 ? 0 : min(kScanRows, seg.len - i * kScanRows)); };
-  const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
+  ScanStates<T, 2 * NN> nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+  auto load_states = [&](int i) { nc.load(i * kTileRows, i < 0 ? 0 : min(kTileRows, seg.len - i * kTileRows)); };
   fetch(tiles - 1);
   load_states(tiles - 1);
   for (int i = tiles - 1; i >= 0; --i) {
-    const int n = min(kScanRows, seg.len - i * kScanRows);
+    const int n = min(kTileRows, seg.len - i * kTileRows);
     fetch(i - 1);
-    scan_wait<1>();
+    wait_for_copies<1>();
     auto& raw = s.raw[i & 1];
 #pragma unroll
-    for (int r = o; r < kScanRows; r += 2) {
-      Two ds = row_pair<T>(raw[1][r]);
-      if (a.z) {
-        const Two z = row_pair<T>(raw[2][r]);
-        ds = mul2(ds, mul2(z, scan_sigmoid(z)));
-      }
-      Two delta = scan_step_of(row_pair<T>(raw[0][r]), bias, a.softplus);
+    for (int r = 0; r < kTileRows; ++r) {
+      Two ds = row_pair<T, CH>(raw[1][r]);
+      if (a.z) ds = mul2(ds, scan_gate(row_pair<T, CH>(raw[2][r])));
+      Two delta = scan_step_of(row_pair<T, CH>(raw[0][r]), bias, a.softplus);
       if (r >= n) delta = ds = 0;
-      total = add2(total, delta);
-      pair_of(s.delta[r]) = delta;
-      pair_of(s.ds[r]) = ds;
+      pair_of<CH>(s.delta[r]) = delta;
+      pair_of<CH>(s.ds[r]) = ds;
     }
     nc.store(s.c);
     __syncwarp();
     load_states(i - 1);
 #pragma unroll
-    for (int r = kScanRows - 1; r >= 0; --r) {
-      Two d[2], ds[2], c[NN];
-      read_pairs<2>(d, &s.delta[r][c4]);
-      read_pairs<2>(ds, &s.ds[r][c4]);
-      read_pairs<NN>(c, &s.c[r][s4]);
+    for (int r = kTileRows - 1; r >= 0; --r) {
+      float d[4], ds[4];
+      Two c[NN / 2];
+      read_numbers<4>(d, &s.delta[r][c4]);
+      read_numbers<4>(ds, &s.ds[r][c4]);
+      read_pairs<NN / 2>(c, &s.c[r][s0]);
 #pragma unroll
-      for (int n = 0; n < NN; ++n)
+      for (int j = 0; j < 4; ++j) {
+        const Two dd = both(d[j]), dsj = both(ds[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) h[j][n] = mul2(scan_decay(d[j], a2[j][n]), fma2(c[n], ds[j], h[j][n]));
+        for (int m = 0; m < NN / 2; ++m) h[j][m] = mul2(scan_decay(dd, a2[j][m]), fma2(c[m], dsj, h[j][m]));
+      }
     }
     __syncwarp();
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  write_pad<NN>(g.seg_back + (int64_t)slot * a.channels * l.pad, h, t, l.pad, n0);
-  if (blockIdx.y == 0) scan_put_sum(l, slot, t, total);  // a grid's last chunk has none yet
-}
-
-// Joins what the chunks carry back, from a grid's last chunk to its first: what
-// enters each from behind, in place of its own, and the gradient of the first
-// state.  A thread takes four states of a channel of a grid.
-constexpr int kJoinBatch = 8;
-__global__ void __launch_bounds__(128) k_scan_join_back(ScanBackwardLaunch g) {
-  let_next_kernel_start();
-  const ScanLaunch& l = g.f;
-  const tb_scan_args& a = l.a;
-  const int per = l.pad / 4, blocks = (int)(((int64_t)a.channels * per + blockDim.x - 1) / blockDim.x);
-  const int b = blockIdx.x / blocks, slot0 = lin_first_slot(l, b);
-  int64_t begin, end;
-  lin_grid_rows(l, b, begin, end);
-  const int n = min(lin_segments_of(l, end - begin), max(0, l.segments - slot0));
-  const int64_t i = (int64_t)(blockIdx.x % blocks) * blockDim.x + threadIdx.x, c = i / per;
-  if (c >= a.channels) return;
-  const int s = (int)(i - c * per) * 4;
-  const int64_t state_at = ((int64_t)b * a.channels + c) * a.states + s;
-  float a2[4], x[4];
+  wait_for_copies<0>();
+  float* to = g.seg_back + ((int64_t)slot * l.wide + t.place + c4) * l.pad + n0 + s0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const bool is = s + k < a.states;
-    a2[k] = is ? a.a[c * a.states + s + k] * kLog2e : 0.f;
-    x[k] = is && g.g.dstate_out ? g.g.dstate_out[state_at + k] : 0.f;
-  }
-  wait_for_last_kernel();
-  float* at = g.seg_back + ((int64_t)slot0 * a.channels + c) * l.pad + s;
-  const float* sum = l.sum + (int64_t)slot0 * a.channels + c;
-  const int64_t next = (int64_t)a.channels * l.pad;
-  const int least = g.g.dstate ? 0 : 1;  // the first chunk's own is made where the gradient is asked for
-  for (int j0 = n - 1; j0 >= 0; j0 -= kJoinBatch) {
-    float4 own[kJoinBatch];
-    float d[kJoinBatch];
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (j0 - j >= least) {
-        own[j] = *reinterpret_cast<const float4*>(at + (j0 - j) * next);
-        d[j] = sum[(int64_t)(j0 - j) * a.channels];
-      }
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (j0 - j >= 0) {
-        *reinterpret_cast<float4*>(at + (j0 - j) * next) = make_float4(x[0], x[1], x[2], x[3]);
-        if (j0 - j >= least) {
-          const float f[4] = {own[j].x, own[j].y, own[j].z, own[j].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = fmaf(scan_decay(d[j], a2[k]), x[k], f[k]);
-        }
-      }
-  }
-  if (g.g.dstate)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s + k < a.states) g.g.dstate[state_at + k] = x[k];
+    for (int m = 0; m < NN / 2; m += 2) write_pairs(to + j * l.pad + 2 * m, h[j][m], h[j][m + 1]);
 }
 
 // ------------------------------------------------------------ all of a chunk
 
+constexpr int CH = 32;  // channels of a warp
+
 template <class T, int NN>
 struct alignas(16) BackShared {
-  float kept[kTiles - 1][128 * NN];  // the states before the tiles but the first
-  float delta[kScanRows][kScanChannels], dx[kScanRows][kScanChannels], ds[kScanRows][kScanChannels];
-  Two b[kScanRows][4 * NN], c[kScanRows][4 * NN];
-  float sums[2][3][4][kScanChannels];  // of two rows: a lane's c . h, g . b, a . q
-  float bc[2][2][36 * NN];             // of two rows: a lane's channels of db, dc; on different banks
-  T raw[4][kScanRows][kScanChannels];  // x, dt, z, dy
+  float own[2][4][32 * NN], start[4][32 * NN];  // the states before two tiles, from zero, and before the chunk: by lanes
+  float before[2][CH];                          // the sums of delta before the tiles
+  float delta[kTileRows][CH], dx[kTileRows][CH], ds[kTileRows][CH];
+  Two b[kTileRows][4 * NN], c[kTileRows][4 * NN];
+  float sums[2][3][4][CH];  // of two rows: a lane's c . h, g . b, a . q
+  float bc[2][2][36 * NN];  // of two rows: a lane's channels of db, dc; on different banks
+  T raw[2][4][kTileRows][CH];  // x, dt, z, dy of two tiles
 };
+
+// 4 NN bytes of the workspace.
+template <int NN>
+__device__ __forceinline__ void copy_states(float* dst, const float* src) {
+  if constexpr (NN == 4) copy_row(dst, src, 16);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
 
 template <class T, int NN, bool kMany>
 __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLaunch g) {
@@ -183,67 +150,91 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   let_next_kernel_start();
   const ScanLaunch& l = g.f;
   const tb_scan_args& a = l.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane >> 4, p = lane & 15;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane_row<CH>(), p = lane_pair<CH>();
   Shared& s = reinterpret_cast<Shared*>(s_raw)[warp];
-  Two(*s_bc)[kScanRows][kStates] = reinterpret_cast<Two(*)[kScanRows][kStates]>(s_raw + kWarps * sizeof(Shared));
+  Two(*s_bc)[kTileRows][kStates] = reinterpret_cast<Two(*)[kTileRows][kStates]>(s_raw + kWarps * sizeof(Shared));
   const int per_run = a.groups * g.quads, run = (int)(blockIdx.x / per_run), at = (int)(blockIdx.x % per_run);
   const int group = at / g.quads, quad = at % g.quads;
-  const ScanTile t = scan_tile(l, group, quad * kWarps + warp);
+  ScanTile t = scan_tile<CH>(l, group, quad * kWarps + warp);
+  const bool placed = (quad * kWarps + warp) * CH < l.group_pad;  // in the workspace; past it the warp adds zeros
+  if (!placed) t.place = (int64_t)group * l.group_pad, t.count = 0;
   const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
-  const Two bias = channel_pair(a.dt_bias, t), skip = channel_pair(a.d, t);
+  const int64_t mine = (t.place + c4) * l.pad + s4;  // the lane's place in a slot of the workspace
+  const Two bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(a.d, t);
   Two sum_d = 0, sum_bias = 0;
-  const int blocks = kMany ? l.pad / kStates : 1;
+  const int blocks = kMany ? l.pad / kStates : 1, chunk_tiles = l.segment / kTileRows;
   for (int k = 0; k < blocks; ++k) {
     const int n0 = k * kStates;
     const bool last = k + 1 == blocks;
     Two a2[2][NN], da[2][NN] = {};
-    read_rates<NN>(a2, a, t, n0);
+    auto as_pairs = [&](Two(&h)[2][NN], const float(&f)[4][NN]) {
+#pragma unroll
+      for (int n = 0; n < NN; ++n) h[0][n] = two(f[0][n], f[1][n]), h[1][n] = two(f[2][n], f[3][n]);
+    };
+    auto nothing = [&](Two(&h)[2][NN]) {
+#pragma unroll
+      for (int n = 0; n < NN; ++n) h[0][n] = h[1][n] = 0;
+    };
+    {
+      float f[4][NN];
+      read_dense<NN>(f, a.a, t, a.states, c4, n0 + s4);
+      as_pairs(a2, f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NN; ++n) a2[j][n] = mul2(a2[j][n], both(kLog2e));
+    }
     for (int slot = run * g.per_run; slot < min((run + 1) * g.per_run, l.segments); ++slot) {
       if (k == 0) {
-        scan_zero_share<T>(l, g.g.dx, g.g.dx_row, slot, t);
-        scan_zero_share<T>(l, g.g.ddt, g.g.ddt_row, slot, t);
-        if (a.z) scan_zero_share<T>(l, g.g.dz, g.g.dz_row, slot, t);
+        scan_zero_share<T, CH>(l, g.g.dx, g.g.dx_row, slot, t);
+        scan_zero_share<T, CH>(l, g.g.ddt, g.g.ddt_row, slot, t);
+        if (a.z) scan_zero_share<T, CH>(l, g.g.dz, g.g.dz_row, slot, t);
       }
       const LinSegment seg = lin_segment(l, slot);
       if (seg.grid < 0 || seg.len == 0) continue;
-      const int64_t row0 = seg.begin + seg.first, own = (int64_t)slot * a.channels * l.pad;
-      const int tiles = (seg.len + kScanRows - 1) / kScanRows;
-      const PairOut<T> out_x(g.g.dx, g.g.dx_row, row0, t), out_dt(g.g.ddt, g.g.ddt_row, row0, t), out_z(g.g.dz, g.g.dz_row, row0, t);
-      ScanStates<T, NN> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0), nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
-      Two h[2][NN];
-      auto stage = [&](int i, bool all) {
-        const int64_t row = row0 + i * kScanRows;
-        const int n = min(kScanRows, seg.len - i * kScanRows);
-        scan_fetch<T>(&s.raw[0][0][0], a.x, a.x_row, row, n, t, l.vec);
-        scan_fetch<T>(&s.raw[1][0][0], a.dt, a.dt_row, row, n, t, l.vec);
-        if (all) {
-          if (a.z) scan_fetch<T>(&s.raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
-          scan_fetch<T>(&s.raw[3][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
-        }
-        scan_fetched();
-        nb.load(i * kScanRows, n);
-        if (all) nc.load(i * kScanRows, n);
-        nb.store(s.b);
-        if (all) nc.store(s.c);
-        scan_wait<0>();
+      const int64_t row0 = seg.begin + seg.first;
+      const int tiles = (seg.len + kTileRows - 1) / kTileRows;
+      const PairOut<T, CH> out_x(g.g.dx, g.g.dx_row, row0, t), out_dt(g.g.ddt, g.g.ddt_row, row0, t), out_z(g.g.dz, g.g.dz_row, row0, t);
+      ScanStates<T, kStates> nb(a.b, a.b_row, t.group * a.b_group, row0, a.states, n0),
+          nc(a.c, a.c_row, t.group * a.c_group, row0, a.states, n0);
+      auto fetch = [&](int i) {
+        if (i >= 0) {
+          const int64_t row = row0 + i * kTileRows;
+          const int n = min(kTileRows, seg.len - i * kTileRows);
+          auto& raw = s.raw[i & 1];
+          scan_fetch<T, CH>(&raw[0][0][0], a.x, a.x_row, row, n, t, l.vec);
+          scan_fetch<T, CH>(&raw[1][0][0], a.dt, a.dt_row, row, n, t, l.vec);
+          if (a.z) scan_fetch<T, CH>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
+          scan_fetch<T, CH>(&raw[3][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
+          if (i) {
+            const int64_t tile = (int64_t)slot * chunk_tiles + i;
+            const float* from = l.tile + tile * l.wide * l.pad + mine + n0;
 #pragma unroll
-        for (int r = o; r < kScanRows; r += 2) {
-          Two delta = scan_step_of(row_pair<T>(s.raw[1][r]), bias, a.softplus);
-          if (r >= n) delta = 0;
-          pair_of(s.delta[r]) = delta;
-          pair_of(s.dx[r]) = mul2(delta, row_pair<T>(s.raw[0][r]));
-          if (all) {
-            Two ds = row_pair<T>(s.raw[3][r]);
-            if (a.z) {
-              const Two z = row_pair<T>(s.raw[2][r]);
-              ds = mul2(ds, mul2(z, scan_sigmoid(z)));
-            }
-            pair_of(s.ds[r]) = r < n ? ds : 0;
+            for (int j = 0; j < 4; ++j) copy_states<NN>(&s.own[i & 1][j][lane * NN], from + j * l.pad);
+            if (lane < CH / 4) copy_row(&s.before[i & 1][lane * 4], l.tile_sum + tile * l.wide + t.place + lane * 4, 16);
           }
         }
-        __syncwarp();
+        copies_on_their_way();
       };
-      auto forward = [&](int r, Two (&e)[2][NN]) {
+      auto load_states = [&](int i) {
+        const int n = i < 0 ? 0 : min(kTileRows, seg.len - i * kTileRows);
+        nb.load(i * kTileRows, n);
+        nc.load(i * kTileRows, n);
+      };
+      Two carry[2][NN], h[2][NN];
+      {
+        const int64_t at_slot = (int64_t)slot * l.wide * l.pad + mine + n0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) copy_states<NN>(&s.start[j][lane * NN], l.seg + at_slot + j * l.pad);
+        fetch(tiles - 1);
+        load_states(tiles - 1);
+        float f[4][NN];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], g.seg_back + at_slot + j * l.pad);
+        as_pairs(carry, f);
+        if (!placed) nothing(carry);
+      }
+      auto forward = [&](int r, Two(&e)[2][NN]) {
         Two d[2], x[2], b[NN];
         read_pairs<2>(d, &s.delta[r][c4]);
         read_pairs<2>(x, &s.dx[r][c4]);
@@ -256,33 +247,61 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
             h[j][n] = fma2(e[j][n], h[j][n], mul2(x[j], b[n]));
           }
       };
-      read_pad<NN>(h, l.seg + own, t, l.pad, n0);
-      for (int i = 0; i + 1 < tiles; ++i) {
-        stage(i, false);
+      for (int i = tiles - 1; i >= 0; --i) {
+        const int rows = min(kTileRows, seg.len - i * kTileRows);
+        auto& raw = s.raw[i & 1];
+        nb.store(s.b);
+        nc.store(s.c);
+        fetch(i - 1);
+        load_states(i - 1);
+        wait_for_copies<1>();
 #pragma unroll
-        for (int r = 0; r < kScanRows; ++r) {
+        for (int m = 0; m < kTileRows / 2; ++m) {
+          const int r = 2 * m + o;
+          Two delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus), ds = row_pair<T, CH>(raw[3][r]);
+          if (a.z) ds = mul2(ds, scan_gate(row_pair<T, CH>(raw[2][r])));
+          if (r >= rows) delta = ds = 0;
+          pair_of<CH>(s.delta[r]) = delta;
+          pair_of<CH>(s.dx[r]) = mul2(delta, row_pair<T, CH>(raw[0][r]));
+          pair_of<CH>(s.ds[r]) = ds;
+        }
+        // the states before the tile
+        {
+          float f[4][NN];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], &s.start[j][lane * NN]);
+          as_pairs(h, f);
+          if (i) {
+            Two d[2], own[2][NN];
+            read_pairs<2>(d, &s.before[i & 1][c4]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], &s.own[i & 1][j][lane * NN]);
+            as_pairs(own, f);
+#pragma unroll
+            for (int n = 0; n < NN; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) h[j][n] = fma2(scan_decay(d[j], a2[j][n]), h[j][n], own[j][n]);
+          }
+        }
+        if (!placed) nothing(h);
+        Two first[2][NN];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int n = 0; n < NN; ++n) first[j][n] = h[j][n];
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
           Two e[2][NN];
           forward(r, e);
         }
-        keep_states<NN>(s.kept[i], h);
-        __syncwarp();
-      }
-      Two carry[2][NN];
-      read_pad<NN>(carry, g.seg_back + own, t, l.pad, n0);
-      for (int i = tiles - 1; i >= 0; --i) {
-        const int rows = min(kScanRows, seg.len - i * kScanRows);
-        stage(i, true);
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
-          if (i) kept_states<NN>(h, s.kept[i - 1]);
-          else read_pad<NN>(h, l.seg + own, t, l.pad, n0);
-          if (half) {
+          if (!half)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              Two e[2][NN];
-              forward(r, e);
-            }
-          }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int n = 0; n < NN; ++n) h[j][n] = first[j][n];
           // the states before four rows and after each, and the rows' decays
           Two hs[5][2][NN], e[4][2][NN];
 #pragma unroll
@@ -322,9 +341,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
               db[n] = fb.x + fb.y;
               dc[n] = fc.x + fc.y;
             }
-            write_pairs(&s.sums[r & 1][0][lane % 4][c4], y);
-            write_pairs(&s.sums[r & 1][1][lane % 4][c4], into);
-            write_pairs(&s.sums[r & 1][2][lane % 4][c4], qa);
+            write_pairs(&s.sums[r & 1][0][lane % 4][c4], y[0], y[1]);
+            write_pairs(&s.sums[r & 1][1][lane % 4][c4], into[0], into[1]);
+            write_pairs(&s.sums[r & 1][2][lane % 4][c4], qa[0], qa[1]);
 #pragma unroll
             for (int n = 0; n < NN; n += 2) {
               const int to = lane / 4 * kStates + s4 + n;
@@ -338,9 +357,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
             Two sum[3];
 #pragma unroll
             for (int v = 0; v < 3; ++v)
-              sum[v] = add2(add2(pair_of(s.sums[o][v][0]), pair_of(s.sums[o][v][1])),
-                            add2(pair_of(s.sums[o][v][2]), pair_of(s.sums[o][v][3])));
-            const int to = i * kScanRows + rr;
+              sum[v] = add2(add2(pair_of<CH>(s.sums[o][v][0]), pair_of<CH>(s.sums[o][v][1])),
+                            add2(pair_of<CH>(s.sums[o][v][2]), pair_of<CH>(s.sums[o][v][3])));
+            const int to = i * kTileRows + rr;
             if (kMany && rr < rows) {
               float* acc = g.acc + ((row0 + to) * a.channels + t.first + 2 * p) * 3;
 #pragma unroll
@@ -356,16 +375,16 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
                   }
             }
             if (rr < rows && last) {
-              const Two xf = row_pair<T>(s.raw[0][rr]), dsf = pair_of(s.ds[rr]);
+              const Two xf = row_pair<T, CH>(raw[0][rr]), dsf = pair_of<CH>(s.ds[rr]);
               const Two inner = fma2(skip, xf, sum[0]);
               Two ddt = fma2(xf, sum[1], mul2(sum[2], both(kLn2)));
-              if (a.softplus) ddt = mul2(ddt, scan_sigmoid(add2(row_pair<T>(s.raw[1][rr]), bias)));
-              out_x.put(to, fma2(skip, dsf, mul2(pair_of(s.delta[rr]), sum[1])));
+              if (a.softplus) ddt = mul2(ddt, scan_sigmoid(add2(row_pair<T, CH>(raw[1][rr]), bias)));
+              out_x.put(to, fma2(skip, dsf, mul2(pair_of<CH>(s.delta[rr]), sum[1])));
               out_dt.put(to, ddt);
               if (a.z) {
-                const Two z = row_pair<T>(s.raw[2][rr]), sg = scan_sigmoid(z);
+                const Two z = row_pair<T, CH>(raw[2][rr]), sg = scan_sigmoid(z);
                 const Two slope = mul2(sg, fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
-                out_z.put(to, mul2(mul2(row_pair<T>(s.raw[3][rr]), inner), slope));
+                out_z.put(to, mul2(mul2(row_pair<T, CH>(raw[3][rr]), inner), slope));
               }
               sum_d = fma2(dsf, xf, sum_d);
               sum_bias = add2(sum_bias, ddt);
@@ -381,26 +400,39 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           }
         }
         __syncthreads();
-        if (threadIdx.x < kScanRows * kStates) {
+        if (threadIdx.x < kTileRows * kStates) {
           const int r = threadIdx.x / kStates, v = threadIdx.x % kStates;
           if (r < rows) {
             const Two f = add2(add2(s_bc[0][r][v], s_bc[1][r][v]), add2(s_bc[2][r][v], s_bc[3][r][v]));
-            const int64_t row = ((int64_t)quad * l.tokens + row0 + i * kScanRows + r) * a.groups + group;
+            const int64_t row = ((int64_t)quad * l.tokens + row0 + i * kTileRows + r) * a.groups + group;
             *reinterpret_cast<Two*>(&g.bc[(row * 2 + v / (2 * NN)) * l.pad + n0 + v % (2 * NN) * 2]) = f;
           }
         }
         __syncthreads();
       }
     }
-    write_pad<NN>(g.part_a + (int64_t)run * a.channels * l.pad, da, t, l.pad, n0);
+    if (placed) {
+      float* to = g.part_a + (int64_t)run * l.wide * l.pad + mine + n0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float f[2][NN];
+#pragma unroll
+        for (int n = 0; n < NN; ++n) {
+          const float2 v = parts(da[j][n]);
+          f[0][n] = v.x, f[1][n] = v.y;
+        }
+        write_numbers<NN>(to + 2 * j * l.pad, f[0]);
+        write_numbers<NN>(to + (2 * j + 1) * l.pad, f[1]);
+      }
+    }
   }
+  wait_for_copies<0>();
   sum_d = add2(sum_d, __shfl_xor_sync(0xffffffffu, sum_d, 16));
   sum_bias = add2(sum_bias, __shfl_xor_sync(0xffffffffu, sum_bias, 16));
-  if (o == 0) {
-    const float2 fd = parts(sum_d), fb = parts(sum_bias);
-    float* to = g.part_d + (int64_t)run * 2 * a.channels + t.first + 2 * p;
-    if (2 * p < t.count) to[0] = fd.x, to[a.channels] = fb.x;
-    if (2 * p + 1 < t.count) to[1] = fd.y, to[a.channels + 1] = fb.y;
+  if (o == 0 && placed) {
+    float* to = g.part_d + (int64_t)run * 2 * l.wide + t.place + 2 * p;
+    *reinterpret_cast<Two*>(to) = sum_d;
+    *reinterpret_cast<Two*>(to + l.wide) = sum_bias;
   }
 }
 
@@ -424,13 +456,13 @@ __global__ void __launch_bounds__(512) k_scan_sums(ScanBackwardLaunch g) {
     ((T*)(which ? g.g.dc : g.g.db))[rg * a.states + n] = RowType<T>::from(sum);
     return;
   }
-  const int64_t per_a = (int64_t)a.channels * l.pad, width = per_a + 2 * (int64_t)a.channels;
+  const int64_t per_a = (int64_t)l.wide * l.pad, width = per_a + 2 * (int64_t)l.wide;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t o = (blockIdx.x - rows_blocks) * 32 + x;
   float sum = 0.f;
   if (o < width) {
     const float* part = o < per_a ? g.part_a + o : g.part_d + (o - per_a);
-    const int64_t stride = o < per_a ? per_a : 2 * (int64_t)a.channels;
+    const int64_t stride = o < per_a ? per_a : 2 * (int64_t)l.wide;
     for (int r = y; r < g.runs; r += 16) sum += part[r * stride];
   }
   s[y][x] = sum;
@@ -438,14 +470,17 @@ __global__ void __launch_bounds__(512) k_scan_sums(ScanBackwardLaunch g) {
   if (y || o >= width) return;
 #pragma unroll
   for (int i = 1; i < 16; ++i) sum += s[i][x];
+  const int64_t place = o < per_a ? o / l.pad : (o - per_a) % l.wide;
+  const int per = a.channels / a.groups, in = (int)(place % l.group_pad);
+  if (in >= per) return;
+  const int64_t c = place / l.group_pad * per + in;
   if (o < per_a) {
-    const int64_t c = o / l.pad;
-    const int n = (int)(o - c * l.pad);
+    const int n = (int)(o % l.pad);
     if (n < a.states) g.g.da[c * a.states + n] = sum;
-  } else if (o - per_a < a.channels) {
-    if (g.g.dd) g.g.dd[o - per_a] = sum;
+  } else if (o - per_a < l.wide) {
+    if (g.g.dd) g.g.dd[c] = sum;
   } else if (g.g.ddt_bias) {
-    g.g.ddt_bias[o - per_a - a.channels] = sum;
+    g.g.ddt_bias[c] = sum;
   }
 }
 
@@ -455,14 +490,15 @@ cudaError_t go_carry(const ScanBackwardLaunch& g, cudaStream_t s) {
   const int bytes = kWarps * sizeof(CarryShared<T, NN>);
   const cudaError_t e = allow_shared(k_scan_carry<T, NN>, bytes, ready);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)((int64_t)g.f.segments * g.f.blocks_x), g.f.pad / (4 * NN));
+  const int64_t blocks_x = ((int64_t)g.f.a.groups * g.f.group_tiles + kWarps - 1) / kWarps;
+  const dim3 grid((unsigned)(g.f.segments * blocks_x), g.f.pad / (2 * NN));
   k_scan_carry<T, NN><<<grid, 32 * kWarps, bytes, s>>>(g);
   return cudaGetLastError();
 }
 template <class T, int NN, bool kMany>
 cudaError_t go_back(const ScanBackwardLaunch& g, cudaStream_t s) {
   static std::atomic<bool> ready[kMaxDevices];
-  const int bytes = kWarps * (sizeof(BackShared<T, NN>) + kScanRows * 8 * NN * sizeof(float));
+  const int bytes = kWarps * (sizeof(BackShared<T, NN>) + kTileRows * 8 * NN * sizeof(float));
   const cudaError_t e = allow_shared(k_scan_backward<T, NN, kMany>, bytes, ready);
   if (e != cudaSuccess) return e;
   return launch_early(k_scan_backward<T, NN, kMany>, (unsigned)((int64_t)g.runs * g.f.a.groups * g.quads), 32 * kWarps, bytes, s,
@@ -470,28 +506,23 @@ cudaError_t go_back(const ScanBackwardLaunch& g, cudaStream_t s) {
 }
 template <class T>
 cudaError_t back(const ScanBackwardLaunch& g, cudaStream_t s) {
-  if (g.f.nn == 2) return go_back<T, 2, false>(g, s);
+  if (g.f.pass == 8) return go_back<T, 2, false>(g, s);
   return g.f.pad == 16 ? go_back<T, 4, false>(g, s) : go_back<T, 4, true>(g, s);
 }
 template <class T>
 cudaError_t carry(const ScanBackwardLaunch& g, cudaStream_t s) {
-  return g.f.nn == 2 ? go_carry<T, 2>(g, s) : go_carry<T, 4>(g, s);
+  return g.f.pass == 8 ? go_carry<T, 4>(g, s) : go_carry<T, 8>(g, s);
 }
 
 }  // namespace
 
-cudaError_t launch_scan_back_states(const void* args, cudaStream_t s) {
+cudaError_t launch_scan_carry(const void* args, cudaStream_t s) {
   const ScanBackwardLaunch& g = *(const ScanBackwardLaunch*)args;
   switch (g.f.a.type) {
     case TB_TYPE_F32: return carry<float>(g, s);
     case TB_TYPE_F16: return carry<__half>(g, s);
     default: return carry<__nv_bfloat16>(g, s);
   }
-}
-cudaError_t launch_scan_back_join(const void* args, cudaStream_t s) {
-  const ScanBackwardLaunch& g = *(const ScanBackwardLaunch*)args;
-  const int64_t items = (int64_t)g.f.a.channels * (g.f.pad / 4);
-  return launch_early(k_scan_join_back, (unsigned)((items + 127) / 128 * g.f.grids), 128, 0, s, true, g);
 }
 cudaError_t launch_scan_backward(const void* args, cudaStream_t s) {
   const ScanBackwardLaunch& g = *(const ScanBackwardLaunch*)args;
@@ -505,7 +536,7 @@ cudaError_t launch_scan_sums(const void* args, cudaStream_t s) {
   const ScanBackwardLaunch& g = *(const ScanBackwardLaunch*)args;
   const tb_scan_args& a = g.f.a;
   const int64_t rows = (g.f.tokens * a.groups * 2 * a.states + 511) / 512;
-  const int64_t columns = ((int64_t)a.channels * (g.f.pad + 2) + 31) / 32;
+  const int64_t columns = ((int64_t)g.f.wide * (g.f.pad + 2) + 31) / 32;
   auto go = [&](auto kernel) { return launch_early(kernel, (unsigned)(rows + columns), 512, 0, s, g.runs > 0, g); };
   switch (a.type) {
     case TB_TYPE_F32: return go(k_scan_sums<float>);

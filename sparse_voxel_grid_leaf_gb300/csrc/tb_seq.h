@@ -92,21 +92,24 @@ struct ConvStepLaunch {
 cudaError_t launch_conv_step(const void* args, cudaStream_t s);
 
 // ------------------------------------------------------------- selective scan
-constexpr int kScanChannels = 32;  // of a warp
-constexpr int kScanChunk = 64;     // rows that the gradient takes at a time
+constexpr int kTileRows = 8;       // of a tile in shared memory
+constexpr int kScanChannels = 64;  // of a walk's warp
 struct ScanLaunch {
   tb_scan_args a;
   const int64_t* offsets;     // as in LinLaunch: the walks of tb_linattn.cuh
   int64_t tokens;
   int32_t grids;
-  int32_t segment, segments;  // rows of one, 0: whole grids; slots
+  int32_t segment, segments;  // rows of one, a multiple of kTileRows, 0: whole grids; slots
   int32_t group_tiles;        // tiles of kScanChannels channels of a group
-  int32_t blocks_x;           // blocks of a slot
-  int32_t pad;                // states of a channel in the workspace, a multiple of 4 * nn
-  int32_t nn;                 // states of a lane
+  int32_t group_pad, wide;    // channels of a group and of all in the workspace
+  int32_t pad;                // states of a channel in the workspace: a multiple of those of a pass
+  int32_t pass;               // states of a pass: 8 or 16
+  int32_t warps, blocks_x;    // of a block; blocks of a slot
   int32_t vec;                // rows that 16-byte copies can read
-  float* seg;                 // [segments, channels, pad]: states of the segments, then those they start from
-  float* sum;                 // [segments, channels]: their sums of delta
+  float* seg;                 // [segments, wide, pad]: states of the segments, then those they start from
+  float* sum;                 // [segments, wide]: their sums of delta
+  float* tile;                // [segments, tiles, wide, pad]: states before the tiles of kTileRows rows, from the segment's
+  float* tile_sum;            // [segments, tiles, wide]: and sums of delta before them; NULL but in the gradient
 };
 cudaError_t launch_scan(const void* args, cudaStream_t s);
 cudaError_t launch_scan_states(const void* args, cudaStream_t s);
@@ -114,15 +117,15 @@ cudaError_t launch_scan_join(const void* args, cudaStream_t s);
 struct ScanBackwardLaunch {
   ScanLaunch f;               // in chunks
   tb_scan_backward_args g;
-  float* seg_back;            // [segments, channels, pad]: the gradient's own sums of the chunks, then what enters them
+  float* seg_back;            // [segments, wide, pad]: the gradient's own sums of the chunks, then what enters them
   float* bc;                  // [quads, tokens, groups, 2, pad]: parts of db and dc
-  float* part_a;              // [runs, channels, pad]: parts of da
-  float* part_d;              // [runs, 2, channels]: parts of dd and ddt_bias
+  float* part_a;              // [runs, wide, pad]: parts of da
+  float* part_d;              // [runs, 2, wide]: parts of dd and ddt_bias
   float* acc;                 // [tokens, channels, 3] sums over the states, where they are more than a pass takes; or NULL
   int32_t quads, runs, per_run;
 };
 cudaError_t launch_scan_backward(const void* args, cudaStream_t s);
-cudaError_t launch_scan_back_states(const void* args, cudaStream_t s);
+cudaError_t launch_scan_carry(const void* args, cudaStream_t s);
 cudaError_t launch_scan_back_join(const void* args, cudaStream_t s);
 cudaError_t launch_scan_sums(const void* args, cudaStream_t s);
 struct ScanStepLaunch {

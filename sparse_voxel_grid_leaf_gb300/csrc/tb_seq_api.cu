@@ -408,12 +408,16 @@ tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream stream) {
 
 // ----------------------------------------------------------- selective scan
 
-// Tiles of kScanChannels channels and blocks of states; 4 warps of tiles a block.
+// Tiles of kScanChannels channels and blocks of states; four warps of tiles a
+// block, fewer where their states would not fit in shared memory.
 static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t groups) {
   l.group_tiles = (int32_t)up(channels / groups, kScanChannels);
-  l.blocks_x = (int32_t)up((int64_t)groups * l.group_tiles, 4);
-  l.nn = states <= 8 ? 2 : 4;
-  l.pad = (int32_t)up(states, 4 * l.nn) * 4 * l.nn;
+  l.group_pad = l.group_tiles * kScanChannels;
+  l.wide = l.group_pad * groups;
+  l.pass = states <= 8 ? 8 : 16;
+  l.pad = (int32_t)up(states, l.pass) * l.pass;
+  l.warps = l.pad <= 32 ? 4 : l.pad <= 128 ? 2 : 1;
+  l.blocks_x = (int32_t)up((int64_t)groups * l.group_tiles, l.warps);
 }
 
 // Rows of a segment of the forward pass, 0: grids are walked whole.  A walk is
@@ -421,14 +425,14 @@ static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t 
 // segments' own states cost most of a walk once more.
 static int32_t scan_segment(int64_t tokens, int32_t grids, int32_t groups, int32_t group_tiles, int sms) {
   const int64_t walks = (int64_t)grids * groups * group_tiles;
-  if (grids <= 0 || walks >= 8ll * sms || tokens < 256ll * grids) return 0;
+  if (grids <= 0 || walks >= 4ll * sms || tokens < 256ll * grids) return 0;
   int64_t seg = up(up(tokens * groups * group_tiles, 12 * sms), 64) * 64;
   if (seg < 64) seg = 64;
   return tokens >= 2 * seg * grids ? (int32_t)seg : 0;
 }
 
 struct ScanCarve {
-  int64_t seg, sum, seg_back, bc, part_a, part_d, acc, bytes;
+  int64_t seg, sum, tile, tile_sum, seg_back, bc, part_a, part_d, acc, bytes;
   int32_t quads, runs, per_run;
 };
 static ScanCarve scan_carve(int64_t slots, int64_t tokens, int32_t channels, int32_t groups, const ScanLaunch& l, bool backward,
@@ -439,20 +443,28 @@ static ScanCarve scan_carve(int64_t slots, int64_t tokens, int32_t channels, int
     c.bytes += up(floats * 4, 256) * 256;
     return at;
   };
-  c.seg = take(slots * channels * l.pad);
-  c.sum = take(slots * channels);
+  c.seg = take(slots * l.wide * l.pad);
+  c.sum = take(slots * l.wide);
   if (!backward) return c;
-  c.quads = (int32_t)up(l.group_tiles, 4);
+  c.tile = take(slots * (l.segment / kTileRows) * l.wide * l.pad);
+  c.tile_sum = take(slots * (l.segment / kTileRows) * l.wide);
+  c.quads = (int32_t)up(channels / groups, 128);
   // blocks take runs of chunks, whose parts of da they keep in registers: as many as make six waves or so
   const int64_t blocks = slots * groups * c.quads;
   c.per_run = (int32_t)up(blocks, 12ll * sms);
   c.runs = (int32_t)up(slots, c.per_run > 0 ? c.per_run : 1);
-  c.seg_back = take(slots * channels * l.pad);
+  c.seg_back = take(slots * l.wide * l.pad);
   c.bc = take((int64_t)c.quads * tokens * groups * 2 * l.pad);
-  c.part_a = take((int64_t)c.runs * channels * l.pad);
-  c.part_d = take((int64_t)c.runs * 2 * channels);
-  if (l.pad > 4 * l.nn) c.acc = take(tokens * channels * 3);
+  c.part_a = take((int64_t)c.runs * l.wide * l.pad);
+  c.part_d = take((int64_t)c.runs * 2 * l.wide);
+  if (l.pad > l.pass) c.acc = take(tokens * channels * 3);
   return c;
+}
+
+// Rows of a chunk of the gradient.
+static int32_t scan_chunk(int64_t tokens, int32_t grids, int32_t wide, int sms) {
+  (void)tokens, (void)grids, (void)wide, (void)sms;
+  return 64;
 }
 
 int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t channels, int32_t states, int32_t groups,
@@ -462,9 +474,9 @@ int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t chann
   scan_shape(l, channels, states, groups);
   int sms = seq_sms();
   if (!sms) sms = 256;
-  const int32_t seg = backward ? kScanChunk : scan_segment(tokens, grids, groups, l.group_tiles, sms);
-  if (!seg) return 0;
-  return scan_carve(segment_slots(tokens, grids, seg), tokens, channels, groups, l, backward, sms).bytes;
+  l.segment = backward ? scan_chunk(tokens, grids, l.wide, sms) : scan_segment(tokens, grids, groups, l.group_tiles, sms);
+  if (!l.segment) return 0;
+  return scan_carve(segment_slots(tokens, grids, l.segment), tokens, channels, groups, l, backward, sms).bytes;
 }
 
 static tb_status scan_sizes(const char* what, int64_t rows, int32_t channels, int32_t states, int32_t groups, int32_t type) {
@@ -482,10 +494,10 @@ static tb_status scan_plan(const char* what, ScanLaunch& l, bool backward, ScanC
   const int size = type_size(a.type);
   scan_shape(l, a.channels, a.states, a.groups);
   l.offsets = a.offsets, l.tokens = a.tokens, l.grids = a.grids;
-  l.segment = backward ? kScanChunk : scan_segment(a.tokens, a.grids, a.groups, l.group_tiles, sms);
+  l.segment = backward ? scan_chunk(a.tokens, a.grids, l.wide, sms) : scan_segment(a.tokens, a.grids, a.groups, l.group_tiles, sms);
   const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
-  const int64_t per_slot = (int64_t)a.groups * up(l.group_tiles, 4) + l.blocks_x;
-  const int64_t join = up((int64_t)a.channels * (l.pad / 4), 128);
+  const int64_t per_slot = (int64_t)a.groups * l.group_tiles;
+  const int64_t join = up((int64_t)l.wide * (l.pad / 4), 128);
   if (slots > kMaxRows / per_slot || a.grids > kMaxRows / join ||
       (backward && a.tokens > kMaxRows / (up((int64_t)a.groups * 2 * a.states, 512) + 1) - join * 32))
     return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 blocks or more", what);
@@ -500,6 +512,10 @@ static tb_status scan_plan(const char* what, ScanLaunch& l, bool backward, ScanC
                     (long long)c.bytes);
   l.seg = (float*)((char*)a.workspace + c.seg);
   l.sum = (float*)((char*)a.workspace + c.sum);
+  if (backward) {
+    l.tile = (float*)((char*)a.workspace + c.tile);
+    l.tile_sum = (float*)((char*)a.workspace + c.tile_sum);
+  }
   return TB_OK;
 }
 
@@ -563,8 +579,7 @@ tb_status tb_selective_scan_backward(const tb_scan_backward_args* args, tb_strea
   const cudaStream_t s = (cudaStream_t)stream;
   if (a.grids) {
     TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, s, launch_scan_states, &g.f));
-    TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, s, launch_scan_back_states, &g));
-    TB_SEQ_CUDA(seq_launch(kSeqSelectiveJoin, s, launch_scan_join, &g.f));
+    TB_SEQ_CUDA(seq_launch(kSeqSelectiveStates, s, launch_scan_carry, &g));
     TB_SEQ_CUDA(seq_launch(kSeqSelectiveJoin, s, launch_scan_back_join, &g));
     TB_SEQ_CUDA(seq_launch(kSeqSelectiveBackward, s, launch_scan_backward, &g));
   }
