@@ -82,22 +82,54 @@ __device__ __forceinline__ Pack<T, V> conv_row(const tb_conv_args& a, int b, int
   return r;
 }
 
+// V channels in pairs (V = 1: one number twice, the second one not used).
+template <class T, int V>
+__device__ __forceinline__ void to_pairs(const Pack<T, V>& p, f32x2 (&f)[(V + 1) / 2]) {
+  float x[V];
+  unpack<T, V>(p, x);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) f[v / 2] = pair(x[v], x[V > 1 ? v + 1 : v]);
+}
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> from_pairs(const f32x2 (&f)[(V + 1) / 2]) {
+  float x[V];
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const float2 y = halves(f[v / 2]);
+    x[v] = y.x;
+    if (V > 1) x[V > 1 ? v + 1 : v] = y.y;
+  }
+  return pack<T, V>(x);
+}
 template <class T, int V, int K>
 struct ConvWeight {
-  float w[K][V], bias[V];
+  static constexpr int P = (V + 1) / 2;
+  f32x2 w[K][P], bias[P];
   __device__ __forceinline__ ConvWeight(const void* weight, const void* b, int c) {
+    auto at = [&](int v, int k) { return RowType<T>::to(((const T*)weight)[(int64_t)(c + v) * K + k]); };
+    auto of = [&](int v) { return b ? RowType<T>::to(((const T*)b)[c + v]) : 0.f; };
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < V; v += 2) {
+      const int second = V > 1 ? v + 1 : v;
 #pragma unroll
-      for (int k = 0; k < K; ++k) w[k][v] = RowType<T>::to(((const T*)weight)[(int64_t)(c + v) * K + k]);
-      bias[v] = b ? RowType<T>::to(((const T*)b)[c + v]) : 0.f;
+      for (int k = 0; k < K; ++k) w[k][v / 2] = pair(at(v, k), at(second, k));
+      bias[v / 2] = pair(of(v), of(second));
     }
   }
 };
 
-// sigmoid(x): at the ends of the range the exponential is 0 or infinite and the
-// quotient 1 or 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// sigmoid(x) = 1 / (1 + exp(-x)): at the ends of the range the exponential is 0
+// or infinite and the quotient 1 or 0.
+__device__ __forceinline__ f32x2 sigmoid(f32x2 x) {
+  const float2 e = halves(mul2(x, both(-1.4426950408889634f)));
+  float2 u;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u.x) : "f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(u.y) : "f"(e.y));
+  const float2 w = halves(add2(pair(u.x, u.y), both(1.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u.x) : "f"(w.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(u.y) : "f"(w.y));
+  return pair(u.x, u.y);
+}
 
 // The last taps - 1 rows of state and grid together.
 template <class T, int V, int K>
@@ -124,7 +156,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
     return;
   }
   const ConvWeight<T, V, K> w(a.weight, a.bias, c);
-  constexpr int B = 4;  // rows in flight
+  constexpr int P = (V + 1) / 2, B = 8;  // pairs of channels; rows in flight
   ConvPieces pieces(a, run * l.run, min((run + 1) * l.run, a.tokens));
   while (pieces.at < pieces.end) {
     int64_t r0, r1;
@@ -134,12 +166,9 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
       for (int64_t r = r0; r < r1; ++r, to += a.y_row) store_pack<T, V>(to, Pack<T, V>{});
       continue;
     }
-    float x[K - 1][V];  // the rows before, oldest first
+    f32x2 x[K][P];  // the rows before, oldest first, and the row
 #pragma unroll
-    for (int i = 0; i < K - 1; ++i) {
-      const Pack<T, V> p = conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c);
-      unpack<T, V>(p, x[i]);
-    }
+    for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
     const T* from = (const T*)a.x + r0 * a.x_row + c;
     Pack<T, V> ahead[B];
     const int n = (int)(r1 - r0);
@@ -147,82 +176,76 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
     for (int i = 0; i < B; ++i)
       if (i < n) ahead[i] = load_pack<T, V>(from + i * a.x_row);
     for (int base = 0; base < n; base += B) {
-      Pack<T, V> now[B];
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        now[i] = ahead[i];
-        if (base + B + i < n) ahead[i] = load_pack<T, V>(from + (base + B + i) * a.x_row);
-      }
 #pragma unroll
       for (int i = 0; i < B; ++i)
         if (base + i < n) {
-          float f[V], o[V];
-          unpack<T, V>(now[i], f);
+          f32x2 o[P];
+          to_pairs<T, V>(ahead[i], x[K - 1]);
+          if (base + B + i < n) ahead[i] = load_pack<T, V>(from + (base + B + i) * a.x_row);
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            float s = w.bias[v];
+          for (int v = 0; v < P; ++v) {
+            f32x2 s = w.bias[v];
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k) s = fmaf(w.w[k][v], x[k][v], s);
-            s = fmaf(w.w[K - 1][v], f[v], s);
-            o[v] = a.silu ? s * sigmoid(s) : s;
+            for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
+            o[v] = a.silu ? mul2(s, sigmoid(s)) : s;
 #pragma unroll
-            for (int k = 0; k < K - 2; ++k) x[k][v] = x[k + 1][v];
-            x[K - 2][v] = f[v];
+            for (int k = 0; k < K - 1; ++k) x[k][v] = x[k + 1][v];
           }
-          store_pack<T, V>(to + (base + i) * a.y_row, pack<T, V>(o));
+          store_pack<T, V>(to + (base + i) * a.y_row, from_pairs<T, V>(o));
         }
     }
   }
 }
 
 // The gradient of pre from that of y.
-__device__ __forceinline__ float conv_slope(float dy, float pre, int silu) {
+__device__ __forceinline__ f32x2 conv_slope(f32x2 dy, f32x2 pre, int silu) {
   if (!silu) return dy;
-  const float s = sigmoid(pre);
-  return dy * (s * fmaf(pre, 1.f - s, 1.f));
+  const f32x2 s = sigmoid(pre), rest = fma2(s, both(-1.f), both(1.f));
+  return mul2(dy, mul2(s, fma2(pre, rest, both(1.f))));
 }
 
 // The gradient of a grid's first state: its row m is the tap m - p of the row at
 // place p, and in a grid of fewer than taps - 1 rows part of the last state.
 template <class T, int V, int K>
 __device__ __forceinline__ void conv_first(const ConvBackwardLaunch& l, int b, int c) {
+  constexpr int P = (V + 1) / 2;
   const tb_conv_args& a = l.f.a;
   const tb_conv_backward_args& g = l.g;
   int64_t begin, end;
   conv_grid(a, b, begin, end);
   const ConvWeight<T, V, K> w(a.weight, a.bias, c);
-  float sum[K - 1][V] = {}, x[2 * K - 2][V];
+  f32x2 sum[K - 1][P] = {}, x[2 * K - 2][P];
 #pragma unroll
   for (int i = 0; i < 2 * K - 2; ++i) {
     Pack<T, V> p{};
     if (i - (K - 1) < end - begin) p = conv_row<T, V, K>(a, b, begin, i - (K - 1), c);
-    unpack<T, V>(p, x[i]);
+    to_pairs<T, V>(p, x[i]);
   }
 #pragma unroll
   for (int p = 0; p < K - 1; ++p) {
     if (p >= end - begin) break;
-    float dy[V];
-    unpack<T, V>(load_pack<T, V>((const T*)g.dy + (begin + p) * g.dy_row + c), dy);
+    f32x2 dy[P];
+    to_pairs<T, V>(load_pack<T, V>((const T*)g.dy + (begin + p) * g.dy_row + c), dy);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float s = w.bias[v];
+    for (int v = 0; v < P; ++v) {
+      f32x2 s = w.bias[v];
 #pragma unroll
-      for (int k = 0; k < K; ++k) s = fmaf(w.w[k][v], x[p + k][v], s);
-      const float d = conv_slope(dy[v], s, a.silu);
+      for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[p + k][v], s);
+      const f32x2 d = conv_slope(dy[v], s, a.silu);
 #pragma unroll
-      for (int m = p; m < K - 1; ++m) sum[m][v] = fmaf(w.w[m - p][v], d, sum[m][v]);
+      for (int m = p; m < K - 1; ++m) sum[m][v] = fma2(w.w[m - p][v], d, sum[m][v]);
     }
   }
 #pragma unroll
   for (int m = 0; m < K - 1; ++m) {
     const int64_t i = m - (end - begin);
     if (g.dstate_out && i >= 0) {
-      float f[V];
-      unpack<T, V>(load_pack<T, V>((const T*)g.dstate_out + ((int64_t)b * (K - 1) + i) * a.channels + c), f);
+      f32x2 f[P];
+      to_pairs<T, V>(load_pack<T, V>((const T*)g.dstate_out + ((int64_t)b * (K - 1) + i) * a.channels + c), f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[m][v] += f[v];
+      for (int v = 0; v < P; ++v) sum[m][v] = add2(sum[m][v], f[v]);
     }
-    store_pack<T, V>((T*)g.dstate + ((int64_t)b * (K - 1) + m) * a.channels + c, pack<T, V>(sum[m]));
+    store_pack<T, V>((T*)g.dstate + ((int64_t)b * (K - 1) + m) * a.channels + c, from_pairs<T, V>(sum[m]));
   }
 }
 
@@ -233,7 +256,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
   let_next_kernel_start();
   const tb_conv_args& a = l.f.a;
   const tb_conv_backward_args& g = l.g;
-  __shared__ float s_part[kConvThreads][V];
+  __shared__ f32x2 s_part[kConvThreads][(V + 1) / 2];
   const int bx = (int)(blockIdx.x % l.f.blocks_x), per_x = l.f.per_x, per_y = kConvThreads / per_x;
   const int64_t by = blockIdx.x / l.f.blocks_x;
   const int c = (bx * per_x + (int)threadIdx.x % per_x) * V, y = (int)threadIdx.x / per_x;
@@ -244,7 +267,8 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
     return;
   }
   const int64_t run = by * per_y + y;
-  float dw[K][V] = {}, db[V] = {};
+  constexpr int P = (V + 1) / 2;
+  f32x2 dw[K + 1][P] = {};  // the last one: dbias
   if (live && run < l.f.runs) {
     const ConvWeight<T, V, K> w(a.weight, a.bias, c);
     ConvPieces pieces(a, run * l.f.run, min((run + 1) * l.f.run, a.tokens));
@@ -256,17 +280,14 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
         for (int64_t r = r0; r < r1; ++r, to += g.dx_row) store_pack<T, V>(to, Pack<T, V>{});
         continue;
       }
-      float x[K][V], d[K][V] = {};  // rows of x and gradients of pre, the last one at [K - 1]
+      f32x2 x[K][P], d[K][P] = {};  // rows of x and gradients of pre, the last one at [K - 1]
 #pragma unroll
-      for (int i = 1; i < K; ++i) {
-        const Pack<T, V> p = conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - K + i, c);
-        unpack<T, V>(p, x[i]);
-      }
+      for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
       const T* from = (const T*)a.x + r0 * a.x_row + c;
       const T* grad = (const T*)g.dy + r0 * g.dy_row + c;
-      const int own = (int)(r1 - r0);                                       // rows of the run
-      const int have = (int)min(pieces.past - r0, (int64_t)own + K - 1);    // rows whose pre has a part in them
-      constexpr int B = 2;
+      const int own = (int)(r1 - r0);                                     // rows of the run
+      const int have = (int)min(pieces.past - r0, (int64_t)own + K - 1);  // rows whose pre has a part in them
+      constexpr int B = 4;
       Pack<T, V> ax[B], ad[B];
       auto load = [&](int i, int u) {
         if (u < have) {
@@ -277,58 +298,58 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
 #pragma unroll
       for (int i = 0; i < B; ++i) load(i, i);
       for (int base = 0; base < own + K - 1; base += B) {
-        Pack<T, V> nx[B], nd[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-          nx[i] = ax[i];
-          nd[i] = ad[i];
-          load(i, base + B + i);
-        }
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-          const int u = base + i;
+          const int u = base + i, t = u - (K - 1);
           if (u >= own + K - 1) break;
-          float f[V] = {}, e[V] = {};
+          f32x2 e[P];
+          to_pairs<T, V>(ax[i], x[K - 1]);
+          to_pairs<T, V>(ad[i], e);
+          load(i, u + B);
           if (u < have) {
-            unpack<T, V>(nx[i], f);
-            unpack<T, V>(nd[i], e);
+#pragma unroll
+            for (int v = 0; v < P; ++v) {
+              f32x2 s = w.bias[v];
+#pragma unroll
+              for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
+              d[K - 1][v] = conv_slope(e[v], s, a.silu);
+            }
+            if (u < own) {
+#pragma unroll
+              for (int v = 0; v < P; ++v) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) dw[k][v] = fma2(d[K - 1][v], x[k][v], dw[k][v]);
+                dw[K][v] = add2(dw[K][v], d[K - 1][v]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < P; ++v) d[K - 1][v] = 0;
+          }
+          if (t >= 0) {
+            f32x2 o[P];
+#pragma unroll
+            for (int v = 0; v < P; ++v) {
+              o[v] = mul2(w.w[K - 1][v], d[0][v]);
+#pragma unroll
+              for (int k = 1; k < K; ++k) o[v] = fma2(w.w[K - 1 - k][v], d[k][v], o[v]);
+            }
+            const int64_t left = pieces.past - 1 - (r0 + t);
+            if (g.dstate_out && left < K - 1) {
+              f32x2 f[P];
+              to_pairs<T, V>(load_pack<T, V>((const T*)g.dstate_out + ((int64_t)b * (K - 1) + K - 2 - left) * a.channels + c), f);
+#pragma unroll
+              for (int v = 0; v < P; ++v) o[v] = add2(o[v], f[v]);
+            }
+            store_pack<T, V>(to + t * g.dx_row, from_pairs<T, V>(o));
           }
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
+          for (int v = 0; v < P; ++v)
 #pragma unroll
             for (int k = 0; k < K - 1; ++k) {
               x[k][v] = x[k + 1][v];
               d[k][v] = d[k + 1][v];
             }
-            x[K - 1][v] = f[v];
-            float s = w.bias[v];
-#pragma unroll
-            for (int k = 0; k < K; ++k) s = fmaf(w.w[k][v], x[k][v], s);
-            d[K - 1][v] = u < have ? conv_slope(e[v], s, a.silu) : 0.f;
-            if (u < own) {
-#pragma unroll
-              for (int k = 0; k < K; ++k) dw[k][v] = fmaf(d[K - 1][v], x[k][v], dw[k][v]);
-              db[v] += d[K - 1][v];
-            }
-          }
-          const int t = u - (K - 1);
-          if (t >= 0) {
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              o[v] = 0.f;
-#pragma unroll
-              for (int k = 0; k < K; ++k) o[v] = fmaf(w.w[K - 1 - k][v], d[k][v], o[v]);
-            }
-            const int64_t left = pieces.past - 1 - (r0 + t);
-            if (g.dstate_out && left < K - 1) {
-              float f2[V];
-              unpack<T, V>(load_pack<T, V>((const T*)g.dstate_out + ((int64_t)b * (K - 1) + K - 2 - left) * a.channels + c), f2);
-#pragma unroll
-              for (int v = 0; v < V; ++v) o[v] += f2[v];
-            }
-            store_pack<T, V>(to + t * g.dx_row, pack<T, V>(o));
-          }
         }
       }
     }
@@ -336,20 +357,22 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
   float* part = g.workspace + by * (K + 1) * a.channels + c;
 #pragma unroll
   for (int k = 0; k <= K; ++k) {
-    float* mine = k < K ? dw[k < K ? k : 0] : db;
     if (per_y > 1) {
       if (k) __syncthreads();
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_part[threadIdx.x][v] = mine[v];
+      for (int v = 0; v < P; ++v) s_part[threadIdx.x][v] = dw[k][v];
       __syncthreads();
       if (y == 0)
         for (int i = 1; i < per_y; ++i)
 #pragma unroll
-          for (int v = 0; v < V; ++v) mine[v] += s_part[threadIdx.x + i * per_x][v];
+          for (int v = 0; v < P; ++v) dw[k][v] = add2(dw[k][v], s_part[threadIdx.x + i * per_x][v]);
     }
     if (live && y == 0)
 #pragma unroll
-      for (int v = 0; v < V; ++v) part[(int64_t)k * a.channels + v] = mine[v];
+      for (int v = 0; v < V; ++v) {
+        const float2 f = halves(dw[k][v / 2]);
+        part[(int64_t)k * a.channels + v] = v % 2 ? f.y : f.x;
+      }
   }
 }
 
@@ -403,20 +426,21 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvStepLaunch l) {
   for (int i = 0; i < K - 1; ++i) row[i] = load_pack<T, V>(state + (int64_t)i * a.channels);
   row[K - 1] = load_pack<T, V>((const T*)a.x + n * a.x_row + c);
   const ConvWeight<T, V, K> w(a.weight, a.bias, c);
-  float o[V];
+  constexpr int P = (V + 1) / 2;
+  f32x2 o[P];
 #pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = w.bias[v];
+  for (int v = 0; v < P; ++v) o[v] = w.bias[v];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    float f[V];
-    unpack<T, V>(row[k], f);
+    f32x2 f[P];
+    to_pairs<T, V>(row[k], f);
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = fmaf(w.w[k][v], f[v], o[v]);
+    for (int v = 0; v < P; ++v) o[v] = fma2(w.w[k][v], f[v], o[v]);
     if (k) store_pack<T, V>(state + (int64_t)(k - 1) * a.channels, row[k]);
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = a.silu ? o[v] * sigmoid(o[v]) : o[v];
-  store_pack<T, V>(to, pack<T, V>(o));
+  for (int v = 0; v < P; ++v) o[v] = a.silu ? mul2(o[v], sigmoid(o[v])) : o[v];
+  store_pack<T, V>(to, from_pairs<T, V>(o));
 }
 
 template <class T, int V, int K>

@@ -15,13 +15,13 @@ namespace {
 
 constexpr int CH = kScanChannels;
 
-// One warp's shared memory.
-template <class T, int NN, bool kOut>
+// One warp's shared memory.  kParts: rows whose sums wait for their outputs.
+template <class T, int NN, int kParts>
 struct alignas(16) WalkShared {
-  T raw[2][kOut ? 3 : 2][kTileRows][CH];  // x, dt, z of two tiles
+  T raw[2][kParts ? 3 : 2][kTileRows][CH];  // x, dt, z of two tiles
   float delta[kTileRows][CH], dx[kTileRows][CH];
-  float b[kTileRows][2 * NN], c[kOut ? kTileRows : 1][2 * NN];
-  float part[kOut ? kTileRows : 1][2][CH];  // c . h over a lane's states
+  float b[kTileRows][2 * NN], c[kParts ? kTileRows : 1][2 * NN];
+  float part[kParts ? kParts : 1][2][CH];  // c . h over a lane's states
 };
 template <int NN>
 constexpr int kept_floats() { return 32 * 4 * NN; }  // of a warp's states of a pass
@@ -31,13 +31,17 @@ constexpr int kept_floats() { return 32 * 4 * NN; }  // of a warp's states of a 
 // (kStates); and those before every tile as well, for the gradient (kTiles).
 enum Walk { kOut, kStates, kTiles };
 
+template <Walk kWalk, bool kMany>
+constexpr int parts_rows() { return kWalk != kOut ? 0 : kMany ? kTileRows : kTileRows / 2; }
+
 // kMany: more states than a pass takes; those of a tile wait in shared memory
 // (after the warps' own part) while the others' pass.
 template <class T, int NN, Walk kWalk, bool kMany>
-__global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
+__global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
   extern __shared__ __align__(16) char s_raw[];
   constexpr bool kGives = kWalk == kOut;
-  typedef WalkShared<T, NN, kGives> Shared;
+  constexpr int kParts = parts_rows<kWalk, kMany>(), kRows = kGives ? kParts : kTileRows;  // at a time
+  typedef WalkShared<T, NN, kParts> Shared;
   if (kGives) wait_for_last_kernel();
   let_next_kernel_start();
   const tb_scan_args& a = l.a;
@@ -55,12 +59,12 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
   const int c4 = lane / 2 * 4, s0 = lane % 2 * NN;
   const int64_t mine = (t.place + c4) * l.pad + s0;  // the lane's place in a slot of the workspace
   float* const own = l.seg + (int64_t)slot * l.wide * l.pad + mine;
-  Two h[4][NN / 2] = {}, a2[4][NN / 2];
-  auto as_pairs = [&](Two(&p)[4][NN / 2], const float(&f)[4][NN], float by) {
+  f32x2 h[4][NN / 2] = {}, a2[4][NN / 2];
+  auto as_pairs = [&](f32x2(&p)[4][NN / 2], const float(&f)[4][NN], float by) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int n = 0; n < NN; n += 2) p[j][n / 2] = two(f[j][n] * by, f[j][n + 1] * by);
+      for (int n = 0; n < NN; n += 2) p[j][n / 2] = pair(f[j][n] * by, f[j][n + 1] * by);
   };
   auto rates = [&](int n0) {
     float f[4][NN];
@@ -92,7 +96,7 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
   auto kept = [&](int k) {
 #pragma unroll
     for (int i = 0; i < NN; ++i) {
-      Two f[2];
+      f32x2 f[2];
       read_pairs<2>(f, s_h + k * kept_floats<NN>() + (i * 32 + lane) * 4);
       h[i * 2 / (NN / 2)][i * 2 % (NN / 2)] = f[0], h[i * 2 / (NN / 2)][i * 2 % (NN / 2) + 1] = f[1];
     }
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
     rates(0);
     first(0);
   }
-  const Two bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(kGives ? a.d : nullptr, t);
+  const f32x2 bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(kGives ? a.d : nullptr, t);
   const int tiles = (seg.len + kTileRows - 1) / kTileRows;
   auto fetch = [&](int i) {
     const int n = min(kTileRows, seg.len - i * kTileRows);
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
     if (kGives) nc.load(i * kTileRows, n);
   };
   PairOut<T, CH> out(a.y, a.y_row, row0, t);
-  Two total = 0;
+  f32x2 total = 0;
   fetch(0);
   load_states(0, 0);
   for (int i = 0; i < tiles; ++i) {
@@ -140,18 +144,54 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
     if (kWalk == kTiles && i) {
       const int64_t tile = (int64_t)slot * (l.segment / kTileRows) + i;
       if (!kMany) write(l.tile + tile * l.wide * l.pad + mine);
-      *reinterpret_cast<Two*>(l.tile_sum + tile * l.wide + t.place + 2 * lane) = total;
+      *reinterpret_cast<f32x2*>(l.tile_sum + tile * l.wide + t.place + 2 * lane) = total;
     }
     wait_for_copies<1>();
     auto& raw = s.raw[i & 1];
 #pragma unroll
     for (int r = 0; r < kTileRows; ++r) {
-      Two delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus);
+      f32x2 delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus);
       if (r >= n) delta = 0;
       total = add2(total, delta);
       pair_of<CH>(s.delta[r]) = delta;
       pair_of<CH>(s.dx[r]) = mul2(delta, row_pair<T, CH>(raw[0][r]));
     }
+    auto walk = [&](int r, int k) {
+      float d[4], x[4], y[4];
+      f32x2 b[NN / 2], c[NN / 2];
+      read_numbers<4>(d, &s.delta[r][c4]);
+      read_numbers<4>(x, &s.dx[r][c4]);
+      read_pairs<NN / 2>(b, &s.b[r][s0]);
+      if constexpr (kGives) read_pairs<NN / 2>(c, &s.c[r][s0]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 dd = both(d[j]), xx = both(x[j]);
+        f32x2 sum = 0;
+#pragma unroll
+        for (int m = 0; m < NN / 2; ++m) {
+          h[j][m] = fma2(scan_decay(dd, a2[j][m]), h[j][m], mul2(xx, b[m]));
+          if (kGives) sum = m ? fma2(c[m], h[j][m], sum) : mul2(c[m], h[j][m]);
+        }
+        const float2 f = halves(sum);
+        y[j] = f.x + f.y;
+      }
+      if constexpr (kGives) {
+        float* to = &s.part[r % kRows][lane % 2][c4];
+        if (kMany && k) {
+          float f[4];
+          read_numbers<4>(f, to);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] += f[j];
+        }
+        write_numbers<4>(to, y);
+      }
+    };
+    auto give = [&](int r) {
+      f32x2 y = add2(pair_of<CH>(s.part[r % kRows][0]), pair_of<CH>(s.part[r % kRows][1]));
+      y = fma2(skip, row_pair<T, CH>(raw[0][r]), y);
+      if (a.z) y = mul2(y, scan_gate(row_pair<T, CH>(raw[2][r])));
+      if (r < n) out.put(r, y);
+    };
     for (int k = 0; k < blocks; ++k) {
       nb.store(s.b);
       if constexpr (kGives) nc.store(s.c);
@@ -164,50 +204,19 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
       if (kMany && k + 1 < blocks) load_states(i, (k + 1) * 2 * NN);
       else load_states(i + 1, 0);
 #pragma unroll
-      for (int r = 0; r < kTileRows; ++r) {
-        float d[4], x[4], y[4];
-        Two b[NN / 2], c[NN / 2];
-        read_numbers<4>(d, &s.delta[r][c4]);
-        read_numbers<4>(x, &s.dx[r][c4]);
-        read_pairs<NN / 2>(b, &s.b[r][s0]);
-        if constexpr (kGives) read_pairs<NN / 2>(c, &s.c[r][s0]);
+      for (int r0 = 0; r0 < kTileRows; r0 += kRows) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const Two dd = both(d[j]), xx = both(x[j]);
-          Two sum = 0;
+        for (int r = r0; r < r0 + kRows; ++r) walk(r, k);
+        if (kMany) keep(k);
+        __syncwarp();
+        if (kGives && k + 1 == blocks) {
 #pragma unroll
-          for (int m = 0; m < NN / 2; ++m) {
-            h[j][m] = fma2(scan_decay(dd, a2[j][m]), h[j][m], mul2(xx, b[m]));
-            if (kGives) sum = m ? fma2(c[m], h[j][m], sum) : mul2(c[m], h[j][m]);
-          }
-          const float2 f = parts(sum);
-          y[j] = f.x + f.y;
-        }
-        if constexpr (kGives) {
-          float* to = &s.part[r][lane % 2][c4];
-          if (kMany && k) {
-            float f[4];
-            read_numbers<4>(f, to);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] += f[j];
-          }
-          write_numbers<4>(to, y);
+          for (int r = r0; r < r0 + kRows; ++r) give(r);
+          __syncwarp();
         }
       }
-      if (kMany) keep(k);
-      __syncwarp();
     }
-    if constexpr (kGives) {
-#pragma unroll
-      for (int r = 0; r < kTileRows; ++r) {
-        Two y = add2(pair_of<CH>(s.part[r][0]), pair_of<CH>(s.part[r][1]));
-        y = fma2(skip, row_pair<T, CH>(raw[0][r]), y);
-        if (a.z) y = mul2(y, scan_gate(row_pair<T, CH>(raw[2][r])));
-        if (r < n) out.put(r, y);
-      }
-      out.at += kTileRows * out.stride;
-      __syncwarp();
-    }
+    out.at += kTileRows * out.stride;
   }
   wait_for_copies<0>();
   const bool ends = kGives && a.state_out && seg.index + 1 == seg.count;
@@ -222,18 +231,18 @@ __global__ void __launch_bounds__(128) k_scan(ScanLaunch l) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int m = 0; m < NN / 2; ++m) {
-            const float2 v = parts(h[j][m]);
+            const float2 v = halves(h[j][m]);
             f[j][2 * m] = v.x, f[j][2 * m + 1] = v.y;
           }
         write_dense<NN>(a.state_out + state_at, f, t, a.states, c4, k * 2 * NN + s0);
       }
     }
-  if (!kGives) *reinterpret_cast<Two*>(l.sum + (int64_t)slot * l.wide + t.place + 2 * lane) = total;
+  if (!kGives) *reinterpret_cast<f32x2*>(l.sum + (int64_t)slot * l.wide + t.place + 2 * lane) = total;
 }
 
 template <class T, int NN, Walk kWalk, bool kMany>
 cudaError_t go(const ScanLaunch& l, cudaStream_t s) {
-  size_t bytes = l.warps * sizeof(WalkShared<T, NN, kWalk == kOut>);
+  size_t bytes = l.warps * sizeof(WalkShared<T, NN, parts_rows<kWalk, kMany>()>);
   if (kMany) bytes += (size_t)l.warps * (l.pad / (2 * NN)) * kept_floats<NN>() * sizeof(float);
   static std::atomic<bool> ready[kMaxDevices];
   const cudaError_t e = allow_shared(k_scan<T, NN, kWalk, kMany>, 227 * 1024, ready);
@@ -258,53 +267,95 @@ cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
 // ---------------------------------------------------------------- one token
 //
 // 8 bytes a state and nothing else of size: the bound is memory.  Four lanes
-// take a channel, V states at a time each.
-template <class T, int V>
-__global__ void __launch_bounds__(128) k_scan_step(ScanStepLaunch l) {
+// take a channel, four states at a time each, of several streams, whose rows
+// and states are loaded a stream ahead.  kVec: states, b and c by vectors of
+// four, up to 16 states a channel (a lane's rates stay in registers).
+constexpr int kStepThreads = 128;
+
+template <class T, bool kVec>
+__global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanStepLaunch l) {
   const tb_scan_step_args& a = l.a;
-  const int64_t n = blockIdx.y + (int64_t)gridDim.y * blockIdx.z;
-  const int c = (int)(blockIdx.x * 32 + threadIdx.x / 4), lane = threadIdx.x % 4;
-  if (n >= a.streams) return;
+  const int blocks_x = (a.channels + 31) / 32, lane = threadIdx.x % 4;
+  const int c = (int)(blockIdx.x % blocks_x) * 32 + threadIdx.x / 4;
+  const int64_t n0 = (int64_t)(blockIdx.x / blocks_x) * l.per_block, n1 = min(n0 + l.per_block, a.streams);
   const bool live = c < a.channels;
-  const int64_t slot = a.slots ? (int64_t)a.slots[n] : n;
-  T* to = (T*)a.y + n * a.y_row + c;
-  if (slot < 0 || slot >= a.num_slots) {
-    if (live && lane == 0) *to = RowType<T>::from(0.f);
-    return;
+  const int group = live ? c / (a.channels / a.groups) : 0;
+  const float bias = live && a.dt_bias ? a.dt_bias[c] : 0.f, skip = live && a.d ? a.d[c] : 0.f;
+  const float* rate = a.a + (int64_t)c * a.states;
+  struct Row {
+    int64_t slot;
+    T x, dt, z;
+    Pack<float, 4> h;
+    Pack<T, 4> b, c;
+  };
+  const int s4 = lane * 4;
+  const bool mine = live && s4 < a.states;
+  float a2[4] = {};
+  if (kVec && mine) {
+    unpack<float, 4>(load_pack<float, 4>(rate + s4), a2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a2[k] *= kLog2e;
   }
-  float sum = 0.f, x = 0.f;
-  if (live) {
-    const int group = c / (a.channels / a.groups);
-    float* h = a.state + (slot * a.channels + c) * (int64_t)a.states;
-    const float* rate = a.a + (int64_t)c * a.states;
-    const T* b = (const T*)a.b + n * a.b_row + group * a.b_group;
-    const T* cc = (const T*)a.c + n * a.c_row + group * a.c_group;
-    x = RowType<T>::to(((const T*)a.x)[n * a.x_row + c]);
-    float delta = RowType<T>::to(((const T*)a.dt)[n * a.dt_row + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+  auto load = [&](int64_t n) {
+    Row r{};
+    r.slot = n >= n1 ? -1 : a.slots ? (int64_t)a.slots[n] : n;
+    if (r.slot < 0 || r.slot >= a.num_slots || !live) return r;
+    r.x = ((const T*)a.x)[n * a.x_row + c];
+    r.dt = ((const T*)a.dt)[n * a.dt_row + c];
+    if (a.z) r.z = ((const T*)a.z)[n * a.z_row + c];
+    if (kVec && mine) {
+      r.h = load_pack<float, 4>(a.state + (r.slot * a.channels + c) * (int64_t)a.states + s4);
+      r.b = load_pack<T, 4>((const T*)a.b + n * a.b_row + group * a.b_group + s4);
+      r.c = load_pack<T, 4>((const T*)a.c + n * a.c_row + group * a.c_group + s4);
+    }
+    return r;
+  };
+  Row next = load(n0);
+  for (int64_t n = n0; n < n1; ++n) {
+    const Row r = next;
+    next = load(n + 1);
+    T* to = (T*)a.y + n * a.y_row + c;
+    if (r.slot < 0 || r.slot >= a.num_slots) {
+      if (live && lane == 0) *to = RowType<T>::from(0.f);
+      continue;
+    }
+    float* const h = a.state + (r.slot * a.channels + c) * (int64_t)a.states;
+    const float x = RowType<T>::to(r.x);
+    float delta = RowType<T>::to(r.dt) + bias, sum = 0.f;
     if (a.softplus) delta = scan_softplus(delta);
     const float dx = delta * x;
-    for (int s = lane * V; s < a.states; s += 4 * V) {
-      float f[V], r[V];
-      unpack<float, V>(load_pack<float, V>(h + s), f);
+    if (kVec) {
+      if (mine) {
+        float f[4], b[4], cc[4];
+        unpack<float, 4>(r.h, f);
+        unpack<T, 4>(r.b, b);
+        unpack<T, 4>(r.c, cc);
 #pragma unroll
-      for (int k = 0; k < V; ++k) r[k] = rate[s + k];
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        f[k] = fmaf(scan_decay(delta, r[k] * kLog2e), f[k], dx * RowType<T>::to(b[s + k]));
-        sum = fmaf(RowType<T>::to(cc[s + k]), f[k], sum);
+        for (int k = 0; k < 4; ++k) {
+          f[k] = fmaf(scan_decay(delta, a2[k]), f[k], dx * b[k]);
+          sum = fmaf(cc[k], f[k], sum);
+        }
+        store_pack<float, 4>(h + s4, pack<float, 4>(f));
       }
-      store_pack<float, V>(h + s, pack<float, V>(f));
+    } else if (live) {
+      const T* b = (const T*)a.b + n * a.b_row + group * a.b_group;
+      const T* cc = (const T*)a.c + n * a.c_row + group * a.c_group;
+      for (int s = lane; s < a.states; s += 4) {
+        const float f = fmaf(scan_decay(delta, rate[s] * kLog2e), h[s], dx * RowType<T>::to(b[s]));
+        sum = fmaf(RowType<T>::to(cc[s]), f, sum);
+        h[s] = f;
+      }
     }
-  }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-  if (live && lane == 0) {
-    float y = a.d ? fmaf(a.d[c], x, sum) : sum;
-    if (a.z) {
-      const float z = RowType<T>::to(((const T*)a.z)[n * a.z_row + c]);
-      y *= z * scan_sigmoid(z);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (live && lane == 0) {
+      float y = fmaf(skip, x, sum);
+      if (a.z) {
+        const float z = RowType<T>::to(r.z);
+        y *= z * scan_sigmoid(z);
+      }
+      *to = RowType<T>::from(y);
     }
-    *to = RowType<T>::from(y);
   }
 }
 
@@ -318,17 +369,16 @@ cudaError_t launch_scan_states(const void* args, cudaStream_t s) {
 
 cudaError_t launch_scan_step(const void* args, cudaStream_t s) {
   const ScanStepLaunch& l = *(const ScanStepLaunch*)args;
-  const unsigned y = (unsigned)(l.a.streams < 32768 ? l.a.streams : 32768);
-  const dim3 grid((l.a.channels + 31) / 32, y, (unsigned)((l.a.streams + y - 1) / y));
+  const int64_t blocks = (l.a.channels + 31) / 32 * ((l.a.streams + l.per_block - 1) / l.per_block);
   auto go = [&](auto four, auto one) {
-    if (l.a.states % 4 == 0) four<<<grid, 128, 0, s>>>(l);
-    else one<<<grid, 128, 0, s>>>(l);
+    if (l.vec) four<<<(unsigned)blocks, kStepThreads, 0, s>>>(l);
+    else one<<<(unsigned)blocks, kStepThreads, 0, s>>>(l);
     return cudaGetLastError();
   };
   switch (l.a.type) {
-    case TB_TYPE_F32: return go(k_scan_step<float, 4>, k_scan_step<float, 1>);
-    case TB_TYPE_F16: return go(k_scan_step<__half, 4>, k_scan_step<__half, 1>);
-    default: return go(k_scan_step<__nv_bfloat16, 4>, k_scan_step<__nv_bfloat16, 1>);
+    case TB_TYPE_F32: return go(k_scan_step<float, true>, k_scan_step<float, false>);
+    case TB_TYPE_F16: return go(k_scan_step<__half, true>, k_scan_step<__half, false>);
+    default: return go(k_scan_step<__nv_bfloat16, true>, k_scan_step<__nv_bfloat16, false>);
   }
 }
 

@@ -23,36 +23,6 @@ namespace tb {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// ------------------------------------------------------------ pairs of numbers
-
-typedef unsigned long long Two;
-__device__ __forceinline__ Two two(float lo, float hi) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 parts(Two x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two add2(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two both(float x) { return two(x, x); }
-
 // --------------------------------------------------------- functions of a step
 
 __device__ __forceinline__ float scan_ex2(float x) {
@@ -70,36 +40,36 @@ __device__ __forceinline__ float scan_rcp(float x) {
 // many decays that a slow state goes through would add up.  2^-25 more in the
 // exponent takes most of that back, and costs nothing as a sum.
 __device__ __forceinline__ float scan_decay(float delta, float a2) { return scan_ex2(fmaf(delta, a2, 0x1p-25f)); }
-__device__ __forceinline__ Two scan_decay(Two delta, Two a2) {
-  const float2 x = parts(fma2(delta, a2, both(0x1p-25f)));
-  return two(scan_ex2(x.x), scan_ex2(x.y));
+__device__ __forceinline__ f32x2 scan_decay(f32x2 delta, f32x2 a2) {
+  const float2 x = halves(fma2(delta, a2, both(0x1p-25f)));
+  return pair(scan_ex2(x.x), scan_ex2(x.y));
 }
 
 // log(1 + exp(v)) = max(v, 0) + log(1 + u), u = exp(-|v|), and log(1 + u) = 2
 // artanh(s), s = u / (2 + u) <= 1/3: small steps keep their relative accuracy.
 // artanh(s) = s + s q P(q), q = s^2, with P of degree 3 fitted to its series on
 // [0, 1/9]: 6e-9 off at most.
-__device__ __forceinline__ Two scan_softplus(Two v) {
-  const float2 f = parts(v);
-  const Two e = mul2(two(-fabsf(f.x), -fabsf(f.y)), both(kLog2e));
-  const float2 g = parts(e);
-  const Two u = two(scan_ex2(g.x), scan_ex2(g.y));
-  const float2 w = parts(add2(u, both(2.f)));
-  const Two s = mul2(u, two(scan_rcp(w.x), scan_rcp(w.y))), q = mul2(s, s);
-  Two p = fma2(both(0.14005993f), q, both(0.14000903f));
+__device__ __forceinline__ f32x2 scan_softplus(f32x2 v) {
+  const float2 f = halves(v);
+  const f32x2 e = mul2(pair(-fabsf(f.x), -fabsf(f.y)), both(kLog2e));
+  const float2 g = halves(e);
+  const f32x2 u = pair(scan_ex2(g.x), scan_ex2(g.y));
+  const float2 w = halves(add2(u, both(2.f)));
+  const f32x2 s = mul2(u, pair(scan_rcp(w.x), scan_rcp(w.y))), q = mul2(s, s);
+  f32x2 p = fma2(both(0.14005993f), q, both(0.14000903f));
   p = fma2(p, q, both(0.20010763f));
   p = fma2(p, q, both(0.3333321f));
-  const Two l = fma2(mul2(p, q), s, s);
-  return fma2(both(2.f), l, two(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
+  const f32x2 l = fma2(mul2(p, q), s, s);
+  return fma2(both(2.f), l, pair(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
 }
-__device__ __forceinline__ float scan_softplus(float v) { return parts(scan_softplus(both(v))).x; }
+__device__ __forceinline__ float scan_softplus(float v) { return halves(scan_softplus(both(v))).x; }
 
 // At the ends of the range the exponential is 0 or infinite and the quotient 1 or 0.
 __device__ __forceinline__ float scan_sigmoid(float v) { return scan_rcp(1.f + scan_ex2(-v * kLog2e)); }
-__device__ __forceinline__ Two scan_sigmoid(Two v) {
-  const float2 e = parts(mul2(v, both(-kLog2e)));
-  const float2 w = parts(add2(two(scan_ex2(e.x), scan_ex2(e.y)), both(1.f)));
-  return two(scan_rcp(w.x), scan_rcp(w.y));
+__device__ __forceinline__ f32x2 scan_sigmoid(f32x2 v) {
+  const float2 e = halves(mul2(v, both(-kLog2e)));
+  const float2 w = halves(add2(pair(scan_ex2(e.x), scan_ex2(e.y)), both(1.f)));
+  return pair(scan_rcp(w.x), scan_rcp(w.y));
 }
 
 // ------------------------------------------------------------ rows of a tile
@@ -155,22 +125,22 @@ __device__ __forceinline__ int lane_pair() { return (threadIdx.x & 31) % (CH / 2
 template <int CH>
 __device__ __forceinline__ int lane_row() { return (threadIdx.x & 31) / (CH / 2); }
 template <class T, int CH>
-__device__ __forceinline__ Two row_pair(const T (&row)[CH]) {
+__device__ __forceinline__ f32x2 row_pair(const T (&row)[CH]) {
   const int p = lane_pair<CH>();
   if constexpr (sizeof(T) == 4) {
-    return reinterpret_cast<const Two*>(row)[p];
+    return reinterpret_cast<const f32x2*>(row)[p];
   } else {
     const float2 f = halves_of(reinterpret_cast<const uint32_t*>(row)[p], T());
-    return two(f.x, f.y);
+    return pair(f.x, f.y);
   }
 }
 template <int CH>
-__device__ __forceinline__ Two& pair_of(float (&row)[CH]) { return reinterpret_cast<Two*>(row)[lane_pair<CH>()]; }
+__device__ __forceinline__ f32x2& pair_of(float (&row)[CH]) { return reinterpret_cast<f32x2*>(row)[lane_pair<CH>()]; }
 // A vector [channels] in 32 bits, zeros where it is NULL or past the tile.
 template <int CH>
-__device__ __forceinline__ Two channel_pair(const float* v, const ScanTile& t) {
+__device__ __forceinline__ f32x2 channel_pair(const float* v, const ScanTile& t) {
   const int c = 2 * lane_pair<CH>();
-  return two(v && c < t.count ? v[t.first + c] : 0.f, v && c + 1 < t.count ? v[t.first + c + 1] : 0.f);
+  return pair(v && c < t.count ? v[t.first + c] : 0.f, v && c + 1 < t.count ? v[t.first + c + 1] : 0.f);
 }
 // Writes rows of a tensor by such pairs.
 template <class T, int CH>
@@ -182,8 +152,8 @@ struct PairOut {
   __device__ __forceinline__ PairOut(void* p, int64_t stride, int64_t row, const ScanTile& t)
       : at((T*)p + row * stride + t.first + 2 * lane_pair<CH>()), stride(stride), count(min(t.count - 2 * lane_pair<CH>(), 2)),
         whole((uintptr_t)at % (2 * sizeof(T)) == 0 && stride % 2 == 0) {}
-  __device__ __forceinline__ void put(int r, Two v) const {
-    const float2 f = parts(v);
+  __device__ __forceinline__ void put(int r, f32x2 v) const {
+    const float2 f = halves(v);
     T* to = at + r * stride;
     if (count == 2 && whole) {
       if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(to) = f;
@@ -195,12 +165,12 @@ struct PairOut {
   }
 };
 // The steps of a row's channels: dt + bias, or its softplus.
-__device__ __forceinline__ Two scan_step_of(Two dt, Two bias, int softplus) {
-  const Two v = add2(dt, bias);
+__device__ __forceinline__ f32x2 scan_step_of(f32x2 dt, f32x2 bias, int softplus) {
+  const f32x2 v = add2(dt, bias);
   return softplus ? scan_softplus(v) : v;
 }
 // z sigmoid(z).
-__device__ __forceinline__ Two scan_gate(Two z) { return mul2(z, scan_sigmoid(z)); }
+__device__ __forceinline__ f32x2 scan_gate(f32x2 z) { return mul2(z, scan_sigmoid(z)); }
 
 // Rows of b or c: kStates states from n0 on, elements 32 apart of kTileRows x kStates.
 template <class T, int kStates>
@@ -227,7 +197,7 @@ struct ScanStates {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) (&dst[0][0])[lane + 32 * i] = RowType<T>::to(f[i]);
   }
-  __device__ __forceinline__ void store(Two (&dst)[kTileRows][kStates]) const {  // twice each
+  __device__ __forceinline__ void store(f32x2 (&dst)[kTileRows][kStates]) const {  // twice each
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) (&dst[0][0])[lane + 32 * i] = both(RowType<T>::to(f[i]));
@@ -236,14 +206,14 @@ struct ScanStates {
 
 // N pairs that lie on 16 bytes.
 template <int N>
-__device__ __forceinline__ void read_pairs(Two (&f)[N], const void* at) {
+__device__ __forceinline__ void read_pairs(f32x2 (&f)[N], const void* at) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const ulonglong2 v = reinterpret_cast<const ulonglong2*>(at)[i / 2];
     f[i] = v.x, f[i + 1] = v.y;
   }
 }
-__device__ __forceinline__ void write_pairs(void* at, Two x, Two y) { *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(x, y); }
+__device__ __forceinline__ void write_pairs(void* at, f32x2 x, f32x2 y) { *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(x, y); }
 
 // N consecutive numbers: in the workspace on 4 N bytes, or on 16; of a dense
 // [channels, states] array anywhere.

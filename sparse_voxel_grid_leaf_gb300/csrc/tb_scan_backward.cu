@@ -51,16 +51,16 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
   if (seg.grid < 0 || (seg.index == 0 && !g.g.dstate)) return;  // the first chunk's goes nowhere else
   const int64_t row0 = seg.begin + seg.first;
   const int c4 = lane / 2 * 4, s0 = lane % 2 * NN;
-  Two h[4][NN / 2] = {}, a2[4][NN / 2];
+  f32x2 h[4][NN / 2] = {}, a2[4][NN / 2];
   {
     float f[4][NN];
     read_dense<NN>(f, a.a, t, a.states, c4, n0 + s0);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int m = 0; m < NN / 2; ++m) a2[j][m] = two(f[j][2 * m] * kLog2e, f[j][2 * m + 1] * kLog2e);
+      for (int m = 0; m < NN / 2; ++m) a2[j][m] = pair(f[j][2 * m] * kLog2e, f[j][2 * m + 1] * kLog2e);
   }
-  const Two bias = channel_pair<CH>(a.dt_bias, t);
+  const f32x2 bias = channel_pair<CH>(a.dt_bias, t);
   const int tiles = (seg.len + kTileRows - 1) / kTileRows;
   auto fetch = [&](int i) {
     if (i >= 0) {
@@ -84,9 +84,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
     auto& raw = s.raw[i & 1];
 #pragma unroll
     for (int r = 0; r < kTileRows; ++r) {
-      Two ds = row_pair<T, CH>(raw[1][r]);
+      f32x2 ds = row_pair<T, CH>(raw[1][r]);
       if (a.z) ds = mul2(ds, scan_gate(row_pair<T, CH>(raw[2][r])));
-      Two delta = scan_step_of(row_pair<T, CH>(raw[0][r]), bias, a.softplus);
+      f32x2 delta = scan_step_of(row_pair<T, CH>(raw[0][r]), bias, a.softplus);
       if (r >= n) delta = ds = 0;
       pair_of<CH>(s.delta[r]) = delta;
       pair_of<CH>(s.ds[r]) = ds;
@@ -97,13 +97,13 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
 #pragma unroll
     for (int r = kTileRows - 1; r >= 0; --r) {
       float d[4], ds[4];
-      Two c[NN / 2];
+      f32x2 c[NN / 2];
       read_numbers<4>(d, &s.delta[r][c4]);
       read_numbers<4>(ds, &s.ds[r][c4]);
       read_pairs<NN / 2>(c, &s.c[r][s0]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const Two dd = both(d[j]), dsj = both(ds[j]);
+        const f32x2 dd = both(d[j]), dsj = both(ds[j]);
 #pragma unroll
         for (int m = 0; m < NN / 2; ++m) h[j][m] = mul2(scan_decay(dd, a2[j][m]), fma2(c[m], dsj, h[j][m]));
       }
@@ -127,7 +127,7 @@ struct alignas(16) BackShared {
   float own[2][4][32 * NN], start[4][32 * NN];  // the states before two tiles, from zero, and before the chunk: by lanes
   float before[2][CH];                          // the sums of delta before the tiles
   float delta[kTileRows][CH], dx[kTileRows][CH], ds[kTileRows][CH];
-  Two b[kTileRows][4 * NN], c[kTileRows][4 * NN];
+  f32x2 b[kTileRows][4 * NN], c[kTileRows][4 * NN];
   float sums[2][3][4][CH];  // of two rows: a lane's c . h, g . b, a . q
   float bc[2][2][36 * NN];  // of two rows: a lane's channels of db, dc; on different banks
   T raw[2][4][kTileRows][CH];  // x, dt, z, dy of two tiles
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   const tb_scan_args& a = l.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, o = lane_row<CH>(), p = lane_pair<CH>();
   Shared& s = reinterpret_cast<Shared*>(s_raw)[warp];
-  Two(*s_bc)[kTileRows][kStates] = reinterpret_cast<Two(*)[kTileRows][kStates]>(s_raw + kWarps * sizeof(Shared));
+  f32x2(*s_bc)[kTileRows][kStates] = reinterpret_cast<f32x2(*)[kTileRows][kStates]>(s_raw + kWarps * sizeof(Shared));
   const int per_run = a.groups * g.quads, run = (int)(blockIdx.x / per_run), at = (int)(blockIdx.x % per_run);
   const int group = at / g.quads, quad = at % g.quads;
   ScanTile t = scan_tile<CH>(l, group, quad * kWarps + warp);
@@ -160,18 +160,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   if (!placed) t.place = (int64_t)group * l.group_pad, t.count = 0;
   const int c4 = lane / 4 * 4, s4 = lane % 4 * NN;
   const int64_t mine = (t.place + c4) * l.pad + s4;  // the lane's place in a slot of the workspace
-  const Two bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(a.d, t);
-  Two sum_d = 0, sum_bias = 0;
+  const f32x2 bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(a.d, t);
+  f32x2 sum_d = 0, sum_bias = 0;
   const int blocks = kMany ? l.pad / kStates : 1, chunk_tiles = l.segment / kTileRows;
   for (int k = 0; k < blocks; ++k) {
     const int n0 = k * kStates;
     const bool last = k + 1 == blocks;
-    Two a2[2][NN], da[2][NN] = {};
-    auto as_pairs = [&](Two(&h)[2][NN], const float(&f)[4][NN]) {
+    f32x2 a2[2][NN], da[2][NN] = {};
+    auto as_pairs = [&](f32x2(&h)[2][NN], const float(&f)[4][NN]) {
 #pragma unroll
-      for (int n = 0; n < NN; ++n) h[0][n] = two(f[0][n], f[1][n]), h[1][n] = two(f[2][n], f[3][n]);
+      for (int n = 0; n < NN; ++n) h[0][n] = pair(f[0][n], f[1][n]), h[1][n] = pair(f[2][n], f[3][n]);
     };
-    auto nothing = [&](Two(&h)[2][NN]) {
+    auto nothing = [&](f32x2(&h)[2][NN]) {
 #pragma unroll
       for (int n = 0; n < NN; ++n) h[0][n] = h[1][n] = 0;
     };
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         nb.load(i * kTileRows, n);
         nc.load(i * kTileRows, n);
       };
-      Two carry[2][NN], h[2][NN];
+      f32x2 carry[2][NN], h[2][NN];
       {
         const int64_t at_slot = (int64_t)slot * l.wide * l.pad + mine + n0;
 #pragma unroll
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         as_pairs(carry, f);
         if (!placed) nothing(carry);
       }
-      auto forward = [&](int r, Two(&e)[2][NN]) {
-        Two d[2], x[2], b[NN];
+      auto forward = [&](int r, f32x2(&e)[2][NN]) {
+        f32x2 d[2], x[2], b[NN];
         read_pairs<2>(d, &s.delta[r][c4]);
         read_pairs<2>(x, &s.dx[r][c4]);
         read_pairs<NN>(b, &s.b[r][s4]);
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
         for (int m = 0; m < kTileRows / 2; ++m) {
           const int r = 2 * m + o;
-          Two delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus), ds = row_pair<T, CH>(raw[3][r]);
+          f32x2 delta = scan_step_of(row_pair<T, CH>(raw[1][r]), bias, a.softplus), ds = row_pair<T, CH>(raw[3][r]);
           if (a.z) ds = mul2(ds, scan_gate(row_pair<T, CH>(raw[2][r])));
           if (r >= rows) delta = ds = 0;
           pair_of<CH>(s.delta[r]) = delta;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], &s.start[j][lane * NN]);
           as_pairs(h, f);
           if (i) {
-            Two d[2], own[2][NN];
+            f32x2 d[2], own[2][NN];
             read_pairs<2>(d, &s.before[i & 1][c4]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], &s.own[i & 1][j][lane * NN]);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           }
         }
         if (!placed) nothing(h);
-        Two first[2][NN];
+        f32x2 first[2][NN];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         __syncwarp();
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          Two e[2][NN];
+          f32x2 e[2][NN];
           forward(r, e);
         }
 #pragma unroll 1
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
               for (int n = 0; n < NN; ++n) h[j][n] = first[j][n];
           // the states before four rows and after each, and the rows' decays
-          Two hs[5][2][NN], e[4][2][NN];
+          f32x2 hs[5][2][NN], e[4][2][NN];
 #pragma unroll
           for (int r = 0; r <= 4; ++r) {
 #pragma unroll
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
           for (int r = 3; r >= 0; --r) {
             const int at_row = 4 * half + r;
-            Two d[2], x[2], ds[2], b[NN], c[NN], y[2] = {}, into[2] = {}, qa[2] = {};
+            f32x2 d[2], x[2], ds[2], b[NN], c[NN], y[2] = {}, into[2] = {}, qa[2] = {};
             float db[NN], dc[NN];
             read_pairs<2>(d, &s.delta[at_row][c4]);
             read_pairs<2>(x, &s.dx[at_row][c4]);
@@ -324,20 +324,20 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
             read_pairs<NN>(c, &s.c[at_row][s4]);
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
-              Two sum_b = 0, sum_c = 0;
+              f32x2 sum_b = 0, sum_c = 0;
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const Two grad = fma2(c[n], ds[j], carry[j][n]);
+                const f32x2 grad = fma2(c[n], ds[j], carry[j][n]);
                 y[j] = n ? fma2(c[n], hs[r + 1][j][n], y[j]) : mul2(c[n], hs[r + 1][j][n]);
                 sum_c = j ? fma2(ds[j], hs[r + 1][j][n], sum_c) : mul2(ds[j], hs[r + 1][j][n]);
                 sum_b = j ? fma2(grad, x[j], sum_b) : mul2(grad, x[j]);
                 into[j] = n ? fma2(grad, b[n], into[j]) : mul2(grad, b[n]);
                 carry[j][n] = mul2(grad, e[r][j][n]);
-                const Two q = mul2(carry[j][n], hs[r][j][n]);
+                const f32x2 q = mul2(carry[j][n], hs[r][j][n]);
                 qa[j] = n ? fma2(q, a2[j][n], qa[j]) : mul2(q, a2[j][n]);
                 da[j][n] = fma2(q, d[j], da[j][n]);
               }
-              const float2 fb = parts(sum_b), fc = parts(sum_c);
+              const float2 fb = halves(sum_b), fc = halves(sum_c);
               db[n] = fb.x + fb.y;
               dc[n] = fc.x + fc.y;
             }
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
             __syncwarp();
             // the sums of two rows, one each half of the warp: by channels, then by states of db and dc
             const int rr = at_row + o;
-            Two sum[3];
+            f32x2 sum[3];
 #pragma unroll
             for (int v = 0; v < 3; ++v)
               sum[v] = add2(add2(pair_of<CH>(s.sums[o][v][0]), pair_of<CH>(s.sums[o][v][1])),
@@ -367,31 +367,31 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
                 if (2 * p + m < t.count)
 #pragma unroll
                   for (int v = 0; v < 3; ++v) {
-                    float2 f = parts(sum[v]);
+                    float2 f = halves(sum[v]);
                     float& mine = m ? f.y : f.x;
                     if (k) mine += acc[3 * m + v];
                     if (!last) acc[3 * m + v] = mine;
-                    sum[v] = two(f.x, f.y);
+                    sum[v] = pair(f.x, f.y);
                   }
             }
             if (rr < rows && last) {
-              const Two xf = row_pair<T, CH>(raw[0][rr]), dsf = pair_of<CH>(s.ds[rr]);
-              const Two inner = fma2(skip, xf, sum[0]);
-              Two ddt = fma2(xf, sum[1], mul2(sum[2], both(kLn2)));
+              const f32x2 xf = row_pair<T, CH>(raw[0][rr]), dsf = pair_of<CH>(s.ds[rr]);
+              const f32x2 inner = fma2(skip, xf, sum[0]);
+              f32x2 ddt = fma2(xf, sum[1], mul2(sum[2], both(kLn2)));
               if (a.softplus) ddt = mul2(ddt, scan_sigmoid(add2(row_pair<T, CH>(raw[1][rr]), bias)));
               out_x.put(to, fma2(skip, dsf, mul2(pair_of<CH>(s.delta[rr]), sum[1])));
               out_dt.put(to, ddt);
               if (a.z) {
-                const Two z = row_pair<T, CH>(raw[2][rr]), sg = scan_sigmoid(z);
-                const Two slope = mul2(sg, fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
+                const f32x2 z = row_pair<T, CH>(raw[2][rr]), sg = scan_sigmoid(z);
+                const f32x2 slope = mul2(sg, fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f)));
                 out_z.put(to, mul2(mul2(row_pair<T, CH>(raw[3][rr]), inner), slope));
               }
               sum_d = fma2(dsf, xf, sum_d);
               sum_bias = add2(sum_bias, ddt);
             }
             if (p < kStates) {
-              const Two* from = reinterpret_cast<const Two*>(&s.bc[o][p / (2 * NN)][0]) + p % (2 * NN);
-              Two f = from[0];
+              const f32x2* from = reinterpret_cast<const f32x2*>(&s.bc[o][p / (2 * NN)][0]) + p % (2 * NN);
+              f32x2 f = from[0];
 #pragma unroll
               for (int m = 1; m < 8; ++m) f = add2(f, from[m * 2 * NN]);
               s_bc[warp][rr][p] = f;
@@ -403,9 +403,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         if (threadIdx.x < kTileRows * kStates) {
           const int r = threadIdx.x / kStates, v = threadIdx.x % kStates;
           if (r < rows) {
-            const Two f = add2(add2(s_bc[0][r][v], s_bc[1][r][v]), add2(s_bc[2][r][v], s_bc[3][r][v]));
+            const f32x2 f = add2(add2(s_bc[0][r][v], s_bc[1][r][v]), add2(s_bc[2][r][v], s_bc[3][r][v]));
             const int64_t row = ((int64_t)quad * l.tokens + row0 + i * kTileRows + r) * a.groups + group;
-            *reinterpret_cast<Two*>(&g.bc[(row * 2 + v / (2 * NN)) * l.pad + n0 + v % (2 * NN) * 2]) = f;
+            *reinterpret_cast<f32x2*>(&g.bc[(row * 2 + v / (2 * NN)) * l.pad + n0 + v % (2 * NN) * 2]) = f;
           }
         }
         __syncthreads();
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         float f[2][NN];
 #pragma unroll
         for (int n = 0; n < NN; ++n) {
-          const float2 v = parts(da[j][n]);
+          const float2 v = halves(da[j][n]);
           f[0][n] = v.x, f[1][n] = v.y;
         }
         write_numbers<NN>(to + 2 * j * l.pad, f[0]);
@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   sum_bias = add2(sum_bias, __shfl_xor_sync(0xffffffffu, sum_bias, 16));
   if (o == 0 && placed) {
     float* to = g.part_d + (int64_t)run * 2 * l.wide + t.place + 2 * p;
-    *reinterpret_cast<Two*>(to) = sum_d;
-    *reinterpret_cast<Two*>(to + l.wide) = sum_bias;
+    *reinterpret_cast<f32x2*>(to) = sum_d;
+    *reinterpret_cast<f32x2*>(to + l.wide) = sum_bias;
   }
 }
 

@@ -130,6 +130,8 @@ cudaError_t launch_scan_back_join(const void* args, cudaStream_t s);
 cudaError_t launch_scan_sums(const void* args, cudaStream_t s);
 struct ScanStepLaunch {
   tb_scan_step_args a;
+  int vec;        // by vectors of four states
+  int per_block;  // streams of a block
 };
 cudaError_t launch_scan_step(const void* args, cudaStream_t s);
 

@@ -421,13 +421,15 @@ static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t 
 }
 
 // Rows of a segment of the forward pass, 0: grids are walked whole.  A walk is
-// sequential along a grid and a warp's, so a call with few of them is split; the
-// segments' own states cost most of a walk once more.
-static int32_t scan_segment(int64_t tokens, int32_t grids, int32_t groups, int32_t group_tiles, int sms) {
-  const int64_t walks = (int64_t)grids * groups * group_tiles;
-  if (grids <= 0 || walks >= 4ll * sms || tokens < 256ll * grids) return 0;
-  int64_t seg = up(up(tokens * groups * group_tiles, 12 * sms), 64) * 64;
-  if (seg < 64) seg = 64;
+// sequential along a grid and a warp's, so a call with few of them is split, so
+// that four blocks a multiprocessor run at once; the segments' own states cost
+// most of a walk once more.
+static int32_t scan_segment(const ScanLaunch& l, int64_t tokens, int32_t grids, int sms) {
+  const int64_t blocks = (int64_t)grids * l.blocks_x;
+  if (grids <= 0 || blocks >= 3ll * sms || tokens < 96ll * grids) return 0;
+  const int64_t slots = 4ll * sms / l.blocks_x - grids;
+  int64_t seg = up(up(tokens, slots > 1 ? slots : 1), kTileRows) * kTileRows;
+  if (seg < 32) seg = 32;
   return tokens >= 2 * seg * grids ? (int32_t)seg : 0;
 }
 
@@ -461,10 +463,12 @@ static ScanCarve scan_carve(int64_t slots, int64_t tokens, int32_t channels, int
   return c;
 }
 
-// Rows of a chunk of the gradient.
-static int32_t scan_chunk(int64_t tokens, int32_t grids, int32_t wide, int sms) {
-  (void)tokens, (void)grids, (void)wide, (void)sms;
-  return 64;
+// Rows of a chunk of the gradient: shorter ones where two blocks a
+// multiprocessor would not run.
+static int32_t scan_chunk(const ScanLaunch& l, int64_t tokens, int32_t groups, int sms) {
+  int32_t chunk = 64;
+  while (chunk > 16 && tokens / chunk * groups * up(l.group_pad, 128) < 2ll * sms) chunk /= 2;
+  return chunk;
 }
 
 int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t channels, int32_t states, int32_t groups,
@@ -474,7 +478,7 @@ int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t chann
   scan_shape(l, channels, states, groups);
   int sms = seq_sms();
   if (!sms) sms = 256;
-  l.segment = backward ? scan_chunk(tokens, grids, l.wide, sms) : scan_segment(tokens, grids, groups, l.group_tiles, sms);
+  l.segment = backward ? scan_chunk(l, tokens, groups, sms) : scan_segment(l, tokens, grids, sms);
   if (!l.segment) return 0;
   return scan_carve(segment_slots(tokens, grids, l.segment), tokens, channels, groups, l, backward, sms).bytes;
 }
@@ -494,7 +498,7 @@ static tb_status scan_plan(const char* what, ScanLaunch& l, bool backward, ScanC
   const int size = type_size(a.type);
   scan_shape(l, a.channels, a.states, a.groups);
   l.offsets = a.offsets, l.tokens = a.tokens, l.grids = a.grids;
-  l.segment = backward ? scan_chunk(a.tokens, a.grids, l.wide, sms) : scan_segment(a.tokens, a.grids, a.groups, l.group_tiles, sms);
+  l.segment = backward ? scan_chunk(l, a.tokens, a.groups, sms) : scan_segment(l, a.tokens, a.grids, sms);
   const int64_t slots = segment_slots(a.tokens, a.grids, l.segment);
   const int64_t per_slot = (int64_t)a.groups * l.group_tiles;
   const int64_t join = up((int64_t)l.wide * (l.pad / 4), 128);
@@ -602,6 +606,18 @@ tb_status tb_selective_scan_step(const tb_scan_step_args* args, tb_stream stream
   if (!a.x || !a.dt || !a.a || !a.b || !a.c || !a.y ||
       (a.num_slots && (!a.state || (uintptr_t)a.state % (a.states % 4 == 0 ? 16 : 4))))
     return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer (states are 16-byte aligned where they are a multiple of 4)", what);
+  const int sms = seq_sms();
+  if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
+  const int size = type_size(a.type);
+  auto fours = [&](const void* p, int64_t row, int64_t group) {
+    return (uintptr_t)p % (4 * size) == 0 && row % 4 == 0 && (a.groups == 1 || group % 4 == 0);
+  };
+  l.vec = a.states % 4 == 0 && a.states <= 16 && aligned16(a.a) && aligned16(a.state) && fours(a.b, a.b_row, a.b_group) &&
+          fours(a.c, a.c_row, a.c_group);
+  // several streams a block, while there are blocks enough: its rates stay in registers
+  const int64_t blocks_x = up(a.channels, 32), per = a.streams * blocks_x / (8ll * sms);
+  l.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+  if (blocks_x > kMaxRows / a.streams) return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 blocks or more", what);
   TB_SEQ_CUDA(seq_launch(kSeqSelectiveStep, (cudaStream_t)stream, launch_scan_step, &l));
   return TB_OK;
 }
