@@ -15,7 +15,7 @@
 namespace tb {
 namespace {
 
-constexpr int kConvThreads = 128;
+constexpr int kConvThreads = 128;  // of a block at most
 
 __device__ __forceinline__ void conv_grid(const tb_conv_args& a, int b, int64_t& begin, int64_t& end) {
   if (!a.offsets) {
@@ -106,8 +106,18 @@ struct ConvWeight {
   static constexpr int P = (V + 1) / 2;
   f32x2 w[K][P], bias[P];
   __device__ __forceinline__ ConvWeight(const void* weight, const void* b, int c) {
-    auto at = [&](int v, int k) { return RowType<T>::to(((const T*)weight)[(int64_t)(c + v) * K + k]); };
-    auto of = [&](int v) { return b ? RowType<T>::to(((const T*)b)[c + v]) : 0.f; };
+    float f[V * K], g[V] = {};  // a vector's channels and taps are consecutive, and whole vectors
+    constexpr int U = V > 1 ? 8 / (int)sizeof(T) : 1;
+#pragma unroll
+    for (int i = 0; i < V * K; i += U) {
+      float u[U];
+      unpack<T, U>(load_pack<T, U>((const T*)weight + (int64_t)c * K + i), u);
+#pragma unroll
+      for (int k = 0; k < U; ++k) f[i + k] = u[k];
+    }
+    if (b) unpack<T, V>(load_pack<T, V>((const T*)b + c), g);
+    auto at = [&](int v, int k) { return f[v * K + k]; };
+    auto of = [&](int v) { return g[v]; };
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
       const int second = V > 1 ? v + 1 : v;
@@ -131,6 +141,67 @@ __device__ __forceinline__ f32x2 sigmoid(f32x2 x) {
   return pair(u.x, u.y);
 }
 
+// N tensors' rows on their way to a thread, `kAhead` rows ahead: each thread's
+// own, through shared memory by asynchronous copies (registers for as many
+// would leave too few threads), or four rows in registers where a vector is
+// smaller than such a copy.
+template <class T, int V, int N>
+struct RowsAhead {
+  static constexpr bool kShared = V * sizeof(T) >= 4;
+  static constexpr int kSlots = kShared ? 16 : 4, kAhead = kShared ? kSlots - 1 : kSlots;
+  static constexpr int kBytes = kShared ? kSlots * N * kConvThreads * V * (int)sizeof(T) : 16;
+  Pack<T, V> held[kShared ? 1 : kSlots][N];
+  Pack<T, V>* mine;
+  const T* from[N];
+  int64_t stride[N];
+  int have;  // rows
+  __device__ __forceinline__ void issue(int u) {
+    if constexpr (kShared) {
+      if (u < have) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + (u % kSlots * N + n) * kConvThreads);
+          const T* at = from[n] + u * stride[n];
+          if constexpr (V * sizeof(T) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(at) : "memory");
+          else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(at), "n"(V * sizeof(T)) : "memory");
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ void start() {
+    if constexpr (kShared) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) issue(u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (u < have) held[u][n] = load_pack<T, V>(from[n] + u * stride[n]);
+    }
+  }
+  // Row u < have; i = u % 4, known to the compiler.
+  __device__ __forceinline__ void take(int u, int i, Pack<T, V> (&row)[N]) {
+    if constexpr (kShared) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+      for (int n = 0; n < N; ++n) row[n] = mine[(u % kSlots * N + n) * kConvThreads];
+      issue(u + kAhead);
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        row[n] = held[i][n];
+        if (u + kSlots < have) held[i][n] = load_pack<T, V>(from[n] + (u + kSlots) * stride[n]);
+      }
+    }
+  }
+  // The rows have been taken, and the slots may be filled again.
+  __device__ __forceinline__ void finish() {
+    if constexpr (kShared) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+};
+
 // The last taps - 1 rows of state and grid together.
 template <class T, int V, int K>
 __device__ __forceinline__ void conv_last(const tb_conv_args& a, int b, int c) {
@@ -146,7 +217,7 @@ __device__ __forceinline__ void conv_last(const tb_conv_args& a, int b, int c) {
 template <class T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
   const tb_conv_args& a = l.a;
-  const int bx = (int)(blockIdx.x % l.blocks_x), per_y = kConvThreads / l.per_x;
+  const int bx = (int)(blockIdx.x % l.blocks_x), per_y = (int)blockDim.x / l.per_x;
   const int64_t by = blockIdx.x / l.blocks_x;
   const int c = (bx * l.per_x + (int)threadIdx.x % l.per_x) * V, y = (int)threadIdx.x / l.per_x;
   if (c >= a.channels || y >= per_y) return;
@@ -155,8 +226,12 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
     if (a.state_out && run - l.runs < a.grids) conv_last<T, V, K>(a, (int)(run - l.runs), c);
     return;
   }
+  __shared__ __align__(16) char s_ahead[RowsAhead<T, V, 1>::kBytes];
+  RowsAhead<T, V, 1> ahead;
+  ahead.mine = reinterpret_cast<Pack<T, V>*>(s_ahead) + threadIdx.x;
+  ahead.stride[0] = a.x_row;
   const ConvWeight<T, V, K> w(a.weight, a.bias, c);
-  constexpr int P = (V + 1) / 2, B = 8;  // pairs of channels; rows in flight
+  constexpr int P = (V + 1) / 2;  // pairs of channels
   ConvPieces pieces(a, run * l.run, min((run + 1) * l.run, a.tokens));
   while (pieces.at < pieces.end) {
     int64_t r0, r1;
@@ -166,34 +241,34 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
       for (int64_t r = r0; r < r1; ++r, to += a.y_row) store_pack<T, V>(to, Pack<T, V>{});
       continue;
     }
+    ahead.from[0] = (const T*)a.x + r0 * a.x_row + c;
+    ahead.have = (int)(r1 - r0);
+    ahead.start();
     f32x2 x[K][P];  // the rows before, oldest first, and the row
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
-    const T* from = (const T*)a.x + r0 * a.x_row + c;
-    Pack<T, V> ahead[B];
-    const int n = (int)(r1 - r0);
+    for (int base = 0; base < ahead.have; base += 4) {
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-      if (i < n) ahead[i] = load_pack<T, V>(from + i * a.x_row);
-    for (int base = 0; base < n; base += B) {
+      for (int i = 0; i < 4; ++i) {
+        if (base + i >= ahead.have) break;
+        Pack<T, V> row[1];
+        f32x2 o[P];
+        ahead.take(base + i, i, row);
+        to_pairs<T, V>(row[0], x[K - 1]);
 #pragma unroll
-      for (int i = 0; i < B; ++i)
-        if (base + i < n) {
-          f32x2 o[P];
-          to_pairs<T, V>(ahead[i], x[K - 1]);
-          if (base + B + i < n) ahead[i] = load_pack<T, V>(from + (base + B + i) * a.x_row);
+        for (int v = 0; v < P; ++v) {
+          f32x2 s = w.bias[v];
 #pragma unroll
-          for (int v = 0; v < P; ++v) {
-            f32x2 s = w.bias[v];
+          for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
+          o[v] = a.silu ? mul2(s, sigmoid(s)) : s;
 #pragma unroll
-            for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
-            o[v] = a.silu ? mul2(s, sigmoid(s)) : s;
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) x[k][v] = x[k + 1][v];
-          }
-          store_pack<T, V>(to + (base + i) * a.y_row, from_pairs<T, V>(o));
+          for (int k = 0; k < K - 1; ++k) x[k][v] = x[k + 1][v];
         }
+        store_pack<T, V>(to, from_pairs<T, V>(o));
+        to += a.y_row;
+      }
     }
+    ahead.finish();
   }
 }
 
@@ -257,7 +332,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
   const tb_conv_args& a = l.f.a;
   const tb_conv_backward_args& g = l.g;
   __shared__ f32x2 s_part[kConvThreads][(V + 1) / 2];
-  const int bx = (int)(blockIdx.x % l.f.blocks_x), per_x = l.f.per_x, per_y = kConvThreads / per_x;
+  const int bx = (int)(blockIdx.x % l.f.blocks_x), per_x = l.f.per_x, per_y = (int)blockDim.x / per_x;
   const int64_t by = blockIdx.x / l.f.blocks_x;
   const int c = (bx * per_x + (int)threadIdx.x % per_x) * V, y = (int)threadIdx.x / per_x;
   const bool live = c < a.channels && y < per_y;
@@ -269,8 +344,12 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
   const int64_t run = by * per_y + y;
   constexpr int P = (V + 1) / 2;
   f32x2 dw[K + 1][P] = {};  // the last one: dbias
+  __shared__ __align__(16) char s_ahead[RowsAhead<T, V, 2>::kBytes];
   if (live && run < l.f.runs) {
     const ConvWeight<T, V, K> w(a.weight, a.bias, c);
+    RowsAhead<T, V, 2> ahead;
+    ahead.mine = reinterpret_cast<Pack<T, V>*>(s_ahead) + threadIdx.x;
+    ahead.stride[0] = a.x_row, ahead.stride[1] = g.dy_row;
     ConvPieces pieces(a, run * l.f.run, min((run + 1) * l.f.run, a.tokens));
     while (pieces.at < pieces.end) {
       int64_t r0, r1;
@@ -283,29 +362,24 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
       f32x2 x[K][P], d[K][P] = {};  // rows of x and gradients of pre, the last one at [K - 1]
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
-      const T* from = (const T*)a.x + r0 * a.x_row + c;
-      const T* grad = (const T*)g.dy + r0 * g.dy_row + c;
       const int own = (int)(r1 - r0);                                     // rows of the run
       const int have = (int)min(pieces.past - r0, (int64_t)own + K - 1);  // rows whose pre has a part in them
-      constexpr int B = 4;
-      Pack<T, V> ax[B], ad[B];
-      auto load = [&](int i, int u) {
-        if (u < have) {
-          ax[i] = load_pack<T, V>(from + u * a.x_row);
-          ad[i] = load_pack<T, V>(grad + u * g.dy_row);
-        }
-      };
+      ahead.from[0] = (const T*)a.x + r0 * a.x_row + c;
+      ahead.from[1] = (const T*)g.dy + r0 * g.dy_row + c;
+      ahead.have = have;
+      ahead.start();
+      for (int base = 0; base < own + K - 1; base += 4) {
 #pragma unroll
-      for (int i = 0; i < B; ++i) load(i, i);
-      for (int base = 0; base < own + K - 1; base += B) {
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const int u = base + i, t = u - (K - 1);
           if (u >= own + K - 1) break;
-          f32x2 e[P];
-          to_pairs<T, V>(ax[i], x[K - 1]);
-          to_pairs<T, V>(ad[i], e);
-          load(i, u + B);
+          f32x2 e[P] = {};
+          if (u < have) {
+            Pack<T, V> row[2];
+            ahead.take(u, i, row);
+            to_pairs<T, V>(row[0], x[K - 1]);
+            to_pairs<T, V>(row[1], e);
+          }
           if (u < have) {
 #pragma unroll
             for (int v = 0; v < P; ++v) {
@@ -352,6 +426,7 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
             }
         }
       }
+      ahead.finish();
     }
   }
   float* part = g.workspace + by * (K + 1) * a.channels + c;
@@ -445,15 +520,15 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_step(ConvStepLaunch l) {
 
 template <class T, int V, int K>
 cudaError_t go(const ConvLaunch& l, cudaStream_t s) {
-  const int64_t per_y = kConvThreads / l.per_x, rows = l.runs + (l.a.state_out ? l.a.grids : 0);
-  k_conv<T, V, K><<<(unsigned)((rows + per_y - 1) / per_y * l.blocks_x), kConvThreads, 0, s>>>(l);
+  const int64_t per_y = l.threads / l.per_x, rows = l.runs + (l.a.state_out ? l.a.grids : 0);
+  k_conv<T, V, K><<<(unsigned)((rows + per_y - 1) / per_y * l.blocks_x), l.threads, 0, s>>>(l);
   return cudaGetLastError();
 }
 template <class T, int V, int K>
 cudaError_t go(const ConvBackwardLaunch& l, cudaStream_t s) {
-  const int64_t per_y = kConvThreads / l.f.per_x, more = l.g.dstate ? (l.f.a.grids + per_y - 1) / per_y : 0;
+  const int64_t per_y = l.f.threads / l.f.per_x, more = l.g.dstate ? (l.f.a.grids + per_y - 1) / per_y : 0;
   if (l.parts + more)
-    k_conv_backward<T, V, K><<<(unsigned)((l.parts + more) * l.f.blocks_x), kConvThreads, 0, s>>>(l);
+    k_conv_backward<T, V, K><<<(unsigned)((l.parts + more) * l.f.blocks_x), l.f.threads, 0, s>>>(l);
   return cudaGetLastError();
 }
 template <class T, int V, int K>

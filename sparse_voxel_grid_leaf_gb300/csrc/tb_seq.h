@@ -73,6 +73,7 @@ struct ConvLaunch {
   tb_conv_args a;
   int vec;       // elements of the vectors that rows are moved by
   int per_x;     // threads of a row in a block; the others take other runs of rows
+  int threads;   // of a block: rows' whole
   int blocks_x;  // blocks of a row
   int run;       // rows of a thread
   int64_t runs;  // runs of rows, after which a block for each grid makes its state

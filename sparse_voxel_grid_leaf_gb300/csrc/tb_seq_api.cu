@@ -309,7 +309,8 @@ static void conv_shape(ConvLaunch& l, int sms, int threads, int least, int most)
   const int64_t cols = l.a.channels / l.vec;
   l.blocks_x = (int)up(cols, 128);
   l.per_x = (int)up(cols, l.blocks_x);
-  const int64_t run = l.a.tokens * cols / ((int64_t)threads * sms);
+  l.threads = (int)up(128 / l.per_x * l.per_x, 32) * 32;
+  const int64_t run = up(l.a.tokens * cols, (int64_t)threads * sms);
   l.run = (int)(run < least ? least : run > most ? most : run);
   l.runs = up(l.a.tokens, l.run);
 }
@@ -331,14 +332,14 @@ tb_status tb_causal_conv(const tb_conv_args* args, tb_stream stream) {
   if (!sms) return seq_fail(TB_ERR_CUDA, "%s: no device", what);
   const int size = type_size(a.type), vec = 16 / size;
   const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, a.y, a.y_row) &&
-                    aligned16(a.state) && aligned16(a.state_out);
+                    aligned16(a.state) && aligned16(a.state_out) && aligned16(a.weight) && aligned16(a.bias);
   l.vec = fits ? vec : 1;
-  conv_shape(l, sms, 512, 4, 32);
+  conv_shape(l, sms, 384, 4, 512);
   TB_SEQ_CUDA(seq_launch(kSeqConv, (cudaStream_t)stream, launch_conv, &l));
   return TB_OK;
 }
 
-constexpr int kConvBackThreads = 768, kConvBackLeast = 8, kConvBackMost = 256;
+constexpr int kConvBackThreads = 384, kConvBackLeast = 8, kConvBackMost = 512;
 
 int64_t tb_causal_conv_backward_workspace(int64_t tokens, int32_t channels, int32_t taps) {
   if (tokens < 0 || channels < 1 || taps < 2 || taps > 4) return 0;
@@ -349,7 +350,7 @@ int64_t tb_causal_conv_backward_workspace(int64_t tokens, int32_t channels, int3
     ConvLaunch l{};
     l.a.tokens = tokens, l.a.channels = channels, l.vec = vec;
     conv_shape(l, sms ? sms : 256, kConvBackThreads, kConvBackLeast, kConvBackMost);
-    const int64_t parts = up(l.runs, 128 / l.per_x);
+    const int64_t parts = up(l.runs, l.threads / l.per_x);
     if (parts > most) most = parts;
   }
   return most * (taps + 1) * channels * (int64_t)sizeof(float);
@@ -376,10 +377,11 @@ tb_status tb_causal_conv_backward(const tb_conv_backward_args* args, tb_stream s
   const int size = type_size(a.type), vec = 8 / size;
   const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, g.dy, g.dy_row) &&
                     conv_fits(vec, size, g.dx, g.dx_row) && conv_fits(vec, size, a.state, 0) &&
-                    conv_fits(vec, size, g.dstate_out, 0) && conv_fits(vec, size, g.dstate, 0);
+                    conv_fits(vec, size, g.dstate_out, 0) && conv_fits(vec, size, g.dstate, 0) && conv_fits(vec, size, a.weight, 0) &&
+                    conv_fits(vec, size, a.bias, 0);
   l.f.vec = fits ? vec : 1;
   conv_shape(l.f, sms, kConvBackThreads, kConvBackLeast, kConvBackMost);
-  l.parts = up(l.f.runs, 128 / l.f.per_x);
+  l.parts = up(l.f.runs, l.f.threads / l.f.per_x);
   if (a.tokens || (g.dstate && a.grids)) TB_SEQ_CUDA(seq_launch(kSeqConvBackward, (cudaStream_t)stream, launch_conv_backward, &l));
   TB_SEQ_CUDA(seq_launch(kSeqConvWeight, (cudaStream_t)stream, launch_conv_weight, &l));
   return TB_OK;
@@ -400,7 +402,7 @@ tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream stream) {
   if (!a.x || !a.weight || !a.y || (a.num_slots && !a.state)) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
   const int size = type_size(a.type), vec = 16 / size;
   const bool fits = a.channels % vec == 0 && conv_fits(vec, size, a.x, a.x_row) && conv_fits(vec, size, a.y, a.y_row) &&
-                    aligned16(a.state);
+                    aligned16(a.state) && aligned16(a.weight) && aligned16(a.bias);
   l.vec = fits ? vec : 1;
   TB_SEQ_CUDA(seq_launch(kSeqConvStep, (cudaStream_t)stream, launch_conv_step, &l));
   return TB_OK;
