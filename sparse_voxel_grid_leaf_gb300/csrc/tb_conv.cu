@@ -12,6 +12,8 @@
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 
+#include <type_traits>
+
 namespace tb {
 namespace {
 
@@ -148,53 +150,47 @@ __device__ __forceinline__ f32x2 sigmoid(f32x2 x) {
 template <class T, int V, int N>
 struct RowsAhead {
   static constexpr bool kShared = V * sizeof(T) >= 4;
-  static constexpr int kSlots = kShared ? 16 : 4, kAhead = kShared ? kSlots - 1 : kSlots;
+  static constexpr int kSlots = kShared ? 16 : 4;
   static constexpr int kBytes = kShared ? kSlots * N * kConvThreads * V * (int)sizeof(T) : 16;
   Pack<T, V> held[kShared ? 1 : kSlots][N];
   Pack<T, V>* mine;
-  const T* from[N];
+  const T* next[N];  // row `asked`
   int64_t stride[N];
-  int have;  // rows
-  __device__ __forceinline__ void issue(int u) {
-    if constexpr (kShared) {
-      if (u < have) {
+  int asked, have;   // rows on their way or taken, of all
+  __device__ __forceinline__ void ask() {
+    if (asked < have) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + (u % kSlots * N + n) * kConvThreads);
-          const T* at = from[n] + u * stride[n];
-          if constexpr (V * sizeof(T) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(at) : "memory");
-          else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(at), "n"(V * sizeof(T)) : "memory");
-        }
+      for (int n = 0; n < N; ++n) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + (asked % kSlots * N + n) * kConvThreads);
+        if constexpr (V * sizeof(T) == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(next[n]) : "memory");
+        else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(next[n]), "n"(V * sizeof(T)) : "memory");
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ void start() {
+  __device__ __forceinline__ void more(int i) {
     if constexpr (kShared) {
+      ask();
+    } else if (asked < have) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) issue(u);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-          if (u < have) held[u][n] = load_pack<T, V>(from[n] + u * stride[n]);
+      for (int n = 0; n < N; ++n) held[i][n] = load_pack<T, V>(next[n]);
     }
+    ++asked;
+#pragma unroll
+    for (int n = 0; n < N; ++n) next[n] += stride[n];
+  }
+  __device__ __forceinline__ void start(int rows) {
+    have = rows;
+    asked = 0;
+#pragma unroll
+    for (int u = 0; u < (kShared ? kSlots - 1 : kSlots); ++u) more(u);
   }
   // Row u < have; i = u % 4, known to the compiler.
   __device__ __forceinline__ void take(int u, int i, Pack<T, V> (&row)[N]) {
-    if constexpr (kShared) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    if constexpr (kShared) asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
 #pragma unroll
-      for (int n = 0; n < N; ++n) row[n] = mine[(u % kSlots * N + n) * kConvThreads];
-      issue(u + kAhead);
-    } else {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        row[n] = held[i][n];
-        if (u + kSlots < have) held[i][n] = load_pack<T, V>(from[n] + (u + kSlots) * stride[n]);
-      }
-    }
+    for (int n = 0; n < N; ++n) row[n] = kShared ? mine[(u % kSlots * N + n) * kConvThreads] : held[kShared ? 0 : i][n];
+    more(i);
   }
   // The rows have been taken, and the slots may be filled again.
   __device__ __forceinline__ void finish() {
@@ -241,33 +237,37 @@ __global__ void __launch_bounds__(kConvThreads) k_conv(ConvLaunch l) {
       for (int64_t r = r0; r < r1; ++r, to += a.y_row) store_pack<T, V>(to, Pack<T, V>{});
       continue;
     }
-    ahead.from[0] = (const T*)a.x + r0 * a.x_row + c;
-    ahead.have = (int)(r1 - r0);
-    ahead.start();
+    const int n = (int)(r1 - r0);
+    ahead.next[0] = (const T*)a.x + r0 * a.x_row + c;
+    ahead.start(n);
     f32x2 x[K][P];  // the rows before, oldest first, and the row
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
-    for (int base = 0; base < ahead.have; base += 4) {
+    auto step = [&](int u, int i) {
+      Pack<T, V> row[1];
+      f32x2 o[P];
+      ahead.take(u, i, row);
+      to_pairs<T, V>(row[0], x[K - 1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (base + i >= ahead.have) break;
-        Pack<T, V> row[1];
-        f32x2 o[P];
-        ahead.take(base + i, i, row);
-        to_pairs<T, V>(row[0], x[K - 1]);
+      for (int v = 0; v < P; ++v) {
+        f32x2 s = w.bias[v];
 #pragma unroll
-        for (int v = 0; v < P; ++v) {
-          f32x2 s = w.bias[v];
+        for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
+        o[v] = a.silu ? mul2(s, sigmoid(s)) : s;
 #pragma unroll
-          for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
-          o[v] = a.silu ? mul2(s, sigmoid(s)) : s;
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) x[k][v] = x[k + 1][v];
-        }
-        store_pack<T, V>(to, from_pairs<T, V>(o));
-        to += a.y_row;
+        for (int k = 0; k < K - 1; ++k) x[k][v] = x[k + 1][v];
       }
+      store_pack<T, V>(to, from_pairs<T, V>(o));
+      to += a.y_row;
+    };
+    int u = 0;
+    for (; u + 4 <= n; u += 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) step(u + i, i);
     }
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (u + i < n) step(u + i, i);
     ahead.finish();
   }
 }
@@ -364,67 +364,78 @@ __global__ void __launch_bounds__(kConvThreads) k_conv_backward(ConvBackwardLaun
       for (int i = 0; i < K - 1; ++i) to_pairs<T, V>(conv_row<T, V, K>(a, b, pieces.begin, r0 - pieces.begin - (K - 1) + i, c), x[i]);
       const int own = (int)(r1 - r0);                                     // rows of the run
       const int have = (int)min(pieces.past - r0, (int64_t)own + K - 1);  // rows whose pre has a part in them
-      ahead.from[0] = (const T*)a.x + r0 * a.x_row + c;
-      ahead.from[1] = (const T*)g.dy + r0 * g.dy_row + c;
-      ahead.have = have;
-      ahead.start();
-      for (int base = 0; base < own + K - 1; base += 4) {
+      ahead.next[0] = (const T*)a.x + r0 * a.x_row + c;
+      ahead.next[1] = (const T*)g.dy + r0 * g.dy_row + c;
+      ahead.start(have);
+      // Row u of x and dy in, row u - (K - 1) of dx out.  kWhole: both are the
+      // run's own, and dx's has K - 1 rows of its grid behind it.
+      auto step = [&](int u, int i, auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        if (kWhole || u < have) {
+          Pack<T, V> row[2];
+          f32x2 e[P];
+          ahead.take(u, i, row);
+          to_pairs<T, V>(row[0], x[K - 1]);
+          to_pairs<T, V>(row[1], e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = base + i, t = u - (K - 1);
-          if (u >= own + K - 1) break;
-          f32x2 e[P] = {};
-          if (u < have) {
-            Pack<T, V> row[2];
-            ahead.take(u, i, row);
-            to_pairs<T, V>(row[0], x[K - 1]);
-            to_pairs<T, V>(row[1], e);
+          for (int v = 0; v < P; ++v) {
+            f32x2 s = w.bias[v];
+#pragma unroll
+            for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
+            d[K - 1][v] = conv_slope(e[v], s, a.silu);
           }
-          if (u < have) {
+          if (kWhole || u < own) {
 #pragma unroll
             for (int v = 0; v < P; ++v) {
-              f32x2 s = w.bias[v];
 #pragma unroll
-              for (int k = 0; k < K; ++k) s = fma2(w.w[k][v], x[k][v], s);
-              d[K - 1][v] = conv_slope(e[v], s, a.silu);
+              for (int k = 0; k < K; ++k) dw[k][v] = fma2(d[K - 1][v], x[k][v], dw[k][v]);
+              dw[K][v] = add2(dw[K][v], d[K - 1][v]);
             }
-            if (u < own) {
-#pragma unroll
-              for (int v = 0; v < P; ++v) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) dw[k][v] = fma2(d[K - 1][v], x[k][v], dw[k][v]);
-                dw[K][v] = add2(dw[K][v], d[K - 1][v]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int v = 0; v < P; ++v) d[K - 1][v] = 0;
           }
-          if (t >= 0) {
-            f32x2 o[P];
+        } else {
 #pragma unroll
-            for (int v = 0; v < P; ++v) {
-              o[v] = mul2(w.w[K - 1][v], d[0][v]);
+          for (int v = 0; v < P; ++v) d[K - 1][v] = 0;
+        }
+        if (kWhole || u >= K - 1) {
+          f32x2 o[P];
 #pragma unroll
-              for (int k = 1; k < K; ++k) o[v] = fma2(w.w[K - 1 - k][v], d[k][v], o[v]);
-            }
-            const int64_t left = pieces.past - 1 - (r0 + t);
+          for (int v = 0; v < P; ++v) {
+            o[v] = mul2(w.w[K - 1][v], d[0][v]);
+#pragma unroll
+            for (int k = 1; k < K; ++k) o[v] = fma2(w.w[K - 1 - k][v], d[k][v], o[v]);
+          }
+          if (!kWhole) {
+            const int64_t left = pieces.past - 1 - (r0 + u - (K - 1));
             if (g.dstate_out && left < K - 1) {
               f32x2 f[P];
               to_pairs<T, V>(load_pack<T, V>((const T*)g.dstate_out + ((int64_t)b * (K - 1) + K - 2 - left) * a.channels + c), f);
 #pragma unroll
               for (int v = 0; v < P; ++v) o[v] = add2(o[v], f[v]);
             }
-            store_pack<T, V>(to + t * g.dx_row, from_pairs<T, V>(o));
           }
-#pragma unroll
-          for (int v = 0; v < P; ++v)
-#pragma unroll
-            for (int k = 0; k < K - 1; ++k) {
-              x[k][v] = x[k + 1][v];
-              d[k][v] = d[k + 1][v];
-            }
+          store_pack<T, V>(to, from_pairs<T, V>(o));
+          to += g.dx_row;
         }
+#pragma unroll
+        for (int v = 0; v < P; ++v)
+#pragma unroll
+          for (int k = 0; k < K - 1; ++k) {
+            x[k][v] = x[k + 1][v];
+            d[k][v] = d[k + 1][v];
+          }
+      };
+      const int all = own + K - 1;
+      int u = 0;
+      while (u < all) {  // four rows at a time
+        if (u >= K - 1 && u + 4 <= own) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) step(u + i, i, std::true_type());
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (u + i < all) step(u + i, i, std::false_type());
+        }
+        u += 4;
       }
       ahead.finish();
     }
