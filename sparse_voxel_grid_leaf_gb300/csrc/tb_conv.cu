@@ -84,25 +84,6 @@ __device__ __forceinline__ Pack<T, V> conv_row(const tb_conv_args& a, int b, int
   return r;
 }
 
-// V channels in pairs (V = 1: one number twice, the second one not used).
-template <class T, int V>
-__device__ __forceinline__ void to_pairs(const Pack<T, V>& p, f32x2 (&f)[(V + 1) / 2]) {
-  float x[V];
-  unpack<T, V>(p, x);
-#pragma unroll
-  for (int v = 0; v < V; v += 2) f[v / 2] = pair(x[v], x[V > 1 ? v + 1 : v]);
-}
-template <class T, int V>
-__device__ __forceinline__ Pack<T, V> from_pairs(const f32x2 (&f)[(V + 1) / 2]) {
-  float x[V];
-#pragma unroll
-  for (int v = 0; v < V; v += 2) {
-    const float2 y = halves(f[v / 2]);
-    x[v] = y.x;
-    if (V > 1) x[V > 1 ? v + 1 : v] = y.y;
-  }
-  return pack<T, V>(x);
-}
 template <class T, int V, int K>
 struct ConvWeight {
   static constexpr int P = (V + 1) / 2;

@@ -56,13 +56,19 @@ __device__ __forceinline__ float2 row_reduce(float x, float y, float2* s, int& t
   return v;
 }
 
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
 // Whether a thread has registers for the next row and the weight next to its
 // row (30000 rows of 4096 in 16 bits, four vectors a thread: 89 us so, 113 with
 // the loads at the row; of 8192, eight vectors: 492 and 181).  The gradient
 // holds dweight as well (15000 rows of 16384, four vectors: 869 and 367).
-template <class T, int V, int NV, bool kBackward>
+// The layer norm holds its rows in 32 bits between its sums, V > 1.
+template <class T, int V, int NV, bool kBackward, bool kMean = false>
 constexpr bool ahead() {
-  return NV * (V * (int)sizeof(T) + 3) / 4 <= (kBackward ? 16 : 32);
+  return kMean && V > 1 ? NV * V <= (kBackward ? 8 : 16) : NV * (V * (int)sizeof(T) + 3) / 4 <= (kBackward ? 16 : 32);
 }
 
 // What takes a row's h w to e4m3, from top = max |h w| and r: max |y| is r top,
@@ -92,7 +98,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
-  constexpr bool kAhead = ahead<T, V, NV, false>();
+  constexpr bool kAhead = ahead<T, V, NV, false, kMean>();
   Pack<T, V> w[NV], px[NV], pr[NV];
   auto load = [&](int64_t row) {
     const T* x = (const T*)a.x + row * a.x_row;
@@ -130,6 +136,51 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm(NormLaunch n) {
       cr[i] = pr[i];
     }
     if (kAhead) load(row + stride);
+    if constexpr (kMean && V > 1) {
+      constexpr int P = V / 2;
+      f32x2 f[NV][P], part = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!live || v >= vecs) continue;
+        to_pairs<T, V>(cx[i], f[i]);
+        if (a.residual) {
+          f32x2 g[P];
+          to_pairs<T, V>(cr[i], g);
+#pragma unroll
+          for (int j = 0; j < P; ++j) f[i][j] = add2(f[i][j], g[j]);
+        }
+        if (a.h_out) store_pack<T, V>((T*)a.h_out + row * a.h_row + (int64_t)v * V, from_pairs<T, V>(f[i]));
+#pragma unroll
+        for (int j = 0; j < P; ++j) part = add2(part, f[i][j]);
+      }
+      float2 sums = halves(part);
+      const float mean = row_reduce<false>(sums.x + sums.y, 0.f, s_red, turn).x * inv_width;
+      part = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live || threadIdx.x + i * blockDim.x >= vecs) continue;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          f[i][j] = add2(f[i][j], both(-mean));
+          part = fma2(f[i][j], f[i][j], part);
+        }
+      }
+      sums = halves(part);
+      const float r = rsqrtf(fmaf(row_reduce<false>(sums.x + sums.y, 0.f, s_red, turn).x, inv_width, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!live || v >= vecs) continue;
+        f32x2 g[P], o[P] = {};
+        to_pairs<T, V>(kAhead ? w[i] : weight(i), g);
+        if (n.bias) to_pairs<T, V>(kAhead ? wb[i] : bias(i), o);
+#pragma unroll
+        for (int j = 0; j < P; ++j) f[i][j] = fma2(f[i][j], mul2(both(r), g[j]), o[j]);
+        store_pack<T, V>((T*)a.y + row * a.y_row + (int64_t)v * V, from_pairs<T, V>(f[i]));
+      }
+      continue;
+    }
     auto sum_of = [&](int i, float (&f)[V]) {
       unpack<T, V>(cx[i], f);
       if (a.residual) {
@@ -226,17 +277,19 @@ __device__ __forceinline__ float norm_along(float r, float mean) { return r * me
 // Rows of dx, and a block's part of dweight in registers over its rows: part
 // [blocks, width] in the workspace, summed by k_norm_weight in a fixed order.
 template <class T, int V, int NV, bool kMean>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunch n) {
+__device__ __forceinline__ void norm_backward(const NormBackwardLaunch& n) {
   let_next_kernel_start();
   const tb_norm_backward_args& a = n.a;
-  extern __shared__ float s_part[];  // [rows, per_row * NV * V] where a block has more than one row
+  extern __shared__ __align__(16) float s_part[];  // [rows, per_row * NV * V] where a block has more than one row
   __shared__ float2 s_red[64];
   int turn = 0;
   const int vecs = a.width / V;
   const float inv_width = 1.f / (float)a.width;
   const int64_t stride = (int64_t)gridDim.x * blockDim.y;
-  constexpr bool kAhead = ahead<T, V, NV, true>();
+  constexpr bool kAhead = ahead<T, V, NV, true, kMean>();
+  constexpr bool kPairs = kMean && V > 1;
   float dw[NV][V] = {}, db[kMean ? NV : 1][V] = {};
+  f32x2 dw2[kPairs ? NV : 1][(V + 1) / 2] = {}, db2[kPairs ? NV : 1][(V + 1) / 2] = {};  // in their place
   Pack<T, V> w[NV], ph[NV], pd[NV], pg[NV];
   auto load = [&](int64_t row) {
 #pragma unroll
@@ -267,6 +320,58 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
       cg[i] = pg[i];
     }
     if (kAhead) load(row + stride);
+    if constexpr (kPairs) {
+      constexpr int P = V / 2;
+      f32x2 h[NV][P], vd[NV][P], one = 0, other = 0;  // the row, weight dy
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live || threadIdx.x + i * blockDim.x >= vecs) continue;
+        f32x2 f[P];
+        to_pairs<T, V>(ch[i], h[i]);
+        to_pairs<T, V>(cd[i], vd[i]);
+        to_pairs<T, V>(kAhead ? w[i] : weight(i), f);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          vd[i][j] = mul2(vd[i][j], f[j]);
+          one = add2(one, h[i][j]);
+          other = add2(other, vd[i][j]);
+        }
+      }
+      float2 x = halves(one), y = halves(other);
+      const float2 means = row_reduce<false>(x.x + x.y, y.x + y.y, s_red, turn);
+      one = other = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!live || threadIdx.x + i * blockDim.x >= vecs) continue;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          h[i][j] = add2(h[i][j], both(-means.x * inv_width));
+          one = fma2(h[i][j], h[i][j], one);
+          other = fma2(h[i][j], vd[i][j], other);
+        }
+      }
+      x = halves(one), y = halves(other);
+      const float2 all = row_reduce<false>(x.x + x.y, y.x + y.y, s_red, turn);
+      const float r = rsqrtf(fmaf(all.x, inv_width, a.eps));
+      const f32x2 m = both(-norm_along(r, all.y * inv_width)), less = both(-means.y * inv_width * r), rr = both(r);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (!live || v >= vecs) continue;
+        f32x2 d[P], g[P];
+        to_pairs<T, V>(cd[i], d);
+        if (a.dh) to_pairs<T, V>(cg[i], g);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          dw2[i][j] = fma2(d[j], mul2(h[i][j], rr), dw2[i][j]);
+          db2[i][j] = add2(db2[i][j], d[j]);
+          h[i][j] = fma2(m, h[i][j], fma2(rr, vd[i][j], less));
+          if (a.dh) h[i][j] = add2(h[i][j], g[j]);
+        }
+        store_pack<T, V>((T*)a.dx + row * a.dx_row + (int64_t)v * V, from_pairs<T, V>(h[i]));
+      }
+      continue;
+    }
     float hh = 0.f, hd = 0.f, mean = 0.f, less = 0.f;
     if constexpr (kMean) {  // of the row, and of weight dy
 #pragma unroll
@@ -360,8 +465,28 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
       }
     }
   };
+  if constexpr (kPairs) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const float2 f = halves(dw2[i][j / 2]), g = halves(db2[i][j / 2]);
+        dw[i][j] = j % 2 ? f.y : f.x;
+        db[i][j] = j % 2 ? g.y : g.x;
+      }
+  }
   put(dw, 0);
   if constexpr (kMean) put(db, 1);
+}
+template <class T, int V, int NV>
+__global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunch n) {
+  norm_backward<T, V, NV, false>(n);
+}
+// One vector a thread in so few registers that 768 threads run on a
+// multiprocessor (384 with the 120 that it would take: 205 us of that, 190 so).
+template <class T, int V, int NV>
+__global__ void __maxnreg__(V > 1 && NV == 1 ? 80 : 128) k_layer_backward(NormBackwardLaunch n) {
+  norm_backward<T, V, NV, true>(n);
 }
 
 // ------------------------------------------- rows that no vector boundary meets
@@ -373,11 +498,6 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_backward(NormBackwardLaunc
 // gradient 81 us and 141).  A group has up to 16 / sizeof(T) rows, a whole
 // number of vectors; fewer, with more warps each, where rows are wide.
 constexpr int kGroupWarps = 32;  // at most
-
-__device__ __forceinline__ void copy_async(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
-}
 
 // Rows [row, row + rows) of a dense tensor of `all` rows, on their way into
 // `dst`, as far into a vector as they lie in theirs: that offset, in elements.
@@ -695,8 +815,8 @@ template <class T, int V, int NV>
 cudaError_t go_back(const NormBackwardLaunch& n, cudaStream_t s) {
   const dim3 block(n.per_row, n.rows);
   const size_t smem = n.rows > 1 ? sizeof(float) * n.rows * n.per_row * NV * V : 0;
-  if (n.layer) k_norm_backward<T, V, NV, true><<<n.blocks, block, smem, s>>>(n);
-  else k_norm_backward<T, V, NV, false><<<n.blocks, block, smem, s>>>(n);
+  if (n.layer) k_layer_backward<T, V, NV><<<n.blocks, block, smem, s>>>(n);
+  else k_norm_backward<T, V, NV><<<n.blocks, block, smem, s>>>(n);
   return cudaGetLastError();
 }
 

@@ -184,6 +184,26 @@ __device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
 }
 __device__ __forceinline__ f32x2 both(float x) { return pair(x, x); }
 
+// A vector as pairs (V = 1: one number twice, the second one not used).
+template <class T, int V>
+__device__ __forceinline__ void to_pairs(const Pack<T, V>& p, f32x2 (&f)[(V + 1) / 2]) {
+  float x[V];
+  unpack<T, V>(p, x);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) f[v / 2] = pair(x[v], x[V > 1 ? v + 1 : v]);
+}
+template <class T, int V>
+__device__ __forceinline__ Pack<T, V> from_pairs(const f32x2 (&f)[(V + 1) / 2]) {
+  float x[V];
+#pragma unroll
+  for (int v = 0; v < V; v += 2) {
+    const float2 y = halves(f[v / 2]);
+    x[v] = y.x;
+    if (V > 1) x[V > 1 ? v + 1 : v] = y.y;
+  }
+  return pack<T, V>(x);
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
