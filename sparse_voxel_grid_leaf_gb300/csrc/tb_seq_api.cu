@@ -513,7 +513,7 @@ static tb_status scan_plan(const char* what, ScanLaunch& l, bool backward, ScanC
           (a.groups == 1 || whole(a.channels / a.groups, size));
   if (!l.segment) return TB_OK;
   c = scan_carve(slots, a.tokens, a.channels, a.groups, l, backward, sms);
-  if (!a.workspace || a.workspace_bytes < c.bytes || ((uintptr_t)a.workspace & 255))
+  if (c.bytes && (!a.workspace || a.workspace_bytes < c.bytes || ((uintptr_t)a.workspace & 255)))
     return seq_fail(TB_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", what, (long long)a.workspace_bytes,
                     (long long)c.bytes);
   l.seg = (float*)((char*)a.workspace + c.seg);
