@@ -267,94 +267,96 @@ cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
 // ---------------------------------------------------------------- one token
 //
 // 8 bytes a state and nothing else of size: the bound is memory.  Four lanes
-// take a channel, four states at a time each, of several streams, whose rows
-// and states are loaded a stream ahead.  kVec: states, b and c by vectors of
-// four, up to 16 states a channel (a lane's rates stay in registers).
+// take a channel, four states at a time each, of four streams at once: a lane
+// makes the step and the gate of one of the streams (by every lane they took
+// more instructions than the states), and the states of all four are on their
+// way together.  256 streams of 2048 channels and 16 states: STEPFIGURE.  kVec:
+// states, b and c by vectors of four, up to 16 states a channel (a lane's rates
+// stay in registers).
 constexpr int kStepThreads = 128;
 
 template <class T, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanStepLaunch l) {
   const tb_scan_step_args& a = l.a;
-  const int blocks_x = (a.channels + 31) / 32, lane = threadIdx.x % 4;
+  const int blocks_x = (a.channels + 31) / 32, lane = threadIdx.x % 4, s4 = lane * 4;
   const int c = (int)(blockIdx.x % blocks_x) * 32 + threadIdx.x / 4;
   const int64_t n0 = (int64_t)(blockIdx.x / blocks_x) * l.per_block, n1 = min(n0 + l.per_block, a.streams);
-  const bool live = c < a.channels;
+  const bool live = c < a.channels, mine = live && s4 < a.states;
   const int group = live ? c / (a.channels / a.groups) : 0;
   const float bias = live && a.dt_bias ? a.dt_bias[c] : 0.f, skip = live && a.d ? a.d[c] : 0.f;
   const float* rate = a.a + (int64_t)c * a.states;
-  struct Row {
-    int64_t slot;
-    T x, dt, z;
-    Pack<float, 4> h;
-    Pack<T, 4> b, c;
-  };
-  const int s4 = lane * 4;
-  const bool mine = live && s4 < a.states;
   float a2[4] = {};
   if (kVec && mine) {
     unpack<float, 4>(load_pack<float, 4>(rate + s4), a2);
 #pragma unroll
     for (int k = 0; k < 4; ++k) a2[k] *= kLog2e;
   }
-  auto load = [&](int64_t n) {
-    Row r{};
-    r.slot = n >= n1 ? -1 : a.slots ? (int64_t)a.slots[n] : n;
-    if (r.slot < 0 || r.slot >= a.num_slots || !live) return r;
-    r.x = ((const T*)a.x)[n * a.x_row + c];
-    r.dt = ((const T*)a.dt)[n * a.dt_row + c];
-    if (a.z) r.z = ((const T*)a.z)[n * a.z_row + c];
-    if (kVec && mine) {
-      r.h = load_pack<float, 4>(a.state + (r.slot * a.channels + c) * (int64_t)a.states + s4);
-      r.b = load_pack<T, 4>((const T*)a.b + n * a.b_row + group * a.b_group + s4);
-      r.c = load_pack<T, 4>((const T*)a.c + n * a.c_row + group * a.c_group + s4);
-    }
-    return r;
-  };
-  Row next = load(n0);
-  for (int64_t n = n0; n < n1; ++n) {
-    const Row r = next;
-    next = load(n + 1);
-    T* to = (T*)a.y + n * a.y_row + c;
-    if (r.slot < 0 || r.slot >= a.num_slots) {
-      if (live && lane == 0) *to = RowType<T>::from(0.f);
-      continue;
-    }
-    float* const h = a.state + (r.slot * a.channels + c) * (int64_t)a.states;
-    const float x = RowType<T>::to(r.x);
-    float delta = RowType<T>::to(r.dt) + bias, sum = 0.f;
-    if (a.softplus) delta = scan_softplus(delta);
-    const float dx = delta * x;
-    if (kVec) {
-      if (mine) {
-        float f[4], b[4], cc[4];
-        unpack<float, 4>(r.h, f);
-        unpack<T, 4>(r.b, b);
-        unpack<T, 4>(r.c, cc);
+  for (int64_t n = n0; n < n1; n += 4) {
+    // the lane's own stream of the four
+    const int64_t own = n + lane;
+    int64_t slot = own >= n1 || !live ? -1 : a.slots ? (int64_t)a.slots[own] : own;
+    if (slot >= a.num_slots || slot < 0) slot = -1;
+    int64_t at[4];  // of each one's states, -1: none
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = fmaf(scan_decay(delta, a2[k]), f[k], dx * b[k]);
-          sum = fmaf(cc[k], f[k], sum);
+    for (int j = 0; j < 4; ++j) at[j] = __shfl_sync(0xffffffffu, slot, j, 4);
+    Pack<float, 4> hp[4];
+    Pack<T, 4> bp[4], cp[4];
+    const T* const b = (const T*)a.b + n * a.b_row + group * a.b_group;
+    const T* const cc = (const T*)a.c + n * a.c_row + group * a.c_group;
+    if (kVec && mine) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (at[j] >= 0) {
+          hp[j] = load_pack<float, 4>(a.state + (at[j] * a.channels + c) * (int64_t)a.states + s4);
+          bp[j] = load_pack<T, 4>(b + j * a.b_row + s4);
+          cp[j] = load_pack<T, 4>(cc + j * a.c_row + s4);
         }
-        store_pack<float, 4>(h + s4, pack<float, 4>(f));
-      }
-    } else if (live) {
-      const T* b = (const T*)a.b + n * a.b_row + group * a.b_group;
-      const T* cc = (const T*)a.c + n * a.c_row + group * a.c_group;
-      for (int s = lane; s < a.states; s += 4) {
-        const float f = fmaf(scan_decay(delta, rate[s] * kLog2e), h[s], dx * RowType<T>::to(b[s]));
-        sum = fmaf(RowType<T>::to(cc[s]), f, sum);
-        h[s] = f;
+    }
+    float x = 0.f, delta = 0.f, z = 0.f;
+    if (slot >= 0) {
+      x = RowType<T>::to(((const T*)a.x)[own * a.x_row + c]);
+      delta = RowType<T>::to(((const T*)a.dt)[own * a.dt_row + c]) + bias;
+      if (a.z) z = RowType<T>::to(((const T*)a.z)[own * a.z_row + c]);
+      if (a.softplus) delta = scan_softplus(delta);
+    }
+    const float dx = delta * x;
+    float sum[4] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float dj = __shfl_sync(0xffffffffu, delta, j, 4), xj = __shfl_sync(0xffffffffu, dx, j, 4);
+      if (at[j] < 0) continue;
+      float* const h = a.state + (at[j] * a.channels + c) * (int64_t)a.states;
+      if (kVec) {
+        if (mine) {
+          float f[4], g[4], r[4];
+          unpack<float, 4>(hp[j], f);
+          unpack<T, 4>(bp[j], g);
+          unpack<T, 4>(cp[j], r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[k] = fmaf(scan_decay(dj, a2[k]), f[k], xj * g[k]);
+            sum[j] = fmaf(r[k], f[k], sum[j]);
+          }
+          store_pack<float, 4>(h + s4, pack<float, 4>(f));
+        }
+      } else {
+        for (int s = lane; s < a.states; s += 4) {
+          const float f = fmaf(scan_decay(dj, rate[s] * kLog2e), h[s], xj * RowType<T>::to(b[j * a.b_row + s]));
+          sum[j] = fmaf(RowType<T>::to(cc[j * a.c_row + s]), f, sum[j]);
+          h[s] = f;
+        }
       }
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (live && lane == 0) {
-      float y = fmaf(skip, x, sum);
-      if (a.z) {
-        const float z = RowType<T>::to(r.z);
-        y *= z * scan_sigmoid(z);
-      }
-      *to = RowType<T>::from(y);
+    // to each lane the sum of its own stream
+    float even = lane & 1 ? sum[1] : sum[0], odd = lane & 1 ? sum[3] : sum[2];
+    even += __shfl_xor_sync(0xffffffffu, lane & 1 ? sum[0] : sum[1], 1);
+    odd += __shfl_xor_sync(0xffffffffu, lane & 1 ? sum[2] : sum[3], 1);
+    float y = lane & 2 ? odd : even;
+    y += __shfl_xor_sync(0xffffffffu, lane & 2 ? even : odd, 2);
+    if (live && own < n1) {
+      y = fmaf(skip, x, y);
+      if (a.z) y *= z * scan_sigmoid(z);
+      ((T*)a.y)[own * a.y_row + c] = RowType<T>::from(slot >= 0 ? y : 0.f);
     }
   }
 }

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           f32x2 e[2][NN];
           forward(r, e);
         }
-#pragma unroll 1
+#pragma unroll
         for (int half = 1; half >= 0; --half) {
           if (!half)
 #pragma unroll
@@ -303,14 +303,17 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
               for (int n = 0; n < NN; ++n) h[j][n] = first[j][n];
           // the states before four rows and after each, and the rows' decays
-          f32x2 hs[5][2][NN], e[4][2][NN];
+          f32x2 hs[5][2][NN];
 #pragma unroll
           for (int r = 0; r <= 4; ++r) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int n = 0; n < NN; ++n) hs[r][j][n] = h[j][n];
-            if (r < 4) forward(4 * half + r, e[r]);
+            if (r < 4) {
+              f32x2 e[2][NN];
+              forward(4 * half + r, e);
+            }
           }
 #pragma unroll
           for (int r = 3; r >= 0; --r) {
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
                 sum_c = j ? fma2(ds[j], hs[r + 1][j][n], sum_c) : mul2(ds[j], hs[r + 1][j][n]);
                 sum_b = j ? fma2(grad, x[j], sum_b) : mul2(grad, x[j]);
                 into[j] = n ? fma2(grad, b[n], into[j]) : mul2(grad, b[n]);
-                carry[j][n] = mul2(grad, e[r][j][n]);
+                carry[j][n] = mul2(grad, scan_decay(d[j], a2[j][n]));
                 const f32x2 q = mul2(carry[j][n], hs[r][j][n]);
                 qa[j] = n ? fma2(q, a2[j][n], qa[j]) : mul2(q, a2[j][n]);
                 da[j][n] = fma2(q, d[j], da[j][n]);

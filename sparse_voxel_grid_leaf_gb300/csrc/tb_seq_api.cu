@@ -616,9 +616,9 @@ tb_status tb_selective_scan_step(const tb_scan_step_args* args, tb_stream stream
   };
   l.vec = a.states % 4 == 0 && a.states <= 16 && aligned16(a.a) && aligned16(a.state) && fours(a.b, a.b_row, a.b_group) &&
           fours(a.c, a.c_row, a.c_group);
-  // several streams a block, while there are blocks enough: its rates stay in registers
-  const int64_t blocks_x = up(a.channels, 32), per = a.streams * blocks_x / (8ll * sms);
-  l.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+  // fours of streams, several a block while there are blocks enough: its rates stay in registers
+  const int64_t blocks_x = up(a.channels, 32), fours_of = a.streams * blocks_x / (32ll * sms);
+  l.per_block = 4 * (int)(fours_of < 1 ? 1 : fours_of > 4 ? 4 : fours_of);
   if (blocks_x > kMaxRows / a.streams) return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 blocks or more", what);
   TB_SEQ_CUDA(seq_launch(kSeqSelectiveStep, (cudaStream_t)stream, launch_scan_step, &l));
   return TB_OK;
