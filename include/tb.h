@@ -609,6 +609,7 @@ TB_API tb_status tb_linear_attention_step(const tb_linear_step_args* args, tb_st
  * first are its state [grids, taps - 1, channels], oldest first (NULL: zeros);
  * state_out (or NULL) gets the last taps - 1 rows of state and grid together.
  * All of one type.  offsets as in tb_linear_args: rows of no grid get zeros.
+ * No output may share memory with an input.
  *
  * The backward call gives, for the gradient dy of y and dstate_out (NULL: zero)
  * of state_out, the gradients dx, dweight, dbias (NULL: not made) and dstate
@@ -660,8 +661,9 @@ TB_API tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream st
  * [grids, channels, states] in 32 bits: the states that grids start from
  * (NULL: zero) and those after each grid's last row, which for a grid without
  * rows is its first.  states <= 256.  offsets as in tb_linear_args: rows of no
- * grid get zeros.  In a channel that meets an infinity, outputs from there on
- * may be NaN where the formula has an infinity.
+ * grid get zeros.  No output may share memory with an input.  In a channel that
+ * meets an infinity, outputs from there on may be NaN where the formula has an
+ * infinity.
  *
  * The backward call gives, for the gradient dy of y and dstate_out (NULL: zero)
  * of state_out, the gradients of every input: dx, ddt, dz (with z), db, dc of
@@ -670,7 +672,9 @@ TB_API tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream st
  * a fixed order.
  *
  * workspace: at least tb_selective_scan_workspace(...) bytes, 256-byte aligned
- * (NULL where that is 0). */
+ * (NULL where that is 0).  The backward call's keeps the states before every
+ * eighth row: states / 2 bytes for each row and channel, and some 40% of that
+ * besides. */
 typedef struct tb_scan_args {
   const void *x, *dt, *b, *c, *z;
   void* y;

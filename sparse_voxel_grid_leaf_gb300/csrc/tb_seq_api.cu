@@ -532,6 +532,8 @@ static tb_status scan_check(const char* what, const tb_scan_args& a) {
   if (!a.offsets && a.grids != 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d grids without offsets", what, a.grids);
   if (a.grids == 0 && a.tokens) return seq_fail(TB_ERR_INVALID_ARG, "%s: tokens without grids", what);
   if (!a.a || (a.tokens && (!a.x || !a.dt || !a.b || !a.c))) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
+  if (up(a.channels / a.groups, kScanChannels) * kScanChannels * a.groups > kMaxRows)
+    return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 channels or more, each group's rounded up to %d", what, kScanChannels);
   return TB_OK;
 }
 
