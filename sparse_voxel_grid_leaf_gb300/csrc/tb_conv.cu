@@ -9,6 +9,11 @@
 // taps - 1 rows in registers; what a run reads of the run before is taps - 1
 // rows.  The gradient walks with two windows, of x and of the gradient of pre:
 // dx_t is known once the gradient of pre at t + taps - 1 is.
+//
+// Measured, bf16, 4 taps and SiLU: 124807 rows of 1024 channels 99 us, 5.2 TB/s
+// (127 with four rows ahead in registers and runs of 32 rows, whose first loads
+// one after another took a quarter); the gradient of 60013 rows of 1536 115 us,
+// 4.8 TB/s (162 while every row asked whether it was the run's own).
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 

@@ -324,6 +324,43 @@ def test_not_a_number_stays_in_its_grid_and_channel():
     assert torch.equal(got, conv)
 
 
+@pytest.mark.parametrize("states", [5, 16, 40])
+def test_steps_of_zero_keep_the_states(states):
+    """exp(0) is 1 to the bit, for every row, tile and segment of a walk, and backward."""
+    lengths = [1500, 3, 77]
+    rows, s, dy, dlast = scan_inputs(14, lengths, 40, states, 1, torch.float32)
+    args = [rows["x"], torch.zeros_like(rows["x"]), rows["a"], rows["b"], rows["c"]]
+    more = dict(softplus=False, offsets=offsets_of(lengths), state=s)
+    _, last = tb.selective_scan(*args, return_state=True, **more)
+    assert torch.equal(last, s)
+    first = tb.selective_scan_backward(torch.zeros_like(dy), *args, dstate=dlast, **more)[8]
+    assert torch.equal(first, dlast)
+    state = s.clone()
+    tb.selective_scan_step(*(v[:3] for v in args[:2]), args[2], *(v[:3] for v in args[3:]), state, softplus=False)
+    assert torch.equal(state, s)
+
+
+def test_many_grids():
+    """More grids than blocks of any kernel, a row or none in each, against the same rows as one token of each stream."""
+    n, dtype = 20000, torch.float32
+    lengths = [i % 2 for i in range(2 * n)]
+    rows, s, dy, dlast = scan_inputs(15, lengths, 8, 16, 1, dtype)
+    args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
+    more = {k: rows[k] for k in ("d", "z", "dt_bias")}
+    y, last = tb.selective_scan(*args, offsets=offsets_of(lengths), state=s, return_state=True, **more)
+    state = s[1::2].clone()
+    want = tb.selective_scan_step(*args, state, **more)
+    assert torch.allclose(y, want, rtol=100 * R.U, atol=100 * R.U * 50) and torch.equal(last[::2], s[::2])
+    assert torch.allclose(last[1::2], state, rtol=100 * R.U, atol=1e-6)
+    got = tb.selective_scan_backward(dy, *args, offsets=offsets_of(lengths), state=s, dstate=dlast, **more)
+    assert torch.equal(got[8][::2], dlast[::2]) and all(torch.isfinite(v).all() for v in got)
+    w, cs = normal(gen(1), 8, 4), normal(gen(2), 2 * n, 3, 8)
+    y, last = tb.causal_conv(args[0], w, offsets=offsets_of(lengths), state=cs, return_state=True)
+    one = cs[1::2].clone()
+    want = tb.causal_conv_step(args[0], w, one)
+    assert torch.allclose(y, want, rtol=1e-5, atol=1e-6) and torch.equal(last[1::2], one) and torch.equal(last[::2], cs[::2])
+
+
 def test_no_rows_and_no_grids():
     rows, s, dy, dlast = scan_inputs(2, [0, 0], 40, 16, 1, torch.float32)
     args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
