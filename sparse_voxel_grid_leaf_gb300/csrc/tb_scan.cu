@@ -277,8 +277,8 @@ cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
 // makes the step and the gate of one of the streams (by every lane they took
 // more instructions than the states), and the states of all four are on their
 // way together.  256 streams of 2048 channels and 16 states: 12.5 us, 5.7 TB/s
-// (17.3 with each lane making every stream's step).  kVec: states, b and c by vectors of four, up to 16 states a channel (a lane's rates
-// stay in registers).
+// (17.3 with each lane making every stream's step).  kVec: states, b and c by
+// vectors of four, up to 16 states a channel (a lane's rates stay in registers).
 constexpr int kStepThreads = 128;
 
 template <class T, bool kVec>

@@ -1,6 +1,6 @@
 // Device helpers shared by the sequence operators (tb_rotary.cu, tb_norm.cu,
-// tb_linattn.cu): 16-byte vectors of the three row types, read and written as
-// 32-bit floats.
+// tb_conv.cu, tb_scan*.cu, tb_linattn*.cu): 16-byte vectors of the three row
+// types, read and written as 32-bit floats, and pairs of those.
 #pragma once
 
 #include <cuda_bf16.h>
