@@ -672,9 +672,16 @@ TB_API tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream st
  * a fixed order.
  *
  * workspace: at least tb_selective_scan_workspace(...) bytes, 256-byte aligned
- * (NULL where that is 0).  The backward call's keeps the states before every
- * eighth row: states / 2 bytes for each row and channel, and some 40% of that
- * besides. */
+ * (NULL where that is 0).  The backward call's, with C channels, each group's
+ * rounded up to 64, N states, rounded up to 8 or to a multiple of 16, and S
+ * slots, one for each grid and one for each 64 rows (down to 16 in small calls):
+ *   C (N + 1) / 2 bytes a row, the states before every eighth one,
+ *   8 N ceil(channels / groups / 128) bytes a row and group, parts of db and dc,
+ *   12 bytes a row and channel where states are more than 16,
+ *   4 C (2 N + 1) bytes a slot, the states at its ends,
+ * and 4 C (N + 2) bytes for each of up to 12 parts a multiprocessor of da.
+ * 124807 rows of 1024 channels with 16 states in 16 grids: 1.5 GB; 20000 grids
+ * of one such row: 3 GB, the slots' almost all of it. */
 typedef struct tb_scan_args {
   const void *x, *dt, *b, *c, *z;
   void* y;

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
     const int n = min(kTileRows, seg.len - i * kTileRows);
     fetch(i + 1);
     if (kWalk == kTiles && i) {
-      const int64_t tile = (int64_t)slot * (l.segment / kTileRows) + i;
+      const int64_t tile = scan_tile_place(row0, i);
       if (!kMany) write(l.tile + tile * l.wide * l.pad + mine);
       *reinterpret_cast<f32x2*>(l.tile_sum + tile * l.wide + t.place + 2 * lane) = total;
     }
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
       if (kMany) {
         rates(k * 2 * NN);
         kept(k);
-        if (kWalk == kTiles && i) write(l.tile + ((int64_t)slot * (l.segment / kTileRows) + i) * l.wide * l.pad + mine + k * 2 * NN);
+        if (kWalk == kTiles && i) write(l.tile + scan_tile_place(row0, i) * l.wide * l.pad + mine + k * 2 * NN);
       }
       if (kMany && k + 1 < blocks) load_states(i, (k + 1) * 2 * NN);
       else load_states(i + 1, 0);

@@ -85,8 +85,9 @@ __device__ __forceinline__ void wait_for_copies() {
   __syncwarp();
 }
 
-// The channels of a warp.  The workspace's arrays have kScanPad channels for
-// each begun so many of a group, so that a tile's place in them is whole.
+// The channels of a warp.  The workspace's arrays have group_pad channels for
+// each group, its own rounded up to kScanChannels: a tile's place in them is
+// whole, and is read and written without a question for its last channels.
 struct ScanTile {
   int group, first, count;  // first channel of all; count <= 0: none
   int64_t place;            // first channel in the workspace
@@ -96,6 +97,12 @@ __device__ __forceinline__ ScanTile scan_tile(const ScanLaunch& l, int group, in
   const int per = l.a.channels / l.a.groups;
   return {group, group * per + tile * CH, min(CH, per - tile * CH), (int64_t)group * l.group_pad + tile * CH};
 }
+
+// Where the workspace holds the states before tile i >= 1 of the segment that
+// starts at row0: as many places as the call has whole tiles, whatever its
+// grids.  Segments that follow one another do not meet there: with len rows, the
+// last of ceil(len / 8) tiles lies before place (row0 + len) / 8.
+__device__ __forceinline__ int64_t scan_tile_place(int64_t row0, int i) { return row0 / kTileRows + i - 1; }
 
 // Rows [row, row + n) of a tile's channels to dst [kTileRows][CH], zeros past
 // them; asynchronous where vectors fit.

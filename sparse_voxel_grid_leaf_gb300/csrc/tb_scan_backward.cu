@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
   const int64_t mine = (t.place + c4) * l.pad + s4;  // the lane's place in a slot of the workspace
   const f32x2 bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(a.d, t);
   f32x2 sum_d = 0, sum_bias = 0;
-  const int blocks = kMany ? l.pad / kStates : 1, chunk_tiles = l.segment / kTileRows;
+  const int blocks = kMany ? l.pad / kStates : 1;
   for (int k = 0; k < blocks; ++k) {
     const int n0 = k * kStates;
     const bool last = k + 1 == blocks;
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
           if (a.z) scan_fetch<T, CH>(&raw[2][0][0], a.z, a.z_row, row, n, t, l.vec);
           scan_fetch<T, CH>(&raw[3][0][0], g.g.dy, g.g.dy_row, row, n, t, l.vec);
           if (i) {
-            const int64_t tile = (int64_t)slot * chunk_tiles + i;
+            const int64_t tile = scan_tile_place(row0, i);
             const float* from = l.tile + tile * l.wide * l.pad + mine + n0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) copy_states<NN>(&s.own[i & 1][j][lane * NN], from + j * l.pad);

@@ -109,8 +109,9 @@ struct ScanLaunch {
   int32_t vec;                // rows that 16-byte copies can read
   float* seg;                 // [segments, wide, pad]: states of the segments, then those they start from
   float* sum;                 // [segments, wide]: their sums of delta
-  float* tile;                // [segments, tiles, wide, pad]: states before the tiles of kTileRows rows, from the segment's
-  float* tile_sum;            // [segments, tiles, wide]: and sums of delta before them; NULL but in the gradient
+  float* tile;                // [tokens / kTileRows, wide, pad]: states before the tiles of kTileRows rows but a segment's
+                              // first, from the segment's
+  float* tile_sum;            // [tokens / kTileRows, wide]: and sums of delta before them; NULL but in the gradient
 };
 cudaError_t launch_scan(const void* args, cudaStream_t s);
 cudaError_t launch_scan_states(const void* args, cudaStream_t s);

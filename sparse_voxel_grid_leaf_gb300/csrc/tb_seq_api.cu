@@ -450,8 +450,8 @@ static ScanCarve scan_carve(int64_t slots, int64_t tokens, int32_t channels, int
   c.seg = take(slots * l.wide * l.pad);
   c.sum = take(slots * l.wide);
   if (!backward) return c;
-  c.tile = take(slots * (l.segment / kTileRows) * l.wide * l.pad);
-  c.tile_sum = take(slots * (l.segment / kTileRows) * l.wide);
+  c.tile = take(tokens / kTileRows * l.wide * l.pad);
+  c.tile_sum = take(tokens / kTileRows * l.wide);
   c.quads = (int32_t)up(channels / groups, 128);
   // blocks take runs of chunks, whose parts of da they keep in registers: as many as make six waves or so
   const int64_t blocks = slots * groups * c.quads;

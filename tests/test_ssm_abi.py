@@ -113,3 +113,27 @@ def test_host_tensors_are_refused(lib):
                  lambda: tb.causal_conv_step(x, torch.zeros(8, 4), torch.zeros(2, 3, 8))):
         with pytest.raises(tb.TBError):
             call()
+
+
+def test_the_gradients_workspace_grows_with_rows_and_slots(lib):
+    """Its arrays one by one, in bytes: what every row takes, and what every segment does, of which a grid has one for
+    each 16 to 64 rows and one more.  A grid's rows are not rounded up to a segment's."""
+    def made(tokens, grids, channels, states, groups):
+        return lib.tb_selective_scan_workspace(ctypes.c_int64(tokens), grids, channels, states, groups, 1)
+
+    def most(tokens, grids, channels, states, groups, sms=256):
+        per = channels // groups
+        wide = (per + 63) // 64 * 64 * groups
+        pad = 8 if states <= 8 else (states + 15) // 16 * 16
+        slots, quads = tokens // 16 + grids, (per + 127) // 128
+        runs = min(slots, 12 * sms // (groups * quads) + 1)
+        row = wide * (pad + 1) / 2 + 8 * pad * groups * quads + (12 * channels if states > 16 else 0)
+        return tokens * row + slots * 4 * wide * (2 * pad + 1) + runs * 4 * wide * (pad + 2) + 10 * 256
+
+    for case in [(20000, 20000, 1024, 16, 1), (60000, 40000, 1024, 16, 1), (32768, 4096, 2048, 16, 1), (16384, 2048, 2048, 64, 1),
+                 (124807, 16, 1024, 16, 1), (1333, 5, 202, 12, 2), (0, 7, 64, 16, 1), (7, 1, 1, 1, 1), (100, 300, 96, 4, 2),
+                 (5000, 1, 300, 256, 3)]:
+        assert 0 < made(*case) <= most(*case), case
+    assert made(20000, 20000, 1024, 16, 1) < 3e9
+    # one more empty grid takes a segment's states at its ends, and their decay
+    assert made(20000, 20001, 1024, 16, 1) - made(20000, 20000, 1024, 16, 1) <= 4 * 1024 * 33 + 4 * 1024 * 18 + 2560

@@ -362,6 +362,37 @@ def test_many_grids():
     assert torch.allclose(y, want, rtol=1e-5, atol=1e-6) and torch.equal(last[1::2], one) and torch.equal(last[::2], cs[::2])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_grids_of_every_length(dtype):
+    """Lengths of 0 to 40 in no order, so that segments start anywhere in eight rows and end anywhere in them."""
+    lengths = [(i * 17) % 41 for i in range(41)]
+    compare_scan(lengths, 72, 16, 1, dtype)
+    compare_scan(lengths, 40, 20, 2, dtype)
+    compare_scan([200] + lengths[:20] + [1] * 30, 16, 4, 1, dtype)
+
+
+def test_many_grids_of_many_channels():
+    """The gradient's workspace is its rows' and its slots'; each grid by itself gives the same."""
+    n, c = 20000, 1024
+    lengths = [1] * n
+    rows, _, dy, _ = scan_inputs(16, lengths, c, 16, 1, torch.bfloat16, state=False)
+    args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
+    more = {k: rows[k] for k in ("d", "z", "dt_bias")}
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    got = tb.selective_scan_backward(dy, *args, offsets=offsets_of(lengths), **more)
+    torch.cuda.synchronize()
+    # 2 states of 16 a channel and grid, and the rest of the workspace and the outputs, each a small part of that
+    assert torch.cuda.max_memory_allocated() - before < 1.35 * 2 * 4 * n * c * 16
+    some = torch.arange(0, n, 997, device="cuda")
+    part = [v[some] if v.shape[0] == n else v for v in args]
+    want = R.scan(*part, more["d"], more["z"][some], more["dt_bias"], True, [1] * len(some), None, dy[some])[2:]
+    for name, v, w in zip(NAMES, got, want):
+        if name in ("dx", "ddt", "db", "dc", "dz"):
+            near(v[some], w, torch.bfloat16, name)
+
+
 def test_no_rows_and_no_grids():
     rows, s, dy, dlast = scan_inputs(2, [0, 0], 40, 16, 1, torch.float32)
     args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
