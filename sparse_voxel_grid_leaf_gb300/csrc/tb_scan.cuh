@@ -45,6 +45,29 @@ __device__ __forceinline__ f32x2 scan_decay(f32x2 delta, f32x2 a2) {
   return pair(scan_ex2(x.x), scan_ex2(x.y));
 }
 
+// exp(delta a) x + own over many rows at once: delta is their sum.  Where a state
+// grows, the factor may be beyond 32 bits although the walk row by row is not: x
+// is zero, or small.  Past 2^127 x takes the rest of the exponent first, and a
+// zero stays one.
+constexpr float kMostExponent = 127.f;
+__device__ __forceinline__ float scan_exponent(float delta, float a2) { return fmaf(delta, a2, 0x1p-25f); }
+__device__ __forceinline__ float scan_exponent(f32x2 delta, f32x2 a2) {  // the larger one
+  const float2 e = halves(fma2(delta, a2, both(0x1p-25f)));
+  return fmaxf(e.x, e.y);
+}
+__device__ __forceinline__ float scan_raised(float e, float x) {  // x 2^(e - 127)
+  return x == 0.f ? x : x * scan_ex2(e - kMostExponent);
+}
+__device__ __forceinline__ float scan_carried(float delta, float a2, float x, float own) {
+  const float e = scan_exponent(delta, a2);
+  if (e > kMostExponent) return fmaf(0x1p127f, scan_raised(e, x), own);
+  return fmaf(scan_ex2(e), x, own);
+}
+__device__ __forceinline__ f32x2 scan_carried(f32x2 delta, f32x2 a2, f32x2 x, f32x2 own) {
+  const float2 d = halves(delta), a = halves(a2), f = halves(x), o = halves(own);
+  return pair(scan_carried(d.x, a.x, f.x, o.x), scan_carried(d.y, a.y, f.y, o.y));
+}
+
 // log(1 + exp(v)) = max(v, 0) + log(1 + u), u = exp(-|v|), and log(1 + u) = 2
 // artanh(s), s = u / (2 + u) <= 1/3: small steps keep their relative accuracy.
 // artanh(s) = s + s q P(q), q = s^2, with P of degree 3 fitted to its series on

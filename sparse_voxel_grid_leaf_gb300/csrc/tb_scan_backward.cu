@@ -286,10 +286,22 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
 #pragma unroll
             for (int j = 0; j < 4; ++j) read_numbers<NN>(f[j], &s.own[i & 1][j][lane * NN]);
             as_pairs(own, f);
+            float most = 0.f;  // one question for all of them
 #pragma unroll
             for (int n = 0; n < NN; ++n)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) h[j][n] = fma2(scan_decay(d[j], a2[j][n]), h[j][n], own[j][n]);
+              for (int j = 0; j < 2; ++j) most = fmaxf(most, scan_exponent(d[j], a2[j][n]));
+            if (most > kMostExponent) {
+#pragma unroll
+              for (int n = 0; n < NN; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) h[j][n] = scan_carried(d[j], a2[j][n], h[j][n], own[j][n]);
+            } else {
+#pragma unroll
+              for (int n = 0; n < NN; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) h[j][n] = fma2(scan_decay(d[j], a2[j][n]), h[j][n], own[j][n]);
+            }
           }
         }
         if (!placed) nothing(h);

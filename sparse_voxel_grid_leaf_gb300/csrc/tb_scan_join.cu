@@ -50,6 +50,24 @@ __device__ __forceinline__ void join(const ScanLaunch& l, float* seg, int b, int
         own[j] = *reinterpret_cast<const float4*>(at + (j0 + j) * next);
         d[j] = sum[(j0 + j) * next_sum];
       }
+    float most = 0.f;  // one question for a batch: its decays stay ahead of the chain
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (j0 + j < count)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, scan_exponent(d[j], a2[k]));
+    if (most > kMostExponent) {  // one by one, read again: few calls come here
+#pragma unroll 1
+      for (int j = j0; j < min(j0 + kBatch, n); ++j) {
+        float f[4];
+        if (j < count) read_numbers<4>(f, at + j * next);
+        write_numbers<4>(at + j * next, x);
+        if (j < count)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = scan_carried(sum[j * next_sum], a2[k], x[k], f[k]);
+      }
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
       if (j0 + j < n) {

@@ -340,6 +340,44 @@ def test_steps_of_zero_keep_the_states(states):
     assert torch.equal(state, s)
 
 
+@pytest.mark.parametrize("states", [4, 16, 20])
+@pytest.mark.parametrize("rate", [3.0, 12.0])
+def test_states_that_grow(states, rate):
+    """Rates above zero.  Over a segment, and over a tile at 12 a row, the decay as a whole is beyond 32 bits, where
+    the walk is not: states that are zero until the last rows, with a gradient that is until the first ones, and small
+    ones that grow for a while."""
+    n, c = 230, 40
+    g = gen(int(rate) + states)
+    a = 1.0 + 0.05 * torch.rand(c, states, generator=g, device="cuda")
+    b, k = normal(g, n, 1, states), normal(g, n, 1, states)
+    few = int(70 / rate)  # exp(74) at most from a state or gradient to the end
+    x, dy = normal(g, n, c), normal(g, n, c)
+    x[:n - few] = 0
+    dy[few:] = 0
+    compare_growth(x, torch.full((n, c), rate, device="cuda"), a, b, k, torch.zeros(1, c, states, device="cuda"), dy,
+                   torch.zeros(1, c, states, device="cuda"))
+    dt = torch.zeros(n, c, device="cuda")
+    dt[:int(120 / rate)] = rate  # exp(126) from first to last, of values that are 1e-36 as they come
+    compare_growth(*(normal(g, n, c, scale=1e-36), dt, a, b, k), *(normal(g, *v, scale=1e-36) for v in ((1, c, states), (n, c), (1, c, states))))
+
+
+def compare_growth(x, dt, a, b, c, state, dy, dlast):
+    lengths = [x.shape[0]]
+    want = R.scan(x, dt, a, b, c, None, None, None, False, lengths, state, dy, dlast)
+    y, last = tb.selective_scan(x, dt, a, b, c, softplus=False, state=state, return_state=True)
+    got = tb.selective_scan_backward(dy, x, dt, a, b, c, softplus=False, state=state, dstate=dlast)
+    # Products of values of 1e-36 are below 2^-126, where a product is off by up to 2^-150 (TINY) whatever its size, and
+    # sums add nothing to that.  db and dc add a product for each channel; g . b, h . c and a . q one for each state, which
+    # ddt and dx multiply by a (below 2) or delta, off by TINY once more; da adds q delta, q off by TINY, for each row.
+    # (A walk of db row by row in 32 bits is off by 4 TINY where it is 1e-43, of 40 channels.)
+    (rows, channels), states = x.shape, a.shape[1]
+    floor = (channels + 3 * states + rows) * (1 + dt.max().double()) * TINY[torch.float32]
+    given = [(name, v) for name, v in zip(NAMES, got) if v is not None]
+    for (name, v), (w, bound) in zip([("y", y), ("last", last)] + given, [w for w, k in zip(want, ["y", "last"] + NAMES)
+                                                                          if k not in ("dd", "dz", "ddt_bias")]):
+        near(v, (w, bound + floor), torch.float32, name)
+
+
 def test_many_grids():
     """More grids than blocks of any kernel, a row or none in each, against the same rows as one token of each stream."""
     n, dtype = 20000, torch.float32
