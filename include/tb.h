@@ -663,7 +663,8 @@ TB_API tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream st
  * rows is its first.  states <= 256.  offsets as in tb_linear_args: rows of no
  * grid get zeros.  No output may share memory with an input.  In a channel that
  * meets an infinity, outputs from there on may be NaN where the formula has an
- * infinity.
+ * infinity.  A rate a of minus infinity is a decay of 0, and of 1 in a step of
+ * zero.
  *
  * The backward call gives, for the gradient dy of y and dstate_out (NULL: zero)
  * of state_out, the gradients of every input: dx, ddt, dz (with z), db, dc of

@@ -67,15 +67,18 @@ __global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
   const int64_t mine = (t.place + c4) * l.pad + s0;  // the lane's place in a slot of the workspace
   float* const own = l.seg + (int64_t)slot * l.wide * l.pad + mine;
   f32x2 h[4][NN / 2] = {}, a2[4][NN / 2];
-  auto as_pairs = [&](f32x2(&p)[4][NN / 2], const float(&f)[4][NN], float by) {
+  auto as_pairs = [&](f32x2(&p)[4][NN / 2], const float(&f)[4][NN]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int n = 0; n < NN; n += 2) p[j][n / 2] = pair(f[j][n] * by, f[j][n + 1] * by);
+      for (int n = 0; n < NN; n += 2) p[j][n / 2] = pair(f[j][n], f[j][n + 1]);
   };
   auto rates = [&](int n0) {
     if (kMany) read_dense<NN>(rate, a.a, t, a.states, c4, n0 + s0);
-    as_pairs(a2, rate, kLog2e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < NN; n += 2) a2[j][n / 2] = pair(scan_rate(rate[j][n]), scan_rate(rate[j][n + 1]));
   };
   auto first = [&](int n0) {
     if (!kGives) return;
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
     } else {
       read_dense<NN>(f, a.state ? a.state + state_at : nullptr, t, a.states, c4, n0 + s0);
     }
-    as_pairs(h, f, 1.f);
+    as_pairs(h, f);
   };
   auto write = [&](float* to) {  // in the workspace
 #pragma unroll
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanStepLaunch l) {
   if (kVec && mine) {
     unpack<float, 4>(load_pack<float, 4>(rate + s4), a2);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) a2[k] *= kLog2e;
+    for (int k = 0; k < 4; ++k) a2[k] = scan_rate(a2[k]);
   }
   for (int64_t n = n0; n < n1; n += 4) {
     // the lane's own stream of the four
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanStepLaunch l) {
         }
       } else {
         for (int s = lane; s < a.states; s += 4) {
-          const float f = fmaf(scan_decay(dj, rate[s] * kLog2e), h[s], xj * RowType<T>::to(b[j * a.b_row + s]));
+          const float f = fmaf(scan_decay(dj, scan_rate(rate[s])), h[s], xj * RowType<T>::to(b[j * a.b_row + s]));
           sum[j] = fmaf(RowType<T>::to(cc[j * a.c_row + s]), f, sum[j]);
           h[s] = f;
         }

@@ -19,6 +19,8 @@
 #include "tb_linattn.cuh"
 #include "tb_seq.cuh"
 
+#include <cfloat>
+
 namespace tb {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -35,7 +37,13 @@ __device__ __forceinline__ float scan_rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(delta a) for a2 = a log2(e).  The instruction rounds towards zero: over
+// a log2(e), finite where a is minus infinity (a channel without memory): the
+// rows past a segment's end in its last tile take steps of zero, whose decay is 1.
+__device__ __forceinline__ float scan_rate(float a) {
+  const float a2 = a * kLog2e;
+  return a2 < -FLT_MAX ? -FLT_MAX : a2;
+}
+// exp(delta a) for a2 = scan_rate(a).  The instruction rounds towards zero: over
 // [-1, 0] its results are 2e-8 to 5e-8 low on average (measured), which the
 // many decays that a slow state goes through would add up.  2^-25 more in the
 // exponent takes most of that back, and costs nothing as a sum.

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int m = 0; m < NN / 2; ++m) a2[j][m] = pair(rate[j][2 * m] * kLog2e, rate[j][2 * m + 1] * kLog2e);
+    for (int m = 0; m < NN / 2; ++m) a2[j][m] = pair(scan_rate(rate[j][2 * m]), scan_rate(rate[j][2 * m + 1]));
   for (int i = tiles - 1; i >= 0; --i) {
     const int n = min(kTileRows, seg.len - i * kTileRows);
     fetch(i - 1);
@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
     {
       float f[4][NN];
       read_dense<NN>(f, a.a, t, a.states, c4, n0 + s4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int n = 0; n < NN; ++n) f[j][n] = scan_rate(f[j][n]);
       as_pairs(a2, f);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int n = 0; n < NN; ++n) a2[j][n] = mul2(a2[j][n], both(kLog2e));
     }
     if (k == 0) wait_for_last_kernel();
     for (int slot = run * g.per_run; slot < min((run + 1) * g.per_run, l.segments); ++slot) {

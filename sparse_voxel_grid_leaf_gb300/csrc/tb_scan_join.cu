@@ -31,7 +31,7 @@ __device__ __forceinline__ void join(const ScanLaunch& l, float* seg, int b, int
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const bool is = in < per && s + k < a.states;
-    a2[k] = is ? a.a[c * a.states + s + k] * kLog2e : 0.f;
+    a2[k] = is ? scan_rate(a.a[c * a.states + s + k]) : 0.f;
     x[k] = is && first ? first[state_at + k] : 0.f;
   }
   wait_for_last_kernel();

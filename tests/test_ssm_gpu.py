@@ -340,6 +340,33 @@ def test_steps_of_zero_keep_the_states(states):
     assert torch.equal(state, s)
 
 
+@pytest.mark.parametrize("states", [5, 16, 40])
+@pytest.mark.parametrize("lengths", [[13, 8, 0, 3], [333], [11] * 30], ids=str)
+def test_rates_of_minus_infinity(states, lengths):
+    """States without memory, next to others: of the reference their rates are finite, and exp(delta a) the same 0."""
+    rows, s, dy, dlast = scan_inputs(41, lengths, 40, states, 1, torch.float32)
+    none = torch.rand(40, states, generator=gen(3), device="cuda") < 0.5
+    none[0], none[1] = True, False
+    args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
+    more = {k: rows[k] for k in ("d", "z", "dt_bias")}
+    args[2] = args[2].masked_fill(none, -1e30)
+    want = R.scan(*args, more["d"], more["z"], more["dt_bias"], True, lengths, s, dy, dlast)
+    args[2] = args[2].masked_fill(none, -float("inf"))
+    y, last = tb.selective_scan(*args, offsets=offsets_of(lengths), state=s, return_state=True, **more)
+    near(y, want[0], torch.float32, "y")
+    near(last, want[1], torch.float32, "last")
+    got = tb.selective_scan_backward(dy, *args, offsets=offsets_of(lengths), state=s, dstate=dlast, **more)
+    for name, v, w in zip(NAMES, got, want[2:]):
+        near(v, w, torch.float32, name)
+    if len(lengths) == 30:
+        state = s.clone()
+        first = torch.arange(0, 330, 11, device="cuda")
+        part = [v[first] if v.shape[0] == 330 else v for v in args]
+        y = tb.selective_scan_step(*part, state, d=more["d"], z=more["z"][first], dt_bias=more["dt_bias"])
+        near(y, tuple(v[first] for v in want[0]), torch.float32, "step")
+        assert torch.isfinite(state).all()
+
+
 @pytest.mark.parametrize("states", [4, 16, 20])
 @pytest.mark.parametrize("rate", [3.0, 12.0])
 def test_states_that_grow(states, rate):
