@@ -410,6 +410,9 @@ tb_status tb_causal_conv_step(const tb_conv_step_args* args, tb_stream stream) {
 
 // ----------------------------------------------------------- selective scan
 
+// Channels in the workspace: each group's rounded up to whole tiles.
+static int64_t scan_wide(int32_t channels, int32_t groups) { return up(channels / groups, kScanChannels) * kScanChannels * groups; }
+
 // Tiles of kScanChannels channels and blocks of states; four warps of tiles a
 // block, fewer where their states would not fit in shared memory.
 static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t groups) {
@@ -476,6 +479,7 @@ static int32_t scan_chunk(const ScanLaunch& l, int64_t tokens, int32_t groups, i
 int64_t tb_selective_scan_workspace(int64_t tokens, int32_t grids, int32_t channels, int32_t states, int32_t groups,
                                     int32_t backward) {
   if (tokens < 0 || grids < 0 || channels < 1 || states < 1 || states > 256 || groups < 1 || channels % groups) return 0;
+  if (tokens > kMaxRows || scan_wide(channels, groups) > kMaxRows) return 0;  // refused by the call
   ScanLaunch l{};
   scan_shape(l, channels, states, groups);
   int sms = seq_sms();
@@ -532,7 +536,7 @@ static tb_status scan_check(const char* what, const tb_scan_args& a) {
   if (!a.offsets && a.grids != 1) return seq_fail(TB_ERR_INVALID_ARG, "%s: %d grids without offsets", what, a.grids);
   if (a.grids == 0 && a.tokens) return seq_fail(TB_ERR_INVALID_ARG, "%s: tokens without grids", what);
   if (!a.a || (a.tokens && (!a.x || !a.dt || !a.b || !a.c))) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
-  if (up(a.channels / a.groups, kScanChannels) * kScanChannels * a.groups > kMaxRows)
+  if (scan_wide(a.channels, a.groups) > kMaxRows)
     return seq_fail(TB_ERR_TOO_LARGE, "%s: 2^31 channels or more, each group's rounded up to %d", what, kScanChannels);
   return TB_OK;
 }

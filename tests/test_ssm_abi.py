@@ -137,3 +137,17 @@ def test_the_gradients_workspace_grows_with_rows_and_slots(lib):
     assert made(20000, 20000, 1024, 16, 1) < 3e9
     # one more empty grid takes a segment's states at its ends, and their decay
     assert made(20000, 20001, 1024, 16, 1) - made(20000, 20000, 1024, 16, 1) <= 4 * 1024 * 33 + 4 * 1024 * 18 + 2560
+
+
+def test_sizes_that_are_refused_ask_for_no_workspace(lib):
+    """2^25 groups of one channel are 2^31 channels in whole tiles: the call refuses them, and the workspace's size is
+    not what 32 bits make of theirs."""
+    n = 1 << 25
+    for backward in (0, 1):
+        assert lib.tb_selective_scan_workspace(ctypes.c_int64(1), 1, n, 1, n, backward) == 0
+        assert lib.tb_selective_scan_workspace(ctypes.c_int64(1 << 31), 1, 8, 16, 1, backward) == 0
+    assert lib.tb_selective_scan_workspace(ctypes.c_int64(1), 1, n - 1, 1, n - 1, 1) > 0
+    args = SCAN.pack(P, P, P, P, 0, P, P, 0, 0, 0, 0, 0, 0, 1, *[n] * 8, 0, 1, n, 1, n, 2, 1)
+    refused(lib, "tb_selective_scan", args, b"2^31 channels")
+    # the gradient's rows, its own gradients and strides behind the struct of the scan
+    refused(lib, "tb_selective_scan_backward", args + bytes(120), b"2^31 channels")
