@@ -831,7 +831,9 @@ cudaError_t pick_back(const NormBackwardLaunch& n, cudaStream_t s) {
       case 1: return go_back<T, V, 1>(n, s);
       case 2: return go_back<T, V, 2>(n, s);
       case 4: return go_back<T, V, 4>(n, s);
-      default: return go_back<T, V, 8>(n, s);
+      case 8:
+        if constexpr (sizeof(T) == 4) return go_back<T, V, 8>(n, s);  // 16384 elements of 16 bits are four vectors of 512 threads
+      default: return cudaErrorInvalidValue;
     }
   }
   return n.nv <= 8 ? go_back<T, 1, 8>(n, s) : go_back<T, 1, 32>(n, s);
