@@ -1,6 +1,6 @@
-// Which rows a block of the linear-attention and selective-scan kernels walks:
-// whole grids, or the segments of a call that splits its grids along the rows.
-// L: a launch with offsets, tokens, grids and segment.
+// Which rows a block of the linear-attention kernels walks: whole grids, or the
+// segments of a call that splits its grids along the rows.  L: a launch with
+// offsets, tokens and grids, of the selective scan too (its segments: tb_scan.cuh).
 #pragma once
 
 #include "tb_seq.h"
@@ -77,14 +77,12 @@ __device__ __forceinline__ void lin_zero_share(const LinLaunch& l, const LinProb
 template <int size> struct LinBits { typedef uint16_t type; };
 template <> struct LinBits<4> { typedef uint32_t type; };
 
-template <class L>
-__device__ __forceinline__ int lin_segments_of(const L& l, int64_t rows) {
+__device__ __forceinline__ int lin_segments_of(const LinLaunch& l, int64_t rows) {
   return rows > 0 ? (int)((rows + l.segment - 1) / l.segment) : 1;
 }
 
 // The segment slot of grid b's first segment.  One warp; the same in all lanes.
-template <class L>
-__device__ __forceinline__ int lin_first_slot(const L& l, int b) {
+__device__ __forceinline__ int lin_first_slot(const LinLaunch& l, int b) {
   int sum = 0;
   for (int i = threadIdx.x & 31; i < b; i += 32) {
     int64_t begin, end;
@@ -97,8 +95,7 @@ __device__ __forceinline__ int lin_first_slot(const L& l, int b) {
 }
 
 // The segment of a slot, found by one warp; the same in all lanes.
-template <class L>
-__device__ __forceinline__ LinSegment lin_segment(const L& l, int slot) {
+__device__ __forceinline__ LinSegment lin_segment(const LinLaunch& l, int slot) {
   LinSegment s;
   s.grid = -1;
   s.slot = slot;

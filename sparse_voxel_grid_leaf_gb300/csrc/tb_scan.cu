@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(128, kMany ? 2 : 4) k_scan(ScanLaunch l) {
   const f32x2 bias = channel_pair<CH>(a.dt_bias, t), skip = channel_pair<CH>(kGives ? a.d : nullptr, t);
   float rate[4][NN];  // on their way while the segment is found
   if (!kMany) read_dense<NN>(rate, a.a, t, a.states, c4, s0);
-  const LinSegment seg = lin_segment(l, slot);
+  const LinSegment seg = scan_segment_of(l, slot);
   if (kGives) scan_zero_share<T, CH>(l, a.y, a.y_row, slot, t);
   if (seg.grid < 0 || (kWalk == kStates && seg.index + 1 == seg.count)) return;  // the last one's own state joins no other
   const int64_t row0 = seg.begin + seg.first, state_at = (int64_t)seg.grid * a.channels * a.states;

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_scan_carry(ScanBackwardLaunch g
   const f32x2 bias = channel_pair<CH>(a.dt_bias, t);
   float rate[4][NN];  // on their way while the segment is found
   read_dense<NN>(rate, a.a, t, a.states, c4, n0 + s0);
-  const LinSegment seg = lin_segment(l, slot);
+  const LinSegment seg = scan_segment_of(l, slot);
   if (seg.grid < 0 || (seg.index == 0 && !g.g.dstate)) {  // the first chunk's goes nowhere else
     wait_for_last_kernel();
     return;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) k_scan_backward(ScanBackwardLa
         scan_zero_share<T, CH>(l, g.g.ddt, g.g.ddt_row, slot, t);
         if (a.z) scan_zero_share<T, CH>(l, g.g.dz, g.g.dz_row, slot, t);
       }
-      const LinSegment seg = lin_segment(l, slot);
+      const LinSegment seg = scan_segment_of(l, slot);
       if (seg.grid < 0 || seg.len == 0) continue;
       const int64_t row0 = seg.begin + seg.first;
       const int tiles = (seg.len + kTileRows - 1) / kTileRows;

@@ -22,11 +22,10 @@ __device__ __forceinline__ void join(const ScanLaunch& l, float* seg, int b, int
   const int s = (int)(i - place * per_channel) * 4, group = (int)(place / l.group_pad), in = (int)(place - (int64_t)group * l.group_pad);
   const int per = a.channels / a.groups;
   const int64_t c = (int64_t)group * per + in, state_at = ((int64_t)b * a.channels + c) * a.states + s;
-  const int slot0 = lin_first_slot(l, b);
+  const int slot0 = scan_first_slot(l, b);
   int64_t begin, end;
   lin_grid_rows(l, b, begin, end);
-  // offsets that decrease name rows twice: their segments are more than the slots, which bound the walk
-  const int n = min(lin_segments_of(l, end - begin), max(0, l.segments - slot0));
+  const int n = scan_segments_of(l, end - begin);
   float a2[4], x[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {

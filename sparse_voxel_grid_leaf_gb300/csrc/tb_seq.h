@@ -97,7 +97,7 @@ constexpr int kTileRows = 8;       // of a tile in shared memory
 constexpr int kScanChannels = 64;  // of a walk's warp
 struct ScanLaunch {
   tb_scan_args a;
-  const int64_t* offsets;     // as in LinLaunch: the walks of tb_linattn.cuh
+  const int64_t* offsets;     // as in LinLaunch
   int64_t tokens;
   int32_t grids;
   int32_t segment, segments;  // rows of one, a multiple of kTileRows, 0: whole grids; slots

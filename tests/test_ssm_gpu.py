@@ -458,6 +458,24 @@ def test_many_grids_of_many_channels():
             near(v[some], w, torch.bfloat16, name)
 
 
+def test_time_of_many_grids_grows_with_their_number():
+    """The gradient of ten times the grids takes ten times as long, and some; by the square it would take a hundred."""
+    def time(n):
+        rows, _, dy, _ = scan_inputs(17, [1] * n, 64, 16, 1, torch.bfloat16, state=False)
+        args, offsets = [rows[k] for k in ("x", "dt", "a", "b", "c")], offsets_of([1] * n)
+        took = []
+        for _ in range(4):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            tb.selective_scan_backward(dy, *args, offsets=offsets)
+            end.record()
+            torch.cuda.synchronize()
+            took.append(start.elapsed_time(end))
+        return min(took[1:])
+
+    assert time(200000) < 25 * time(20000)
+
+
 def test_no_rows_and_no_grids():
     rows, s, dy, dlast = scan_inputs(2, [0, 0], 40, 16, 1, torch.float32)
     args = [rows[k] for k in ("x", "dt", "a", "b", "c")]
