@@ -18,7 +18,11 @@
 // square would lose the digits of rows whose mean is large), both over the row
 // in registers, in pairs of numbers.  Measured, bf16: 124807 rows of 1024 with
 // the residual's addition 164 us, 6.2 TB/s (192 in single numbers); the gradient
-// of 60013 rows of 1536 187 us, 3.9 TB/s.
+// of 60013 rows of 1536 187 us, 3.9 TB/s.  Wide rows are more than the registers
+// hold next to the gradient's sums: past 8192 elements it spills some 1000 bytes a
+// thread (7500 rows of 16384 in bf16 552 us, 3.8 times the bytes' time, where
+// 15000 of 8192 take 302 and 30000 of 4096 308, twice that time); in 32 bits
+// 30000 rows of 4096 take 334 us, 1.14 times, 7500 of 16384 1098, 3.7 times.
 #include "tb_seq.cuh"
 #include "tb_seq.h"
 

@@ -9,10 +9,18 @@
 // states first (from zero), their joining, then the outputs.  A segment's decay
 // as a whole is exp(a sum of delta), so joining needs the sum alone.
 //
-// A row of 64 channels and 16 states takes 148 instructions in the states' pass
-// (284 cycles a scheduler, the multiply-add pipe 70% and the exponentials 55%
-// busy) and 205 in the outputs' (420): a prompt of 65537 rows, 2048 channels in
-// bf16 is 1.09 ms, where its bytes alone would be 0.16.
+// A row of 64 channels and 16 states takes 148 instructions in the states' pass,
+// 284 cycles a scheduler: of those 62 paired multiply-adds at their rate (2.45
+// cycles each) would take 53%, 36 exponentials and quotients (4 cycles) 51%; the
+// counters have the issue slots 56% and the exponentials 56% busy, and in the
+// outputs' pass (205 instructions, 420 cycles, 36 bytes spilled a thread in 16
+// bits) 54 and 41%.  Nothing is full; which wait leads was not measured.  A prompt
+// of 65537 rows, 2048 channels in bf16 is 1.10 ms, where its bytes alone would be
+// 0.16.
+//
+// Past 16 states a warp takes its channels' states in blocks of 16, in turn for
+// every eight rows, and fewer warps run: a prompt of 16384 rows, 2048 channels
+// 0.31 ms with 16 states, 0.64 with 32, 1.39 with 64, 2.83 with 128.
 #include "tb_scan.cuh"
 
 namespace tb {
@@ -281,7 +289,9 @@ cudaError_t by_type(const ScanLaunch& l, cudaStream_t s) {
 // more instructions than the states), and the states of all four are on their
 // way together.  256 streams of 2048 channels and 16 states: 12.5 us, 5.7 TB/s
 // (17.3 with each lane making every stream's step).  kVec: states, b and c by
-// vectors of four, up to 16 states a channel (a lane's rates stay in registers).
+// vectors of four, up to 16 states a channel (a lane's rates stay in registers);
+// element by element 64 states of those streams take 108 us, where their bytes
+// take 41.
 constexpr int kStepThreads = 128;
 
 template <class T, bool kVec>

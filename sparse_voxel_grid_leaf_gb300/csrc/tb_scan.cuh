@@ -10,9 +10,8 @@
 // and then go through shared memory: a lane writes its part, and the lane of a
 // channel (or state) reads and adds what belongs to it.
 //
-// The walks are bound by issued instructions, shared memory and exponentials
-// in about equal parts, so numbers go in pairs, two to an instruction
-// (fma.rn.f32x2).  What belongs to a row and a channel (steps, gates, outputs)
+// Issued instructions, exponentials and multiply-adds are each about half of a
+// walk's time, so numbers go in pairs, two to an instruction (fma.rn.f32x2).  What belongs to a row and a channel (steps, gates, outputs)
 // is done by pairs of channels as well.
 #pragma once
 

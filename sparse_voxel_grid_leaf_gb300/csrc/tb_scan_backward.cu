@@ -21,7 +21,9 @@
 // two blocks of four warps a multiprocessor, whose waits for one another's
 // results leave the issue slots 40% busy.  16 grids of 124807 rows, 1024
 // channels of 16 states in bf16: 3.8 ms for all of it, of which this kernel 2.8,
-// the chunks' states 0.47 and what they carry 0.43.
+// the chunks' states 0.47 and what they carry 0.43.  More than 16 states are
+// taken in blocks of 16, all rows for each: forward and gradient of 16384 rows,
+// 1024 channels 0.73 ms with 16, 3.30 with 64.
 #include "tb_scan.cuh"
 
 namespace tb {

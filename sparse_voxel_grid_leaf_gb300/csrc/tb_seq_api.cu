@@ -302,6 +302,8 @@ static tb_status conv_check(const char* what, const tb_conv_args& a) {
   if (!a.weight || (a.tokens && !a.x)) return seq_fail(TB_ERR_INVALID_ARG, "%s: bad pointer", what);
   return TB_OK;
 }
+// Rows that miss whole vectors go element by element: 60013 rows of 1028 channels
+// in bf16 174 us, of 1024 53; with the gradient 279 and 138.
 // Threads along the channels: up to 128 of a block, evenly over the blocks; rows
 // of fewer share one.  Runs of rows are as long as gives every multiprocessor
 // `threads` threads, within bounds.
@@ -339,6 +341,8 @@ tb_status tb_causal_conv(const tb_conv_args* args, tb_stream stream) {
   return TB_OK;
 }
 
+// Threads a multiprocessor that a wave of runs is cut for.  Registers (124 in 16
+// bits, 92 in 32) would hold 512 and 640.
 constexpr int kConvBackThreads = 384, kConvBackLeast = 8, kConvBackMost = 512;
 
 int64_t tb_causal_conv_backward_workspace(int64_t tokens, int32_t channels, int32_t taps) {
@@ -428,7 +432,10 @@ static void scan_shape(ScanLaunch& l, int32_t channels, int32_t states, int32_t 
 // Rows of a segment of the forward pass, 0: grids are walked whole.  A walk is
 // sequential along a grid and a warp's, so a call with few of them is split, so
 // that four blocks a multiprocessor run at once; the segments' own states cost
-// most of a walk once more.
+// most of a walk once more (66300 rows of 2048 channels: one grid, split, 1.12 ms;
+// 64 of 1035 rows each, whole, 0.78).  The rule knows how many grids there are and
+// not how long: one of 60000 rows among 63 of 100 is one warp's walk for each 64
+// channels and takes 28 ms.
 static int32_t scan_segment(const ScanLaunch& l, int64_t tokens, int32_t grids, int sms) {
   const int64_t blocks = (int64_t)grids * l.blocks_x;
   if (grids <= 0 || blocks >= 3ll * sms || tokens < 96ll * grids) return 0;
