@@ -458,6 +458,33 @@ def test_many_grids_of_many_channels():
             near(v[some], w, torch.bfloat16, name)
 
 
+@pytest.mark.parametrize("lead,tail", [(0, 0), (130, 0), (130, 95), (700, 1300)])
+def test_segments_between_rows_of_no_grid(lead, tail):
+    """Segments by the first rows of their grids: rows before and past them, more grids than a warp has lanes, empty ones
+    at both ends."""
+    for lengths in ([0, 0, 700, 0, 25, 1, 0], [90 + i % 7 for i in range(70)], [0] * 40 + [900] + [0] * 40):
+        n = sum(lengths)
+        rows, s, dy, dlast = scan_inputs(51, lengths, 16, 16, 1, torch.float32)
+        names = ("x", "dt", "a", "b", "c")
+        want = R.scan(*(rows[k] for k in names), rows["d"], rows["z"], rows["dt_bias"], True, lengths, s, dy, dlast)
+
+        def padded(t):
+            if t is None or t.shape[0] != n:
+                return t
+            return torch.cat([t.new_full((lead,) + t.shape[1:], float("nan")), t, t.new_full((tail,) + t.shape[1:], float("inf"))])
+
+        args = [padded(rows[k]) if k != "a" else rows[k] for k in names]
+        more = dict(d=rows["d"], z=padded(rows["z"]), dt_bias=rows["dt_bias"], offsets=offsets_of(lengths, lead), state=s)
+        y, last = tb.selective_scan(*args, return_state=True, **more)
+        near(last, want[1], torch.float32, "last")
+        got = tb.selective_scan_backward(padded(dy), *args, dstate=dlast, **more)
+        for name, v, w in zip(["y"] + NAMES, (y,) + tuple(got), want[:1] + want[2:]):
+            if name in ("y", "dx", "ddt", "dz", "db", "dc"):
+                assert (v[:lead] == 0).all() and (v[lead + n:] == 0).all(), name
+                v = v[lead:lead + n]
+            near(v, w, torch.float32, name)
+
+
 def test_time_of_many_grids_grows_with_their_number():
     """The gradient of ten times the grids takes ten times as long, and some; by the square it would take a hundred."""
     def time(n):
